@@ -18,7 +18,7 @@ import torch
 own = False
 
 E4M3_MAX = 448.0
-E_MIN, E_MAX = -60, 60          # range of the scales' exponents
+E_MIN, E_MAX = -48, 48          # range of the scales' exponents
 
 
 # ---------------------------------------------------------------- cases
@@ -464,7 +464,7 @@ def _exact_append(case, s):
             for m in ("k", "v"):
                 x = new[m][lo - (t - n): hi - (t - n)].transpose(0, 1)
                 amax = x.abs().amax(dim=(1, 2))
-                unit = torch.exp2(torch.ceil(torch.log2(amax / 448.0)).clamp(-60, 60))
+                unit = torch.exp2(torch.ceil(torch.log2(amax / 448.0)).clamp(-48, 48))
                 if lo > j * ps:
                     unit = torch.maximum(unit, scales[m][at])
                     kept = codes[m][at][:, : lo - j * ps] * (scales[m][at] / unit)[:, None, None]
