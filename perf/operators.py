@@ -153,9 +153,11 @@ def _exponent(amax):
 
 
 def _bounds_of(codes):
-    """floor and ceil of 127 / 448 times the codes' values, [..., page, d] -> [..., page, d] each (as floats)."""
+    """floor and ceil of 127 / 448 times the codes' values, [..., page, d] -> [..., page, d] each (as floats).
+
+    On a GPU a division by a number is a product with its rounded reciprocal, which takes 448 to just above 127."""
     t = codes * 127.0 / E4M3_MAX
-    return torch.floor(t), torch.ceil(t)
+    return torch.floor(t).clamp(min=-127.0), torch.ceil(t).clamp(max=127.0)
 
 
 def prepare(case, seed):
