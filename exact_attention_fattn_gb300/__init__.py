@@ -27,3 +27,13 @@ from .attention import (  # noqa: F401
     fattn_set_wait_budget,
     workspace_for,
 )
+from .cache import (  # noqa: F401
+    Fp8Cache,
+    fattn_cache_alloc,
+    fattn_cache_append,
+    fattn_cache_fwd,
+    fattn_cache_fwd_workspace_bytes,
+    fattn_cache_select,
+    fattn_cache_select_workspace_bytes,
+    fattn_rope_table,
+)

@@ -19,9 +19,22 @@ FATTN_ERR_CUDA = 3
 FATTN_ERR_TIMEOUT = 4
 FATTN_ERR_TOO_LARGE = 5
 FATTN_ERR_DEBUG_CHECK = 6
+FATTN_ERR_BAD_INDEX = 7
 NOALLOC_SCRATCH_BYTES = 64 * 1024 * 1024
 
 _c_int, _c_float, _c_size, _vp = ctypes.c_int, ctypes.c_float, ctypes.c_size_t, ctypes.c_void_p
+_c_ll = ctypes.c_longlong
+
+
+class CacheStruct(ctypes.Structure):
+    """fattn_cache of include/fattn.h."""
+
+    _fields_ = [("k", _vp), ("v", _vp), ("k_scale", _vp), ("v_scale", _vp), ("k_bounds", _vp),
+                ("page_stride", _c_ll), ("pages", _c_int), ("Hkv", _c_int), ("page", _c_int),
+                ("d", _c_int)]
+
+
+_cache_p = ctypes.POINTER(CacheStruct)
 
 # name -> (restype, argtypes); the order of argtypes follows include/fattn.h
 SIGNATURES = {
@@ -51,6 +64,15 @@ SIGNATURES = {
                                           ctypes.c_longlong, _vp, _vp]),
     "fattn_bwd_pair_schedule_items": (_c_int, [_c_int, _c_int, _c_int, _c_int, _c_int,
                                                ctypes.c_longlong, _vp, _vp]),
+    "fattn_cache_append": (_c_int, [_cache_p, _vp, _c_ll, _vp, _c_ll, _vp, _c_ll, _vp, _c_int, _vp,
+                                    _c_int, _c_int, _c_int, _vp, _vp, _vp, _c_int, _c_int, _c_int,
+                                    _vp]),
+    "fattn_cache_fwd_workspace_bytes": (_c_size, [_c_int, _c_int, _c_int, _c_int, _c_int, _c_int]),
+    "fattn_cache_fwd": (_c_int, [_cache_p, _vp, _c_ll, _vp, _vp, _vp, _vp, _vp, _vp, _c_int, _vp,
+                                 _c_size, _c_int, _c_int, _c_int, _c_int, _c_int, _c_float, _vp]),
+    "fattn_cache_select_workspace_bytes": (_c_size, [_c_int, _c_int, _c_int]),
+    "fattn_cache_select": (_c_int, [_cache_p, _vp, _c_ll, _vp, _vp, _vp, _vp, _c_int, _c_int,
+                                    _c_int, _vp, _c_size, _c_int, _c_int, _c_int, _c_int, _vp]),
     "fattn_check_status": (_c_int, [_vp]),
     "fattn_status_string": (ctypes.c_char_p, [_c_int]),
     "fattn_set_wait_budget": (None, [ctypes.c_longlong]),

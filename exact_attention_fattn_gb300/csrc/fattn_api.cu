@@ -144,6 +144,30 @@ size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 int from_cuda(cudaError_t e) { return e == cudaSuccess ? FATTN_OK : FATTN_ERR_CUDA; }
 
 }  // namespace
+
+int call_setup(DeviceStatus** status, long long* wait_budget) {
+  const int rc = device_setup(status);
+  if (rc != FATTN_OK) return rc;
+  std::lock_guard<std::mutex> lock(g_mu);
+  *wait_budget = g_budget;
+  return FATTN_OK;
+}
+
+int make_rows_map_u8(CUtensorMap* m, const void* ptr, int inner, long long rows, int slabs,
+                     long long slab_stride, int box_rows) {
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(inner), static_cast<cuuint64_t>(rows),
+                              static_cast<cuuint64_t>(slabs)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(inner),
+                                 static_cast<cuuint64_t>(slab_stride)};
+  const cuuint32_t box[3] = {static_cast<cuuint32_t>(inner), static_cast<cuuint32_t>(box_rows), 1u};
+  const cuuint32_t estr[3] = {1u, 1u, 1u};
+  CUresult r = g_encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(ptr), dims,
+                        strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                        inner == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? FATTN_OK : FATTN_ERR_CUDA;
+}
+
 }  // namespace fattn
 
 using namespace fattn;
@@ -586,6 +610,7 @@ const char* fattn_status_string(int status) {
     case FATTN_ERR_TIMEOUT: return "kernel wait timed out";
     case FATTN_ERR_TOO_LARGE: return "problem exceeds the built-in scratch of fattn_bwd_noalloc";
     case FATTN_ERR_DEBUG_CHECK: return "a debug-build range check failed in a kernel";
+    case FATTN_ERR_BAD_INDEX: return "a sequence start, length or page number is out of range";
     default: return "unknown status";
   }
 }

@@ -1,0 +1,91 @@
+// Shared by the kernels of the paged 8-bit cache: the cache's layout, the
+// ragged batch that a call works on, and the checks of what the host cannot
+// see (sequence starts, lengths and page numbers live on the device).
+#pragma once
+
+#include "fattn_internal.h"
+#include "fattn_ptx.cuh"
+
+namespace fattn {
+
+constexpr unsigned int kStatusBadIndex = 7;  // == FATTN_ERR_BAD_INDEX
+
+// What a kernel found out of range (DeviceStatus::where).
+enum CacheSite : unsigned int {
+  kSiteSeqStart = 401,   // q_start not ascending inside [0, T], or kv_len outside its page table
+  kSitePage = 402,       // a page number outside the cache
+  kSitePosition = 403,   // a new token before position 0 or past the rotation table
+  kSiteSelected = 404,   // a selected page outside the page table
+};
+
+__device__ __forceinline__ void record_bad_index(DeviceStatus* st, unsigned int site) {
+  if (atomicCAS(&st->code, 0u, kStatusBadIndex) == 0u) {
+    st->where = site;
+    st->block = blockIdx.x + gridDim.x * (blockIdx.y + gridDim.y * blockIdx.z);
+  }
+}
+
+// One sequence of a call: its rows [r0, r0 + n) and its cached tokens.  A
+// sequence whose numbers make no sense is empty (n = len = 0), !ok.
+struct SeqInfo {
+  int r0, n, len;
+  bool ok;
+};
+
+__device__ __forceinline__ SeqInfo seq_info(const CacheSeqs& s, int b, int page_shift) {
+  SeqInfo q;
+  q.r0 = __ldg(s.q_start + b);
+  const int r1 = __ldg(s.q_start + b + 1);
+  q.len = __ldg(s.kv_len + b);
+  q.ok = q.r0 >= 0 && r1 >= q.r0 && r1 <= s.T && q.len >= 0 &&
+         q.len <= (static_cast<long long>(s.max_pages) << page_shift);
+  q.n = q.ok ? r1 - q.r0 : 0;
+  if (!q.ok) q.len = 0;
+  return q;
+}
+
+// The largest b in [0, B) with f(b) <= x, f ascending, found by a whole warp
+// 32 values at a time (one round of loads up to 32 sequences, two up to 1024).
+// Any b in [0, B) when f is not ascending or f(0) > x.
+template <class F>
+__device__ __forceinline__ int find_last_warp(int B, int x, F f) {
+  const int lane = threadIdx.x & 31;
+  int lo = 0, n = B;
+  while (n > 1) {
+    const int step = (n + 31) / 32;
+    const int off = lane * step;
+    const bool le = off < n && f(lo + off) <= x;
+    const unsigned int m = __ballot_sync(0xffffffffu, le);
+    const int last = m ? 31 - __clz(m) : 0;
+    lo += last * step;
+    n = min(step, n - last * step);
+  }
+  return lo;
+}
+
+// 2^e as fp32, e in [-126, 127].
+__device__ __forceinline__ float exp2i(int e) { return __int_as_float((e + 127) << 23); }
+
+// Exponents of the cache's scales: a scale is 2^e, kScaleExpMin <= e <= kScaleExpMax.
+constexpr int kScaleExpMin = -48;
+constexpr int kScaleExpMax = 48;
+
+// log2 of a scale, whatever the memory holds: the exponent field, clamped.
+__device__ __forceinline__ int scale_exp(float s) {
+  const int e = static_cast<int>((__float_as_uint(s) >> 23) & 0xffu) - 127;
+  return max(kScaleExpMin, min(kScaleExpMax, e));
+}
+
+// Two e4m3 codes (low 16 bits) -> two halves, exactly.
+__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t codes) {
+  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(codes & 0xffffu),
+                                                   __NV_E4M3);
+  return static_cast<uint32_t>(h.x) | (static_cast<uint32_t>(h.y) << 16);
+}
+
+__device__ __forceinline__ float2 e4m3x2_to_f32x2(uint32_t codes) {
+  const uint32_t h = e4m3x2_to_f16x2(codes);
+  return __half22float2(*reinterpret_cast<const __half2*>(&h));
+}
+
+}  // namespace fattn

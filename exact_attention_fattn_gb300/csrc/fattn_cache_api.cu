@@ -1,0 +1,283 @@
+// C-ABI boundary of the paged 8-bit cache: argument checks, tensor maps,
+// workspace layout and the choice of kernel.  See include/fattn.h.
+#include <math.h>
+#include <stdint.h>
+
+#include <nvtx3/nvToolsExt.h>
+
+#include "../../include/fattn.h"
+#include "fattn_internal.h"
+
+namespace fattn {
+namespace {
+
+struct NvtxScope {
+  explicit NvtxScope(const char* name) { nvtxRangePushA(name); }
+  ~NvtxScope() { nvtxRangePop(); }
+  NvtxScope(const NvtxScope&) = delete;
+  NvtxScope& operator=(const NvtxScope&) = delete;
+};
+
+bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
+constexpr int kMaxSeqs = 4096;
+constexpr int kMaxKvHeads = 1024;
+constexpr int kMaxGroup = 128;
+
+int check_cache(const fattn_cache* c) {
+  if (!c) return FATTN_ERR_INVALID_ARG;
+  if (c->d != 64 && c->d != 128) return FATTN_ERR_UNSUPPORTED;
+  if (c->page != 32 && c->page != 64 && c->page != 128) return FATTN_ERR_UNSUPPORTED;
+  if (c->pages <= 0 || c->Hkv <= 0 || c->Hkv > kMaxKvHeads) return FATTN_ERR_INVALID_ARG;
+  if (!c->k || !c->v || !c->k_scale || !c->v_scale) return FATTN_ERR_INVALID_ARG;
+  if (!aligned(c->k, 16) || !aligned(c->v, 16) || !aligned(c->k_scale, 4) ||
+      !aligned(c->v_scale, 4) || !aligned(c->k_bounds, 16))
+    return FATTN_ERR_INVALID_ARG;
+  const long long least = static_cast<long long>(c->Hkv) * c->page * c->d;
+  if (c->page_stride < least || c->page_stride % 16 != 0 || c->page_stride >= (1ll << 40))
+    return FATTN_ERR_INVALID_ARG;
+  return FATTN_OK;
+}
+
+int check_batch(const fattn_cache* c, const int* page_table, const int* q_start, const int* kv_len,
+                int T, int B, int max_pages) {
+  if (!page_table || !q_start || !kv_len) return FATTN_ERR_INVALID_ARG;
+  if (!aligned(page_table, 4) || !aligned(q_start, 4) || !aligned(kv_len, 4))
+    return FATTN_ERR_INVALID_ARG;
+  if (T <= 0 || B <= 0 || B > kMaxSeqs || max_pages <= 0) return FATTN_ERR_INVALID_ARG;
+  if (static_cast<long long>(max_pages) * c->page > 0x7fff0000ll) return FATTN_ERR_INVALID_ARG;
+  return FATTN_OK;
+}
+
+int check_heads(const fattn_cache* c, int T, int Hq) {
+  if (Hq <= 0 || Hq % c->Hkv != 0 || Hq / c->Hkv > kMaxGroup) return FATTN_ERR_INVALID_ARG;
+  if (static_cast<long long>(T) * Hq > 0x7fffffffll) return FATTN_ERR_INVALID_ARG;
+  return FATTN_OK;
+}
+
+int check_rows(const void* p, long long row, long long least) {
+  if (!p || !aligned(p, 16) || row < least || row % 8 != 0) return FATTN_ERR_INVALID_ARG;
+  return FATTN_OK;
+}
+
+int page_shift(int page) { return page == 32 ? 5 : (page == 64 ? 6 : 7); }
+
+CacheSeqs seqs_of(const int* page_table, const int* q_start, const int* kv_len, int T, int B,
+                  int max_pages) {
+  CacheSeqs s;
+  s.q_start = q_start;
+  s.kv_len = kv_len;
+  s.table = page_table;
+  s.T = T;
+  s.B = B;
+  s.max_pages = max_pages;
+  return s;
+}
+
+size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
+
+// Partial results of the units that CTAs share: two per CTA.
+struct AttnWorkspace {
+  size_t o_off, ml_off, rec_off, total;
+};
+
+AttnWorkspace attn_workspace(int rows, int d) {
+  AttnWorkspace w;
+  const size_t slots = 2 * static_cast<size_t>(kCacheMaxCtas) * rows;
+  w.o_off = 0;
+  w.ml_off = align256(slots * d * sizeof(float));
+  w.rec_off = w.ml_off + align256(slots * sizeof(float2));
+  w.total = w.rec_off + align256(2 * kCacheMaxCtas * sizeof(int4));
+  return w;
+}
+
+}  // namespace
+}  // namespace fattn
+
+using namespace fattn;
+
+extern "C" {
+
+int fattn_cache_append(const fattn_cache* cache, const void* k_new, long long k_row,
+                       const void* v_new, long long v_row, const void* q, long long q_row,
+                       void* q_out, int Hq, const float* rope, int rope_len, int rope_dim,
+                       int interleaved, const int* page_table, const int* q_start,
+                       const int* kv_len, int T, int B, int max_pages, fattn_stream_t stream) {
+  const NvtxScope nvtx_range("fattn_cache_append");
+  int rc = check_cache(cache);
+  if (rc != FATTN_OK) return rc;
+  if ((rc = check_batch(cache, page_table, q_start, kv_len, T, B, max_pages)) != FATTN_OK) return rc;
+  const long long kv_least = static_cast<long long>(cache->Hkv) * cache->d;
+  if ((rc = check_rows(k_new, k_row, kv_least)) != FATTN_OK) return rc;
+  if ((rc = check_rows(v_new, v_row, kv_least)) != FATTN_OK) return rc;
+  if ((q == nullptr) != (q_out == nullptr)) return FATTN_ERR_INVALID_ARG;
+  if (q) {
+    if ((rc = check_heads(cache, T, Hq)) != FATTN_OK) return rc;
+    const long long q_least = static_cast<long long>(Hq) * cache->d;
+    if ((rc = check_rows(q, q_row, q_least)) != FATTN_OK) return rc;
+    if (!aligned(q_out, 16) || (q_out == q && q_row != q_least)) return FATTN_ERR_INVALID_ARG;
+  }
+  if (rope) {
+    if (!aligned(rope, 16) || rope_len <= 0 || rope_dim <= 0 || rope_dim > cache->d ||
+        rope_dim % 16 != 0)
+      return FATTN_ERR_INVALID_ARG;
+  } else if (rope_dim != 0) {
+    return FATTN_ERR_INVALID_ARG;
+  }
+  const long long blocks =
+      (T / cache->page + 2ll * B) * cache->Hkv + (q ? static_cast<long long>(T) : 0);
+  if (blocks > 0x7fffffffll) return FATTN_ERR_INVALID_ARG;
+  CacheAppendArgs a{};
+  long long budget = 0;
+  if ((rc = call_setup(&a.status, &budget)) != FATTN_OK) return rc;
+  a.s = seqs_of(page_table, q_start, kv_len, T, B, max_pages);
+  a.k = static_cast<uint8_t*>(cache->k);
+  a.v = static_cast<uint8_t*>(cache->v);
+  a.k_scale = cache->k_scale;
+  a.v_scale = cache->v_scale;
+  a.bounds = static_cast<int8_t*>(cache->k_bounds);
+  a.page_stride = cache->page_stride;
+  a.pages = cache->pages;
+  a.Hkv = cache->Hkv;
+  a.k_new = static_cast<const uint16_t*>(k_new);
+  a.v_new = static_cast<const uint16_t*>(v_new);
+  a.q = static_cast<const uint16_t*>(q);
+  a.q_out = static_cast<uint16_t*>(q_out);
+  a.k_row = k_row;
+  a.v_row = v_row;
+  a.q_row = q_row;
+  a.Hq = q ? Hq : 0;
+  a.rope = rope;
+  a.rope_len = rope_len;
+  a.rope_dim = rope_dim;
+  a.interleaved = interleaved != 0;
+  return launch_cache_append(cache->page, cache->d, a, reinterpret_cast<cudaStream_t>(stream)) ==
+                 cudaSuccess
+             ? FATTN_OK
+             : FATTN_ERR_CUDA;
+}
+
+size_t fattn_cache_fwd_workspace_bytes(int T, int B, int Hq, int Hkv, int d, int n_selected) {
+  if (T <= 0 || B <= 0 || B > kMaxSeqs || Hkv <= 0 || Hkv > kMaxKvHeads || Hq <= 0 ||
+      Hq % Hkv != 0 || Hq / Hkv > kMaxGroup || (d != 64 && d != 128) || n_selected < 0)
+    return 0;
+  return attn_workspace(kDecodeRows, d).total;
+}
+
+int fattn_cache_fwd(const fattn_cache* cache, const void* q, long long q_row, void* o, float* lse,
+                    const int* page_table, const int* q_start, const int* kv_len,
+                    const int* selected, int n_selected, void* workspace, size_t workspace_bytes,
+                    int T, int B, int Hq, int max_pages, int causal, float scale,
+                    fattn_stream_t stream) {
+  const NvtxScope nvtx_range("fattn_cache_fwd");
+  int rc = check_cache(cache);
+  if (rc != FATTN_OK) return rc;
+  if ((rc = check_batch(cache, page_table, q_start, kv_len, T, B, max_pages)) != FATTN_OK) return rc;
+  if ((rc = check_heads(cache, T, Hq)) != FATTN_OK) return rc;
+  if ((rc = check_rows(q, q_row, static_cast<long long>(Hq) * cache->d)) != FATTN_OK) return rc;
+  if (!o || !aligned(o, 16) || !lse || !aligned(lse, 4)) return FATTN_ERR_INVALID_ARG;
+  if ((selected == nullptr) != (n_selected == 0) || n_selected < 0 || !aligned(selected, 4))
+    return FATTN_ERR_INVALID_ARG;
+  if (static_cast<long long>(n_selected) * cache->page > 0x7fff0000ll) return FATTN_ERR_INVALID_ARG;
+  if (!isfinite(scale) || !(scale > 0.f)) return FATTN_ERR_INVALID_ARG;
+  if (!workspace || !aligned(workspace, 256) ||
+      workspace_bytes < fattn_cache_fwd_workspace_bytes(T, B, Hq, cache->Hkv, cache->d, n_selected))
+    return FATTN_ERR_INVALID_ARG;
+  CacheAttnArgs a{};
+  if ((rc = call_setup(&a.status, &a.wait_budget)) != FATTN_OK) return rc;
+  a.s = seqs_of(page_table, q_start, kv_len, T, B, max_pages);
+  a.q = static_cast<const uint16_t*>(q);
+  a.q_row = q_row;
+  a.o = static_cast<uint16_t*>(o);
+  a.lse = lse;
+  a.k_scale = cache->k_scale;
+  a.v_scale = cache->v_scale;
+  a.selected = selected;
+  a.n_selected = n_selected;
+  a.pages = cache->pages;
+  a.Hkv = cache->Hkv;
+  a.group = Hq / cache->Hkv;
+  a.page_shift = page_shift(cache->page);
+  a.causal = causal != 0;
+  a.scale_log2 = scale * 1.4426950408889634f;
+  const AttnWorkspace w = attn_workspace(kDecodeRows, cache->d);
+  char* base = static_cast<char*>(workspace);
+  a.part_o = reinterpret_cast<float*>(base + w.o_off);
+  a.part_ml = reinterpret_cast<float2*>(base + w.ml_off);
+  a.rec = reinterpret_cast<int4*>(base + w.rec_off);
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return FATTN_ERR_CUDA;
+  const int max_ctas = sms < kCacheMaxCtas ? sms : kCacheMaxCtas;
+  // 256-key chunks of all units, at most (the lengths are on the device)
+  const long long keys = selected ? static_cast<long long>(n_selected) * cache->page
+                                  : static_cast<long long>(max_pages) * cache->page;
+  const long long units =
+      selected ? static_cast<long long>(T) * cache->Hkv * ((a.group + kDecodeRows - 1) / kDecodeRows)
+               : (static_cast<long long>(T) * a.group / kDecodeRows + B) * cache->Hkv;
+  const long long per = (keys + 255) / 256;
+  if (units > (1ll << 38) / per) return FATTN_ERR_TOO_LARGE;
+  const long long chunks = units * per;
+  a.grid = chunks < max_ctas ? static_cast<int>(chunks) : max_ctas;
+  CUtensorMap tk, tv;
+  const long long rows = static_cast<long long>(cache->Hkv) * cache->page;
+  if ((rc = make_rows_map_u8(&tk, cache->k, cache->d, rows, cache->pages, cache->page_stride, 32)) !=
+          FATTN_OK ||
+      (rc = make_rows_map_u8(&tv, cache->v, cache->d, rows, cache->pages, cache->page_stride, 32)) !=
+          FATTN_OK)
+    return rc;
+  return launch_cache_decode(cache->d, tk, tv, a, reinterpret_cast<cudaStream_t>(stream)) ==
+                 cudaSuccess
+             ? FATTN_OK
+             : FATTN_ERR_CUDA;
+}
+
+size_t fattn_cache_select_workspace_bytes(int T, int Hkv, int max_pages) {
+  if (T <= 0 || Hkv <= 0 || Hkv > kMaxKvHeads || max_pages <= 0) return 0;
+  return align256(static_cast<size_t>(T) * Hkv * max_pages * sizeof(float));
+}
+
+int fattn_cache_select(const fattn_cache* cache, const void* q, long long q_row,
+                       const int* page_table, const int* q_start, const int* kv_len,
+                       int* selected, int n_selected, int n_first, int n_recent, void* workspace,
+                       size_t workspace_bytes, int T, int B, int Hq, int max_pages,
+                       fattn_stream_t stream) {
+  const NvtxScope nvtx_range("fattn_cache_select");
+  int rc = check_cache(cache);
+  if (rc != FATTN_OK) return rc;
+  if (!cache->k_bounds) return FATTN_ERR_INVALID_ARG;
+  if ((rc = check_batch(cache, page_table, q_start, kv_len, T, B, max_pages)) != FATTN_OK) return rc;
+  if ((rc = check_heads(cache, T, Hq)) != FATTN_OK) return rc;
+  if ((rc = check_rows(q, q_row, static_cast<long long>(Hq) * cache->d)) != FATTN_OK) return rc;
+  if (!selected || !aligned(selected, 4) || n_selected <= 0 || n_first < 0 || n_recent < 0 ||
+      static_cast<long long>(n_first) + n_recent > n_selected)
+    return FATTN_ERR_INVALID_ARG;
+  if (static_cast<long long>(T) * cache->Hkv * n_selected > (1ll << 40)) return FATTN_ERR_INVALID_ARG;
+  if (max_pages > 65535 * 128) return FATTN_ERR_INVALID_ARG;   // the grid's third extent
+  if (!workspace || !aligned(workspace, 256) ||
+      workspace_bytes < fattn_cache_select_workspace_bytes(T, cache->Hkv, max_pages))
+    return FATTN_ERR_INVALID_ARG;
+  CacheSelectArgs a{};
+  long long budget = 0;
+  if ((rc = call_setup(&a.status, &budget)) != FATTN_OK) return rc;
+  a.s = seqs_of(page_table, q_start, kv_len, T, B, max_pages);
+  a.q = static_cast<const uint16_t*>(q);
+  a.q_row = q_row;
+  a.k_scale = cache->k_scale;
+  a.bounds = static_cast<const int8_t*>(cache->k_bounds);
+  a.pages = cache->pages;
+  a.Hkv = cache->Hkv;
+  a.group = Hq / cache->Hkv;
+  a.page_shift = page_shift(cache->page);
+  a.scores = static_cast<float*>(workspace);
+  a.selected = selected;
+  a.n_selected = n_selected;
+  a.n_first = n_first;
+  a.n_recent = n_recent;
+  return launch_cache_select(cache->d, a, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? FATTN_OK
+             : FATTN_ERR_CUDA;
+}
+
+}  // extern "C"

@@ -1,0 +1,699 @@
+// Attention over the paged 8-bit cache for few query rows per sequence
+// (single tokens, short drafts).
+//
+// The rows of a unit -- up to 16 (token, query head) pairs of one sequence
+// that share a kv head -- meet every cached key of that head once, so the
+// call is bound by reading the cache, 2 d bytes a token and kv head.  With
+// 16 rows or fewer a 128-row tcgen05 tile would be mostly padding; the
+// products go to mma.sync m16n8k16, whose rate (about a quarter of tcgen05's)
+// is several times what the memory can feed.
+//
+// Codes become halves in registers: an e4m3 value is exact in fp16.  Queries
+// are scaled by a power of two per row into fp16's range, exactly unless an
+// entry is 2^-14 below its row's largest; probabilities are rounded to fp16
+// (11 bits) for P V and summed in fp32 unrounded.
+//
+// Softmax with the value scales inside: with sv_p the value scale of page p
+// and l_p its log2,
+//   x_j = s_j + l_p(j),  m = running max of x,  P'_j = 2^(x_j - m),
+//   O = sum P'_j V8_j,   l = sum_p 2^(-l_p) sum_{j in p} P'_j,
+// so O / l is the result and m + log2 l the log-sum-exp, with one exponential
+// per score and no product by the scales left over; |l_p| <= 48 keeps the sum
+// in range.
+//
+// Work split: a unit's keys are cut into chunks of 256 and the chunks of all
+// units, in order, are dealt to the CTAs in equal contiguous shares, so
+// lengths may differ by any factor.  A CTA's 8 warps take 32 keys of each
+// chunk, each with its own softmax state and its own ring of TMA tiles (no
+// barrier inside a chunk), and are joined through shared memory when the
+// CTA's part of the unit ends.  A unit that several CTAs share is joined from
+// their partial results in a second kernel, in order, so results do not
+// depend on timing.
+#include <cuda_fp16.h>
+
+#include "fattn_cache.cuh"
+
+namespace fattn {
+
+namespace {
+
+constexpr int kWarps = 8;
+constexpr int kThreads = kWarps * 32;
+constexpr int kRows = kDecodeRows;
+constexpr int kTileKeys = 32;                       // keys a warp takes of a chunk
+constexpr int kChunkKeys = kWarps * kTileKeys;
+constexpr float kLn2 = 0.69314718055994530942f;
+
+template <int D>
+struct DecCfg {
+  static constexpr int kTileBytes = kTileKeys * D;  // K or V of a tile
+  static constexpr int kStages = 2;
+  static constexpr int kStageBytes = 2 * kTileBytes;
+  static constexpr int kRingBytes = kWarps * kStages * kStageBytes;
+  static constexpr int kJoinOff = kRingBytes;       // [kWarps][kRows][D] fp32
+  static constexpr int kMlOff = kJoinOff + kWarps * kRows * D * 4;    // [kWarps][kRows] float2
+  static constexpr int kBarOff = kMlOff + kWarps * kRows * 8;
+  static constexpr int kMiscOff = kBarOff + kWarps * kStages * 8;
+  static constexpr int kPreOff = kMiscOff + 128;    // [B + 1] long long
+  static constexpr int kSmemFixed = kPreOff + 1024;
+};
+
+__device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
+                                        uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint2 ld_shared_v2(uint32_t addr) {
+  uint2 v;
+  asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr) : "memory");
+  return v;
+}
+
+__device__ __forceinline__ uint32_t pack_f16x2(float a, float b) {
+  const __half2 h = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// A unit: rows [16 rb, ..) of a sequence's n * group rows, one kv head.
+// Sparse calls take each token as a sequence of its own (r0 = token, n = 1).
+struct Unit {
+  int seq;            // sequence, sparse: token
+  int rb, head;
+  int r0, n;          // rows of the call
+  int pos0;           // position of row r0
+  int len;            // keys that exist
+  int table_row;      // row of the page table
+  long long c0;       // first chunk
+  int chunks;
+};
+
+// Chunks of the whole call, and the unit of a chunk.  pre: dense calls only,
+// chunks before each sequence (shared memory, [B + 1]).
+struct Schedule {
+  const CacheAttnArgs* a;
+  const long long* pre;
+  int sparse_chunks;      // chunks of every sparse unit
+  int sparse_blocks;      // row blocks of a token's group
+
+  __device__ __forceinline__ long long total() const {
+    if (a->selected != nullptr)
+      return static_cast<long long>(a->s.T) * a->Hkv * sparse_blocks * sparse_chunks;
+    return pre[a->s.B];
+  }
+  __device__ __forceinline__ Unit unit_of(long long j) const {
+    Unit u;
+    if (a->selected != nullptr) {
+      const long long id = j / sparse_chunks;
+      u.c0 = id * sparse_chunks;
+      u.chunks = sparse_chunks;
+      const long long hb = id / a->Hkv;
+      u.head = static_cast<int>(id - hb * a->Hkv);
+      u.rb = static_cast<int>(hb % sparse_blocks);
+      u.seq = static_cast<int>(hb / sparse_blocks);
+      u.r0 = u.seq;
+      u.n = 0;
+      u.pos0 = u.len = u.table_row = 0;
+      return u;   // its sequence is looked up by finish()
+    }
+    int lo = 0, hi = a->s.B;   // the last b with pre[b] <= j
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (pre[mid] <= j) lo = mid; else hi = mid;
+    }
+    const SeqInfo q = seq_info(a->s, lo, a->page_shift);
+    u.seq = u.table_row = lo;
+    u.r0 = q.r0;
+    u.n = q.n;
+    u.len = q.len;
+    u.pos0 = q.len - q.n;
+    u.chunks = (q.len + kChunkKeys - 1) / kChunkKeys;
+    const int id = static_cast<int>((j - pre[lo]) / u.chunks);
+    u.c0 = pre[lo] + static_cast<long long>(id) * u.chunks;
+    u.rb = id / a->Hkv;
+    u.head = id - u.rb * a->Hkv;
+    return u;
+  }
+  // The sequence of a sparse unit's token: a guess that holds where all
+  // sequences have the same number of rows, else a search.
+  __device__ __forceinline__ void finish(Unit& u) const {
+    if (a->selected == nullptr) return;
+    const int* qs = a->s.q_start;
+    int b = static_cast<int>(static_cast<long long>(u.r0) * a->s.B / a->s.T);
+    if (u.r0 < __ldg(qs + b) || u.r0 >= __ldg(qs + b + 1)) {
+      b = 0;
+      for (int hi = a->s.B; hi - b > 1;) {
+        const int mid = (b + hi) >> 1;
+        if (__ldg(qs + mid) <= u.r0) b = mid; else hi = mid;
+      }
+    }
+    const SeqInfo q = seq_info(a->s, b, a->page_shift);
+    if (!q.ok) record_bad_index(a->status, kSiteSeqStart);
+    u.table_row = b;
+    if (u.r0 < q.r0 || u.r0 >= q.r0 + q.n) {
+      u.n = 0;     // a row behind the last sequence
+      u.len = u.pos0 = 0;
+      return;
+    }
+    u.n = 1;
+    u.pos0 = q.len - q.n + (u.r0 - q.r0);
+    u.len = a->causal ? max(0, min(q.len, u.pos0 + 1)) : q.len;
+  }
+};
+
+// First chunk of CTA c of G over W chunks, and the CTA of chunk j.
+__device__ __forceinline__ long long cta_first(long long W, int G, int c) { return W * c / G; }
+__device__ __forceinline__ int cta_of(long long W, int G, long long j) {
+  return static_cast<int>(((j + 1) * G - 1) / W);
+}
+
+// One tile of a warp, as lane i of a batch of 32 looks it up.
+struct Tile {
+  int pid;        // page, or -1: nothing to read
+  int y;          // row of the page's [Hkv * page] rows
+  int key0;       // position of its first key
+  float ks;       // K scale
+  float lv;       // log2 of the V scale
+};
+
+__device__ __forceinline__ Tile shfl_tile(const Tile& t, int src) {
+  Tile r;
+  r.pid = __shfl_sync(0xffffffffu, t.pid, src);
+  r.y = __shfl_sync(0xffffffffu, t.y, src);
+  r.key0 = __shfl_sync(0xffffffffu, t.key0, src);
+  r.ks = __shfl_sync(0xffffffffu, t.ks, src);
+  r.lv = __shfl_sync(0xffffffffu, t.lv, src);
+  return r;
+}
+
+template <int D, bool SPARSE>
+__global__ void __launch_bounds__(kThreads, 1)
+    decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                  const CacheAttnArgs a) {
+  using C = DecCfg<D>;
+  constexpr int kK = D / 16;            // k steps of Q K^T
+  constexpr int kVals = D / 4;          // consecutive columns of O a thread holds per row
+  constexpr int kTiles8 = kVals / 2;    // n8 tiles of P V
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  const uint32_t sbase = smem_u32(smem);
+  float* join = reinterpret_cast<float*>(smem + C::kJoinOff);
+  float2* ml = reinterpret_cast<float2*>(smem + C::kMlOff);
+  uint32_t* misc = reinterpret_cast<uint32_t*>(smem + C::kMiscOff);
+  long long* pre = reinterpret_cast<long long*>(smem + C::kPreOff);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int r = lane >> 2, c = lane & 3;
+  const uint32_t ring = sbase + warp * C::kStages * C::kStageBytes;
+  const uint32_t bar0 = sbase + C::kBarOff + warp * C::kStages * 8;
+  const int G = a.grid, cta = blockIdx.x;
+
+  if (lane == 0) {
+    for (int s = 0; s < C::kStages; ++s) mbar_init(bar0 + 8 * s, 1);
+    tma_prefetch_desc(&tm_k);
+    tma_prefetch_desc(&tm_v);
+  }
+  if (tid == 0) misc[0] = 0u;
+  fence_barrier_init();
+
+  // ---- chunks before each sequence
+  if constexpr (!SPARSE) {
+    const int per = (a.s.B + kThreads - 1) / kThreads;
+    const int b0 = min(a.s.B, tid * per), b1 = min(a.s.B, b0 + per);
+    long long sum = 0;
+    for (int b = b0; b < b1; ++b) {
+      const SeqInfo q = seq_info(a.s, b, a.page_shift);
+      if (!q.ok && cta == 0) record_bad_index(a.status, kSiteSeqStart);
+      const long long blocks = (static_cast<long long>(q.n) * a.group + kRows - 1) / kRows;
+      sum += blocks * a.Hkv * ((q.len + kChunkKeys - 1) / kChunkKeys);
+    }
+    long long incl = sum;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const long long t = __shfl_up_sync(0xffffffffu, incl, off);
+      if (lane >= off) incl += t;
+    }
+    long long* wtot = reinterpret_cast<long long*>(ml);
+    if (lane == 31) wtot[warp] = incl;
+    __syncthreads();
+    long long at = incl - sum;
+    for (int w = 0; w < warp; ++w) at += wtot[w];
+    for (int b = b0; b < b1; ++b) {
+      pre[b] = at;
+      const SeqInfo q = seq_info(a.s, b, a.page_shift);
+      const long long blocks = (static_cast<long long>(q.n) * a.group + kRows - 1) / kRows;
+      at += blocks * a.Hkv * ((q.len + kChunkKeys - 1) / kChunkKeys);
+      // Rows of a sequence with no keys at all see nothing.
+      if (q.len == 0 && q.n > 0 && b % G == cta) {
+        const long long cnt = static_cast<long long>(q.n) * a.Hkv * a.group;
+        uint4* o = reinterpret_cast<uint4*>(a.o + static_cast<long long>(q.r0) * a.Hkv * a.group * D);
+        for (long long i = 0; i < cnt * (D / 8); ++i) o[i] = make_uint4(0u, 0u, 0u, 0u);
+        float* l = a.lse + static_cast<long long>(q.r0) * a.Hkv * a.group;
+        for (long long i = 0; i < cnt; ++i) l[i] = -INFINITY;
+      }
+    }
+    if (tid == kThreads - 1) pre[a.s.B] = at;
+  }
+  __syncthreads();
+
+  const Schedule sched{&a, pre, SPARSE ? ((a.n_selected << a.page_shift) + kChunkKeys - 1) / kChunkKeys : 0,
+                       (a.group + kRows - 1) / kRows};
+  const long long W = sched.total();
+  const long long j0 = cta_first(W, G, cta), j1 = cta_first(W, G, cta + 1);
+  const int n_tiles = static_cast<int>(j1 - j0);   // of this warp, and of every other
+  const WaitCtx wc{a.wait_budget, reinterpret_cast<volatile uint32_t*>(&misc[0]), a.status};
+
+  // The tiles of chunks j0 + 32 k .. + 31, one per lane.
+  auto look_up = [&](int k) -> Tile {
+    Tile t{-1, 0, 0, 0.f, 0.f};
+    const int i = 32 * k + lane;
+    Unit u{};
+    if (i < n_tiles) u = sched.unit_of(j0 + i);
+    if (i < n_tiles) sched.finish(u);
+    if (i >= n_tiles || u.n == 0) return t;
+    const int at = static_cast<int>(j0 + i - u.c0) * kChunkKeys + warp * kTileKeys;
+    const int page = 1 << a.page_shift;
+    int entry = at >> a.page_shift;
+    const int off = at & (page - 1);
+    if constexpr (SPARSE) {
+      if (entry >= a.n_selected) return t;
+      entry = __ldg(a.selected + (static_cast<long long>(u.seq) * a.Hkv + u.head) * a.n_selected + entry);
+      if (entry < 0) return t;
+      if (entry >= a.s.max_pages) {
+        record_bad_index(a.status, kSiteSelected);
+        return t;
+      }
+    }
+    const long long key0 = (static_cast<long long>(entry) << a.page_shift) + off;
+    if (key0 >= u.len) return t;
+    const int pid = __ldg(a.s.table + static_cast<long long>(u.table_row) * a.s.max_pages + entry);
+    if (pid < 0 || pid >= a.pages) {
+      record_bad_index(a.status, kSitePage);
+      return t;
+    }
+    t.pid = pid;
+    t.y = u.head * page + off;
+    t.key0 = static_cast<int>(key0);
+    const long long sc = static_cast<long long>(pid) * a.Hkv + u.head;
+    t.ks = __ldg(a.k_scale + sc);
+    t.lv = static_cast<float>(scale_exp(__ldg(a.v_scale + sc)));
+    return t;
+  };
+  auto issue = [&](const Tile& t, int stage) {   // converged warp
+    if (t.pid < 0) return;
+    const uint32_t dst = ring + stage * C::kStageBytes;
+    mbar_arrive_expect_tx_w(bar0 + 8 * stage, C::kStageBytes);
+    tma_load_3d_w(dst, &tm_k, bar0 + 8 * stage, 0, t.y, t.pid);
+    tma_load_3d_w(dst + C::kTileBytes, &tm_v, bar0 + 8 * stage, 0, t.y, t.pid);
+  };
+
+  Tile cur = look_up(0), next = cur;
+  if (n_tiles > 32) next = look_up(1);
+  int pending = 0;                                  // stages with a copy in flight, one bit each
+#pragma unroll
+  for (int s = 0; s < C::kStages; ++s) {
+    if (s < n_tiles) {
+      const Tile t = shfl_tile(cur, s);
+      issue(t, s);
+      if (t.pid >= 0) pending |= 1 << s;
+    }
+  }
+  uint32_t phases = 0u;                             // parity of each stage's next completion
+  bool ok = true;
+  bool shared_unit = false;                         // thread 0: this CTA's last unit goes on
+
+  int i = 0;                                        // tile of this warp
+  while (i < n_tiles) {
+    // ---- the CTA's part of one unit: chunks [j0 + i, j0 + end)
+    Unit u = sched.unit_of(j0 + i);
+    sched.finish(u);
+    const int end = static_cast<int>(min(j1, u.c0 + u.chunks) - j0);
+    const bool starts = j0 + i == u.c0, ends = j0 + end == u.c0 + u.chunks;
+    const bool whole = starts && ends;
+    // A CTA shares at most two units: the one it starts inside (slot 0) and
+    // the one that goes on after it (slot 1).
+    const int slot = starts ? 1 : 0;
+
+    // Queries as fp16 A fragments: row r or r + 8, columns kVals * c ...
+    // (a k step's four columns of a thread are consecutive in memory).
+    uint32_t qa[kK][4];
+    float cs[2];                                    // log2(e) * scale, the row's power of two in it
+    int lim[2];                                     // keys the row sees
+#pragma unroll
+    for (int hh = 0; hh < 2; ++hh) {
+      const int rr = u.rb * kRows + r + 8 * hh;
+      const bool on = rr < u.n * a.group;
+      const int token = on ? rr / a.group : 0;
+      lim[hh] = on ? (a.causal ? max(0, min(u.len, u.pos0 + token + 1)) : u.len) : 0;
+      uint32_t w[D / 8];
+#pragma unroll
+      for (int q = 0; q < D / 8; ++q) w[q] = 0u;
+      if (on) {
+        const uint4* p = reinterpret_cast<const uint4*>(
+            a.q + (u.r0 + token) * a.q_row +
+            (static_cast<long long>(u.head) * a.group + rr - token * a.group) * D + kVals * c);
+#pragma unroll
+        for (int q = 0; q < D / 32; ++q) {
+          const uint4 x = __ldg(p + q);
+          w[4 * q] = x.x;
+          w[4 * q + 1] = x.y;
+          w[4 * q + 2] = x.z;
+          w[4 * q + 3] = x.w;
+        }
+      }
+      uint32_t mx = 0u;                             // largest exponent field of the row
+#pragma unroll
+      for (int q = 0; q < D / 8; ++q) mx = max(mx, max((w[q] >> 7) & 0xffu, (w[q] >> 23) & 0xffu));
+      mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+      mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+      const int e = max(-126, min(126, static_cast<int>(mx) - 127));
+      const float down = exp2i(-e);
+      cs[hh] = a.scale_log2 * exp2i(e);
+#pragma unroll
+      for (int kk = 0; kk < kK; ++kk) {
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          const uint32_t x = w[2 * kk + q];
+          qa[kk][2 * q + hh] = pack_f16x2(__uint_as_float(x << 16) * down,
+                                          __uint_as_float(x & 0xffff0000u) * down);
+        }
+      }
+    }
+
+    float o[kTiles8][4];
+#pragma unroll
+    for (int t = 0; t < kTiles8; ++t)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) o[t][q] = 0.f;
+    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+
+    for (; i < end; ++i) {
+      const int stage = i % C::kStages;
+      const Tile t = shfl_tile(cur, i & 31);
+      if (t.pid >= 0 && ok) {
+        ok = mbar_wait_warp(bar0 + 8 * stage, phases >> stage & 1u, wc, kWaitKvFull);
+        if (ok) pending &= ~(1 << stage);
+      }
+      if (t.pid >= 0 && ok) {
+        phases ^= 1u << stage;
+        const uint32_t kt = ring + stage * C::kStageBytes, vt = kt + C::kTileBytes;
+        // ---- S = Q K^T, 32 keys in four n8 tiles
+        float s[4][4];
+#pragma unroll
+        for (int n = 0; n < 4; ++n) {
+          s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.f;
+          const int key = 8 * n + r;
+          uint32_t w[D / 16];                       // the thread's kVals codes of this key
+          if constexpr (D == 128) {
+            const uint4 x = ld_shared_v4(kt + key * 128 + (((2 * c) ^ (key & 7)) << 4));
+            const uint4 y = ld_shared_v4(kt + key * 128 + (((2 * c + 1) ^ (key & 7)) << 4));
+            w[0] = x.x; w[1] = x.y; w[2] = x.z; w[3] = x.w;
+            w[4] = y.x; w[5] = y.y; w[6] = y.z; w[7] = y.w;
+          } else {
+            const uint4 x = ld_shared_v4(kt + key * 64 + ((c ^ ((key >> 1) & 3)) << 4));
+            w[0] = x.x; w[1] = x.y; w[2] = x.z; w[3] = x.w;
+          }
+#pragma unroll
+          for (int kk = 0; kk < kK; ++kk)
+            mma_f16(s[n], qa[kk], e4m3x2_to_f16x2(w[kk]), e4m3x2_to_f16x2(w[kk] >> 16));
+        }
+        // ---- exponents, mask, running maximum
+        const float f0 = cs[0] * t.ks, f1 = cs[1] * t.ks;
+        const bool edge = t.key0 + kTileKeys > min(lim[0], lim[1]);
+        float x0 = -INFINITY, x1 = -INFINITY;
+#pragma unroll
+        for (int n = 0; n < 4; ++n) {
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+            s[n][q] = fmaf(s[n][q], f0, t.lv);
+            s[n][2 + q] = fmaf(s[n][2 + q], f1, t.lv);
+            if (edge) {
+              const int key = t.key0 + 8 * n + 2 * c + q;
+              if (key >= lim[0]) s[n][q] = -INFINITY;
+              if (key >= lim[1]) s[n][2 + q] = -INFINITY;
+            }
+            x0 = fmaxf(x0, s[n][q]);
+            x1 = fmaxf(x1, s[n][2 + q]);
+          }
+        }
+        x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, 1));
+        x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, 1));
+        x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, 2));
+        x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, 2));
+        const bool up = x0 > m[0] || x1 > m[1];
+        if (__any_sync(0xffffffffu, up)) {
+          const float n0 = fmaxf(m[0], x0), n1 = fmaxf(m[1], x1);
+          const float b0 = n0 == -INFINITY ? 1.f : ex2_approx(m[0] - n0);
+          const float b1 = n1 == -INFINITY ? 1.f : ex2_approx(m[1] - n1);
+          m[0] = n0;
+          m[1] = n1;
+          l[0] *= b0;
+          l[1] *= b1;
+#pragma unroll
+          for (int q = 0; q < kTiles8; ++q) {
+            o[q][0] *= b0;
+            o[q][1] *= b0;
+            o[q][2] *= b1;
+            o[q][3] *= b1;
+          }
+        }
+        const float m0 = m[0] == -INFINITY ? 0.f : m[0], m1 = m[1] == -INFINITY ? 0.f : m[1];
+        float sum0 = 0.f, sum1 = 0.f;
+        uint32_t pa[2][4];
+#pragma unroll
+        for (int n = 0; n < 4; ++n) {
+          const float p0 = ex2_approx(s[n][0] - m0), p1 = ex2_approx(s[n][1] - m0);
+          const float p2 = ex2_approx(s[n][2] - m1), p3 = ex2_approx(s[n][3] - m1);
+          sum0 += p0 + p1;
+          sum1 += p2 + p3;
+          pa[n >> 1][2 * (n & 1)] = pack_f16x2(p0, p1);
+          pa[n >> 1][2 * (n & 1) + 1] = pack_f16x2(p2, p3);
+        }
+        const float inv = ex2_approx(-t.lv);
+        l[0] = fmaf(sum0, inv, l[0]);
+        l[1] = fmaf(sum1, inv, l[1]);
+        // ---- O += P V: the thread's columns of four keys per k step, bytes
+        // paired by key
+        const int left = u.len - t.key0;             // keys of the tile that exist
+#pragma unroll
+        for (int kk = 0; kk < 2; ++kk) {
+          constexpr int kW = kTiles8 / 4;            // words: columns kTiles8 * r ...
+          uint32_t w[4][kW];
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const int key = 16 * kk + 2 * c + (q & 1) + 8 * (q >> 1);
+            if constexpr (D == 128) {
+              const uint4 x = ld_shared_v4(vt + key * 128 + ((r ^ (key & 7)) << 4));
+              w[q][0] = x.x; w[q][1] = x.y; w[q][2] = x.z; w[q][3] = x.w;
+            } else {
+              const uint2 x =
+                  ld_shared_v2(vt + key * 64 + (((r >> 1) ^ ((key >> 1) & 3)) << 4) + 8 * (r & 1));
+              w[q][0] = x.x; w[q][1] = x.y;
+            }
+            // Slots behind the sequence's end hold anything, NaN codes too.
+            if (left < kTileKeys && key >= left) {
+#pragma unroll
+              for (int z = 0; z < kW; ++z) w[q][z] = 0u;
+            }
+          }
+#pragma unroll
+          for (int z = 0; z < kW; ++z) {
+            const uint32_t e0 = __byte_perm(w[0][z], w[1][z], 0x5140);
+            const uint32_t e1 = __byte_perm(w[0][z], w[1][z], 0x7362);
+            const uint32_t g0 = __byte_perm(w[2][z], w[3][z], 0x5140);
+            const uint32_t g1 = __byte_perm(w[2][z], w[3][z], 0x7362);
+            mma_f16(o[4 * z], pa[kk], e4m3x2_to_f16x2(e0), e4m3x2_to_f16x2(g0));
+            mma_f16(o[4 * z + 1], pa[kk], e4m3x2_to_f16x2(e0 >> 16), e4m3x2_to_f16x2(g0 >> 16));
+            mma_f16(o[4 * z + 2], pa[kk], e4m3x2_to_f16x2(e1), e4m3x2_to_f16x2(g1));
+            mma_f16(o[4 * z + 3], pa[kk], e4m3x2_to_f16x2(e1 >> 16), e4m3x2_to_f16x2(g1 >> 16));
+          }
+        }
+      }
+      // ---- the stage's next tile
+      __syncwarp();
+      const int ahead = i + C::kStages;
+      if (ahead < n_tiles) {
+        const Tile f = shfl_tile((ahead >> 5) == (i >> 5) ? cur : next, ahead & 31);
+        if (f.pid >= 0 && ok) {
+          issue(f, stage);
+          pending |= 1 << stage;
+        }
+      }
+      if ((i & 31) == 31) {
+        cur = next;
+        const int k = (i >> 5) + 2;
+        if (32 * k < n_tiles) next = look_up(k);
+      }
+    }
+
+    // ---- the warps' results, joined
+#pragma unroll
+    for (int hh = 0; hh < 2; ++hh) {
+      l[hh] += __shfl_xor_sync(0xffffffffu, l[hh], 1);
+      l[hh] += __shfl_xor_sync(0xffffffffu, l[hh], 2);
+      if (c == 0) ml[warp * kRows + r + 8 * hh] = make_float2(m[hh], l[hh]);
+      // Row r's columns kVals c + ..., 16 bytes at a time, the slots permuted
+      // within 128 bytes so that eight neighbouring lanes meet eight banks.
+      float* base = join + (warp * kRows + r + 8 * hh) * D + kVals * c;
+      const int key = (c + 4 * (r & 1)) & (kVals / 4 - 1);
+#pragma unroll
+      for (int q = 0; q < kVals / 4; ++q) {
+        // columns kVals c + 4 q ..: the first half of them are n = 2 c, then n = 2 c + 1
+        const int t0 = (4 * q) % kTiles8, n1 = 4 * q / kTiles8;
+        *reinterpret_cast<float4*>(base + 4 * (q ^ key)) =
+            make_float4(o[t0][2 * hh + n1], o[t0 + 1][2 * hh + n1], o[t0 + 2][2 * hh + n1],
+                        o[t0 + 3][2 * hh + n1]);
+      }
+    }
+    __syncthreads();
+    if (!whole && tid < kRows) {
+      float mm = -INFINITY, ll = 0.f;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) mm = fmaxf(mm, ml[w * kRows + tid].x);
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        const float2 x = ml[w * kRows + tid];
+        if (x.x != -INFINITY) ll += x.y * ex2_approx(x.x - mm);
+        else if (x.y != x.y) ll = x.y;               // a NaN row
+      }
+      a.part_ml[(2 * cta + slot) * kRows + tid] = make_float2(mm, ll);
+    }
+    for (int f = tid; f < kRows * (D / 4); f += kThreads) {
+      const int row = f / (D / 4), q4 = f % (D / 4);
+      const int rr = u.rb * kRows + row;
+      if (rr >= u.n * a.group) continue;
+      float mm = -INFINITY;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) mm = fmaxf(mm, ml[w * kRows + row].x);
+      const int cq = q4 / (kVals / 4);
+      const int key = (cq + 4 * (row & 1)) & (kVals / 4 - 1);
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+      float ll = 0.f;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        const float2 x = ml[w * kRows + row];
+        const float b = x.x == -INFINITY ? (x.y != x.y ? x.y : 0.f) : ex2_approx(x.x - mm);
+        const float4 v = *reinterpret_cast<const float4*>(
+            join + (w * kRows + row) * D + kVals * cq + 4 * ((q4 % (kVals / 4)) ^ key));
+        ll = fmaf(x.y, b, ll);
+        acc.x = fmaf(v.x, b, acc.x);
+        acc.y = fmaf(v.y, b, acc.y);
+        acc.z = fmaf(v.z, b, acc.z);
+        acc.w = fmaf(v.w, b, acc.w);
+      }
+      if (whole) {
+        const int token = rr / a.group;
+        const long long at = (static_cast<long long>(u.r0 + token) * a.Hkv + u.head) * a.group +
+                             (rr - token * a.group);
+        const float inv = ll == 0.f ? 0.f : 1.f / ll;
+        *reinterpret_cast<uint2*>(a.o + at * D + 4 * q4) =
+            make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+        if (q4 == 0) a.lse[at] = ll == 0.f ? -INFINITY : (mm + log2f(ll)) * kLn2;
+      } else {
+        *reinterpret_cast<float4*>(a.part_o + ((2ll * cta + slot) * kRows + row) * D + 4 * q4) = acc;
+      }
+    }
+    if (tid == 0 && starts && !ends) {
+      // The first CTA of a shared unit says what is to be joined.
+      a.rec[2 * cta] = make_int4(u.r0, u.n, u.rb, u.head);
+      a.rec[2 * cta + 1] = make_int4(cta_of(W, G, u.c0 + u.chunks - 1), static_cast<int>(W),
+                                     static_cast<int>(W >> 32), 0);
+      shared_unit = true;
+    }
+    __syncthreads();
+  }
+  if (tid == 0 && !shared_unit) a.rec[2 * cta] = make_int4(0, 0, 0, 0);
+  // Copies in flight land before the CTA exits (only after a wait gave up).
+  for (int s = 0; s < C::kStages; ++s)
+    if (pending >> s & 1) mbar_wait_drain(bar0 + 8 * s, phases >> s & 1u, a.wait_budget);
+}
+
+// Joins the partial results of the units that several CTAs share, in the
+// order of their keys: block (c, y) takes two rows of the unit that goes on
+// after CTA c.  Four groups of D / 4 threads a row walk the parts.
+template <int D>
+__global__ void __launch_bounds__(2 * D) join_kernel(const CacheAttnArgs a) {
+  constexpr int kF4 = D / 4, kGroups = 4, kRowsPerBlock = 2;
+  static_assert(kF4 * kGroups * kRowsPerBlock == 2 * D, "threads");
+  __shared__ float4 part[kGroups][kRowsPerBlock][kF4];
+  __shared__ float2 pml[kGroups][kRowsPerBlock];
+  const int cta = blockIdx.x, G = a.grid;
+  const int4 rec = a.rec[2 * cta];
+  if (rec.y == 0) return;                            // nothing shared from here
+  const int4 more = a.rec[2 * cta + 1];
+  const long long W = (static_cast<long long>(more.z) << 32) | static_cast<unsigned int>(more.y);
+  const int q4 = threadIdx.x % kF4, local = threadIdx.x / kF4 % kRowsPerBlock;
+  const int group = threadIdx.x / (kF4 * kRowsPerBlock);
+  const int row = blockIdx.y * kRowsPerBlock + local;
+  const int rr = rec.z * kRows + row;
+  const bool on = rr < rec.y * a.group;
+  float m = -INFINITY, l = 0.f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int p = cta + group; on && p <= more.x; p += kGroups) {
+    if (cta_first(W, G, p) == cta_first(W, G, p + 1)) continue;   // a CTA without work
+    const long long slot = 2ll * p + (p == cta ? 1 : 0);
+    const float2 x = a.part_ml[slot * kRows + row];
+    const float4 v = *reinterpret_cast<const float4*>(a.part_o + (slot * kRows + row) * D + 4 * q4);
+    const float n = fmaxf(m, x.x);
+    const float b0 = n == -INFINITY ? 1.f : ex2_approx(m - n);
+    const float b1 = n == -INFINITY ? 1.f : ex2_approx(x.x - n);
+    m = n;
+    l = fmaf(l, b0, x.y * b1);
+    acc.x = fmaf(acc.x, b0, v.x * b1);
+    acc.y = fmaf(acc.y, b0, v.y * b1);
+    acc.z = fmaf(acc.z, b0, v.z * b1);
+    acc.w = fmaf(acc.w, b0, v.w * b1);
+  }
+  part[group][local][q4] = acc;
+  if (q4 == 0) pml[group][local] = make_float2(m, l);
+  __syncthreads();
+  if (group != 0 || !on) return;
+#pragma unroll
+  for (int g = 1; g < kGroups; ++g) {
+    const float2 x = pml[g][local];
+    const float4 v = part[g][local][q4];
+    const float n = fmaxf(m, x.x);
+    const float b0 = n == -INFINITY ? 1.f : ex2_approx(m - n);
+    const float b1 = n == -INFINITY ? 1.f : ex2_approx(x.x - n);
+    m = n;
+    l = fmaf(l, b0, x.y * b1);
+    acc.x = fmaf(acc.x, b0, v.x * b1);
+    acc.y = fmaf(acc.y, b0, v.y * b1);
+    acc.z = fmaf(acc.z, b0, v.z * b1);
+    acc.w = fmaf(acc.w, b0, v.w * b1);
+  }
+  const int token = rr / a.group;
+  const long long at = (static_cast<long long>(rec.x + token) * a.Hkv + rec.w) * a.group +
+                       (rr - token * a.group);
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  *reinterpret_cast<uint2*>(a.o + at * D + 4 * q4) =
+      make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+  if (q4 == 0) a.lse[at] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+}
+
+template <int D, bool SPARSE>
+cudaError_t launch_t(const CUtensorMap& tk, const CUtensorMap& tv, const CacheAttnArgs& a,
+                     cudaStream_t stream) {
+  auto kern = decode_kernel<D, SPARSE>;
+  const int smem = DecCfg<D>::kSmemFixed + (SPARSE ? 0 : (a.s.B + 1) * 8);
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  kern<<<a.grid, kThreads, smem, stream>>>(tk, tv, a);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  join_kernel<D><<<dim3(a.grid, kRows / 2), 2 * D, 0, stream>>>(a);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_cache_decode(int d, const CUtensorMap& tk, const CUtensorMap& tv,
+                                const CacheAttnArgs& a, cudaStream_t stream) {
+  if (a.selected != nullptr)
+    return d == 64 ? launch_t<64, true>(tk, tv, a, stream) : launch_t<128, true>(tk, tv, a, stream);
+  return d == 64 ? launch_t<64, false>(tk, tv, a, stream) : launch_t<128, false>(tk, tv, a, stream);
+}
+
+}  // namespace fattn

@@ -98,6 +98,95 @@ cudaError_t launch_bwd2_main(bool causal, const CUtensorMap& tq, const CUtensorM
 cudaError_t launch_dq_convert(const float* dq_accum, void* dq, long long elems, float scale,
                               cudaStream_t stream);
 
+// ------------------------------------------------------------------ paged 8-bit cache
+
+// A ragged batch: sequence b has rows q_start[b] .. q_start[b + 1] of the
+// call's T rows, kv_len[b] cached tokens (its new ones included) and its
+// pages in table[b * max_pages ..].  All on the device.
+struct CacheSeqs {
+  const int* q_start;
+  const int* kv_len;
+  const int* table;
+  int T, B, max_pages;
+};
+
+struct CacheAppendArgs {
+  CacheSeqs s;
+  uint8_t* k;                 // e4m3 codes [pages, Hkv, page, d], pages page_stride bytes apart
+  uint8_t* v;
+  float* k_scale;             // [pages, Hkv]
+  float* v_scale;
+  int8_t* bounds;             // [pages, Hkv, 2, d] or nullptr
+  long long page_stride;
+  int pages, Hkv;
+  const uint16_t* k_new;      // bf16 rows, k_row elements apart
+  const uint16_t* v_new;
+  const uint16_t* q;          // bf16 rows, or nullptr
+  uint16_t* q_out;            // bf16 [T, Hq, d]
+  long long k_row, v_row, q_row;
+  int Hq;
+  const float* rope;          // [rope_len, rope_dim]: cosines, then sines; or nullptr
+  int rope_len, rope_dim, interleaved;
+  DeviceStatus* status;
+};
+
+cudaError_t launch_cache_append(int page, int d, const CacheAppendArgs& a, cudaStream_t stream);
+
+struct CacheSelectArgs {
+  CacheSeqs s;
+  const uint16_t* q;
+  long long q_row;
+  const float* k_scale;
+  const int8_t* bounds;
+  int pages, Hkv, group, page_shift;
+  float* scores;              // workspace [T, Hkv, max_pages]
+  int* selected;              // [T, Hkv, n_selected]
+  int n_selected, n_first, n_recent;
+  DeviceStatus* status;
+};
+
+cudaError_t launch_cache_select(int d, const CacheSelectArgs& a, cudaStream_t stream);
+
+struct CacheAttnArgs {
+  CacheSeqs s;
+  const uint16_t* q;
+  long long q_row;
+  uint16_t* o;                // bf16 [T, Hq, d]
+  float* lse;                 // [T, Hq]
+  const float* k_scale;
+  const float* v_scale;
+  const int* selected;        // [T, Hkv, n_selected] or nullptr
+  int n_selected;
+  int pages, Hkv, group, page_shift, causal;
+  float scale_log2;
+  float* part_o;              // workspace: partial outputs of the units that CTAs share
+  float2* part_ml;
+  int4* rec;
+  int grid;                   // CTAs of the main kernel
+  DeviceStatus* status;
+  long long wait_budget;
+};
+
+// Workspace layout of the attention over the cache, for `rows` rows a tile.
+constexpr int kCacheMaxCtas = 152;   // the SMs of one GB300
+constexpr int kDecodeRows = 16;
+
+// Few rows per sequence (tiles of 16, mma.sync); tk, tv: 3-D uint8 views
+// {d, Hkv * page, pages} of the codes, boxes of 32 rows, swizzled by a row's
+// width.
+cudaError_t launch_cache_decode(int d, const CUtensorMap& tk, const CUtensorMap& tv,
+                                const CacheAttnArgs& a, cudaStream_t stream);
+
+// Per-device state for entry points outside fattn_api.cu: checks the device,
+// gives the status word and the wait budget.  Returns a fattn_status.
+int call_setup(DeviceStatus** status, long long* wait_budget);
+
+// 3-D uint8 view {inner, rows, slabs} (rows inner bytes apart, slabs
+// slab_stride), boxes of box_rows whole rows, swizzled by the row's width
+// (inner 64 or 128).  Returns a fattn_status.
+int make_rows_map_u8(CUtensorMap* m, const void* ptr, int inner, long long rows, int slabs,
+                     long long slab_stride, int box_rows);
+
 cudaError_t launch_selftest_timeout(DeviceStatus* status, long long budget, cudaStream_t stream);
 
 }  // namespace fattn

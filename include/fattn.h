@@ -45,8 +45,10 @@ typedef enum {
   FATTN_ERR_CUDA = 3,        /* a CUDA runtime/driver call failed */
   FATTN_ERR_TIMEOUT = 4,     /* a kernel gave up on a pipeline wait */
   FATTN_ERR_TOO_LARGE = 5,   /* the problem needs more scratch than fattn_bwd_noalloc has */
-  FATTN_ERR_DEBUG_CHECK = 6  /* debug builds only (FATTN_DEBUG): a kernel found an index out of
+  FATTN_ERR_DEBUG_CHECK = 6, /* debug builds only (FATTN_DEBUG): a kernel found an index out of
                                 its range, skipped the access and recorded the site */
+  FATTN_ERR_BAD_INDEX = 7    /* a cache call's q_start, kv_len, page_table or selected pages are
+                                out of range; the kernel skipped what they point at */
 } fattn_status;
 
 /*
@@ -271,9 +273,126 @@ int fattn_bwd_pair_schedule_items(int B, int H, int N, int causal, int clusters,
                                   int* cluster_start, int* items);
 
 /*
+ * Attention over a paged 8-bit cache
+ * ----------------------------------
+ * Answering token by token needs the keys and values of earlier tokens.  The
+ * pages have no counterpart to these entry points; they carry the FP8
+ * forward's block quantization to a cache that the caller owns.  Keys and
+ * values are e4m3 codes with one scale per page and kv head:
+ *   k, v             : uint8 [pages, Hkv, page, d], contiguous within a page; the pages of
+ *                      both lie page_stride bytes apart (at least Hkv*page*d, a multiple of 16);
+ *                      16-byte aligned
+ *   k_scale, v_scale : fp32 [pages, Hkv], each a power of two 2^e, -48 <= e <= 48; a value is
+ *                      code * scale
+ *   k_bounds         : int8 [pages, Hkv, 2, d] or NULL: per column the lower and the upper bound
+ *                      of the page's key codes in units of 448/127 of the scale (for
+ *                      fattn_cache_select); 16-byte aligned
+ *   page             : 32, 64 or 128 tokens;  d: 64 or 128;  Hkv <= 1024
+ *
+ * A call works on a ragged batch of B <= 4096 sequences, described on the
+ * device so that a captured graph can be replayed on other lengths:
+ *   q_start    : int [B+1], ascending; rows q_start[b] .. q_start[b+1]-1 of the call's T rows are
+ *                the new tokens of sequence b (none is allowed).  Rows from q_start[B] on are
+ *                padding: nothing of theirs is read or written.
+ *   kv_len     : int [B], the tokens of sequence b in the cache, its new ones included; the last
+ *                n_b = q_start[b+1]-q_start[b] of them are the new ones, so row i of the sequence
+ *                has position kv_len[b] - n_b + i
+ *   page_table : int [B, max_pages]; token t of sequence b is slot t % page of page
+ *                page_table[b][t / page]; entries past ceil(kv_len/page) are not read
+ * Query head h belongs to kv head h / (Hq / Hkv); Hkv divides Hq, Hq / Hkv <= 128.  Rows of
+ * q, k_new and v_new may lie further apart than they are long (slices of one projection):
+ * q_row, k_row, v_row are their distances in elements, multiples of 8.
+ * The kernels check these numbers before they use them: a sequence with
+ * senseless q_start or kv_len counts as empty, tokens on a page outside the cache count as
+ * absent, and fattn_check_status() reports FATTN_ERR_BAD_INDEX.
+ */
+typedef struct {
+  void* k;
+  void* v;
+  float* k_scale;
+  float* v_scale;
+  void* k_bounds;
+  long long page_stride;
+  int pages, Hkv, page, d;
+} fattn_cache;
+
+/*
+ * Append the batch's new tokens to the cache, keys rotated by their positions.
+ * Rotation: with rope = fp32 [rope_len, rope_dim], row p the rope_dim/2
+ * cosines of position p's angles and then the sines, column pairs (a, b) of a
+ * head become (a cos - b sin, b cos + a sin); the pairs are columns (i,
+ * i + rope_dim/2), or (2i, 2i+1) when interleaved != 0; columns from rope_dim on
+ * stay.  rope_dim is a multiple of 16 up to d; rope NULL (rope_dim 0) rotates
+ * nothing.  fp32, every product and sum rounded.
+ * Quantization: a page and head has scale 2^e with e the smallest exponent in
+ * [-48, 48] for which amax <= 448 * 2^e over its tokens, or the exponent it has if that is
+ * larger; code = e4m3(x * 2^-e), nearest even, saturated.  When new tokens
+ * raise e, the page's earlier codes are multiplied by the power of two and
+ * rounded again.  A page whose slot 0 is among the new tokens starts over.
+ * A token with a NaN in a head's key or value gets a NaN key and a zero
+ * value: the rows that attend to it become NaN, and no others.
+ *   k_new, v_new : in, bf16 rows of Hkv*d
+ *   q, q_out     : in, bf16 rows of Hq*d, and out, bf16 [T, Hq, d]: the queries rotated likewise
+ *                  (q_out may be q when its rows are contiguous); both NULL: none
+ * A page that receives tokens must belong to one sequence only.  Positions
+ * below 0 or from rope_len on are FATTN_ERR_BAD_INDEX.  Returns a fattn_status.
+ */
+int fattn_cache_append(const fattn_cache* cache, const void* k_new, long long k_row,
+                       const void* v_new, long long v_row, const void* q, long long q_row,
+                       void* q_out, int Hq, const float* rope, int rope_len, int rope_dim,
+                       int interleaved, const int* page_table, const int* q_start,
+                       const int* kv_len, int T, int B, int max_pages, fattn_stream_t stream);
+
+/*
+ * Attention of the batch's rows over their sequences' cached tokens.  Row i
+ * sees the tokens before position kv_len, and with causal != 0 those up to its
+ * own position; a row that sees nothing gets O = 0 and L = -inf.
+ *   q          : in,  bf16 rows of Hq*d (rotated)
+ *   o, lse     : out, bf16 [T, Hq, d] and fp32 [T, Hq], as for fattn_fwd
+ *   selected   : in, int [T, Hkv, n_selected] or NULL (n_selected 0): row t's heads of kv head h
+ *                attend only to the pages page_table[b][selected[t][h][i]] of their sequence;
+ *                negative entries stand for none, an entry named twice counts twice
+ *   workspace  : at least fattn_cache_fwd_workspace_bytes(T, B, Hq, Hkv, d, n_selected) bytes,
+ *                256-byte aligned; contents on entry ignored; calls that may overlap need
+ *                one each
+ * Value slots behind a sequence's end may hold anything; those before it hold
+ * no NaN code (fattn_cache_append writes none).  Results do not depend on
+ * timing.  Returns a fattn_status.
+ */
+size_t fattn_cache_fwd_workspace_bytes(int T, int B, int Hq, int Hkv, int d, int n_selected);
+int fattn_cache_fwd(const fattn_cache* cache, const void* q, long long q_row, void* o, float* lse,
+                    const int* page_table, const int* q_start, const int* kv_len,
+                    const int* selected, int n_selected, void* workspace, size_t workspace_bytes,
+                    int T, int B, int Hq, int max_pages, int causal, float scale,
+                    fattn_stream_t stream);
+
+/*
+ * Choose, for each row and kv head, the n_selected pages of the row's
+ * sequence that matter most, by an upper bound of the sum of the group's
+ * scores from the cache's k_bounds:
+ *   q8 = round(q * (127 / amax)), amax over the group's Hq/Hkv * d entries (fp32; zero below 2^-100),
+ *   score(page) = float(sum_d (sum_h max(q8,0)) hi_d + (sum_h min(q8,0)) lo_d) * k_scale,
+ * the sums in whole numbers, so the choice is exact.  The first n_first pages
+ * and the last n_recent up to the row's own are always taken (n_first + n_recent <= n_selected); ties go to
+ * the lower page.  A row with no more than n_selected pages takes them all.
+ *   q         : in,  bf16 rows of Hq*d, as for fattn_cache_fwd
+ *   selected  : out, int [T, Hkv, n_selected]: ascending, -1 behind the last
+ *   workspace : at least fattn_cache_select_workspace_bytes(T, Hkv, max_pages), 256-byte aligned;
+ *               contents on entry ignored
+ * Returns a fattn_status.
+ */
+size_t fattn_cache_select_workspace_bytes(int T, int Hkv, int max_pages);
+int fattn_cache_select(const fattn_cache* cache, const void* q, long long q_row,
+                       const int* page_table, const int* q_start, const int* kv_len,
+                       int* selected, int n_selected, int n_first, int n_recent, void* workspace,
+                       size_t workspace_bytes, int T, int B, int Hq, int max_pages,
+                       fattn_stream_t stream);
+
+/*
  * Synchronise `stream`, then report the first error since the last call:
- * a pending asynchronous CUDA error (FATTN_ERR_CUDA) or a kernel wait
- * timeout recorded on the current device (FATTN_ERR_TIMEOUT).  Clears the
+ * a pending asynchronous CUDA error (FATTN_ERR_CUDA), a kernel wait timeout
+ * (FATTN_ERR_TIMEOUT) or an index that a cache call found out of range
+ * (FATTN_ERR_BAD_INDEX) recorded on the current device.  Clears the
  * device status word.  Returns FATTN_OK when neither happened.
  */
 int fattn_check_status(fattn_stream_t stream);

@@ -39,3 +39,4 @@ from .fp8 import (  # noqa: F401
     hadamard_rotate_fp32,
     attention_fp8_reference,
 )
+from . import cache  # noqa: F401
