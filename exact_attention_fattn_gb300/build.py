@@ -29,7 +29,8 @@ DEBUG_BUILD_DIR = os.path.join(PKG, "_build_debug")
 DEBUG_FLAGS = ["-DFATTN_DEBUG", "-DFATTN_FWD_STAGES=2"]
 SOURCES = ["fattn_api.cu", "fattn_fwd.cu", "fattn_bwd.cu", "fattn_bwd2.cu", "fattn_bwd_aux.cu",
            "fattn_fp8.cu", "fattn_sched.cu", "fattn_cache_api.cu", "fattn_cache_append.cu",
-           "fattn_cache_decode.cu", "fattn_cache_select.cu"]
+           "fattn_cache_chunk.cu", "fattn_cache_decode.cu", "fattn_cache_join.cu",
+           "fattn_cache_select.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I", INCLUDE,
          "--expt-relaxed-constexpr"]

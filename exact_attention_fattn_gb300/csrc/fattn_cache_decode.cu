@@ -78,6 +78,11 @@ __device__ __forceinline__ uint32_t pack_f16x2(float a, float b) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
+// Chunks of a unit: at least one, so that rows that see nothing are written.
+__device__ __forceinline__ int chunks_of(int len) {
+  return max(1, (len + kChunkKeys - 1) / kChunkKeys);
+}
+
 // A unit: rows [16 rb, ..) of a sequence's n * group rows, one kv head.
 // Sparse calls take each token as a sequence of its own (r0 = token, n = 1).
 struct Unit {
@@ -130,7 +135,7 @@ struct Schedule {
     u.n = q.n;
     u.len = q.len;
     u.pos0 = q.len - q.n;
-    u.chunks = (q.len + kChunkKeys - 1) / kChunkKeys;
+    u.chunks = chunks_of(q.len);
     const int id = static_cast<int>((j - pre[lo]) / u.chunks);
     u.c0 = pre[lo] + static_cast<long long>(id) * u.chunks;
     u.rb = id / a->Hkv;
@@ -164,12 +169,6 @@ struct Schedule {
   }
 };
 
-// First chunk of CTA c of G over W chunks, and the CTA of chunk j.
-__device__ __forceinline__ long long cta_first(long long W, int G, int c) { return W * c / G; }
-__device__ __forceinline__ int cta_of(long long W, int G, long long j) {
-  return static_cast<int>(((j + 1) * G - 1) / W);
-}
-
 // One tile of a warp, as lane i of a batch of 32 looks it up.
 struct Tile {
   int pid;        // page, or -1: nothing to read
@@ -192,7 +191,7 @@ __device__ __forceinline__ Tile shfl_tile(const Tile& t, int src) {
 template <int D, bool SPARSE>
 __global__ void __launch_bounds__(kThreads, 1)
     decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
-                  const CacheAttnArgs a) {
+                  const __grid_constant__ CacheAttnArgs a) {
   using C = DecCfg<D>;
   constexpr int kK = D / 16;            // k steps of Q K^T
   constexpr int kVals = D / 4;          // consecutive columns of O a thread holds per row
@@ -228,7 +227,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const SeqInfo q = seq_info(a.s, b, a.page_shift);
       if (!q.ok && cta == 0) record_bad_index(a.status, kSiteSeqStart);
       const long long blocks = (static_cast<long long>(q.n) * a.group + kRows - 1) / kRows;
-      sum += blocks * a.Hkv * ((q.len + kChunkKeys - 1) / kChunkKeys);
+      sum += blocks * a.Hkv * chunks_of(q.len);
     }
     long long incl = sum;
 #pragma unroll
@@ -245,15 +244,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       pre[b] = at;
       const SeqInfo q = seq_info(a.s, b, a.page_shift);
       const long long blocks = (static_cast<long long>(q.n) * a.group + kRows - 1) / kRows;
-      at += blocks * a.Hkv * ((q.len + kChunkKeys - 1) / kChunkKeys);
-      // Rows of a sequence with no keys at all see nothing.
-      if (q.len == 0 && q.n > 0 && b % G == cta) {
-        const long long cnt = static_cast<long long>(q.n) * a.Hkv * a.group;
-        uint4* o = reinterpret_cast<uint4*>(a.o + static_cast<long long>(q.r0) * a.Hkv * a.group * D);
-        for (long long i = 0; i < cnt * (D / 8); ++i) o[i] = make_uint4(0u, 0u, 0u, 0u);
-        float* l = a.lse + static_cast<long long>(q.r0) * a.Hkv * a.group;
-        for (long long i = 0; i < cnt; ++i) l[i] = -INFINITY;
-      }
+      at += blocks * a.Hkv * chunks_of(q.len);
     }
     if (tid == kThreads - 1) pre[a.s.B] = at;
   }
@@ -611,69 +602,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (pending >> s & 1) mbar_wait_drain(bar0 + 8 * s, phases >> s & 1u, a.wait_budget);
 }
 
-// Joins the partial results of the units that several CTAs share, in the
-// order of their keys: block (c, y) takes two rows of the unit that goes on
-// after CTA c.  Four groups of D / 4 threads a row walk the parts.
-template <int D>
-__global__ void __launch_bounds__(2 * D) join_kernel(const CacheAttnArgs a) {
-  constexpr int kF4 = D / 4, kGroups = 4, kRowsPerBlock = 2;
-  static_assert(kF4 * kGroups * kRowsPerBlock == 2 * D, "threads");
-  __shared__ float4 part[kGroups][kRowsPerBlock][kF4];
-  __shared__ float2 pml[kGroups][kRowsPerBlock];
-  const int cta = blockIdx.x, G = a.grid;
-  const int4 rec = a.rec[2 * cta];
-  if (rec.y == 0) return;                            // nothing shared from here
-  const int4 more = a.rec[2 * cta + 1];
-  const long long W = (static_cast<long long>(more.z) << 32) | static_cast<unsigned int>(more.y);
-  const int q4 = threadIdx.x % kF4, local = threadIdx.x / kF4 % kRowsPerBlock;
-  const int group = threadIdx.x / (kF4 * kRowsPerBlock);
-  const int row = blockIdx.y * kRowsPerBlock + local;
-  const int rr = rec.z * kRows + row;
-  const bool on = rr < rec.y * a.group;
-  float m = -INFINITY, l = 0.f;
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int p = cta + group; on && p <= more.x; p += kGroups) {
-    if (cta_first(W, G, p) == cta_first(W, G, p + 1)) continue;   // a CTA without work
-    const long long slot = 2ll * p + (p == cta ? 1 : 0);
-    const float2 x = a.part_ml[slot * kRows + row];
-    const float4 v = *reinterpret_cast<const float4*>(a.part_o + (slot * kRows + row) * D + 4 * q4);
-    const float n = fmaxf(m, x.x);
-    const float b0 = n == -INFINITY ? 1.f : ex2_approx(m - n);
-    const float b1 = n == -INFINITY ? 1.f : ex2_approx(x.x - n);
-    m = n;
-    l = fmaf(l, b0, x.y * b1);
-    acc.x = fmaf(acc.x, b0, v.x * b1);
-    acc.y = fmaf(acc.y, b0, v.y * b1);
-    acc.z = fmaf(acc.z, b0, v.z * b1);
-    acc.w = fmaf(acc.w, b0, v.w * b1);
-  }
-  part[group][local][q4] = acc;
-  if (q4 == 0) pml[group][local] = make_float2(m, l);
-  __syncthreads();
-  if (group != 0 || !on) return;
-#pragma unroll
-  for (int g = 1; g < kGroups; ++g) {
-    const float2 x = pml[g][local];
-    const float4 v = part[g][local][q4];
-    const float n = fmaxf(m, x.x);
-    const float b0 = n == -INFINITY ? 1.f : ex2_approx(m - n);
-    const float b1 = n == -INFINITY ? 1.f : ex2_approx(x.x - n);
-    m = n;
-    l = fmaf(l, b0, x.y * b1);
-    acc.x = fmaf(acc.x, b0, v.x * b1);
-    acc.y = fmaf(acc.y, b0, v.y * b1);
-    acc.z = fmaf(acc.z, b0, v.z * b1);
-    acc.w = fmaf(acc.w, b0, v.w * b1);
-  }
-  const int token = rr / a.group;
-  const long long at = (static_cast<long long>(rec.x + token) * a.Hkv + rec.w) * a.group +
-                       (rr - token * a.group);
-  const float inv = l == 0.f ? 0.f : 1.f / l;
-  *reinterpret_cast<uint2*>(a.o + at * D + 4 * q4) =
-      make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
-  if (q4 == 0) a.lse[at] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
-}
-
 template <int D, bool SPARSE>
 cudaError_t launch_t(const CUtensorMap& tk, const CUtensorMap& tv, const CacheAttnArgs& a,
                      cudaStream_t stream) {
@@ -683,8 +611,7 @@ cudaError_t launch_t(const CUtensorMap& tk, const CUtensorMap& tv, const CacheAt
   if (e != cudaSuccess) return e;
   kern<<<a.grid, kThreads, smem, stream>>>(tk, tv, a);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  join_kernel<D><<<dim3(a.grid, kRows / 2), 2 * D, 0, stream>>>(a);
-  return cudaGetLastError();
+  return launch_cache_join(D, kRows, a, stream);
 }
 
 }  // namespace

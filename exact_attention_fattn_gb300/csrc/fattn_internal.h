@@ -167,15 +167,23 @@ struct CacheAttnArgs {
   long long wait_budget;
 };
 
-// Workspace layout of the attention over the cache, for `rows` rows a tile.
 constexpr int kCacheMaxCtas = 152;   // the SMs of one GB300
 constexpr int kDecodeRows = 16;
+constexpr int kChunkRows = 256;
 
 // Few rows per sequence (tiles of 16, mma.sync); tk, tv: 3-D uint8 views
 // {d, Hkv * page, pages} of the codes, boxes of 32 rows, swizzled by a row's
 // width.
 cudaError_t launch_cache_decode(int d, const CUtensorMap& tk, const CUtensorMap& tv,
                                 const CacheAttnArgs& a, cudaStream_t stream);
+
+// Many rows per sequence (units of 256, tcgen05); tk, tv: the same views with
+// boxes of one page's rows.
+cudaError_t launch_cache_chunk(int d, const CUtensorMap& tk, const CUtensorMap& tv,
+                               const CacheAttnArgs& a, cudaStream_t stream);
+
+// Joins the units of `rows` rows that CTAs of either kernel shared.
+cudaError_t launch_cache_join(int d, int rows, const CacheAttnArgs& a, cudaStream_t stream);
 
 // Per-device state for entry points outside fattn_api.cu: checks the device,
 // gives the status word and the wait budget.  Returns a fattn_status.

@@ -44,7 +44,8 @@ typedef enum {
   FATTN_ERR_UNSUPPORTED = 2, /* d not in {64,128}, or the device is not sm_103 */
   FATTN_ERR_CUDA = 3,        /* a CUDA runtime/driver call failed */
   FATTN_ERR_TIMEOUT = 4,     /* a kernel gave up on a pipeline wait */
-  FATTN_ERR_TOO_LARGE = 5,   /* the problem needs more scratch than fattn_bwd_noalloc has */
+  FATTN_ERR_TOO_LARGE = 5,   /* the problem needs more scratch than fattn_bwd_noalloc has, or
+                                fattn_cache_fwd more than 2^31 pieces of work */
   FATTN_ERR_DEBUG_CHECK = 6, /* debug builds only (FATTN_DEBUG): a kernel found an index out of
                                 its range, skipped the access and recorded the site */
   FATTN_ERR_BAD_INDEX = 7    /* a cache call's q_start, kv_len, page_table or selected pages are

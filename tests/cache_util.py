@@ -80,10 +80,12 @@ def check_attention(o, lse, want, d, amax_q, kmax):
     """o, lse: arrays; want: oracle.cache.attend's (O, L, A, D).
 
     A score s = scale sum_c q_c k_c is summed in fp32 from exact products of a
-    query of at least 18 bits below its row's largest entry (the kernels scale
-    rows by powers of two into fp16, or split them into two e4m3 parts) and a
-    code, so it is off by at most
-      delta = (d + 8) 2^-23 D + 2^-18 scale amax_q sum_c |k_c| + 2^-20,
+    code and a query's entry.  The entry is either its row's scaled by a power
+    of two into fp16 (off by 2^-25 of the largest at most) or the sum of two
+    e4m3 parts of the row scaled so that its largest is at least 224, off by at
+    most half a subnormal step, 2^-10: 2^-17 of the largest.  A score is off by
+    at most
+      delta = (d + 8) 2^-23 D + 2^-17 scale amax_q sum_c |k_c| + 2^-20,
     the first term counting truncated sums, the last the exponential's own
     error.  A probability is rounded to fp16 once (2^-11) and the output to
     bf16 (2^-8): |dO| <= 2^-8 |O| + (2^-11 + 2 delta)(A + |O|) and |dL| <= delta
@@ -91,7 +93,7 @@ def check_attention(o, lse, want, d, amax_q, kmax):
     most 2^-25 of the largest: 2^-25 n |V|, below what A's term leaves."""
     O, L, A, D = want
     live = ~np.isnan(L)
-    delta = (d + 8) * 2.0 ** -23 * D + 2.0 ** -18 * amax_q * kmax * d / np.sqrt(d) + 2.0 ** -20
+    delta = (d + 8) * 2.0 ** -23 * D + 2.0 ** -17 * amax_q * kmax * d / np.sqrt(d) + 2.0 ** -20
     allow = BF16_STEP * np.abs(O) + (F16_STEP + 2 * delta[..., None]) * (A + np.abs(O)) + 2.0 ** -24 * np.nan_to_num(A).max()
     err = np.abs(o - O)
     assert np.isfinite(o[live]).all()
