@@ -83,16 +83,25 @@ __device__ __forceinline__ int scale_exp(float s) {
   return max(kScaleExpMin, min(kScaleExpMax, e));
 }
 
-// Two e4m3 codes (low 16 bits) -> two halves, exactly.
-__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t codes) {
-  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(codes & 0xffffu),
-                                                   __NV_E4M3);
-  return static_cast<uint32_t>(h.x) | (static_cast<uint32_t>(h.y) << 16);
+// Four e4m3 codes -> two pairs of halves, exactly.  The 16-bit halves are
+// named inside the asm: through the header's conversion, which returns a
+// struct, the same two conversions ran at 8.7 instead of 21 quads a clock and SM
+// (with one more operation each).
+__device__ __forceinline__ void e4m3x4_to_f16x4(uint32_t codes, uint32_t& lo, uint32_t& hi) {
+  asm("{\n\t.reg .b16 l, h;\n\t"
+      "mov.b32 {l, h}, %2;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %0, l;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(codes));
 }
 
-__device__ __forceinline__ float2 e4m3x2_to_f32x2(uint32_t codes) {
-  const uint32_t h = e4m3x2_to_f16x2(codes);
-  return __half22float2(*reinterpret_cast<const __half2*>(&h));
+__device__ __forceinline__ float4 e4m3x4_to_f32x4(uint32_t codes) {
+  uint32_t lo, hi;
+  e4m3x4_to_f16x4(codes, lo, hi);
+  const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&lo));
+  const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&hi));
+  return make_float4(a.x, a.y, b.x, b.y);
 }
 
 }  // namespace fattn

@@ -76,9 +76,10 @@ CacheSeqs seqs_of(const int* page_table, const int* q_start, const int* kv_len, 
 
 size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 
-// Partial results of the units that CTAs share: two per CTA.
+// Partial results of the units that CTAs share, two per CTA, and, for the
+// tcgen05 kernel, half a unit's rows per CTA to pass between its warpgroups.
 struct AttnWorkspace {
-  size_t o_off, ml_off, rec_off, total;
+  size_t o_off, ml_off, rec_off, xo_off, xml_off, total;
 };
 
 AttnWorkspace attn_workspace(int rows, int d) {
@@ -87,7 +88,10 @@ AttnWorkspace attn_workspace(int rows, int d) {
   w.o_off = 0;
   w.ml_off = align256(slots * d * sizeof(float));
   w.rec_off = w.ml_off + align256(slots * sizeof(float2));
-  w.total = w.rec_off + align256(2 * kCacheMaxCtas * sizeof(int4));
+  w.xo_off = w.rec_off + align256(2 * kCacheMaxCtas * sizeof(int4));
+  const size_t xch = rows == kChunkRows ? static_cast<size_t>(kCacheMaxCtas) * (kChunkRows / 2) : 0;
+  w.xml_off = w.xo_off + align256(xch * d * sizeof(float));
+  w.total = w.xml_off + align256(xch * sizeof(float2));
   return w;
 }
 
@@ -214,6 +218,8 @@ int fattn_cache_fwd(const fattn_cache* cache, const void* q, long long q_row, vo
   a.part_o = reinterpret_cast<float*>(base + w.o_off);
   a.part_ml = reinterpret_cast<float2*>(base + w.ml_off);
   a.rec = reinterpret_cast<int4*>(base + w.rec_off);
+  a.xch_o = reinterpret_cast<float4*>(base + w.xo_off);
+  a.xch_ml = reinterpret_cast<float2*>(base + w.xml_off);
   int dev = 0, sms = 0;
   if (cudaGetDevice(&dev) != cudaSuccess ||
       cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)

@@ -104,9 +104,9 @@ __device__ __forceinline__ uint2 encode8(const float (&f)[8], float mul) {
 }
 
 __device__ __forceinline__ uint32_t rescale4(uint32_t w, float mul) {
-  const float2 a = e4m3x2_to_f32x2(w), b = e4m3x2_to_f32x2(w >> 16);
-  return pack_e4m3x4(__fmul_rn(a.x, mul), __fmul_rn(a.y, mul), __fmul_rn(b.x, mul),
-                     __fmul_rn(b.y, mul));
+  const float4 x = e4m3x4_to_f32x4(w);
+  return pack_e4m3x4(__fmul_rn(x.x, mul), __fmul_rn(x.y, mul), __fmul_rn(x.z, mul),
+                     __fmul_rn(x.w, mul));
 }
 
 // Bounds of the codes are kept in units of 448 / 127 of the scale.
@@ -295,14 +295,12 @@ __global__ void __launch_bounds__(kAppThreads) append_kernel(const CacheAppendAr
       bf16x8_to_f32(vw[s], vf);
       cv = encode8(vf, mv);
       if (a.bounds != nullptr) {
-        const uint32_t cw[4] = {ck.x, ck.x >> 16, ck.y, ck.y >> 16};
+        const float4 x0 = e4m3x4_to_f32x4(ck.x), x1 = e4m3x4_to_f32x4(ck.y);
+        const float x[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float2 x = e4m3x2_to_f32x2(cw[i]);
-          low[2 * i] = fminf(low[2 * i], x.x);
-          high[2 * i] = fmaxf(high[2 * i], x.x);
-          low[2 * i + 1] = fminf(low[2 * i + 1], x.y);
-          high[2 * i + 1] = fmaxf(high[2 * i + 1], x.y);
+        for (int i = 0; i < 8; ++i) {
+          low[i] = fminf(low[i], x[i]);
+          high[i] = fmaxf(high[i], x[i]);
         }
       }
     }

@@ -32,8 +32,10 @@
 // results in a second kernel, in order.
 //
 // Warps: 0-3 softmax of row tile 0, 4-7 of row tile 1 (they also bring their
-// rows of Q in, as hi and lo parts), 8 tensor memory and MMA issue, 9 TMA, 10-11
-// conversion of V.  TMEM: S_t [128 t, 128 t + 128), P aliases S, O_t at 256 + d t.
+// rows of Q in, as hi and lo parts), 8 tensor memory and MMA issue, 9 TMA, 10 the
+// walk over the CTA's share (it publishes one segment after the other in
+// shared memory, so that no other role holds the schedule in registers), 11
+// idle, 12-15 conversion of V.  TMEM: S_t [128 t, 128 t + 128), P aliases S, O_t at 256 + d t.
 #include <cuda_fp16.h>
 
 #include "fattn_cache.cuh"
@@ -45,16 +47,23 @@ namespace {
 constexpr int kBM = 128;              // rows per tile
 constexpr int kBN = 128;              // keys per tile
 constexpr int kUnitRows = kChunkRows;
-constexpr int kThreads = 384;
+constexpr int kThreads = 512;
 constexpr int kMmaWarp = 8;
 constexpr int kLoadWarp = 9;
+constexpr int kWalkWarp = 10;
+constexpr int kConvWarp0 = 12;
+constexpr int kSegs = 4;              // segments in the shared ring
+constexpr int kSegReaders = 8 + 2 + 4;   // warps that read each of them
 constexpr float kLn2 = 0.69314718055994530942f;
 constexpr float kTau = 8.f;
-// The same split as the dense forward: 128 x 72 + 256 x 216 = 384 x 168.
-constexpr int kLaunchRegs = 168;
-constexpr int kCtrlRegs = 72;
-constexpr int kSoftmaxRegs = 216;
-static_assert(128 * kCtrlRegs + 256 * kSoftmaxRegs == kThreads * kLaunchRegs, "register split");
+// Register split: 256 x 200 + 128 x 56 + 128 x 56 = 512 x 128, exactly the
+// launch total, so setmaxnreg.inc can always complete.
+constexpr int kLaunchRegs = 128;
+constexpr int kSoftmaxRegs = 200;
+constexpr int kCtrlRegs = 56;
+constexpr int kConvRegs = 56;
+static_assert(256 * kSoftmaxRegs + 128 * kCtrlRegs + 128 * kConvRegs == kThreads * kLaunchRegs,
+              "register split");
 static_assert(kUnitRows == 2 * kBM, "rows of a unit");
 
 template <int D>
@@ -71,10 +80,12 @@ struct ChunkCfg {
   static constexpr int kHOff = kVOff + kVStages * kCodeTile;
   static constexpr int kBarOff = kHOff + 2 * kHalfTile;
   // k_full[] k_empty[] v_full[] v_empty[] h_full[2] h_empty[2] q_full[2]
-  // s_full[2] p_full[2] o_full[2] o_empty[2] mma_done
-  static constexpr int kNumBars = 2 * kKStages + 2 * kVStages + 15;
+  // s_full[2] p_full[2] o_full[2] o_empty[2] mma_done x_full x_empty
+  // seg_full[] seg_empty[]
+  static constexpr int kNumBars = 2 * kKStages + 2 * kVStages + 17 + 2 * kSegs;
   static constexpr int kMiscOff = kBarOff + kNumBars * 8;   // tmem, abort, valid[kVStages]
-  static constexpr int kPreOff = kMiscOff + 64;             // [B + 1] int
+  static constexpr int kSegOff = (kMiscOff + 32 + 15) / 16 * 16;
+  static constexpr int kPreOff = kSegOff + kSegs * 64;      // [B + 1] int
   static constexpr int kSmemFixed = kPreOff + 1024;
   __device__ static constexpr uint32_t col_s(int t) { return 128u * t; }
   __device__ static constexpr uint32_t col_o(int t) { return 256u + D * t; }
@@ -120,16 +131,29 @@ __device__ __forceinline__ int tiles_of(const CacheAttnArgs& a, int n, int len, 
 }
 
 // One CTA's part of a unit: key tiles [a, e) for the rows from 256 rb of a
-// sequence; row tile t has tiles up to e_t[t] (a where it has none).
-struct Seg {
-  int b, rb, head;
-  int r0, n, len;
-  int a, e, nt;
-  int e_t[2];
-  bool starts, ends;
+// sequence.  Slot t (a softmax warpgroup with its TMEM columns) takes row tile
+// t and key tiles from j0(t) up to last(t).  A unit of at most 128 rows is
+// narrow: both slots take its one row tile, slot 0 the even key tiles of the
+// part and slot 1 the odd ones, and are joined at the end, so that one slot's
+// softmax runs beside the other's products there, too.
+struct __align__(16) Seg {
+  int b, rb, head, nt;
+  int r0, n, len, flags;
+  int a, e, e0, pad;
+  static constexpr int kStarts = 1, kEnds = 2, kNarrow = 4, kLast = 8;
+  __device__ __forceinline__ bool narrow() const { return flags & kNarrow; }
+  __device__ __forceinline__ bool whole() const { return (flags & 3) == 3; }
+  __device__ __forceinline__ int j0(int t) const { return narrow() ? a + t : a; }
+  __device__ __forceinline__ int last(int t) const { return t == 0 ? e0 : e; }
+  __device__ __forceinline__ bool active(int t) const { return j0(t) < last(t); }
+  // Row of the sequence's n * group of thread r of slot t (T * Hq < 2^31).
+  __device__ __forceinline__ int row(int t, int r) const {
+    return rb * kUnitRows + (narrow() ? 0 : t * kBM) + r;
+  }
 };
+static_assert(sizeof(Seg) <= 64, "ring slot");
 
-// Walks a CTA's share; every warp that needs it runs its own, converged.
+// Walks a CTA's share (one converged warp).
 struct Walker {
   const CacheAttnArgs& a;
   const int* pre;           // key tiles before each sequence
@@ -203,34 +227,24 @@ struct Walker {
     s.a = at;
     s.e = static_cast<int>(min(static_cast<long long>(nt), at + left));
     s.nt = nt;
-    s.starts = at == 0;
-    s.ends = s.e == nt;
-    const bool second = static_cast<long long>(rb) * kUnitRows + kBM <
-                        static_cast<long long>(q.n) * a.group;
-    s.e_t[0] = max(s.a, min(s.e, tiles_of(a, q.n, q.len, rb, kBM)));
-    s.e_t[1] = second ? s.e : s.a;
+    const bool narrow = static_cast<long long>(rb) * kUnitRows + kBM >= static_cast<long long>(q.n) * a.group;
+    s.flags = (at == 0 ? Seg::kStarts : 0) | (s.e == nt ? Seg::kEnds : 0) | (narrow ? Seg::kNarrow : 0);
+    s.e0 = narrow ? s.e : max(s.a, min(s.e, tiles_of(a, q.n, q.len, rb, kBM)));
     left -= s.e - s.a;
     at = s.e;
     return true;
   }
 };
 
-// 32 pages of a sequence, one per lane.
-struct Window {
-  int base, pid;
-  __device__ __forceinline__ void load(const CacheAttnArgs& a, const Seg& s, int first) {
-    base = first;
-    pid = -1;
-    const int p = first + static_cast<int>(threadIdx.x & 31);
-    if ((static_cast<long long>(p) << a.page_shift) < s.len) {
-      pid = __ldg(a.s.table + static_cast<long long>(s.b) * a.s.max_pages + p);
-      if (pid < 0 || pid >= a.pages) {
-        record_bad_index(a.status, kSitePage);
-        pid = -1;
-      }
-    }
-  }
-};
+// Page `first` + lane of a sequence; -1 where it has none or a senseless one.
+__device__ __forceinline__ int page_of_lane(const CacheAttnArgs& a, int b, int len, int first) {
+  const int p = first + static_cast<int>(threadIdx.x & 31);
+  if ((static_cast<long long>(p) << a.page_shift) >= len) return -1;
+  const int pid = __ldg(a.s.table + static_cast<long long>(b) * a.s.max_pages + p);
+  if (pid >= 0 && pid < a.pages) return pid;
+  record_bad_index(a.status, kSitePage);
+  return -1;
+}
 
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -254,7 +268,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto p_full = [&](uint32_t t) { return rest + 64u + 8u * t; };
   auto o_full = [&](uint32_t t) { return rest + 80u + 8u * t; };
   auto o_empty = [&](uint32_t t) { return rest + 96u + 8u * t; };
-  const uint32_t mma_done = rest + 112u;
+  const uint32_t mma_done = rest + 112u, x_full = rest + 120u, x_empty = rest + 128u;
+  auto seg_full = [&](uint32_t i) { return rest + 136u + 8u * (i % kSegs); };
+  auto seg_empty = [&](uint32_t i) { return rest + 136u + 8u * (kSegs + i % kSegs); };
+  const Seg* segs = reinterpret_cast<const Seg*>(smem + C::kSegOff);   // 64 bytes apart
+  auto seg_at = [&](uint32_t i) -> const Seg& {
+    return *reinterpret_cast<const Seg*>(reinterpret_cast<const uint8_t*>(segs) + 64u * (i % kSegs));
+  };
   uint32_t* misc = reinterpret_cast<uint32_t*>(smem + C::kMiscOff);
   volatile uint32_t* valid = misc + 2;   // per V stage: which 32-key groups were loaded
   int* pre = reinterpret_cast<int*>(smem + C::kPreOff);
@@ -269,10 +289,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int s = 0; s < C::kVStages; ++s) {
       mbar_init(v_full(s), 1);
-      mbar_init(v_empty(s), 2);
+      mbar_init(v_empty(s), 4);
     }
     for (int t = 0; t < 2; ++t) {
-      mbar_init(h_full(t), 2);
+      mbar_init(h_full(t), 4);
       mbar_init(h_empty(t), 1);
       mbar_init(q_full(t), 4);
       mbar_init(s_full(t), 1);
@@ -281,6 +301,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(o_empty(t), 128);
     }
     mbar_init(mma_done, 1);
+    mbar_init(x_full, 128);
+    mbar_init(x_empty, 128);
+    for (int i = 0; i < kSegs; ++i) {
+      mbar_init(seg_full(i), 1);
+      mbar_init(seg_empty(i), kSegReaders);
+    }
     misc[1] = 0u;
     fence_barrier_init();
   }
@@ -329,7 +355,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = misc[0];
   const WaitCtx wc{args.wait_budget, reinterpret_cast<volatile uint32_t*>(&misc[1]), args.status};
   const long long W = pre[args.s.B];
-  const long long j0 = cta_first(W, G, cta), j1 = cta_first(W, G, cta + 1);
+  // Segment i of the CTA; a reader that is done with it hands it back.
+  auto wait_seg = [&](uint32_t i) {
+    return mbar_wait_warp(seg_full(i), (i / kSegs) & 1, wc, kWaitSegment);
+  };
+  auto done_seg = [&](uint32_t i) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(seg_empty(i));
+  };
 
   if (warp < 8) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
@@ -342,22 +375,21 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tO = tmem + lane_off + C::col_o(t);
     const uint32_t q_smem = sbase + C::kQOff + t * C::kQBytes;
     const int pages_log = 7 - args.page_shift;   // log2 of the pages per key tile
-    uint32_t s_count = 0, o_count = 0;
+    uint32_t s_count = 0, o_count = 0, x_count = 0;
     bool ok = true;
 
     // This thread's row of the segment's Q, split into e4m3 parts; returns
     // log2(e) * scale times the power of two that was taken out.
     auto load_q = [&](const Seg& s) -> float {
-      const long long rr = static_cast<long long>(s.rb) * kUnitRows + t * kBM + r_tile;
-      const bool on = rr < static_cast<long long>(s.n) * args.group;
+      const int rr = s.row(t, r_tile);
+      const bool on = rr < s.n * args.group;
       uint4 w[D / 8];
 #pragma unroll
       for (int i = 0; i < D / 8; ++i) w[i] = make_uint4(0u, 0u, 0u, 0u);
       if (on) {
-        const int token = static_cast<int>(rr / args.group);
+        const int token = rr / args.group;
         const uint4* p = reinterpret_cast<const uint4*>(
-            args.q + (s.r0 + token) * args.q_row +
-            (static_cast<long long>(s.head) * args.group + (rr - static_cast<long long>(token) * args.group)) * D);
+            args.q + (s.r0 + token) * args.q_row + (s.head * args.group + rr - token * args.group) * D);
 #pragma unroll
         for (int i = 0; i < D / 8; ++i) w[i] = __ldg(p + i);
       }
@@ -383,8 +415,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           const float x0 = __uint_as_float(a0 << 16) * down, x1 = __uint_as_float(a0 & 0xffff0000u) * down;
           const float x2 = __uint_as_float(a1 << 16) * down, x3 = __uint_as_float(a1 & 0xffff0000u) * down;
           hi[z] = pack_e4m3x4(x0, x1, x2, x3);
-          const float2 h0 = e4m3x2_to_f32x2(hi[z]), h1 = e4m3x2_to_f32x2(hi[z] >> 16);
-          lo[z] = pack_e4m3x4(x0 - h0.x, x1 - h0.y, x2 - h1.x, x3 - h1.y);
+          const float4 h = e4m3x4_to_f32x4(hi[z]);
+          lo[z] = pack_e4m3x4(x0 - h.x, x1 - h.y, x2 - h.z, x3 - h.w);
         }
         st_shared_v4(q_smem + code_off<D>(r_tile, i), hi[0], hi[1], hi[2], hi[3]);
         st_shared_v4(q_smem + C::kCodeTile + code_off<D>(r_tile, i), lo[0], lo[1], lo[2], lo[3]);
@@ -395,61 +427,71 @@ __global__ void __launch_bounds__(kThreads, 1)
       return args.scale_log2 * exp2i(ec);
     };
 
-    Walker walk(args, pre, j0, j1);
-    Seg s{}, sn{};
-    bool more = walk.next(sn);
+    uint32_t si = 0;                      // segment
     float c_row = 0.f;
-    if (more && sn.e_t[t] > sn.a) c_row = load_q(sn);
-    while (ok && more) {
-      s = sn;
-      more = walk.next(sn);
-      const bool whole = s.starts && s.ends;
-      const long long rr = static_cast<long long>(s.rb) * kUnitRows + t * kBM + r_tile;
-      const bool on = rr < static_cast<long long>(s.n) * args.group;
-      const int token = on ? static_cast<int>(rr / args.group) : 0;
+    ok = wait_seg(0);
+    if (ok && !(seg_at(0).flags & Seg::kLast) && seg_at(0).active(t)) c_row = load_q(seg_at(0));
+    for (; ok && !(seg_at(si).flags & Seg::kLast); ++si) {
+      const Seg& s = seg_at(si);
       // Keys the row sees.  Rows past the unit's last see all (their queries
       // are zero), so that they need no mask.
-      const int lim = !on || !args.causal ? s.len : max(0, min(s.len, s.len - s.n + token + 1));
+      int lim = s.len;
+      if (args.causal) {
+        const int rr = s.row(t, r_tile);
+        if (rr < s.n * args.group) lim = max(0, min(s.len, s.len - s.n + rr / args.group + 1));
+      }
       float m_ref = -INFINITY, l = 0.f;
       const float c0 = c_row;
-      const int nj = s.e_t[t];
-      Window win;
+      const int jb = s.j0(t), nj = s.last(t), step = s.narrow() ? 2 : 1;
+      // 32 pages, one per lane: page, K scale, log2 of the V scale
+      int w_base = 0, w_pid = -1;
       float w_ks = 0.f, w_lv = 0.f;
       auto load_window = [&](int first) {
-        win.load(args, s, first);
-        w_ks = 0.f;
-        w_lv = 0.f;
-        if (win.pid >= 0) {
-          const long long sc = static_cast<long long>(win.pid) * args.Hkv + s.head;
+        w_base = first;
+        w_pid = page_of_lane(args, s.b, s.len, first);
+        w_ks = w_lv = 0.f;
+        if (w_pid >= 0) {
+          const long long sc = static_cast<long long>(w_pid) * args.Hkv + s.head;
           w_ks = __ldg(args.k_scale + sc);
           w_lv = static_cast<float>(scale_exp(__ldg(args.v_scale + sc)));
         }
       };
-      if (s.a < nj) load_window(s.a << pages_log);
-      for (int j = s.a; j < nj; ++j) {
-        if (((j + 1) << pages_log) - win.base > 32) load_window(j << pages_log);
-        float cg[4], lg[4];               // per 32 columns: exponent factor, log2 of the V scale
-        bool hole = false;                // a page that is not there
-#pragma unroll
-        for (int g = 0; g < 4; ++g) {
-          const int p = ((j * kBN + 32 * g) >> args.page_shift) - win.base;
-          const float ks = __shfl_sync(0xffffffffu, w_ks, p);
-          lg[g] = __shfl_sync(0xffffffffu, w_lv, p);
-          // positive, so that a masked score stays -inf (|S| < 2^26: what is
-          // lost is far below the last bit of a probability)
-          cg[g] = fmaxf(c0 * ks, 1e-37f);
-          hole |= __shfl_sync(0xffffffffu, win.pid, p) < 0;
-        }
+      if (jb < nj) load_window(jb << pages_log);
+      for (int j = jb; j < nj; j += step) {
+        if (((j + 1) << pages_log) - w_base > 32) load_window(j << pages_log);
+        // Per 32 columns: factor of the exponent (positive, so that a masked
+        // score stays -inf; |S| < 2^26, so what is lost is far below the last
+        // bit of a probability), log2 of the V scale, and keys to be seen.
+        const int kv0 = j * kBN;
+        const int p0 = (kv0 >> args.page_shift) - w_base;
+        auto page_at = [&](int g) { return p0 + (32 * g >> args.page_shift); };
+        auto cg_of = [&](int g) {
+          return fmaxf(c0 * __shfl_sync(0xffffffffu, w_ks, page_at(g)), 1e-37f);
+        };
+        auto lg_of = [&](int g) { return __shfl_sync(0xffffffffu, w_lv, page_at(g)); };
+        auto lim_of = [&](int g) {
+          return __shfl_sync(0xffffffffu, w_pid, page_at(g)) < 0 ? 0 : lim - kv0 - 32 * g;
+        };
+        const unsigned int missing = __ballot_sync(0xffffffffu, w_pid < 0);
+        const int p3 = page_at(3);
+        const bool hole = (missing >> p0 & (0xffffffffu >> (31 - (p3 - p0)))) != 0u;
+        const bool masked = __any_sync(0xffffffffu, kv0 + kBN > lim || hole);
         ok = __all_sync(0xffffffffu, mbar_wait(s_full(t), s_count & 1, wc, kWaitSFull));
         if (!ok) break;
         ++s_count;
         tc_fence_after();
+        // ---- scores, each 32 columns with their maximum
         uint32_t s0[32], s1[32], s2[32], s3[32];
-        float mg[4];
+        float mg[4], cg[4], lg[4];
         tmem_ld32_max(tS + 0, s0, mg[0]);
         tmem_ld32_max(tS + 32, s1, mg[1]);
         tmem_ld32_max(tS + 64, s2, mg[2]);
         tmem_ld32_max(tS + 96, s3, mg[3]);
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          cg[g] = cg_of(g);
+          lg[g] = lg_of(g);
+        }
         tmem_ld_wait32(s0);
         reg_fence32(s1);
         reg_fence32(s2);
@@ -457,25 +499,21 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int g = 0; g < 4; ++g) reg_fence1(mg[g]);
         uint32_t* sv[4] = {s0, s1, s2, s3};
-        const int kv0 = j * kBN;
-        if (__any_sync(0xffffffffu, kv0 + kBN > lim || hole)) {
-          const int lt = lim - kv0;
+        if (masked) {
 #pragma unroll
           for (int g = 0; g < 4; ++g) {
-            const int p = ((kv0 + 32 * g) >> args.page_shift) - win.base;
-            const int lh = __shfl_sync(0xffffffffu, win.pid, p) < 0 ? 0 : lt;
+            const int lh = lim_of(g);
             mg[g] = -INFINITY;
 #pragma unroll
             for (int i = 0; i < 32; ++i) {
-              if (g * 32 + i >= lh) sv[g][i] = __float_as_uint(-INFINITY);
+              if (i >= lh) sv[g][i] = __float_as_uint(-INFINITY);
               mg[g] = fmaxf(mg[g], __uint_as_float(sv[g][i]));
             }
           }
         }
-        float x[4];
-#pragma unroll
-        for (int g = 0; g < 4; ++g) x[g] = fmaf(mg[g], cg[g], lg[g]);
-        const float m_new = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
+        const float m_new = fmaxf(fmax3(fmaf(mg[0], cg[0], lg[0]), fmaf(mg[1], cg[1], lg[1]),
+                                        fmaf(mg[2], cg[2], lg[2])),
+                                  fmaf(mg[3], cg[3], lg[3]));
         const bool need = m_new > m_ref + kTau;
         const bool rescale = __any_sync(0xffffffffu, need);
         float alpha = 1.f;
@@ -485,13 +523,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           l *= alpha;
         }
         const float m_use = m_ref == -INFINITY ? 0.f : m_ref;
-        float rs[4];
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
           uint32_t pk[16];
           uint64_t e2 = 0ull;
-          const uint64_t c2 = splat2(cg[g]);
-          const uint64_t nm2 = splat2(lg[g] - m_use);
+          const uint64_t c2 = splat2(cg[g]), nm2 = splat2(lg[g] - m_use);
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
             uint32_t x0, x1;
@@ -505,27 +541,27 @@ __global__ void __launch_bounds__(kThreads, 1)
           tmem_st16(tS + 16 * g, pk);
           uint32_t u0, u1;
           unpack2(e2, u0, u1);
-          rs[g] = (__uint_as_float(u0) + __uint_as_float(u1)) * ex2_approx(-lg[g]);
+          l = fmaf(__uint_as_float(u0) + __uint_as_float(u1), ex2_approx(-lg[g]), l);
         }
-        if (rescale && j > s.a) {
+        if (rescale && j > jb) {
           // P V of the last tile has completed: it was issued before this S.
-          uint32_t o[D / 32][32];
-#pragma unroll
-          for (int ch = 0; ch < D / 32; ++ch) tmem_ld32(tO + 32 * ch, o[ch]);
-          tmem_ld_wait32(o[0]);
-#pragma unroll
-          for (int ch = 1; ch < D / 32; ++ch) reg_fence32(o[ch]);
           const uint64_t a2 = splat2(alpha);
+#pragma unroll 1
+          for (int ch = 0; ch < D / 32; ch += 2) {
+            uint32_t o0[32], o1[32];
+            tmem_ld32(tO + 32 * ch, o0);
+            tmem_ld32(tO + 32 * ch + 32, o1);
+            tmem_ld_wait32(o0);
+            reg_fence32(o1);
 #pragma unroll
-          for (int ch = 0; ch < D / 32; ++ch) {
-#pragma unroll
-            for (int i = 0; i < 16; ++i)
-              unpack2(fmul2(pack2(o[ch][2 * i], o[ch][2 * i + 1]), a2), o[ch][2 * i],
-                      o[ch][2 * i + 1]);
-            tmem_st32(tO + 32 * ch, o[ch]);
+            for (int i = 0; i < 16; ++i) {
+              unpack2(fmul2(pack2(o0[2 * i], o0[2 * i + 1]), a2), o0[2 * i], o0[2 * i + 1]);
+              unpack2(fmul2(pack2(o1[2 * i], o1[2 * i + 1]), a2), o1[2 * i], o1[2 * i + 1]);
+            }
+            tmem_st32(tO + 32 * ch, o0);
+            tmem_st32(tO + 32 * ch + 32, o1);
           }
         }
-        l += (rs[0] + rs[1]) + (rs[2] + rs[3]);
         tmem_st_wait();
         tc_fence_before();
         mbar_arrive(p_full(t));
@@ -533,65 +569,119 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok) break;
       // The next segment's Q: this tile's last S has been read, so its
       // product has left the buffer.
-      if (more && sn.e_t[t] > sn.a) c_row = load_q(sn);
+      if (!(ok = wait_seg(si + 1))) break;
+      if (!(seg_at(si + 1).flags & Seg::kLast) && seg_at(si + 1).active(t)) c_row = load_q(seg_at(si + 1));
 
       // ---- results
-      const long long slot = 2ll * cta + (s.starts ? 1 : 0);
-      if (nj == s.a) {
-        // Nothing for this row tile here (causality, or no rows at all): an
-        // empty part, where the unit has other parts.
-        if (!whole && on) {
-          float4* p = reinterpret_cast<float4*>(args.part_o + (slot * kUnitRows + t * kBM + r_tile) * D);
-          for (int i = 0; i < D / 4; ++i) p[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-          args.part_ml[slot * kUnitRows + t * kBM + r_tile] = make_float2(-INFINITY, 0.f);
+      const bool whole = s.whole();
+      const int rr = s.row(t, r_tile);
+      const bool on = rr < s.n * args.group;
+      const long long slot = 2ll * cta + (s.flags & Seg::kStarts);
+      float4* part = reinterpret_cast<float4*>(args.part_o + (slot * kUnitRows + t * kBM + r_tile) * D);
+      float2* part_ml = args.part_ml + slot * kUnitRows + t * kBM + r_tile;
+      if (jb >= nj) {
+        // Nothing for this row tile here (causality): an empty part.
+        if (!s.narrow() && !whole && on) {
+#pragma unroll 1
+          for (int i = 0; i < D / 4; ++i) part[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+          *part_ml = make_float2(-INFINITY, 0.f);
         }
+        done_seg(si);
         continue;
       }
       ok = __all_sync(0xffffffffu, mbar_wait(o_full(t), o_count & 1, wc, kWaitOFull));
       if (!ok) break;
       ++o_count;
       tc_fence_after();
-      if (!whole) {
-        float4* p = reinterpret_cast<float4*>(args.part_o + (slot * kUnitRows + t * kBM + r_tile) * D);
-#pragma unroll
+      // Narrow: slot 1 leaves its rows in the CTA's part of the workspace
+      // (16 bytes of 32 neighbouring rows side by side), slot 0 joins them.
+      float4* xch = args.xch_o + static_cast<long long>(cta) * kBM * (D / 4) + r_tile;
+      float2* xch_ml = args.xch_ml + cta * kBM + r_tile;
+      if (s.narrow() && t == 1) {
+        if (x_count > 0) {
+          ok = __all_sync(0xffffffffu, mbar_wait(x_empty, (x_count - 1) & 1, wc, kWaitDrain));
+          if (!ok) break;
+        }
+        ++x_count;
+#pragma unroll 1
         for (int ch = 0; ch < D / 32; ++ch) {
           uint32_t o[32];
           tmem_ld32(tO + 32 * ch, o);
           tmem_ld_wait32(o);
-          if (on) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-              p[8 * ch + i] = make_float4(__uint_as_float(o[4 * i]), __uint_as_float(o[4 * i + 1]),
-                                          __uint_as_float(o[4 * i + 2]), __uint_as_float(o[4 * i + 3]));
-          }
+          for (int i = 0; i < 8; ++i)
+            xch[(8 * ch + i) * kBM] = make_float4(__uint_as_float(o[4 * i]), __uint_as_float(o[4 * i + 1]),
+                                                  __uint_as_float(o[4 * i + 2]), __uint_as_float(o[4 * i + 3]));
         }
+        *xch_ml = make_float2(m_ref, l);
         tc_fence_before();
         mbar_arrive(o_empty(t));
-        if (on) args.part_ml[slot * kUnitRows + t * kBM + r_tile] = make_float2(m_ref, l);
+        mbar_arrive(x_full);
+        done_seg(si);
         continue;
       }
+      const bool joined = s.narrow() && s.e - s.a > 1;
+      float a0 = 1.f, a1 = 0.f;
+      if (joined) {
+        ok = __all_sync(0xffffffffu, mbar_wait(x_full, x_count & 1, wc, kWaitDrain));
+        if (!ok) break;
+        ++x_count;
+        const float2 x = *xch_ml;
+        const float m = fmaxf(m_ref, x.x), m0 = m == -INFINITY ? 0.f : m;
+        a0 = ex2_approx(m_ref - m0);
+        a1 = ex2_approx(x.x - m0);
+        // a row without any key keeps its zeros; a NaN stays one
+        l = l * a0 + x.y * a1;
+        m_ref = m;
+      }
+      // O in pieces of 64 columns.
       const float inv = l == 0.f ? 0.f : 1.f / l;
-      uint32_t pw[D / 2];
+      const int token = rr / args.group;
+      const long long out_row =
+          on ? (static_cast<long long>(s.r0 + token) * args.Hkv + s.head) * args.group +
+                   (rr - token * args.group)
+             : -1;
+      const int li = lane & 7;
+#pragma unroll 1
+      for (int h = 0; h < D / 64; ++h) {
+        uint32_t o[2][32];
+        tmem_ld32(tO + 64 * h, o[0]);
+        tmem_ld32(tO + 64 * h + 32, o[1]);
+        tmem_ld_wait32(o[0]);
+        reg_fence32(o[1]);
+        if (joined) {
 #pragma unroll
-      for (int ch = 0; ch < D / 32; ++ch) {
-        uint32_t o[32];
-        tmem_ld32(tO + 32 * ch, o);
-        tmem_ld_wait32(o);
+          for (int i = 0; i < 16; ++i) {
+            const float4 v = xch[(16 * h + i) * kBM];
+            const float f[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int z = 0; z < 4; ++z) {
+              uint32_t& x = o[i >> 3][4 * (i & 7) + z];
+              x = __float_as_uint(fmaf(f[z], a1, __uint_as_float(x) * a0));
+            }
+          }
+        }
+        if (!whole) {
+          if (on) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const uint32_t* x = &o[i >> 3][4 * (i & 7)];
+              part[16 * h + i] = make_float4(__uint_as_float(x[0]), __uint_as_float(x[1]),
+                                             __uint_as_float(x[2]), __uint_as_float(x[3]));
+            }
+          }
+          continue;
+        }
+        uint32_t pw[32];                  // the row as bf16 pairs; 16-byte chunk c = words 4 c ..
         const uint64_t i2 = splat2(inv);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
+        for (int i = 0; i < 32; ++i) {
           uint32_t y0, y1;
-          unpack2(fmul2(pack2(o[2 * i], o[2 * i + 1]), i2), y0, y1);
-          pw[16 * ch + i] = pack_bf16x2(__uint_as_float(y0), __uint_as_float(y1));
+          unpack2(fmul2(pack2(o[i >> 4][2 * (i & 15)], o[i >> 4][2 * (i & 15) + 1]), i2), y0, y1);
+          pw[i] = pack_bf16x2(__uint_as_float(y0), __uint_as_float(y1));
         }
-      }
-      tc_fence_before();
-      mbar_arrive(o_empty(t));
-      // Whole 128-byte lines: 8 lanes exchange 16-byte chunks, an 8 x 8
-      // transpose per 128 bytes, so that a warp store writes 4 lines.
-      const int li = lane & 7;
-#pragma unroll
-      for (int h = 0; h < D / 64; ++h) {
+        // Whole 128-byte lines: 8 lanes exchange 16-byte chunks, an 8 x 8
+        // transpose, so that a warp store writes 4 lines.
 #pragma unroll
         for (int dd = 4; dd >= 1; dd >>= 1) {
           const bool up = (li & dd) != 0;
@@ -600,30 +690,30 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (jj & dd) continue;
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
-              const uint32_t lo = pw[4 * (8 * h + jj) + q];
-              const uint32_t hi = pw[4 * (8 * h + jj + dd) + q];
+              const uint32_t lo = pw[4 * jj + q];
+              const uint32_t hi = pw[4 * (jj + dd) + q];
               const uint32_t got = __shfl_xor_sync(0xffffffffu, up ? lo : hi, dd);
-              pw[4 * (8 * h + jj) + q] = up ? got : lo;
-              pw[4 * (8 * h + jj + dd) + q] = up ? hi : got;
+              pw[4 * jj + q] = up ? got : lo;
+              pw[4 * (jj + dd) + q] = up ? hi : got;
             }
           }
         }
-      }
-      const long long out_row =
-          on ? (static_cast<long long>(s.r0 + token) * args.Hkv + s.head) * args.group +
-                   (rr - static_cast<long long>(token) * args.group)
-             : -1;
 #pragma unroll
-      for (int jj = 0; jj < 8; ++jj) {
-        const long long row = __shfl_sync(0xffffffffu, out_row, (lane & ~7) + jj);
-        if (row < 0) continue;
-#pragma unroll
-        for (int h = 0; h < D / 64; ++h)
-          __stcs(reinterpret_cast<uint4*>(args.o + row * D + 64 * h + 8 * li),
-                 make_uint4(pw[4 * (8 * h + jj)], pw[4 * (8 * h + jj) + 1], pw[4 * (8 * h + jj) + 2],
-                            pw[4 * (8 * h + jj) + 3]));
+        for (int jj = 0; jj < 8; ++jj) {
+          const long long row = __shfl_sync(0xffffffffu, out_row, (lane & ~7) + jj);
+          if (row >= 0)
+            __stcs(reinterpret_cast<uint4*>(args.o + row * D + 64 * h + 8 * li),
+                   make_uint4(pw[4 * jj], pw[4 * jj + 1], pw[4 * jj + 2], pw[4 * jj + 3]));
+        }
       }
-      if (on) args.lse[out_row] = l == 0.f ? -INFINITY : (m_ref + log2f(l)) * kLn2;
+      tc_fence_before();
+      mbar_arrive(o_empty(t));
+      if (joined) mbar_arrive(x_empty);
+      if (on) {
+        if (whole) args.lse[out_row] = l == 0.f ? -INFINITY : (m_ref + log2f(l)) * kLn2;
+        else *part_ml = make_float2(m_ref, l);
+      }
+      done_seg(si);
     }
   } else if (warp == kMmaWarp) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kCtrlRegs));
@@ -653,59 +743,101 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto wait_k = [&]() {
       return mbar_wait_warp(k_full(kc % C::kKStages), (kc / C::kKStages) & 1, wc, kWaitKvFull);
     };
-    Walker walk(args, pre, j0, j1);
-    Seg s;
-    bool ok = true;
-    while (ok && walk.next(s)) {
-      // first scores of both tiles
-      if (!(ok = wait_k())) break;
-      for (int t = 0; t < 2 && ok; ++t) {
-        if (s.e_t[t] <= s.a) continue;
-        ok = mbar_wait_warp(q_full(t), qc[t]++ & 1, wc, kWaitQFull);
-        if (!ok) break;
-        tc_fence_after();
-        issue_s(t);
+    // One segment, tiles [a, e), row tile t up to e_t.  Its bounds come
+    // through a shuffle, which tells the compiler that they are the same in
+    // every lane: MMAs issued under branches that it takes for divergent cost
+    // their issue several times over (measured: 5500 cycles a step of 32
+    // MMAs where the tensor core needs 2048).
+    auto uniform = [](int x) { return __shfl_sync(0xffffffffu, x, 0); };
+    auto run = [&](const int a, const int e, const int e0, const int e1) -> bool {
+      if (!wait_k()) return false;
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        if ((t ? e1 : e0) > a) {
+          if (!mbar_wait_warp(q_full(t), qc[t]++ & 1, wc, kWaitQFull)) return false;
+          tc_fence_after();
+          issue_s(t);
+        }
       }
-      if (!ok) break;
       mma_commit_w(k_empty(kc % C::kKStages));
       ++kc;
-      for (int j = s.a; j < s.e && ok; ++j) {
-        bool k_ready = false;
-        ok = mbar_wait_warp(h_full(hc & 1), (hc >> 1) & 1, wc, kWaitDsFull);
-        for (int t = 0; t < 2 && ok; ++t) {
-          if (j < s.e_t[t]) {
-            if (j == s.a && oc[t] > 0) {
-              ok = mbar_wait_warp(o_empty(t), (oc[t] - 1) & 1, wc, kWaitOFull);
-              if (!ok) break;
-            }
-            ok = mbar_wait_warp(p_full(t), pc[t]++ & 1, wc, kWaitPFull);
-            if (!ok) break;
+      for (int j = a; j < e; ++j) {
+        if (!mbar_wait_warp(h_full(hc & 1), (hc >> 1) & 1, wc, kWaitDsFull)) return false;
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          const int et = t ? e1 : e0;
+          // A K tile that neither row tile needs any more is taken all the same.
+          if (t == 0 && j + 1 < e && !wait_k()) return false;
+          if (j < et) {
+            if (j == a && oc[t] > 0 && !mbar_wait_warp(o_empty(t), (oc[t] - 1) & 1, wc, kWaitOFull))
+              return false;
+            if (!mbar_wait_warp(p_full(t), pc[t]++ & 1, wc, kWaitPFull)) return false;
             tc_fence_after();
-            issue_pv(t, j > s.a ? 1u : 0u);
-            if (j + 1 == s.e_t[t]) {
+            issue_pv(t, j > a ? 1u : 0u);
+            if (j + 1 == et) {
               mma_commit_w(o_full(t));
               ++oc[t];
             }
           }
-          if (j + 1 < s.e_t[t]) {
-            if (!k_ready) {
-              if (!(ok = wait_k())) break;
-              k_ready = true;
-              tc_fence_after();
-            }
-            issue_s(t);
-          }
+          if (j + 1 < et) issue_s(t);
         }
-        if (!ok) break;
         mma_commit_w(h_empty(hc & 1));
         ++hc;
-        if (j + 1 < s.e) {
-          // Both tiles may be done with their keys before the unit is: the K
-          // tile is then taken unread.
-          if (!k_ready && !(ok = wait_k())) break;
+        if (j + 1 < e) {
           mma_commit_w(k_empty(kc % C::kKStages));
           ++kc;
         }
+      }
+      return true;
+    };
+    // A narrow part of n key tiles: tile i is slot i & 1's.
+    auto run_narrow = [&](const int n) -> bool {
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        if (t < n) {
+          if (!wait_k()) return false;
+          if (!mbar_wait_warp(q_full(t), qc[t]++ & 1, wc, kWaitQFull)) return false;
+          tc_fence_after();
+          issue_s(t);
+          mma_commit_w(k_empty(kc % C::kKStages));
+          ++kc;
+        }
+      }
+      for (int i = 0; i < n; i += 2) {
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          if (i + t < n) {
+            if (!mbar_wait_warp(h_full(hc & 1), (hc >> 1) & 1, wc, kWaitDsFull)) return false;
+            if (i == 0 && oc[t] > 0 && !mbar_wait_warp(o_empty(t), (oc[t] - 1) & 1, wc, kWaitOFull))
+              return false;
+            if (i + t + 2 < n && !wait_k()) return false;
+            if (!mbar_wait_warp(p_full(t), pc[t]++ & 1, wc, kWaitPFull)) return false;
+            tc_fence_after();
+            issue_pv(t, i > 0 ? 1u : 0u);
+            mma_commit_w(h_empty(hc & 1));
+            ++hc;
+            if (i + t + 2 < n) {
+              issue_s(t);
+              mma_commit_w(k_empty(kc % C::kKStages));
+              ++kc;
+            } else {
+              mma_commit_w(o_full(t));
+              ++oc[t];
+            }
+          }
+        }
+      }
+      return true;
+    };
+    for (uint32_t si = 0; wait_seg(si); ++si) {
+      const Seg& s = seg_at(si);
+      const int flags = uniform(s.flags), a = uniform(s.a), e = uniform(s.e), e0 = uniform(s.e0);
+      if (flags & Seg::kLast) break;
+      done_seg(si);
+      if (flags & Seg::kNarrow) {
+        if (!run_narrow(e - a)) break;
+      } else {
+        if (!run(a, e, e0, e)) break;
       }
     }
     // No MMA may still be running when TMEM is released.
@@ -718,17 +850,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int per_log = 7 - args.page_shift, per = 1 << per_log;   // pages per key tile
     const uint32_t page_bytes = static_cast<uint32_t>(D) << args.page_shift;
     uint32_t kn = 0, vn = 0;              // K and V tiles asked for so far
-    Walker walk(args, pre, j0, j1);
-    Seg s{};
     bool ok = true;
-    while (ok && walk.next(s)) {
-      Window cur, nxt;
-      cur.load(args, s, s.a << per_log);
-      nxt.load(args, s, cur.base + 32);
+    for (uint32_t si = 0; ok && wait_seg(si); ++si) {
+      const Seg s = seg_at(si);
+      if (s.flags & Seg::kLast) break;
+      done_seg(si);
+      int base = s.a << per_log;          // 32 pages here, the next 32 on the way
+      int cur = page_of_lane(args, s.b, s.len, base), nxt = page_of_lane(args, s.b, s.len, base + 32);
       for (int j = s.a; j < s.e; ++j) {
-        if ((j << per_log) >= cur.base + 32) {
+        if ((j << per_log) >= base + 32) {
+          base += 32;
           cur = nxt;
-          nxt.load(args, s, cur.base + 32);
+          nxt = page_of_lane(args, s.b, s.len, base + 32);
         }
         int pid[4];
         uint32_t mask = 0u, bytes = 0u;
@@ -736,7 +869,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = 0; i < 4; ++i) {
           pid[i] = -1;
           if (i < per) {
-            pid[i] = __shfl_sync(0xffffffffu, cur.pid, (j << per_log) + i - cur.base);
+            pid[i] = __shfl_sync(0xffffffffu, cur, (j << per_log) + i - base);
             if (pid[i] >= 0) {
               mask |= ((1u << (4 >> per_log)) - 1u) << (i * (4 >> per_log));
               bytes += page_bytes;
@@ -772,23 +905,53 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++vn;
       }
     }
-    if (lane == 0) {
-      // What is to be joined: the unit that this CTA starts and others go on
-      // with (its last one).
-      const bool shared_unit = ok && j1 > j0 && s.starts && !s.ends;
-      args.rec[2 * cta] = shared_unit ? make_int4(s.r0, s.n, s.rb, s.head) : make_int4(0, 0, 0, 0);
-      if (shared_unit)
-        args.rec[2 * cta + 1] = make_int4(cta_of(W, G, j1 - (s.e - s.a) + s.nt - 1),
-                                          static_cast<int>(W), static_cast<int>(W >> 32), 0);
-    }
     // Every copy this warp started must have landed before the CTA exits.
     for (uint32_t r = kn > C::kKStages ? kn - C::kKStages : 0; r < kn; ++r)
       mbar_wait_drain(k_full(r % C::kKStages), (r / C::kKStages) & 1, args.wait_budget);
     for (uint32_t r = vn > C::kVStages ? vn - C::kVStages : 0; r < vn; ++r)
       mbar_wait_drain(v_full(r % C::kVStages), (r / C::kVStages) & 1, args.wait_budget);
     __syncwarp();
-  } else {
+  } else if (warp < kConvWarp0) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kCtrlRegs));
+    // ================================================================ schedule
+    if (warp == kWalkWarp) {
+      const long long j0 = cta_first(W, G, cta), j1 = cta_first(W, G, cta + 1);
+      Walker walk(args, pre, j0, j1);
+      Seg s{};
+      bool any = false;
+      for (uint32_t i = 0;; ++i) {
+        Seg x{};
+        const bool more = walk.next(x);
+        if (more) {
+          s = x;
+          any = true;
+        } else {
+          x.flags = Seg::kLast;
+        }
+        if (i >= kSegs && !mbar_wait_warp(seg_empty(i), (i / kSegs - 1) & 1, wc, kWaitSegment)) {
+          any = false;
+          break;
+        }
+        if (lane == 0) {
+          const_cast<Seg&>(seg_at(i)) = x;
+          mbar_arrive(seg_full(i));
+        }
+        __syncwarp();
+        if (!more) break;
+      }
+      if (lane == 0) {
+        // What is to be joined: the unit that this CTA starts and others go
+        // on with (its last one).
+        const bool shared_unit = any && (s.flags & (Seg::kStarts | Seg::kEnds)) == Seg::kStarts;
+        args.rec[2 * cta] = shared_unit ? make_int4(s.r0, s.n, s.rb, s.head) : make_int4(0, 0, 0, 0);
+        if (shared_unit)
+          args.rec[2 * cta + 1] = make_int4(cta_of(W, G, j1 - (s.e - s.a) + s.nt - 1),
+                                            static_cast<int>(W), static_cast<int>(W >> 32), 0);
+      }
+      __syncwarp();
+    }
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kConvRegs));
     // ================================================================ V to fp16
     // The fp16 tile is laid out as the P V product reads it: two chunks of 64
     // columns, rows of 128 bytes with the 128-byte swizzle.  A thread takes
@@ -796,16 +959,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     // neighbouring lanes two rows of four, so that their stores meet
     // different banks.
     constexpr int CH = D / 16;            // 16-byte chunks of a code row
-    constexpr int kIter = kBN * CH / 64;
-    const int ct = tid - 32 * 10;         // 0 .. 63
+    constexpr int kIter = kBN * CH / 128;
+    const int ct = tid - 32 * kConvWarp0;   // 0 .. 127
     auto row_of = [](int id) { return D == 128 ? (id >> 4) * 2 + (id >> 2 & 1) : id >> 2; };
     auto chunk_of = [](int id) { return D == 128 ? (id & 3) | (id >> 3 & 1) << 2 : id & 3; };
     uint32_t cnt = 0;
-    Walker walk(args, pre, j0, j1);
-    Seg s;
     bool ok = true;
-    while (ok && walk.next(s)) {
-      for (int j = s.a; j < s.e; ++j) {
+    for (uint32_t si = 0; ok && wait_seg(si); ++si) {
+      const int a = seg_at(si).a, e = seg_at(si).e, len = seg_at(si).len, flags = seg_at(si).flags;
+      if (flags & Seg::kLast) break;
+      done_seg(si);
+      for (int j = a; j < e; ++j) {
         const uint32_t st = cnt % C::kVStages, hs = cnt & 1;
         if (!mbar_wait_warp(v_full(st), (cnt / C::kVStages) & 1, wc, kWaitKvFull) ||
             (cnt > 1 && !mbar_wait_warp(h_empty(hs), ((cnt >> 1) - 1) & 1, wc, kWaitMmaDone))) {
@@ -815,14 +979,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t src = sbase + C::kVOff + st * C::kCodeTile;
         const uint32_t dst = sbase + C::kHOff + hs * C::kHalfTile;
         const uint32_t mask = valid[st];
-        const int left = s.len - j * kBN;          // keys of the tile that exist
+        const int left = len - j * kBN;            // keys of the tile that exist
         const bool edge = left < kBN || mask != 0xfu;
-#pragma unroll
+        // Not unrolled: the kernel's roles share the instruction caches, and
+        // 6 KB of straight-line conversion here made every one of them wait
+        // for instructions (measured: 2 x 2048 rows on 16384 keys 1142 us
+        // unrolled, 767 us so).
+#pragma unroll 1
         for (int i0 = 0; i0 < kIter; i0 += 4) {
           uint4 w[4];
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const int id = ct + 64 * (i0 + i), row = row_of(id), c = chunk_of(id);
+            const int id = ct + 128 * (i0 + i), row = row_of(id), c = chunk_of(id);
             w[i] = ld_shared_v4(src + code_off<D>(row, c));
             // Slots behind the end and pages that were not loaded hold
             // anything, NaN codes too.
@@ -830,15 +998,16 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const int id = ct + 64 * (i0 + i), row = row_of(id), c = chunk_of(id);
+            const int id = ct + 128 * (i0 + i), row = row_of(id), c = chunk_of(id);
             const uint32_t base = dst + (c >> 2) * C::kHalfChunk + row * 128;
             const int c2 = 2 * (c & 3);            // 16-byte chunk of the fp16 row
-            st_shared_v4(base + ((c2 ^ (row & 7)) << 4), e4m3x2_to_f16x2(w[i].x),
-                         e4m3x2_to_f16x2(w[i].x >> 16), e4m3x2_to_f16x2(w[i].y),
-                         e4m3x2_to_f16x2(w[i].y >> 16));
-            st_shared_v4(base + (((c2 + 1) ^ (row & 7)) << 4), e4m3x2_to_f16x2(w[i].z),
-                         e4m3x2_to_f16x2(w[i].z >> 16), e4m3x2_to_f16x2(w[i].w),
-                         e4m3x2_to_f16x2(w[i].w >> 16));
+            uint4 x, y;
+            e4m3x4_to_f16x4(w[i].x, x.x, x.y);
+            e4m3x4_to_f16x4(w[i].y, x.z, x.w);
+            e4m3x4_to_f16x4(w[i].z, y.x, y.y);
+            e4m3x4_to_f16x4(w[i].w, y.z, y.w);
+            st_shared_v4(base + ((c2 ^ (row & 7)) << 4), x.x, x.y, x.z, x.w);
+            st_shared_v4(base + (((c2 + 1) ^ (row & 7)) << 4), y.x, y.y, y.z, y.w);
           }
         }
         fence_proxy_async_smem();

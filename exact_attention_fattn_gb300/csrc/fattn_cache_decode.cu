@@ -408,8 +408,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             w[0] = x.x; w[1] = x.y; w[2] = x.z; w[3] = x.w;
           }
 #pragma unroll
-          for (int kk = 0; kk < kK; ++kk)
-            mma_f16(s[n], qa[kk], e4m3x2_to_f16x2(w[kk]), e4m3x2_to_f16x2(w[kk] >> 16));
+          for (int kk = 0; kk < kK; ++kk) {
+            uint32_t b0, b1;
+            e4m3x4_to_f16x4(w[kk], b0, b1);
+            mma_f16(s[n], qa[kk], b0, b1);
+          }
         }
         // ---- exponents, mask, running maximum
         const float f0 = cs[0] * t.ks, f1 = cs[1] * t.ks;
@@ -496,10 +499,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t e1 = __byte_perm(w[0][z], w[1][z], 0x7362);
             const uint32_t g0 = __byte_perm(w[2][z], w[3][z], 0x5140);
             const uint32_t g1 = __byte_perm(w[2][z], w[3][z], 0x7362);
-            mma_f16(o[4 * z], pa[kk], e4m3x2_to_f16x2(e0), e4m3x2_to_f16x2(g0));
-            mma_f16(o[4 * z + 1], pa[kk], e4m3x2_to_f16x2(e0 >> 16), e4m3x2_to_f16x2(g0 >> 16));
-            mma_f16(o[4 * z + 2], pa[kk], e4m3x2_to_f16x2(e1), e4m3x2_to_f16x2(g1));
-            mma_f16(o[4 * z + 3], pa[kk], e4m3x2_to_f16x2(e1 >> 16), e4m3x2_to_f16x2(g1 >> 16));
+            uint32_t b0, b1, b2, b3, c0, c1, c2, c3;
+            e4m3x4_to_f16x4(e0, b0, b1);
+            e4m3x4_to_f16x4(e1, b2, b3);
+            e4m3x4_to_f16x4(g0, c0, c1);
+            e4m3x4_to_f16x4(g1, c2, c3);
+            mma_f16(o[4 * z], pa[kk], b0, c0);
+            mma_f16(o[4 * z + 1], pa[kk], b1, c1);
+            mma_f16(o[4 * z + 2], pa[kk], b2, c2);
+            mma_f16(o[4 * z + 3], pa[kk], b3, c3);
           }
         }
       }

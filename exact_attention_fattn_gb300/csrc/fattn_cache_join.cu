@@ -1,6 +1,13 @@
 // Second kernel of the attention over the paged 8-bit cache: units whose keys
 // several CTAs shared are put together from the parts they left in the
-// workspace (unnormalised rows of O in fp32, reference maximum and sum).
+// workspace (unnormalised rows of O in fp32, reference maximum and sum), in
+// the order of their keys.
+//
+// Bound: latency where a unit has many parts (one long sequence: up to 152 of
+// them), bytes where units are large (256 rows, two or three parts each).  A
+// thread has 4 columns of a row; the rows of a block are 4 for the small
+// units, whose parts are walked by four groups side by side, and 32 for the
+// large ones, walked by one.
 #include "fattn_cache.cuh"
 
 namespace fattn {
@@ -9,72 +16,79 @@ namespace {
 
 constexpr float kLn2 = 0.69314718055994530942f;
 
-// Joins the partial results of the units that several CTAs share, in the
-// order of their keys: block (c, y) takes two rows of the unit that goes on
-// after CTA c.  Four groups of D / 4 threads a row walk the parts.
+struct Part {
+  float m, l;
+  float4 o;
+};
+
+__device__ __forceinline__ void merge(Part& a, const Part& b) {
+  const float m = fmaxf(a.m, b.m), m0 = m == -INFINITY ? 0.f : m;
+  const float x = ex2_approx(a.m - m0), y = ex2_approx(b.m - m0);
+  a.m = m;
+  a.l = fmaf(a.l, x, b.l * y);
+  a.o.x = fmaf(a.o.x, x, b.o.x * y);
+  a.o.y = fmaf(a.o.y, x, b.o.y * y);
+  a.o.z = fmaf(a.o.z, x, b.o.z * y);
+  a.o.w = fmaf(a.o.w, x, b.o.w * y);
+}
+
+// Block (c, y): rows [y R, y R + R) of the unit that CTA c starts and others go
+// on with.
 template <int D, int ROWS>
-__global__ void __launch_bounds__(2 * D) join_kernel(const CacheAttnArgs a) {
-  constexpr int kF4 = D / 4, kGroups = 4, kRowsPerBlock = 2;
-  static_assert(kF4 * kGroups * kRowsPerBlock == 2 * D, "threads");
-  __shared__ float4 part[kGroups][kRowsPerBlock][kF4];
-  __shared__ float2 pml[kGroups][kRowsPerBlock];
+struct JoinCfg {
+  static constexpr int kF4 = D / 4;                            // threads per row
+  static constexpr int kGroups = ROWS == kDecodeRows ? 4 : 1;
+  static constexpr int kRows = ROWS == kDecodeRows ? 4 : 32;   // rows per block
+  static constexpr int kPerThread = ROWS == kDecodeRows ? 1 : 4;   // rows a thread takes in turn
+  static constexpr int kThreads = kF4 * kGroups * (kRows / kPerThread);
+};
+
+template <int D, int ROWS>
+__global__ void __launch_bounds__(JoinCfg<D, ROWS>::kThreads) join_kernel(const CacheAttnArgs a) {
+  using J = JoinCfg<D, ROWS>;
+  __shared__ Part side[J::kGroups][J::kRows / J::kPerThread][J::kF4];
   const int cta = blockIdx.x, G = a.grid;
   const int4 rec = a.rec[2 * cta];
-  if (rec.y == 0) return;                            // nothing shared from here
+  const int rows = rec.y * a.group - rec.z * ROWS;   // of the unit, from its first
+  if (rec.y == 0 || static_cast<int>(blockIdx.y) * J::kRows >= rows) return;
   const int4 more = a.rec[2 * cta + 1];
   const long long W = (static_cast<long long>(more.z) << 32) | static_cast<unsigned int>(more.y);
-  const int q4 = threadIdx.x % kF4, local = threadIdx.x / kF4 % kRowsPerBlock;
-  const int group = threadIdx.x / (kF4 * kRowsPerBlock);
-  const int row = blockIdx.y * kRowsPerBlock + local;
-  const long long rr = static_cast<long long>(rec.z) * ROWS + row;
-  const bool on = rr < static_cast<long long>(rec.y) * a.group;
-  float m = -INFINITY, l = 0.f;
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int p = cta + group; on && p <= more.x; p += kGroups) {
-    if (cta_first(W, G, p) == cta_first(W, G, p + 1)) continue;   // a CTA without work
-    const long long slot = 2ll * p + (p == cta ? 1 : 0);
-    const float2 x = a.part_ml[slot * ROWS + row];
-    const float4 v = *reinterpret_cast<const float4*>(a.part_o + (slot * ROWS + row) * D + 4 * q4);
-    const float n = fmaxf(m, x.x);
-    const float b0 = n == -INFINITY ? 1.f : ex2_approx(m - n);
-    const float b1 = n == -INFINITY ? 1.f : ex2_approx(x.x - n);
-    m = n;
-    l = fmaf(l, b0, x.y * b1);
-    acc.x = fmaf(acc.x, b0, v.x * b1);
-    acc.y = fmaf(acc.y, b0, v.y * b1);
-    acc.z = fmaf(acc.z, b0, v.z * b1);
-    acc.w = fmaf(acc.w, b0, v.w * b1);
-  }
-  part[group][local][q4] = acc;
-  if (q4 == 0) pml[group][local] = make_float2(m, l);
-  __syncthreads();
-  if (group != 0 || !on) return;
+  const int q4 = threadIdx.x % J::kF4, local = threadIdx.x / J::kF4 % (J::kRows / J::kPerThread);
+  const int group = threadIdx.x / (J::kF4 * (J::kRows / J::kPerThread));
 #pragma unroll
-  for (int g = 1; g < kGroups; ++g) {
-    const float2 x = pml[g][local];
-    const float4 v = part[g][local][q4];
-    const float n = fmaxf(m, x.x);
-    const float b0 = n == -INFINITY ? 1.f : ex2_approx(m - n);
-    const float b1 = n == -INFINITY ? 1.f : ex2_approx(x.x - n);
-    m = n;
-    l = fmaf(l, b0, x.y * b1);
-    acc.x = fmaf(acc.x, b0, v.x * b1);
-    acc.y = fmaf(acc.y, b0, v.y * b1);
-    acc.z = fmaf(acc.z, b0, v.z * b1);
-    acc.w = fmaf(acc.w, b0, v.w * b1);
+  for (int z = 0; z < J::kPerThread; ++z) {
+    const int row = blockIdx.y * J::kRows + z * (J::kRows / J::kPerThread) + local;
+    const bool on = row < min(rows, ROWS);
+    Part p{-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
+    for (int c = cta + group; on && c <= more.x; c += J::kGroups) {
+      if (cta_first(W, G, c) == cta_first(W, G, c + 1)) continue;   // a CTA without work
+      const long long at = (2ll * c + (c == cta ? 1 : 0)) * ROWS + row;
+      const float2 ml = __ldg(a.part_ml + at);
+      merge(p, Part{ml.x, ml.y, __ldg(reinterpret_cast<const float4*>(a.part_o + at * D) + q4)});
+    }
+    if constexpr (J::kGroups > 1) {
+      side[group][local][q4] = p;
+      __syncthreads();
+      if (group != 0) return;
+#pragma unroll
+      for (int g = 1; g < J::kGroups; ++g) merge(p, side[g][local][q4]);
+    }
+    if (!on) continue;
+    const int rr = rec.z * ROWS + row, token = rr / a.group;
+    const long long out = (static_cast<long long>(rec.x + token) * a.Hkv + rec.w) * a.group +
+                          (rr - token * a.group);
+    const float inv = p.l == 0.f ? 0.f : 1.f / p.l;
+    *reinterpret_cast<uint2*>(a.o + out * D + 4 * q4) =
+        make_uint2(pack_bf16x2(p.o.x * inv, p.o.y * inv), pack_bf16x2(p.o.z * inv, p.o.w * inv));
+    if (q4 == 0) a.lse[out] = p.l == 0.f ? -INFINITY : (p.m + log2f(p.l)) * kLn2;
   }
-  const int token = static_cast<int>(rr / a.group);
-  const long long at = (static_cast<long long>(rec.x + token) * a.Hkv + rec.w) * a.group +
-                       (rr - static_cast<long long>(token) * a.group);
-  const float inv = l == 0.f ? 0.f : 1.f / l;
-  *reinterpret_cast<uint2*>(a.o + at * D + 4 * q4) =
-      make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
-  if (q4 == 0) a.lse[at] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
 }
 
 template <int D, int ROWS>
 cudaError_t launch_t(const CacheAttnArgs& a, cudaStream_t stream) {
-  join_kernel<D, ROWS><<<dim3(a.grid, ROWS / 2), 2 * D, 0, stream>>>(a);
+  using J = JoinCfg<D, ROWS>;
+  static_assert(J::kThreads <= 1024, "block size");
+  join_kernel<D, ROWS><<<dim3(a.grid, ROWS / J::kRows), J::kThreads, 0, stream>>>(a);
   return cudaGetLastError();
 }
 

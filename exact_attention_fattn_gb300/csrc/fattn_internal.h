@@ -162,6 +162,8 @@ struct CacheAttnArgs {
   float* part_o;              // workspace: partial outputs of the units that CTAs share
   float2* part_ml;
   int4* rec;
+  float4* xch_o;              // tcgen05 kernel: exchange between a CTA's two softmax warpgroups
+  float2* xch_ml;
   int grid;                   // CTAs of the main kernel
   DeviceStatus* status;
   long long wait_budget;

@@ -34,6 +34,7 @@ enum WaitSite : unsigned int {
   kWaitDqEmpty = 12,
   kWaitDpFull = 13,
   kWaitDqOrder = 14,
+  kWaitSegment = 15,
 };
 
 constexpr unsigned int kStatusTimeout = 4;  // == FATTN_ERR_TIMEOUT
