@@ -77,12 +77,13 @@ CacheSeqs seqs_of(const int* page_table, const int* q_start, const int* kv_len, 
 size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 
 // Partial results of the units that CTAs share, two per CTA, and, for the
-// tcgen05 kernel, half a unit's rows per CTA to pass between its warpgroups.
+// tcgen05 kernel, half a unit's rows per CTA to pass between its warpgroups
+// and the call's q_rows queries in two parts.
 struct AttnWorkspace {
-  size_t o_off, ml_off, rec_off, xo_off, xml_off, total;
+  size_t o_off, ml_off, rec_off, xo_off, xml_off, q_off, qs_off, total;
 };
 
-AttnWorkspace attn_workspace(int rows, int d) {
+AttnWorkspace attn_workspace(int rows, int d, size_t q_rows) {
   AttnWorkspace w;
   const size_t slots = 2 * static_cast<size_t>(kCacheMaxCtas) * rows;
   w.o_off = 0;
@@ -91,7 +92,10 @@ AttnWorkspace attn_workspace(int rows, int d) {
   w.xo_off = w.rec_off + align256(2 * kCacheMaxCtas * sizeof(int4));
   const size_t xch = rows == kChunkRows ? static_cast<size_t>(kCacheMaxCtas) * (kChunkRows / 2) : 0;
   w.xml_off = w.xo_off + align256(xch * d * sizeof(float));
-  w.total = w.xml_off + align256(xch * sizeof(float2));
+  w.q_off = w.xml_off + align256(xch * sizeof(float2));
+  if (rows != kChunkRows) q_rows = 0;
+  w.qs_off = w.q_off + 2 * align256(q_rows * d);
+  w.total = w.qs_off + align256(q_rows * sizeof(float));
   return w;
 }
 
@@ -172,7 +176,9 @@ size_t fattn_cache_fwd_workspace_bytes(int T, int B, int Hq, int Hkv, int d, int
   if (T <= 0 || B <= 0 || B > kMaxSeqs || Hkv <= 0 || Hkv > kMaxKvHeads || Hq <= 0 ||
       Hq % Hkv != 0 || Hq / Hkv > kMaxGroup || (d != 64 && d != 128) || n_selected < 0)
     return 0;
-  return attn_workspace(few_rows(T, B, Hq / Hkv, n_selected) ? kDecodeRows : kChunkRows, d).total;
+  return attn_workspace(few_rows(T, B, Hq / Hkv, n_selected) ? kDecodeRows : kChunkRows, d,
+                        static_cast<size_t>(T) * Hq)
+      .total;
 }
 
 int fattn_cache_fwd(const fattn_cache* cache, const void* q, long long q_row, void* o, float* lse,
@@ -213,13 +219,17 @@ int fattn_cache_fwd(const fattn_cache* cache, const void* q, long long q_row, vo
   a.scale_log2 = scale * 1.4426950408889634f;
   const bool few = few_rows(T, B, a.group, n_selected);
   const int unit_rows = few ? kDecodeRows : kChunkRows, piece_keys = few ? 256 : 128;
-  const AttnWorkspace w = attn_workspace(unit_rows, cache->d);
+  const size_t q_rows = static_cast<size_t>(T) * Hq;
+  const AttnWorkspace w = attn_workspace(unit_rows, cache->d, q_rows);
   char* base = static_cast<char*>(workspace);
   a.part_o = reinterpret_cast<float*>(base + w.o_off);
   a.part_ml = reinterpret_cast<float2*>(base + w.ml_off);
   a.rec = reinterpret_cast<int4*>(base + w.rec_off);
   a.xch_o = reinterpret_cast<float4*>(base + w.xo_off);
   a.xch_ml = reinterpret_cast<float2*>(base + w.xml_off);
+  a.q_codes = reinterpret_cast<uint8_t*>(base + w.q_off);
+  a.q_lo = static_cast<long long>(align256(q_rows * cache->d));
+  a.q_scale = reinterpret_cast<float*>(base + w.qs_off);
   int dev = 0, sms = 0;
   if (cudaGetDevice(&dev) != cudaSuccess ||
       cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)

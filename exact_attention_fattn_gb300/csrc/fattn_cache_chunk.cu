@@ -11,7 +11,8 @@
 //     is the sum of two e4m3 rows: hi = e4m3(x), lo = e4m3(x - hi), exact for
 //     entries down to 2^-9 of the row's largest and off by at most 2^-10 of
 //     224 below.  Two products at twice the 16-bit rate cost what one 16-bit
-//     product would, and K needs no conversion.
+//     product would, and K needs no conversion.  A kernel in front splits Q
+//     once and lays its rows out as the products read them.
 //   O += P V    in fp16 (kind::f16): probabilities to fp16 in tensor memory
 //     (one rounding, 2^-11), V's codes to fp16, exactly, by two converter
 //     warps between the TMA ring and the MMA's tiles.  An e4m3 P would lose
@@ -31,10 +32,10 @@
 // tiles causality cuts off; units that CTAs share are joined from partial
 // results in a second kernel, in order.
 //
-// Warps: 0-3 softmax of row tile 0, 4-7 of row tile 1 (they also bring their
-// rows of Q in, as hi and lo parts), 8 tensor memory and MMA issue, 9 TMA, 10 the
-// walk over the CTA's share (it publishes one segment after the other in
-// shared memory, so that no other role holds the schedule in registers), 11
+// Warps: 0-3 softmax of row tile 0, 4-7 of row tile 1, 8 tensor memory and MMA
+// issue, 9 loads, 10 the walk over the CTA's share (it publishes one segment
+// after the other in shared memory, so that no other role holds the schedule
+// in registers), 11
 // idle, 12-15 conversion of V.  TMEM: S_t [128 t, 128 t + 128), P aliases S, O_t at 256 + d t.
 #include <cuda_fp16.h>
 
@@ -81,8 +82,8 @@ struct ChunkCfg {
   static constexpr int kBarOff = kHOff + 2 * kHalfTile;
   // k_full[] k_empty[] v_full[] v_empty[] h_full[2] h_empty[2] q_full[2]
   // s_full[2] p_full[2] o_full[2] o_empty[2] mma_done x_full x_empty
-  // seg_full[] seg_empty[]
-  static constexpr int kNumBars = 2 * kKStages + 2 * kVStages + 17 + 2 * kSegs;
+  // seg_full[] seg_empty[] q_empty[2]
+  static constexpr int kNumBars = 2 * kKStages + 2 * kVStages + 17 + 2 * kSegs + 2;
   static constexpr int kMiscOff = kBarOff + kNumBars * 8;   // tmem, abort, valid[kVStages]
   static constexpr int kSegOff = (kMiscOff + 32 + 15) / 16 * 16;
   static constexpr int kPreOff = kSegOff + kSegs * 64;      // [B + 1] int
@@ -146,6 +147,10 @@ struct __align__(16) Seg {
   __device__ __forceinline__ int j0(int t) const { return narrow() ? a + t : a; }
   __device__ __forceinline__ int last(int t) const { return t == 0 ? e0 : e; }
   __device__ __forceinline__ bool active(int t) const { return j0(t) < last(t); }
+  // First row of the (sequence, head) in the split Q.
+  __device__ __forceinline__ long long q_row(const CacheAttnArgs& a) const {
+    return (static_cast<long long>(r0) * a.Hkv + static_cast<long long>(head) * n) * a.group;
+  }
   // Row of the sequence's n * group of thread r of slot t (T * Hq < 2^31).
   __device__ __forceinline__ int row(int t, int r) const {
     return rb * kUnitRows + (narrow() ? 0 : t * kBM) + r;
@@ -271,6 +276,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t mma_done = rest + 112u, x_full = rest + 120u, x_empty = rest + 128u;
   auto seg_full = [&](uint32_t i) { return rest + 136u + 8u * (i % kSegs); };
   auto seg_empty = [&](uint32_t i) { return rest + 136u + 8u * (kSegs + i % kSegs); };
+  auto q_empty = [&](uint32_t t) { return rest + 136u + 16u * kSegs + 8u * t; };
   const Seg* segs = reinterpret_cast<const Seg*>(smem + C::kSegOff);   // 64 bytes apart
   auto seg_at = [&](uint32_t i) -> const Seg& {
     return *reinterpret_cast<const Seg*>(reinterpret_cast<const uint8_t*>(segs) + 64u * (i % kSegs));
@@ -294,7 +300,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int t = 0; t < 2; ++t) {
       mbar_init(h_full(t), 4);
       mbar_init(h_empty(t), 1);
-      mbar_init(q_full(t), 4);
+      mbar_init(q_full(t), 1);
+      mbar_init(q_empty(t), 1);
       mbar_init(s_full(t), 1);
       mbar_init(p_full(t), 128);
       mbar_init(o_full(t), 1);
@@ -373,75 +380,26 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t lane_off = static_cast<uint32_t>(wq * 32) << 16;
     const uint32_t tS = tmem + lane_off + C::col_s(t);
     const uint32_t tO = tmem + lane_off + C::col_o(t);
-    const uint32_t q_smem = sbase + C::kQOff + t * C::kQBytes;
     const int pages_log = 7 - args.page_shift;   // log2 of the pages per key tile
     uint32_t s_count = 0, o_count = 0, x_count = 0;
     bool ok = true;
 
-    // This thread's row of the segment's Q, split into e4m3 parts; returns
-    // log2(e) * scale times the power of two that was taken out.
-    auto load_q = [&](const Seg& s) -> float {
-      const int rr = s.row(t, r_tile);
-      const bool on = rr < s.n * args.group;
-      uint4 w[D / 8];
-#pragma unroll
-      for (int i = 0; i < D / 8; ++i) w[i] = make_uint4(0u, 0u, 0u, 0u);
-      if (on) {
-        const int token = rr / args.group;
-        const uint4* p = reinterpret_cast<const uint4*>(
-            args.q + (s.r0 + token) * args.q_row + (s.head * args.group + rr - token * args.group) * D);
-#pragma unroll
-        for (int i = 0; i < D / 8; ++i) w[i] = __ldg(p + i);
-      }
-      uint32_t mx = 0u;                  // largest magnitude's bf16 bits
-#pragma unroll
-      for (int i = 0; i < D / 8; ++i) {
-        const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
-#pragma unroll
-        for (int z = 0; z < 4; ++z) mx = max(mx, max(u[z] & 0x7fffu, (u[z] >> 16) & 0x7fffu));
-      }
-      // x = q * 2^(8 - E) <= 448 where the mantissa is at most 1.75, one less above
-      const int e = static_cast<int>(mx >> 7) - 127 - 8 + ((mx & 0x7fu) > 0x60u ? 1 : 0);
-      const int ec = max(-126, min(126, e));
-      // a row with an infinity or a NaN becomes NaN
-      const float down = mx >= 0x7f80u ? __int_as_float(0x7fffffff) : exp2i(-ec);
-#pragma unroll
-      for (int i = 0; i < D / 16; ++i) {   // 16 columns: one 16-byte chunk of codes
-        uint32_t hi[4], lo[4];
-#pragma unroll
-        for (int z = 0; z < 4; ++z) {
-          const uint4 v = w[2 * i + (z >> 1)];
-          const uint32_t a0 = z & 1 ? v.z : v.x, a1 = z & 1 ? v.w : v.y;
-          const float x0 = __uint_as_float(a0 << 16) * down, x1 = __uint_as_float(a0 & 0xffff0000u) * down;
-          const float x2 = __uint_as_float(a1 << 16) * down, x3 = __uint_as_float(a1 & 0xffff0000u) * down;
-          hi[z] = pack_e4m3x4(x0, x1, x2, x3);
-          const float4 h = e4m3x4_to_f32x4(hi[z]);
-          lo[z] = pack_e4m3x4(x0 - h.x, x1 - h.y, x2 - h.z, x3 - h.w);
-        }
-        st_shared_v4(q_smem + code_off<D>(r_tile, i), hi[0], hi[1], hi[2], hi[3]);
-        st_shared_v4(q_smem + C::kCodeTile + code_off<D>(r_tile, i), lo[0], lo[1], lo[2], lo[3]);
-      }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(q_full(t));
-      return args.scale_log2 * exp2i(ec);
-    };
-
-    uint32_t si = 0;                      // segment
-    float c_row = 0.f;
-    ok = wait_seg(0);
-    if (ok && !(seg_at(0).flags & Seg::kLast) && seg_at(0).active(t)) c_row = load_q(seg_at(0));
-    for (; ok && !(seg_at(si).flags & Seg::kLast); ++si) {
+    for (uint32_t si = 0; ok; ++si) {
+      if (!(ok = wait_seg(si))) break;
       const Seg& s = seg_at(si);
+      if (s.flags & Seg::kLast) break;
       // Keys the row sees.  Rows past the unit's last see all (their queries
       // are zero), so that they need no mask.
       int lim = s.len;
-      if (args.causal) {
+      float m_ref = -INFINITY, l = 0.f, c0 = 1.f;
+      {
         const int rr = s.row(t, r_tile);
-        if (rr < s.n * args.group) lim = max(0, min(s.len, s.len - s.n + rr / args.group + 1));
+        if (rr < s.n * args.group) {
+          if (args.causal) lim = max(0, min(s.len, s.len - s.n + rr / args.group + 1));
+          // log2(e) * scale times the power of two taken out of the row
+          c0 = args.scale_log2 * __ldg(args.q_scale + s.q_row(args) + rr);
+        }
       }
-      float m_ref = -INFINITY, l = 0.f;
-      const float c0 = c_row;
       const int jb = s.j0(t), nj = s.last(t), step = s.narrow() ? 2 : 1;
       // 32 pages, one per lane: page, K scale, log2 of the V scale
       int w_base = 0, w_pid = -1;
@@ -567,11 +525,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_arrive(p_full(t));
       }
       if (!ok) break;
-      // The next segment's Q: this tile's last S has been read, so its
-      // product has left the buffer.
-      if (!(ok = wait_seg(si + 1))) break;
-      if (!(seg_at(si + 1).flags & Seg::kLast) && seg_at(si + 1).active(t)) c_row = load_q(seg_at(si + 1));
-
       // ---- results
       const bool whole = s.whole();
       const int rr = s.row(t, r_tile);
@@ -634,76 +587,44 @@ __global__ void __launch_bounds__(kThreads, 1)
         l = l * a0 + x.y * a1;
         m_ref = m;
       }
-      // O in pieces of 64 columns.
+      // O, 32 columns at a time; compact on purpose (this code is out of the
+      // instruction caches whenever it runs).
       const float inv = l == 0.f ? 0.f : 1.f / l;
       const int token = rr / args.group;
       const long long out_row =
-          on ? (static_cast<long long>(s.r0 + token) * args.Hkv + s.head) * args.group +
-                   (rr - token * args.group)
-             : -1;
-      const int li = lane & 7;
+          (static_cast<long long>(s.r0 + token) * args.Hkv + s.head) * args.group + (rr - token * args.group);
 #pragma unroll 1
-      for (int h = 0; h < D / 64; ++h) {
-        uint32_t o[2][32];
-        tmem_ld32(tO + 64 * h, o[0]);
-        tmem_ld32(tO + 64 * h + 32, o[1]);
-        tmem_ld_wait32(o[0]);
-        reg_fence32(o[1]);
+      for (int ch = 0; ch < D / 32; ++ch) {
+        uint32_t o[32];
+        tmem_ld32(tO + 32 * ch, o);
+        tmem_ld_wait32(o);
         if (joined) {
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const float4 v = xch[(16 * h + i) * kBM];
+          for (int i = 0; i < 8; ++i) {
+            const float4 v = xch[(8 * ch + i) * kBM];
             const float f[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-            for (int z = 0; z < 4; ++z) {
-              uint32_t& x = o[i >> 3][4 * (i & 7) + z];
-              x = __float_as_uint(fmaf(f[z], a1, __uint_as_float(x) * a0));
-            }
+            for (int z = 0; z < 4; ++z)
+              o[4 * i + z] = __float_as_uint(fmaf(f[z], a1, __uint_as_float(o[4 * i + z]) * a0));
           }
         }
-        if (!whole) {
-          if (on) {
+        if (!on) continue;
+        if (whole) {
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const uint32_t* x = &o[i >> 3][4 * (i & 7)];
-              part[16 * h + i] = make_float4(__uint_as_float(x[0]), __uint_as_float(x[1]),
-                                             __uint_as_float(x[2]), __uint_as_float(x[3]));
-            }
+          for (int i = 0; i < 4; ++i) {
+            uint32_t w[4];
+#pragma unroll
+            for (int z = 0; z < 4; ++z)
+              w[z] = pack_bf16x2(__uint_as_float(o[8 * i + 2 * z]) * inv,
+                                 __uint_as_float(o[8 * i + 2 * z + 1]) * inv);
+            *reinterpret_cast<uint4*>(args.o + out_row * D + 32 * ch + 8 * i) =
+                make_uint4(w[0], w[1], w[2], w[3]);
           }
-          continue;
-        }
-        uint32_t pw[32];                  // the row as bf16 pairs; 16-byte chunk c = words 4 c ..
-        const uint64_t i2 = splat2(inv);
+        } else {
 #pragma unroll
-        for (int i = 0; i < 32; ++i) {
-          uint32_t y0, y1;
-          unpack2(fmul2(pack2(o[i >> 4][2 * (i & 15)], o[i >> 4][2 * (i & 15) + 1]), i2), y0, y1);
-          pw[i] = pack_bf16x2(__uint_as_float(y0), __uint_as_float(y1));
-        }
-        // Whole 128-byte lines: 8 lanes exchange 16-byte chunks, an 8 x 8
-        // transpose, so that a warp store writes 4 lines.
-#pragma unroll
-        for (int dd = 4; dd >= 1; dd >>= 1) {
-          const bool up = (li & dd) != 0;
-#pragma unroll
-          for (int jj = 0; jj < 8; ++jj) {
-            if (jj & dd) continue;
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              const uint32_t lo = pw[4 * jj + q];
-              const uint32_t hi = pw[4 * (jj + dd) + q];
-              const uint32_t got = __shfl_xor_sync(0xffffffffu, up ? lo : hi, dd);
-              pw[4 * jj + q] = up ? got : lo;
-              pw[4 * (jj + dd) + q] = up ? hi : got;
-            }
-          }
-        }
-#pragma unroll
-        for (int jj = 0; jj < 8; ++jj) {
-          const long long row = __shfl_sync(0xffffffffu, out_row, (lane & ~7) + jj);
-          if (row >= 0)
-            __stcs(reinterpret_cast<uint4*>(args.o + row * D + 64 * h + 8 * li),
-                   make_uint4(pw[4 * jj], pw[4 * jj + 1], pw[4 * jj + 2], pw[4 * jj + 3]));
+          for (int i = 0; i < 8; ++i)
+            part[8 * ch + i] = make_float4(__uint_as_float(o[4 * i]), __uint_as_float(o[4 * i + 1]),
+                                           __uint_as_float(o[4 * i + 2]), __uint_as_float(o[4 * i + 3]));
         }
       }
       tc_fence_before();
@@ -757,6 +678,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!mbar_wait_warp(q_full(t), qc[t]++ & 1, wc, kWaitQFull)) return false;
           tc_fence_after();
           issue_s(t);
+          if (a + 1 == (t ? e1 : e0)) mma_commit_w(q_empty(t));   // its only scores
         }
       }
       mma_commit_w(k_empty(kc % C::kKStages));
@@ -779,7 +701,10 @@ __global__ void __launch_bounds__(kThreads, 1)
               ++oc[t];
             }
           }
-          if (j + 1 < et) issue_s(t);
+          if (j + 1 < et) {
+            issue_s(t);
+            if (j + 2 == et) mma_commit_w(q_empty(t));
+          }
         }
         mma_commit_w(h_empty(hc & 1));
         ++hc;
@@ -799,6 +724,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!mbar_wait_warp(q_full(t), qc[t]++ & 1, wc, kWaitQFull)) return false;
           tc_fence_after();
           issue_s(t);
+          if (t + 2 >= n) mma_commit_w(q_empty(t));
           mma_commit_w(k_empty(kc % C::kKStages));
           ++kc;
         }
@@ -818,6 +744,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             ++hc;
             if (i + t + 2 < n) {
               issue_s(t);
+              if (i + t + 4 >= n) mma_commit_w(q_empty(t));
               mma_commit_w(k_empty(kc % C::kKStages));
               ++kc;
             } else {
@@ -850,6 +777,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int per_log = 7 - args.page_shift, per = 1 << per_log;   // pages per key tile
     const uint32_t page_bytes = static_cast<uint32_t>(D) << args.page_shift;
     uint32_t kn = 0, vn = 0;              // K and V tiles asked for so far
+    uint32_t qn[2] = {0u, 0u};            // and Q tiles
     bool ok = true;
     for (uint32_t si = 0; ok && wait_seg(si); ++si) {
       const Seg s = seg_at(si);
@@ -889,6 +817,25 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (pid[i] >= 0)
             tma_load_3d_w(kd + i * page_bytes, &tm_k, k_full(ks), 0, s.head << args.page_shift, pid[i]);
         ++kn;
+        if (j == s.a) {
+          // Q's two parts, up to 128 rows each; rows past the unit's last
+          // keep what the buffer held (their results go nowhere).
+#pragma unroll 1
+          for (int t = 0; t < 2 && ok; ++t) {
+            if (!s.active(t)) continue;
+            if (qn[t] > 0) ok = mbar_wait_warp(q_empty(t), (qn[t] - 1) & 1, wc, kWaitQFull);
+            if (!ok) break;
+            const int first = s.row(t, 0);
+            const uint32_t nb = static_cast<uint32_t>(min(kBM, s.n * args.group - first)) * D;
+            const uint8_t* src = args.q_codes + (s.q_row(args) + first) * D;
+            const uint32_t dst = sbase + C::kQOff + t * C::kQBytes;
+            mbar_arrive_expect_tx_w(q_full(t), 2 * nb);
+            bulk_load_1d_w(dst, src, nb, q_full(t));
+            bulk_load_1d_w(dst + C::kCodeTile, src + args.q_lo, nb, q_full(t));
+            ++qn[t];
+          }
+          if (!ok) break;
+        }
         if (vn >= C::kVStages &&
             !mbar_wait_warp(v_empty(vs), (vn / C::kVStages - 1) & 1, wc, kWaitKvEmpty)) {
           ok = false;
@@ -910,6 +857,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_wait_drain(k_full(r % C::kKStages), (r / C::kKStages) & 1, args.wait_budget);
     for (uint32_t r = vn > C::kVStages ? vn - C::kVStages : 0; r < vn; ++r)
       mbar_wait_drain(v_full(r % C::kVStages), (r / C::kVStages) & 1, args.wait_budget);
+    for (int t = 0; t < 2; ++t)
+      if (qn[t] > 0) mbar_wait_drain(q_full(t), (qn[t] - 1) & 1, args.wait_budget);
     __syncwarp();
   } else if (warp < kConvWarp0) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kCtrlRegs));
@@ -1030,6 +979,72 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
+// Splits the call's queries: row x = q * 2^-e, its largest entry in [224, 448]
+// (up to 448 where the mantissa allows), into hi = e4m3(x) and lo =
+// e4m3(x - hi).  Rows go to where the products read them: those of a sequence and
+// kv head in one run, (token, query head) order, 16-byte chunks swizzled as in
+// shared memory, so that a tile is one plain copy.  Bound: 2 d bytes in and out
+// a row.
+template <int D>
+__global__ void __launch_bounds__(256) split_kernel(const __grid_constant__ CacheAttnArgs a) {
+  constexpr int kLanes = D / 16;          // 16 columns each
+  const int Hq = a.Hkv * a.group;
+  const long long id = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x;
+  const long long row = id / kLanes;
+  const int c = static_cast<int>(id % kLanes);
+  if (row >= static_cast<long long>(a.s.T) * Hq) return;   // whole groups of lanes
+  const int token = static_cast<int>(row / Hq), hq = static_cast<int>(row % Hq);
+  // the token's sequence: a guess for sequences of equal rows, else a search
+  int b = static_cast<int>(static_cast<long long>(token) * a.s.B / a.s.T);
+  if (token < __ldg(a.s.q_start + b) || token >= __ldg(a.s.q_start + b + 1)) {
+    b = 0;
+    for (int hi = a.s.B; hi - b > 1;) {
+      const int mid = (b + hi) >> 1;
+      if (__ldg(a.s.q_start + mid) <= token) b = mid; else hi = mid;
+    }
+  }
+  const SeqInfo q = seq_info(a.s, b, a.page_shift);
+  const bool on = token >= q.r0 && token < q.r0 + q.n;
+  uint4 w[2] = {make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u)};
+  if (on) {
+    const uint4* p = reinterpret_cast<const uint4*>(a.q + token * a.q_row + hq * D + 16 * c);
+    w[0] = __ldg(p);
+    w[1] = __ldg(p + 1);
+  }
+  const uint32_t u[8] = {w[0].x, w[0].y, w[0].z, w[0].w, w[1].x, w[1].y, w[1].z, w[1].w};
+  uint32_t mx = 0u;                        // the largest magnitude's bits
+#pragma unroll
+  for (int i = 0; i < 8; ++i) mx = max(mx, max(u[i] & 0x7fffu, (u[i] >> 16) & 0x7fffu));
+  // a row's lanes are neighbours, and all of them are here
+  const unsigned int lanes = ((1u << kLanes) - 1u) << (threadIdx.x & 31 & ~(kLanes - 1));
+#pragma unroll
+  for (int off = kLanes / 2; off > 0; off >>= 1) mx = max(mx, __shfl_xor_sync(lanes, mx, off));
+  if (!on) return;                         // behind the last sequence
+  const int e = static_cast<int>(mx >> 7) - 127 - 8 + ((mx & 0x7fu) > 0x60u ? 1 : 0);
+  const int ec = max(-126, min(126, e));
+  // a row with an infinity or a NaN becomes NaN
+  const float down = mx >= 0x7f80u ? __int_as_float(0x7fffffff) : exp2i(-ec);
+  uint32_t hi[4], lo[4];
+#pragma unroll
+  for (int z = 0; z < 4; ++z) {
+    const float x0 = __uint_as_float(u[2 * z] << 16) * down;
+    const float x1 = __uint_as_float(u[2 * z] & 0xffff0000u) * down;
+    const float x2 = __uint_as_float(u[2 * z + 1] << 16) * down;
+    const float x3 = __uint_as_float(u[2 * z + 1] & 0xffff0000u) * down;
+    hi[z] = pack_e4m3x4(x0, x1, x2, x3);
+    const float4 h = e4m3x4_to_f32x4(hi[z]);
+    lo[z] = pack_e4m3x4(x0 - h.x, x1 - h.y, x2 - h.z, x3 - h.w);
+  }
+  const int head = hq / a.group;
+  const int rr = (token - q.r0) * a.group + (hq - head * a.group);
+  const long long out = (static_cast<long long>(q.r0) * a.Hkv + static_cast<long long>(head) * q.n) * a.group + rr;
+  // swizzle of the row's place in its tile (tiles start at multiples of 128 rows)
+  uint8_t* dst = a.q_codes + out * D - static_cast<long long>(rr & 7) * D + code_off<D>(rr & 7, c);
+  *reinterpret_cast<uint4*>(dst) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+  *reinterpret_cast<uint4*>(dst + a.q_lo) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+  if (c == 0) a.q_scale[out] = exp2i(ec);
+}
+
 template <int D>
 cudaError_t launch_t(const CUtensorMap& tk, const CUtensorMap& tv, const CacheAttnArgs& a,
                      cudaStream_t stream) {
@@ -1041,6 +1056,9 @@ cudaError_t launch_t(const CUtensorMap& tk, const CUtensorMap& tv, const CacheAt
   cudaFuncAttributes fa;
   if ((e = cudaFuncGetAttributes(&fa, kern)) != cudaSuccess) return e;
   if (fa.numRegs != kLaunchRegs) return cudaErrorInvalidConfiguration;
+  const long long lanes = static_cast<long long>(a.s.T) * a.Hkv * a.group * (D / 16);
+  split_kernel<D><<<static_cast<unsigned>((lanes + 255) / 256), 256, 0, stream>>>(a);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
   kern<<<a.grid, kThreads, smem, stream>>>(tk, tv, a);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   return launch_cache_join(D, kUnitRows, a, stream);

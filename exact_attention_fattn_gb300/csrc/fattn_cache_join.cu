@@ -6,7 +6,7 @@
 // Bound: latency where a unit has many parts (one long sequence: up to 152 of
 // them), bytes where units are large (256 rows, two or three parts each).  A
 // thread has 4 columns of a row; the rows of a block are 4 for the small
-// units, whose parts are walked by four groups side by side, and 32 for the
+// units, whose parts are walked by four groups side by side, and 8 for the
 // large ones, walked by one.
 #include "fattn_cache.cuh"
 
@@ -38,50 +38,46 @@ template <int D, int ROWS>
 struct JoinCfg {
   static constexpr int kF4 = D / 4;                            // threads per row
   static constexpr int kGroups = ROWS == kDecodeRows ? 4 : 1;
-  static constexpr int kRows = ROWS == kDecodeRows ? 4 : 32;   // rows per block
-  static constexpr int kPerThread = ROWS == kDecodeRows ? 1 : 4;   // rows a thread takes in turn
-  static constexpr int kThreads = kF4 * kGroups * (kRows / kPerThread);
+  static constexpr int kRows = ROWS == kDecodeRows ? 4 : 8;    // rows per block
+  static constexpr int kThreads = kF4 * kGroups * kRows;
 };
 
 template <int D, int ROWS>
 __global__ void __launch_bounds__(JoinCfg<D, ROWS>::kThreads) join_kernel(const CacheAttnArgs a) {
   using J = JoinCfg<D, ROWS>;
-  __shared__ Part side[J::kGroups][J::kRows / J::kPerThread][J::kF4];
+  __shared__ Part side[J::kGroups][J::kRows][J::kF4];
   const int cta = blockIdx.x, G = a.grid;
   const int4 rec = a.rec[2 * cta];
   const int rows = rec.y * a.group - rec.z * ROWS;   // of the unit, from its first
   if (rec.y == 0 || static_cast<int>(blockIdx.y) * J::kRows >= rows) return;
   const int4 more = a.rec[2 * cta + 1];
   const long long W = (static_cast<long long>(more.z) << 32) | static_cast<unsigned int>(more.y);
-  const int q4 = threadIdx.x % J::kF4, local = threadIdx.x / J::kF4 % (J::kRows / J::kPerThread);
-  const int group = threadIdx.x / (J::kF4 * (J::kRows / J::kPerThread));
-#pragma unroll
-  for (int z = 0; z < J::kPerThread; ++z) {
-    const int row = blockIdx.y * J::kRows + z * (J::kRows / J::kPerThread) + local;
-    const bool on = row < min(rows, ROWS);
-    Part p{-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
-    for (int c = cta + group; on && c <= more.x; c += J::kGroups) {
-      if (cta_first(W, G, c) == cta_first(W, G, c + 1)) continue;   // a CTA without work
-      const long long at = (2ll * c + (c == cta ? 1 : 0)) * ROWS + row;
-      const float2 ml = __ldg(a.part_ml + at);
-      merge(p, Part{ml.x, ml.y, __ldg(reinterpret_cast<const float4*>(a.part_o + at * D) + q4)});
-    }
-    if constexpr (J::kGroups > 1) {
-      side[group][local][q4] = p;
-      __syncthreads();
-      if (group != 0) return;
-#pragma unroll
-      for (int g = 1; g < J::kGroups; ++g) merge(p, side[g][local][q4]);
-    }
-    if (!on) continue;
-    const int rr = rec.z * ROWS + row, token = rr / a.group;
-    const long long out = (static_cast<long long>(rec.x + token) * a.Hkv + rec.w) * a.group +
-                          (rr - token * a.group);
-    const float inv = p.l == 0.f ? 0.f : 1.f / p.l;
-    *reinterpret_cast<uint2*>(a.o + out * D + 4 * q4) =
-        make_uint2(pack_bf16x2(p.o.x * inv, p.o.y * inv), pack_bf16x2(p.o.z * inv, p.o.w * inv));
-    if (q4 == 0) a.lse[out] = p.l == 0.f ? -INFINITY : (p.m + log2f(p.l)) * kLn2;
+  const int q4 = threadIdx.x % J::kF4, local = threadIdx.x / J::kF4 % J::kRows;
+  const int group = threadIdx.x / (J::kF4 * J::kRows);
+  const int row = blockIdx.y * J::kRows + local;
+  const bool on = row < min(rows, ROWS);
+  Part p{-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
+  for (int c = cta + group; on && c <= more.x; c += J::kGroups) {
+    if (cta_first(W, G, c) == cta_first(W, G, c + 1)) continue;   // a CTA without work
+    const long long at = (2ll * c + (c == cta ? 1 : 0)) * ROWS + row;
+    const float2 ml = __ldg(a.part_ml + at);
+    merge(p, Part{ml.x, ml.y, __ldg(reinterpret_cast<const float4*>(a.part_o + at * D) + q4)});
   }
+  if constexpr (J::kGroups > 1) {
+    side[group][local][q4] = p;
+    __syncthreads();
+    if (group != 0) return;
+#pragma unroll
+    for (int g = 1; g < J::kGroups; ++g) merge(p, side[g][local][q4]);
+  }
+  if (!on) return;
+  const int rr = rec.z * ROWS + row, token = rr / a.group;
+  const long long out = (static_cast<long long>(rec.x + token) * a.Hkv + rec.w) * a.group +
+                        (rr - token * a.group);
+  const float inv = p.l == 0.f ? 0.f : 1.f / p.l;
+  *reinterpret_cast<uint2*>(a.o + out * D + 4 * q4) =
+      make_uint2(pack_bf16x2(p.o.x * inv, p.o.y * inv), pack_bf16x2(p.o.z * inv, p.o.w * inv));
+  if (q4 == 0) a.lse[out] = p.l == 0.f ? -INFINITY : (p.m + log2f(p.l)) * kLn2;
 }
 
 template <int D, int ROWS>

@@ -164,6 +164,9 @@ struct CacheAttnArgs {
   int4* rec;
   float4* xch_o;              // tcgen05 kernel: exchange between a CTA's two softmax warpgroups
   float2* xch_ml;
+  uint8_t* q_codes;           // its queries as e4m3 pairs: hi [T * Hq, d], lo q_lo bytes further
+  long long q_lo;
+  float* q_scale;             // the power of two taken out of each row
   int grid;                   // CTAs of the main kernel
   DeviceStatus* status;
   long long wait_budget;
