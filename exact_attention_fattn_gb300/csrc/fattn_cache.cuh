@@ -104,4 +104,30 @@ __device__ __forceinline__ float4 e4m3x4_to_f32x4(uint32_t codes) {
   return make_float4(a.x, a.y, b.x, b.y);
 }
 
+// A query row as the sum of two e4m3 rows.  `mx`: the bf16 bits of its
+// largest magnitude.  The row is scaled by query_factor, a power of two, so
+// that its largest entry lies in [224, 448] (448 = 1.75 * 2^8: up to 448 where the
+// mantissa is at most 1.75, one power less above); query_scale undoes it.  A
+// row with an infinity or a NaN becomes NaN.
+__device__ __forceinline__ int query_exp(uint32_t mx) {
+  const int e = static_cast<int>(mx >> 7) - 127 - 8 + ((mx & 0x7fu) > 0x60u ? 1 : 0);
+  return max(-126, min(126, e));
+}
+__device__ __forceinline__ float query_scale(uint32_t mx) { return exp2i(query_exp(mx)); }
+__device__ __forceinline__ float query_factor(uint32_t mx) {
+  return mx >= 0x7f80u ? __int_as_float(0x7fffffff) : exp2i(-query_exp(mx));
+}
+
+// Four columns (two words of bf16 pairs) -> hi = e4m3(x), lo = e4m3(x - hi).  x has 8
+// significant bits and hi the first 4 (rounded), so lo is exact while it is
+// not subnormal and off by at most 2^-10 then.
+__device__ __forceinline__ void split_query4(uint32_t p, uint32_t q, float factor, uint32_t& hi,
+                                             uint32_t& lo) {
+  const float x0 = __uint_as_float(p << 16) * factor, x1 = __uint_as_float(p & 0xffff0000u) * factor;
+  const float x2 = __uint_as_float(q << 16) * factor, x3 = __uint_as_float(q & 0xffff0000u) * factor;
+  hi = pack_e4m3x4(x0, x1, x2, x3);
+  const float4 h = e4m3x4_to_f32x4(hi);
+  lo = pack_e4m3x4(x0 - h.x, x1 - h.y, x2 - h.z, x3 - h.w);
+}
+
 }  // namespace fattn

@@ -85,12 +85,13 @@ struct AttnWorkspace {
 
 AttnWorkspace attn_workspace(int rows, int d, size_t q_rows) {
   AttnWorkspace w;
-  const size_t slots = 2 * static_cast<size_t>(kCacheMaxCtas) * rows;
+  const int ctas = kSms * (rows == kChunkRows ? kChunkCtas : kDecodeCtas);
+  const size_t slots = 2 * static_cast<size_t>(ctas) * rows;
   w.o_off = 0;
   w.ml_off = align256(slots * d * sizeof(float));
   w.rec_off = w.ml_off + align256(slots * sizeof(float2));
-  w.xo_off = w.rec_off + align256(2 * kCacheMaxCtas * sizeof(int4));
-  const size_t xch = rows == kChunkRows ? static_cast<size_t>(kCacheMaxCtas) * (kChunkRows / 2) : 0;
+  w.xo_off = w.rec_off + align256(2 * ctas * sizeof(int4));
+  const size_t xch = rows == kChunkRows ? static_cast<size_t>(ctas) * (kChunkRows / 2) : 0;
   w.xml_off = w.xo_off + align256(xch * d * sizeof(float));
   w.q_off = w.xml_off + align256(xch * sizeof(float2));
   if (rows != kChunkRows) q_rows = 0;
@@ -218,7 +219,7 @@ int fattn_cache_fwd(const fattn_cache* cache, const void* q, long long q_row, vo
   a.causal = causal != 0;
   a.scale_log2 = scale * 1.4426950408889634f;
   const bool few = few_rows(T, B, a.group, n_selected);
-  const int unit_rows = few ? kDecodeRows : kChunkRows, piece_keys = few ? 256 : 128;
+  const int unit_rows = few ? kDecodeRows : kChunkRows, piece_keys = few ? kDecodeKeys : kChunkTileKeys;
   const size_t q_rows = static_cast<size_t>(T) * Hq;
   const AttnWorkspace w = attn_workspace(unit_rows, cache->d, q_rows);
   char* base = static_cast<char*>(workspace);
@@ -234,7 +235,7 @@ int fattn_cache_fwd(const fattn_cache* cache, const void* q, long long q_row, vo
   if (cudaGetDevice(&dev) != cudaSuccess ||
       cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
     return FATTN_ERR_CUDA;
-  const int max_ctas = sms < kCacheMaxCtas ? sms : kCacheMaxCtas;
+  const int max_ctas = (sms < kSms ? sms : kSms) * (few ? kDecodeCtas : kChunkCtas);
   // Pieces of keys of all units, at most (the lengths are on the device).
   const long long keys = static_cast<long long>(selected ? n_selected : max_pages) * cache->page;
   const long long units =

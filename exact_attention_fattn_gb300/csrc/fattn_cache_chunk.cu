@@ -24,8 +24,9 @@
 //   x_j = c_p s_j + l_p,  P'_j = 2^(x_j - m),  l = sum_p 2^(-l_p) sum P'.
 // A page is at least 32 tokens, so c and l_p are constant over each 32-column
 // TMEM load and the row maximum comes from the load itself (tcgen05.ld.red).
-// The reference m moves only when a row's maximum passes it by more than 8
-// (fp16 holds 2^8 times a probability easily).
+// The reference moves only when a row's maximum passes it by more than 8, and P'
+// is 2^7 times what it says, 2^15 at most: fp16 then holds probabilities down to
+// 2^-31 of the largest.
 //
 // Work split: the key tiles of all units, in order, are dealt to the CTAs in
 // equal contiguous shares, whatever the sequences' lengths and however many
@@ -57,6 +58,7 @@ constexpr int kSegs = 4;              // segments in the shared ring
 constexpr int kSegReaders = 8 + 2 + 4;   // warps that read each of them
 constexpr float kLn2 = 0.69314718055994530942f;
 constexpr float kTau = 8.f;
+constexpr float kLift = 7.f;
 // Register split: 256 x 200 + 128 x 56 + 128 x 56 = 512 x 128, exactly the
 // launch total, so setmaxnreg.inc can always complete.
 constexpr int kLaunchRegs = 128;
@@ -480,7 +482,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (need) m_ref = m_new;
           l *= alpha;
         }
-        const float m_use = m_ref == -INFINITY ? 0.f : m_ref;
+        const float m_use = m_ref == -INFINITY ? 0.f : m_ref - kLift;
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
           uint32_t pk[16];
@@ -631,8 +633,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_arrive(o_empty(t));
       if (joined) mbar_arrive(x_empty);
       if (on) {
-        if (whole) args.lse[out_row] = l == 0.f ? -INFINITY : (m_ref + log2f(l)) * kLn2;
-        else *part_ml = make_float2(m_ref, l);
+        if (whole) args.lse[out_row] = l == 0.f ? -INFINITY : (m_ref - kLift + log2f(l)) * kLn2;
+        else *part_ml = make_float2(m_ref - kLift, l);
       }
       done_seg(si);
     }
@@ -1020,21 +1022,10 @@ __global__ void __launch_bounds__(256) split_kernel(const __grid_constant__ Cach
 #pragma unroll
   for (int off = kLanes / 2; off > 0; off >>= 1) mx = max(mx, __shfl_xor_sync(lanes, mx, off));
   if (!on) return;                         // behind the last sequence
-  const int e = static_cast<int>(mx >> 7) - 127 - 8 + ((mx & 0x7fu) > 0x60u ? 1 : 0);
-  const int ec = max(-126, min(126, e));
-  // a row with an infinity or a NaN becomes NaN
-  const float down = mx >= 0x7f80u ? __int_as_float(0x7fffffff) : exp2i(-ec);
+  const float factor = query_factor(mx);
   uint32_t hi[4], lo[4];
 #pragma unroll
-  for (int z = 0; z < 4; ++z) {
-    const float x0 = __uint_as_float(u[2 * z] << 16) * down;
-    const float x1 = __uint_as_float(u[2 * z] & 0xffff0000u) * down;
-    const float x2 = __uint_as_float(u[2 * z + 1] << 16) * down;
-    const float x3 = __uint_as_float(u[2 * z + 1] & 0xffff0000u) * down;
-    hi[z] = pack_e4m3x4(x0, x1, x2, x3);
-    const float4 h = e4m3x4_to_f32x4(hi[z]);
-    lo[z] = pack_e4m3x4(x0 - h.x, x1 - h.y, x2 - h.z, x3 - h.w);
-  }
+  for (int z = 0; z < 4; ++z) split_query4(u[2 * z], u[2 * z + 1], factor, hi[z], lo[z]);
   const int head = hq / a.group;
   const int rr = (token - q.r0) * a.group + (hq - head * a.group);
   const long long out = (static_cast<long long>(q.r0) * a.Hkv + static_cast<long long>(head) * q.n) * a.group + rr;
@@ -1042,7 +1033,7 @@ __global__ void __launch_bounds__(256) split_kernel(const __grid_constant__ Cach
   uint8_t* dst = a.q_codes + out * D - static_cast<long long>(rr & 7) * D + code_off<D>(rr & 7, c);
   *reinterpret_cast<uint4*>(dst) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
   *reinterpret_cast<uint4*>(dst + a.q_lo) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-  if (c == 0) a.q_scale[out] = exp2i(ec);
+  if (c == 0) a.q_scale[out] = query_scale(mx);
 }
 
 template <int D>

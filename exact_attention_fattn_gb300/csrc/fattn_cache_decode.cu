@@ -5,30 +5,34 @@
 // that share a kv head -- meet every cached key of that head once, so the
 // call is bound by reading the cache, 2 d bytes a token and kv head.  With
 // 16 rows or fewer a 128-row tcgen05 tile would be mostly padding; the
-// products go to mma.sync m16n8k16, whose rate (about a quarter of tcgen05's)
-// is several times what the memory can feed.
+// products go to mma.sync m16n8k16 in fp16 (measured on GB300: 8 cycles each
+// per SM quarter, 512 per 128 keys and SM, where the memory needs 1400).
 //
 // Codes become halves in registers: an e4m3 value is exact in fp16.  Queries
 // are scaled by a power of two per row into fp16's range, exactly unless an
 // entry is 2^-14 below its row's largest; probabilities are rounded to fp16
-// (11 bits) for P V and summed in fp32 unrounded.
+// (11 bits) for P V and summed in fp32 unrounded.  (mma.sync on the codes
+// themselves, with Q in two e4m3 parts, is 20 % slower: the compiler converts
+// both operands in front of every such product.)
 //
 // Softmax with the value scales inside: with sv_p the value scale of page p
 // and l_p its log2,
-//   x_j = s_j + l_p(j),  m = running max of x,  P'_j = 2^(x_j - m),
+//   x_j = s_j + l_p(j),  m = running max of x - 14,  P'_j = 2^(x_j - m),
 //   O = sum P'_j V8_j,   l = sum_p 2^(-l_p) sum_{j in p} P'_j,
 // so O / l is the result and m + log2 l the log-sum-exp, with one exponential
 // per score and no product by the scales left over; |l_p| <= 48 keeps the sum
-// in range.
+// in range.  With the reference 14 below the maximum fp16 holds probabilities
+// down to 2^-38 of the largest, so that many small ones are not lost.
 //
-// Work split: a unit's keys are cut into chunks of 256 and the chunks of all
+// Work split: a unit's keys are cut into chunks of 128 and the chunks of all
 // units, in order, are dealt to the CTAs in equal contiguous shares, so
-// lengths may differ by any factor.  A CTA's 8 warps take 32 keys of each
+// lengths may differ by any factor.  A CTA's 4 warps take 32 keys of each
 // chunk, each with its own softmax state and its own ring of TMA tiles (no
 // barrier inside a chunk), and are joined through shared memory when the
-// CTA's part of the unit ends.  A unit that several CTAs share is joined from
-// their partial results in a second kernel, in order, so results do not
-// depend on timing.
+// CTA's part of the unit ends; the next unit's queries are on their way to
+// shared memory by then, and a second CTA on the SM works meanwhile.  A unit that
+// several CTAs share is joined from their partial results in a second
+// kernel, in order, so results do not depend on timing.
 #include <cuda_fp16.h>
 
 #include "fattn_cache.cuh"
@@ -37,12 +41,14 @@ namespace fattn {
 
 namespace {
 
-constexpr int kWarps = 8;
+constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kRows = kDecodeRows;
 constexpr int kTileKeys = 32;                       // keys a warp takes of a chunk
 constexpr int kChunkKeys = kWarps * kTileKeys;
+static_assert(kChunkKeys == kDecodeKeys, "pieces of work");
 constexpr float kLn2 = 0.69314718055994530942f;
+constexpr float kLift = 14.f;                       // log2 of the largest P' (fp16 holds 65504)
 
 template <int D>
 struct DecCfg {
@@ -52,9 +58,10 @@ struct DecCfg {
   static constexpr int kRingBytes = kWarps * kStages * kStageBytes;
   static constexpr int kJoinOff = kRingBytes;       // [kWarps][kRows][D] fp32
   static constexpr int kMlOff = kJoinOff + kWarps * kRows * D * 4;    // [kWarps][kRows] float2
-  static constexpr int kBarOff = kMlOff + kWarps * kRows * 8;
-  static constexpr int kMiscOff = kBarOff + kWarps * kStages * 8;
-  static constexpr int kPreOff = kMiscOff + 128;    // [B + 1] long long
+  static constexpr int kQOff = kMlOff + kWarps * kRows * 8;           // [2][kRows][D] bf16
+  static constexpr int kBarOff = kQOff + 2 * kRows * D * 2;
+  static constexpr int kMiscOff = kBarOff + kWarps * kStages * 8;     // abort, then two units
+  static constexpr int kPreOff = kMiscOff + 128;    // [B + 1] int
   static constexpr int kSmemFixed = kPreOff + 1024;
 };
 
@@ -92,60 +99,79 @@ struct Unit {
   int pos0;           // position of row r0
   int len;            // keys that exist
   int table_row;      // row of the page table
-  long long c0;       // first chunk
-  int chunks;
+  int c0, chunks;     // first chunk, and how many
 };
 
 // Chunks of the whole call, and the unit of a chunk.  pre: dense calls only,
 // chunks before each sequence (shared memory, [B + 1]).
 struct Schedule {
   const CacheAttnArgs* a;
-  const long long* pre;
+  const int* pre;
   int sparse_chunks;      // chunks of every sparse unit
   int sparse_blocks;      // row blocks of a token's group
 
-  __device__ __forceinline__ long long total() const {
-    if (a->selected != nullptr)
-      return static_cast<long long>(a->s.T) * a->Hkv * sparse_blocks * sparse_chunks;
-    return pre[a->s.B];
+  __device__ __forceinline__ int total() const {
+    return a->selected != nullptr ? a->s.T * a->Hkv * sparse_blocks * sparse_chunks : pre[a->s.B];
   }
-  __device__ __forceinline__ Unit unit_of(long long j) const {
+  __device__ __forceinline__ Unit sequence(int b) const {
+    const SeqInfo q = seq_info(a->s, b, a->page_shift);
     Unit u;
+    u.seq = u.table_row = b;
+    u.rb = u.head = 0;
+    u.r0 = q.r0;
+    u.n = q.n;
+    u.len = q.len;
+    u.pos0 = q.len - q.n;
+    u.c0 = pre[b];
+    u.chunks = chunks_of(q.len);
+    return u;
+  }
+  __device__ __forceinline__ Unit unit_of(int j) const {
     if (a->selected != nullptr) {
-      const long long id = j / sparse_chunks;
+      Unit u;
+      const int id = j / sparse_chunks, hb = id / a->Hkv;
       u.c0 = id * sparse_chunks;
       u.chunks = sparse_chunks;
-      const long long hb = id / a->Hkv;
-      u.head = static_cast<int>(id - hb * a->Hkv);
-      u.rb = static_cast<int>(hb % sparse_blocks);
-      u.seq = static_cast<int>(hb / sparse_blocks);
-      u.r0 = u.seq;
-      u.n = 0;
-      u.pos0 = u.len = u.table_row = 0;
-      return u;   // its sequence is looked up by finish()
+      u.head = id - hb * a->Hkv;
+      u.rb = hb % sparse_blocks;
+      u.seq = hb / sparse_blocks;
+      finish(u);
+      return u;
     }
     int lo = 0, hi = a->s.B;   // the last b with pre[b] <= j
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
       if (pre[mid] <= j) lo = mid; else hi = mid;
     }
-    const SeqInfo q = seq_info(a->s, lo, a->page_shift);
-    u.seq = u.table_row = lo;
-    u.r0 = q.r0;
-    u.n = q.n;
-    u.len = q.len;
-    u.pos0 = q.len - q.n;
-    u.chunks = chunks_of(q.len);
-    const int id = static_cast<int>((j - pre[lo]) / u.chunks);
-    u.c0 = pre[lo] + static_cast<long long>(id) * u.chunks;
+    Unit u = sequence(lo);
+    const int id = (j - u.c0) / u.chunks;
+    u.c0 += id * u.chunks;
     u.rb = id / a->Hkv;
     u.head = id - u.rb * a->Hkv;
     return u;
   }
+  // The unit after u; there is one.
+  __device__ __forceinline__ void advance(Unit& u) const {
+    u.c0 += u.chunks;
+    if (++u.head < a->Hkv) return;
+    u.head = 0;
+    ++u.rb;
+    if (a->selected != nullptr) {
+      if (u.rb < sparse_blocks) return;
+      u.rb = 0;
+      ++u.seq;
+      finish(u);
+      return;
+    }
+    if (u.rb * kRows < u.n * a->group) return;
+    int b = u.seq;
+    while (b + 1 < a->s.B && pre[b + 1] == pre[b + 2]) ++b;   // sequences without rows
+    u = sequence(min(b + 1, a->s.B - 1));
+  }
   // The sequence of a sparse unit's token: a guess that holds where all
   // sequences have the same number of rows, else a search.
   __device__ __forceinline__ void finish(Unit& u) const {
-    if (a->selected == nullptr) return;
+    u.r0 = u.seq;
     const int* qs = a->s.q_start;
     int b = static_cast<int>(static_cast<long long>(u.r0) * a->s.B / a->s.T);
     if (u.r0 < __ldg(qs + b) || u.r0 >= __ldg(qs + b + 1)) {
@@ -189,7 +215,7 @@ __device__ __forceinline__ Tile shfl_tile(const Tile& t, int src) {
 }
 
 template <int D, bool SPARSE>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kThreads, 2)
     decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                   const __grid_constant__ CacheAttnArgs a) {
   using C = DecCfg<D>;
@@ -203,7 +229,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   float* join = reinterpret_cast<float*>(smem + C::kJoinOff);
   float2* ml = reinterpret_cast<float2*>(smem + C::kMlOff);
   uint32_t* misc = reinterpret_cast<uint32_t*>(smem + C::kMiscOff);
-  long long* pre = reinterpret_cast<long long*>(smem + C::kPreOff);
+  int* pre = reinterpret_cast<int*>(smem + C::kPreOff);
+  Unit* units = reinterpret_cast<Unit*>(smem + C::kMiscOff + 16);   // this one and the next
+  static_assert(sizeof(Unit) * 2 + 16 <= 128, "two units");
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int r = lane >> 2, c = lane & 3;
   const uint32_t ring = sbase + warp * C::kStages * C::kStageBytes;
@@ -222,50 +250,60 @@ __global__ void __launch_bounds__(kThreads, 1)
   if constexpr (!SPARSE) {
     const int per = (a.s.B + kThreads - 1) / kThreads;
     const int b0 = min(a.s.B, tid * per), b1 = min(a.s.B, b0 + per);
-    long long sum = 0;
+    int sum = 0;
     for (int b = b0; b < b1; ++b) {
       const SeqInfo q = seq_info(a.s, b, a.page_shift);
       if (!q.ok && cta == 0) record_bad_index(a.status, kSiteSeqStart);
-      const long long blocks = (static_cast<long long>(q.n) * a.group + kRows - 1) / kRows;
-      sum += blocks * a.Hkv * chunks_of(q.len);
+      pre[b] = sum;
+      sum += (q.n * a.group + kRows - 1) / kRows * a.Hkv * chunks_of(q.len);
     }
-    long long incl = sum;
+    int incl = sum;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
-      const long long t = __shfl_up_sync(0xffffffffu, incl, off);
+      const int t = __shfl_up_sync(0xffffffffu, incl, off);
       if (lane >= off) incl += t;
     }
-    long long* wtot = reinterpret_cast<long long*>(ml);
+    int* wtot = reinterpret_cast<int*>(ml);
     if (lane == 31) wtot[warp] = incl;
     __syncthreads();
-    long long at = incl - sum;
+    int at = incl - sum;
     for (int w = 0; w < warp; ++w) at += wtot[w];
-    for (int b = b0; b < b1; ++b) {
-      pre[b] = at;
-      const SeqInfo q = seq_info(a.s, b, a.page_shift);
-      const long long blocks = (static_cast<long long>(q.n) * a.group + kRows - 1) / kRows;
-      at += blocks * a.Hkv * chunks_of(q.len);
-    }
-    if (tid == kThreads - 1) pre[a.s.B] = at;
+    for (int b = b0; b < b1; ++b) pre[b] += at;
+    if (tid == kThreads - 1) pre[a.s.B] = at + sum;
   }
   __syncthreads();
 
   const Schedule sched{&a, pre, SPARSE ? ((a.n_selected << a.page_shift) + kChunkKeys - 1) / kChunkKeys : 0,
                        (a.group + kRows - 1) / kRows};
-  const long long W = sched.total();
-  const long long j0 = cta_first(W, G, cta), j1 = cta_first(W, G, cta + 1);
-  const int n_tiles = static_cast<int>(j1 - j0);   // of this warp, and of every other
+  const int W = sched.total();
+  const int j0 = static_cast<int>(cta_first(W, G, cta)), j1 = static_cast<int>(cta_first(W, G, cta + 1));
+  const int n_tiles = j1 - j0;                      // of this warp, and of every other
   const WaitCtx wc{a.wait_budget, reinterpret_cast<volatile uint32_t*>(&misc[0]), a.status};
+
+  // A unit's queries into shared memory, rows past its last as zeros.
+  auto fetch_q = [&](const Unit& u, int buf) {
+    for (int x = tid; x < kRows * (D / 8); x += kThreads) {
+      const int row = x / (D / 8), col = x % (D / 8), rr = u.rb * kRows + row;
+      const bool on = rr < u.n * a.group;
+      const int token = on ? rr / a.group : 0;
+      const uint16_t* src = a.q + (u.r0 + token) * a.q_row +
+                            (static_cast<long long>(u.head) * a.group + (on ? rr - token * a.group : 0)) * D + 8 * col;
+      const uint32_t dst = sbase + C::kQOff + ((buf * kRows + row) * D + 8 * col) * 2;
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(on ? src : a.q),
+                   "r"(on ? 16 : 0)
+                   : "memory");
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
 
   // The tiles of chunks j0 + 32 k .. + 31, one per lane.
   auto look_up = [&](int k) -> Tile {
     Tile t{-1, 0, 0, 0.f, 0.f};
     const int i = 32 * k + lane;
-    Unit u{};
-    if (i < n_tiles) u = sched.unit_of(j0 + i);
-    if (i < n_tiles) sched.finish(u);
-    if (i >= n_tiles || u.n == 0) return t;
-    const int at = static_cast<int>(j0 + i - u.c0) * kChunkKeys + warp * kTileKeys;
+    if (i >= n_tiles) return t;
+    const Unit u = sched.unit_of(j0 + i);
+    if (u.n == 0) return t;
+    const int at = (j0 + i - u.c0) * kChunkKeys + warp * kTileKeys;
     const int page = 1 << a.page_shift;
     int entry = at >> a.page_shift;
     const int off = at & (page - 1);
@@ -293,40 +331,51 @@ __global__ void __launch_bounds__(kThreads, 1)
     t.lv = static_cast<float>(scale_exp(__ldg(a.v_scale + sc)));
     return t;
   };
-  auto issue = [&](const Tile& t, int stage) {   // converged warp
-    if (t.pid < 0) return;
+  // Tile `src` of a batch into a stage (converged warp): whether there is one.
+  auto issue = [&](const Tile& batch, int src, int stage) -> bool {
+    const int pid = __shfl_sync(0xffffffffu, batch.pid, src);
+    const int y = __shfl_sync(0xffffffffu, batch.y, src);
+    if (pid < 0) return false;
     const uint32_t dst = ring + stage * C::kStageBytes;
     mbar_arrive_expect_tx_w(bar0 + 8 * stage, C::kStageBytes);
-    tma_load_3d_w(dst, &tm_k, bar0 + 8 * stage, 0, t.y, t.pid);
-    tma_load_3d_w(dst + C::kTileBytes, &tm_v, bar0 + 8 * stage, 0, t.y, t.pid);
+    tma_load_3d_w(dst, &tm_k, bar0 + 8 * stage, 0, y, pid);
+    tma_load_3d_w(dst + C::kTileBytes, &tm_v, bar0 + 8 * stage, 0, y, pid);
+    return true;
   };
 
+  if (n_tiles > 0) {
+    const Unit u = sched.unit_of(j0);
+    fetch_q(u, 0);
+    if (tid == 0) units[0] = u;
+  }
   Tile cur = look_up(0), next = cur;
-  if (n_tiles > 32) next = look_up(1);
   int pending = 0;                                  // stages with a copy in flight, one bit each
 #pragma unroll
-  for (int s = 0; s < C::kStages; ++s) {
-    if (s < n_tiles) {
-      const Tile t = shfl_tile(cur, s);
-      issue(t, s);
-      if (t.pid >= 0) pending |= 1 << s;
-    }
-  }
+  for (int s = 0; s < C::kStages; ++s)
+    if (s < n_tiles && issue(cur, s, s)) pending |= 1 << s;
   uint32_t phases = 0u;                             // parity of each stage's next completion
   bool ok = true;
   bool shared_unit = false;                         // thread 0: this CTA's last unit goes on
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
+  __syncthreads();
 
   int i = 0;                                        // tile of this warp
-  while (i < n_tiles) {
+  for (int seg = 0; i < n_tiles; ++seg) {
     // ---- the CTA's part of one unit: chunks [j0 + i, j0 + end)
-    Unit u = sched.unit_of(j0 + i);
-    sched.finish(u);
-    const int end = static_cast<int>(min(j1, u.c0 + u.chunks) - j0);
+    const Unit u = units[seg & 1];
+    const int end = min(j1, u.c0 + u.chunks) - j0;
     const bool starts = j0 + i == u.c0, ends = j0 + end == u.c0 + u.chunks;
     const bool whole = starts && ends;
     // A CTA shares at most two units: the one it starts inside (slot 0) and
     // the one that goes on after it (slot 1).
     const int slot = starts ? 1 : 0;
+    if (end < n_tiles) {
+      // the buffers' last readers are two barriers back
+      Unit nu = u;
+      sched.advance(nu);
+      fetch_q(nu, (seg + 1) & 1);
+      if (tid == 0) units[(seg + 1) & 1] = nu;
+    }
 
     // Queries as fp16 A fragments: row r or r + 8, columns kVals * c ...
     // (a k step's four columns of a thread are consecutive in memory).
@@ -340,20 +389,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int token = on ? rr / a.group : 0;
       lim[hh] = on ? (a.causal ? max(0, min(u.len, u.pos0 + token + 1)) : u.len) : 0;
       uint32_t w[D / 8];
+      const uint32_t qp = sbase + C::kQOff + (((seg & 1) * kRows + r + 8 * hh) * D + kVals * c) * 2;
 #pragma unroll
-      for (int q = 0; q < D / 8; ++q) w[q] = 0u;
-      if (on) {
-        const uint4* p = reinterpret_cast<const uint4*>(
-            a.q + (u.r0 + token) * a.q_row +
-            (static_cast<long long>(u.head) * a.group + rr - token * a.group) * D + kVals * c);
-#pragma unroll
-        for (int q = 0; q < D / 32; ++q) {
-          const uint4 x = __ldg(p + q);
-          w[4 * q] = x.x;
-          w[4 * q + 1] = x.y;
-          w[4 * q + 2] = x.z;
-          w[4 * q + 3] = x.w;
-        }
+      for (int q = 0; q < D / 32; ++q) {
+        const uint4 x = ld_shared_v4(qp + 16 * q);
+        w[4 * q] = x.x;
+        w[4 * q + 1] = x.y;
+        w[4 * q + 2] = x.z;
+        w[4 * q + 3] = x.w;
       }
       uint32_t mx = 0u;                             // largest exponent field of the row
 #pragma unroll
@@ -435,8 +478,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, 1));
         x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, 1));
-        x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, 2));
-        x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, 2));
+        x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, 2)) - kLift;
+        x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, 2)) - kLift;
         const bool up = x0 > m[0] || x1 > m[1];
         if (__any_sync(0xffffffffu, up)) {
           const float n0 = fmaxf(m[0], x0), n1 = fmaxf(m[1], x1);
@@ -515,19 +558,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       const int ahead = i + C::kStages;
       if (ahead < n_tiles) {
-        const Tile f = shfl_tile((ahead >> 5) == (i >> 5) ? cur : next, ahead & 31);
-        if (f.pid >= 0 && ok) {
-          issue(f, stage);
-          pending |= 1 << stage;
-        }
+        const bool same = (ahead >> 5) == (i >> 5);
+        if (ok && issue(same ? cur : next, ahead & 31, stage)) pending |= 1 << stage;
       }
-      if ((i & 31) == 31) {
-        cur = next;
-        const int k = (i >> 5) + 2;
-        if (32 * k < n_tiles) next = look_up(k);
-      }
+      if ((i & 31) == 8 && (i | 31) + 1 < n_tiles) next = look_up((i >> 5) + 1);
+      if ((i & 31) == 31) cur = next;
     }
 
+    asm volatile("cp.async.wait_group 0;" ::: "memory");   // the next unit's queries
     // ---- the warps' results, joined
 #pragma unroll
     for (int hh = 0; hh < 2; ++hh) {
@@ -598,8 +636,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (tid == 0 && starts && !ends) {
       // The first CTA of a shared unit says what is to be joined.
       a.rec[2 * cta] = make_int4(u.r0, u.n, u.rb, u.head);
-      a.rec[2 * cta + 1] = make_int4(cta_of(W, G, u.c0 + u.chunks - 1), static_cast<int>(W),
-                                     static_cast<int>(W >> 32), 0);
+      a.rec[2 * cta + 1] = make_int4(cta_of(W, G, u.c0 + u.chunks - 1), W, 0, 0);
       shared_unit = true;
     }
     __syncthreads();
@@ -614,7 +651,7 @@ template <int D, bool SPARSE>
 cudaError_t launch_t(const CUtensorMap& tk, const CUtensorMap& tv, const CacheAttnArgs& a,
                      cudaStream_t stream) {
   auto kern = decode_kernel<D, SPARSE>;
-  const int smem = DecCfg<D>::kSmemFixed + (SPARSE ? 0 : (a.s.B + 1) * 8);
+  const int smem = DecCfg<D>::kSmemFixed + (SPARSE ? 0 : (a.s.B + 1) * 4);
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   kern<<<a.grid, kThreads, smem, stream>>>(tk, tv, a);

@@ -172,9 +172,13 @@ struct CacheAttnArgs {
   long long wait_budget;
 };
 
-constexpr int kCacheMaxCtas = 152;   // the SMs of one GB300
-constexpr int kDecodeRows = 16;
+constexpr int kSms = 152;            // of one GB300
+constexpr int kDecodeRows = 16;      // rows of a unit, keys of a piece of its work and CTAs per SM
+constexpr int kDecodeKeys = 128;
+constexpr int kDecodeCtas = 2;
 constexpr int kChunkRows = 256;
+constexpr int kChunkTileKeys = 128;
+constexpr int kChunkCtas = 1;
 
 // Few rows per sequence (tiles of 16, mma.sync); tk, tv: 3-D uint8 views
 // {d, Hkv * page, pages} of the codes, boxes of 32 rows, swizzled by a row's
