@@ -1041,12 +1041,17 @@ cudaError_t launch_t(const CUtensorMap& tk, const CUtensorMap& tv, const CacheAt
                      cudaStream_t stream) {
   auto kern = chunk_kernel<D>;
   const int smem = ChunkCfg<D>::kSmemFixed + (a.s.B + 1) * 4;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  static SmemLimit limit;
+  cudaError_t e = limit.raise(reinterpret_cast<const void*>(kern), smem);
   if (e != cudaSuccess) return e;
   // The register split inside the kernel is only valid for this launch size.
-  cudaFuncAttributes fa;
-  if ((e = cudaFuncGetAttributes(&fa, kern)) != cudaSuccess) return e;
-  if (fa.numRegs != kLaunchRegs) return cudaErrorInvalidConfiguration;
+  static std::atomic<int> regs{0};
+  if (regs.load(std::memory_order_relaxed) == 0) {
+    cudaFuncAttributes fa;
+    if ((e = cudaFuncGetAttributes(&fa, kern)) != cudaSuccess) return e;
+    regs.store(fa.numRegs, std::memory_order_relaxed);
+  }
+  if (regs.load(std::memory_order_relaxed) != kLaunchRegs) return cudaErrorInvalidConfiguration;
   const long long lanes = static_cast<long long>(a.s.T) * a.Hkv * a.group * (D / 16);
   split_kernel<D><<<static_cast<unsigned>((lanes + 255) / 256), 256, 0, stream>>>(a);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;

@@ -652,7 +652,8 @@ cudaError_t launch_t(const CUtensorMap& tk, const CUtensorMap& tv, const CacheAt
                      cudaStream_t stream) {
   auto kern = decode_kernel<D, SPARSE>;
   const int smem = DecCfg<D>::kSmemFixed + (SPARSE ? 0 : (a.s.B + 1) * 4);
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  static SmemLimit limit;
+  cudaError_t e = limit.raise(reinterpret_cast<const void*>(kern), smem);
   if (e != cudaSuccess) return e;
   kern<<<a.grid, kThreads, smem, stream>>>(tk, tv, a);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
