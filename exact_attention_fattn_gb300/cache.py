@@ -249,8 +249,12 @@ def fattn_cache_select(q, cache: Fp8Cache, page_table, q_start, kv_len, n_select
         out = torch.empty((T, cs.Hkv, n_selected), dtype=torch.int32, device=q.device)
     else:
         _check_like(out, (T, cs.Hkv, n_selected), torch.int32, dev, "out")
-    ws = _workspace(workspace, fattn_cache_select_workspace_bytes(T, cs.Hkv, max_pages), q.device, dev)
+    need = fattn_cache_select_workspace_bytes(T, cs.Hkv, max_pages)
+    ws_ptr = ws_bytes = 0
+    if workspace is not None or need != 256:   # 256: the scores stay on chip
+        ws = _workspace(workspace, need, q.device, dev)
+        ws_ptr, ws_bytes = ws.data_ptr(), ws.numel()
     _call(_lib.load().fattn_cache_select, dev, ctypes.byref(cs), q.data_ptr(), q_row, page_table.data_ptr(),
           q_start.data_ptr(), kv_len.data_ptr(), out.data_ptr(), n_selected, n_first, n_recent,
-          ws.data_ptr(), ws.numel(), T, B, heads, max_pages)
+          ws_ptr, ws_bytes, T, B, heads, max_pages)
     return out

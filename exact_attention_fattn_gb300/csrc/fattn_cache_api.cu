@@ -157,8 +157,9 @@ int fattn_cache_append(const fattn_cache* cache, const void* k_new, long long k_
   } else if (rope_dim != 0) {
     return FATTN_ERR_INVALID_ARG;
   }
-  const long long blocks =
-      (T / cache->page + 2ll * B) * cache->Hkv + (q ? static_cast<long long>(T) : 0);
+  // one block per page and head at most, and one per 8 groups of 8 heads of q
+  const long long blocks = (T / cache->page + 2ll * B) * cache->Hkv +
+                           (q ? static_cast<long long>(T) * ((Hq + 7) / 8) / 8 + 1 : 0);
   if (blocks > 0x7fffffffll) return FATTN_ERR_INVALID_ARG;
   CacheAppendArgs a{};
   long long budget = 0;
@@ -278,6 +279,7 @@ int fattn_cache_fwd(const fattn_cache* cache, const void* q, long long q_row, vo
 
 size_t fattn_cache_select_workspace_bytes(int T, int Hkv, int max_pages) {
   if (T <= 0 || Hkv <= 0 || Hkv > kMaxKvHeads || max_pages <= 0) return 0;
+  if (cache_select_at_once(T, Hkv, max_pages)) return 256;
   return align256(static_cast<size_t>(T) * Hkv * max_pages * sizeof(float));
 }
 
@@ -298,8 +300,9 @@ int fattn_cache_select(const fattn_cache* cache, const void* q, long long q_row,
     return FATTN_ERR_INVALID_ARG;
   if (static_cast<long long>(T) * cache->Hkv * n_selected > (1ll << 40)) return FATTN_ERR_INVALID_ARG;
   if (max_pages > 65535 * 128) return FATTN_ERR_INVALID_ARG;   // the grid's third extent
-  if (!workspace || !aligned(workspace, 256) ||
-      workspace_bytes < fattn_cache_select_workspace_bytes(T, cache->Hkv, max_pages))
+  const bool at_once = cache_select_at_once(T, cache->Hkv, max_pages);
+  if (!at_once && (!workspace || !aligned(workspace, 256) ||
+                   workspace_bytes < fattn_cache_select_workspace_bytes(T, cache->Hkv, max_pages)))
     return FATTN_ERR_INVALID_ARG;
   CacheSelectArgs a{};
   long long budget = 0;

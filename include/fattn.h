@@ -379,7 +379,8 @@ int fattn_cache_fwd(const fattn_cache* cache, const void* q, long long q_row, vo
  *   q         : in,  bf16 rows of Hq*d, as for fattn_cache_fwd
  *   selected  : out, int [T, Hkv, n_selected]: ascending, -1 behind the last
  *   workspace : at least fattn_cache_select_workspace_bytes(T, Hkv, max_pages), 256-byte aligned;
- *               contents on entry ignored
+ *               contents on entry ignored; NULL (0 bytes) will do where that function says 256, the
+ *               sizes that keep their scores on chip
  * Returns a fattn_status.
  */
 size_t fattn_cache_select_workspace_bytes(int T, int Hkv, int max_pages);
