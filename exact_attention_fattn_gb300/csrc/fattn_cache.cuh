@@ -25,6 +25,58 @@ __device__ __forceinline__ void record_bad_index(DeviceStatus* st, unsigned int 
   }
 }
 
+// Waits of these kernels, as compact as they can be: the code of all of a
+// CTA's roles shares the instruction caches, and a role that waits for its
+// instructions holds the others up.  A wait that runs out leaves its site in
+// the CTA's abort word, on which every other wait gives up; the kernel reports
+// it once, at its end (report_abort).
+struct Waits {
+  long long budget;            // cycles
+  volatile uint32_t* abort;    // shared memory
+};
+
+__device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, const Waits& w, unsigned int site) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const long long t0 = clock64();
+  while (!mbar_try_wait(bar, parity)) {
+    if (*w.abort) return false;
+    if (clock64() - t0 > w.budget) {
+      *w.abort = site;
+      return false;
+    }
+  }
+  return true;
+}
+
+// All lanes wait; the warp goes on only if every lane saw the phase.
+__device__ __forceinline__ bool wait_bar_warp(uint32_t bar, uint32_t parity, const Waits& w,
+                                              unsigned int site) {
+  return __all_sync(0xffffffffu, wait_bar(bar, parity, w, site));
+}
+
+__device__ __forceinline__ void report_abort(uint32_t site, DeviceStatus* st) {
+  if (site != 0u && atomicCAS(&st->code, 0u, kStatusTimeout) == 0u) {
+    st->where = site;
+    st->block = blockIdx.x;
+  }
+}
+
+// One thread's copies (it has the barrier to itself, or its warp waits for it).
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const void* tmap, uint32_t bar, int c0, int c1,
+                                            int c2) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(tmap)), "r"(bar), "r"(c0), "r"(c1), "r"(c2)
+      : "memory");
+}
+__device__ __forceinline__ void bulk_load_1d(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+      "l"(src), "r"(bytes), "r"(bar)
+      : "memory");
+}
+
 // One sequence of a call: its rows [r0, r0 + n) and its cached tokens.  A
 // sequence whose numbers make no sense is empty (n = len = 0), !ok.
 struct SeqInfo {

@@ -77,10 +77,9 @@ CacheSeqs seqs_of(const int* page_table, const int* q_start, const int* kv_len, 
 size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 
 // Partial results of the units that CTAs share, two per CTA, and, for the
-// tcgen05 kernel, half a unit's rows per CTA to pass between its warpgroups
-// and the call's q_rows queries in two parts.
+// tcgen05 kernel, the call's q_rows queries in two parts.
 struct AttnWorkspace {
-  size_t o_off, ml_off, rec_off, xo_off, xml_off, q_off, qs_off, total;
+  size_t o_off, ml_off, rec_off, q_off, qs_off, total;
 };
 
 AttnWorkspace attn_workspace(int rows, int d, size_t q_rows) {
@@ -90,10 +89,7 @@ AttnWorkspace attn_workspace(int rows, int d, size_t q_rows) {
   w.o_off = 0;
   w.ml_off = align256(slots * d * sizeof(float));
   w.rec_off = w.ml_off + align256(slots * sizeof(float2));
-  w.xo_off = w.rec_off + align256(2 * ctas * sizeof(int4));
-  const size_t xch = rows == kChunkRows ? static_cast<size_t>(ctas) * (kChunkRows / 2) : 0;
-  w.xml_off = w.xo_off + align256(xch * d * sizeof(float));
-  w.q_off = w.xml_off + align256(xch * sizeof(float2));
+  w.q_off = w.rec_off + align256(2 * ctas * sizeof(int4));
   if (rows != kChunkRows) q_rows = 0;
   w.qs_off = w.q_off + 2 * align256(q_rows * d);
   w.total = w.qs_off + align256(q_rows * sizeof(float));
@@ -244,8 +240,6 @@ int fattn_cache_fwd(const fattn_cache* cache, const void* q, long long q_row, vo
   a.part_o = reinterpret_cast<float*>(base + w.o_off);
   a.part_ml = reinterpret_cast<float2*>(base + w.ml_off);
   a.rec = reinterpret_cast<int4*>(base + w.rec_off);
-  a.xch_o = reinterpret_cast<float4*>(base + w.xo_off);
-  a.xch_ml = reinterpret_cast<float2*>(base + w.xml_off);
   a.q_codes = reinterpret_cast<uint8_t*>(base + w.q_off);
   a.q_lo = static_cast<long long>(align256(q_rows * cache->d));
   a.q_scale = reinterpret_cast<float*>(base + w.qs_off);

@@ -88,7 +88,8 @@ struct ChunkCfg {
   static constexpr int kNumBars = 2 * kKStages + 2 * kVStages + 17 + 2 * kSegs + 2;
   static constexpr int kMiscOff = kBarOff + kNumBars * 8;   // tmem, abort, valid[kVStages]
   static constexpr int kSegOff = (kMiscOff + 32 + 15) / 16 * 16;
-  static constexpr int kPreOff = kSegOff + kSegs * 64;      // [B + 1] int
+  static constexpr int kXmlOff = kSegOff + kSegs * 64;      // [kBM] float2
+  static constexpr int kPreOff = kXmlOff + kBM * 8;         // [B + 1] int
   static constexpr int kSmemFixed = kPreOff + 1024;
   __device__ static constexpr uint32_t col_s(int t) { return 128u * t; }
   __device__ static constexpr uint32_t col_o(int t) { return 256u + D * t; }
@@ -114,6 +115,38 @@ __device__ __forceinline__ uint32_t code_off(int r, int c) {
   return r * D + ((D == 128 ? c ^ (r & 7) : c ^ ((r >> 1) & 3)) << 4);
 }
 
+// MMAs and their commits from one lane of the converged MMA warp, chosen once
+// (`lead`): an election in front of each costs 25 instructions, more than the
+// MMA's own.
+__device__ __forceinline__ uint32_t elect_lane() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\tselp.u32 %0, 1, 0, e;\n\t}" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void mma_codes(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                          uint32_t accumulate, uint32_t lead) {
+  asm volatile(
+      "{\n\t.reg .pred p, e;\n\tsetp.ne.b32 e, %5, 0;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(lead)
+      : "memory");
+}
+__device__ __forceinline__ void mma_halves(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                           uint32_t accumulate, uint32_t lead) {
+  asm volatile(
+      "{\n\t.reg .pred p, e;\n\tsetp.ne.b32 e, %5, 0;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(lead)
+      : "memory");
+}
+__device__ __forceinline__ void commit_to(uint32_t bar, uint32_t lead) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\tsetp.ne.b32 e, %1, 0;\n\t"
+      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar),
+      "r"(lead)
+      : "memory");
+}
+
 // kind::f16 with fp16 A and B (format code 0), fp32 D; B is MN-major.
 __host__ __device__ constexpr uint32_t idesc_f16_f32(int M, int N) {
   return (1u << 4) | (1u << 16) | (static_cast<uint32_t>(N >> 3) << 17) |
@@ -124,21 +157,21 @@ __host__ __device__ constexpr uint32_t idesc_f16_f32(int M, int N) {
 // sees pos0 + R / g + 1 keys, so rows before row E see at most pos0 + ceil(E / g).
 // At least one, so that rows that see nothing are written, too.
 __device__ __forceinline__ int tiles_of(const CacheAttnArgs& a, int n, int len, int rb, int rows) {
-  const long long g = a.group;
-  const long long all = (len + kBN - 1) / kBN;
-  if (!a.causal) return static_cast<int>(max(1ll, all));
-  const long long end = min(n * g, static_cast<long long>(rb) * kUnitRows + rows);
-  const long long keys = (len - n) * g + end;
-  const long long nt = keys <= 0 ? 0 : (keys + kBN * g - 1) / (kBN * g);
-  return static_cast<int>(max(1ll, min(all, nt)));
+  int keys = len;
+  if (a.causal) {
+    const int end = min(n * a.group, rb * kUnitRows + rows);   // T * Hq < 2^31
+    keys = len - n + (end + a.group - 1) / a.group;
+  }
+  return max(1, (keys + kBN - 1) / kBN);
 }
 
 // One CTA's part of a unit: key tiles [a, e) for the rows from 256 rb of a
 // sequence.  Slot t (a softmax warpgroup with its TMEM columns) takes row tile
 // t and key tiles from j0(t) up to last(t).  A unit of at most 128 rows is
 // narrow: both slots take its one row tile, slot 0 the even key tiles of the
-// part and slot 1 the odd ones, and are joined at the end, so that one slot's
-// softmax runs beside the other's products there, too.
+// part and slot 1 the odd ones, so that one slot's softmax runs beside the
+// other's products there, too; slot 0's warps read both O's out of TMEM at the
+// end.
 struct __align__(16) Seg {
   int b, rb, head, nt;
   int r0, n, len, flags;
@@ -243,14 +276,11 @@ struct Walker {
   }
 };
 
-// Page `first` + lane of a sequence; -1 where it has none or a senseless one.
+// Page `first` + lane of a sequence, as the table has it; -1 past its end.
 __device__ __forceinline__ int page_of_lane(const CacheAttnArgs& a, int b, int len, int first) {
   const int p = first + static_cast<int>(threadIdx.x & 31);
   if ((static_cast<long long>(p) << a.page_shift) >= len) return -1;
-  const int pid = __ldg(a.s.table + static_cast<long long>(b) * a.s.max_pages + p);
-  if (pid >= 0 && pid < a.pages) return pid;
-  record_bad_index(a.status, kSitePage);
-  return -1;
+  return __ldg(a.s.table + static_cast<long long>(b) * a.s.max_pages + p);
 }
 
 template <int D>
@@ -362,11 +392,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = misc[0];
-  const WaitCtx wc{args.wait_budget, reinterpret_cast<volatile uint32_t*>(&misc[1]), args.status};
+  const Waits wc{args.wait_budget, reinterpret_cast<volatile uint32_t*>(&misc[1])};
   const long long W = pre[args.s.B];
   // Segment i of the CTA; a reader that is done with it hands it back.
   auto wait_seg = [&](uint32_t i) {
-    return mbar_wait_warp(seg_full(i), (i / kSegs) & 1, wc, kWaitSegment);
+    return wait_bar_warp(seg_full(i), (i / kSegs) & 1, wc, kWaitSegment);
   };
   auto done_seg = [&](uint32_t i) {
     __syncwarp();
@@ -383,7 +413,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tS = tmem + lane_off + C::col_s(t);
     const uint32_t tO = tmem + lane_off + C::col_o(t);
     const int pages_log = 7 - args.page_shift;   // log2 of the pages per key tile
-    uint32_t s_count = 0, o_count = 0, x_count = 0;
+    uint32_t s_count = 0, o_count = 0, x_count = 0, o1_count = 0;   // o1: slot 1's, as slot 0 counts them
+    float2* xml = reinterpret_cast<float2*>(smem + C::kXmlOff);
     bool ok = true;
 
     for (uint32_t si = 0; ok; ++si) {
@@ -409,6 +440,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       auto load_window = [&](int first) {
         w_base = first;
         w_pid = page_of_lane(args, s.b, s.len, first);
+        if (w_pid >= args.pages) w_pid = -1;   // the loader reports it
         w_ks = w_lv = 0.f;
         if (w_pid >= 0) {
           const long long sc = static_cast<long long>(w_pid) * args.Hkv + s.head;
@@ -436,7 +468,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int p3 = page_at(3);
         const bool hole = (missing >> p0 & (0xffffffffu >> (31 - (p3 - p0)))) != 0u;
         const bool masked = __any_sync(0xffffffffu, kv0 + kBN > lim || hole);
-        ok = __all_sync(0xffffffffu, mbar_wait(s_full(t), s_count & 1, wc, kWaitSFull));
+        ok = wait_bar_warp(s_full(t), s_count & 1, wc, kWaitSFull);
         if (!ok) break;
         ++s_count;
         tc_fence_after();
@@ -541,36 +573,24 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int i = 0; i < D / 4; ++i) part[i] = make_float4(0.f, 0.f, 0.f, 0.f);
           *part_ml = make_float2(-INFINITY, 0.f);
         }
+        if (t == 0 && s.active(1)) ++o1_count;
         done_seg(si);
         continue;
       }
-      ok = __all_sync(0xffffffffu, mbar_wait(o_full(t), o_count & 1, wc, kWaitOFull));
+      // (Slot 0 waits for a narrow unit's second O; it is long there when slot 1
+      // comes to its next one.)
+      if (!(s.narrow() && t == 1))
+        ok = wait_bar_warp(o_full(t), o_count & 1, wc, kWaitOFull);
       if (!ok) break;
       ++o_count;
       tc_fence_after();
-      // Narrow: slot 1 leaves its rows in the CTA's part of the workspace
-      // (16 bytes of 32 neighbouring rows side by side), slot 0 joins them.
-      float4* xch = args.xch_o + static_cast<long long>(cta) * kBM * (D / 4) + r_tile;
-      float2* xch_ml = args.xch_ml + cta * kBM + r_tile;
       if (s.narrow() && t == 1) {
         if (x_count > 0) {
-          ok = __all_sync(0xffffffffu, mbar_wait(x_empty, (x_count - 1) & 1, wc, kWaitDrain));
+          ok = wait_bar_warp(x_empty, (x_count - 1) & 1, wc, kWaitDrain);
           if (!ok) break;
         }
         ++x_count;
-#pragma unroll 1
-        for (int ch = 0; ch < D / 32; ++ch) {
-          uint32_t o[32];
-          tmem_ld32(tO + 32 * ch, o);
-          tmem_ld_wait32(o);
-#pragma unroll
-          for (int i = 0; i < 8; ++i)
-            xch[(8 * ch + i) * kBM] = make_float4(__uint_as_float(o[4 * i]), __uint_as_float(o[4 * i + 1]),
-                                                  __uint_as_float(o[4 * i + 2]), __uint_as_float(o[4 * i + 3]));
-        }
-        *xch_ml = make_float2(m_ref, l);
-        tc_fence_before();
-        mbar_arrive(o_empty(t));
+        xml[r_tile] = make_float2(m_ref, l);
         mbar_arrive(x_full);
         done_seg(si);
         continue;
@@ -578,17 +598,20 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool joined = s.narrow() && s.e - s.a > 1;
       float a0 = 1.f, a1 = 0.f;
       if (joined) {
-        ok = __all_sync(0xffffffffu, mbar_wait(x_full, x_count & 1, wc, kWaitDrain));
+        ok = wait_bar_warp(x_full, x_count & 1, wc, kWaitDrain) &&
+             wait_bar_warp(o_full(1), o1_count & 1, wc, kWaitOFull);
         if (!ok) break;
         ++x_count;
-        const float2 x = *xch_ml;
+        const float2 x = xml[r_tile];
         const float m = fmaxf(m_ref, x.x), m0 = m == -INFINITY ? 0.f : m;
         a0 = ex2_approx(m_ref - m0);
         a1 = ex2_approx(x.x - m0);
         // a row without any key keeps its zeros; a NaN stays one
         l = l * a0 + x.y * a1;
         m_ref = m;
+        tc_fence_after();
       }
+      if (s.active(1)) ++o1_count;
       // O, 32 columns at a time; compact on purpose (this code is out of the
       // instruction caches whenever it runs).
       const float inv = l == 0.f ? 0.f : 1.f / l;
@@ -599,17 +622,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int ch = 0; ch < D / 32; ++ch) {
         uint32_t o[32];
         tmem_ld32(tO + 32 * ch, o);
-        tmem_ld_wait32(o);
         if (joined) {
+          uint32_t o1[32];
+          tmem_ld32(tmem + lane_off + C::col_o(1) + 32 * ch, o1);
+          tmem_ld_wait32(o);
+          reg_fence32(o1);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const float4 v = xch[(8 * ch + i) * kBM];
-            const float f[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-            for (int z = 0; z < 4; ++z)
-              o[4 * i + z] = __float_as_uint(fmaf(f[z], a1, __uint_as_float(o[4 * i + z]) * a0));
-          }
+          for (int i = 0; i < 32; ++i)
+            o[i] = __float_as_uint(fmaf(__uint_as_float(o1[i]), a1, __uint_as_float(o[i]) * a0));
         }
+        tmem_ld_wait32(o);
         if (!on) continue;
         if (whole) {
 #pragma unroll
@@ -631,7 +653,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       tc_fence_before();
       mbar_arrive(o_empty(t));
-      if (joined) mbar_arrive(x_empty);
+      if (joined) {
+        mbar_arrive(o_empty(1));
+        mbar_arrive(x_empty);
+      }
       if (on) {
         if (whole) args.lse[out_row] = l == 0.f ? -INFINITY : (m_ref - kLift + log2f(l)) * kLn2;
         else *part_ml = make_float2(m_ref - kLift, l);
@@ -641,30 +666,30 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp == kMmaWarp) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kCtrlRegs));
     // ================================================================ MMA issue
+    const uint32_t lead = elect_lane();
     constexpr uint32_t idesc_qk = idesc_e4m3_f32(kBM, kBN);
     constexpr uint32_t idesc_pv = idesc_f16_f32(kBM, D);
     uint32_t kc = 0, hc = 0;              // K tiles and fp16 V tiles taken so far
     uint32_t qc[2] = {0u, 0u}, pc[2] = {0u, 0u}, oc[2] = {0u, 0u};
     auto issue_s = [&](int t) {
       const uint64_t db = sdesc_codes<D>(sbase + C::kKOff + (kc % C::kKStages) * C::kCodeTile);
+      const uint64_t da = sdesc_codes<D>(sbase + C::kQOff + t * C::kQBytes);
 #pragma unroll
-      for (int part = 0; part < 2; ++part) {
-        const uint64_t da = sdesc_codes<D>(sbase + C::kQOff + t * C::kQBytes + part * C::kCodeTile);
-#pragma unroll
-        for (int kk = 0; kk < D / 32; ++kk)
-          mma_ss_f8_w(tmem + C::col_s(t), da + 2 * kk, db + 2 * kk, idesc_qk, part + kk > 0 ? 1u : 0u);
+      for (int i = 0; i < D / 16; ++i) {          // the hi part's steps, then the lo part's
+        const uint32_t kk = 2u * (i & (D / 32 - 1)), part = i >= D / 32 ? C::kCodeTile >> 4 : 0u;
+        mma_codes(tmem + C::col_s(t), da + (kk + part), db + kk, idesc_qk, i > 0 ? 1u : 0u, lead);
       }
-      mma_commit_w(s_full(t));
+      commit_to(s_full(t), lead);
     };
     auto issue_pv = [&](int t, uint32_t acc) {
       const uint64_t dv = sdesc_sw128(sbase + C::kHOff + (hc & 1) * C::kHalfTile, C::kHalfChunk, 1024);
 #pragma unroll
       for (int kk = 0; kk < kBN / 16; ++kk)
-        mma_ts_w(tmem + C::col_o(t), tmem + C::col_s(t) + 8 * kk, dv + ((kk * 2048) >> 4), idesc_pv,
-                 kk > 0 ? 1u : acc);
+        mma_halves(tmem + C::col_o(t), tmem + C::col_s(t) + 8 * kk, dv + ((kk * 2048) >> 4), idesc_pv,
+                   kk > 0 ? 1u : acc, lead);
     };
     auto wait_k = [&]() {
-      return mbar_wait_warp(k_full(kc % C::kKStages), (kc / C::kKStages) & 1, wc, kWaitKvFull);
+      return wait_bar_warp(k_full(kc % C::kKStages), (kc / C::kKStages) & 1, wc, kWaitKvFull);
     };
     // One segment, tiles [a, e), row tile t up to e_t.  Its bounds come
     // through a shuffle, which tells the compiler that they are the same in
@@ -677,41 +702,41 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
         if ((t ? e1 : e0) > a) {
-          if (!mbar_wait_warp(q_full(t), qc[t]++ & 1, wc, kWaitQFull)) return false;
+          if (!wait_bar_warp(q_full(t), qc[t]++ & 1, wc, kWaitQFull)) return false;
           tc_fence_after();
           issue_s(t);
-          if (a + 1 == (t ? e1 : e0)) mma_commit_w(q_empty(t));   // its only scores
+          if (a + 1 == (t ? e1 : e0)) commit_to(q_empty(t), lead);   // its only scores
         }
       }
-      mma_commit_w(k_empty(kc % C::kKStages));
+      commit_to(k_empty(kc % C::kKStages), lead);
       ++kc;
       for (int j = a; j < e; ++j) {
-        if (!mbar_wait_warp(h_full(hc & 1), (hc >> 1) & 1, wc, kWaitDsFull)) return false;
+        if (!wait_bar_warp(h_full(hc & 1), (hc >> 1) & 1, wc, kWaitDsFull)) return false;
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
           const int et = t ? e1 : e0;
           // A K tile that neither row tile needs any more is taken all the same.
           if (t == 0 && j + 1 < e && !wait_k()) return false;
           if (j < et) {
-            if (j == a && oc[t] > 0 && !mbar_wait_warp(o_empty(t), (oc[t] - 1) & 1, wc, kWaitOFull))
+            if (j == a && oc[t] > 0 && !wait_bar_warp(o_empty(t), (oc[t] - 1) & 1, wc, kWaitOFull))
               return false;
-            if (!mbar_wait_warp(p_full(t), pc[t]++ & 1, wc, kWaitPFull)) return false;
+            if (!wait_bar_warp(p_full(t), pc[t]++ & 1, wc, kWaitPFull)) return false;
             tc_fence_after();
             issue_pv(t, j > a ? 1u : 0u);
             if (j + 1 == et) {
-              mma_commit_w(o_full(t));
+              commit_to(o_full(t), lead);
               ++oc[t];
             }
           }
           if (j + 1 < et) {
             issue_s(t);
-            if (j + 2 == et) mma_commit_w(q_empty(t));
+            if (j + 2 == et) commit_to(q_empty(t), lead);
           }
         }
-        mma_commit_w(h_empty(hc & 1));
+        commit_to(h_empty(hc & 1), lead);
         ++hc;
         if (j + 1 < e) {
-          mma_commit_w(k_empty(kc % C::kKStages));
+          commit_to(k_empty(kc % C::kKStages), lead);
           ++kc;
         }
       }
@@ -723,11 +748,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int t = 0; t < 2; ++t) {
         if (t < n) {
           if (!wait_k()) return false;
-          if (!mbar_wait_warp(q_full(t), qc[t]++ & 1, wc, kWaitQFull)) return false;
+          if (!wait_bar_warp(q_full(t), qc[t]++ & 1, wc, kWaitQFull)) return false;
           tc_fence_after();
           issue_s(t);
-          if (t + 2 >= n) mma_commit_w(q_empty(t));
-          mma_commit_w(k_empty(kc % C::kKStages));
+          if (t + 2 >= n) commit_to(q_empty(t), lead);
+          commit_to(k_empty(kc % C::kKStages), lead);
           ++kc;
         }
       }
@@ -735,22 +760,22 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
           if (i + t < n) {
-            if (!mbar_wait_warp(h_full(hc & 1), (hc >> 1) & 1, wc, kWaitDsFull)) return false;
-            if (i == 0 && oc[t] > 0 && !mbar_wait_warp(o_empty(t), (oc[t] - 1) & 1, wc, kWaitOFull))
+            if (!wait_bar_warp(h_full(hc & 1), (hc >> 1) & 1, wc, kWaitDsFull)) return false;
+            if (i == 0 && oc[t] > 0 && !wait_bar_warp(o_empty(t), (oc[t] - 1) & 1, wc, kWaitOFull))
               return false;
             if (i + t + 2 < n && !wait_k()) return false;
-            if (!mbar_wait_warp(p_full(t), pc[t]++ & 1, wc, kWaitPFull)) return false;
+            if (!wait_bar_warp(p_full(t), pc[t]++ & 1, wc, kWaitPFull)) return false;
             tc_fence_after();
             issue_pv(t, i > 0 ? 1u : 0u);
-            mma_commit_w(h_empty(hc & 1));
+            commit_to(h_empty(hc & 1), lead);
             ++hc;
             if (i + t + 2 < n) {
               issue_s(t);
-              if (i + t + 4 >= n) mma_commit_w(q_empty(t));
-              mma_commit_w(k_empty(kc % C::kKStages));
+              if (i + t + 4 >= n) commit_to(q_empty(t), lead);
+              commit_to(k_empty(kc % C::kKStages), lead);
               ++kc;
             } else {
-              mma_commit_w(o_full(t));
+              commit_to(o_full(t), lead);
               ++oc[t];
             }
           }
@@ -770,7 +795,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
     // No MMA may still be running when TMEM is released.
-    mma_commit_w(mma_done);
+    commit_to(mma_done, lead);
     mbar_wait_drain(mma_done, 0, args.wait_budget);
     __syncwarp();
   } else if (warp == kLoadWarp) {
@@ -799,8 +824,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = 0; i < 4; ++i) {
           pid[i] = -1;
           if (i < per) {
-            pid[i] = __shfl_sync(0xffffffffu, cur, (j << per_log) + i - base);
-            if (pid[i] >= 0) {
+            const int p = (j << per_log) + i;
+            pid[i] = __shfl_sync(0xffffffffu, cur, p - base);
+            if (pid[i] < 0 || pid[i] >= args.pages) {
+              if (lane == 0 && (static_cast<long long>(p) << args.page_shift) < s.len)
+                record_bad_index(args.status, kSitePage);
+              pid[i] = -1;
+            } else {
               mask |= ((1u << (4 >> per_log)) - 1u) << (i * (4 >> per_log));
               bytes += page_bytes;
             }
@@ -808,16 +838,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         const uint32_t ks = kn % C::kKStages, vs = vn % C::kVStages;
         if (kn >= C::kKStages &&
-            !mbar_wait_warp(k_empty(ks), (kn / C::kKStages - 1) & 1, wc, kWaitKvEmpty)) {
+            !wait_bar_warp(k_empty(ks), (kn / C::kKStages - 1) & 1, wc, kWaitKvEmpty)) {
           ok = false;
           break;
         }
-        const uint32_t kd = sbase + C::kKOff + ks * C::kCodeTile;
-        mbar_arrive_expect_tx_w(k_full(ks), bytes);
+        if (lane == 0) {
+          mbar_arrive_expect_tx(k_full(ks), bytes);
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (pid[i] >= 0)
-            tma_load_3d_w(kd + i * page_bytes, &tm_k, k_full(ks), 0, s.head << args.page_shift, pid[i]);
+          for (int i = 0; i < 4; ++i)
+            if (pid[i] >= 0)
+              tma_load_3d(sbase + C::kKOff + ks * C::kCodeTile + i * page_bytes, &tm_k, k_full(ks), 0,
+                          s.head << args.page_shift, pid[i]);
+        }
         ++kn;
         if (j == s.a) {
           // Q's two parts, up to 128 rows each; rows past the unit's last
@@ -825,32 +857,35 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
           for (int t = 0; t < 2 && ok; ++t) {
             if (!s.active(t)) continue;
-            if (qn[t] > 0) ok = mbar_wait_warp(q_empty(t), (qn[t] - 1) & 1, wc, kWaitQFull);
+            if (qn[t] > 0) ok = wait_bar_warp(q_empty(t), (qn[t] - 1) & 1, wc, kWaitQFull);
             if (!ok) break;
             const int first = s.row(t, 0);
             const uint32_t nb = static_cast<uint32_t>(min(kBM, s.n * args.group - first)) * D;
             const uint8_t* src = args.q_codes + (s.q_row(args) + first) * D;
             const uint32_t dst = sbase + C::kQOff + t * C::kQBytes;
-            mbar_arrive_expect_tx_w(q_full(t), 2 * nb);
-            bulk_load_1d_w(dst, src, nb, q_full(t));
-            bulk_load_1d_w(dst + C::kCodeTile, src + args.q_lo, nb, q_full(t));
+            if (lane == 0) {
+              mbar_arrive_expect_tx(q_full(t), 2 * nb);
+              bulk_load_1d(dst, src, nb, q_full(t));
+              bulk_load_1d(dst + C::kCodeTile, src + args.q_lo, nb, q_full(t));
+            }
             ++qn[t];
           }
           if (!ok) break;
         }
         if (vn >= C::kVStages &&
-            !mbar_wait_warp(v_empty(vs), (vn / C::kVStages - 1) & 1, wc, kWaitKvEmpty)) {
+            !wait_bar_warp(v_empty(vs), (vn / C::kVStages - 1) & 1, wc, kWaitKvEmpty)) {
           ok = false;
           break;
         }
-        const uint32_t vd = sbase + C::kVOff + vs * C::kCodeTile;
-        if (lane == 0) valid[vs] = mask;
-        __syncwarp();
-        mbar_arrive_expect_tx_w(v_full(vs), bytes);
+        if (lane == 0) {
+          valid[vs] = mask;
+          mbar_arrive_expect_tx(v_full(vs), bytes);
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (pid[i] >= 0)
-            tma_load_3d_w(vd + i * page_bytes, &tm_v, v_full(vs), 0, s.head << args.page_shift, pid[i]);
+          for (int i = 0; i < 4; ++i)
+            if (pid[i] >= 0)
+              tma_load_3d(sbase + C::kVOff + vs * C::kCodeTile + i * page_bytes, &tm_v, v_full(vs), 0,
+                          s.head << args.page_shift, pid[i]);
+        }
         ++vn;
       }
     }
@@ -879,7 +914,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         } else {
           x.flags = Seg::kLast;
         }
-        if (i >= kSegs && !mbar_wait_warp(seg_empty(i), (i / kSegs - 1) & 1, wc, kWaitSegment)) {
+        if (i >= kSegs && !wait_bar_warp(seg_empty(i), (i / kSegs - 1) & 1, wc, kWaitSegment)) {
           any = false;
           break;
         }
@@ -922,8 +957,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       done_seg(si);
       for (int j = a; j < e; ++j) {
         const uint32_t st = cnt % C::kVStages, hs = cnt & 1;
-        if (!mbar_wait_warp(v_full(st), (cnt / C::kVStages) & 1, wc, kWaitKvFull) ||
-            (cnt > 1 && !mbar_wait_warp(h_empty(hs), ((cnt >> 1) - 1) & 1, wc, kWaitMmaDone))) {
+        if (!wait_bar_warp(v_full(st), (cnt / C::kVStages) & 1, wc, kWaitKvFull) ||
+            (cnt > 1 && !wait_bar_warp(h_empty(hs), ((cnt >> 1) - 1) & 1, wc, kWaitMmaDone))) {
           ok = false;
           break;
         }
@@ -937,10 +972,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         // for instructions (measured: 2 x 2048 rows on 16384 keys 1142 us
         // unrolled, 767 us so).
 #pragma unroll 1
-        for (int i0 = 0; i0 < kIter; i0 += 4) {
-          uint4 w[4];
+        for (int i0 = 0; i0 < kIter; i0 += 2) {
+          uint4 w[2];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
+          for (int i = 0; i < 2; ++i) {
             const int id = ct + 128 * (i0 + i), row = row_of(id), c = chunk_of(id);
             w[i] = ld_shared_v4(src + code_off<D>(row, c));
             // Slots behind the end and pages that were not loaded hold
@@ -948,7 +983,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (edge && (row >= left || !(mask >> (row >> 5) & 1u))) w[i] = make_uint4(0u, 0u, 0u, 0u);
           }
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
+          for (int i = 0; i < 2; ++i) {
             const int id = ct + 128 * (i0 + i), row = row_of(id), c = chunk_of(id);
             const uint32_t base = dst + (c >> 2) * C::kHalfChunk + row * 128;
             const int c2 = 2 * (c & 3);            // 16-byte chunk of the fp16 row
@@ -975,6 +1010,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   tc_fence_before();
   __syncthreads();
+  if (tid == 0) report_abort(misc[1], args.status);
   if (warp == kMmaWarp) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);

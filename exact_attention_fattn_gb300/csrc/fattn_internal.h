@@ -167,9 +167,7 @@ struct CacheAttnArgs {
   float* part_o;              // workspace: partial outputs of the units that CTAs share
   float2* part_ml;
   int4* rec;
-  float4* xch_o;              // tcgen05 kernel: exchange between a CTA's two softmax warpgroups
-  float2* xch_ml;
-  uint8_t* q_codes;           // its queries as e4m3 pairs: hi [T * Hq, d], lo q_lo bytes further
+  uint8_t* q_codes;           // tcgen05 kernel: queries as e4m3 pairs, hi [T * Hq, d], lo q_lo bytes further
   long long q_lo;
   float* q_scale;             // the power of two taken out of each row
   int grid;                   // CTAs of the main kernel
