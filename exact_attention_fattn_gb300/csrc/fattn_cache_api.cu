@@ -97,10 +97,21 @@ AttnWorkspace attn_workspace(int rows, int d, size_t q_rows) {
 }
 
 // Which kernel: units of 16 rows on mma.sync, or of 256 on tcgen05.  Pages
-// selected per token leave a unit the group's rows of one token; otherwise
-// the rows of an average sequence decide.
-bool few_rows(int T, int B, int group, int n_selected) {
-  return n_selected > 0 || static_cast<long long>(T) * group <= static_cast<long long>(kDecodeRows) * B;
+// selected per token leave a unit the group's rows of one token.  Otherwise the rows of
+// an average sequence decide: up to 16 are one unit; with 2 to 4 units a
+// sequence the first kernel reads every key that often (out of L2 after the first
+// time) but starts and ends sooner, so it takes small calls.  Measured, 8 kv
+// heads, d = 128, mma.sync / tcgen05 us: 24 rows, 32 x 1000 tokens 41 / 53, 32 x
+// 4000 95 / 93, 16 x 16000 166 / 136; 40 rows, 32 x up to 4000 94 / 82; d = 64: 64
+// rows, 4 x 8000 39 / 39, 40 rows, 32 x 1000 37 / 49, 16 x 16000 158 / 126.
+// tokens: at most as many times a kv head the call can reach, -1 for unknown.
+bool few_rows(int T, int B, int group, int d, int n_selected, long long tokens) {
+  const long long units = (static_cast<long long>(T) * group + kDecodeRows * static_cast<long long>(B) - 1) /
+                          (kDecodeRows * static_cast<long long>(B));
+  if (n_selected > 0 || units <= 1) return true;
+  if (units > 4 || tokens < 0) return false;
+  const long long limit = (units == 2 ? 1ll << 19 : (units == 3 ? 1ll << 17 : 1ll << 16)) * (d == 64 ? 4 : 1);
+  return tokens <= limit;
 }
 
 }  // namespace
@@ -191,7 +202,8 @@ size_t fattn_cache_fwd_workspace_bytes(int T, int B, int Hq, int Hkv, int d, int
   if (T <= 0 || B <= 0 || B > kMaxSeqs || Hkv <= 0 || Hkv > kMaxKvHeads || Hq <= 0 ||
       Hq % Hkv != 0 || Hq / Hkv > kMaxGroup || (d != 64 && d != 128) || n_selected < 0)
     return 0;
-  return attn_workspace(few_rows(T, B, Hq / Hkv, n_selected) ? kDecodeRows : kChunkRows, d,
+  // of the larger layout, where the cache's size decides
+  return attn_workspace(few_rows(T, B, Hq / Hkv, d, n_selected, -1) ? kDecodeRows : kChunkRows, d,
                         static_cast<size_t>(T) * Hq)
       .total;
 }
@@ -232,7 +244,9 @@ int fattn_cache_fwd(const fattn_cache* cache, const void* q, long long q_row, vo
   a.page_shift = page_shift(cache->page);
   a.causal = causal != 0;
   a.scale_log2 = scale * 1.4426950408889634f;
-  const bool few = few_rows(T, B, a.group, n_selected);
+  const long long reach = static_cast<long long>(B) * max_pages;
+  const long long tokens = (reach < cache->pages ? reach : cache->pages) * cache->page * cache->Hkv;
+  const bool few = few_rows(T, B, a.group, cache->d, n_selected, tokens);
   const int unit_rows = few ? kDecodeRows : kChunkRows, piece_keys = few ? kDecodeKeys : kChunkTileKeys;
   const size_t q_rows = static_cast<size_t>(T) * Hq;
   const AttnWorkspace w = attn_workspace(unit_rows, cache->d, q_rows);

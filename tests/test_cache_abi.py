@@ -87,12 +87,15 @@ def test_bad_fwd(lib):  # noqa: F811
 
 
 def test_bad_select(lib):  # noqa: F811
-    need = lib.fattn_cache_select_workspace_bytes(3, 2, 2)
-    assert need >= 3 * 2 * 2 * 4
+    # Sizes whose scores stay on chip need no workspace; many pages do.
+    assert lib.fattn_cache_select_workspace_bytes(3, 2, 2) == 256
+    need = lib.fattn_cache_select_workspace_bytes(3, 2, 20000)
+    assert need >= 3 * 2 * 20000 * 4
     assert _select(lib, _cache(k_bounds=0)) == 1
     assert _select(lib, _cache(k_bounds=GOOD + 8)) == 1
     for kw in (dict(selected=0), dict(selected=GOOD + 2), dict(n_selected=0), dict(n_first=-1), dict(n_recent=-1),
-               dict(n_first=3, n_recent=2), dict(ws=0), dict(ws=GOOD + 16), dict(ws_bytes=need - 1)):
+               dict(n_first=3, n_recent=2), dict(ws=0, max_pages=20000), dict(ws=GOOD + 16, max_pages=20000),
+               dict(ws_bytes=need - 1, max_pages=20000)):
         assert _select(lib, _cache(), **kw) == 1, kw
     assert lib.fattn_cache_select_workspace_bytes(0, 2, 2) == 0
     assert lib.fattn_cache_select_workspace_bytes(3, 2, 0) == 0
