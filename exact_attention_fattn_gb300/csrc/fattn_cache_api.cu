@@ -84,7 +84,7 @@ struct AttnWorkspace {
 
 AttnWorkspace attn_workspace(int rows, int d, size_t q_rows) {
   AttnWorkspace w;
-  const int ctas = kSms * (rows == kChunkRows ? kChunkCtas : kDecodeCtas);
+  const int ctas = kSms * (rows == kChunkRows ? kChunkCtas : decode_ctas(d));
   const size_t slots = 2 * static_cast<size_t>(ctas) * rows;
   w.o_off = 0;
   w.ml_off = align256(slots * d * sizeof(float));
@@ -261,13 +261,13 @@ int fattn_cache_fwd(const fattn_cache* cache, const void* q, long long q_row, vo
   if (cudaGetDevice(&dev) != cudaSuccess ||
       cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
     return FATTN_ERR_CUDA;
-  const int max_ctas = (sms < kSms ? sms : kSms) * (few ? kDecodeCtas : kChunkCtas);
+  const int max_ctas = (sms < kSms ? sms : kSms) * (few ? decode_ctas(cache->d) : kChunkCtas);
   // Pieces of keys of all units, at most (the lengths are on the device).
   const long long keys = static_cast<long long>(selected ? n_selected : max_pages) * cache->page;
   const long long units =
       (selected ? static_cast<long long>(T) * ((a.group + unit_rows - 1) / unit_rows)
                 : static_cast<long long>(T) * a.group / unit_rows + B) * cache->Hkv;
-  const long long per = (keys + piece_keys - 1) / piece_keys;
+  const long long per = (keys + piece_keys - 1) / piece_keys + (few ? kDecodeUnitCost : 0);
   if (units > 0x7fffffffll / per) return FATTN_ERR_TOO_LARGE;   // the kernels number them in 32 bits
   const long long pieces = units * per;
   a.grid = pieces < max_ctas ? static_cast<int>(pieces) : max_ctas;

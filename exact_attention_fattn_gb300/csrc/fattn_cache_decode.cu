@@ -26,11 +26,14 @@
 //
 // Work split: a unit's keys are cut into chunks of 128 and the chunks of all
 // units, in order, are dealt to the CTAs in equal contiguous shares, so
-// lengths may differ by any factor.  A CTA's 4 warps take 32 keys of each
-// chunk, each with its own softmax state and its own ring of TMA tiles (no
+// lengths may differ by any factor.  A unit counts two pieces more than it has
+// chunks, about what beginning and ending it costs, so that CTAs with many
+// short units end with the others (the token batch of the figures below: 108
+// us without them, 103 with one, 101 with two and with three).  A CTA's 4
+// warps take 32 keys of each chunk, each with its own softmax state and its own ring of TMA tiles (no
 // barrier inside a chunk), and are joined through shared memory when the
 // CTA's part of the unit ends; the next unit's queries are on their way to
-// shared memory by then, and a second CTA on the SM works meanwhile.  A unit that
+// shared memory by then, and the SM's other CTAs work meanwhile.  A unit that
 // several CTAs share is joined from their partial results in a second
 // kernel, in order, so results do not depend on timing.
 #include <cuda_fp16.h>
@@ -56,8 +59,9 @@ struct DecCfg {
   static constexpr int kStages = 2;
   static constexpr int kStageBytes = 2 * kTileBytes;
   static constexpr int kRingBytes = kWarps * kStages * kStageBytes;
-  static constexpr int kJoinOff = kRingBytes;       // [kWarps][kRows][D] fp32
-  static constexpr int kMlOff = kJoinOff + kWarps * kRows * D * 4;    // [kWarps][kRows] float2
+  // A warp's rows of O at the end of a unit go where its last tile was.
+  static_assert(kRows * D * 4 <= kStageBytes, "a stage holds a warp's O");
+  static constexpr int kMlOff = kRingBytes;         // [kWarps][kRows] float2
   static constexpr int kQOff = kMlOff + kWarps * kRows * 8;           // [2][kRows][D] bf16
   static constexpr int kBarOff = kQOff + 2 * kRows * D * 2;
   static constexpr int kMiscOff = kBarOff + kWarps * kStages * 8;     // abort, then two units
@@ -99,11 +103,14 @@ struct Unit {
   int pos0;           // position of row r0
   int len;            // keys that exist
   int table_row;      // row of the page table
-  int c0, chunks;     // first chunk, and how many
+  int c0, chunks;     // first piece of work, and chunks; pieces() with what the unit itself costs
+  __device__ __forceinline__ int pieces(bool sparse) const {
+    return chunks + (sparse ? 0 : kDecodeUnitCost);   // sparse units all have the same number
+  }
 };
 
-// Chunks of the whole call, and the unit of a chunk.  pre: dense calls only,
-// chunks before each sequence (shared memory, [B + 1]).
+// Pieces of work of the whole call, and the unit of a piece.  pre: dense calls
+// only, pieces before each sequence (shared memory, [B + 1]).
 struct Schedule {
   const CacheAttnArgs* a;
   const int* pre;
@@ -144,15 +151,15 @@ struct Schedule {
       if (pre[mid] <= j) lo = mid; else hi = mid;
     }
     Unit u = sequence(lo);
-    const int id = (j - u.c0) / u.chunks;
-    u.c0 += id * u.chunks;
+    const int id = (j - u.c0) / u.pieces(false);
+    u.c0 += id * u.pieces(false);
     u.rb = id / a->Hkv;
     u.head = id - u.rb * a->Hkv;
     return u;
   }
   // The unit after u; there is one.
   __device__ __forceinline__ void advance(Unit& u) const {
-    u.c0 += u.chunks;
+    u.c0 += u.pieces(a->selected != nullptr);
     if (++u.head < a->Hkv) return;
     u.head = 0;
     ++u.rb;
@@ -215,7 +222,7 @@ __device__ __forceinline__ Tile shfl_tile(const Tile& t, int src) {
 }
 
 template <int D, bool SPARSE>
-__global__ void __launch_bounds__(kThreads, 2)
+__global__ void __launch_bounds__(kThreads, decode_ctas(D))
     decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                   const __grid_constant__ CacheAttnArgs a) {
   using C = DecCfg<D>;
@@ -226,7 +233,6 @@ __global__ void __launch_bounds__(kThreads, 2)
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   const uint32_t sbase = smem_u32(smem);
-  float* join = reinterpret_cast<float*>(smem + C::kJoinOff);
   float2* ml = reinterpret_cast<float2*>(smem + C::kMlOff);
   uint32_t* misc = reinterpret_cast<uint32_t*>(smem + C::kMiscOff);
   int* pre = reinterpret_cast<int*>(smem + C::kPreOff);
@@ -246,7 +252,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   if (tid == 0) misc[0] = 0u;
   fence_barrier_init();
 
-  // ---- chunks before each sequence
+  // ---- pieces of work before each sequence
   if constexpr (!SPARSE) {
     const int per = (a.s.B + kThreads - 1) / kThreads;
     const int b0 = min(a.s.B, tid * per), b1 = min(a.s.B, b0 + per);
@@ -255,7 +261,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       const SeqInfo q = seq_info(a.s, b, a.page_shift);
       if (!q.ok && cta == 0) record_bad_index(a.status, kSiteSeqStart);
       pre[b] = sum;
-      sum += (q.n * a.group + kRows - 1) / kRows * a.Hkv * chunks_of(q.len);
+      sum += (q.n * a.group + kRows - 1) / kRows * a.Hkv * (chunks_of(q.len) + kDecodeUnitCost);
     }
     int incl = sum;
 #pragma unroll
@@ -278,7 +284,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   const int W = sched.total();
   const int j0 = static_cast<int>(cta_first(W, G, cta)), j1 = static_cast<int>(cta_first(W, G, cta + 1));
   const int n_tiles = j1 - j0;                      // of this warp, and of every other
-  const WaitCtx wc{a.wait_budget, reinterpret_cast<volatile uint32_t*>(&misc[0]), a.status};
+  const Waits wc{a.wait_budget, reinterpret_cast<volatile uint32_t*>(&misc[0])};
 
   // A unit's queries into shared memory, rows past its last as zeros.
   auto fetch_q = [&](const Unit& u, int buf) {
@@ -296,13 +302,13 @@ __global__ void __launch_bounds__(kThreads, 2)
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
 
-  // The tiles of chunks j0 + 32 k .. + 31, one per lane.
+  // The tiles of pieces j0 + 32 k .. + 31, one per lane.
   auto look_up = [&](int k) -> Tile {
     Tile t{-1, 0, 0, 0.f, 0.f};
     const int i = 32 * k + lane;
     if (i >= n_tiles) return t;
     const Unit u = sched.unit_of(j0 + i);
-    if (u.n == 0) return t;
+    if (u.n == 0 || j0 + i - u.c0 >= u.chunks) return t;
     const int at = (j0 + i - u.c0) * kChunkKeys + warp * kTileKeys;
     const int page = 1 << a.page_shift;
     int entry = at >> a.page_shift;
@@ -336,10 +342,13 @@ __global__ void __launch_bounds__(kThreads, 2)
     const int pid = __shfl_sync(0xffffffffu, batch.pid, src);
     const int y = __shfl_sync(0xffffffffu, batch.y, src);
     if (pid < 0) return false;
-    const uint32_t dst = ring + stage * C::kStageBytes;
-    mbar_arrive_expect_tx_w(bar0 + 8 * stage, C::kStageBytes);
-    tma_load_3d_w(dst, &tm_k, bar0 + 8 * stage, 0, y, pid);
-    tma_load_3d_w(dst + C::kTileBytes, &tm_v, bar0 + 8 * stage, 0, y, pid);
+    if (lane == 0) {
+      const uint32_t dst = ring + stage * C::kStageBytes;
+      mbar_arrive_expect_tx(bar0 + 8 * stage, C::kStageBytes);
+      tma_load_3d(dst, &tm_k, bar0 + 8 * stage, 0, y, pid);
+      tma_load_3d(dst + C::kTileBytes, &tm_v, bar0 + 8 * stage, 0, y, pid);
+    }
+    __syncwarp();
     return true;
   };
 
@@ -356,16 +365,23 @@ __global__ void __launch_bounds__(kThreads, 2)
   uint32_t phases = 0u;                             // parity of each stage's next completion
   bool ok = true;
   bool shared_unit = false;                         // thread 0: this CTA's last unit goes on
+  // The tile that follows tile t in its stage; cur holds the tiles of `batch`.
+  auto refill = [&](int t, int batch) {
+    const int ahead = t + C::kStages, stage = t % C::kStages;
+    if (ok && ahead < n_tiles && issue((ahead >> 5) == batch ? cur : next, ahead & 31, stage))
+      pending |= 1 << stage;
+  };
   asm volatile("cp.async.wait_group 0;" ::: "memory");
   __syncthreads();
 
   int i = 0;                                        // tile of this warp
   for (int seg = 0; i < n_tiles; ++seg) {
-    // ---- the CTA's part of one unit: chunks [j0 + i, j0 + end)
+    // ---- the CTA's part of one unit: pieces [j0 + i, j0 + end)
     const Unit u = units[seg & 1];
-    const int end = min(j1, u.c0 + u.chunks) - j0;
-    const bool starts = j0 + i == u.c0, ends = j0 + end == u.c0 + u.chunks;
+    const int end = min(j1, u.c0 + u.pieces(SPARSE)) - j0;
+    const bool starts = j0 + i == u.c0, ends = j0 + end >= u.c0 + u.chunks;
     const bool whole = starts && ends;
+    const bool some = j0 + i < u.c0 + u.chunks;     // else no keys, and no part, are left for this CTA
     // A CTA shares at most two units: the one it starts inside (slot 0) and
     // the one that goes on after it (slot 1).
     const int slot = starts ? 1 : 0;
@@ -428,7 +444,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       const int stage = i % C::kStages;
       const Tile t = shfl_tile(cur, i & 31);
       if (t.pid >= 0 && ok) {
-        ok = mbar_wait_warp(bar0 + 8 * stage, phases >> stage & 1u, wc, kWaitKvFull);
+        ok = wait_bar_warp(bar0 + 8 * stage, phases >> stage & 1u, wc, kWaitKvFull);
         if (ok) pending &= ~(1 << stage);
       }
       if (t.pid >= 0 && ok) {
@@ -554,19 +570,19 @@ __global__ void __launch_bounds__(kThreads, 2)
           }
         }
       }
-      // ---- the stage's next tile
+      // ---- the stage's next tile (the unit's last one waits for the join)
       __syncwarp();
-      const int ahead = i + C::kStages;
-      if (ahead < n_tiles) {
-        const bool same = (ahead >> 5) == (i >> 5);
-        if (ok && issue(same ? cur : next, ahead & 31, stage)) pending |= 1 << stage;
-      }
+      if (i + 1 < end) refill(i, i >> 5);
       if ((i & 31) == 8 && (i | 31) + 1 < n_tiles) next = look_up((i >> 5) + 1);
       if ((i & 31) == 31) cur = next;
     }
 
     asm volatile("cp.async.wait_group 0;" ::: "memory");   // the next unit's queries
     // ---- the warps' results, joined
+    const int free_stage = (end - 1) % C::kStages;
+    auto join = [&](int w) {
+      return reinterpret_cast<float*>(smem + (w * C::kStages + free_stage) * C::kStageBytes);
+    };
 #pragma unroll
     for (int hh = 0; hh < 2; ++hh) {
       l[hh] += __shfl_xor_sync(0xffffffffu, l[hh], 1);
@@ -574,7 +590,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       if (c == 0) ml[warp * kRows + r + 8 * hh] = make_float2(m[hh], l[hh]);
       // Row r's columns kVals c + ..., 16 bytes at a time, the slots permuted
       // within 128 bytes so that eight neighbouring lanes meet eight banks.
-      float* base = join + (warp * kRows + r + 8 * hh) * D + kVals * c;
+      float* base = join(warp) + (r + 8 * hh) * D + kVals * c;
       const int key = (c + 4 * (r & 1)) & (kVals / 4 - 1);
 #pragma unroll
       for (int q = 0; q < kVals / 4; ++q) {
@@ -586,7 +602,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       }
     }
     __syncthreads();
-    if (!whole && tid < kRows) {
+    if (some && !whole && tid < kRows) {
       float mm = -INFINITY, ll = 0.f;
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) mm = fmaxf(mm, ml[w * kRows + tid].x);
@@ -598,7 +614,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       }
       a.part_ml[(2 * cta + slot) * kRows + tid] = make_float2(mm, ll);
     }
-    for (int f = tid; f < kRows * (D / 4); f += kThreads) {
+    for (int f = tid; some && f < kRows * (D / 4); f += kThreads) {
       const int row = f / (D / 4), q4 = f % (D / 4);
       const int rr = u.rb * kRows + row;
       if (rr >= u.n * a.group) continue;
@@ -614,7 +630,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         const float2 x = ml[w * kRows + row];
         const float b = x.x == -INFINITY ? (x.y != x.y ? x.y : 0.f) : ex2_approx(x.x - mm);
         const float4 v = *reinterpret_cast<const float4*>(
-            join + (w * kRows + row) * D + kVals * cq + 4 * ((q4 % (kVals / 4)) ^ key));
+            join(w) + row * D + kVals * cq + 4 * ((q4 % (kVals / 4)) ^ key));
         ll = fmaf(x.y, b, ll);
         acc.x = fmaf(v.x, b, acc.x);
         acc.y = fmaf(v.y, b, acc.y);
@@ -640,8 +656,11 @@ __global__ void __launch_bounds__(kThreads, 2)
       shared_unit = true;
     }
     __syncthreads();
+    fence_proxy_async_smem();       // TMA writes where the join was
+    refill(end - 1, end >> 5);
   }
   if (tid == 0 && !shared_unit) a.rec[2 * cta] = make_int4(0, 0, 0, 0);
+  if (tid == 0) report_abort(misc[0], a.status);
   // Copies in flight land before the CTA exits (only after a wait gave up).
   for (int s = 0; s < C::kStages; ++s)
     if (pending >> s & 1) mbar_wait_drain(bar0 + 8 * s, phases >> s & 1u, a.wait_budget);

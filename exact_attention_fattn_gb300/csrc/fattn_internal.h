@@ -178,7 +178,8 @@ struct CacheAttnArgs {
 constexpr int kSms = 152;            // of one GB300
 constexpr int kDecodeRows = 16;      // rows of a unit, keys of a piece of its work and CTAs per SM
 constexpr int kDecodeKeys = 128;
-constexpr int kDecodeCtas = 2;
+constexpr int kDecodeUnitCost = 2;   // pieces that a unit counts beyond its chunks
+constexpr int decode_ctas(int d) { return d == 64 ? 3 : 2; }
 constexpr int kChunkRows = 256;
 constexpr int kChunkTileKeys = 128;
 constexpr int kChunkCtas = 1;
