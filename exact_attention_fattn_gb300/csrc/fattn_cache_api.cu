@@ -267,7 +267,7 @@ int fattn_cache_fwd(const fattn_cache* cache, const void* q, long long q_row, vo
   const long long units =
       (selected ? static_cast<long long>(T) * ((a.group + unit_rows - 1) / unit_rows)
                 : static_cast<long long>(T) * a.group / unit_rows + B) * cache->Hkv;
-  const long long per = (keys + piece_keys - 1) / piece_keys + (few ? kDecodeUnitCost : 0);
+  const long long per = (keys + piece_keys - 1) / piece_keys + (few ? kDecodeUnitCost : kChunkUnitCost);
   if (units > 0x7fffffffll / per) return FATTN_ERR_TOO_LARGE;   // the kernels number them in 32 bits
   const long long pieces = units * per;
   a.grid = pieces < max_ctas ? static_cast<int>(pieces) : max_ctas;
