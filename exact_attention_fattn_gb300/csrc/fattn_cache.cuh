@@ -61,6 +61,30 @@ __device__ __forceinline__ void report_abort(uint32_t site, DeviceStatus* st) {
   }
 }
 
+// A call's kernels depend on the one before: the next is launched while that one
+// runs (allow_child, on every CTA's way) and waits, in every CTA, for its end and
+// for what it wrote (wait_for_parent; read with plain loads, whose order behind it
+// the compiler keeps).  A call's first kernel is launched in plain stream order,
+// so whatever was there before the call is complete for all of them.
+__device__ __forceinline__ void allow_child() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_for_parent() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+template <typename... P, typename... A>
+cudaError_t launch_child(void (*kernel)(P...), dim3 grid, dim3 block, int smem, cudaStream_t stream,
+                         const A&... args) {
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, P(args)...);
+}
+
 // One thread's copies (it has the barrier to itself, or its warp waits for it).
 __device__ __forceinline__ void tma_load_3d(uint32_t dst, const void* tmap, uint32_t bar, int c0, int c1,
                                             int c2) {

@@ -422,6 +422,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     float2* xml = reinterpret_cast<float2*>(smem + C::kXmlOff);
     bool ok = true;
 
+    wait_for_parent();                    // q_scale
     for (uint32_t si = 0; ok; ++si) {
       if (!(ok = wait_seg(si))) break;
       const Seg& s = seg_at(si);
@@ -435,7 +436,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (rr < s.n * args.group) {
           if (args.causal) lim = max(0, min(s.len, s.len - s.n + rr / args.group + 1));
           // log2(e) * scale times the power of two taken out of the row
-          c0 = args.scale_log2 * __ldg(args.q_scale + s.q_row(args) + rr);
+          c0 = args.scale_log2 * args.q_scale[s.q_row(args) + rr];
         }
       }
       const int jb = s.j0(t), nj = s.last(t), step = s.narrow() ? 2 : 1;
@@ -811,6 +812,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t kn = 0, vn = 0;              // K and V tiles asked for so far
     uint32_t qn[2] = {0u, 0u};            // and Q tiles
     bool ok = true;
+    wait_for_parent();                    // q_codes
     for (uint32_t si = 0; ok && wait_seg(si); ++si) {
       const Seg s = seg_at(si);
       if (s.flags & Seg::kLast) break;
@@ -1015,6 +1017,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   tc_fence_before();
   __syncthreads();
+  allow_child();
   if (tid == 0) report_abort(misc[1], args.status);
   if (warp == kMmaWarp) {
     tc_fence_after();
@@ -1030,6 +1033,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 // a row.
 template <int D>
 __global__ void __launch_bounds__(256) split_kernel(const __grid_constant__ CacheAttnArgs a) {
+  allow_child();
   constexpr int kLanes = D / 16;          // 16 columns each
   const int Hq = a.Hkv * a.group;
   const long long id = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x;
@@ -1096,8 +1100,7 @@ cudaError_t launch_t(const CUtensorMap& tk, const CUtensorMap& tv, const CacheAt
   const long long lanes = static_cast<long long>(a.s.T) * a.Hkv * a.group * (D / 16);
   split_kernel<D><<<static_cast<unsigned>((lanes + 255) / 256), 256, 0, stream>>>(a);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  kern<<<a.grid, kThreads, smem, stream>>>(tk, tv, a);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  if ((e = launch_child(kern, a.grid, kThreads, smem, stream, tk, tv, a)) != cudaSuccess) return e;
   return launch_cache_join(D, kUnitRows, a, stream);
 }
 

@@ -47,6 +47,7 @@ __global__ void __launch_bounds__(JoinCfg<D, ROWS>::kThreads) join_kernel(const 
   using J = JoinCfg<D, ROWS>;
   __shared__ Part side[J::kGroups][J::kRows][J::kF4];
   const int cta = blockIdx.x, G = a.grid;
+  wait_for_parent();
   const int4 rec = a.rec[2 * cta];
   const int rows = rec.y * a.group - rec.z * ROWS;   // of the unit, from its first
   if (rec.y == 0 || static_cast<int>(blockIdx.y) * J::kRows >= rows) return;
@@ -60,8 +61,8 @@ __global__ void __launch_bounds__(JoinCfg<D, ROWS>::kThreads) join_kernel(const 
   for (int c = cta + group; on && c <= more.x; c += J::kGroups) {
     if (cta_first(W, G, c) == cta_first(W, G, c + 1)) continue;   // a CTA without work
     const long long at = (2ll * c + (c == cta ? 1 : 0)) * ROWS + row;
-    const float2 ml = __ldg(a.part_ml + at);
-    merge(p, Part{ml.x, ml.y, __ldg(reinterpret_cast<const float4*>(a.part_o + at * D) + q4)});
+    const float2 ml = a.part_ml[at];
+    merge(p, Part{ml.x, ml.y, reinterpret_cast<const float4*>(a.part_o + at * D)[q4]});
   }
   if constexpr (J::kGroups > 1) {
     side[group][local][q4] = p;
@@ -84,8 +85,7 @@ template <int D, int ROWS>
 cudaError_t launch_t(const CacheAttnArgs& a, cudaStream_t stream) {
   using J = JoinCfg<D, ROWS>;
   static_assert(J::kThreads <= 1024, "block size");
-  join_kernel<D, ROWS><<<dim3(a.grid, ROWS / J::kRows), J::kThreads, 0, stream>>>(a);
-  return cudaGetLastError();
+  return launch_child(join_kernel<D, ROWS>, dim3(a.grid, ROWS / J::kRows), J::kThreads, 0, stream, a);
 }
 
 }  // namespace

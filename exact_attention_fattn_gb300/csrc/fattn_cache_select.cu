@@ -292,6 +292,7 @@ template <int D>
 __global__ void __launch_bounds__(kSelThreads, 4) score_kernel(const __grid_constant__ CacheSelectArgs a) {
   using S = Scorer<D, kSelThreads>;
   __shared__ typename S::Shared sh;
+  allow_child();
   const int row = blockIdx.x, head = blockIdx.y, p0 = blockIdx.z * S::kPages;
   int b, pos;
   if (!row_position(a, row, b, pos)) return;
@@ -304,6 +305,7 @@ __global__ void __launch_bounds__(kSelThreads, 4) score_kernel(const __grid_cons
 // Grid (T, Hkv): choice from the workspace.
 __global__ void __launch_bounds__(kSelThreads, 4) choose_kernel(const __grid_constant__ CacheSelectArgs a) {
   __shared__ ChooseShared sh;
+  wait_for_parent();
   const int row = blockIdx.x, head = blockIdx.y;
   int b, pos;
   if (!row_position(a, row, b, pos)) return;
@@ -325,8 +327,7 @@ cudaError_t launch_t(const CacheSelectArgs& a, cudaStream_t stream) {
   score_kernel<D><<<dim3(a.s.T, a.Hkv, (a.s.max_pages + kPages - 1) / kPages), kSelThreads, 0, stream>>>(a);
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  choose_kernel<<<pairs, kSelThreads, 0, stream>>>(a);
-  return cudaGetLastError();
+  return launch_child(choose_kernel, pairs, kSelThreads, 0, stream, a);
 }
 
 }  // namespace
