@@ -120,6 +120,14 @@ __device__ __forceinline__ SeqInfo seq_info(const CacheSeqs& s, int b, int page_
   return q;
 }
 
+// Pieces of work of a whole call.  The host has bounded them to 32 bits for
+// sequences one behind the other; with overlapping ones the call does nothing.
+__device__ __forceinline__ int total_of(long long pieces, DeviceStatus* st) {
+  if (pieces <= 0x7fffffffll) return static_cast<int>(pieces);
+  if (blockIdx.x == 0) record_bad_index(st, kSiteSeqStart);
+  return 0;
+}
+
 // The largest b in [0, B) with f(b) <= x, f ascending, found by a whole warp
 // 32 values at a time (one round of loads up to 32 sequences, two up to 1024).
 // Any b in [0, B) when f is not ascending or f(0) > x.

@@ -391,7 +391,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     long long at = incl - sum;
     for (int w = 0; w < warp; ++w) at += wtot[w];
     for (int b = b0; b < b1; ++b) pre[b] += static_cast<int>(at);
-    if (tid == kThreads - 1) pre[args.s.B] = static_cast<int>(at + sum);
+    if (tid == kThreads - 1) pre[args.s.B] = total_of(at + sum, args.status);
   }
   tc_fence_before();
   __syncthreads();

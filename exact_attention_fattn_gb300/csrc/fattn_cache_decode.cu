@@ -264,26 +264,28 @@ __global__ void __launch_bounds__(kThreads, decode_ctas(D))
   if constexpr (!SPARSE) {
     const int per = (a.s.B + kThreads - 1) / kThreads;
     const int b0 = min(a.s.B, tid * per), b1 = min(a.s.B, b0 + per);
-    int sum = 0;
+    // 64 bits: sequences whose rows overlap may need more than the call can
+    long long sum = 0;
     for (int b = b0; b < b1; ++b) {
       const SeqInfo q = seq_info(a.s, b, a.page_shift);
       if (!q.ok && cta == 0) record_bad_index(a.status, kSiteSeqStart);
-      pre[b] = sum;
-      sum += (q.n * a.group + kRows - 1) / kRows * a.Hkv * (chunks_of(q.len) + kDecodeUnitCost);
+      pre[b] = static_cast<int>(sum);
+      sum += static_cast<long long>((q.n * a.group + kRows - 1) / kRows) * a.Hkv *
+             (chunks_of(q.len) + kDecodeUnitCost);
     }
-    int incl = sum;
+    long long incl = sum;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
-      const int t = __shfl_up_sync(0xffffffffu, incl, off);
+      const long long t = __shfl_up_sync(0xffffffffu, incl, off);
       if (lane >= off) incl += t;
     }
-    int* wtot = reinterpret_cast<int*>(ml);
+    long long* wtot = reinterpret_cast<long long*>(ml);
     if (lane == 31) wtot[warp] = incl;
     __syncthreads();
-    int at = incl - sum;
+    long long at = incl - sum;
     for (int w = 0; w < warp; ++w) at += wtot[w];
-    for (int b = b0; b < b1; ++b) pre[b] += at;
-    if (tid == kThreads - 1) pre[a.s.B] = at + sum;
+    for (int b = b0; b < b1; ++b) pre[b] += static_cast<int>(at);
+    if (tid == kThreads - 1) pre[a.s.B] = total_of(at + sum, a.status);
   }
   __syncthreads();
 

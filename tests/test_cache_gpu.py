@@ -531,3 +531,128 @@ def test_two_streams_at_once():
         for x, y in zip(got, want):
             assert torch.equal(x[0], y[0]) and torch.equal(x[1], y[1])
     status_ok()
+
+
+# ------------------------------------------------------------------ sizes at the kernels' edges
+
+@pytest.mark.parametrize("d,page", [(64, 32), (64, 128), (128, 32), (128, 64), (128, 128)])
+def test_attend_row_counts_around_the_tiles(d, page):
+    """Units of 65 to 300 rows on one key tile to four, whole and shared
+    between CTAs, beside a single token."""
+    check(Batch(141, [65, 256, 134, 257, 1, 500, 300, 128, 390], [65, 128, 129, 255, 1, 257, 300, 127, 66], 2, 1, d, page))
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("g,news", [(12, [7, 6, 11]), (5, [40, 52, 26]), (33, [4, 3, 9])])
+def test_attend_groups_that_split_tiles_unevenly(d, g, news):
+    """Rows of one token on both sides of a tile's end."""
+    check(Batch(142, [900, 131, 513], news, 1, g, d, 64))
+
+
+@pytest.mark.parametrize("news,g", [(1, 2), (5, 16)])
+def test_attend_most_sequences(news, g):
+    """4096 sequences of a few tokens, some without rows."""
+    r = np.random.default_rng(143)
+    lens = [int(x) for x in r.integers(news, 40, 4096)]
+    check(Batch(143, lens, [news if i % 7 else 0 for i in range(4096)], 1, g, 128, 32, pad_rows=3))
+
+
+@pytest.mark.parametrize("seed", range(16))
+def test_attend_drawn_batches(seed):
+    r = np.random.default_rng(1000 + seed)
+    d, page, g, hkv = (int(r.choice(x)) for x in ([64, 128], [32, 64, 128], [1, 2, 3, 5, 8, 16], [1, 2, 3]))
+    B = int(r.integers(1, 9))
+    most = int(r.choice([1, 4, 30, 200]))
+    lens = [int(x) for x in np.exp(r.uniform(0, np.log(3000), B)).astype(int) + 1]
+    news = [min(t, int(r.integers(0, most + 1))) for t in lens]
+    news[0] = max(1, news[0])
+    check(Batch(150 + seed, lens, news, hkv, g, d, page, pad_rows=seed % 3), causal=seed % 5 != 0)
+
+
+@pytest.mark.parametrize("lens,news,hkv,k", [
+    ([2300 * 32], [2], 1, 20),                      # scores in the workspace: few rows
+    ([2300 * 32 - 5, 70], [80, 2], 2, 20),          # on chip: a pair for every SM
+    ([10400 * 32 - 31], [80], 2, 40)])              # in the workspace: more pages than fit
+def test_select_many_pages(lens, news, hkv, k):
+    b = Batch(144, lens, news, hkv, 2, 64, 32)
+    assert np.array_equal(run_select(b, k, 1, 2), C.select(b.q, b.cache, b.table, b.q_start, b.kv_len, k, 1, 2))
+
+
+# ------------------------------------------------------------------ memory the caller owns
+
+def test_queries_rotated_in_place():
+    b = Batch(145, [150, 40], [60, 1], 2, 4, 128, 64, pad_rows=2, filled=False)
+    c, *where = b.device()
+    rope = K.fattn_rope_table(150, 96)
+    q = b.rows(b.q)
+    want = K.fattn_cache_append(b.rows(b.k_new), b.rows(b.v_new), c, *where, rope=rope, q=q)[:61].clone()
+    got = K.fattn_cache_append(b.rows(b.k_new), b.rows(b.v_new), c, *where, rope=rope, q=q, q_out=q)
+    assert got is q and torch.equal(q[:61], want) and torch.equal(q[61:], b.rows(b.q)[61:])
+    status_ok()
+
+
+def test_one_workspace_of_the_stated_size_for_call_after_call():
+    """Whatever the last call left in it; nothing behind it is written."""
+    bs = [Batch(146, [900, 131], [1, 1], 2, 4, 128, 64), Batch(147, [900, 500], [90, 200], 2, 4, 128, 64),
+          Batch(148, [700, 64], [3, 2], 2, 16, 64, 32)]
+    ws = None
+    for b in bs * 2:
+        c, *where = b.device()
+        q = b.rows(b.q)
+        sel = K.fattn_cache_select(q, c, *where, 4)
+        for s in (None, sel):
+            need = K.fattn_cache_fwd_workspace_bytes(b.T, 2, b.hq, 2, b.d, 0 if s is None else 4)
+            if ws is None:
+                ws = torch.full((1 << 27,), 0xFF, dtype=torch.uint8, device="cuda")
+            assert need < ws.numel()
+            ws[need:need + 4096] = 0xA5
+            got = K.fattn_cache_fwd(q, c, *where, selected=s, workspace=ws[:need])
+            want = K.fattn_cache_fwd(q, c, *where, selected=s)
+            assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+            assert bool((ws[need:need + 4096] == 0xA5).all())
+    status_ok()
+
+
+def test_streams_and_graphs_at_once():
+    """Both attention kernels, the selection and a replayed graph on four
+    streams; every call has its own workspace."""
+    bs = [Batch(161, [3000, 200], [1, 1], 2, 4, 128, 64), Batch(162, [2000, 700], [300, 90], 2, 4, 128, 64),
+          Batch(163, [4000, 900], [2, 1], 2, 4, 64, 32), Batch(164, [1500, 1100], [70, 250], 2, 4, 64, 128)]
+    dev = [b.device() for b in bs]
+    qs = [b.rows(b.q) for b in bs]
+
+    def call(i):
+        q, d = qs[i], dev[i]
+        sel = K.fattn_cache_select(q, *d, 5) if i == 2 else None
+        return K.fattn_cache_fwd(q, *d, selected=sel)
+
+    want = [tuple(x.clone() for x in call(i)) for i in range(4)]
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out3 = call(3)
+    streams = [torch.cuda.Stream() for _ in bs]
+    for _ in range(20):
+        got = [None] * 4
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                if i == 3:
+                    graph.replay()
+                    got[3] = out3
+                else:
+                    got[i] = call(i)
+        torch.cuda.synchronize()
+        for x, y in zip(got, want):
+            assert torch.equal(x[0], y[0]) and torch.equal(x[1], y[1])
+    status_ok()
+
+
+@pytest.mark.parametrize("news", [3, 90])
+def test_overlapping_sequences_are_reported(news):
+    """q_start that goes back: the sequence between is empty, and reported."""
+    b = Batch(149, [200, 150, 180], [news, 0, 0], 1, 2, 64, 32)
+    b.q_start = np.array([0, news, 0, news], dtype=np.int32)
+    c, *where = b.device()
+    K.fattn_cache_fwd(b.rows(b.q), c, *where)
+    assert A.fattn_check_status() == _lib.FATTN_ERR_BAD_INDEX
+    status_ok()
