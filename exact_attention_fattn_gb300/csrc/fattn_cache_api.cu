@@ -101,16 +101,18 @@ AttnWorkspace attn_workspace(int rows, int d, size_t q_rows) {
 // an average sequence decide: up to 16 are one unit; with 2 to 4 units a
 // sequence the first kernel reads every key that often (out of L2 after the first
 // time) but starts and ends sooner, so it takes small calls.  Measured, 8 kv
-// heads, d = 128, mma.sync / tcgen05 us: 24 rows, 32 x 1000 tokens 41 / 53, 32 x
-// 4000 95 / 93, 16 x 16000 166 / 136; 40 rows, 32 x up to 4000 94 / 82; d = 64: 64
-// rows, 4 x 8000 39 / 39, 40 rows, 32 x 1000 37 / 49, 16 x 16000 158 / 126.
+// heads, mma.sync / tcgen05 us: d = 128: 16 rows, 32 x 1000 tokens 29 / 47, 16 x
+// 16000 93 / 133; 24 rows, 32 x 2000 57 / 63, 32 x 4000 94 / 90; 40 rows, 32 x 500
+// 37 / 36, 32 x up to 4000 93 / 72; 64 rows, 8 x 1000 26.7 / 27.1, 32 x 500 46 / 37.
+// d = 64: 24 rows, 16 x 16000 103 / 125; 40 rows, 32 x 1000 36 / 43, 32 x 4000 86 /
+// 83; 64 rows, 4 x 8000 37 / 34.
 // tokens: at most as many times a kv head the call can reach, -1 for unknown.
 bool few_rows(int T, int B, int group, int d, int n_selected, long long tokens) {
   const long long units = (static_cast<long long>(T) * group + kDecodeRows * static_cast<long long>(B) - 1) /
                           (kDecodeRows * static_cast<long long>(B));
   if (n_selected > 0 || units <= 1) return true;
   if (units > 4 || tokens < 0) return false;
-  const long long limit = (units == 2 ? 1ll << 19 : (units == 3 ? 1ll << 17 : 1ll << 16)) * (d == 64 ? 4 : 1);
+  const long long limit = (units == 2 ? 1ll << 19 : 1ll << 16) * (d == 64 && units < 4 ? 4 : 1);
   return tokens <= limit;
 }
 
