@@ -289,7 +289,7 @@ int fattn_cache_fwd(const fattn_cache* cache, const void* q, long long q_row, vo
 
 size_t fattn_cache_select_workspace_bytes(int T, int Hkv, int max_pages) {
   if (T <= 0 || Hkv <= 0 || Hkv > kMaxKvHeads || max_pages <= 0) return 0;
-  if (cache_select_at_once(T, Hkv, max_pages)) return 256;
+  if (cache_select_at_once(max_pages)) return 256;
   return align256(static_cast<size_t>(T) * Hkv * max_pages * sizeof(float));
 }
 
@@ -310,7 +310,7 @@ int fattn_cache_select(const fattn_cache* cache, const void* q, long long q_row,
     return FATTN_ERR_INVALID_ARG;
   if (static_cast<long long>(T) * cache->Hkv * n_selected > (1ll << 40)) return FATTN_ERR_INVALID_ARG;
   if (max_pages > 65535 * 128) return FATTN_ERR_INVALID_ARG;   // the grid's third extent
-  const bool at_once = cache_select_at_once(T, cache->Hkv, max_pages);
+  const bool at_once = cache_select_at_once(max_pages);
   if (!at_once && (!workspace || !aligned(workspace, 256) ||
                    workspace_bytes < fattn_cache_select_workspace_bytes(T, cache->Hkv, max_pages)))
     return FATTN_ERR_INVALID_ARG;

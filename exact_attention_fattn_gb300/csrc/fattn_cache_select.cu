@@ -11,11 +11,13 @@
 // follow the definition choose the same pages.  Ties go to the lower page.
 //
 // Bound: the bounds' bytes, 2 d a page and head, streamed 16 bytes a lane with 8
-// pages in flight per group of lanes, against 16 x 8 bit dot products.  The
-// choice is a radix select, eight bits of the scores at a time.  Where the
-// (row, head) pairs fill the GPU or the pages are few, one CTA scores and
-// chooses for one pair, scores in shared memory; a few pairs with many pages
-// are scored by CTAs of 128 or 256 pages each and chosen from by a second kernel.
+// pages in flight per group of lanes, against 16 x 8 bit dot products, and latency
+// where the pages are few.  The choice is a radix select, eight bits of the scores
+// at a time.  A cluster of up to 8 CTAs scores and chooses for one (row, head) pair,
+// scores in the first one's shared memory; where they do not fit there (10000
+// pages), CTAs of 128 or 256 pages each score into the workspace and a second
+// kernel chooses.  Measured: one row of 12 pairs on 938 pages, with the attention, 21.2
+// us (23.6 without clusters).
 #include "fattn_cache.cuh"
 
 namespace fattn {
@@ -48,6 +50,22 @@ __device__ __forceinline__ int4 ld_stream(const int8_t* p) {
                : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
                : "l"(p));
   return v;
+}
+
+// Cluster barrier, and a store to the shared memory of a cluster's first CTA.
+__device__ __forceinline__ void cluster_arrive() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t first_cta_addr(uint32_t addr) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(addr));
+  return r;
+}
+__device__ __forceinline__ void st_cluster(uint32_t addr, float x) {
+  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(x) : "memory");
 }
 
 // The group's query sums A- and A+ of a row and head, and from them the
@@ -127,9 +145,10 @@ struct Scorer {
     }
     return r;
   }
-  // Scores of the pages looked up, to out[page]; -inf for a page that is not
-  // there.
-  __device__ __forceinline__ void score(const Pages& r, int n, float* out) const {
+  // Scores of the pages looked up, as out(page, score); -inf for a page that is
+  // not there.
+  template <class Out>
+  __device__ __forceinline__ void score(const Pages& r, int n, Out out) const {
     const int gl = threadIdx.x % LP, src0 = (threadIdx.x & 31) & ~(LP - 1);
     int4 w[kInFlight];
 #pragma unroll
@@ -155,7 +174,7 @@ struct Scorer {
       if (gl == i) mine_sum = s;
     }
     if (gl < kInFlight && r.mine < n)
-      out[r.mine] = r.pid >= 0 ? __fmul_rn(__int2float_rn(mine_sum), r.ks) : -INFINITY;
+      out(r.mine, r.pid >= 0 ? __fmul_rn(__int2float_rn(mine_sum), r.ks) : -INFINITY);
   }
 };
 
@@ -261,7 +280,8 @@ __device__ __forceinline__ bool take_all(const CacheSelectArgs& a, int n, int* o
   return true;
 }
 
-// Grid (T, Hkv): scores and choice.
+// Grid (T, Hkv, C) in clusters of C along z: the cluster's CTAs score 1 / C of a
+// pair's pages each, into the first one's shared memory, and that one chooses.
 template <int D>
 __global__ void __launch_bounds__(kOnceThreads, 2) select_kernel(const __grid_constant__ CacheSelectArgs a) {
   using S = Scorer<D, kOnceThreads>;
@@ -270,18 +290,32 @@ __global__ void __launch_bounds__(kOnceThreads, 2) select_kernel(const __grid_co
     ChooseShared choose;
   } sh;
   extern __shared__ float scores[];
-  const int row = blockIdx.x, head = blockIdx.y;
+  const int row = blockIdx.x, head = blockIdx.y, rank = blockIdx.z;
+  const bool shared = gridDim.z > 1;
+  if (shared) cluster_arrive();        // the first CTA has started when others write to it
   int b, pos;
+  // the same for all CTAs of a cluster
   if (!row_position(a, row, b, pos)) return;
   const int n = pos < 0 ? 0 : (pos >> a.page_shift) + 1;
   int* out = a.selected + (static_cast<long long>(row) * a.Hkv + head) * a.n_selected;
-  if (take_all(a, n, out)) return;
+  if (n <= a.n_selected) {
+    if (rank == 0) take_all(a, n, out);
+    return;
+  }
+  const int p1 = rank * S::kPages, step = gridDim.z * S::kPages;
   const S s(a, sh.score, row, head, b);
-  typename S::Pages next = s.look_up(0, n);
-  for (int p0 = 0; p0 < n; p0 += S::kPages) {
+  typename S::Pages next = s.look_up(p1, n);
+  const uint32_t to = first_cta_addr(smem_u32(scores));
+  if (shared) cluster_wait();
+  for (int p0 = p1; p0 < n; p0 += step) {
     const typename S::Pages cur = next;
-    if (p0 + S::kPages < n) next = s.look_up(p0 + S::kPages, n);
-    s.score(cur, n, scores);
+    if (p0 + step < n) next = s.look_up(p0 + step, n);
+    s.score(cur, n, [&](int page, float x) { st_cluster(to + 4 * page, x); });
+  }
+  if (shared) {
+    cluster_arrive();
+    cluster_wait();
+    if (rank != 0) return;
   }
   __syncthreads();
   choose<kOnceThreads>(a, sh.choose, scores, n, out);
@@ -299,7 +333,8 @@ __global__ void __launch_bounds__(kSelThreads, 4) score_kernel(const __grid_cons
   const int n = pos < 0 ? 0 : (pos >> a.page_shift) + 1;
   if (p0 >= n || n <= a.n_selected) return;   // few pages: all are taken
   const S s(a, sh, row, head, b);
-  s.score(s.look_up(p0, n), n, a.scores + (static_cast<long long>(row) * a.Hkv + head) * a.s.max_pages);
+  float* out = a.scores + (static_cast<long long>(row) * a.Hkv + head) * a.s.max_pages;
+  s.score(s.look_up(p0, n), n, [&](int page, float x) { out[page] = x; });
 }
 
 // Grid (T, Hkv): choice from the workspace.
@@ -319,9 +354,24 @@ __global__ void __launch_bounds__(kSelThreads, 4) choose_kernel(const __grid_con
 template <int D>
 cudaError_t launch_t(const CacheSelectArgs& a, cudaStream_t stream) {
   const dim3 pairs(a.s.T, a.Hkv);
-  if (cache_select_at_once(a.s.T, a.Hkv, a.s.max_pages)) {
-    select_kernel<D><<<pairs, kOnceThreads, a.s.max_pages * sizeof(float), stream>>>(a);
-    return cudaGetLastError();
+  if (cache_select_at_once(a.s.max_pages)) {
+    // as many CTAs per pair as have pages and fit the GPU beside the others
+    constexpr int kPages = Scorer<D, kOnceThreads>::kPages;
+    const long long n_pairs = static_cast<long long>(a.s.T) * a.Hkv;
+    unsigned ctas = 1;
+    while (ctas < 8 && 2 * ctas * n_pairs <= 2 * kSms && static_cast<int>(ctas) * kPages < a.s.max_pages) ctas *= 2;
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = attr.val.clusterDim.y = 1;
+    attr.val.clusterDim.z = ctas;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(pairs.x, pairs.y, ctas);
+    cfg.blockDim = kOnceThreads;
+    cfg.dynamicSmemBytes = a.s.max_pages * sizeof(float);
+    cfg.stream = stream;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, select_kernel<D>, a);
   }
   constexpr int kPages = Scorer<D, kSelThreads>::kPages;
   score_kernel<D><<<dim3(a.s.T, a.Hkv, (a.s.max_pages + kPages - 1) / kPages), kSelThreads, 0, stream>>>(a);
@@ -332,14 +382,12 @@ cudaError_t launch_t(const CacheSelectArgs& a, cudaStream_t stream) {
 
 }  // namespace
 
-// One kernel up to 2048 pages, or where there is a pair for every SM.  Measured
-// with the attention over 16 selected pages of 64, 8 kv heads (one kernel / two):
-// 1 row, 512 pages 21.2 / 21.3 us, 2048 pages 28.0 / 26.0 (and one launch and one
-// allocation less for the host, 6 us), 8192 pages 64 / 46; 16 rows, 2048 pages 43 / 49.
-bool cache_select_at_once(int T, int Hkv, int max_pages) {
-  if (max_pages > kOncePages) return false;
-  return max_pages <= 2048 || static_cast<long long>(T) * Hkv >= kSms;
-}
+// One kernel as long as a pair's scores fit one CTA's shared memory.  Measured
+// with the attention over 16 selected pages of 64, 8 kv heads, d = 128 (one kernel
+// in clusters / without clusters / two kernels, us): 1 row, 2048 pages 21.8 / 28 /
+// 27.4; 1 row, 8000 pages 35 / 64 / 45; 4 rows, 4000 pages 34 / - / 42; 16 rows, 2000
+// pages 43 in each way.
+bool cache_select_at_once(int max_pages) { return max_pages <= kOncePages; }
 
 cudaError_t launch_cache_select(int d, const CacheSelectArgs& a, cudaStream_t stream) {
   return d == 64 ? launch_t<64>(a, stream) : launch_t<128>(a, stream);

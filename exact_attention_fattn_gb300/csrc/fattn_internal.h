@@ -149,7 +149,7 @@ struct CacheSelectArgs {
 
 // Whether a selection is one kernel that keeps its scores in shared memory
 // (no workspace), or two with the scores between them.
-bool cache_select_at_once(int T, int Hkv, int max_pages);
+bool cache_select_at_once(int max_pages);
 cudaError_t launch_cache_select(int d, const CacheSelectArgs& a, cudaStream_t stream);
 
 struct CacheAttnArgs {

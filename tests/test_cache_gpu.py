@@ -570,9 +570,10 @@ def test_attend_drawn_batches(seed):
 
 
 @pytest.mark.parametrize("lens,news,hkv,k", [
-    ([2300 * 32], [2], 1, 20),                      # scores in the workspace: few rows
-    ([2300 * 32 - 5, 70], [80, 2], 2, 20),          # on chip: a pair for every SM
-    ([10400 * 32 - 31], [80], 2, 40)])              # in the workspace: more pages than fit
+    ([2300 * 32], [2], 1, 20),                      # eight CTAs a pair
+    ([2300 * 32 - 5, 70], [70, 2], 1, 20),          # four, and pairs with fewer pages than the CTAs start at
+    ([2300 * 32 - 5, 70], [80, 2], 2, 20),          # one
+    ([10400 * 32 - 31], [80], 2, 40)])              # scores in the workspace: more pages than fit
 def test_select_many_pages(lens, news, hkv, k):
     b = Batch(144, lens, news, hkv, 2, 64, 32)
     assert np.array_equal(run_select(b, k, 1, 2), C.select(b.q, b.cache, b.table, b.q_start, b.kv_len, k, 1, 2))
