@@ -19,9 +19,10 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB_PATH = os.path.join(PKG, "libfattn.so")
 BUILD_DIR = os.path.join(PKG, "_build")
-# Debug variant for tests: every kernel range-checks its computed shared-
+# Debug variant for tests: every dense kernel range-checks its computed shared-
 # memory, TMEM and global indices (a failed check is reported as
-# FATTN_ERR_DEBUG_CHECK, not a trap), and the forward's K/V ring has its
+# FATTN_ERR_DEBUG_CHECK, not a trap; the paged cache's kernels check what they
+# read from the device in every build), and the forward's K/V ring has its
 # minimum depth of two stages, so that the ring phases wrap as often as
 # they can.
 DEBUG_LIB_PATH = os.path.join(PKG, "libfattn_debug.so")

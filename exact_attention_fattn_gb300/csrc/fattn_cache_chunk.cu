@@ -14,7 +14,7 @@
 //     product would, and K needs no conversion.  A kernel in front splits Q
 //     once and lays its rows out as the products read them.
 //   O += P V    in fp16 (kind::f16): probabilities to fp16 in tensor memory
-//     (one rounding, 2^-11), V's codes to fp16, exactly, by two converter
+//     (one rounding, 2^-11), V's codes to fp16, exactly, by four converter
 //     warps between the TMA ring and the MMA's tiles.  An e4m3 P would lose
 //     2^-4 of every probability; splitting P as Q is would cost the softmax
 //     warps three conversions per pair, and they set the pace already.
@@ -27,6 +27,13 @@
 // The reference moves only when a row's maximum passes it by more than 8, and P'
 // is 2^7 times what it says, 2^15 at most: fp16 then holds probabilities down to
 // 2^-31 of the largest.
+//
+// Bound: the chain of a row tile, its S (512 cycles of MMA), the softmax (about
+// 1600), its P V (512) and the hand-overs, which the other tile's chain does not
+// quite fill: 3370 cycles a step of both, 2048 of them MMA (2 x 2048 rows of 32
+// heads on 16384 keys: 688 us, 1390 TFLOP/s, 0.71 of the measured bf16 rate,
+// tensor pipe 60 % busy).  Handing P over in two parts, so that P V starts on the
+// first, was slower (719 us).
 //
 // Work split: the key tiles of all units, in order, are dealt to the CTAs in
 // equal contiguous shares, whatever the sequences' lengths and however many
