@@ -579,6 +579,41 @@ def test_select_many_pages(lens, news, hkv, k):
     assert np.array_equal(run_select(b, k, 1, 2), C.select(b.q, b.cache, b.table, b.q_start, b.kv_len, k, 1, 2))
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("news", [[1, 1], [3, 0], [2, 70]])
+def test_largest_group(d, news):
+    """128 query heads share a kv head: one token's rows are eight small units or
+    half a large one."""
+    b = Batch(181, [300, 129], news, 1, 128, d, 64, pad_rows=1)
+    check(b)
+    sel = np.full((b.T, 1, 3), -1, np.int32)
+    sel[:, 0, 0], sel[:, 0, 2] = 1, 0
+    check(b, selected=sel)
+
+
+@pytest.mark.parametrize("news", [[1, 1], [30, 2]])
+def test_most_kv_heads(news):
+    b = Batch(182, [70, 33], news, 1024, 1, 64, 32)
+    check(b)
+    check_append(Batch(183, [70, 33], news, 1024, 1, 64, 32, filled=False))
+    assert np.array_equal(run_select(b, 2, 0, 1), C.select(b.q, b.cache, b.table, b.q_start, b.kv_len, 2, 0, 1))
+
+
+@pytest.mark.parametrize("causal", [True, False])
+def test_one_token_cached(causal):
+    for d, page in ((64, 32), (128, 128)):
+        check(Batch(184, [1], [1], 1, 1, d, page), causal)
+        check(Batch(185, [1, 2, 1], [0, 2, 1], 2, 40, d, page), causal)
+
+
+def test_strided_queries_and_pages_for_many_rows():
+    """Rows cut out of one projection, pages apart, 300 rows a sequence."""
+    b = Batch(186, [700, 310], [300, 310], 2, 2, 128, 64, pad_rows=3)
+    wide = torch.full((b.T, b.hq * b.d + 64), 9.0, dtype=torch.bfloat16, device="cuda")
+    wide[:, :b.hq * b.d] = b.rows(b.q).flatten(1)
+    check(b, page_gap=48, q=wide[:, :b.hq * b.d].unflatten(1, (b.hq, b.d)))
+
+
 # ------------------------------------------------------------------ memory the caller owns
 
 def test_queries_rotated_in_place():
