@@ -26,6 +26,7 @@ namespace {
 
 constexpr int kSelThreads = 256;
 constexpr int kOnceThreads = 512;
+constexpr int kFewThreads = 128;
 constexpr int kInFlight = 8;         // pages in flight per lane group
 constexpr int kOncePages = 10000;    // scores that fit the 48 KB every kernel may use
 
@@ -205,7 +206,7 @@ __device__ __forceinline__ void choose(const CacheSelectArgs& a, ChooseShared& s
   uint32_t prefix = 0u;
   int left = k;
   for (int shift = 24; shift >= 0; shift -= 8) {
-    if (tid < 256) sh.hist[tid] = 0;
+    for (int i = tid; i < 256; i += NT) sh.hist[i] = 0;
     __syncthreads();
     const uint32_t above = shift == 24 ? 0u : (0xffffffffu << (shift + 8));
     for (int i = tid; i < n; i += NT) {
@@ -282,9 +283,9 @@ __device__ __forceinline__ bool take_all(const CacheSelectArgs& a, int n, int* o
 
 // Grid (T, Hkv, C) in clusters of C along z: the cluster's CTAs score 1 / C of a
 // pair's pages each, into the first one's shared memory, and that one chooses.
-template <int D>
-__global__ void __launch_bounds__(kOnceThreads, 2) select_kernel(const __grid_constant__ CacheSelectArgs a) {
-  using S = Scorer<D, kOnceThreads>;
+template <int D, int NT>
+__global__ void __launch_bounds__(NT, 1024 / NT) select_kernel(const __grid_constant__ CacheSelectArgs a) {
+  using S = Scorer<D, NT>;
   __shared__ union {
     typename S::Shared score;
     ChooseShared choose;
@@ -318,7 +319,7 @@ __global__ void __launch_bounds__(kOnceThreads, 2) select_kernel(const __grid_co
     if (rank != 0) return;
   }
   __syncthreads();
-  choose<kOnceThreads>(a, sh.choose, scores, n, out);
+  choose<NT>(a, sh.choose, scores, n, out);
 }
 
 // Grid (T, Hkv, chunks of pages): scores to the workspace.
@@ -351,27 +352,39 @@ __global__ void __launch_bounds__(kSelThreads, 4) choose_kernel(const __grid_con
   choose<kSelThreads>(a, sh, a.scores + at * a.s.max_pages, n, out);
 }
 
+template <int D, int NT>
+cudaError_t launch_once(const CacheSelectArgs& a, unsigned ctas, cudaStream_t stream) {
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = attr.val.clusterDim.y = 1;
+  attr.val.clusterDim.z = ctas;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(a.s.T, a.Hkv, ctas);
+  cfg.blockDim = NT;
+  cfg.dynamicSmemBytes = a.s.max_pages * sizeof(float);
+  cfg.stream = stream;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, select_kernel<D, NT>, a);
+}
+
 template <int D>
 cudaError_t launch_t(const CacheSelectArgs& a, cudaStream_t stream) {
   const dim3 pairs(a.s.T, a.Hkv);
   if (cache_select_at_once(a.s.max_pages)) {
-    // as many CTAs per pair as have pages and fit the GPU beside the others
-    constexpr int kPages = Scorer<D, kOnceThreads>::kPages;
+    // Many pairs, or few pages: CTAs of 128 threads, eight to an SM, as a pair's
+    // time is mostly latency.  Measured with the attention over 5 pages (d = 128,
+    // 128 / 512 threads, us): 384 pairs, 100 pages 24.8 / 33.2, 400 pages 33.6 /
+    // 36.8; 1536 pairs, 24 pages 51 / 87, 400 pages 81 / 93; 160 pairs, 100 pages
+    // 20.5 / 21.9, but 400 pages 26.7 / 23.5.
     const long long n_pairs = static_cast<long long>(a.s.T) * a.Hkv;
+    if (n_pairs > 2 * kSms || a.s.max_pages <= 2 * Scorer<D, kFewThreads>::kPages)
+      return launch_once<D, kFewThreads>(a, 1, stream);
+    // Otherwise as many CTAs per pair as have pages and fit the GPU beside the others.
+    constexpr int kPages = Scorer<D, kOnceThreads>::kPages;
     unsigned ctas = 1;
-    while (ctas < 8 && 2 * ctas * n_pairs <= 2 * kSms && static_cast<int>(ctas) * kPages < a.s.max_pages) ctas *= 2;
-    cudaLaunchAttribute attr{};
-    attr.id = cudaLaunchAttributeClusterDimension;
-    attr.val.clusterDim.x = attr.val.clusterDim.y = 1;
-    attr.val.clusterDim.z = ctas;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(pairs.x, pairs.y, ctas);
-    cfg.blockDim = kOnceThreads;
-    cfg.dynamicSmemBytes = a.s.max_pages * sizeof(float);
-    cfg.stream = stream;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, select_kernel<D>, a);
+    while (ctas < 8 && ctas * n_pairs <= kSms && static_cast<int>(ctas) * kPages < a.s.max_pages) ctas *= 2;
+    return launch_once<D, kOnceThreads>(a, ctas, stream);
   }
   constexpr int kPages = Scorer<D, kSelThreads>::kPages;
   score_kernel<D><<<dim3(a.s.T, a.Hkv, (a.s.max_pages + kPages - 1) / kPages), kSelThreads, 0, stream>>>(a);

@@ -573,6 +573,7 @@ def test_attend_drawn_batches(seed):
     ([2300 * 32], [2], 1, 20),                      # eight CTAs a pair
     ([2300 * 32 - 5, 70], [70, 2], 1, 20),          # four, and pairs with fewer pages than the CTAs start at
     ([2300 * 32 - 5, 70], [80, 2], 2, 20),          # one
+    ([500 * 32 - 3, 9000], [30, 150], 2, 20),       # small CTAs, pages in several turns
     ([10400 * 32 - 31], [80], 2, 40)])              # scores in the workspace: more pages than fit
 def test_select_many_pages(lens, news, hkv, k):
     b = Batch(144, lens, news, hkv, 2, 64, 32)
