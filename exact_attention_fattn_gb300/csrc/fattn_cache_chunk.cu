@@ -31,17 +31,18 @@
 // Bound: the chain of a row tile, its S (512 cycles of MMA), the softmax (about
 // 1600), its P V (512) and the hand-overs, which the other tile's chain does not
 // quite fill: 3370 cycles a step of both, 2048 of them MMA (2 x 2048 rows of 32
-// heads on 16384 keys: 688 us, 1390 TFLOP/s, 0.71 of the measured bf16 rate,
+// heads on 16384 keys: 677 us, 1420 TFLOP/s, 0.73 of the measured bf16 rate,
 // tensor pipe 60 % busy).  Handing P over in two parts, so that P V starts on the
-// first, was slower (719 us).
+// first, was slower (719 against 688 us).  Short prompts are bound by the units'
+// ends: the softmax warps' set-up, masked tiles and stores.
 //
 // Work split: the key tiles of all units, in order, are dealt to the CTAs in
 // equal contiguous shares, whatever the sequences' lengths and however many
 // tiles causality cuts off; units that CTAs share are joined from partial
-// results in a second kernel, in order.  A unit counts five tiles more than it
+// results in a second kernel, in order.  A unit counts three tiles more than it
 // has, about what its beginning and its end cost (5 rows of 8 heads on 32
-// sequences: 80 us without them, 76 with three, 72.6 with five, 73.4 with eight;
-// 2 x 2048 rows on 16384 keys: 694, 689, 688, 691).
+// sequences: 80 us without them, 68.4 with three, 69.3 with five; 19 prompts of up
+// to 895 tokens: 297 with three, 304 with five).
 //
 // Warps: 0-3 softmax of row tile 0, 4-7 of row tile 1, 8 tensor memory and MMA
 // issue, 9 loads, 10 the walk over the CTA's share (it publishes one segment
@@ -288,6 +289,15 @@ struct Walker {
   }
 };
 
+__device__ __forceinline__ void st_global_v8(void* p, const uint32_t (&w)[8]) {   // 32-byte aligned
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]),
+               "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+               : "memory");
+}
+__device__ __forceinline__ void prefetch_l1(const void* p) {
+  asm volatile("prefetch.global.L1 [%0];" ::"l"(p));
+}
+
 // Page `first` + lane of a sequence, as the table has it; -1 past its end.
 __device__ __forceinline__ int page_of_lane(const CacheAttnArgs& a, int b, int len, int first) {
   const int p = first + static_cast<int>(threadIdx.x & 31);
@@ -508,6 +518,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int g = 0; g < 4; ++g) {
             const int lh = lim_of(g);
+            if (!__any_sync(0xffffffffu, lh < 32)) continue;   // most of a diagonal tile
             mg[g] = -INFINITY;
 #pragma unroll
             for (int i = 0; i < 32; ++i) {
@@ -626,7 +637,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (s.active(1)) ++o1_count;
       // O, 32 columns at a time; compact on purpose (this code is out of the
-      // instruction caches whenever it runs).
+      // instruction caches whenever it runs).  A lane has a row, so each store
+      // writes 32 lines and their number is what the loop costs: 32 bytes a lane
+      // instead of 16 took short prompts (19 of up to 895 tokens, 56 heads) from 311
+      // to 304 us; exchanging chunks between lanes for whole lines cost more than it
+      // gave (328).
+      const bool o_wide = (reinterpret_cast<uintptr_t>(args.o) & 31) == 0;
       const float inv = l == 0.f ? 0.f : 1.f / l;
       const int token = rr / args.group;
       const long long out_row =
@@ -648,20 +664,27 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!on) continue;
         if (whole) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            uint32_t w[4];
+          for (int i = 0; i < 2; ++i) {
+            uint32_t w[8];
 #pragma unroll
-            for (int z = 0; z < 4; ++z)
-              w[z] = pack_bf16x2(__uint_as_float(o[8 * i + 2 * z]) * inv,
-                                 __uint_as_float(o[8 * i + 2 * z + 1]) * inv);
-            *reinterpret_cast<uint4*>(args.o + out_row * D + 32 * ch + 8 * i) =
-                make_uint4(w[0], w[1], w[2], w[3]);
+            for (int z = 0; z < 8; ++z)
+              w[z] = pack_bf16x2(__uint_as_float(o[16 * i + 2 * z]) * inv,
+                                 __uint_as_float(o[16 * i + 2 * z + 1]) * inv);
+            uint16_t* dst = args.o + out_row * D + 32 * ch + 16 * i;
+            if (o_wide) {
+              st_global_v8(dst, w);
+            } else {
+              reinterpret_cast<uint4*>(dst)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+              reinterpret_cast<uint4*>(dst)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+            }
           }
         } else {
 #pragma unroll
-          for (int i = 0; i < 8; ++i)
-            part[8 * ch + i] = make_float4(__uint_as_float(o[4 * i]), __uint_as_float(o[4 * i + 1]),
-                                           __uint_as_float(o[4 * i + 2]), __uint_as_float(o[4 * i + 3]));
+          for (int i = 0; i < 4; ++i) {
+            const uint32_t w[8] = {o[8 * i],     o[8 * i + 1], o[8 * i + 2], o[8 * i + 3],
+                                   o[8 * i + 4], o[8 * i + 5], o[8 * i + 6], o[8 * i + 7]};
+            st_global_v8(part + 8 * ch + 2 * i, w);
+          }
         }
       }
       tc_fence_before();
@@ -938,6 +961,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         __syncwarp();
         if (!more) break;
+        // The segment's first scales, which the softmax warps will ask for, to L1.
+        const int pid = page_of_lane(args, x.b, x.len, x.a << (7 - args.page_shift));
+        if (pid >= 0 && pid < args.pages) {
+          const long long sc = static_cast<long long>(pid) * args.Hkv + x.head;
+          prefetch_l1(args.k_scale + sc);
+          prefetch_l1(args.v_scale + sc);
+        }
       }
       if (lane == 0) {
         // What is to be joined: the unit that this CTA starts and others go

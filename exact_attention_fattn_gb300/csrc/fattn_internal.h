@@ -182,7 +182,7 @@ constexpr int kDecodeUnitCost = 2;   // pieces that a unit counts beyond its chu
 constexpr int decode_ctas(int d) { return d == 64 ? 3 : 2; }
 constexpr int kChunkRows = 256;
 constexpr int kChunkTileKeys = 128;
-constexpr int kChunkUnitCost = 5;
+constexpr int kChunkUnitCost = 3;
 constexpr int kChunkCtas = 1;
 
 // Few rows per sequence (tiles of 16, mma.sync); tk, tv: 3-D uint8 views

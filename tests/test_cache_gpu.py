@@ -615,6 +615,22 @@ def test_strided_queries_and_pages_for_many_rows():
     check(b, page_gap=48, q=wide[:, :b.hq * b.d].unflatten(1, (b.hq, b.d)))
 
 
+@pytest.mark.parametrize("news", [[1, 2], [40, 300]])
+@pytest.mark.parametrize("d", [64, 128])
+def test_outputs_on_a_16_byte_boundary(news, d):
+    b = Batch(187, [700, 310], news, 2, 2, d, 64)
+    c, *where = b.device()
+    q = b.rows(b.q)
+    buf = torch.full((q.numel() + 16,), 7.0, dtype=torch.bfloat16, device="cuda")
+    out = buf[8:8 + q.numel()].view(q.shape)
+    assert out.data_ptr() % 32 == 16
+    o, lse = K.fattn_cache_fwd(q, c, *where)
+    o2, lse2 = K.fattn_cache_fwd(q, c, *where, out=out)
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
+    assert bool((buf[:8] == 7.0).all()) and bool((buf[8 + q.numel():] == 7.0).all())
+    status_ok()
+
+
 # ------------------------------------------------------------------ memory the caller owns
 
 def test_queries_rotated_in_place():
