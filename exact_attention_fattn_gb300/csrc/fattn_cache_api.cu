@@ -101,11 +101,11 @@ AttnWorkspace attn_workspace(int rows, int d, size_t q_rows) {
 // an average sequence decide: up to 16 are one unit; with 2 to 4 units a
 // sequence the first kernel reads every key that often (out of L2 after the first
 // time) but starts and ends sooner, so it takes small calls.  Measured, 8 kv
-// heads, mma.sync / tcgen05 us: d = 128: 16 rows, 32 x 1000 tokens 29 / 47, 16 x
-// 16000 93 / 133; 24 rows, 32 x 2000 57 / 63, 32 x 4000 94 / 90; 40 rows, 32 x 500
-// 37 / 36, 32 x up to 4000 93 / 72; 64 rows, 8 x 1000 26.7 / 27.1, 32 x 500 46 / 37.
-// d = 64: 24 rows, 16 x 16000 103 / 125; 40 rows, 32 x 1000 36 / 43, 32 x 4000 86 /
-// 83; 64 rows, 4 x 8000 37 / 34.
+// heads, mma.sync / tcgen05 us: d = 128: 16 rows, 32 x 1000 tokens 29 / 45, 16 x
+// 16000 93 / 128; 24 rows, 32 x 2000 57 / 59, 32 x 4000 94 / 84; 40 rows, 32 x 500
+// 37 / 35, 32 x up to 4000 93 / 67; 64 rows, 8 x 1000 26.7 / 26.2, 1 x 8000 23.5 / 32,
+// 32 x 500 46 / 36.  d = 64: 24 rows, 16 x 16000 103 / 123; 40 rows, 32 x 1000 36 /
+// 42, 32 x 4000 86 / 80; 64 rows, 4 x 8000 37 / 33.
 // tokens: at most as many times a kv head the call can reach, -1 for unknown.
 bool few_rows(int T, int B, int group, int d, int n_selected, long long tokens) {
   const long long units = (static_cast<long long>(T) * group + kDecodeRows * static_cast<long long>(B) - 1) /
