@@ -57,7 +57,7 @@ def fattn_rope_table(positions: int, rope_dim: int, theta: float = 10000.0,
 # mostly the host's: each attribute of a tensor is read once, devices are
 # compared by index, and the scale, the stream and the current device come
 # without a tensor or a context manager.  On GB300's host a call of
-# fattn_cache_fwd took 44.7 us before and 21 us so, 8 of them in the library.
+# fattn_cache_fwd took 44.7 us before and 21 us so, 6 of them for the library.
 
 _SCALES = {d: default_scale(d) for d in (64, 128)}
 

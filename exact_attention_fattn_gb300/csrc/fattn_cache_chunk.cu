@@ -31,7 +31,7 @@
 // Bound: the chain of a row tile, its S (512 cycles of MMA), the softmax (about
 // 1600), its P V (512) and the hand-overs, which the other tile's chain does not
 // quite fill: 3370 cycles a step of both, 2048 of them MMA (2 x 2048 rows of 32
-// heads on 16384 keys: 677 us, 1420 TFLOP/s, 0.73 of the measured bf16 rate,
+// heads on 16384 keys: 671 us, 1430 TFLOP/s, 0.73 of the measured bf16 rate,
 // tensor pipe 60 % busy).  Handing P over in two parts, so that P V starts on the
 // first, was slower (719 against 688 us).  Short prompts are bound by the units'
 // ends: the softmax warps' set-up, masked tiles and stores.
@@ -1067,17 +1067,21 @@ __global__ void __launch_bounds__(kThreads, 1)
 // e4m3(x - hi).  Rows go to where the products read them: those of a sequence and
 // kv head in one run, (token, query head) order, 16-byte chunks swizzled as in
 // shared memory, so that a tile is one plain copy.  Bound: 2 d bytes in and out
-// a row.
+// a row.  A thread takes 16 columns of kSplitRows rows of one token, so that the
+// search for its sequence is shared and the loads go out together: 19 prompts with
+// 160 MB of queries took 298 us with one row a thread (55 of them here), 288 with
+// two, 285 with four, 290 with eight.
+constexpr int kSplitRows = 4;
+
 template <int D>
 __global__ void __launch_bounds__(256) split_kernel(const __grid_constant__ CacheAttnArgs a) {
   allow_child();
   constexpr int kLanes = D / 16;          // 16 columns each
-  const int Hq = a.Hkv * a.group;
-  const long long id = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x;
-  const long long row = id / kLanes;
-  const int c = static_cast<int>(id % kLanes);
-  if (row >= static_cast<long long>(a.s.T) * Hq) return;   // whole groups of lanes
-  const int token = static_cast<int>(row / Hq), hq = static_cast<int>(row % Hq);
+  const int Hq = a.Hkv * a.group, groups = (Hq + kSplitRows - 1) / kSplitRows;
+  const int item = static_cast<int>((static_cast<long long>(blockIdx.x) * 256 + threadIdx.x) / kLanes);
+  const int c = threadIdx.x % kLanes;
+  const int token = item / groups, h0 = (item - token * groups) * kSplitRows;
+  if (token >= a.s.T) return;              // whole groups of lanes
   // the token's sequence: a guess for sequences of equal rows, else a search
   int b = static_cast<int>(static_cast<long long>(token) * a.s.B / a.s.T);
   if (token < __ldg(a.s.q_start + b) || token >= __ldg(a.s.q_start + b + 1)) {
@@ -1088,34 +1092,39 @@ __global__ void __launch_bounds__(256) split_kernel(const __grid_constant__ Cach
     }
   }
   const SeqInfo q = seq_info(a.s, b, a.page_shift);
-  const bool on = token >= q.r0 && token < q.r0 + q.n;
-  uint4 w[2] = {make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u)};
-  if (on) {
-    const uint4* p = reinterpret_cast<const uint4*>(a.q + token * a.q_row + hq * D + 16 * c);
-    w[0] = __ldg(p);
-    w[1] = __ldg(p + 1);
-  }
-  const uint32_t u[8] = {w[0].x, w[0].y, w[0].z, w[0].w, w[1].x, w[1].y, w[1].z, w[1].w};
-  uint32_t mx = 0u;                        // the largest magnitude's bits
+  if (token < q.r0 || token >= q.r0 + q.n) return;   // behind the last sequence
+  uint4 w[kSplitRows][2];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) mx = max(mx, max(u[i] & 0x7fffu, (u[i] >> 16) & 0x7fffu));
+  for (int k = 0; k < kSplitRows; ++k) {
+    const uint4* p = reinterpret_cast<const uint4*>(a.q + token * a.q_row + min(h0 + k, Hq - 1) * D + 16 * c);
+    w[k][0] = __ldg(p);
+    w[k][1] = __ldg(p + 1);
+  }
   // a row's lanes are neighbours, and all of them are here
   const unsigned int lanes = ((1u << kLanes) - 1u) << (threadIdx.x & 31 & ~(kLanes - 1));
 #pragma unroll
-  for (int off = kLanes / 2; off > 0; off >>= 1) mx = max(mx, __shfl_xor_sync(lanes, mx, off));
-  if (!on) return;                         // behind the last sequence
-  const float factor = query_factor(mx);
-  uint32_t hi[4], lo[4];
+  for (int k = 0; k < kSplitRows; ++k) {
+    if (h0 + k >= Hq) break;
+    const uint32_t u[8] = {w[k][0].x, w[k][0].y, w[k][0].z, w[k][0].w,
+                           w[k][1].x, w[k][1].y, w[k][1].z, w[k][1].w};
+    uint32_t mx = 0u;                        // the largest magnitude's bits
 #pragma unroll
-  for (int z = 0; z < 4; ++z) split_query4(u[2 * z], u[2 * z + 1], factor, hi[z], lo[z]);
-  const int head = hq / a.group;
-  const int rr = (token - q.r0) * a.group + (hq - head * a.group);
-  const long long out = (static_cast<long long>(q.r0) * a.Hkv + static_cast<long long>(head) * q.n) * a.group + rr;
-  // swizzle of the row's place in its tile (tiles start at multiples of 128 rows)
-  uint8_t* dst = a.q_codes + out * D - static_cast<long long>(rr & 7) * D + code_off<D>(rr & 7, c);
-  *reinterpret_cast<uint4*>(dst) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-  *reinterpret_cast<uint4*>(dst + a.q_lo) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-  if (c == 0) a.q_scale[out] = query_scale(mx);
+    for (int i = 0; i < 8; ++i) mx = max(mx, max(u[i] & 0x7fffu, (u[i] >> 16) & 0x7fffu));
+#pragma unroll
+    for (int off = kLanes / 2; off > 0; off >>= 1) mx = max(mx, __shfl_xor_sync(lanes, mx, off));
+    const float factor = query_factor(mx);
+    uint32_t hi[4], lo[4];
+#pragma unroll
+    for (int z = 0; z < 4; ++z) split_query4(u[2 * z], u[2 * z + 1], factor, hi[z], lo[z]);
+    const int hq = h0 + k, head = hq / a.group;
+    const int rr = (token - q.r0) * a.group + (hq - head * a.group);
+    const long long out = (static_cast<long long>(q.r0) * a.Hkv + static_cast<long long>(head) * q.n) * a.group + rr;
+    // swizzle of the row's place in its tile (tiles start at multiples of 128 rows)
+    uint8_t* dst = a.q_codes + out * D - static_cast<long long>(rr & 7) * D + code_off<D>(rr & 7, c);
+    *reinterpret_cast<uint4*>(dst) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+    *reinterpret_cast<uint4*>(dst + a.q_lo) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+    if (c == 0) a.q_scale[out] = query_scale(mx);
+  }
 }
 
 template <int D>
@@ -1134,7 +1143,8 @@ cudaError_t launch_t(const CUtensorMap& tk, const CUtensorMap& tv, const CacheAt
     regs.store(fa.numRegs, std::memory_order_relaxed);
   }
   if (regs.load(std::memory_order_relaxed) != kLaunchRegs) return cudaErrorInvalidConfiguration;
-  const long long lanes = static_cast<long long>(a.s.T) * a.Hkv * a.group * (D / 16);
+  const long long lanes =
+      static_cast<long long>(a.s.T) * ((a.Hkv * a.group + kSplitRows - 1) / kSplitRows) * (D / 16);
   split_kernel<D><<<static_cast<unsigned>((lanes + 255) / 256), 256, 0, stream>>>(a);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   if ((e = launch_child(kern, a.grid, kThreads, smem, stream, tk, tv, a)) != cudaSuccess) return e;

@@ -3,11 +3,12 @@
 // workspace (unnormalised rows of O in fp32, reference maximum and sum), in
 // the order of their keys.
 //
-// Bound: latency where a unit has many parts (one long sequence: up to 152 of
+// Bound: latency where a unit has many parts (one long sequence: up to 304 of
 // them), bytes where units are large (256 rows, two or three parts each).  A
-// thread has 4 columns of a row; the rows of a block are 4 for the small
-// units, whose parts are walked by four groups side by side, and 8 for the
-// large ones, walked by one.
+// thread has 4 columns of a row; the small units' parts are walked by four groups
+// of threads side by side, the large ones' by one, two rows a thread whose loads
+// go out together (32 sequences of 40 rows, whole call: 67.1 us with one row, 66.5
+// with two, 68.1 with four).
 #include "fattn_cache.cuh"
 
 namespace fattn {
@@ -32,13 +33,15 @@ __device__ __forceinline__ void merge(Part& a, const Part& b) {
   a.o.w = fmaf(a.o.w, x, b.o.w * y);
 }
 
-// Block (c, y): rows [y R, y R + R) of the unit that CTA c starts and others go
+// Block (c, y): rows [y kBlock, ..) of the unit that CTA c starts and others go
 // on with.
 template <int D, int ROWS>
 struct JoinCfg {
   static constexpr int kF4 = D / 4;                            // threads per row
   static constexpr int kGroups = ROWS == kDecodeRows ? 4 : 1;
-  static constexpr int kRows = ROWS == kDecodeRows ? 4 : 8;    // rows per block
+  static constexpr int kRows = ROWS == kDecodeRows ? 4 : 8;    // rows at a time
+  static constexpr int kPer = ROWS == kDecodeRows ? 1 : 2;     // rows per thread
+  static constexpr int kBlock = kRows * kPer;
   static constexpr int kThreads = kF4 * kGroups * kRows;
 };
 
@@ -50,42 +53,55 @@ __global__ void __launch_bounds__(JoinCfg<D, ROWS>::kThreads) join_kernel(const 
   wait_for_parent();
   const int4 rec = a.rec[2 * cta];
   const int rows = rec.y * a.group - rec.z * ROWS;   // of the unit, from its first
-  if (rec.y == 0 || static_cast<int>(blockIdx.y) * J::kRows >= rows) return;
+  if (rec.y == 0 || static_cast<int>(blockIdx.y) * J::kBlock >= rows) return;
   const int4 more = a.rec[2 * cta + 1];
   const long long W = (static_cast<long long>(more.z) << 32) | static_cast<unsigned int>(more.y);
   const int q4 = threadIdx.x % J::kF4, local = threadIdx.x / J::kF4 % J::kRows;
   const int group = threadIdx.x / (J::kF4 * J::kRows);
-  const int row = blockIdx.y * J::kRows + local;
-  const bool on = row < min(rows, ROWS);
-  Part p{-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
-  for (int c = cta + group; on && c <= more.x; c += J::kGroups) {
+  const int row0 = blockIdx.y * J::kBlock + local, end = min(rows, ROWS);
+  Part p[J::kPer];
+#pragma unroll
+  for (int k = 0; k < J::kPer; ++k) p[k] = Part{-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
+  for (int c = cta + group; c <= more.x; c += J::kGroups) {
     if (cta_first(W, G, c) == cta_first(W, G, c + 1)) continue;   // a CTA without work
-    const long long at = (2ll * c + (c == cta ? 1 : 0)) * ROWS + row;
-    const float2 ml = a.part_ml[at];
-    merge(p, Part{ml.x, ml.y, reinterpret_cast<const float4*>(a.part_o + at * D)[q4]});
+    const long long at = (2ll * c + (c == cta ? 1 : 0)) * ROWS;
+    Part x[J::kPer];
+#pragma unroll
+    for (int k = 0; k < J::kPer; ++k) {
+      const int row = min(row0 + k * J::kRows, end - 1);          // a row that is there, to load
+      const float2 ml = a.part_ml[at + row];
+      x[k] = Part{ml.x, ml.y, reinterpret_cast<const float4*>(a.part_o + (at + row) * D)[q4]};
+    }
+#pragma unroll
+    for (int k = 0; k < J::kPer; ++k) merge(p[k], x[k]);
   }
   if constexpr (J::kGroups > 1) {
-    side[group][local][q4] = p;
+    static_assert(J::kPer == 1, "one row a thread");
+    side[group][local][q4] = p[0];
     __syncthreads();
     if (group != 0) return;
 #pragma unroll
-    for (int g = 1; g < J::kGroups; ++g) merge(p, side[g][local][q4]);
+    for (int g = 1; g < J::kGroups; ++g) merge(p[0], side[g][local][q4]);
   }
-  if (!on) return;
-  const int rr = rec.z * ROWS + row, token = rr / a.group;
-  const long long out = (static_cast<long long>(rec.x + token) * a.Hkv + rec.w) * a.group +
-                        (rr - token * a.group);
-  const float inv = p.l == 0.f ? 0.f : 1.f / p.l;
-  *reinterpret_cast<uint2*>(a.o + out * D + 4 * q4) =
-      make_uint2(pack_bf16x2(p.o.x * inv, p.o.y * inv), pack_bf16x2(p.o.z * inv, p.o.w * inv));
-  if (q4 == 0) a.lse[out] = p.l == 0.f ? -INFINITY : (p.m + log2f(p.l)) * kLn2;
+#pragma unroll
+  for (int k = 0; k < J::kPer; ++k) {
+    const int row = row0 + k * J::kRows;
+    if (row >= end) continue;
+    const int rr = rec.z * ROWS + row, token = rr / a.group;
+    const long long out = (static_cast<long long>(rec.x + token) * a.Hkv + rec.w) * a.group +
+                          (rr - token * a.group);
+    const float inv = p[k].l == 0.f ? 0.f : 1.f / p[k].l;
+    *reinterpret_cast<uint2*>(a.o + out * D + 4 * q4) = make_uint2(
+        pack_bf16x2(p[k].o.x * inv, p[k].o.y * inv), pack_bf16x2(p[k].o.z * inv, p[k].o.w * inv));
+    if (q4 == 0) a.lse[out] = p[k].l == 0.f ? -INFINITY : (p[k].m + log2f(p[k].l)) * kLn2;
+  }
 }
 
 template <int D, int ROWS>
 cudaError_t launch_t(const CacheAttnArgs& a, cudaStream_t stream) {
   using J = JoinCfg<D, ROWS>;
   static_assert(J::kThreads <= 1024, "block size");
-  return launch_child(join_kernel<D, ROWS>, dim3(a.grid, ROWS / J::kRows), J::kThreads, 0, stream, a);
+  return launch_child(join_kernel<D, ROWS>, dim3(a.grid, ROWS / J::kBlock), J::kThreads, 0, stream, a);
 }
 
 }  // namespace
