@@ -118,22 +118,6 @@ bool few_rows(int T, int B, int group, int d, int n_selected, long long tokens) 
 
 }  // namespace
 
-cudaError_t SmemLimit::raise(const void* kernel, int bytes) {
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-  if (bytes_[dev].load(std::memory_order_relaxed) >= bytes) return cudaSuccess;
-  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-  if (e != cudaSuccess) return e;
-  // Another thread may have asked for more meanwhile: its limit has to win.
-  int had = bytes_[dev].load(std::memory_order_relaxed);
-  while (had < bytes && !bytes_[dev].compare_exchange_weak(had, bytes, std::memory_order_relaxed)) {
-  }
-  if (had > bytes) return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, had);
-  return cudaSuccess;
-}
-
 }  // namespace fattn
 
 using namespace fattn;

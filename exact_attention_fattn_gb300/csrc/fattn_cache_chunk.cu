@@ -50,6 +50,8 @@
 // in registers), 11 idle, 12-15 conversion of V.  TMEM: S_t [128 t, 128 t + 128), P aliases S, O_t at 256 + d t.
 #include <cuda_fp16.h>
 
+#include <atomic>
+
 #include "fattn_cache.cuh"
 
 namespace fattn {

@@ -6,7 +6,7 @@
 #include <stddef.h>
 #include <stdint.h>
 
-#include <atomic>
+#include "fattn_smem_limit.h"
 
 namespace fattn {
 
@@ -198,16 +198,6 @@ cudaError_t launch_cache_chunk(int d, const CUtensorMap& tk, const CUtensorMap& 
 
 // Joins the units of `rows` rows that CTAs of either kernel shared.
 cudaError_t launch_cache_join(int d, int rows, const CacheAttnArgs& a, cudaStream_t stream);
-
-// Dynamic shared memory of a kernel, asked for once per device and size (the
-// attribute call costs the host 0.3 us, which single-token calls notice).
-class SmemLimit {
- public:
-  cudaError_t raise(const void* kernel, int bytes);
-
- private:
-  std::atomic<int> bytes_[64] = {};
-};
 
 // Per-device state for entry points outside fattn_api.cu: checks the device,
 // gives the status word and the wait budget.  Returns a fattn_status.
