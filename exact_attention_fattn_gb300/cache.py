@@ -128,9 +128,16 @@ def _check_like(t, shape, dtype, dev, name):
     return t
 
 
-_current_device, _raw_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
-_raw_alloc, _raw_free = (torch._C._cuda_cudaCachingAllocator_raw_alloc,
-                         torch._C._cuda_cudaCachingAllocator_raw_delete)
+def _public_stream(dev: int) -> int:
+    return torch.cuda.current_stream(dev).cuda_stream
+
+
+# torch's own shortcuts where this torch has them (one without CUDA has none, and
+# they carry no promise), else what is public.
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _public_stream)
+_raw_alloc = getattr(torch._C, "_cuda_cudaCachingAllocator_raw_alloc", None)
+_raw_free = getattr(torch._C, "_cuda_cudaCachingAllocator_raw_delete", None)
 
 
 def _call(fn, dev, *args):
@@ -223,7 +230,7 @@ def fattn_cache_fwd(q, cache: Fp8Cache, page_table, q_start, kv_len, causal: boo
         _check_like(lse, (T, heads), torch.float32, dev, "lse")
     need = fattn_cache_fwd_workspace_bytes(T, B, heads, cs.Hkv, d, n_sel)
     scratch = 0
-    if workspace is None and need and _current_device() == dev:
+    if workspace is None and need and _raw_alloc and _raw_free and _current_device() == dev:
         # a block of the allocator that the stream's next calls may have, without a tensor around it
         scratch = ws_ptr = _raw_alloc(need, _raw_stream(dev))
     else:

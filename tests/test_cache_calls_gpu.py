@@ -47,3 +47,20 @@ def test_threads_with_batches_of_different_sizes():
         want = K.fattn_cache_fwd(qs[i], *dev[i])
         assert torch.equal(got[i][0], want[0]) and torch.equal(got[i][1], want[1])
     assert A.fattn_check_status() == 0
+
+
+@pytest.mark.parametrize("news", [1, 60])
+def test_host_path_on_public_functions_alone(news, monkeypatch):
+    b = Batch(310, [500, 90], [news, news], 2, 2, 128, 64)
+    d, q = b.device(), b.rows(b.q)
+    want = K.fattn_cache_fwd(q, *d)
+    monkeypatch.setattr(K, "_current_device", torch.cuda.current_device)
+    monkeypatch.setattr(K, "_raw_stream", K._public_stream)
+    monkeypatch.setattr(K, "_raw_alloc", None)
+    for s in (torch.cuda.current_stream(), torch.cuda.Stream()):
+        torch.cuda.synchronize()
+        with torch.cuda.stream(s):
+            got = K.fattn_cache_fwd(q, *d)
+        s.synchronize()
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    assert A.fattn_check_status() == 0
