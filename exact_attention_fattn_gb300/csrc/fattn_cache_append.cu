@@ -147,10 +147,18 @@ __device__ __forceinline__ void rescale_rows(uint8_t* base, int rows, float mul)
   }
 }
 
+// Why nothing of a sequence is appended or rotated (0: all of it is).  Its queries
+// and its keys are left out together.
+__device__ __forceinline__ unsigned int append_fault(const CacheAppendArgs& a, const SeqInfo& q) {
+  if (!q.ok) return kSiteSeqStart;
+  if (q.n > 0 && (q.len < q.n || (a.rope_dim > 0 && q.len > a.rope_len))) return kSitePosition;
+  return 0u;
+}
+
 // Queries: CH lanes take a token's columns, each for kQHeads heads, whose
 // angles are the same.  Item = token * groups of heads + group; a block of NT threads has
 // NT / CH items.
-template <int D>
+template <int D, int SHIFT>
 __device__ __forceinline__ void rotate_q(const CacheAppendArgs& a, int item) {
   constexpr int CH = D / 8;
   const int cc = threadIdx.x % CH;
@@ -168,13 +176,14 @@ __device__ __forceinline__ void rotate_q(const CacheAppendArgs& a, int item) {
         if (__ldg(a.s.q_start + mid) <= row) b = mid; else hi = mid;
       }
     }
-    const int r0 = __ldg(a.s.q_start + b), r1 = __ldg(a.s.q_start + b + 1);
-    on = row >= r0 && row < r1;          // else behind the last sequence
-    const int pos = __ldg(a.s.kv_len + b) - (r1 - r0) + (row - r0);
-    if (on && (pos < 0 || (a.rope_dim > 0 && pos >= a.rope_len))) {
-      record_bad_index(a.status, kSitePosition);
+    const SeqInfo q = seq_info(a.s, b, SHIFT);
+    on = row >= q.r0 && row < q.r0 + q.n;    // else behind the last sequence, or of a senseless one
+    const unsigned int site = append_fault(a, q);
+    if (site != 0u) {
+      record_bad_index(a.status, site);
       on = false;
     }
+    const int pos = q.len - q.n + (row - q.r0);
     if (on && a.rope_dim > 0) cs = a.rope + static_cast<long long>(pos) * a.rope_dim;
   }
   uint4 w[kQHeads];
@@ -252,17 +261,14 @@ __device__ __forceinline__ PageWork find_page(const CacheAppendArgs& a, int u) {
   auto first_unit = [&](int i) { return (__ldg(a.s.q_start + i) >> SHIFT) + 2 * i; };
   const int b = find_last_warp(a.s.B, u, first_unit);
   w.q = seq_info(a.s, b, SHIFT);
-  if (!w.q.ok) {
-    if (threadIdx.x == 0) record_bad_index(a.status, kSiteSeqStart);
+  const unsigned int site = append_fault(a, w.q);
+  if (site != 0u) {
+    if (threadIdx.x == 0) record_bad_index(a.status, site);
     return w;
   }
   const int nth = u - first_unit(b);
   if (nth < 0 || w.q.n == 0) return w;
   const int pos0 = w.q.len - w.q.n;
-  if (pos0 < 0 || (a.rope_dim > 0 && w.q.len > a.rope_len)) {
-    if (threadIdx.x == 0) record_bad_index(a.status, kSitePosition);
-    return w;
-  }
   w.p = (pos0 >> SHIFT) + nth;
   if (w.p >= (w.q.len + PAGE - 1) >> SHIFT) return w;
   w.lo = max(pos0 - (w.p << SHIFT), 0);
@@ -286,7 +292,7 @@ __global__ void __launch_bounds__(kThreads, 8) append_kernel(const __grid_consta
   const int cc = tid % CH, row = tid / CH;
   const long long kv_blocks = static_cast<long long>(units) * a.Hkv;
   if (blockIdx.x >= kv_blocks) {
-    rotate_q<D>(a, static_cast<int>(blockIdx.x - kv_blocks) * kRows + row);
+    rotate_q<D, SHIFT>(a, static_cast<int>(blockIdx.x - kv_blocks) * kRows + row);
     return;
   }
   const int u = blockIdx.x / a.Hkv, head = blockIdx.x - u * a.Hkv;

@@ -336,7 +336,8 @@ typedef struct {
  *   q, q_out     : in, bf16 rows of Hq*d, and out, bf16 [T, Hq, d]: the queries rotated likewise
  *                  (q_out may be q when its rows are contiguous); both NULL: none
  * A page that receives tokens must belong to one sequence only.  Positions
- * below 0 or from rope_len on are FATTN_ERR_BAD_INDEX.  Returns a fattn_status.
+ * below 0 or from rope_len on are FATTN_ERR_BAD_INDEX; of a sequence that has
+ * any, nothing is appended and no query written.  Returns a fattn_status.
  */
 int fattn_cache_append(const fattn_cache* cache, const void* k_new, long long k_row,
                        const void* v_new, long long v_row, const void* q, long long q_row,

@@ -8,11 +8,14 @@ import numpy as np
 import pytest
 import torch
 
-from cache_util import Batch
+import oracle
+from cache_util import Batch, to_bf16
+from exact_attention_fattn_gb300 import _lib
 from exact_attention_fattn_gb300 import attention as A
 from exact_attention_fattn_gb300 import cache as K
 
 pytestmark = pytest.mark.gpu
+C = oracle.cache
 
 
 def test_threads_with_batches_of_different_sizes():
@@ -63,4 +66,48 @@ def test_host_path_on_public_functions_alone(news, monkeypatch):
             got = K.fattn_cache_fwd(q, *d)
         s.synchronize()
         assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    assert A.fattn_check_status() == 0
+
+
+@pytest.mark.parametrize("what", ["longer than its table", "negative length", "more new than cached",
+                                  "past the rotation's table", "q_start past the rows"])
+@pytest.mark.parametrize("rope_dim", [0, 64])
+def test_append_leaves_out_the_queries_of_senseless_sequences(what, rope_dim):
+    """A sequence whose keys are not appended has its rows of q_out left alone,
+    too, and the other sequences are served."""
+    if what == "past the rotation's table" and rope_dim == 0:
+        pytest.skip("no rotation, no table")
+    b = Batch(320, [60, 90, 40], [5, 40, 3], 2, 2, 64, 32, filled=False)
+    c, table, qs, kl = b.device()
+    rope, bad = None, 1
+    if rope_dim:
+        rope = K.fattn_rope_table(70 if what == "past the rotation's table" else 400, rope_dim)
+    if what == "longer than its table":
+        kl[1] = b.max_pages * 32 + 1
+    elif what == "negative length":
+        kl[1] = -1
+    elif what == "more new than cached":
+        kl[1] = 39                    # rows of positions -1 .. 38
+    elif what == "q_start past the rows":
+        bad = 2
+        qs[3] = b.T + 1
+    before = [x.clone() for x in c]
+    q_out = torch.full((b.T, b.hq, b.d), 7.0, dtype=torch.bfloat16, device="cuda")
+    K.fattn_cache_append(b.rows(b.k_new), b.rows(b.v_new), c, table, qs, kl, rope=rope, q=b.rows(b.q), q_out=q_out)
+    assert A.fattn_check_status() == _lib.FATTN_ERR_BAD_INDEX
+    rows = slice(int(b.q_start[bad]), int(b.q_start[bad + 1]))
+    pages = table[bad, :-(-b.lens[bad] // 32)].long()
+    assert all(torch.equal(x[pages], y[pages]) for x, y in zip(c, before))
+    assert bool((q_out[rows] == 7.0).all())
+    # the others: as without that sequence
+    b.q_start = np.concatenate([[0], np.cumsum([n if i != bad else 0 for i, n in enumerate(b.news)])]).astype(np.int32)
+    keep = np.ones(b.T, bool)
+    keep[rows] = False
+    want = {k: v.copy() for k, v in b.cache.items()}
+    q = C.append(want, b.k_new[keep], b.v_new[keep], b.table, b.q_start, b.kv_len,
+                 None if rope is None else rope.cpu().numpy(), False, b.q[keep])
+    for name in ("k", "v", "k_scale", "v_scale"):
+        assert np.array_equal(getattr(c, name).cpu().numpy(), want[name]), name
+    assert np.array_equal(c.k_bounds.cpu().numpy(), want["bounds"])
+    assert np.array_equal(q_out.float().cpu().numpy()[keep], to_bf16(q))
     assert A.fattn_check_status() == 0
