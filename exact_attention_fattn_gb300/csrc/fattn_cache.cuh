@@ -120,6 +120,16 @@ __device__ __forceinline__ SeqInfo seq_info(const CacheSeqs& s, int b, int page_
   return q;
 }
 
+// Reports the sequences first, first + step, .. that make no sense.  A kernel that
+// searches for its rows' or pages' sequences would otherwise miss some: where
+// q_start goes back, a search passes over the sequence, and rows may seem to
+// belong to none.
+__device__ __forceinline__ void check_seqs(const CacheSeqs& s, int first, int step, int page_shift,
+                                           DeviceStatus* st) {
+  for (int b = first; b < s.B; b += step)
+    if (!seq_info(s, b, page_shift).ok) record_bad_index(st, kSiteSeqStart);
+}
+
 // Pieces of work of a whole call.  The host has bounded them to 32 bits for
 // sequences one behind the other; with overlapping ones the call does nothing.
 __device__ __forceinline__ int total_of(long long pieces, DeviceStatus* st) {

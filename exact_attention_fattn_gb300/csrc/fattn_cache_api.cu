@@ -150,9 +150,9 @@ int fattn_cache_append(const fattn_cache* cache, const void* k_new, long long k_
   } else if (rope_dim != 0) {
     return FATTN_ERR_INVALID_ARG;
   }
-  // one block per page and head at most, and one per 8 groups of 8 heads of q
+  // one block per page and head at most, one per 8 groups of 8 heads of q, and one that checks the batch
   const long long blocks = (T / cache->page + 2ll * B) * cache->Hkv +
-                           (q ? static_cast<long long>(T) * ((Hq + 7) / 8) / 8 + 1 : 0);
+                           (q ? static_cast<long long>(T) * ((Hq + 7) / 8) / 8 + 1 : 0) + 1;
   if (blocks > 0x7fffffffll) return FATTN_ERR_INVALID_ARG;
   CacheAppendArgs a{};
   long long budget = 0;

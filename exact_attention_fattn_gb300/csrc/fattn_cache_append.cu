@@ -291,6 +291,10 @@ __global__ void __launch_bounds__(kThreads, 8) append_kernel(const __grid_consta
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int cc = tid % CH, row = tid / CH;
   const long long kv_blocks = static_cast<long long>(units) * a.Hkv;
+  if (blockIdx.x == gridDim.x - 1) {   // a block of its own: in a unit's it cost 1.3 us of 6.9
+    check_seqs(a.s, tid, NT, SHIFT, a.status);
+    return;
+  }
   if (blockIdx.x >= kv_blocks) {
     rotate_q<D, SHIFT>(a, static_cast<int>(blockIdx.x - kv_blocks) * kRows + row);
     return;
@@ -399,7 +403,7 @@ cudaError_t launch_t(const CacheAppendArgs& a, cudaStream_t stream) {
   const long long units = (a.s.T >> SHIFT) + 2ll * a.s.B;
   const long long items = a.q != nullptr ? static_cast<long long>(a.s.T) * ((a.Hq + kQHeads - 1) / kQHeads) : 0;
   const int per = kThreads / (D / 8);
-  const long long blocks = units * a.Hkv + (items + per - 1) / per;
+  const long long blocks = units * a.Hkv + (items + per - 1) / per + 1;
   if (blocks > 0x7fffffffll) return cudaErrorInvalidValue;
   append_kernel<D, SHIFT><<<static_cast<unsigned>(blocks), kThreads, 0, stream>>>(a, static_cast<int>(units));
   return cudaGetLastError();

@@ -281,8 +281,9 @@ __device__ __forceinline__ bool take_all(const CacheSelectArgs& a, int n, int* o
   return true;
 }
 
-// Grid (T, Hkv, C) in clusters of C along z: the cluster's CTAs score 1 / C of a
+// Grid (T + 1, Hkv, C) in clusters of C along z: the cluster's CTAs score 1 / C of a
 // pair's pages each, into the first one's shared memory, and that one chooses.
+// The last row's CTAs check the batch.
 template <int D, int NT>
 __global__ void __launch_bounds__(NT, 1024 / NT) select_kernel(const __grid_constant__ CacheSelectArgs a) {
   using S = Scorer<D, NT>;
@@ -293,6 +294,10 @@ __global__ void __launch_bounds__(NT, 1024 / NT) select_kernel(const __grid_cons
   extern __shared__ float scores[];
   const int row = blockIdx.x, head = blockIdx.y, rank = blockIdx.z;
   const bool shared = gridDim.z > 1;
+  if (row == a.s.T) {                  // CTAs of their own (beside a pair's scores it cost 1.5 us of 22)
+    if (head == 0 && rank == 0) check_seqs(a.s, threadIdx.x, NT, a.page_shift, a.status);
+    return;
+  }
   if (shared) cluster_arrive();        // the first CTA has started when others write to it
   int b, pos;
   // the same for all CTAs of a cluster
@@ -341,8 +346,9 @@ __global__ void __launch_bounds__(kSelThreads, 4) score_kernel(const __grid_cons
 // Grid (T, Hkv): choice from the workspace.
 __global__ void __launch_bounds__(kSelThreads, 4) choose_kernel(const __grid_constant__ CacheSelectArgs a) {
   __shared__ ChooseShared sh;
-  wait_for_parent();
   const int row = blockIdx.x, head = blockIdx.y;
+  if (row == 0 && head == 0) check_seqs(a.s, threadIdx.x, kSelThreads, a.page_shift, a.status);
+  wait_for_parent();
   int b, pos;
   if (!row_position(a, row, b, pos)) return;
   const int n = pos < 0 ? 0 : (pos >> a.page_shift) + 1;
@@ -359,7 +365,7 @@ cudaError_t launch_once(const CacheSelectArgs& a, unsigned ctas, cudaStream_t st
   attr.val.clusterDim.x = attr.val.clusterDim.y = 1;
   attr.val.clusterDim.z = ctas;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(a.s.T, a.Hkv, ctas);
+  cfg.gridDim = dim3(static_cast<unsigned>(a.s.T) + 1u, a.Hkv, ctas);
   cfg.blockDim = NT;
   cfg.dynamicSmemBytes = a.s.max_pages * sizeof(float);
   cfg.stream = stream;

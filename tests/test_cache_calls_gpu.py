@@ -111,3 +111,42 @@ def test_append_leaves_out_the_queries_of_senseless_sequences(what, rope_dim):
     assert np.array_equal(c.k_bounds.cpu().numpy(), want["bounds"])
     assert np.array_equal(q_out.float().cpu().numpy()[keep], to_bf16(q))
     assert A.fattn_check_status() == 0
+
+
+@pytest.mark.parametrize("call", ["append", "append with queries", "attend", "attend selected", "select"])
+@pytest.mark.parametrize("starts", [[0, 100, 0, 100], [0, 60, 40, 100], "long"])
+def test_starts_that_go_back_are_reported(call, starts):
+    """A sequence whose rows end before they begin is found by no search for a
+    row or a page; rows of its neighbours may then belong to none."""
+    if starts == "long":
+        b = Batch(330, [600] * 600, [1] * 600, 1, 1, 64, 128)
+        b.q_start[500] = 0
+    else:
+        b = Batch(331, [120, 130, 140], [100, 0, 0], 1, 2, 64, 32)
+        b.q_start = np.array(starts, dtype=np.int32)
+    c, *where = b.device()
+    q = b.rows(b.q)
+    if call.startswith("append"):
+        K.fattn_cache_append(b.rows(b.k_new), b.rows(b.v_new), c, *where, q=q if "queries" in call else None)
+    elif call == "attend":
+        K.fattn_cache_fwd(q, c, *where)
+    elif call == "select":
+        K.fattn_cache_select(q, c, *where, 2)
+    else:
+        sel = torch.zeros((b.T, 1, 1), dtype=torch.int32, device="cuda")
+        K.fattn_cache_fwd(q, c, *where, selected=sel)
+    assert A.fattn_check_status() == _lib.FATTN_ERR_BAD_INDEX
+    assert A.fattn_check_status() == 0
+
+
+@pytest.mark.parametrize("B,T", [(600, 1), (4096, 3), (40, 700)])
+def test_good_starts_are_not_reported(B, T):
+    """Most sequences without rows, rows in front of the first and behind the last."""
+    news = [0] * B
+    news[B // 2] = T
+    b = Batch(332, [900 if n else 40 for n in news], news, 1, 1, 64, 128, pad_rows=2)
+    c, *where = b.device()
+    sel = K.fattn_cache_select(b.rows(b.q), c, *where, 2)
+    K.fattn_cache_fwd(b.rows(b.q), c, *where, selected=sel)
+    K.fattn_cache_append(b.rows(b.k_new), b.rows(b.v_new), c, *where)
+    assert A.fattn_check_status() == 0
