@@ -441,7 +441,8 @@ __global__ void __launch_bounds__(kThreads, decode_ctas(D))
       mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
       mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
       const int e = max(-126, min(126, static_cast<int>(mx) - 127));
-      const float down = exp2i(-e);
+      // a row with an infinity becomes NaN, as its scores say, also if all are -inf
+      const float down = mx == 0xffu ? __int_as_float(0x7fffffff) : exp2i(-e);
       cs[hh] = a.scale_log2 * exp2i(e);
 #pragma unroll
       for (int kk = 0; kk < kK; ++kk) {

@@ -348,7 +348,8 @@ int fattn_cache_append(const fattn_cache* cache, const void* k_new, long long k_
 /*
  * Attention of the batch's rows over their sequences' cached tokens.  Row i
  * sees the tokens before position kv_len, and with causal != 0 those up to its
- * own position; a row that sees nothing gets O = 0 and L = -inf.
+ * own position; a row that sees nothing gets O = 0 and L = -inf, and one that
+ * sees a key and has an infinity or a NaN in its query becomes NaN.
  *   q          : in,  bf16 rows of Hq*d (rotated)
  *   o, lse     : out, bf16 [T, Hq, d] and fp32 [T, Hq], as for fattn_fwd
  *   selected   : in, int [T, Hkv, n_selected] or NULL (n_selected 0): row t's heads of kv head h

@@ -150,3 +150,32 @@ def test_good_starts_are_not_reported(B, T):
     K.fattn_cache_fwd(b.rows(b.q), c, *where, selected=sel)
     K.fattn_cache_append(b.rows(b.k_new), b.rows(b.v_new), c, *where)
     assert A.fattn_check_status() == 0
+
+
+@pytest.mark.parametrize("news", [1, 3, 40])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("bad", [np.inf, -np.inf, np.nan])
+def test_infinite_queries(news, d, bad):
+    """A query with an infinity has infinite scores and so a NaN row, also
+    where all of them are -inf; it is no row that sees nothing.  Other rows
+    and, in a group, other heads are as they were."""
+    b = Batch(340, [150, 70], [news, news], 1, 3, d, 32)
+    for p in b.table[:, :5].ravel():
+        if p < b.pages:               # one sign in column 9: every score is -inf, or every one inf
+            x = b.cache["k"][p, 0, :, 9]
+            b.cache["k"][p, 0, :, 9] = np.where(x & 0x7F == 0x7F, x, (x & 0x7F) | 0x80 | 1)
+    clean = b.device()
+    o0, l0 = K.fattn_cache_fwd(b.rows(b.q), *clean)
+    row = news // 2
+    b.q[row, 1, 9] = bad
+    sel = torch.zeros((b.T, 1, 1), dtype=torch.int32, device="cuda")
+    for kw in ({}, {"causal": False}, {"selected": sel}):
+        o, l = K.fattn_cache_fwd(b.rows(b.q), *clean, **kw)
+        assert bool(torch.isnan(o[row, 1]).all()) and bool(torch.isnan(l[row, 1])), kw
+        if kw == {}:
+            keep = torch.ones((b.T, 3), dtype=torch.bool, device="cuda")
+            keep[row, 1] = False
+            assert torch.equal(o[keep], o0[keep]) and torch.equal(l[keep], l0[keep])
+        else:
+            assert int(torch.isnan(l).sum()) == 1
+    assert A.fattn_check_status() == 0
