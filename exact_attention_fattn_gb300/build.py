@@ -19,15 +19,14 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB_PATH = os.path.join(PKG, "libfattn.so")
 BUILD_DIR = os.path.join(PKG, "_build")
-# Debug variant for tests: every dense kernel range-checks its computed shared-
+# Debug variant for tests: every kernel range-checks its computed shared-
 # memory, TMEM and global indices (a failed check is reported as
-# FATTN_ERR_DEBUG_CHECK, not a trap; the paged cache's kernels check what they
-# read from the device in every build), and the forward's K/V ring has its
-# minimum depth of two stages, so that the ring phases wrap as often as
-# they can.
+# FATTN_ERR_DEBUG_CHECK, not a trap), and the forward's K/V ring and the paged
+# cache's K ring have their minimum depth of two stages, so that the ring phases
+# wrap as often as they can.
 DEBUG_LIB_PATH = os.path.join(PKG, "libfattn_debug.so")
 DEBUG_BUILD_DIR = os.path.join(PKG, "_build_debug")
-DEBUG_FLAGS = ["-DFATTN_DEBUG", "-DFATTN_FWD_STAGES=2"]
+DEBUG_FLAGS = ["-DFATTN_DEBUG", "-DFATTN_FWD_STAGES=2", "-DFATTN_CACHE_K_STAGES=2"]
 SOURCES = ["fattn_api.cu", "fattn_fwd.cu", "fattn_bwd.cu", "fattn_bwd2.cu", "fattn_bwd_aux.cu",
            "fattn_fp8.cu", "fattn_sched.cu", "fattn_cache_api.cu", "fattn_cache_append.cu",
            "fattn_cache_chunk.cu", "fattn_cache_decode.cu", "fattn_cache_join.cu",

@@ -25,6 +25,18 @@ __device__ __forceinline__ void record_bad_index(DeviceStatus* st, unsigned int 
   }
 }
 
+// Debug builds' checks of what these kernels compute (dcheck; sites 601 on).
+// Every shared-memory offset lies in the launch's dynamic share, and `n` entries
+// from `at` on in an array of `size`.
+__device__ __forceinline__ uint32_t dynamic_smem_bytes() {
+  uint32_t r;
+  asm("mov.u32 %0, %%dynamic_smem_size;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ bool inside(long long at, long long n, long long size) {
+  return at >= 0 && at + n <= size;
+}
+
 // Waits of these kernels, as compact as they can be: the code of all of a
 // CTA's roles shares the instruction caches, and a role that waits for its
 // instructions holds the others up.  A wait that runs out leaves its site in

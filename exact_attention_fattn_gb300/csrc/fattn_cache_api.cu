@@ -84,12 +84,11 @@ struct AttnWorkspace {
 
 AttnWorkspace attn_workspace(int rows, int d, size_t q_rows) {
   AttnWorkspace w;
-  const int ctas = kSms * (rows == kChunkRows ? kChunkCtas : decode_ctas(d));
-  const size_t slots = 2 * static_cast<size_t>(ctas) * rows;
+  const size_t slots = static_cast<size_t>(part_rows(d, rows));
   w.o_off = 0;
   w.ml_off = align256(slots * d * sizeof(float));
   w.rec_off = w.ml_off + align256(slots * sizeof(float2));
-  w.q_off = w.rec_off + align256(2 * ctas * sizeof(int4));
+  w.q_off = w.rec_off + align256(slots / rows * sizeof(int4));
   if (rows != kChunkRows) q_rows = 0;
   w.qs_off = w.q_off + 2 * align256(q_rows * d);
   w.total = w.qs_off + align256(q_rows * sizeof(float));

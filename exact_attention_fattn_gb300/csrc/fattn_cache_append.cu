@@ -184,7 +184,8 @@ __device__ __forceinline__ void rotate_q(const CacheAppendArgs& a, int item) {
       on = false;
     }
     const int pos = q.len - q.n + (row - q.r0);
-    if (on && a.rope_dim > 0) cs = a.rope + static_cast<long long>(pos) * a.rope_dim;
+    if (on && a.rope_dim > 0 && dcheck(inside(pos, 1, a.rope_len), a.status, 601))
+      cs = a.rope + static_cast<long long>(pos) * a.rope_dim;
   }
   uint4 w[kQHeads];
 #pragma unroll
@@ -198,7 +199,9 @@ __device__ __forceinline__ void rotate_q(const CacheAppendArgs& a, int item) {
   for (int i = 0; i < kQHeads; ++i) {
     float f[8];
     rotate8<CH>(w[i], f, ang, a.rope_dim, a.interleaved, cc);
-    if (on && h0 + i < a.Hq)
+    if (on && h0 + i < a.Hq &&
+        dcheck(inside((static_cast<long long>(row) * a.Hq + h0 + i) * D + 8 * cc, 8,
+                      static_cast<long long>(a.s.T) * a.Hq * D), a.status, 602))
       *reinterpret_cast<uint4*>(a.q_out + (static_cast<long long>(row) * a.Hq + h0 + i) * D + 8 * cc) =
           make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
                      pack_bf16x2(f[6], f[7]));
@@ -307,6 +310,14 @@ __global__ void __launch_bounds__(kThreads, 8) append_kernel(const __grid_consta
   const int ek_old = scale_exp(a.k_scale[sc]), ev_old = scale_exp(a.v_scale[sc]);
   uint8_t* kp = a.k + pw.pid * a.page_stride + static_cast<long long>(head) * PAGE * D;
   uint8_t* vp = a.v + pw.pid * a.page_stride + static_cast<long long>(head) * PAGE * D;
+  // the head's page, its slots and their rows of the call
+  if (!dcheck(inside(pw.pid * a.page_stride + static_cast<long long>(head) * PAGE * D, PAGE * D,
+                     a.pages * a.page_stride) &&
+                  inside(sc, 1, static_cast<long long>(a.pages) * a.Hkv) && lo >= 0 && lo < hi && hi <= PAGE &&
+                  inside(pw.q.r0 + ((pw.p << SHIFT) + lo - pos0), hi - lo, a.s.T) &&
+                  (a.rope_dim == 0 || inside((pw.p << SHIFT) + lo, hi - lo, a.rope_len)),
+              a.status, 603))
+    return;
 
   float kf[8], vf[8];
   bool nan_row = false;
@@ -392,6 +403,7 @@ __global__ void __launch_bounds__(kThreads, 8) append_kernel(const __grid_consta
         high[z] = fmaxf(high[z], x[z]);
       }
     }
+    if (!dcheck(inside(t * D + 8 * cc, 8, PAGE * D), a.status, 604)) continue;
     *reinterpret_cast<uint2*>(kp + t * D + 8 * cc) = ck;
     *reinterpret_cast<uint2*>(vp + t * D + 8 * cc) = cv;
   }

@@ -58,6 +58,9 @@ namespace fattn {
 
 namespace {
 
+#ifndef FATTN_CACHE_K_STAGES
+#define FATTN_CACHE_K_STAGES 3
+#endif
 constexpr int kBM = 128;              // rows per tile
 constexpr int kBN = 128;              // keys per tile
 constexpr int kUnitRows = kChunkRows;
@@ -87,7 +90,7 @@ struct ChunkCfg {
   static constexpr int kQBytes = 2 * kCodeTile;          // hi, lo of one row tile
   static constexpr int kHalfTile = kBN * D * 2;          // fp16 V tile
   static constexpr int kHalfChunk = kBN * 128;           // 64 columns of it
-  static constexpr int kKStages = 3;
+  static constexpr int kKStages = FATTN_CACHE_K_STAGES;   // two at least
   static constexpr int kVStages = 2;                     // codes; two fp16 tiles follow
   static constexpr int kQOff = 0;
   static constexpr int kKOff = 2 * kQBytes;
@@ -343,6 +346,13 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int cta = blockIdx.x, G = args.grid;
+  [[maybe_unused]] constexpr long long kPartRows = part_rows(D, kUnitRows);
+  [[maybe_unused]] const long long q_rows = static_cast<long long>(args.s.T) * args.Hkv * args.group;
+  if (!dcheck(smem_u32(pre + args.s.B + 1) <= smem_u32(smem_raw) + dynamic_smem_bytes() &&
+                  2ll * (cta + 1) * kUnitRows <= kPartRows && C::col_s(1) + kBN <= C::col_o(0) &&
+                  C::col_o(1) + D <= 512,
+              args.status, 641))
+    return;
 
   if (tid == 0) {
     for (int s = 0; s < C::kKStages; ++s) {
@@ -452,7 +462,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       float m_ref = -INFINITY, l = 0.f, c0 = 1.f;
       {
         const int rr = s.row(t, r_tile);
-        if (rr < s.n * args.group) {
+        if (rr < s.n * args.group && dcheck(inside(s.q_row(args) + rr, 1, q_rows), args.status, 642)) {
           if (args.causal) lim = max(0, min(s.len, s.len - s.n + rr / args.group + 1));
           // log2(e) * scale times the power of two taken out of the row
           c0 = args.scale_log2 * args.q_scale[s.q_row(args) + rr];
@@ -588,8 +598,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ---- results
       const bool whole = s.whole();
       const int rr = s.row(t, r_tile);
-      const bool on = rr < s.n * args.group;
       const long long slot = 2ll * cta + (s.flags & Seg::kStarts);
+      const bool on = rr < s.n * args.group &&
+                      dcheck(inside(slot * kUnitRows + t * kBM + r_tile, 1, kPartRows), args.status, 643);
       float4* part = reinterpret_cast<float4*>(args.part_o + (slot * kUnitRows + t * kBM + r_tile) * D);
       float2* part_ml = args.part_ml + slot * kUnitRows + t * kBM + r_tile;
       if (jb >= nj) {
@@ -663,7 +674,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             o[i] = __float_as_uint(fmaf(__uint_as_float(o1[i]), a1, __uint_as_float(o[i]) * a0));
         }
         tmem_ld_wait32(o);
-        if (!on) continue;
+        if (!on || !dcheck(inside(out_row, 1, q_rows), args.status, 644)) continue;
         if (whole) {
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
@@ -881,6 +892,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           ok = false;
           break;
         }
+        ok = dcheck(in_range(sbase + C::kKOff + ks * C::kCodeTile, C::kCodeTile, sbase + C::kKOff, sbase + C::kVOff) &&
+                        in_range(sbase + C::kVOff + vs * C::kCodeTile, C::kCodeTile, sbase + C::kVOff, sbase + C::kHOff) &&
+                        bytes <= static_cast<uint32_t>(C::kCodeTile) && inside(s.head, 1, args.Hkv),
+                    args.status, 645);
+        if (!ok) break;
         if (lane == 0) {
           mbar_arrive_expect_tx(k_full(ks), bytes);
 #pragma unroll
@@ -902,6 +918,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t nb = static_cast<uint32_t>(min(kBM, s.n * args.group - first)) * D;
             const uint8_t* src = args.q_codes + (s.q_row(args) + first) * D;
             const uint32_t dst = sbase + C::kQOff + t * C::kQBytes;
+            ok = dcheck(first < s.n * args.group && nb <= static_cast<uint32_t>(C::kCodeTile) &&
+                            in_range(dst, C::kCodeTile + nb, sbase + C::kQOff, sbase + C::kKOff) &&
+                            inside((s.q_row(args) + first) * D, nb, q_rows * D),
+                        args.status, 646);
+            if (!ok) break;
             if (lane == 0) {
               mbar_arrive_expect_tx(q_full(t), 2 * nb);
               bulk_load_1d(dst, src, nb, q_full(t));
@@ -1033,6 +1054,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int id = ct + 128 * (i0 + i), row = row_of(id), c = chunk_of(id);
             const uint32_t base = dst + (c >> 2) * C::kHalfChunk + row * 128;
             const int c2 = 2 * (c & 3);            // 16-byte chunk of the fp16 row
+            if (!dcheck(in_range(src + code_off<D>(row, c), 16, sbase + C::kVOff, sbase + C::kHOff) &&
+                            in_range(base, 128, sbase + C::kHOff, sbase + C::kBarOff),
+                        args.status, 647))
+              continue;
             uint4 x, y;
             e4m3x4_to_f16x4(w[i].x, x.x, x.y);
             e4m3x4_to_f16x4(w[i].y, x.z, x.w);
@@ -1122,6 +1147,11 @@ __global__ void __launch_bounds__(256) split_kernel(const __grid_constant__ Cach
     const int rr = (token - q.r0) * a.group + (hq - head * a.group);
     const long long out = (static_cast<long long>(q.r0) * a.Hkv + static_cast<long long>(head) * q.n) * a.group + rr;
     // swizzle of the row's place in its tile (tiles start at multiples of 128 rows)
+    if (!dcheck(inside(out, 1, static_cast<long long>(a.s.T) * Hq) &&
+                    inside(out * D - static_cast<long long>(rr & 7) * D + code_off<D>(rr & 7, c), 16,
+                           static_cast<long long>(a.s.T) * Hq * D),
+                a.status, 648))
+      continue;
     uint8_t* dst = a.q_codes + out * D - static_cast<long long>(rr & 7) * D + code_off<D>(rr & 7, c);
     *reinterpret_cast<uint4*>(dst) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
     *reinterpret_cast<uint4*>(dst + a.q_lo) = make_uint4(lo[0], lo[1], lo[2], lo[3]);

@@ -256,6 +256,11 @@ __global__ void __launch_bounds__(kThreads, decode_ctas(D))
   const uint32_t ring = sbase + warp * C::kStages * C::kStageBytes;
   const uint32_t bar0 = sbase + C::kBarOff + warp * C::kStages * 8;
   const int G = a.grid, cta = blockIdx.x;
+  [[maybe_unused]] constexpr long long kPartRows = part_rows(D, kRows);
+  if (!dcheck(smem_u32(pre + (SPARSE ? 0 : a.s.B + 1)) <= smem_u32(smem_raw) + dynamic_smem_bytes() &&
+                  2ll * (cta + 1) * kRows <= kPartRows,
+              a.status, 631))
+    return;
 
   if (lane == 0) {
     for (int s = 0; s < C::kStages; ++s) mbar_init(bar0 + 8 * s, 1);
@@ -310,6 +315,10 @@ __global__ void __launch_bounds__(kThreads, decode_ctas(D))
       const uint16_t* src = a.q + (u.r0 + token) * a.q_row +
                             (static_cast<long long>(u.head) * a.group + (on ? rr - token * a.group : 0)) * D + 8 * col;
       const uint32_t dst = sbase + C::kQOff + ((buf * kRows + row) * D + 8 * col) * 2;
+      if (!dcheck(in_range(dst, 16, sbase + C::kQOff, sbase + C::kBarOff) &&
+                      (!on || (inside(u.r0 + token, 1, a.s.T) && inside(u.head, 1, a.Hkv))),
+                  a.status, 632))
+        continue;
       asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(on ? src : a.q),
                    "r"(on ? 16 : 0)
                    : "memory");
@@ -357,6 +366,10 @@ __global__ void __launch_bounds__(kThreads, decode_ctas(D))
     const int pid = __shfl_sync(0xffffffffu, batch.pid, src);
     const int y = __shfl_sync(0xffffffffu, batch.y, src);
     if (pid < 0) return false;
+    if (!dcheck(stage >= 0 && in_range(ring + stage * C::kStageBytes, C::kStageBytes, sbase, sbase + C::kRingBytes) &&
+                    pid < a.pages && inside(y, kTileKeys, static_cast<long long>(a.Hkv) << a.page_shift),
+                a.status, 633))
+      return false;
     if (lane == 0) {
       const uint32_t dst = ring + stage * C::kStageBytes;
       mbar_arrive_expect_tx(bar0 + 8 * stage, C::kStageBytes);
@@ -615,6 +628,8 @@ __global__ void __launch_bounds__(kThreads, decode_ctas(D))
       // within 128 bytes so that eight neighbouring lanes meet eight banks.
       float* base = join(warp) + (r + 8 * hh) * D + kVals * c;
       const int key = (c + 4 * (r & 1)) & (kVals / 4 - 1);
+      if (!dcheck(in_range(smem_u32(base), kVals * 4, sbase, sbase + C::kRingBytes) && free_stage >= 0, a.status, 634))
+        continue;
 #pragma unroll
       for (int q = 0; q < kVals / 4; ++q) {
         // columns kVals c + 4 q ..: the first half of them are n = 2 c, then n = 2 c + 1
@@ -635,7 +650,8 @@ __global__ void __launch_bounds__(kThreads, decode_ctas(D))
         if (x.x != -INFINITY) ll += x.y * ex2_approx(x.x - mm);
         else if (x.y != x.y) ll = x.y;               // a NaN row
       }
-      a.part_ml[(2 * cta + slot) * kRows + tid] = make_float2(mm, ll);
+      if (dcheck(inside((2 * cta + slot) * kRows + tid, 1, kPartRows), a.status, 635))
+        a.part_ml[(2 * cta + slot) * kRows + tid] = make_float2(mm, ll);
     }
     for (int f = tid; some && f < kRows * (D / 4); f += kThreads) {
       const int row = f / (D / 4), q4 = f % (D / 4);
@@ -664,11 +680,12 @@ __global__ void __launch_bounds__(kThreads, decode_ctas(D))
         const int token = rr / a.group;
         const long long at = (static_cast<long long>(u.r0 + token) * a.Hkv + u.head) * a.group +
                              (rr - token * a.group);
+        if (!dcheck(inside(at, 1, static_cast<long long>(a.s.T) * a.Hkv * a.group), a.status, 636)) continue;
         const float inv = ll == 0.f ? 0.f : 1.f / ll;
         *reinterpret_cast<uint2*>(a.o + at * D + 4 * q4) =
             make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
         if (q4 == 0) a.lse[at] = ll == 0.f ? -INFINITY : (mm + log2f(ll)) * kLn2;
-      } else {
+      } else if (dcheck(inside((2ll * cta + slot) * kRows + row, 1, kPartRows), a.status, 637)) {
         *reinterpret_cast<float4*>(a.part_o + ((2ll * cta + slot) * kRows + row) * D + 4 * q4) = acc;
       }
     }

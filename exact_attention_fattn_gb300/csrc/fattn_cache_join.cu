@@ -48,6 +48,7 @@ struct JoinCfg {
 template <int D, int ROWS>
 __global__ void __launch_bounds__(JoinCfg<D, ROWS>::kThreads) join_kernel(const CacheAttnArgs a) {
   using J = JoinCfg<D, ROWS>;
+  [[maybe_unused]] constexpr long long kPartRows = part_rows(D, ROWS);
   __shared__ Part side[J::kGroups][J::kRows][J::kF4];
   const int cta = blockIdx.x, G = a.grid;
   // selected pages: the kernel in front searches for its rows' sequences
@@ -68,10 +69,11 @@ __global__ void __launch_bounds__(JoinCfg<D, ROWS>::kThreads) join_kernel(const 
   for (int c = cta + group; c <= more.x; c += J::kGroups) {
     if (cta_first(W, G, c) == cta_first(W, G, c + 1)) continue;   // a CTA without work
     const long long at = (2ll * c + (c == cta ? 1 : 0)) * ROWS;
-    Part x[J::kPer];
+    Part x[J::kPer] = {};
 #pragma unroll
     for (int k = 0; k < J::kPer; ++k) {
       const int row = min(row0 + k * J::kRows, end - 1);          // a row that is there, to load
+      if (!dcheck(row >= 0 && inside(at + row, 1, kPartRows), a.status, 621)) continue;
       const float2 ml = a.part_ml[at + row];
       x[k] = Part{ml.x, ml.y, reinterpret_cast<const float4*>(a.part_o + (at + row) * D)[q4]};
     }
@@ -93,6 +95,7 @@ __global__ void __launch_bounds__(JoinCfg<D, ROWS>::kThreads) join_kernel(const 
     const int rr = rec.z * ROWS + row, token = rr / a.group;
     const long long out = (static_cast<long long>(rec.x + token) * a.Hkv + rec.w) * a.group +
                           (rr - token * a.group);
+    if (!dcheck(inside(out, 1, static_cast<long long>(a.s.T) * a.Hkv * a.group), a.status, 622)) continue;
     const float inv = p[k].l == 0.f ? 0.f : 1.f / p[k].l;
     *reinterpret_cast<uint2*>(a.o + out * D + 4 * q4) = make_uint2(
         pack_bf16x2(p[k].o.x * inv, p[k].o.y * inv), pack_bf16x2(p[k].o.z * inv, p[k].o.w * inv));

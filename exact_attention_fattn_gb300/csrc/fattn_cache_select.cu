@@ -174,7 +174,7 @@ struct Scorer {
       for (int off = LP / 2; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
       if (gl == i) mine_sum = s;
     }
-    if (gl < kInFlight && r.mine < n)
+    if (gl < kInFlight && r.mine < n && dcheck(inside(r.mine, 1, a.s.max_pages), a.status, 611))
       out(r.mine, r.pid >= 0 ? __fmul_rn(__int2float_rn(mine_sum), r.ks) : -INFINITY);
   }
 };
@@ -270,7 +270,7 @@ __device__ __forceinline__ void choose(const CacheSelectArgs& a, ChooseShared& s
       all += sh.wsum[1][w];
     }
     done += all;
-    if (take && slot < k) out[slot] = i;
+    if (take && slot < k && dcheck(inside(slot, 1, k) && inside(i, 1, n), a.status, 614)) out[slot] = i;
   }
 }
 
@@ -304,6 +304,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) select_kernel(const __grid_cons
   if (!row_position(a, row, b, pos)) return;
   const int n = pos < 0 ? 0 : (pos >> a.page_shift) + 1;
   int* out = a.selected + (static_cast<long long>(row) * a.Hkv + head) * a.n_selected;
+  if (!dcheck(row < a.s.T && head < a.Hkv && n <= a.s.max_pages, a.status, 615)) return;
   if (n <= a.n_selected) {
     if (rank == 0) take_all(a, n, out);
     return;
@@ -316,7 +317,9 @@ __global__ void __launch_bounds__(NT, 1024 / NT) select_kernel(const __grid_cons
   for (int p0 = p1; p0 < n; p0 += step) {
     const typename S::Pages cur = next;
     if (p0 + step < n) next = s.look_up(p0 + step, n);
-    s.score(cur, n, [&](int page, float x) { st_cluster(to + 4 * page, x); });
+    s.score(cur, n, [&](int page, float x) {
+      if (dcheck(inside(4 * page, 4, dynamic_smem_bytes()), a.status, 612)) st_cluster(to + 4 * page, x);
+    });
   }
   if (shared) {
     cluster_arrive();
@@ -339,7 +342,9 @@ __global__ void __launch_bounds__(kSelThreads, 4) score_kernel(const __grid_cons
   const int n = pos < 0 ? 0 : (pos >> a.page_shift) + 1;
   if (p0 >= n || n <= a.n_selected) return;   // few pages: all are taken
   const S s(a, sh, row, head, b);
-  float* out = a.scores + (static_cast<long long>(row) * a.Hkv + head) * a.s.max_pages;
+  const long long at = (static_cast<long long>(row) * a.Hkv + head) * a.s.max_pages;
+  if (!dcheck(inside(at, n, static_cast<long long>(a.s.T) * a.Hkv * a.s.max_pages), a.status, 613)) return;
+  float* out = a.scores + at;
   s.score(s.look_up(p0, n), n, [&](int page, float x) { out[page] = x; });
 }
 

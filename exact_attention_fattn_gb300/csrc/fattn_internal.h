@@ -184,6 +184,10 @@ constexpr int kChunkRows = 256;
 constexpr int kChunkTileKeys = 128;
 constexpr int kChunkUnitCost = 3;
 constexpr int kChunkCtas = 1;
+// Rows of partial results in the workspace: two units of a CTA, `rows` each.
+constexpr long long part_rows(int d, int rows) {
+  return 2ll * kSms * (rows == kChunkRows ? kChunkCtas : decode_ctas(d)) * rows;
+}
 
 // Few rows per sequence (tiles of 16, mma.sync); tk, tv: 3-D uint8 views
 // {d, Hkv * page, pages} of the codes, boxes of 32 rows, swizzled by a row's
