@@ -500,7 +500,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     mma_end:
       mma_commit_w(bar(kBarMmaDone));
-      mbar_wait_drain(bar(kBarMmaDone), 0, args.wait_budget);
+      mbar_wait_drain(bar(kBarMmaDone), 0);
     }
     __syncwarp();
   } else if (warp == kLoadWarp) {
@@ -582,11 +582,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       // Every copy this warp started must have landed before the CTA exits.
       for (uint32_t g = issued_q > 2 ? issued_q - 2 : 0; g < issued_q; ++g)
-        mbar_wait_drain(bar(kBarQFull + (g & 1)), (g >> 1) & 1, args.wait_budget);
+        mbar_wait_drain(bar(kBarQFull + (g & 1)), (g >> 1) & 1);
       for (uint32_t g = issued_do > 2 ? issued_do - 2 : 0; g < issued_do; ++g)
-        mbar_wait_drain(bar(kBarDoFull + (g & 1)), (g >> 1) & 1, args.wait_budget);
-      if (items_v > 0) mbar_wait_drain(bar(kBarVFull), (items_v - 1) & 1, args.wait_budget);
-      if (items_k > 0) mbar_wait_drain(bar(kBarKFull), (items_k - 1) & 1, args.wait_budget);
+        mbar_wait_drain(bar(kBarDoFull + (g & 1)), (g >> 1) & 1);
+      if (items_v > 0) mbar_wait_drain(bar(kBarVFull), (items_v - 1) & 1);
+      if (items_k > 0) mbar_wait_drain(bar(kBarKFull), (items_k - 1) & 1);
     }
     __syncwarp();
   } else if (warp == kReduceWarp) {

@@ -533,7 +533,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       mma2_commit_both_w(bar(kBMmaDone));
-      mbar_drain_cl(bar(kBMmaDone), 0, args.wait_budget);
+      mbar_drain_cl(bar(kBMmaDone), 0);
     }
     __syncwarp();
   } else if (warp == kLoadWarp) {
@@ -629,21 +629,21 @@ __global__ void __launch_bounds__(kThreads, 1)
       // Every copy of either CTA that completes on the leader's barriers must
       // have landed before the pair exits: drain the phases posted last.
       for (uint32_t g = issued > 2 ? issued - 2 : 0; g < issued; ++g) {
-        mbar_drain_cl(bar(kBQsFull + (g & 1)), (g >> 1) & 1, args.wait_budget);
-        mbar_drain_cl(bar(kBDosFull + (g & 1)), (g >> 1) & 1, args.wait_budget);
+        mbar_drain_cl(bar(kBQsFull + (g & 1)), (g >> 1) & 1);
+        mbar_drain_cl(bar(kBDosFull + (g & 1)), (g >> 1) & 1);
       }
-      if (dov_posted > 0) mbar_drain_cl(bar(kBDovFull), (dov_posted - 1) & 1, args.wait_budget);
-      if (qk_posted > 0) mbar_drain_cl(bar(kBQkFull), (qk_posted - 1) & 1, args.wait_budget);
-      if (k_items > 0) mbar_drain_cl(bar(kBKFull), (k_items - 1) & 1, args.wait_budget);
-      if (v_items > 0) mbar_drain_cl(bar(kBVFull), (v_items - 1) & 1, args.wait_budget);
-      if (kq_items > 0) mbar_drain_cl(bar(kBKqFull), (kq_items - 1) & 1, args.wait_budget);
+      if (dov_posted > 0) mbar_drain_cl(bar(kBDovFull), (dov_posted - 1) & 1);
+      if (qk_posted > 0) mbar_drain_cl(bar(kBQkFull), (qk_posted - 1) & 1);
+      if (k_items > 0) mbar_drain_cl(bar(kBKFull), (k_items - 1) & 1);
+      if (v_items > 0) mbar_drain_cl(bar(kBVFull), (v_items - 1) & 1);
+      if (kq_items > 0) mbar_drain_cl(bar(kBKqFull), (kq_items - 1) & 1);
     } else if (!ok) {
       // The leader may have stopped posting: give this CTA's last copies
       // time to land before the pair exits (they finish within microseconds).
       for (int t = 0; t < 64; ++t) __nanosleep(1000);
     }
     for (uint32_t g = issued > 2 ? issued - 2 : 0; g < issued; ++g)
-      mbar_drain_cl(bar(kBLdFull + (g & 1)), (g >> 1) & 1, args.wait_budget);
+      mbar_drain_cl(bar(kBLdFull + (g & 1)), (g >> 1) & 1);
     __syncwarp();
   } else if (warp == kReduceWarp) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kCtrlRegs));

@@ -845,7 +845,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     // No MMA may still be running when TMEM is released.
     commit_to(mma_done, lead);
-    mbar_wait_drain(mma_done, 0, args.wait_budget);
+    mbar_wait_drain(mma_done, 0);
     __syncwarp();
   } else if (warp == kLoadWarp) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kCtrlRegs));
@@ -951,11 +951,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     // Every copy this warp started must have landed before the CTA exits.
     for (uint32_t r = kn > C::kKStages ? kn - C::kKStages : 0; r < kn; ++r)
-      mbar_wait_drain(k_full(r % C::kKStages), (r / C::kKStages) & 1, args.wait_budget);
+      mbar_wait_drain(k_full(r % C::kKStages), (r / C::kKStages) & 1);
     for (uint32_t r = vn > C::kVStages ? vn - C::kVStages : 0; r < vn; ++r)
-      mbar_wait_drain(v_full(r % C::kVStages), (r / C::kVStages) & 1, args.wait_budget);
+      mbar_wait_drain(v_full(r % C::kVStages), (r / C::kVStages) & 1);
     for (int t = 0; t < 2; ++t)
-      if (qn[t] > 0) mbar_wait_drain(q_full(t), (qn[t] - 1) & 1, args.wait_budget);
+      if (qn[t] > 0) mbar_wait_drain(q_full(t), (qn[t] - 1) & 1);
     __syncwarp();
   } else if (warp < kConvWarp0) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kCtrlRegs));

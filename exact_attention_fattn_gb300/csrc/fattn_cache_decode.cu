@@ -704,7 +704,7 @@ __global__ void __launch_bounds__(kThreads, decode_ctas(D))
   if (tid == 0) report_abort(misc[0], a.status);
   // Copies in flight land before the CTA exits (only after a wait gave up).
   for (int s = 0; s < C::kStages; ++s)
-    if (pending >> s & 1) mbar_wait_drain(bar0 + 8 * s, phases >> s & 1u, a.wait_budget);
+    if (pending >> s & 1) mbar_wait_drain(bar0 + 8 * s, phases >> s & 1u);
 }
 
 template <int D, bool SPARSE>

@@ -719,7 +719,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     mma_end:
       // No MMA may still be running when TMEM is released.
       mma_commit_w(b.mma_done);
-      mbar_wait_drain(b.mma_done, 0, args.wait_budget);
+      mbar_wait_drain(b.mma_done, 0);
     }
     __syncwarp();
   } else if (warp == kLoadWarp) {
@@ -811,11 +811,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       // Every copy this warp started must have landed before the CTA exits.
       for (uint32_t r = kvb > C::kStages ? kvb - C::kStages : 0; r < kvb; ++r)
-        mbar_wait_drain(b.kv_full0 + 8u * (r % C::kStages), (r / C::kStages) & 1,
-                        args.wait_budget);
+        mbar_wait_drain(b.kv_full0 + 8u * (r % C::kStages), (r / C::kStages) & 1);
       for (int sl = 0; sl < 2; ++sl)
-        if (ql[sl] > 0) mbar_wait_drain(q_full_bar(sl), (ql[sl] - 1) & 1, args.wait_budget);
-      if (items > 0) mbar_wait_drain(b.q_full, (items - 1) & 1, args.wait_budget);
+        if (ql[sl] > 0) mbar_wait_drain(q_full_bar(sl), (ql[sl] - 1) & 1);
+      if (items > 0) mbar_wait_drain(b.q_full, (items - 1) & 1);
     }
     __syncwarp();
   } else {

@@ -133,12 +133,16 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, const W
   }
 }
 
-// Same, but with a fixed budget and no abort check: used to drain
-// asynchronous copies that are known to finish on their own.
-__device__ __forceinline__ bool mbar_wait_drain(uint32_t bar, uint32_t parity, long long budget) {
+// Same, but without an abort check, and for kDrainCycles (about a second) whatever
+// the budget: used to drain copies and MMAs that are known to finish on their
+// own, within microseconds.  A CTA must not end before they do, also where a
+// short budget has just ended its other waits.
+constexpr long long kDrainCycles = 1ll << 31;
+
+__device__ __forceinline__ bool mbar_wait_drain(uint32_t bar, uint32_t parity) {
   const long long t0 = clock64();
   while (!mbar_try_wait(bar, parity)) {
-    if (clock64() - t0 > budget) return false;
+    if (clock64() - t0 > kDrainCycles) return false;
   }
   return true;
 }
@@ -578,10 +582,10 @@ __device__ __forceinline__ bool mbar_wait_cl_warp(uint32_t bar, uint32_t parity,
   return __all_sync(0xffffffffu, mbar_wait_cl(bar, parity, w, site));
 }
 
-__device__ __forceinline__ bool mbar_drain_cl(uint32_t bar, uint32_t parity, long long budget) {
+__device__ __forceinline__ bool mbar_drain_cl(uint32_t bar, uint32_t parity) {
   const long long t0 = clock64();
   while (!mbar_try_wait_cl(bar, parity)) {
-    if (clock64() - t0 > budget) return false;
+    if (clock64() - t0 > kDrainCycles) return false;   // as mbar_wait_drain
   }
   return true;
 }

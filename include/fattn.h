@@ -407,6 +407,8 @@ const char* fattn_status_string(int status);
 /*
  * Budget, in SM clock cycles, for every pipeline wait inside the kernels
  * (default 2^31, about one second).  Values <= 0 restore the default.
+ * What a kernel has started itself it sees end, whatever the budget: copies
+ * and products in flight are given 2^31 cycles.
  * Applies to launches made after the call, from any thread.
  */
 void fattn_set_wait_budget(long long cycles);

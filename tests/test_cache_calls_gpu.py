@@ -179,3 +179,25 @@ def test_infinite_queries(news, d, bad):
         else:
             assert int(torch.isnan(l).sum()) == 1
     assert A.fattn_check_status() == 0
+
+
+@pytest.mark.parametrize("news", [1, 60])
+@pytest.mark.parametrize("d", [64, 128])
+def test_a_wait_budget_that_runs_out(news, d):
+    """Waits that give up are reported, and the next call, on the same memory
+    and on tensor memory that the last one handed back, is right."""
+    b = Batch(350, [3000, 700], [news, news], 2, 2, d, 64)
+    where, q = b.device(), b.rows(b.q)
+    want = K.fattn_cache_fwd(q, *where)
+    assert A.fattn_check_status() == 0
+    A.fattn_set_wait_budget(1)
+    try:
+        for _ in range(3):
+            K.fattn_cache_fwd(q, *where)
+            assert A.fattn_check_status() in (_lib.FATTN_OK, _lib.FATTN_ERR_TIMEOUT)
+    finally:
+        A.fattn_set_wait_budget(0)
+    for _ in range(3):
+        got = K.fattn_cache_fwd(q, *where)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    assert A.fattn_check_status() == 0
