@@ -17,6 +17,7 @@ from . import _lib
 from .attention import default_scale
 
 PAGE_SIZES = (32, 64, 128)
+MAX_KV_HEADS = 1024
 
 
 class Fp8Cache(NamedTuple):
@@ -33,8 +34,8 @@ class Fp8Cache(NamedTuple):
 def fattn_cache_alloc(pages: int, kv_heads: int, d: int, page: int = 64, device="cuda",
                       bounds: bool = False) -> Fp8Cache:
     """An empty cache of ``pages`` pages of ``page`` tokens (codes zero, scales 1)."""
-    if pages < 1 or kv_heads < 1 or page not in PAGE_SIZES or d not in (64, 128):
-        raise ValueError("need pages, kv_heads >= 1, page in (32, 64, 128) and d in (64, 128)")
+    if pages < 1 or not 1 <= kv_heads <= MAX_KV_HEADS or page not in PAGE_SIZES or d not in (64, 128):
+        raise ValueError(f"need pages >= 1, kv_heads from 1 to {MAX_KV_HEADS}, page in (32, 64, 128) and d in (64, 128)")
     k, v = (torch.zeros((pages, kv_heads, page, d), dtype=torch.uint8, device=device)
             for _ in range(2))
     ks, vs = (torch.ones((pages, kv_heads), dtype=torch.float32, device=device) for _ in range(2))

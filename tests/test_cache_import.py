@@ -29,3 +29,13 @@ else:
 def test_import_without_torchs_private_names():
     r = subprocess.run([sys.executable, "-c", PROGRAM], cwd=ROOT, capture_output=True, text=True, timeout=300)
     assert r.returncode == 0, r.stderr
+
+
+def test_alloc_refuses_what_no_call_takes():
+    import pytest
+
+    import exact_attention_fattn_gb300 as F
+
+    assert F.fattn_cache_alloc(1, 1024, 64, page=32, device="cpu").k.shape[1] == 1024
+    with pytest.raises(ValueError):
+        F.fattn_cache_alloc(1, 1025, 64, page=32, device="cpu")
