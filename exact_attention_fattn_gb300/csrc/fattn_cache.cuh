@@ -120,16 +120,19 @@ struct SeqInfo {
   bool ok;
 };
 
-__device__ __forceinline__ SeqInfo seq_info(const CacheSeqs& s, int b, int page_shift) {
+__device__ __forceinline__ SeqInfo seq_info(const CacheSeqs& s, int r0, int r1, int len, int page_shift) {
   SeqInfo q;
-  q.r0 = __ldg(s.q_start + b);
-  const int r1 = __ldg(s.q_start + b + 1);
-  q.len = __ldg(s.kv_len + b);
+  q.r0 = r0;
+  q.len = len;
   q.ok = q.r0 >= 0 && r1 >= q.r0 && r1 <= s.T && q.len >= 0 &&
          q.len <= (static_cast<long long>(s.max_pages) << page_shift);
   q.n = q.ok ? r1 - q.r0 : 0;
   if (!q.ok) q.len = 0;
   return q;
+}
+
+__device__ __forceinline__ SeqInfo seq_info(const CacheSeqs& s, int b, int page_shift) {
+  return seq_info(s, __ldg(s.q_start + b), __ldg(s.q_start + b + 1), __ldg(s.kv_len + b), page_shift);
 }
 
 // Reports the sequences first, first + step, .. that make no sense.  A kernel that
@@ -141,6 +144,22 @@ __device__ __forceinline__ void check_seqs(const CacheSeqs& s, int first, int st
   for (int b = first; b < s.B; b += step)
     if (!seq_info(s, b, page_shift).ok) record_bad_index(st, kSiteSeqStart);
 }
+
+// The same where a thread cannot wait for its first sequence's numbers: it asks
+// for them at once and reports later (loads that the compiler leaves in place).
+struct SeqCheck {
+  int b, r0, r1, len;
+  __device__ __forceinline__ SeqCheck(const CacheSeqs& s, int first) : b(first), r0(0), r1(0), len(0) {
+    if (b >= s.B) return;
+    asm volatile("ld.global.nc.s32 %0, [%1];" : "=r"(r0) : "l"(s.q_start + b));
+    asm volatile("ld.global.nc.s32 %0, [%1];" : "=r"(r1) : "l"(s.q_start + b + 1));
+    asm volatile("ld.global.nc.s32 %0, [%1];" : "=r"(len) : "l"(s.kv_len + b));
+  }
+  __device__ __forceinline__ void report(const CacheSeqs& s, int step, int page_shift, DeviceStatus* st) const {
+    if (b < s.B && !seq_info(s, r0, r1, len, page_shift).ok) record_bad_index(st, kSiteSeqStart);
+    check_seqs(s, b + step, step, page_shift, st);
+  }
+};
 
 // Pieces of work of a whole call.  The host has bounded them to 32 bits for
 // sequences one behind the other; with overlapping ones the call does nothing.

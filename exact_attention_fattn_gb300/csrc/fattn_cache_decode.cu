@@ -262,6 +262,9 @@ __global__ void __launch_bounds__(kThreads, decode_ctas(D))
               a.status, 631))
     return;
 
+  // a sparse call searches for its tokens' sequences only (in the join's
+  // kernel this check cost 0.6 us of 39)
+  const SeqCheck check(a.s, SPARSE ? cta * kThreads + tid : a.s.B);
   if (lane == 0) {
     for (int s = 0; s < C::kStages; ++s) mbar_init(bar0 + 8 * s, 1);
     tma_prefetch_desc(&tm_k);
@@ -406,6 +409,7 @@ __global__ void __launch_bounds__(kThreads, decode_ctas(D))
       pending |= 1 << stage;
   };
   asm volatile("cp.async.wait_group 0;" ::: "memory");
+  if constexpr (SPARSE) check.report(a.s, G * kThreads, a.page_shift, a.status);
   __syncthreads();
 
   int i = 0;                                        // tile of this warp

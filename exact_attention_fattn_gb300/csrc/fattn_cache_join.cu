@@ -51,9 +51,6 @@ __global__ void __launch_bounds__(JoinCfg<D, ROWS>::kThreads) join_kernel(const 
   [[maybe_unused]] constexpr long long kPartRows = part_rows(D, ROWS);
   __shared__ Part side[J::kGroups][J::kRows][J::kF4];
   const int cta = blockIdx.x, G = a.grid;
-  // selected pages: the kernel in front searches for its rows' sequences
-  if (a.selected != nullptr && blockIdx.y == 0)
-    check_seqs(a.s, cta * J::kThreads + threadIdx.x, G * J::kThreads, a.page_shift, a.status);
   wait_for_parent();
   const int4 rec = a.rec[2 * cta];
   const int rows = rec.y * a.group - rec.z * ROWS;   // of the unit, from its first
