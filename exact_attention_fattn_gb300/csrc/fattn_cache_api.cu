@@ -105,7 +105,15 @@ AttnWorkspace attn_workspace(int rows, int d, size_t q_rows) {
 // 37 / 35, 32 x up to 4000 93 / 67; 64 rows, 8 x 1000 26.7 / 26.2, 1 x 8000 23.5 / 32,
 // 32 x 500 46 / 36.  d = 64: 24 rows, 16 x 16000 103 / 123; 40 rows, 32 x 1000 36 /
 // 42, 32 x 4000 86 / 80; 64 rows, 4 x 8000 37 / 33.
-// tokens: at most as many times a kv head the call can reach, -1 for unknown.
+// tokens: at most as many times a kv head the call can reach, -1 for unknown.  The
+// lengths are on the device, so this is what the page tables and the pool could
+// hold; the measurements above are with tables as wide as the longest sequence.
+// Where both are much larger than what is in use, 2 to 4 units go to tcgen05 however
+// short the sequences are (exact table / table of 2048 pages and 16 times the pool,
+// us: 64 rows, 1 x 8000 23.5 / 30.7, 8 x 1000 26.7 / 23.3; d = 64: 40 rows, 32 x 1000
+// 31.4 / 37.3, 24 rows, 16 x 16000 82 / 98.5).  Likewise a batch that mixes pieces of
+// prompts with single tokens is served as its average: 255 single tokens on 1000 to
+// 4000 keys and a piece of 700 on 16000 take 962 us in one call, 212 + 153 in two.
 bool few_rows(int T, int B, int group, int d, int n_selected, long long tokens) {
   const long long units = (static_cast<long long>(T) * group + kDecodeRows * static_cast<long long>(B) - 1) /
                           (kDecodeRows * static_cast<long long>(B));

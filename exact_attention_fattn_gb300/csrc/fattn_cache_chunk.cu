@@ -31,7 +31,7 @@
 // Bound: the chain of a row tile, its S (512 cycles of MMA), the softmax (about
 // 1600), its P V (512) and the hand-overs, which the other tile's chain does not
 // quite fill: 3370 cycles a step of both, 2048 of them MMA (2 x 2048 rows of 32
-// heads on 16384 keys: 671 us, 1430 TFLOP/s, 0.73 of the measured bf16 rate,
+// heads on 16384 keys: 672 us, 1417 TFLOP/s, 0.73 of the measured bf16 rate,
 // tensor pipe 60 % busy).  Handing P over in two parts, so that P V starts on the
 // first, was slower (719 against 688 us).  Short prompts are bound by the units'
 // ends: the softmax warps' set-up, masked tiles and stores.
@@ -131,8 +131,7 @@ __device__ __forceinline__ uint32_t code_off(int r, int c) {
 }
 
 // MMAs and their commits from one lane of the converged MMA warp, chosen once
-// (`lead`): an election in front of each costs 25 instructions, more than the
-// MMA's own.
+// (`lead`) instead of in front of each.
 __device__ __forceinline__ uint32_t elect_lane() {
   uint32_t r;
   asm volatile("{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\tselp.u32 %0, 1, 0, e;\n\t}" : "=r"(r));
@@ -456,8 +455,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!(ok = wait_seg(si))) break;
       const Seg& s = seg_at(si);
       if (s.flags & Seg::kLast) break;
-      // Keys the row sees.  Rows past the unit's last see all (their queries
-      // are zero), so that they need no mask.
+      // Keys the row sees.  Rows past the unit's last see all, so that they need no
+      // mask.  Their queries are whatever shared memory held, and so are their
+      // scores, NaN included; but a row of S, P and O depends on its own query
+      // only, a rescale that such a row sets off multiplies the others by 1, and
+      // nothing of such a row is stored.
       int lim = s.len;
       float m_ref = -INFINITY, l = 0.f, c0 = 1.f;
       {

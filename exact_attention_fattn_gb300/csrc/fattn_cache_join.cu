@@ -3,8 +3,8 @@
 // workspace (unnormalised rows of O in fp32, reference maximum and sum), in
 // the order of their keys.
 //
-// Bound: latency where a unit has many parts (one long sequence: up to 304 of
-// them), bytes where units are large (256 rows, two or three parts each).  A
+// Bound: latency where a unit has many parts (one long sequence: as many as the
+// few-rows kernel has CTAs, 304, or 456 for d = 64), bytes where units are large (256 rows, two or three parts each).  A
 // thread has 4 columns of a row; the small units' parts are walked by four groups
 // of threads side by side, the large ones' by one, two rows a thread whose loads
 // go out together (32 sequences of 40 rows, whole call: 67.1 us with one row, 66.5

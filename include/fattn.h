@@ -327,7 +327,8 @@ typedef struct {
  * nothing.  fp32, every product and sum rounded.
  * Quantization: a page and head has scale 2^e with e the smallest exponent in
  * [-48, 48] for which amax <= 448 * 2^e over its tokens, or the exponent it has if that is
- * larger; code = e4m3(x * 2^-e), nearest even, saturated.  When new tokens
+ * larger; code = e4m3(x * 2^-e), nearest even, saturated (so an infinity becomes
+ * 448 * 2^48, which leaves nothing of its page's other tokens).  When new tokens
  * raise e, the page's earlier codes are multiplied by the power of two and
  * rounded again.  A page whose slot 0 is among the new tokens starts over.
  * A token with a NaN in a head's key or value gets a NaN key and a zero
@@ -359,8 +360,17 @@ int fattn_cache_append(const fattn_cache* cache, const void* k_new, long long k_
  *                256-byte aligned; contents on entry ignored; calls that may overlap need
  *                one each
  * Value slots behind a sequence's end may hold anything; those before it hold
- * no NaN code (fattn_cache_append writes none).  Results do not depend on
- * timing.  Returns a fattn_status.
+ * no NaN code (fattn_cache_append writes none).
+ * Rounding: a query enters the products off by at most 2^-17 of its row's
+ * largest entry (exact for entries above 2^-9 of it), probabilities are rounded
+ * to fp16 (2^-11) for P V, and O to bf16 (2^-8); scores, sums, maxima and the
+ * accumulators are fp32.
+ * One of two kernels, for few and for many rows, serves the whole call.  The
+ * choice goes by the rows of an average sequence, T * (Hq / Hkv) / B, and for 17 to 64
+ * of them also by min(B * max_pages, pages), as the lengths are on the device.
+ * Selected pages go to the one for few rows.  Both are right for every batch;
+ * their results may differ in the last bits.  A batch that mixes pieces of prompts with many single tokens is faster as two calls.
+ * Results do not depend on timing.  Returns a fattn_status.
  */
 size_t fattn_cache_fwd_workspace_bytes(int T, int B, int Hq, int Hkv, int d, int n_selected);
 int fattn_cache_fwd(const fattn_cache* cache, const void* q, long long q_row, void* o, float* lse,
@@ -383,7 +393,7 @@ int fattn_cache_fwd(const fattn_cache* cache, const void* q, long long q_row, vo
  *   workspace : at least fattn_cache_select_workspace_bytes(T, Hkv, max_pages), 256-byte aligned;
  *               contents on entry ignored; NULL (0 bytes) will do where that function says 256, the
  *               sizes that keep their scores on chip
- * Returns a fattn_status.
+ * max_pages is at most 65535 * 128 here.  Returns a fattn_status.
  */
 size_t fattn_cache_select_workspace_bytes(int T, int Hkv, int max_pages);
 int fattn_cache_select(const fattn_cache* cache, const void* q, long long q_row,
