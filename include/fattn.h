@@ -369,7 +369,8 @@ int fattn_cache_append(const fattn_cache* cache, const void* k_new, long long k_
  * choice goes by the rows of an average sequence, T * (Hq / Hkv) / B, and for 17 to 64
  * of them also by min(B * max_pages, pages), as the lengths are on the device.
  * Selected pages go to the one for few rows.  Both are right for every batch;
- * their results may differ in the last bits.  A batch that mixes pieces of prompts with many single tokens is faster as two calls.
+ * their results may differ in the last bits.  A batch that mixes pieces of
+ * prompts with many single tokens is faster as two calls.
  * Results do not depend on timing.  Returns a fattn_status.
  */
 size_t fattn_cache_fwd_workspace_bytes(int T, int B, int Hq, int Hkv, int d, int n_selected);
