@@ -5,10 +5,10 @@
 //
 // Bound: latency where a unit has many parts (one long sequence: as many as the
 // few-rows kernel has CTAs, 304, or 456 for d = 64), bytes where units are large
-// (256 rows, two or three parts each).  A thread has 4 columns of a row; the small units' parts are walked by four groups
-// of threads side by side, the large ones' by one, two rows a thread whose loads
-// go out together (32 sequences of 40 rows, whole call: 67.1 us with one row, 66.5
-// with two, 68.1 with four).
+// (256 rows, two or three parts each).  A thread has 4 columns of a row; the small
+// units' parts are walked by four groups of threads side by side, the large ones'
+// by one, two rows a thread whose loads go out together (32 sequences of 40 rows,
+// whole call: 67.1 us with one row, 66.5 with two, 68.1 with four).
 #include "fattn_cache.cuh"
 
 namespace fattn {
