@@ -37,3 +37,20 @@ from .cache import (  # noqa: F401
     fattn_cache_select_workspace_bytes,
     fattn_rope_table,
 )
+from .latent import (  # noqa: F401
+    LatentCache,
+    fattn_latent_alloc,
+    fattn_latent_append,
+    fattn_latent_fwd,
+    fattn_latent_fwd_workspace_bytes,
+)
+from .pages import (  # noqa: F401
+    PagePool,
+    fattn_pages_alloc,
+    fattn_pages_compact,
+    fattn_pages_extend,
+    fattn_pages_fork,
+    fattn_pages_free,
+    fattn_pages_workspace_bytes,
+)
+from .rope import fattn_rope, fattn_rope_bwd  # noqa: F401

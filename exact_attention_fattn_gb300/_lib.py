@@ -20,6 +20,7 @@ FATTN_ERR_TIMEOUT = 4
 FATTN_ERR_TOO_LARGE = 5
 FATTN_ERR_DEBUG_CHECK = 6
 FATTN_ERR_BAD_INDEX = 7
+FATTN_ERR_NO_PAGES = 8
 NOALLOC_SCRATCH_BYTES = 64 * 1024 * 1024
 
 _c_int, _c_float, _c_size, _vp = ctypes.c_int, ctypes.c_float, ctypes.c_size_t, ctypes.c_void_p
@@ -34,7 +35,29 @@ class CacheStruct(ctypes.Structure):
                 ("d", _c_int)]
 
 
+class LatentCacheStruct(ctypes.Structure):
+    """fattn_latent_cache of include/fattn.h."""
+
+    _fields_ = [("data", _vp), ("page_stride", _c_ll), ("pages", _c_int), ("page", _c_int), ("rank", _c_int)]
+
+
+class PagePoolStruct(ctypes.Structure):
+    """fattn_page_pool of include/fattn.h."""
+
+    _fields_ = [("refs", _vp), ("pages", _c_int), ("page", _c_int)]
+
+
+class PlaneStruct(ctypes.Structure):
+    """fattn_plane of include/fattn.h."""
+
+    _fields_ = [("base", _vp), ("stride", _c_ll), ("bytes", _c_ll)]
+
+
 _cache_p = ctypes.POINTER(CacheStruct)
+_latent_p = ctypes.POINTER(LatentCacheStruct)
+_pool_p = ctypes.POINTER(PagePoolStruct)
+_plane_p = ctypes.POINTER(PlaneStruct)
+_ll_p = ctypes.POINTER(_c_ll)
 
 # name -> (restype, argtypes); the order of argtypes follows include/fattn.h
 SIGNATURES = {
@@ -73,6 +96,18 @@ SIGNATURES = {
     "fattn_cache_select_workspace_bytes": (_c_size, [_c_int, _c_int, _c_int]),
     "fattn_cache_select": (_c_int, [_cache_p, _vp, _c_ll, _vp, _vp, _vp, _vp, _c_int, _c_int,
                                     _c_int, _vp, _c_size, _c_int, _c_int, _c_int, _c_int, _vp]),
+    "fattn_rope": (_c_int, [_vp, _ll_p, _vp, _ll_p, _vp, _c_int, _c_int, _c_int, _c_int, _vp, _c_ll, _c_int, _c_int,
+                            _c_int, _c_int, _vp]),
+    "fattn_latent_append": (_c_int, [_latent_p, _vp, _c_ll, _vp, _c_ll, _vp, _c_ll, _c_ll, _vp, _c_int, _vp, _c_int,
+                                     _c_int, _vp, _vp, _vp, _c_int, _c_int, _c_int, _vp]),
+    "fattn_latent_fwd_workspace_bytes": (_c_size, [_c_int, _c_int, _c_int, _c_int]),
+    "fattn_latent_fwd": (_c_int, [_latent_p, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _c_size, _c_int, _c_int, _c_int, _c_int,
+                                  _c_int, _c_float, _vp]),
+    "fattn_pages_fork": (_c_int, [_pool_p, _vp, _vp, _vp, _vp, _c_int, _c_int, _c_int, _vp]),
+    "fattn_pages_workspace_bytes": (_c_size, [_c_int, _c_int]),
+    "fattn_pages_extend": (_c_int, [_pool_p, _plane_p, _c_int, _vp, _vp, _vp, _vp, _c_size, _c_int, _c_int, _vp]),
+    "fattn_pages_free": (_c_int, [_pool_p, _vp, _vp, _vp, _c_int, _c_int, _c_int, _vp]),
+    "fattn_pages_compact": (_c_int, [_pool_p, _plane_p, _c_int, _vp, _vp, _vp, _c_size, _c_int, _c_int, _vp]),
     "fattn_check_status": (_c_int, [_vp]),
     "fattn_status_string": (ctypes.c_char_p, [_c_int]),
     "fattn_set_wait_budget": (None, [ctypes.c_longlong]),

@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import math
 from typing import NamedTuple, Optional
 
 import torch
@@ -43,15 +44,31 @@ def fattn_cache_alloc(pages: int, kv_heads: int, d: int, page: int = 64, device=
     return Fp8Cache(k, v, ks, vs, b)
 
 
-def fattn_rope_table(positions: int, rope_dim: int, theta: float = 10000.0,
-                     device="cuda") -> torch.Tensor:
+def fattn_rope_table(positions: int, rope_dim: int, theta: float = 10000.0, device="cuda", factor: float = 1.0,
+                     original: int = 0, ramp: tuple = (1.0, 32.0), magnitude: float | None = None) -> torch.Tensor:
     """fp32 [positions, rope_dim]: the cosines, then the sines, of the angles
-    p * theta**(-2 i / rope_dim); taken in 64 bits, for far positions."""
+    p * theta**(-2 i / rope_dim); taken in 64 bits, for far positions.
+
+    For contexts ``factor`` times as long as the model was trained on, angles
+    are divided by the factor: all of them (``original`` 0), or, with
+    ``original`` the trained length, those that turn less than ramp[0] times in
+    it, while those that turn ramp[1] times or more stay and those between go
+    over linearly; the table is then multiplied by ``magnitude`` (by default
+    0.1 ln(factor) + 1), which scales the scores by its square."""
     if positions < 1 or rope_dim < 16 or rope_dim % 16:
         raise ValueError("rope_dim must be a multiple of 16, and there must be a position")
+    if not (factor >= 1.0 and math.isfinite(factor)) or original < 0 or not 0 <= ramp[0] < ramp[1]:
+        raise ValueError("need a factor of 1 or more, original >= 0 and 0 <= ramp[0] < ramp[1]")
     inv = theta ** (-torch.arange(0, rope_dim, 2, dtype=torch.float64, device=device) / rope_dim)
+    if original:
+        keep = ((original * inv / (2 * math.pi) - ramp[0]) / (ramp[1] - ramp[0])).clamp(0.0, 1.0)
+        inv = inv * (keep + (1.0 - keep) / factor)
+        if magnitude is None:
+            magnitude = 0.1 * math.log(factor) + 1.0
+    else:
+        inv = inv / factor
     ang = torch.arange(positions, dtype=torch.float64, device=device)[:, None] * inv
-    return torch.cat([ang.cos(), ang.sin()], dim=1).float()
+    return (torch.cat([ang.cos(), ang.sin()], dim=1) * (1.0 if magnitude is None else magnitude)).float()
 
 
 # The functions below run once per layer and token, where a call's latency is

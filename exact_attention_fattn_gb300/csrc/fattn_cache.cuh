@@ -16,6 +16,8 @@ enum CacheSite : unsigned int {
   kSitePage = 402,       // a page number outside the cache
   kSitePosition = 403,   // a new token before position 0 or past the rotation table
   kSiteSelected = 404,   // a selected page outside the page table
+  kSiteRows = 405,       // a sequence that cannot be forked or freed
+  kSiteRefs = 406,       // a page freed more often than it was taken, or no free page left
 };
 
 __device__ __forceinline__ void record_bad_index(DeviceStatus* st, unsigned int site) {

@@ -203,6 +203,61 @@ cudaError_t launch_cache_chunk(int d, const CUtensorMap& tk, const CUtensorMap& 
 // Joins the units of `rows` rows that CTAs of either kernel shared.
 cudaError_t launch_cache_join(int d, int rows, const CacheAttnArgs& a, cudaStream_t stream);
 
+// ------------------------------------------------------------------ paged latent cache
+
+constexpr int kLatentRope = 64;      // columns of the rotated key part
+
+struct LatentAppendArgs {
+  CacheSeqs s;
+  uint16_t* data;             // bf16 [pages, page, rank + 64], pages page_stride elements apart
+  long long page_stride;
+  int pages, page_shift, rank;
+  const uint16_t* latent;     // bf16 rows of rank and of 64 columns
+  const uint16_t* k_rope;
+  long long latent_row, k_row;
+  const uint16_t* q_rope;     // bf16 [T, Hq, 64], or nullptr
+  long long qr_row, qr_head;
+  uint16_t* q;                // bf16 [T, Hq, rank + 64]: its last 64 columns are written
+  int Hq;
+  const float* rope;          // [rope_len, 64] or nullptr
+  int rope_len, interleaved;
+  DeviceStatus* status;
+};
+
+cudaError_t launch_latent_append(const LatentAppendArgs& a, cudaStream_t stream);
+
+struct LatentAttnArgs {
+  CacheSeqs s;
+  uint16_t* o;                // bf16 [T, Hq, rank]
+  float* lse;                 // [T, Hq]
+  int pages, page_shift, Hq, causal;
+  float scale_log2;
+  int span, shares;           // row blocks that work side by side, and their groups; span * shares CTAs
+  float* part_o;              // workspace: partial outputs of the units that CTAs share
+  float2* part_ml;
+  int4* rec;
+  DeviceStatus* status;
+  long long wait_budget;
+};
+
+constexpr int kLatentKeys = 64;      // keys of a tile
+constexpr int kLatentUnitCost = 2;   // tiles that a unit counts beyond its own
+
+// Rows of a unit for calls of `rows` rows an average sequence.
+constexpr int latent_rows(long long rows) { return rows <= 16 ? 16 : (rows <= 32 ? 32 : 64); }
+
+// rows: 16, 32 or 64 rows a unit; rank: 256 or 512.  tk: 3-D bf16 view {rank + 64, page,
+// pages} of the cache, boxes of 64 columns and min(page, 64) rows; tq: 2-D bf16
+// view {rank + 64, T * Hq} of the queries, boxes of 64 columns and `rows` rows; both
+// with a 128-byte swizzle.
+cudaError_t launch_latent_attn(int rows, int rank, const CUtensorMap& tk, const CUtensorMap& tq,
+                               const LatentAttnArgs& a, cudaStream_t stream);
+
+// Tensor map of bf16 rows: `rank` dimensions (2 or 3) of the given extents, strides of
+// all but the first in elements, boxes {64, box_rows, 1}.  Returns a fattn_status.
+int make_rows_map_bf16(CUtensorMap* m, const void* ptr, int dims, const long long* extents, const long long* strides,
+                       int box_rows);
+
 // Per-device state for entry points outside fattn_api.cu: checks the device,
 // gives the status word and the wait budget.  Returns a fattn_status.
 int call_setup(DeviceStatus** status, long long* wait_budget);

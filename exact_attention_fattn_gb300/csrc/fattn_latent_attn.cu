@@ -1,0 +1,885 @@
+// Attention over the paged latent cache: one row of rank + 64 columns a token is
+// its key for every query head, and the row's first rank columns are its value
+// (the absorbed form: queries come multiplied with the keys' up-projection, and
+// what is returned is still to be multiplied with the values').
+//
+//   S^T = K Q^T      [64 keys x N rows], rank + 64 columns summed
+//   O^T += V^T P^T   [rank x N rows], 128 columns of V at a time
+//
+// Rows are N = 16, 32 or 64 (token, head) pairs of a sequence, and they are the
+// products' N, not their M: with M = 128 rows the accumulator of 512 columns would
+// fill tensor memory, and so would Q, 147 KB, shared memory; with 64 rows as M
+// tcgen05 runs at half its rate.  So keys (64) are the first product's M and V's
+// columns (128) the second's, and both read the same tile of the cache, K-major as
+// K and MN-major as V^T.  A tile stays in shared memory between the two.  P^T goes
+// through shared memory, K-major (stmatrix, transposed).
+//
+// Softmax: tensor memory gives a warp 16 keys of all rows (M = 64 uses 16 lanes of
+// each quarter), so a thread has two keys of N / 4 rows, whose references m
+// and sums l it keeps in registers.  A row's reference moves only when a score
+// passes it by more than 2^8; whether one does is one vote of the four warps, so
+// that most tiles need no maximum over keys at all.  P is rounded to bf16 (half a
+// step: 2^-8 of a probability), as V is; scores, sums, references and accumulators
+// are fp32.
+//
+// Work split: the key tiles of all units, in order, are dealt in equal contiguous
+// shares; a unit is a group of `span` row blocks of one sequence, and a share is
+// worked on by as many CTAs side by side, one a row block, so that the group's
+// keys come out of DRAM once.  Units that shares split are joined in a second
+// kernel, in order.
+//
+// Warps: 0-3 softmax and results, 4 tensor memory and MMA issue, 5 loads, 6 the
+// walk over the share (it publishes one segment after the other), 7 idle.
+// TMEM: S at N (tile & 1), O^T at 2 N + N block.
+#include <float.h>
+
+#include "fattn_cache.cuh"
+
+namespace fattn {
+
+namespace {
+
+constexpr int kKeys = kLatentKeys;
+constexpr int kThreads = 256;
+constexpr int kMmaWarp = 4;
+constexpr int kLoadWarp = 5;
+constexpr int kWalkWarp = 6;
+constexpr int kSegs = 4;
+constexpr int kSegReaders = 6;
+constexpr float kLn2 = 0.69314718055994530942f;
+constexpr float kTau = 8.f;
+constexpr int kSmemMax = 232448;
+constexpr int kValid = 8;             // tiles whose masks are kept; more than the ring holds
+
+template <int N, int R>
+struct Cfg {
+  static constexpr int kChunks = R / 64 + 1;         // 64-column parts of a query; the rotated one first
+  static constexpr int kPairs = R / 128;             // 128-column parts of a cached row
+  static constexpr int kQChunk = N * 128;
+  static constexpr int kRopeTile = kKeys * 128;      // 64 columns of a tile
+  static constexpr int kPairTile = 2 * kRopeTile;
+  static constexpr int kQOff = 0;
+  static constexpr int kPOff = kChunks * kQChunk;
+  static constexpr int kRingOff = kPOff + kQChunk;
+  static constexpr int kMisc = 2304;
+  static constexpr int kUnits = (kSmemMax - kRingOff - kMisc) / kRopeTile;
+  // Two tiles at least: the scores of one are computed before the values of the
+  // one before are done with.
+#ifdef FATTN_LATENT_MIN_RING
+  static constexpr int kRopes = 2;
+  static constexpr int kRing = 2 * kPairs;
+#else
+  static constexpr int kRopes0 = (kUnits + 2 * kPairs) / (2 * kPairs + 1);
+  static constexpr int kRopes = kRopes0 + ((kUnits - kRopes0) & 1);
+  static constexpr int kRing = (kUnits - kRopes) / 2;
+#endif
+  static_assert(kRopes >= 2 && kRing >= 2 * kPairs && kRopes + 2 * kRing <= kUnits, "ring");
+  static_assert(kRing / kPairs + 2 <= kValid, "masks");
+  static constexpr int kRopeOff = kRingOff + kRing * kPairTile;
+  static constexpr int kBarOff = kRopeOff + kRopes * kRopeTile;
+  // pair_full[] pair_empty[] rope_full[] rope_empty[] q_full q_empty s_full[2] p_full
+  // pv_done mma_done seg_full[] seg_empty[]
+  static constexpr int kNumBars = 2 * kRing + 2 * kRopes + 7 + 2 * kSegs;
+  static constexpr int kMiscOff = kBarOff + kNumBars * 8;       // tmem, abort, start of the share
+  static constexpr int kValidOff = kMiscOff + 32;
+  static constexpr int kSegOff = (kValidOff + 4 * kValid + 15) / 16 * 16;
+  static constexpr int kXOff = kSegOff + kSegs * 48;            // [4][N] float
+  static constexpr int kAlphaOff = kXOff + 16 * N;              // [N] float
+  static constexpr int kSmem = kAlphaOff + 4 * N;
+  static_assert(kSmem <= kSmemMax, "shared memory");
+  __device__ static constexpr uint32_t col_s(uint32_t buf) { return N * buf; }
+  __device__ static constexpr uint32_t col_o(int pair) { return 2 * N + N * pair; }
+  static_assert(2 * N + N * kPairs <= 512, "tensor memory");
+};
+
+// ------------------------------------------------------------------ PTX
+
+__device__ __forceinline__ uint32_t elect_lane() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\tselp.u32 %0, 1, 0, e;\n\t}" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void mma_lead(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                         uint32_t accumulate, uint32_t lead) {
+  asm volatile(
+      "{\n\t.reg .pred p, e;\n\tsetp.ne.b32 e, %5, 0;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(lead)
+      : "memory");
+}
+__device__ __forceinline__ void commit_lead(uint32_t bar, uint32_t lead) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\tsetp.ne.b32 e, %1, 0;\n\t"
+      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar),
+      "r"(lead)
+      : "memory");
+}
+__device__ __forceinline__ void tma_load_2d(uint32_t dst, const void* tmap, uint32_t bar, int c0, int c1) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(tmap)), "r"(bar), "r"(c0), "r"(c1)
+      : "memory");
+}
+
+// 16 lanes x N columns: thread t gets, for each 8 columns i, r[4 i], r[4 i + 1] of
+// lane t / 4, columns 8 i + 2 (t % 4) and the next, and r[4 i + 2], r[4 i + 3] of
+// lane t / 4 + 8.  Valid after the wait.
+__device__ __forceinline__ void tmem_ld_rows(uint32_t taddr, uint32_t (&r)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(taddr)
+               : "memory");
+}
+__device__ __forceinline__ void tmem_ld_rows(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, "
+      "%14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_ld_rows(uint32_t taddr, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x8.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+        "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+        "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr)
+      : "memory");
+}
+// 32 lanes x 16 columns, a lane's in its thread.
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, "
+      "%14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+}
+// Waits for this thread's loads; the registers pass through, so that no use of
+// them is scheduled before.
+template <int K>
+__device__ __forceinline__ void tmem_ld_wait(uint32_t (&r)[K]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < K; ++i) asm volatile("" : "+r"(r[i])::"memory");
+}
+// Four 8 x 8 matrices of 16-bit elements, each transposed on its way.
+__device__ __forceinline__ void stmatrix_x4_trans(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b),
+               "r"(c), "r"(d)
+               : "memory");
+}
+// Barrier of the four softmax warps; true if `x` is in any thread.
+__device__ __forceinline__ bool softmax_any(bool x) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %1, 0;\n\t"
+      "barrier.cta.red.or.pred q, 1, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(static_cast<uint32_t>(x))
+      : "memory");
+  return r != 0;
+}
+__device__ __forceinline__ void softmax_sync() { asm volatile("barrier.cta.sync 1, 128;" ::: "memory"); }
+
+// ------------------------------------------------------------------ schedule
+
+// A sequence's groups of `rows` rows in order, with the key tiles that each sees
+// (the quotient of its last row and the heads is carried along).
+struct Groups {
+  long long rows, all;       // rows of a group and of the sequence
+  long long end;             // row behind the current group
+  int len, n, Hq, causal;
+  __device__ __forceinline__ Groups(const LatentAttnArgs& a, const SeqInfo& q, int group_rows, long long first = 0)
+      : rows(group_rows), all(static_cast<long long>(q.n) * a.Hq), end((first + 1) * group_rows), len(q.len), n(q.n),
+        Hq(a.Hq), causal(a.causal) {}
+  __device__ __forceinline__ bool live() const { return end - rows < all; }
+  __device__ __forceinline__ void next() { end += rows; }
+  // At least one, so that rows that see nothing are written, too.
+  __device__ __forceinline__ int tiles() const {
+    int keys = len;
+    if (causal) {
+      const unsigned int e = static_cast<unsigned int>(min(end, all));   // T * Hq < 2^31
+      keys = len - n + static_cast<int>((e + Hq - 1) / Hq);
+    }
+    return max(1, (keys + kKeys - 1) / kKeys);
+  }
+};
+
+// One share's part of a unit: key tiles [a, e) of nt for row group rg of a sequence.
+struct __align__(16) Seg {
+  int b, rg, r0, n;
+  int len, flags, a, e;
+  int nt, pad0, pad1, pad2;
+  static constexpr int kStarts = 1, kEnds = 2, kLast = 8;
+  __device__ __forceinline__ bool whole() const { return (flags & 3) == 3; }
+};
+static_assert(sizeof(Seg) == 48, "ring slot");
+
+// Walks a share.
+struct Walker {
+  const LatentAttnArgs& a;
+  int group_rows;
+  long long left;           // tiles (and what units count beyond) still to walk
+  int b, rg, at, nt;
+  SeqInfo q;
+  __device__ __forceinline__ long long all_rows() const { return static_cast<long long>(q.n) * a.Hq; }
+  __device__ __forceinline__ Walker(const LatentAttnArgs& args, int rows, int first_b, long long rem, long long todo)
+      : a(args), group_rows(rows), left(todo), b(first_b), rg(0), at(0), nt(0) {
+    if (left <= 0) return;
+    q = seq_info(a.s, b, a.page_shift);
+    Groups g(a, q, group_rows);
+    nt = g.tiles();
+    while (rem >= nt + kLatentUnitCost && g.live()) {
+      rem -= nt + kLatentUnitCost;
+      ++rg;
+      g.next();
+      nt = g.tiles();
+    }
+    at = static_cast<int>(rem);
+  }
+  __device__ __forceinline__ bool next(Seg& s) {
+    if (left <= 0) return false;
+    if (at >= nt) {                     // tiles that stand for the unit itself
+      left -= nt + kLatentUnitCost - at;
+      at = 0;
+      if (left <= 0) return false;
+      if (static_cast<long long>(++rg) * group_rows >= all_rows()) {
+        rg = 0;
+        // work is left, so a sequence with rows follows
+        do {
+          if (++b >= a.s.B) return false;
+          q = seq_info(a.s, b, a.page_shift);
+        } while (q.n == 0);
+      }
+      nt = Groups(a, q, group_rows, rg).tiles();
+    }
+    s.b = b;
+    s.rg = rg;
+    s.r0 = q.r0;
+    s.n = q.n;
+    s.len = q.len;
+    s.a = at;
+    s.e = static_cast<int>(min(static_cast<long long>(nt), at + left));
+    s.nt = nt;
+    s.flags = (at == 0 ? Seg::kStarts : 0) | (s.e == nt ? Seg::kEnds : 0);
+    left -= s.e - s.a;
+    at = s.e;
+    return true;
+  }
+};
+
+// ------------------------------------------------------------------ kernel
+
+template <int N, int R>
+__global__ void __launch_bounds__(kThreads, 1)
+    latent_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_q,
+                  const __grid_constant__ LatentAttnArgs args) {
+  using C = Cfg<N, R>;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const uint32_t sbase = smem_u32(smem);
+  const uint32_t bar0 = sbase + C::kBarOff;
+  auto pair_full = [&](uint32_t s) { return bar0 + 8u * s; };
+  auto pair_empty = [&](uint32_t s) { return bar0 + 8u * (C::kRing + s); };
+  auto rope_full = [&](uint32_t s) { return bar0 + 8u * (2 * C::kRing + s); };
+  auto rope_empty = [&](uint32_t s) { return bar0 + 8u * (2 * C::kRing + C::kRopes + s); };
+  const uint32_t rest = bar0 + 16u * (C::kRing + C::kRopes);
+  const uint32_t q_full = rest, q_empty = rest + 8u, p_full = rest + 32u, pv_done = rest + 40u, mma_done = rest + 48u;
+  auto s_full = [&](uint32_t buf) { return rest + 16u + 8u * buf; };
+  auto seg_full = [&](uint32_t i) { return rest + 56u + 8u * (i % kSegs); };
+  auto seg_empty = [&](uint32_t i) { return rest + 56u + 8u * (kSegs + i % kSegs); };
+  uint32_t* misc = reinterpret_cast<uint32_t*>(smem + C::kMiscOff);
+  volatile uint32_t* valid = reinterpret_cast<volatile uint32_t*>(smem + C::kValidOff);
+  auto seg_at = [&](uint32_t i) -> const Seg& {
+    return *reinterpret_cast<const Seg*>(smem + C::kSegOff + 48u * (i % kSegs));
+  };
+  float* xs = reinterpret_cast<float*>(smem + C::kXOff);          // [4][N]
+  float* alphas = reinterpret_cast<float*>(smem + C::kAlphaOff);   // [N]
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int share = blockIdx.x / args.span, block = blockIdx.x - share * args.span;
+  const int G = args.shares, group_rows = args.span * N;
+  if (!dcheck((sbase & 1023u) == 0u && C::kSmem <= static_cast<int>(dynamic_smem_bytes()) && share < G, args.status, 691))
+    return;
+
+  if (tid == 0) {
+    for (int s = 0; s < C::kRing; ++s) {
+      mbar_init(pair_full(s), 1);
+      mbar_init(pair_empty(s), 1);
+    }
+    for (int s = 0; s < C::kRopes; ++s) {
+      mbar_init(rope_full(s), 1);
+      mbar_init(rope_empty(s), 1);
+    }
+    mbar_init(q_full, 1);
+    mbar_init(q_empty, 1);
+    mbar_init(s_full(0), 1);
+    mbar_init(s_full(1), 1);
+    mbar_init(p_full, 128);
+    mbar_init(pv_done, 1);
+    mbar_init(mma_done, 1);
+    for (int i = 0; i < kSegs; ++i) {
+      mbar_init(seg_full(i), 1);
+      mbar_init(seg_empty(i), kSegReaders);
+    }
+    misc[1] = 0u;
+    fence_barrier_init();
+  }
+  if (warp == kMmaWarp) {
+    tmem_alloc(smem_u32(&misc[0]), 512);
+    tmem_relinquish();
+  }
+  if (warp == kLoadWarp && lane == 0) {
+    tma_prefetch_desc(&tm_k);
+    tma_prefetch_desc(&tm_q);
+  }
+  // ---- the share: where its first tile lies.  The scan's scratch is in the masks'
+  // and references' place, which nothing uses yet.
+  long long W, j0, j1;
+  {
+    long long* wtot = reinterpret_cast<long long*>(xs);
+    const int per = (args.s.B + kThreads - 1) / kThreads;
+    const int b0 = min(args.s.B, tid * per), b1 = min(args.s.B, b0 + per);
+    auto weight = [&](int b, bool report) -> long long {
+      const SeqInfo q = seq_info(args.s, b, args.page_shift);
+      if (report && !q.ok && blockIdx.x == 0) record_bad_index(args.status, kSiteSeqStart);
+      long long w = 0;
+      for (Groups g(args, q, group_rows); g.live(); g.next()) w += g.tiles() + kLatentUnitCost;
+      return w;
+    };
+    long long sum = 0;
+    for (int b = b0; b < b1; ++b) sum += weight(b, true);
+    long long incl = sum;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const long long t = __shfl_up_sync(0xffffffffu, incl, off);
+      if (lane >= off) incl += t;
+    }
+    if (lane == 31) wtot[warp] = incl;
+    __syncthreads();
+    long long at = incl - sum, all = 0;
+    for (int w = 0; w < kThreads / 32; ++w) {
+      if (w < warp) at += wtot[w];
+      all += wtot[w];
+    }
+    W = total_of(all, args.status);
+    j0 = cta_first(W, G, share);
+    j1 = cta_first(W, G, share + 1);
+    if (j0 < j1 && at <= j0 && j0 < at + sum) {
+      int b = b0;
+      for (long long w; b + 1 < b1 && at + (w = weight(b, false)) <= j0; ++b) at += w;
+      misc[4] = static_cast<uint32_t>(b);
+      misc[5] = static_cast<uint32_t>(j0 - at);    // W < 2^31
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = misc[0];
+  const Waits wc{args.wait_budget, reinterpret_cast<volatile uint32_t*>(&misc[1])};
+  auto wait_seg = [&](uint32_t i) { return wait_bar_warp(seg_full(i), (i / kSegs) & 1, wc, kWaitSegment); };
+  auto done_seg = [&](uint32_t i) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(seg_empty(i));
+  };
+  // First row of this CTA's block in the sequence's n * Hq (T * Hq < 2^31, and the
+  // blocks' padding below 2^10).
+  auto first_row = [&](const Seg& s) { return static_cast<long long>(s.rg) * group_rows + block * N; };
+  auto rows_of = [&](const Seg& s) { return static_cast<long long>(s.n) * args.Hq; };
+
+  if (warp < 4) {
+    // ================================================================ softmax
+    constexpr int NC = N / 4;             // rows of a thread, two keys each
+    const float c = args.scale_log2;
+    const int key_in = 16 * warp + (lane >> 2);
+    const uint32_t lane_off = static_cast<uint32_t>(warp * 32) << 16;
+    uint32_t tiles = 0;                   // of this CTA so far: S and P V in turn
+    // All decisions that a barrier follows are the same in the four warps; a wait
+    // that ran out makes the next vote end the loop for all.
+    bool fail = false;
+    for (uint32_t si = 0;; ++si) {
+      fail |= !wait_seg(si);
+      if (softmax_any(fail)) break;
+      const Seg s = seg_at(si);
+      done_seg(si);
+      if (s.flags & Seg::kLast) break;
+      const long long row0 = first_row(s), rows = rows_of(s);
+      if (row0 >= rows) continue;
+      const int live = static_cast<int>(min(static_cast<long long>(N), rows - row0));
+      // Keys that a row sees.  Rows behind the block's last see all; nothing of theirs
+      // is stored, and a row of S, P and O depends on its own query only.
+      auto lim_of = [&](int col) {
+        if (!args.causal || col >= live) return s.len;
+        return max(0, min(s.len, s.len - s.n + static_cast<int>(static_cast<unsigned int>(row0 + col) / args.Hq) + 1));
+      };
+      const int lim_min = lim_of(0);      // rows see no fewer keys than the first
+      float m[NC], l[NC];
+#pragma unroll
+      for (int i = 0; i < NC; ++i) {
+        m[i] = -FLT_MAX;
+        l[i] = 0.f;
+      }
+      bool holes = false;
+      for (int j = s.a; j < s.e; ++j, ++tiles) {
+        const int kv0 = j * kKeys;
+        const uint32_t pair0 = tiles * C::kPairs;
+        uint32_t x[N / 2];
+        fail |= !wait_bar_warp(s_full(tiles & 1), (tiles >> 1) & 1, wc, kWaitSFull);
+        // The masks came with the tile; its slots are not used again before P V.
+        fail |= !wait_bar_warp(pair_full(pair0 % C::kRing), (pair0 / C::kRing) & 1, wc, kWaitKvFull);
+        tc_fence_after();
+        tmem_ld_rows(tmem + lane_off + C::col_s(tiles & 1), x);
+        const uint32_t mask = valid[tiles % kValid];
+        tmem_ld_wait(x);
+        const bool edge = mask != 3u || kv0 + kKeys > s.len;
+        holes |= (((kv0 < s.len ? 1u : 0u) | (kv0 + 32 < s.len ? 2u : 0u)) & ~mask) != 0u;
+        if (edge || kv0 + kKeys > lim_min) {
+          const bool there0 = mask >> (key_in >> 5) & 1u, there1 = mask >> ((key_in + 8) >> 5) & 1u;
+#pragma unroll
+          for (int i = 0; i < NC; ++i) {
+            const int lim = lim_of(8 * (i >> 1) + 2 * (lane & 3) + (i & 1)) - kv0;
+            uint32_t& x0 = x[4 * (i >> 1) + (i & 1)];
+            uint32_t& x1 = x[4 * (i >> 1) + 2 + (i & 1)];
+            if (!there0 || key_in >= lim) x0 = __float_as_uint(-INFINITY);
+            if (!there1 || key_in + 8 >= lim) x1 = __float_as_uint(-INFINITY);
+          }
+        }
+        auto s0 = [&](int i) { return __uint_as_float(x[4 * (i >> 1) + (i & 1)]); };
+        auto s1 = [&](int i) { return __uint_as_float(x[4 * (i >> 1) + 2 + (i & 1)]); };
+        float top = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < NC; ++i) top = fmaxf(top, fmaf(fmaxf(s0(i), s1(i)), c, -m[i]));
+        if (softmax_any(top > kTau || fail)) {
+          // ---- some row's reference moves
+          float mx[NC];
+#pragma unroll
+          for (int i = 0; i < NC; ++i) {
+            mx[i] = fmaxf(s0(i), s1(i)) * c;
+#pragma unroll
+            for (int off = 4; off < 32; off <<= 1) mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], off));
+            if (lane < 4) xs[warp * N + 8 * (i >> 1) + 2 * lane + (i & 1)] = mx[i];
+          }
+          if (j > s.a) fail |= !wait_bar_warp(pv_done, (tiles - 1) & 1, wc, kWaitMmaDone);
+          if (softmax_any(fail)) {
+            fail = true;
+            break;
+          }
+#pragma unroll
+          for (int i = 0; i < NC; ++i) {
+            const int col = 8 * (i >> 1) + 2 * (lane & 3) + (i & 1);
+            const float t = fmaxf(fmaxf(xs[col], xs[N + col]), fmaxf(xs[2 * N + col], xs[3 * N + col]));
+            const bool move = t > m[i] + kTau;
+            const float al = move ? ex2_approx(m[i] - t) : 1.f;
+            if (move) m[i] = t;
+            l[i] *= al;
+            if (warp == 0 && lane < 4) alphas[col] = al;
+          }
+          softmax_sync();
+          if (j > s.a) {
+            tc_fence_after();
+#pragma unroll 1
+            for (int p = 0; p < C::kPairs * N / 16; ++p) {
+              uint32_t o[16];
+              const uint32_t at = tmem + lane_off + C::col_o(0) + 16 * p;
+              tmem_ld16(at, o);
+              const float4* al = reinterpret_cast<const float4*>(alphas + (16 * p) % N);
+              tmem_ld_wait(o);
+#pragma unroll
+              for (int z = 0; z < 4; ++z) {
+                const float4 f = al[z];
+                o[4 * z] = __float_as_uint(__uint_as_float(o[4 * z]) * f.x);
+                o[4 * z + 1] = __float_as_uint(__uint_as_float(o[4 * z + 1]) * f.y);
+                o[4 * z + 2] = __float_as_uint(__uint_as_float(o[4 * z + 2]) * f.z);
+                o[4 * z + 3] = __float_as_uint(__uint_as_float(o[4 * z + 3]) * f.w);
+              }
+              tmem_st16(at, o);
+            }
+            tmem_st_wait();
+          }
+        }
+        // ---- probabilities, bf16 pairs of neighbouring rows
+        uint32_t pk[N / 4];
+#pragma unroll
+        for (int i = 0; i < NC; i += 2) {
+          const float p00 = ex2_approx(fmaf(s0(i), c, -m[i])), p01 = ex2_approx(fmaf(s0(i + 1), c, -m[i + 1]));
+          const float p10 = ex2_approx(fmaf(s1(i), c, -m[i])), p11 = ex2_approx(fmaf(s1(i + 1), c, -m[i + 1]));
+          pk[i] = pack_bf16x2(p00, p01);
+          pk[i + 1] = pack_bf16x2(p10, p11);
+          l[i] += p00 + p10;
+          l[i + 1] += p01 + p11;
+        }
+        if (tiles > 0) fail |= !wait_bar_warp(pv_done, (tiles - 1) & 1, wc, kWaitMmaDone);   // P is free
+#pragma unroll
+        for (int i = 0; i < N / 16; ++i) {
+          const int row = 16 * i + 8 * (lane >> 4) + (lane & 7), chunk = 2 * warp + (lane >> 3 & 1);
+          const uint32_t dst = sbase + C::kPOff + row * 128 + ((chunk ^ (lane & 7)) << 4);
+          if (dcheck(in_range(dst, 16, sbase + C::kPOff, sbase + C::kRingOff), args.status, 692))
+            stmatrix_x4_trans(dst, pk[4 * i], pk[4 * i + 1], pk[4 * i + 2], pk[4 * i + 3]);
+        }
+        if (edge) {
+          // Slots behind the end and pages that were not loaded hold anything, and zero
+          // times a NaN is a NaN.
+#pragma unroll 1
+          for (int id = tid; id < C::kPairs * 2 * kKeys * 8; id += 128) {
+            const int r = id >> 3 & (kKeys - 1), half = id >> 9;   // 8 pieces a row, 64 rows a half pair
+            if (kv0 + r < s.len && (mask >> (r >> 5) & 1u)) continue;
+            const uint32_t slot = (pair0 + (half >> 1)) % C::kRing;
+            const uint32_t dst = sbase + C::kRingOff + slot * C::kPairTile + (half & 1) * C::kRopeTile + r * 128 + (id & 7) * 16;
+            if (dcheck(in_range(dst, 16, sbase + C::kRingOff, sbase + C::kRopeOff), args.status, 693))
+              st_shared_v4(dst, 0u, 0u, 0u, 0u);
+          }
+        }
+        fence_proxy_async_smem();
+        tc_fence_before();
+        mbar_arrive(p_full);
+      }
+      // ---- results
+      fail |= !wait_bar_warp(pv_done, (tiles - 1) & 1, wc, kWaitOFull);
+#pragma unroll
+      for (int i = 0; i < NC; ++i) {
+#pragma unroll
+        for (int off = 4; off < 32; off <<= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], off);
+        const int col = 8 * (i >> 1) + 2 * (lane & 3) + (i & 1);
+        if (lane < 4) xs[warp * N + col] = l[i];
+        if (warp == 0 && lane < 4) alphas[col] = m[i];
+      }
+      if (softmax_any(fail)) break;
+      tc_fence_after();
+      const bool whole = s.whole();
+      const long long slot = 2ll * blockIdx.x + (s.flags & Seg::kStarts);
+      const long long out0 = static_cast<long long>(s.r0) * args.Hq + row0;
+      if (tid < N) {
+        float lt = (xs[tid] + xs[N + tid]) + (xs[2 * N + tid] + xs[3 * N + tid]);
+        const float mt = alphas[tid];
+        // All scores of keys that the row sees are -inf: its query holds an infinity.
+        if (lt == 0.f && !holes && lim_of(tid) > s.a * kKeys) lt = __int_as_float(0x7fffffff);
+        if (tid < live) {
+          if (whole) args.lse[out0 + tid] = lt == 0.f ? -INFINITY : (mt + log2f(lt)) * kLn2;
+          else args.part_ml[slot * N + tid] = make_float2(mt, lt);
+        }
+        alphas[tid] = lt == 0.f ? 0.f : 1.f / lt;
+      }
+      softmax_sync();
+#pragma unroll 1
+      for (int p = 0; p < C::kPairs * N / 16; ++p) {
+        const int pair = 16 * p / N, r0 = 16 * p % N;
+        if (r0 >= live) continue;
+        uint32_t o[16];
+        tmem_ld16(tmem + lane_off + C::col_o(0) + 16 * p, o);
+        tmem_ld_wait(o);
+        const int dim = 128 * pair + 32 * warp + lane;
+        if (whole) {
+          // Lanes hold neighbouring columns: two of them swap a row each, so that a
+          // store has two columns of one row.
+#pragma unroll
+          for (int z = 0; z < 16; z += 2) {
+            const float f0 = __uint_as_float(o[z]) * alphas[r0 + z], f1 = __uint_as_float(o[z + 1]) * alphas[r0 + z + 1];
+            const float got = __shfl_xor_sync(0xffffffffu, lane & 1 ? f0 : f1, 1);
+            const int row = r0 + z + (lane & 1);
+            if (row < live && dcheck(inside(out0 + row, 1, static_cast<long long>(args.s.T) * args.Hq), args.status, 694))
+              *reinterpret_cast<uint32_t*>(args.o + (out0 + row) * R + (dim & ~1)) =
+                  lane & 1 ? pack_bf16x2(got, f1) : pack_bf16x2(f0, got);
+          }
+        } else {
+          float* part = args.part_o + (slot * N + r0) * R + dim;
+#pragma unroll
+          for (int z = 0; z < 16; ++z)
+            if (r0 + z < live && dcheck(slot < 2ll * kSms, args.status, 695)) part[z * R] = __uint_as_float(o[z]);
+        }
+      }
+    }
+  } else if (warp == kMmaWarp) {
+    // ================================================================ MMA issue
+    const uint32_t lead = elect_lane();
+    constexpr uint32_t idesc_s = idesc_bf16_f32(kKeys, N, false, false);
+    constexpr uint32_t idesc_o = idesc_bf16_f32(128, N, true, false);
+    uint32_t tiles = 0, pvs = 0, q_count = 0;
+    // The bounds come through a shuffle, which tells the compiler that they are the
+    // same in every lane.
+    auto uniform = [](int v) { return __shfl_sync(0xffffffffu, v, 0); };
+    auto product4 = [&](uint32_t d, uint32_t a, uint32_t b, uint32_t acc) {   // 64 columns
+      const uint64_t da = sdesc_sw128(a, 16, 1024), db = sdesc_sw128(b, 16, 1024);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) mma_lead(d, da + 2 * k, db + 2 * k, idesc_s, k > 0 ? 1u : acc, lead);
+    };
+    auto scores = [&](bool last) -> bool {
+      const uint32_t d = tmem + C::col_s(tiles & 1), slot = tiles % C::kRopes;
+      if (!wait_bar_warp(rope_full(slot), (tiles / C::kRopes) & 1, wc, kWaitKvFull)) return false;
+      tc_fence_after();
+      product4(d, sbase + C::kRopeOff + slot * C::kRopeTile, sbase + C::kQOff, 0u);
+      commit_lead(rope_empty(slot), lead);
+#pragma unroll
+      for (int p = 0; p < C::kPairs; ++p) {
+        const uint32_t at = tiles * C::kPairs + p, ps = at % C::kRing;
+        if (!wait_bar_warp(pair_full(ps), (at / C::kRing) & 1, wc, kWaitKvFull)) return false;
+        const uint32_t k = sbase + C::kRingOff + ps * C::kPairTile, q = sbase + C::kQOff + (1 + 2 * p) * C::kQChunk;
+        product4(d, k, q, 1u);
+        product4(d, k + C::kRopeTile, q + C::kQChunk, 1u);
+      }
+      commit_lead(s_full(tiles & 1), lead);
+      if (last) commit_lead(q_empty, lead);
+      ++tiles;
+      return true;
+    };
+    auto values = [&](uint32_t acc) -> bool {
+      if (!wait_bar_warp(p_full, pvs & 1, wc, kWaitPFull)) return false;
+      tc_fence_after();
+      const uint64_t db = sdesc_sw128(sbase + C::kPOff, 16, 1024);
+#pragma unroll
+      for (int p = 0; p < C::kPairs; ++p) {
+        const uint32_t ps = (pvs * C::kPairs + p) % C::kRing;
+        const uint64_t da = sdesc_sw128(sbase + C::kRingOff + ps * C::kPairTile, C::kRopeTile, 1024);
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          mma_lead(tmem + C::col_o(p), da + ((k * 2048) >> 4), db + 2 * k, idesc_o, k > 0 ? 1u : acc, lead);
+        commit_lead(pair_empty(ps), lead);
+      }
+      commit_lead(pv_done, lead);
+      ++pvs;
+      return true;
+    };
+    auto run = [&](const int n) -> bool {
+      if (!wait_bar_warp(q_full, q_count++ & 1, wc, kWaitQFull)) return false;
+      tc_fence_after();
+      for (int i = 0; i < n; ++i) {
+        if (!scores(i + 1 == n)) return false;
+        if (i > 0 && !values(i > 1 ? 1u : 0u)) return false;
+      }
+      return values(n > 1 ? 1u : 0u);
+    };
+    for (uint32_t si = 0; wait_seg(si); ++si) {
+      const Seg& s = seg_at(si);
+      const int flags = uniform(s.flags), n = uniform(s.e - s.a);
+      const bool mine = uniform(first_row(s) < rows_of(s) ? 1 : 0) != 0;
+      done_seg(si);
+      if (flags & Seg::kLast) break;
+      if (mine && !run(n)) break;
+    }
+    // No MMA may still be running when TMEM is released.
+    commit_lead(mma_done, lead);
+    mbar_wait_drain(mma_done, 0);
+    __syncwarp();
+  } else if (warp == kLoadWarp) {
+    // ================================================================ TMA producer
+    uint32_t tiles = 0, q_count = 0;
+    uint32_t ropes = 0, pairs = 0;        // asked for so far
+    const int page = 1 << args.page_shift, box = min(page, kKeys), boxes = kKeys / box;
+    bool ok = true;
+    for (uint32_t si = 0; ok && wait_seg(si); ++si) {
+      const Seg s = seg_at(si);
+      done_seg(si);
+      if (s.flags & Seg::kLast) break;
+      const long long row0 = first_row(s);
+      if (row0 >= rows_of(s)) continue;
+      if (q_count > 0 && !wait_bar_warp(q_empty, (q_count - 1) & 1, wc, kWaitQFull)) break;
+      ++q_count;
+      if (lane == 0) {
+        mbar_arrive_expect_tx(q_full, C::kChunks * C::kQChunk);
+        const int row = static_cast<int>(static_cast<long long>(s.r0) * args.Hq + row0);
+#pragma unroll 1
+        for (int i = 0; i < C::kChunks; ++i)
+          tma_load_2d(sbase + C::kQOff + i * C::kQChunk, &tm_q, q_full, i == 0 ? R : 64 * (i - 1), row);
+      }
+      __syncwarp();
+      for (int j = s.a; j < s.e; ++j, ++tiles) {
+        // The tile's pages: one, or two of 32 tokens.
+        int pid[2] = {-1, -1};
+        uint32_t mask = 0u;
+        for (int i = 0; i < boxes; ++i) {
+          const int t = j * kKeys + i * box;
+          if (t >= s.len) break;
+          const int p = __ldg(args.s.table + static_cast<long long>(s.b) * args.s.max_pages + (t >> args.page_shift));
+          if (p < 0 || p >= args.pages) {
+            if (lane == 0) record_bad_index(args.status, kSitePage);
+          } else {
+            pid[i] = p;
+            mask |= boxes == 1 ? 3u : 1u << i;
+          }
+        }
+        const int row = (j * kKeys) & (page - 1);
+        const uint32_t part = static_cast<uint32_t>(box) * 128u;
+        const uint32_t bytes = (pid[0] >= 0 ? part : 0u) + (pid[1] >= 0 ? part : 0u);
+        auto load64 = [&](uint32_t dst, uint32_t bar, int col) {
+          if (pid[0] >= 0) tma_load_3d(dst, &tm_k, bar, col, row, pid[0]);
+          if (pid[1] >= 0) tma_load_3d(dst + part, &tm_k, bar, col, row, pid[1]);
+        };
+        const uint32_t rs = tiles % C::kRopes;
+        if (tiles >= C::kRopes && !wait_bar_warp(rope_empty(rs), (tiles / C::kRopes - 1) & 1, wc, kWaitKvEmpty)) {
+          ok = false;
+          break;
+        }
+        if (lane == 0) {
+          mbar_arrive_expect_tx(rope_full(rs), bytes);
+          load64(sbase + C::kRopeOff + rs * C::kRopeTile, rope_full(rs), R);
+        }
+        ++ropes;
+        __syncwarp();
+        for (int p = 0; p < C::kPairs; ++p) {
+          const uint32_t at = tiles * C::kPairs + p, ps = at % C::kRing;
+          if (at >= C::kRing && !wait_bar_warp(pair_empty(ps), (at / C::kRing - 1) & 1, wc, kWaitKvEmpty)) {
+            ok = false;
+            break;
+          }
+          if (lane == 0) {
+            if (p == 0) valid[tiles % kValid] = mask;
+            const uint32_t dst = sbase + C::kRingOff + ps * C::kPairTile;
+            mbar_arrive_expect_tx(pair_full(ps), 2 * bytes);
+            load64(dst, pair_full(ps), 128 * p);
+            load64(dst + C::kRopeTile, pair_full(ps), 128 * p + 64);
+          }
+          ++pairs;
+          __syncwarp();
+        }
+        if (!ok) break;
+      }
+    }
+    // Every copy this warp started must have landed before the CTA exits.
+    for (uint32_t r = ropes > C::kRopes ? ropes - C::kRopes : 0; r < ropes; ++r)
+      mbar_wait_drain(rope_full(r % C::kRopes), (r / C::kRopes) & 1);
+    for (uint32_t r = pairs > C::kRing ? pairs - C::kRing : 0; r < pairs; ++r)
+      mbar_wait_drain(pair_full(r % C::kRing), (r / C::kRing) & 1);
+    if (q_count > 0) mbar_wait_drain(q_full, (q_count - 1) & 1);
+    __syncwarp();
+  } else if (warp == kWalkWarp) {
+    // ================================================================ schedule
+    Walker walk(args, group_rows, static_cast<int>(misc[4]), static_cast<long long>(misc[5]), j1 - j0);
+    Seg s{};
+    bool any = false;
+    for (uint32_t i = 0;; ++i) {
+      Seg x{};
+      const bool more = walk.next(x);
+      if (more) {
+        s = x;
+        any = true;
+      } else {
+        x.flags = Seg::kLast;
+      }
+      if (i >= kSegs && !wait_bar_warp(seg_empty(i), (i / kSegs - 1) & 1, wc, kWaitSegment)) {
+        any = false;
+        break;
+      }
+      if (lane == 0) {
+        const_cast<Seg&>(seg_at(i)) = x;
+        mbar_arrive(seg_full(i));
+      }
+      __syncwarp();
+      if (!more) break;
+    }
+    if (lane == 0 && block == 0) {
+      // What is to be joined: the unit that this share starts and others go on with
+      // (its last one).
+      const bool shared_unit = any && (s.flags & (Seg::kStarts | Seg::kEnds)) == Seg::kStarts;
+      args.rec[2 * share] = shared_unit ? make_int4(s.r0, s.n, s.rg, 0) : make_int4(0, 0, 0, 0);
+      if (shared_unit)
+        args.rec[2 * share + 1] = make_int4(cta_of(W, G, j1 - (s.e - s.a) + s.nt - 1), static_cast<int>(W), 0, 0);
+    }
+    __syncwarp();
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  allow_child();
+  if (tid == 0) report_abort(misc[1], args.status);
+  if (warp == kMmaWarp) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// ------------------------------------------------------------------ join
+
+struct Part {
+  float m, l;
+  float4 o;
+};
+__device__ __forceinline__ void merge(Part& a, const Part& b) {
+  const float m = fmaxf(a.m, b.m);
+  const float x = ex2_approx(a.m - m), y = ex2_approx(b.m - m);
+  a.m = m;
+  a.l = fmaf(a.l, x, b.l * y);
+  a.o.x = fmaf(a.o.x, x, b.o.x * y);
+  a.o.y = fmaf(a.o.y, x, b.o.y * y);
+  a.o.z = fmaf(a.o.z, x, b.o.z * y);
+  a.o.w = fmaf(a.o.w, x, b.o.w * y);
+}
+
+// Block (s, y): rows of the unit that share s starts and others go on with.  Four
+// groups of threads have 4 columns each of a row: four rows where the parts are
+// few, a quarter of one row's parts where they are many.
+constexpr int kJoinGroups = 4;
+constexpr int kJoinMany = 6;
+
+template <int N, int R>
+__global__ void __launch_bounds__(kJoinGroups * R / 4) join_kernel(const LatentAttnArgs a) {
+  __shared__ Part side[kJoinGroups][R / 4];
+  const int share = blockIdx.x, G = a.shares;
+  wait_for_parent();
+  const int4 rec = a.rec[2 * share];
+  if (rec.y == 0) return;
+  const int4 more = a.rec[2 * share + 1];
+  const long long W = more.y;
+  const long long first = static_cast<long long>(rec.z) * a.span * N;       // of the sequence's rows
+  const int rows = static_cast<int>(min(static_cast<long long>(a.span * N), static_cast<long long>(rec.y) * a.Hq - first));
+  const int q4 = threadIdx.x % (R / 4), group = threadIdx.x / (R / 4);
+  const bool many = more.x - share + 1 > kJoinMany;
+  const int row = many ? blockIdx.y : kJoinGroups * blockIdx.y + group;
+  if ((many ? row : kJoinGroups * static_cast<int>(blockIdx.y)) >= rows) return;
+  Part p{-FLT_MAX, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
+  if (row < rows) {
+    const int step = many ? kJoinGroups : 1;
+#pragma unroll 4
+    for (int t = share + (many ? group : 0); t <= more.x; t += step) {
+      if (cta_first(W, G, t) == cta_first(W, G, t + 1)) continue;   // a share without work
+      const long long at = (2ll * (t * a.span + row / N) + (t == share ? 1 : 0)) * N + row % N;
+      if (!dcheck(inside(at, 1, 2ll * kSms * N), a.status, 696)) continue;
+      const float2 ml = a.part_ml[at];
+      merge(p, Part{ml.x, ml.y, reinterpret_cast<const float4*>(a.part_o + at * R)[q4]});
+    }
+  }
+  if (many) {
+    side[group][q4] = p;
+    __syncthreads();
+    if (group != 0) return;
+#pragma unroll
+    for (int g = 1; g < kJoinGroups; ++g) merge(p, side[g][q4]);
+  }
+  if (row >= rows) return;
+  const long long out = static_cast<long long>(rec.x) * a.Hq + first + row;
+  if (!dcheck(inside(out, 1, static_cast<long long>(a.s.T) * a.Hq), a.status, 697)) return;
+  const float inv = p.l == 0.f ? 0.f : 1.f / p.l;
+  *reinterpret_cast<uint2*>(a.o + out * R + 4 * q4) =
+      make_uint2(pack_bf16x2(p.o.x * inv, p.o.y * inv), pack_bf16x2(p.o.z * inv, p.o.w * inv));
+  if (q4 == 0) a.lse[out] = p.l == 0.f ? -INFINITY : (p.m + log2f(p.l)) * kLn2;
+}
+
+template <int N, int R>
+cudaError_t launch_t(const CUtensorMap& tk, const CUtensorMap& tq, const LatentAttnArgs& a, cudaStream_t stream) {
+  auto kern = latent_kernel<N, R>;
+  static SmemLimit limit;
+  cudaError_t e = limit.raise(reinterpret_cast<const void*>(kern), Cfg<N, R>::kSmem);
+  if (e != cudaSuccess) return e;
+  kern<<<a.span * a.shares, kThreads, Cfg<N, R>::kSmem, stream>>>(tk, tq, a);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  if (a.shares == 1) return cudaSuccess;   // nothing is shared
+  return launch_child(join_kernel<N, R>, dim3(a.shares, a.span * N), kJoinGroups * R / 4, 0, stream, a);
+}
+
+}  // namespace
+
+cudaError_t launch_latent_attn(int rows, int rank, const CUtensorMap& tk, const CUtensorMap& tq,
+                               const LatentAttnArgs& a, cudaStream_t stream) {
+  if (rank == 256)
+    return rows == 16 ? launch_t<16, 256>(tk, tq, a, stream)
+                      : (rows == 32 ? launch_t<32, 256>(tk, tq, a, stream) : launch_t<64, 256>(tk, tq, a, stream));
+  return rows == 16 ? launch_t<16, 512>(tk, tq, a, stream)
+                    : (rows == 32 ? launch_t<32, 512>(tk, tq, a, stream) : launch_t<64, 512>(tk, tq, a, stream));
+}
+
+}  // namespace fattn

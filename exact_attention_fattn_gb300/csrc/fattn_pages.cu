@@ -1,0 +1,572 @@
+// Pages of a cache: how often the tables name each page is counted on the
+// device, and forking, growing (with a copy of a shared last page), freeing and
+// compacting are kernels, so that they can be captured between the steps that
+// use the pages.  A page is free while its count is zero; the lowest free pages
+// are taken first, so results do not depend on timing.
+//
+// Bound: latency for the counts (a few integers a page; one CTA, so that the
+// order needs no second launch), bytes for the copies.  A CTA copies one piece of
+// a page at a time, four 16-byte loads a thread in flight, and takes the next
+// piece of the call's list, whose length only the device knows.
+#include <stdint.h>
+
+#include <nvtx3/nvToolsExt.h>
+
+#include "../../include/fattn.h"
+#include "fattn_cache.cuh"
+
+namespace fattn {
+
+namespace {
+
+constexpr int kPlanes = 5;
+constexpr int kMaxSeqs = 4096;
+constexpr int kScanThreads = 1024;
+constexpr int kScanPages = 16;          // counts a thread looks at in one turn
+constexpr int kCopyThreads = 256;
+constexpr int kPieceBytes = 16384;      // of a page's largest plane, a CTA's turn
+constexpr unsigned int kStatusNoPages = FATTN_ERR_NO_PAGES;
+
+struct Tables {
+  int* table;                 // [B, max_pages]
+  int B, max_pages, page_shift, pages;
+  int* refs;                  // [pages]
+  DeviceStatus* status;
+  __device__ __forceinline__ long long cap() const { return static_cast<long long>(max_pages) << page_shift; }
+  __device__ __forceinline__ int held(int len) const {
+    return static_cast<int>((static_cast<long long>(len) + (1 << page_shift) - 1) >> page_shift);
+  }
+  __device__ __forceinline__ bool is_page(int p) const { return p >= 0 && p < pages; }
+};
+
+// What a call's second kernel copies: pages src[i] -> dst[i], i < *count.
+struct CopyList {
+  int* count;
+  int* src;
+  int* dst;
+};
+
+struct Planes {
+  uint8_t* base[kPlanes];
+  long long stride[kPlanes];
+  long long bytes[kPlanes];
+  int wide[kPlanes];          // 16-byte copies
+  int n, pieces;
+};
+
+// Exclusive prefix sum over the block of one number a thread; `total` to all.
+__device__ __forceinline__ long long block_scan(long long x, long long* side, long long& total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  long long incl = x;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const long long t = __shfl_up_sync(0xffffffffu, incl, off);
+    if (lane >= off) incl += t;
+  }
+  __syncthreads();            // side may still be read
+  if (lane == 31) side[warp] = incl;
+  __syncthreads();
+  if (warp == 0) {
+    long long w = side[lane];
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const long long t = __shfl_up_sync(0xffffffffu, w, off);
+      if (lane >= off) w += t;
+    }
+    side[lane] = w;
+  }
+  __syncthreads();
+  total = side[31];
+  return incl - x + (warp > 0 ? side[warp - 1] : 0);
+}
+
+// The counts of kScanPages pages from `first` on; pages behind the last count as
+// `fill`.
+__device__ __forceinline__ void load_refs(const int* refs, int pages, int first, int fill, int (&r)[kScanPages]) {
+  if (first + kScanPages <= pages && (reinterpret_cast<uintptr_t>(refs) & 15) == 0) {
+#pragma unroll
+    for (int i = 0; i < kScanPages; i += 4) {
+      const int4 x = *reinterpret_cast<const int4*>(refs + first + i);
+      r[i] = x.x;
+      r[i + 1] = x.y;
+      r[i + 2] = x.z;
+      r[i + 3] = x.w;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < kScanPages; ++i) r[i] = first + i < pages ? refs[first + i] : fill;
+  }
+}
+
+// ------------------------------------------------------------------ fork, free
+
+// Block i: sequence child[i] becomes a copy of parent[i], pages shared.
+__global__ void __launch_bounds__(128) fork_kernel(const Tables t, int* kv_len, const int* parent, const int* child,
+                                                   int n) {
+  const int i = blockIdx.x;
+  const int p = parent[i], c = child[i];
+  bool bad = p < 0 || p >= t.B || c < 0 || c >= t.B;
+  // A child is named once and is nobody's parent, so that the blocks' order does not matter.
+  for (int j = threadIdx.x; j < n; j += blockDim.x) bad |= (j != i && child[j] == c) || parent[j] == c;
+  bad = __syncthreads_or(bad);
+  if (!bad) {
+    const int len = kv_len[p];
+    bad = len < 0 || len > t.cap() || kv_len[c] != 0;
+    // Every thread has read kv_len[c] before one of them writes it.
+    bad = __syncthreads_or(bad);
+    if (!bad) {
+      const int* from = t.table + static_cast<long long>(p) * t.max_pages;
+      int* to = t.table + static_cast<long long>(c) * t.max_pages;
+      const int held = t.held(len);
+      for (int k = threadIdx.x; k < held; k += blockDim.x) {
+        const int page = from[k];
+        to[k] = page;
+        if (t.is_page(page)) atomicAdd(t.refs + page, 1);
+        else record_bad_index(t.status, kSitePage);
+      }
+      if (threadIdx.x == 0) kv_len[c] = len;
+    }
+  }
+  if (bad && threadIdx.x == 0) record_bad_index(t.status, kSiteRows);
+}
+
+// Block i: sequence rows[i] gives its pages back.  Of a row named twice the first
+// one counts.
+__global__ void __launch_bounds__(128) free_kernel(const Tables t, int* kv_len, const int* rows, int n) {
+  const int i = blockIdx.x;
+  const int r = rows[i];
+  if (r < 0 || r >= t.B) {
+    if (threadIdx.x == 0) record_bad_index(t.status, kSiteRows);
+    return;
+  }
+  bool twice = false;
+  for (int j = threadIdx.x; j < i; j += blockDim.x) twice |= rows[j] == r;
+  if (__syncthreads_or(twice)) return;
+  const int len = kv_len[r];
+  __syncthreads();
+  if (len < 0 || len > t.cap()) {
+    if (threadIdx.x == 0) record_bad_index(t.status, kSiteRows);
+    return;
+  }
+  const int held = t.held(len);
+  const int* row = t.table + static_cast<long long>(r) * t.max_pages;
+  for (int k = threadIdx.x; k < held; k += blockDim.x) {
+    const int page = row[k];
+    if (!t.is_page(page)) {
+      record_bad_index(t.status, kSitePage);
+    } else if (atomicSub(t.refs + page, 1) <= 0) {
+      atomicAdd(t.refs + page, 1);        // was free already
+      record_bad_index(t.status, kSiteRefs);
+    }
+  }
+  if (threadIdx.x == 0) kv_len[r] = 0;
+}
+
+// ------------------------------------------------------------------ extend
+
+// Sequences from old_len to new_len tokens, in order: one whose next token falls
+// into a page that others name too gets a copy of it (the last of those that
+// write to it keeps it), and all get the pages they lack.
+__global__ void __launch_bounds__(kScanThreads) extend_kernel(const Tables t, const int* old_len, const int* new_len,
+                                                              int* free_list, CopyList list) {
+  __shared__ long long side[32];
+  __shared__ __align__(16) int tails[kMaxSeqs];   // shared last page that sequence b writes to, or -1
+  __shared__ int starts[kMaxSeqs];      // pages taken by earlier sequences, times two, + 1 if b gets a copy
+  __shared__ int found_all;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  allow_child();
+  auto lens = [&](int b, int& o, int& w) {
+    o = old_len[b];
+    w = new_len[b];
+    if (o >= 0 && w >= o && w <= t.cap()) return true;
+    o = w = 0;
+    return false;
+  };
+  for (int b = tid; b < t.B; b += kScanThreads) {
+    int o, w, tail = -1;
+    if (!lens(b, o, w)) record_bad_index(t.status, kSiteSeqStart);
+    if (w > o && (o & ((1 << t.page_shift) - 1)) != 0) {
+      const int p = t.table[static_cast<long long>(b) * t.max_pages + (o >> t.page_shift)];
+      if (!t.is_page(p)) record_bad_index(t.status, kSitePage);
+      else if (t.refs[p] >= 2) tail = p;
+    }
+    tails[b] = tail;
+  }
+  __syncthreads();
+  // ---- pages that each sequence takes, and which of them are copies
+  const int per = (t.B + kScanThreads - 1) / kScanThreads;
+  const int b0 = min(t.B, tid * per), b1 = min(t.B, b0 + per);
+  long long sum = 0;                     // pages, and copies in the upper half
+  for (int b = b0; b < b1; ++b) {
+    int copy = 0;
+    if (tails[b] >= 0) {
+      int before = 0;
+      const int tail = tails[b];
+      int e = 0;
+      for (; e + 4 <= b; e += 4) {
+        const int4 x = *reinterpret_cast<const int4*>(tails + e);
+        before += (x.x == tail) + (x.y == tail) + (x.z == tail) + (x.w == tail);
+      }
+      for (; e < b; ++e) before += tails[e] == tail;
+      copy = t.refs[tails[b]] - before >= 2 ? 1 : 0;
+    }
+    int o, w;
+    lens(b, o, w);
+    starts[b] = copy;
+    sum += (static_cast<long long>(copy) << 40) + copy + t.held(w) - t.held(o);
+  }
+  long long total;
+  long long at = block_scan(sum, side, total);
+  const long long want = total & ((1ll << 40) - 1);
+  // ---- the lowest free pages
+  if (tid == 0) found_all = want <= t.pages;
+  __syncthreads();
+  if (found_all) {
+    long long seen = 0;
+    for (long long base = 0; base < t.pages && seen < want; base += kScanThreads * kScanPages) {
+      int r[kScanPages], n = 0;
+      const int first = static_cast<int>(min(base + tid * kScanPages, static_cast<long long>(t.pages)));
+      load_refs(t.refs, t.pages, first, 1, r);
+#pragma unroll
+      for (int i = 0; i < kScanPages; ++i) n += r[i] == 0 ? 1 : 0;
+      long long all;
+      long long rank = seen + block_scan(n, side, all);
+#pragma unroll
+      for (int i = 0; i < kScanPages; ++i)
+        if (r[i] == 0) {
+          if (rank < want && dcheck(inside(rank, 1, t.pages), t.status, 671)) free_list[rank] = first + i;
+          ++rank;
+        }
+      seen += all;
+    }
+    __syncthreads();
+    if (tid == 0) found_all = seen >= want;
+    __syncthreads();
+  }
+  const bool granted = found_all;
+  if (tid == 0) {
+    *list.count = granted ? static_cast<int>(total >> 40) : 0;
+    if (!granted && atomicCAS(&t.status->code, 0u, kStatusNoPages) == 0u) {
+      t.status->where = kSiteRefs;
+      t.status->block = 0u;
+    }
+  }
+  // ---- copies, and where each sequence's pages begin (a call that takes more than the
+  // pool has was refused above, so the starts fit)
+  for (int b = b0; b < b1; ++b) {
+    int o, w;
+    lens(b, o, w);
+    const int copy = starts[b], begin = granted ? static_cast<int>(at & ((1ll << 40) - 1)) : 0;
+    starts[b] = 2 * begin + copy;
+    if (copy && granted) {
+      const int i = static_cast<int>(at >> 40), to = free_list[begin];
+      if (dcheck(inside(i, 1, t.B) && inside(begin, 1, t.pages), t.status, 672)) {
+        list.src[i] = tails[b];
+        list.dst[i] = to;
+        t.table[static_cast<long long>(b) * t.max_pages + (o >> t.page_shift)] = to;
+        atomicSub(t.refs + tails[b], 1);
+      }
+    }
+    at += (static_cast<long long>(copy) << 40) + copy + t.held(w) - t.held(o);
+  }
+  __syncthreads();
+  for (int i = tid; granted && i < want; i += kScanThreads) t.refs[free_list[i]] = 1;
+  // ---- new entries, a warp to a sequence
+  for (int b = warp; b < t.B; b += kScanThreads / 32) {
+    int o, w;
+    lens(b, o, w);
+    const int k0 = t.held(o), k1 = t.held(w), begin = (starts[b] >> 1) + (starts[b] & 1);
+    int* row = t.table + static_cast<long long>(b) * t.max_pages;
+    for (int k = k0 + lane; k < k1; k += 32)
+      if (dcheck(inside(k, 1, t.max_pages), t.status, 673)) row[k] = granted ? free_list[begin + k - k0] : -1;
+  }
+}
+
+// ------------------------------------------------------------------ compact
+
+// The k-th held page from `total` on goes to the k-th free page below, total the
+// number of pages held.
+__global__ void __launch_bounds__(kScanThreads) plan_kernel(const Tables t, int* to_page, CopyList list, int* limit) {
+  __shared__ long long side[32];
+  const int tid = threadIdx.x;
+  allow_child();
+  long long held = 0;
+  for (long long base = 0; base < t.pages; base += kScanThreads * kScanPages) {
+    int r[kScanPages];
+    load_refs(t.refs, t.pages, static_cast<int>(min(base + tid * kScanPages, static_cast<long long>(t.pages))), 0, r);
+#pragma unroll
+    for (int i = 0; i < kScanPages; ++i) held += r[i] > 0 ? 1 : 0;
+  }
+  long long total;
+  block_scan(held, side, total);
+  long long seen = 0;                    // holes, and pages to move in the upper half
+  for (long long base = 0; base < t.pages; base += kScanThreads * kScanPages) {
+    int r[kScanPages];
+    const int first = static_cast<int>(min(base + tid * kScanPages, static_cast<long long>(t.pages)));
+    load_refs(t.refs, t.pages, first, 0, r);
+    long long n = 0;
+#pragma unroll
+    for (int i = 0; i < kScanPages; ++i) {
+      const int p = first + i;
+      if (p < total && r[i] <= 0) n += 1;
+      if (p >= total && r[i] > 0) n += 1ll << 32;
+    }
+    long long all;
+    const long long at = seen + block_scan(n, side, all);
+    int hole = static_cast<int>(at & 0xffffffffll), move = static_cast<int>(at >> 32);
+#pragma unroll
+    for (int i = 0; i < kScanPages; ++i) {
+      const int p = first + i;
+      if (!dcheck(hole <= t.pages / 2 && move <= t.pages / 2, t.status, 674)) break;
+      if (p < total && p < t.pages && r[i] <= 0) list.dst[hole++] = p;
+      if (p >= total && r[i] > 0) list.src[move++] = p;
+    }
+    seen += all;
+  }
+  __syncthreads();
+  const int moves = static_cast<int>(seen >> 32);
+  for (int i = tid; i < moves; i += kScanThreads) {
+    const int from = list.src[i], to = list.dst[i];
+    to_page[from] = to;
+    t.refs[to] = t.refs[from];
+    t.refs[from] = 0;
+  }
+  if (tid == 0) {
+    *list.count = moves;
+    *limit = static_cast<int>(total);
+  }
+}
+
+// ------------------------------------------------------------------ copies
+
+template <class V>
+__device__ __forceinline__ void copy_span(uint8_t* to, const uint8_t* from, long long bytes) {
+  constexpr int kAhead = 4;
+  const V* s = reinterpret_cast<const V*>(from);
+  V* d = reinterpret_cast<V*>(to);
+  const int n = static_cast<int>(bytes / sizeof(V));
+  int i = threadIdx.x;
+  for (; i + (kAhead - 1) * kCopyThreads < n; i += kAhead * kCopyThreads) {
+    V x[kAhead];
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) x[k] = s[i + k * kCopyThreads];
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) d[i + k * kCopyThreads] = x[k];
+  }
+  for (; i < n; i += kCopyThreads) d[i] = s[i];
+}
+
+// Copies the list's pages; blocks from copy_blocks on rewrite the table where
+// pages have moved (compact; to_page is nullptr otherwise).
+__global__ void __launch_bounds__(kCopyThreads) copy_kernel(const Tables t, const __grid_constant__ Planes planes,
+                                                            CopyList list, int copy_blocks, const int* kv_len,
+                                                            const int* to_page, const int* limit) {
+  wait_for_parent();
+  const int n = *list.count;
+  if (n == 0) return;
+  if (static_cast<int>(blockIdx.x) >= copy_blocks) {
+    const int lim = *limit;
+    for (int b = blockIdx.x - copy_blocks; b < t.B; b += gridDim.x - copy_blocks) {
+      const int len = kv_len[b];
+      if (len < 0 || len > t.cap()) {
+        if (threadIdx.x == 0) record_bad_index(t.status, kSiteSeqStart);
+        continue;
+      }
+      int* row = t.table + static_cast<long long>(b) * t.max_pages;
+      const int held = t.held(len);
+      for (int k = threadIdx.x; k < held; k += kCopyThreads) {
+        const int p = row[k];
+        if (!t.is_page(p)) record_bad_index(t.status, kSitePage);
+        else if (p >= lim) row[k] = to_page[p];
+      }
+    }
+    return;
+  }
+  const long long items = static_cast<long long>(n) * planes.pieces;
+  for (long long w = blockIdx.x; w < items; w += copy_blocks) {
+    const int i = static_cast<int>(w / planes.pieces), piece = static_cast<int>(w - static_cast<long long>(i) * planes.pieces);
+    const long long from = list.src[i], to = list.dst[i];
+    if (!dcheck(inside(from, 1, t.pages) && inside(to, 1, t.pages), t.status, 675)) continue;
+    for (int k = 0; k < planes.n; ++k) {
+      const long long unit = planes.wide[k] ? 16 : 4;
+      const long long per = (planes.bytes[k] / unit + planes.pieces - 1) / planes.pieces * unit;
+      const long long lo = min(planes.bytes[k], piece * per), span = min(planes.bytes[k], lo + per) - lo;
+      uint8_t* d = planes.base[k] + to * planes.stride[k] + lo;
+      const uint8_t* s = planes.base[k] + from * planes.stride[k] + lo;
+      if (planes.wide[k]) copy_span<uint4>(d, s, span);
+      else copy_span<uint32_t>(d, s, span);
+    }
+  }
+}
+
+// ------------------------------------------------------------------ host
+
+struct Range {
+  explicit Range(const char* name) { nvtxRangePushA(name); }
+  ~Range() { nvtxRangePop(); }
+};
+
+bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
+
+int check_pool(const fattn_page_pool* pool, const int* page_table, const int* kv_len, int B, int max_pages) {
+  if (!pool || !pool->refs || !aligned(pool->refs, 4) || pool->pages <= 0) return FATTN_ERR_INVALID_ARG;
+  if (pool->page != 32 && pool->page != 64 && pool->page != 128) return FATTN_ERR_UNSUPPORTED;
+  if (!page_table || !kv_len || !aligned(page_table, 4) || !aligned(kv_len, 4)) return FATTN_ERR_INVALID_ARG;
+  if (B <= 0 || B > kMaxSeqs || max_pages <= 0) return FATTN_ERR_INVALID_ARG;
+  if (static_cast<long long>(max_pages) * pool->page > 0x7fff0000ll || pool->pages >= (1 << 30))
+    return FATTN_ERR_INVALID_ARG;
+  return FATTN_OK;
+}
+
+int check_planes(const fattn_page_pool* pool, const fattn_plane* planes, int n, Planes& out) {
+  if (!planes || n <= 0 || n > kPlanes) return FATTN_ERR_INVALID_ARG;
+  long long most = 0;
+  for (int i = 0; i < n; ++i) {
+    const fattn_plane& p = planes[i];
+    if (!p.base || !aligned(p.base, 4) || p.bytes <= 0 || p.bytes % 4 != 0 || p.stride % 4 != 0 ||
+        p.stride < p.bytes || p.stride >= (1ll << 40) || p.bytes > 0x7fffffffll)
+      return FATTN_ERR_INVALID_ARG;
+    out.base[i] = static_cast<uint8_t*>(p.base);
+    out.stride[i] = p.stride;
+    out.bytes[i] = p.bytes;
+    out.wide[i] = aligned(p.base, 16) && p.bytes % 16 == 0 && p.stride % 16 == 0;
+    most = p.bytes > most ? p.bytes : most;
+  }
+  (void)pool;
+  out.n = n;
+  out.pieces = static_cast<int>((most + kPieceBytes - 1) / kPieceBytes);
+  return FATTN_OK;
+}
+
+Tables tables_of(const fattn_page_pool* pool, int* page_table, int B, int max_pages, DeviceStatus* status) {
+  Tables t;
+  t.table = page_table;
+  t.B = B;
+  t.max_pages = max_pages;
+  t.page_shift = pool->page == 32 ? 5 : (pool->page == 64 ? 6 : 7);
+  t.pages = pool->pages;
+  t.refs = pool->refs;
+  t.status = status;
+  return t;
+}
+
+// count and limit, then two lists of pages, then one entry a page
+struct PagesWorkspace {
+  size_t src, dst, map, total;
+};
+PagesWorkspace workspace_of(int pages, int B) {
+  PagesWorkspace w;
+  const size_t list = align256((static_cast<size_t>(pages / 2 > B ? pages / 2 : B) + 1) * sizeof(int));
+  w.src = 256;
+  w.dst = w.src + list;
+  w.map = w.dst + list;
+  w.total = w.map + align256(static_cast<size_t>(pages) * sizeof(int));
+  return w;
+}
+
+int copy_grid(long long most_items) {
+  const long long all = 8ll * kSms;       // 2048 threads an SM
+  return static_cast<int>(most_items < all ? most_items : all);
+}
+
+int from_launch(cudaError_t e) { return e == cudaSuccess ? FATTN_OK : FATTN_ERR_CUDA; }
+
+}  // namespace
+
+}  // namespace fattn
+
+using namespace fattn;
+
+extern "C" {
+
+int fattn_pages_fork(const fattn_page_pool* pool, int* page_table, int* kv_len, const int* parent, const int* child,
+                     int n, int B, int max_pages, fattn_stream_t stream) {
+  const Range range("fattn_pages_fork");
+  int rc = check_pool(pool, page_table, kv_len, B, max_pages);
+  if (rc != FATTN_OK) return rc;
+  if (!parent || !child || !aligned(parent, 4) || !aligned(child, 4) || n <= 0 || n > B) return FATTN_ERR_INVALID_ARG;
+  DeviceStatus* status = nullptr;
+  long long budget = 0;
+  if ((rc = call_setup(&status, &budget)) != FATTN_OK) return rc;
+  fork_kernel<<<n, 128, 0, reinterpret_cast<cudaStream_t>(stream)>>>(tables_of(pool, page_table, B, max_pages, status),
+                                                                     kv_len, parent, child, n);
+  return from_launch(cudaGetLastError());
+}
+
+int fattn_pages_free(const fattn_page_pool* pool, int* page_table, int* kv_len, const int* rows, int n, int B,
+                     int max_pages, fattn_stream_t stream) {
+  const Range range("fattn_pages_free");
+  int rc = check_pool(pool, page_table, kv_len, B, max_pages);
+  if (rc != FATTN_OK) return rc;
+  if (!rows || !aligned(rows, 4) || n <= 0 || n > kMaxSeqs) return FATTN_ERR_INVALID_ARG;
+  DeviceStatus* status = nullptr;
+  long long budget = 0;
+  if ((rc = call_setup(&status, &budget)) != FATTN_OK) return rc;
+  free_kernel<<<n, 128, 0, reinterpret_cast<cudaStream_t>(stream)>>>(tables_of(pool, page_table, B, max_pages, status),
+                                                                     kv_len, rows, n);
+  return from_launch(cudaGetLastError());
+}
+
+size_t fattn_pages_workspace_bytes(int pages, int B) {
+  if (pages <= 0 || pages >= (1 << 30) || B <= 0 || B > kMaxSeqs) return 0;
+  return workspace_of(pages, B).total;
+}
+
+int fattn_pages_extend(const fattn_page_pool* pool, const fattn_plane* planes, int n_planes, int* page_table,
+                       const int* old_len, const int* new_len, void* workspace, size_t workspace_bytes, int B,
+                       int max_pages, fattn_stream_t stream) {
+  const Range range("fattn_pages_extend");
+  int rc = check_pool(pool, page_table, old_len, B, max_pages);
+  if (rc != FATTN_OK) return rc;
+  if (!new_len || !aligned(new_len, 4)) return FATTN_ERR_INVALID_ARG;
+  Planes p{};
+  if ((rc = check_planes(pool, planes, n_planes, p)) != FATTN_OK) return rc;
+  const PagesWorkspace w = workspace_of(pool->pages, B);
+  if (!workspace || !aligned(workspace, 256) || workspace_bytes < w.total) return FATTN_ERR_INVALID_ARG;
+  DeviceStatus* status = nullptr;
+  long long budget = 0;
+  if ((rc = call_setup(&status, &budget)) != FATTN_OK) return rc;
+  char* base = static_cast<char*>(workspace);
+  const CopyList list{reinterpret_cast<int*>(base), reinterpret_cast<int*>(base + w.src),
+                      reinterpret_cast<int*>(base + w.dst)};
+  const Tables t = tables_of(pool, page_table, B, max_pages, status);
+  const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  extend_kernel<<<1, kScanThreads, 0, st>>>(t, old_len, new_len, reinterpret_cast<int*>(base + w.map), list);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return FATTN_ERR_CUDA;
+  const int grid = copy_grid(static_cast<long long>(B) * p.pieces);
+  return from_launch(launch_child(copy_kernel, grid, kCopyThreads, 0, st, t, p, list, grid,
+                                  static_cast<const int*>(nullptr), static_cast<const int*>(nullptr),
+                                  static_cast<const int*>(nullptr)));
+}
+
+int fattn_pages_compact(const fattn_page_pool* pool, const fattn_plane* planes, int n_planes, int* page_table,
+                        const int* kv_len, void* workspace, size_t workspace_bytes, int B, int max_pages,
+                        fattn_stream_t stream) {
+  const Range range("fattn_pages_compact");
+  int rc = check_pool(pool, page_table, kv_len, B, max_pages);
+  if (rc != FATTN_OK) return rc;
+  Planes p{};
+  if ((rc = check_planes(pool, planes, n_planes, p)) != FATTN_OK) return rc;
+  const PagesWorkspace w = workspace_of(pool->pages, B);
+  if (!workspace || !aligned(workspace, 256) || workspace_bytes < w.total) return FATTN_ERR_INVALID_ARG;
+  DeviceStatus* status = nullptr;
+  long long budget = 0;
+  if ((rc = call_setup(&status, &budget)) != FATTN_OK) return rc;
+  char* base = static_cast<char*>(workspace);
+  const CopyList list{reinterpret_cast<int*>(base), reinterpret_cast<int*>(base + w.src),
+                      reinterpret_cast<int*>(base + w.dst)};
+  int* limit = reinterpret_cast<int*>(base) + 1;
+  int* to_page = reinterpret_cast<int*>(base + w.map);
+  const Tables t = tables_of(pool, page_table, B, max_pages, status);
+  const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  plan_kernel<<<1, kScanThreads, 0, st>>>(t, to_page, list, limit);
+  if (cudaGetLastError() != cudaSuccess) return FATTN_ERR_CUDA;
+  const int copies = copy_grid((static_cast<long long>(pool->pages) / 2 + 1) * p.pieces);
+  const int rows = B < 2 * kSms ? B : 2 * kSms;
+  return from_launch(launch_child(copy_kernel, copies + rows, kCopyThreads, 0, st, t, p, list, copies, kv_len,
+                                  static_cast<const int*>(to_page), static_cast<const int*>(limit)));
+}
+
+}  // extern "C"

@@ -48,8 +48,10 @@ typedef enum {
                                 fattn_cache_fwd more than 2^31 pieces of work */
   FATTN_ERR_DEBUG_CHECK = 6, /* debug builds only (FATTN_DEBUG): a kernel found an index out of
                                 its range, skipped the access and recorded the site */
-  FATTN_ERR_BAD_INDEX = 7    /* a cache call's q_start, kv_len, page_table or selected pages are
-                                out of range; the kernel skipped what they point at */
+  FATTN_ERR_BAD_INDEX = 7,   /* a cache call's q_start, kv_len, page_table, positions or selected
+                                pages are out of range; the kernel skipped what they point at */
+  FATTN_ERR_NO_PAGES = 8     /* fattn_pages_extend: the pool has too few free pages; no sequence
+                                was given any */
 } fattn_status;
 
 /*
@@ -404,10 +406,175 @@ int fattn_cache_select(const fattn_cache* cache, const void* q, long long q_row,
                        fattn_stream_t stream);
 
 /*
+ * Rotary positions
+ * ----------------
+ * y = x with the pairs of each row's first rope_dim columns rotated by the angles
+ * of the row's position, (a cos - b sin, b cos + a sin); the other columns stay.  With
+ * transposed != 0 by the negated angles: the gradient, dx = R^T dy.  Pairs, the
+ * table (fp32 [rope_len, rope_dim]) and the arithmetic (fp32, every product and sum
+ * rounded, then one rounding to bf16) are those of fattn_cache_append.
+ *   x, y       : bf16 rows of d columns, row (b, h, n) of [B, H, N, d] at
+ *                b strides[0] + h strides[1] + n strides[2] elements; strides are multiples of 8,
+ *                from 0 (x only) up to 2^40, and rows of y do not overlap.  y may be x with the same
+ *                strides, and then only the rotated columns are touched; otherwise
+ *                they share no element.  d is a multiple of 16 up to 1024 (FATTN_ERR_UNSUPPORTED)
+ *   positions  : int, row (b, n) at positions[b * positions_stride + n] (0: the same for all
+ *                b), or NULL: n.  Rows whose position is outside [0, rope_len) are not
+ *                written and are FATTN_ERR_BAD_INDEX
+ * rope_dim is a multiple of 16 up to d.  Returns a fattn_status.
+ */
+int fattn_rope(const void* x, const long long* x_strides, void* y, const long long* y_strides,
+               const float* rope, int rope_len, int rope_dim, int interleaved, int transposed,
+               const int* positions, long long positions_stride, int B, int H, int N, int d,
+               fattn_stream_t stream);
+
+/*
+ * Attention over a paged latent cache
+ * -----------------------------------
+ * Where the keys and values of all heads are products of one latent vector a token,
+ * the cache holds that vector and the token's rotated key part, which the heads
+ * share, and queries come multiplied with the keys' product (the absorbed form):
+ *   data  : bf16 [pages, page, rank + 64], contiguous within a page, the pages page_stride
+ *           elements apart (a multiple of 8, below 2^38); 16-byte aligned.  Columns 0 .. rank-1 are a
+ *           token's latent, its value for every head; all columns are its key
+ *   rank  : 256 or 512;  page: 32, 64 or 128 tokens
+ * The batch is described as for fattn_cache_fwd: q_start, kv_len, page_table, checked
+ * by the kernels.  Query heads: Hq <= 1024.
+ */
+typedef struct {
+  void* data;
+  long long page_stride;
+  int pages, page, rank;
+} fattn_latent_cache;
+
+/*
+ * Append the batch's new tokens: latents as they are, key parts rotated by their
+ * positions (as in fattn_cache_append, rope_dim 64; rope NULL rotates nothing), and
+ * the queries' parts likewise.
+ *   latent  : in, bf16 rows of rank columns, latent_row elements apart
+ *   k_rope  : in, bf16 rows of 64 columns, k_row apart (both multiples of 8: slices of
+ *             one projection)
+ *   q_rope  : in, bf16 [T, Hq, 64], rows q_row and heads q_head elements apart (multiples of 8)
+ *   q       : out, bf16 [T, Hq, rank + 64], contiguous: columns rank .. rank+63 are written.
+ *             q_rope and q may be the same columns of one buffer; both NULL: none
+ * A token with an infinity or a NaN in its latent or key part gets a NaN key part
+ * and a zero latent: the rows that attend to it become NaN, and no others.
+ * A page that receives tokens must belong to one sequence only.  Positions below 0 or
+ * from rope_len on are FATTN_ERR_BAD_INDEX; of a sequence that has any, nothing is
+ * appended and no query written.  Returns a fattn_status.
+ */
+int fattn_latent_append(const fattn_latent_cache* cache, const void* latent, long long latent_row,
+                        const void* k_rope, long long k_row, const void* q_rope, long long q_row,
+                        long long q_head, void* q, int Hq, const float* rope, int rope_len,
+                        int interleaved, const int* page_table, const int* q_start,
+                        const int* kv_len, int T, int B, int max_pages, fattn_stream_t stream);
+
+/*
+ * Attention of the batch's rows over their sequences' cached tokens: with c_j the
+ * latent and k_j all columns of token j,
+ *   s_j = scale q . k_j,  O = sum_j softmax(s)_j c_j,  L = log sum_j exp(s_j)
+ * per row and head.  Masks, rows that see nothing and queries with an infinity or a
+ * NaN as in fattn_cache_fwd.
+ *   q         : in,  bf16 [T, Hq, rank + 64], contiguous
+ *   o, lse    : out, bf16 [T, Hq, rank] and fp32 [T, Hq]
+ *   workspace : at least fattn_latent_fwd_workspace_bytes(T, B, Hq, rank) bytes, 256-byte
+ *               aligned; contents on entry ignored; calls that may overlap need one each
+ * Slots behind a sequence's end may hold anything; latents before it are finite
+ * (fattn_latent_append writes no others).
+ * Rounding: probabilities are rounded to bf16 (2^-8) for the second product, and O to
+ * bf16 (2^-8); scores, sums, maxima and the accumulators are fp32.
+ * The rows of an average sequence, T * Hq / B, decide how the call is laid out; a batch that
+ * mixes pieces of prompts with many single tokens is faster as two calls.
+ * Results do not depend on timing.  Returns a fattn_status.
+ */
+size_t fattn_latent_fwd_workspace_bytes(int T, int B, int Hq, int rank);
+int fattn_latent_fwd(const fattn_latent_cache* cache, const void* q, void* o, float* lse,
+                     const int* page_table, const int* q_start, const int* kv_len, void* workspace,
+                     size_t workspace_bytes, int T, int B, int Hq, int max_pages, int causal,
+                     float scale, fattn_stream_t stream);
+
+/*
+ * The pages of a cache
+ * --------------------
+ * Sequences may share pages (a prompt and its samples).  A pool counts, on the device, how
+ * many table entries name each page, so that pages can be taken, shared and given back
+ * between the steps of a captured graph:
+ *   refs  : int [pages], zeros for an empty pool; a page is free while its count is 0
+ *   page  : 32, 64 or 128 tokens;  pages < 2^30
+ * Sequence b holds the first ceil(len/page) entries of its row of page_table [B, max_pages];
+ * the others are neither read nor written.  B <= 4096.  The lowest free pages are taken
+ * first, so results do not depend on timing.
+ *
+ * A cache is any number of planes (at most 5), page p of each at base + p * stride bytes:
+ * bytes, stride and base are multiples of 4 (of 16 for wide copies).  A
+ * fattn_cache has k, v, k_scale, v_scale and k_bounds, a fattn_latent_cache one.
+ */
+typedef struct {
+  int* refs;
+  int pages, page;
+} fattn_page_pool;
+
+typedef struct {
+  void* base;
+  long long stride, bytes;
+} fattn_plane;
+
+/*
+ * Sequence child[i] becomes a copy of sequence parent[i] that shares its pages: its table
+ * entries, its length (kv_len, in and out), and one more count for each of its pages.
+ *   parent, child : int [n] on the device, n <= B.  A child has length 0 before; one that has not, is
+ *                   named twice, is out of range or is also a parent is
+ *                   FATTN_ERR_BAD_INDEX and left as it is
+ * Returns a fattn_status.
+ */
+int fattn_pages_fork(const fattn_page_pool* pool, int* page_table, int* kv_len, const int* parent,
+                     const int* child, int n, int B, int max_pages, fattn_stream_t stream);
+
+/*
+ * Make room for the tokens old_len[b] .. new_len[b]-1 of every sequence, to be called
+ * before they are appended.  In order of b: where token old_len[b] falls into a page that it
+ * shares, the sequence gets a copy of that page for itself (the last that still has the
+ * page keeps it), and then the pages it lacks.
+ *   old_len, new_len : int [B] on the device, 0 <= old_len <= new_len <= max_pages * page; a
+ *                      sequence with others is FATTN_ERR_BAD_INDEX and gets nothing
+ *   workspace        : at least fattn_pages_workspace_bytes(pages, B), 256-byte aligned; contents on
+ *                      entry ignored; calls that may overlap need one each
+ * With too few free pages no sequence gets any: tables and counts stay as they are, but
+ * that the entries to be filled become -1 (so that appending leaves those tokens out), and
+ * fattn_check_status() reports FATTN_ERR_NO_PAGES.  Shared pages then still are, so
+ * nothing may be appended before the host has looked.  Returns a fattn_status.
+ */
+size_t fattn_pages_workspace_bytes(int pages, int B);
+int fattn_pages_extend(const fattn_page_pool* pool, const fattn_plane* planes, int n_planes,
+                       int* page_table, const int* old_len, const int* new_len, void* workspace,
+                       size_t workspace_bytes, int B, int max_pages, fattn_stream_t stream);
+
+/*
+ * The sequences rows[i] (int [n] on the device, n <= 4096) give their pages back: one
+ * count less for each, and length 0 (kv_len, in and out).  Of a row named twice the
+ * first counts; a row out of range, or a page that was free already, is FATTN_ERR_BAD_INDEX.
+ * Returns a fattn_status.
+ */
+int fattn_pages_free(const fattn_page_pool* pool, int* page_table, int* kv_len, const int* rows,
+                     int n, int B, int max_pages, fattn_stream_t stream);
+
+/*
+ * Move the pool's pages together: with U pages held, the k-th held page from U on goes to the
+ * k-th free page below U, in every plane, count and table entry.  kv_len [B] says which
+ * entries sequences hold (pages taken for tokens beyond it would be lost: give the
+ * lengths that fattn_pages_extend was given).  Workspace as for fattn_pages_extend.
+ * Returns a fattn_status.
+ */
+int fattn_pages_compact(const fattn_page_pool* pool, const fattn_plane* planes, int n_planes,
+                        int* page_table, const int* kv_len, void* workspace, size_t workspace_bytes,
+                        int B, int max_pages, fattn_stream_t stream);
+
+/*
  * Synchronise `stream`, then report the first error since the last call:
  * a pending asynchronous CUDA error (FATTN_ERR_CUDA), a kernel wait timeout
- * (FATTN_ERR_TIMEOUT) or an index that a cache call found out of range
- * (FATTN_ERR_BAD_INDEX) recorded on the current device.  Clears the
+ * (FATTN_ERR_TIMEOUT), an index that a cache call found out of range
+ * (FATTN_ERR_BAD_INDEX) or a pool without enough free pages (FATTN_ERR_NO_PAGES)
+ * recorded on the current device.  Clears the
  * device status word.  Returns FATTN_OK when neither happened.
  */
 int fattn_check_status(fattn_stream_t stream);
