@@ -228,6 +228,8 @@ cudaError_t launch_latent_append(const LatentAppendArgs& a, cudaStream_t stream)
 
 struct LatentAttnArgs {
   CacheSeqs s;
+  const uint16_t* data;       // bf16 [pages, page, rank + 64], pages page_stride elements apart
+  long long page_stride;
   uint16_t* o;                // bf16 [T, Hq, rank]
   float* lse;                 // [T, Hq]
   int pages, page_shift, Hq, causal;

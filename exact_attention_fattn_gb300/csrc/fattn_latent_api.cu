@@ -167,6 +167,8 @@ int fattn_latent_fwd(const fattn_latent_cache* cache, const void* q, void* o, fl
   LatentAttnArgs a{};
   if ((rc = call_setup(&a.status, &a.wait_budget)) != FATTN_OK) return rc;
   a.s = seqs_of(page_table, q_start, kv_len, T, B, max_pages);
+  a.data = static_cast<const uint16_t*>(cache->data);
+  a.page_stride = cache->page_stride;
   a.o = static_cast<uint16_t*>(o);
   a.lse = lse;
   a.pages = cache->pages;

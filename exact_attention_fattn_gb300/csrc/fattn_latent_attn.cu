@@ -17,7 +17,7 @@
 // Softmax: tensor memory gives a warp 16 keys of all rows (M = 64 uses 16 lanes of
 // each quarter), so a thread has two keys of N / 4 rows, whose references m
 // and sums l it keeps in registers.  A row's reference moves only when a score
-// passes it by more than 2^8; whether one does is one vote of the four warps, so
+// passes it by more than 2^8; whether one does is one vote of the warps, so
 // that most tiles need no maximum over keys at all.  P is rounded to bf16 (half a
 // step: 2^-8 of a probability), as V is; scores, sums, references and accumulators
 // are fp32.
@@ -28,8 +28,9 @@
 // keys come out of DRAM once.  Units that shares split are joined in a second
 // kernel, in order.
 //
-// Warps: 0-3 softmax and results, 4 tensor memory and MMA issue, 5 loads, 6 the
-// walk over the share (it publishes one segment after the other), 7 idle.
+// Warps: 0-3 softmax and results (0-7 with 64 rows, half of them each), then one for
+// tensor memory and MMA issue, one for loads, one for the walk over the share (it
+// publishes one segment after the other) and an idle one.
 // TMEM: S at N (tile & 1), O^T at 2 N + N block.
 #include <float.h>
 
@@ -40,12 +41,7 @@ namespace fattn {
 namespace {
 
 constexpr int kKeys = kLatentKeys;
-constexpr int kThreads = 256;
-constexpr int kMmaWarp = 4;
-constexpr int kLoadWarp = 5;
-constexpr int kWalkWarp = 6;
 constexpr int kSegs = 4;
-constexpr int kSegReaders = 6;
 constexpr float kLn2 = 0.69314718055994530942f;
 constexpr float kTau = 8.f;
 constexpr int kSmemMax = 232448;
@@ -53,6 +49,15 @@ constexpr int kValid = 8;             // tiles whose masks are kept; more than t
 
 template <int N, int R>
 struct Cfg {
+  // With 64 rows two warps share a quarter of tensor memory, 32 rows each.
+  static constexpr int kHalves = N == 64 ? 2 : 1;
+  static constexpr int kCols = N / kHalves;          // rows of a softmax warp
+  static constexpr int kSoftmax = 128 * kHalves;     // threads
+  static constexpr int kMmaWarp = 4 * kHalves;
+  static constexpr int kLoadWarp = kMmaWarp + 1;
+  static constexpr int kWalkWarp = kMmaWarp + 2;
+  static constexpr int kThreads = 32 * (kMmaWarp + 4);
+  static constexpr int kSegReaders = 4 * kHalves + 2;
   static constexpr int kChunks = R / 64 + 1;         // 64-column parts of a query; the rotated one first
   static constexpr int kPairs = R / 128;             // 128-column parts of a cached row
   static constexpr int kQChunk = N * 128;
@@ -85,8 +90,9 @@ struct Cfg {
   static constexpr int kSegOff = (kValidOff + 4 * kValid + 15) / 16 * 16;
   static constexpr int kXOff = kSegOff + kSegs * 48;            // [4][N] float
   static constexpr int kAlphaOff = kXOff + 16 * N;              // [N] float
-  static constexpr int kSmem = kAlphaOff + 4 * N;
-  static_assert(kSmem <= kSmemMax, "shared memory");
+  static constexpr int kLimOff = kAlphaOff + 4 * N;             // [N] int
+  static constexpr int kSmem = kLimOff + 4 * N;
+  static_assert(kSmem <= kSmemMax && kNumBars < kThreads, "shared memory");
   __device__ static constexpr uint32_t col_s(uint32_t buf) { return N * buf; }
   __device__ static constexpr uint32_t col_o(int pair) { return 2 * N + N * pair; }
   static_assert(2 * N + N * kPairs <= 512, "tensor memory");
@@ -122,9 +128,28 @@ __device__ __forceinline__ void tma_load_2d(uint32_t dst, const void* tmap, uint
       : "memory");
 }
 
+// Whether a phase has completed; unlike try_wait it does not stay to see.
+__device__ __forceinline__ bool bar_done(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return __all_sync(0xffffffffu, ok != 0);
+}
+
 // 16 lanes x N columns: thread t gets, for each 8 columns i, r[4 i], r[4 i + 1] of
 // lane t / 4, columns 8 i + 2 (t % 4) and the next, and r[4 i + 2], r[4 i + 3] of
 // lane t / 4 + 8.  Valid after the wait.
+__device__ __forceinline__ void tmem_ld_rows(uint32_t taddr, uint32_t (&r)[4]) {
+  asm volatile("tcgen05.ld.sync.aligned.16x256b.x1.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(taddr)
+               : "memory");
+}
 __device__ __forceinline__ void tmem_ld_rows(uint32_t taddr, uint32_t (&r)[8]) {
   asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
@@ -176,39 +201,71 @@ __device__ __forceinline__ void stmatrix_x4_trans(uint32_t addr, uint32_t a, uin
                "r"(c), "r"(d)
                : "memory");
 }
-// Barrier of the four softmax warps; true if `x` is in any thread.
-__device__ __forceinline__ bool softmax_any(bool x) {
+// Entry `first` + lane of a sequence's row of the page table; -1 past its end.
+__device__ __forceinline__ int page_of_lane(const LatentAttnArgs& a, int b, int len, int first) {
+  const int p = first + static_cast<int>(threadIdx.x & 31);
+  if ((static_cast<long long>(p) << a.page_shift) >= len) return -1;
+  return __ldg(a.s.table + static_cast<long long>(b) * a.s.max_pages + p);
+}
+// Barrier of the softmax warps; true if `x` is in any thread.
+template <int THREADS>
+__device__ __forceinline__ bool barrier_any(bool x) {
   uint32_t r;
   asm volatile(
       "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %1, 0;\n\t"
-      "barrier.cta.red.or.pred q, 1, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      "barrier.cta.red.or.pred q, 1, %2, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
       : "=r"(r)
-      : "r"(static_cast<uint32_t>(x))
+      : "r"(static_cast<uint32_t>(x)), "n"(THREADS)
       : "memory");
   return r != 0;
 }
-__device__ __forceinline__ void softmax_sync() { asm volatile("barrier.cta.sync 1, 128;" ::: "memory"); }
+template <int THREADS>
+__device__ __forceinline__ void barrier_sync() {
+  asm volatile("barrier.cta.sync 1, %0;" ::"n"(THREADS) : "memory");
+}
 
 // ------------------------------------------------------------------ schedule
 
-// A sequence's groups of `rows` rows in order, with the key tiles that each sees
-// (the quotient of its last row and the heads is carried along).
+// First tile of share c of W < 2^31 dealt to G <= 152 shares: floor(W c / G).
+__device__ __forceinline__ int share_first(int W, int G, int c) {
+  const int q = W / G;
+  return q * c + (W - q * G) * c / G;
+}
+
+// A sequence's groups of `rows` rows in order, with the key tiles that each sees.
+// The tokens before the group's end, end = tok * Hq + rem, are carried along, so that
+// long prompts cost no division a group.
 struct Groups {
-  long long rows, all;       // rows of a group and of the sequence
-  long long end;             // row behind the current group
+  int rows, all;             // rows of a group and of the sequence (T * Hq < 2^31 - 1024)
+  int end, tok, rem;
+  int dtok, drem;
   int len, n, Hq, causal;
-  __device__ __forceinline__ Groups(const LatentAttnArgs& a, const SeqInfo& q, int group_rows, long long first = 0)
-      : rows(group_rows), all(static_cast<long long>(q.n) * a.Hq), end((first + 1) * group_rows), len(q.len), n(q.n),
-        Hq(a.Hq), causal(a.causal) {}
+  __device__ __forceinline__ Groups(const LatentAttnArgs& a, const SeqInfo& q, int group_rows, int first = 0)
+      : rows(group_rows), all(q.n * a.Hq), end(group_rows), len(q.len), n(q.n), Hq(a.Hq), causal(a.causal) {
+    dtok = group_rows / Hq;
+    drem = group_rows - dtok * Hq;
+    tok = dtok;
+    rem = drem;
+    if (first > 0) {
+      end = static_cast<int>(min(static_cast<long long>(first + 1) * group_rows, 0x7fffffffll));
+      tok = end / Hq;
+      rem = end - tok * Hq;
+    }
+  }
   __device__ __forceinline__ bool live() const { return end - rows < all; }
-  __device__ __forceinline__ void next() { end += rows; }
+  __device__ __forceinline__ void next() {
+    end = static_cast<int>(min(static_cast<long long>(end) + rows, 0x7fffffffll));
+    tok += dtok;
+    rem += drem;
+    if (rem >= Hq) {
+      rem -= Hq;
+      ++tok;
+    }
+  }
   // At least one, so that rows that see nothing are written, too.
   __device__ __forceinline__ int tiles() const {
     int keys = len;
-    if (causal) {
-      const unsigned int e = static_cast<unsigned int>(min(end, all));   // T * Hq < 2^31
-      keys = len - n + static_cast<int>((e + Hq - 1) / Hq);
-    }
+    if (causal) keys = len - n + min(n, tok + (rem > 0 ? 1 : 0));
     return max(1, (keys + kKeys - 1) / kKeys);
   }
 };
@@ -227,11 +284,11 @@ static_assert(sizeof(Seg) == 48, "ring slot");
 struct Walker {
   const LatentAttnArgs& a;
   int group_rows;
-  long long left;           // tiles (and what units count beyond) still to walk
+  int left;                 // tiles (and what units count beyond) still to walk
   int b, rg, at, nt;
   SeqInfo q;
   __device__ __forceinline__ long long all_rows() const { return static_cast<long long>(q.n) * a.Hq; }
-  __device__ __forceinline__ Walker(const LatentAttnArgs& args, int rows, int first_b, long long rem, long long todo)
+  __device__ __forceinline__ Walker(const LatentAttnArgs& args, int rows, int first_b, int rem, int todo)
       : a(args), group_rows(rows), left(todo), b(first_b), rg(0), at(0), nt(0) {
     if (left <= 0) return;
     q = seq_info(a.s, b, a.page_shift);
@@ -243,7 +300,7 @@ struct Walker {
       g.next();
       nt = g.tiles();
     }
-    at = static_cast<int>(rem);
+    at = rem;
   }
   __device__ __forceinline__ bool next(Seg& s) {
     if (left <= 0) return false;
@@ -267,7 +324,7 @@ struct Walker {
     s.n = q.n;
     s.len = q.len;
     s.a = at;
-    s.e = static_cast<int>(min(static_cast<long long>(nt), at + left));
+    s.e = min(nt, at + left);
     s.nt = nt;
     s.flags = (at == 0 ? Seg::kStarts : 0) | (s.e == nt ? Seg::kEnds : 0);
     left -= s.e - s.a;
@@ -279,10 +336,11 @@ struct Walker {
 // ------------------------------------------------------------------ kernel
 
 template <int N, int R>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(Cfg<N, R>::kThreads, 1)
     latent_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_q,
                   const __grid_constant__ LatentAttnArgs args) {
   using C = Cfg<N, R>;
+  constexpr int kThreads = C::kThreads, kMmaWarp = C::kMmaWarp, kLoadWarp = C::kLoadWarp, kWalkWarp = C::kWalkWarp;
   extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t sbase = smem_u32(smem);
   const uint32_t bar0 = sbase + C::kBarOff;
@@ -302,6 +360,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   };
   float* xs = reinterpret_cast<float*>(smem + C::kXOff);          // [4][N]
   float* alphas = reinterpret_cast<float*>(smem + C::kAlphaOff);   // [N]
+  int* lims = reinterpret_cast<int*>(smem + C::kLimOff);           // [N]
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int share = blockIdx.x / args.span, block = blockIdx.x - share * args.span;
@@ -309,29 +368,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (!dcheck((sbase & 1023u) == 0u && C::kSmem <= static_cast<int>(dynamic_smem_bytes()) && share < G, args.status, 691))
     return;
 
-  if (tid == 0) {
-    for (int s = 0; s < C::kRing; ++s) {
-      mbar_init(pair_full(s), 1);
-      mbar_init(pair_empty(s), 1);
-    }
-    for (int s = 0; s < C::kRopes; ++s) {
-      mbar_init(rope_full(s), 1);
-      mbar_init(rope_empty(s), 1);
-    }
-    mbar_init(q_full, 1);
-    mbar_init(q_empty, 1);
-    mbar_init(s_full(0), 1);
-    mbar_init(s_full(1), 1);
-    mbar_init(p_full, 128);
-    mbar_init(pv_done, 1);
-    mbar_init(mma_done, 1);
-    for (int i = 0; i < kSegs; ++i) {
-      mbar_init(seg_full(i), 1);
-      mbar_init(seg_empty(i), kSegReaders);
-    }
-    misc[1] = 0u;
+  // The first sequence's numbers of each thread, on their way to the scan below.
+  const SeqCheck mine(args.s, tid);
+  if (tid < C::kNumBars) {
+    const uint32_t bar = bar0 + 8u * tid;
+    mbar_init(bar, bar == p_full ? C::kSoftmax : (bar >= seg_empty(0) ? C::kSegReaders : 1));
     fence_barrier_init();
   }
+  if (tid == C::kNumBars) misc[1] = 0u;
   if (warp == kMmaWarp) {
     tmem_alloc(smem_u32(&misc[0]), 512);
     tmem_relinquish();
@@ -340,22 +384,28 @@ __global__ void __launch_bounds__(kThreads, 1)
     tma_prefetch_desc(&tm_k);
     tma_prefetch_desc(&tm_q);
   }
-  // ---- the share: where its first tile lies.  The scan's scratch is in the masks'
-  // and references' place, which nothing uses yet.
-  long long W, j0, j1;
+  // ---- the share: where its first tile lies.  The scan's scratch is in the
+  // references' place, which nothing uses yet.
+  int W, j0, j1;
   {
     long long* wtot = reinterpret_cast<long long*>(xs);
     const int per = (args.s.B + kThreads - 1) / kThreads;
     const int b0 = min(args.s.B, tid * per), b1 = min(args.s.B, b0 + per);
-    auto weight = [&](int b, bool report) -> long long {
-      const SeqInfo q = seq_info(args.s, b, args.page_shift);
-      if (report && !q.ok && blockIdx.x == 0) record_bad_index(args.status, kSiteSeqStart);
+    auto info = [&](int b) {
+      return b == mine.b ? seq_info(args.s, mine.r0, mine.r1, mine.len, args.page_shift)
+                         : seq_info(args.s, b, args.page_shift);
+    };
+    auto weight = [&](const SeqInfo& q) {
       long long w = 0;
       for (Groups g(args, q, group_rows); g.live(); g.next()) w += g.tiles() + kLatentUnitCost;
       return w;
     };
     long long sum = 0;
-    for (int b = b0; b < b1; ++b) sum += weight(b, true);
+    for (int b = b0; b < b1; ++b) {
+      const SeqInfo q = info(b);
+      if (!q.ok && blockIdx.x == 0) record_bad_index(args.status, kSiteSeqStart);
+      sum += weight(q);
+    }
     long long incl = sum;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
@@ -370,13 +420,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       all += wtot[w];
     }
     W = total_of(all, args.status);
-    j0 = cta_first(W, G, share);
-    j1 = cta_first(W, G, share + 1);
+    j0 = share_first(W, G, share);
+    j1 = share_first(W, G, share + 1);
     if (j0 < j1 && at <= j0 && j0 < at + sum) {
       int b = b0;
-      for (long long w; b + 1 < b1 && at + (w = weight(b, false)) <= j0; ++b) at += w;
+      for (long long w; b + 1 < b1 && at + (w = weight(info(b))) <= j0; ++b) at += w;
       misc[4] = static_cast<uint32_t>(b);
-      misc[5] = static_cast<uint32_t>(j0 - at);    // W < 2^31
+      misc[5] = static_cast<uint32_t>(j0 - at);
     }
   }
   tc_fence_before();
@@ -394,14 +444,18 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto first_row = [&](const Seg& s) { return static_cast<long long>(s.rg) * group_rows + block * N; };
   auto rows_of = [&](const Seg& s) { return static_cast<long long>(s.n) * args.Hq; };
 
-  if (warp < 4) {
+  if (warp < kMmaWarp) {
     // ================================================================ softmax
-    constexpr int NC = N / 4;             // rows of a thread, two keys each
+    constexpr int NW = C::kCols, NC = NW / 4;   // rows of a warp; of a thread, two keys each
+    auto softmax_any = [](bool x) { return barrier_any<C::kSoftmax>(x); };
+    auto softmax_sync = [] { barrier_sync<C::kSoftmax>(); };
     const float c = args.scale_log2;
-    const int key_in = 16 * warp + (lane >> 2);
-    const uint32_t lane_off = static_cast<uint32_t>(warp * 32) << 16;
+    const int quarter = warp & 3, col0 = NW * (warp >> 2);
+    const int key_in = 16 * quarter + (lane >> 2);
+    const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
+    auto col_of = [&](int i) { return col0 + 8 * (i >> 1) + 2 * (lane & 3) + (i & 1); };
     uint32_t tiles = 0;                   // of this CTA so far: S and P V in turn
-    // All decisions that a barrier follows are the same in the four warps; a wait
+    // All decisions that a barrier follows are the same in these warps; a wait
     // that ran out makes the next vote end the loop for all.
     bool fail = false;
     for (uint32_t si = 0;; ++si) {
@@ -415,11 +469,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int live = static_cast<int>(min(static_cast<long long>(N), rows - row0));
       // Keys that a row sees.  Rows behind the block's last see all; nothing of theirs
       // is stored, and a row of S, P and O depends on its own query only.
-      auto lim_of = [&](int col) {
-        if (!args.causal || col >= live) return s.len;
-        return max(0, min(s.len, s.len - s.n + static_cast<int>(static_cast<unsigned int>(row0 + col) / args.Hq) + 1));
-      };
-      const int lim_min = lim_of(0);      // rows see no fewer keys than the first
+      if (tid < N) {
+        const int seen = s.len - s.n + static_cast<int>(static_cast<unsigned int>(row0 + tid) / args.Hq) + 1;
+        lims[tid] = args.causal && tid < live ? max(0, min(s.len, seen)) : s.len;
+      }
+      softmax_sync();
+      const int lim_min = lims[0];        // rows see no fewer keys than the first
       float m[NC], l[NC];
 #pragma unroll
       for (int i = 0; i < NC; ++i) {
@@ -430,12 +485,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int j = s.a; j < s.e; ++j, ++tiles) {
         const int kv0 = j * kKeys;
         const uint32_t pair0 = tiles * C::kPairs;
-        uint32_t x[N / 2];
+        uint32_t x[NW / 2];
         fail |= !wait_bar_warp(s_full(tiles & 1), (tiles >> 1) & 1, wc, kWaitSFull);
         // The masks came with the tile; its slots are not used again before P V.
         fail |= !wait_bar_warp(pair_full(pair0 % C::kRing), (pair0 / C::kRing) & 1, wc, kWaitKvFull);
         tc_fence_after();
-        tmem_ld_rows(tmem + lane_off + C::col_s(tiles & 1), x);
+        tmem_ld_rows(tmem + lane_off + C::col_s(tiles & 1) + col0, x);
         const uint32_t mask = valid[tiles % kValid];
         tmem_ld_wait(x);
         const bool edge = mask != 3u || kv0 + kKeys > s.len;
@@ -444,7 +499,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const bool there0 = mask >> (key_in >> 5) & 1u, there1 = mask >> ((key_in + 8) >> 5) & 1u;
 #pragma unroll
           for (int i = 0; i < NC; ++i) {
-            const int lim = lim_of(8 * (i >> 1) + 2 * (lane & 3) + (i & 1)) - kv0;
+            const int lim = lims[col_of(i)] - kv0;
             uint32_t& x0 = x[4 * (i >> 1) + (i & 1)];
             uint32_t& x1 = x[4 * (i >> 1) + 2 + (i & 1)];
             if (!there0 || key_in >= lim) x0 = __float_as_uint(-INFINITY);
@@ -464,7 +519,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mx[i] = fmaxf(s0(i), s1(i)) * c;
 #pragma unroll
             for (int off = 4; off < 32; off <<= 1) mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], off));
-            if (lane < 4) xs[warp * N + 8 * (i >> 1) + 2 * lane + (i & 1)] = mx[i];
+            if (lane < 4) xs[quarter * N + col_of(i)] = mx[i];
           }
           if (j > s.a) fail |= !wait_bar_warp(pv_done, (tiles - 1) & 1, wc, kWaitMmaDone);
           if (softmax_any(fail)) {
@@ -473,23 +528,24 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
 #pragma unroll
           for (int i = 0; i < NC; ++i) {
-            const int col = 8 * (i >> 1) + 2 * (lane & 3) + (i & 1);
+            const int col = col_of(i);
             const float t = fmaxf(fmaxf(xs[col], xs[N + col]), fmaxf(xs[2 * N + col], xs[3 * N + col]));
             const bool move = t > m[i] + kTau;
             const float al = move ? ex2_approx(m[i] - t) : 1.f;
             if (move) m[i] = t;
             l[i] *= al;
-            if (warp == 0 && lane < 4) alphas[col] = al;
+            if (quarter == 0 && lane < 4) alphas[col] = al;
           }
           softmax_sync();
           if (j > s.a) {
             tc_fence_after();
 #pragma unroll 1
-            for (int p = 0; p < C::kPairs * N / 16; ++p) {
+            for (int p = 0; p < C::kPairs * NW / 16; ++p) {
               uint32_t o[16];
-              const uint32_t at = tmem + lane_off + C::col_o(0) + 16 * p;
+              const int r0 = col0 + 16 * p % NW;
+              const uint32_t at = tmem + lane_off + C::col_o(16 * p / NW) + r0;
               tmem_ld16(at, o);
-              const float4* al = reinterpret_cast<const float4*>(alphas + (16 * p) % N);
+              const float4* al = reinterpret_cast<const float4*>(alphas + r0);
               tmem_ld_wait(o);
 #pragma unroll
               for (int z = 0; z < 4; ++z) {
@@ -505,7 +561,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         // ---- probabilities, bf16 pairs of neighbouring rows
-        uint32_t pk[N / 4];
+        uint32_t pk[NW / 4];
 #pragma unroll
         for (int i = 0; i < NC; i += 2) {
           const float p00 = ex2_approx(fmaf(s0(i), c, -m[i])), p01 = ex2_approx(fmaf(s0(i + 1), c, -m[i + 1]));
@@ -517,8 +573,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (tiles > 0) fail |= !wait_bar_warp(pv_done, (tiles - 1) & 1, wc, kWaitMmaDone);   // P is free
 #pragma unroll
-        for (int i = 0; i < N / 16; ++i) {
-          const int row = 16 * i + 8 * (lane >> 4) + (lane & 7), chunk = 2 * warp + (lane >> 3 & 1);
+        for (int i = 0; i < NW / 16; ++i) {
+          const int row = col0 + 16 * i + 8 * (lane >> 4) + (lane & 7), chunk = 2 * quarter + (lane >> 3 & 1);
           const uint32_t dst = sbase + C::kPOff + row * 128 + ((chunk ^ (lane & 7)) << 4);
           if (dcheck(in_range(dst, 16, sbase + C::kPOff, sbase + C::kRingOff), args.status, 692))
             stmatrix_x4_trans(dst, pk[4 * i], pk[4 * i + 1], pk[4 * i + 2], pk[4 * i + 3]);
@@ -527,7 +583,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           // Slots behind the end and pages that were not loaded hold anything, and zero
           // times a NaN is a NaN.
 #pragma unroll 1
-          for (int id = tid; id < C::kPairs * 2 * kKeys * 8; id += 128) {
+          for (int id = tid; id < C::kPairs * 2 * kKeys * 8; id += C::kSoftmax) {
             const int r = id >> 3 & (kKeys - 1), half = id >> 9;   // 8 pieces a row, 64 rows a half pair
             if (kv0 + r < s.len && (mask >> (r >> 5) & 1u)) continue;
             const uint32_t slot = (pair0 + (half >> 1)) % C::kRing;
@@ -546,9 +602,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int i = 0; i < NC; ++i) {
 #pragma unroll
         for (int off = 4; off < 32; off <<= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], off);
-        const int col = 8 * (i >> 1) + 2 * (lane & 3) + (i & 1);
-        if (lane < 4) xs[warp * N + col] = l[i];
-        if (warp == 0 && lane < 4) alphas[col] = m[i];
+        const int col = col_of(i);
+        if (lane < 4) xs[quarter * N + col] = l[i];
+        if (quarter == 0 && lane < 4) alphas[col] = m[i];
       }
       if (softmax_any(fail)) break;
       tc_fence_after();
@@ -559,7 +615,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         float lt = (xs[tid] + xs[N + tid]) + (xs[2 * N + tid] + xs[3 * N + tid]);
         const float mt = alphas[tid];
         // All scores of keys that the row sees are -inf: its query holds an infinity.
-        if (lt == 0.f && !holes && lim_of(tid) > s.a * kKeys) lt = __int_as_float(0x7fffffff);
+        if (lt == 0.f && !holes && lims[tid] > s.a * kKeys) lt = __int_as_float(0x7fffffff);
         if (tid < live) {
           if (whole) args.lse[out0 + tid] = lt == 0.f ? -INFINITY : (mt + log2f(lt)) * kLn2;
           else args.part_ml[slot * N + tid] = make_float2(mt, lt);
@@ -567,28 +623,53 @@ __global__ void __launch_bounds__(kThreads, 1)
         alphas[tid] = lt == 0.f ? 0.f : 1.f / lt;
       }
       softmax_sync();
+      if (whole) {
+        // Rows of O^T, half of the block's a turn: pairs of rows to bf16, transposed through
+        // this warp's part of P's place (32 columns a row, 16-byte chunks swizzled), so
+        // that a store has 16 bytes a lane.
+        constexpr int HB = NW / 2;
+        const uint32_t stage = sbase + C::kPOff + warp * HB * 64;
 #pragma unroll 1
-      for (int p = 0; p < C::kPairs * N / 16; ++p) {
-        const int pair = 16 * p / N, r0 = 16 * p % N;
-        if (r0 >= live) continue;
-        uint32_t o[16];
-        tmem_ld16(tmem + lane_off + C::col_o(0) + 16 * p, o);
-        tmem_ld_wait(o);
-        const int dim = 128 * pair + 32 * warp + lane;
-        if (whole) {
-          // Lanes hold neighbouring columns: two of them swap a row each, so that a
-          // store has two columns of one row.
+        for (int t = 0; t < 2 * C::kPairs; ++t) {
+          const int r0 = col0 + (t & 1) * HB;
+          if (r0 >= live) continue;
+          uint32_t lo[HB / 2], hi[HB / 2];          // columns 0 .. 15 and 16 .. 31 of the warp's
+          const uint32_t at = tmem + lane_off + C::col_o(t >> 1) + r0;
+          tmem_ld_rows(at, lo);
+          tmem_ld_rows(at + (16u << 16), hi);
+          tmem_ld_wait(lo);
+          tmem_ld_wait(hi);
+          __syncwarp();
 #pragma unroll
-          for (int z = 0; z < 16; z += 2) {
-            const float f0 = __uint_as_float(o[z]) * alphas[r0 + z], f1 = __uint_as_float(o[z + 1]) * alphas[r0 + z + 1];
-            const float got = __shfl_xor_sync(0xffffffffu, lane & 1 ? f0 : f1, 1);
-            const int row = r0 + z + (lane & 1);
-            if (row < live && dcheck(inside(out0 + row, 1, static_cast<long long>(args.s.T) * args.Hq), args.status, 694))
-              *reinterpret_cast<uint32_t*>(args.o + (out0 + row) * R + (dim & ~1)) =
-                  lane & 1 ? pack_bf16x2(got, f1) : pack_bf16x2(f0, got);
+          for (int i = 0; i < HB / 8; ++i) {
+            const float2 f = *reinterpret_cast<const float2*>(alphas + r0 + 8 * i + 2 * (lane & 3));
+            auto pair_of = [&](const uint32_t* r) {
+              return pack_bf16x2(__uint_as_float(r[0]) * f.x, __uint_as_float(r[1]) * f.y);
+            };
+            const int row = 8 * i + (lane & 7), chunk = lane >> 3;
+            stmatrix_x4_trans(stage + row * 64 + ((chunk ^ (row >> 1 & 3)) << 4), pair_of(lo + 4 * i), pair_of(lo + 4 * i + 2),
+                              pair_of(hi + 4 * i), pair_of(hi + 4 * i + 2));
           }
-        } else {
-          float* part = args.part_o + (slot * N + r0) * R + dim;
+          __syncwarp();
+#pragma unroll
+          for (int i = 0; i < HB / 8; ++i) {
+            const int row = 8 * i + (lane >> 2), chunk = lane & 3;
+            const uint4 w = ld_shared_v4(stage + row * 64 + ((chunk ^ (row >> 1 & 3)) << 4));
+            if (r0 + row < live &&
+                dcheck(inside(out0 + r0 + row, 1, static_cast<long long>(args.s.T) * args.Hq), args.status, 694))
+              *reinterpret_cast<uint4*>(args.o + (out0 + r0 + row) * R + 128 * (t >> 1) + 32 * quarter + 8 * chunk) = w;
+          }
+        }
+      } else {
+        // 16 rows at a time, a column a lane: whole lines.
+#pragma unroll 2
+        for (int p = 0; p < C::kPairs * NW / 16; ++p) {
+          const int pair = 16 * p / NW, r0 = col0 + 16 * p % NW;
+          if (r0 >= live) continue;
+          uint32_t o[16];
+          tmem_ld16(tmem + lane_off + C::col_o(pair) + r0, o);
+          float* part = args.part_o + (slot * N + r0) * R + 128 * pair + 32 * quarter + lane;
+          tmem_ld_wait(o);
 #pragma unroll
           for (int z = 0; z < 16; ++z)
             if (r0 + z < live && dcheck(slot < 2ll * kSms, args.status, 695)) part[z * R] = __uint_as_float(o[z]);
@@ -609,50 +690,75 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
       for (int k = 0; k < 4; ++k) mma_lead(d, da + 2 * k, db + 2 * k, idesc_s, k > 0 ? 1u : acc, lead);
     };
-    auto scores = [&](bool last) -> bool {
-      const uint32_t d = tmem + C::col_s(tiles & 1), slot = tiles % C::kRopes;
-      if (!wait_bar_warp(rope_full(slot), (tiles / C::kRopes) & 1, wc, kWaitKvFull)) return false;
-      tc_fence_after();
-      product4(d, sbase + C::kRopeOff + slot * C::kRopeTile, sbase + C::kQOff, 0u);
-      commit_lead(rope_empty(slot), lead);
-#pragma unroll
-      for (int p = 0; p < C::kPairs; ++p) {
-        const uint32_t at = tiles * C::kPairs + p, ps = at % C::kRing;
-        if (!wait_bar_warp(pair_full(ps), (at / C::kRing) & 1, wc, kWaitKvFull)) return false;
-        const uint32_t k = sbase + C::kRingOff + ps * C::kPairTile, q = sbase + C::kQOff + (1 + 2 * p) * C::kQChunk;
-        product4(d, k, q, 1u);
-        product4(d, k + C::kRopeTile, q + C::kQChunk, 1u);
-      }
-      commit_lead(s_full(tiles & 1), lead);
-      if (last) commit_lead(q_empty, lead);
-      ++tiles;
-      return true;
+    auto keep_waiting = [&](long long& t0) -> bool {
+      const long long now = clock64();
+      if (t0 == 0) t0 = now;
+      if (now - t0 > wc.budget && *wc.abort == 0u) *wc.abort = kWaitKvFull;
+      return __all_sync(0xffffffffu, *wc.abort == 0u);
     };
-    auto values = [&](uint32_t acc) -> bool {
-      if (!wait_bar_warp(p_full, pvs & 1, wc, kWaitPFull)) return false;
-      tc_fence_after();
+    // Slots and phases of the tile whose scores come next, and of the one whose values do.
+    uint32_t rs = 0, rph = 0, ks = 0, kph = 0, vs = 0;
+    auto values = [&](uint32_t acc) {
       const uint64_t db = sdesc_sw128(sbase + C::kPOff, 16, 1024);
 #pragma unroll
       for (int p = 0; p < C::kPairs; ++p) {
-        const uint32_t ps = (pvs * C::kPairs + p) % C::kRing;
-        const uint64_t da = sdesc_sw128(sbase + C::kRingOff + ps * C::kPairTile, C::kRopeTile, 1024);
+        const uint64_t da = sdesc_sw128(sbase + C::kRingOff + vs * C::kPairTile, C::kRopeTile, 1024);
 #pragma unroll
         for (int k = 0; k < 4; ++k)
           mma_lead(tmem + C::col_o(p), da + ((k * 2048) >> 4), db + 2 * k, idesc_o, k > 0 ? 1u : acc, lead);
-        commit_lead(pair_empty(ps), lead);
+        commit_lead(pair_empty(vs), lead);
+        vs = vs + 1 == C::kRing ? 0u : vs + 1;
       }
       commit_lead(pv_done, lead);
       ++pvs;
-      return true;
     };
     auto run = [&](const int n) -> bool {
       if (!wait_bar_warp(q_full, q_count++ & 1, wc, kWaitQFull)) return false;
       tc_fence_after();
-      for (int i = 0; i < n; ++i) {
-        if (!scores(i + 1 == n)) return false;
-        if (i > 0 && !values(i > 1 ? 1u : 0u)) return false;
+      for (int i = 0; i <= n; ++i) {
+        bool due = i > 0;                 // values of tile i - 1
+        if (i < n) {
+          // Scores of tile i.  While its first columns are not there, the values of the tile
+          // before go first where their probabilities are: a tile's slots are free only after
+          // that product, and behind scores that wait it would hold up the loads.
+          for (long long t0 = 0; !bar_done(rope_full(rs), rph) || !bar_done(pair_full(ks), kph);) {
+            if (due && bar_done(p_full, pvs & 1)) {
+              tc_fence_after();
+              values(i > 1 ? 1u : 0u);
+              due = false;
+            }
+            if (!keep_waiting(t0)) return false;
+          }
+          tc_fence_after();
+          const uint32_t d = tmem + C::col_s(tiles & 1);
+          product4(d, sbase + C::kRopeOff + rs * C::kRopeTile, sbase + C::kQOff, 0u);
+          commit_lead(rope_empty(rs), lead);
+          if (++rs == C::kRopes) {
+            rs = 0;
+            rph ^= 1u;
+          }
+#pragma unroll
+          for (int p = 0; p < C::kPairs; ++p) {
+            if (p > 0 && !wait_bar_warp(pair_full(ks), kph, wc, kWaitKvFull)) return false;
+            const uint32_t k = sbase + C::kRingOff + ks * C::kPairTile, q = sbase + C::kQOff + (1 + 2 * p) * C::kQChunk;
+            product4(d, k, q, 1u);
+            product4(d, k + C::kRopeTile, q + C::kQChunk, 1u);
+            if (++ks == C::kRing) {
+              ks = 0;
+              kph ^= 1u;
+            }
+          }
+          commit_lead(s_full(tiles & 1), lead);
+          if (i + 1 == n) commit_lead(q_empty, lead);
+          ++tiles;
+        }
+        if (due) {
+          if (!wait_bar_warp(p_full, pvs & 1, wc, kWaitPFull)) return false;
+          tc_fence_after();
+          values(i > 1 ? 1u : 0u);
+        }
       }
-      return values(n > 1 ? 1u : 0u);
+      return true;
     };
     for (uint32_t si = 0; wait_seg(si); ++si) {
       const Seg& s = seg_at(si);
@@ -688,27 +794,32 @@ __global__ void __launch_bounds__(kThreads, 1)
           tma_load_2d(sbase + C::kQOff + i * C::kQChunk, &tm_q, q_full, i == 0 ? R : 64 * (i - 1), row);
       }
       __syncwarp();
+      // 32 of the table's entries, one a lane, and the next 32 on their way.
+      int base = (s.a * kKeys) >> args.page_shift;
+      int cur = page_of_lane(args, s.b, s.len, base), nxt = page_of_lane(args, s.b, s.len, base + 32);
       for (int j = s.a; j < s.e; ++j, ++tiles) {
-        // The tile's pages: one, or two of 32 tokens.
-        int pid[2] = {-1, -1};
-        uint32_t mask = 0u;
-        for (int i = 0; i < boxes; ++i) {
-          const int t = j * kKeys + i * box;
-          if (t >= s.len) break;
-          const int p = __ldg(args.s.table + static_cast<long long>(s.b) * args.s.max_pages + (t >> args.page_shift));
-          if (p < 0 || p >= args.pages) {
-            if (lane == 0) record_bad_index(args.status, kSitePage);
-          } else {
-            pid[i] = p;
-            mask |= boxes == 1 ? 3u : 1u << i;
-          }
+        const int first = (j * kKeys) >> args.page_shift;
+        if (first >= base + 32) {
+          base += 32;
+          cur = nxt;
+          nxt = page_of_lane(args, s.b, s.len, base + 32);
         }
+        auto page_at = [&](int p) { return __shfl_sync(0xffffffffu, cur, p - base); };
+        // The tile's pages: one, or two of 32 tokens.
+        int pid0 = page_at(first), pid1 = boxes == 2 ? page_at(first + 1) : -1;
+        if (pid0 >= args.pages || pid1 >= args.pages || (pid0 < 0 && j * kKeys < s.len) ||
+            (boxes == 2 && pid1 < 0 && j * kKeys + box < s.len)) {
+          if (lane == 0) record_bad_index(args.status, kSitePage);
+          if (pid0 >= args.pages) pid0 = -1;
+          if (pid1 >= args.pages) pid1 = -1;
+        }
+        const uint32_t mask = (pid0 >= 0 ? (boxes == 1 ? 3u : 1u) : 0u) | (pid1 >= 0 ? 2u : 0u);
         const int row = (j * kKeys) & (page - 1);
         const uint32_t part = static_cast<uint32_t>(box) * 128u;
-        const uint32_t bytes = (pid[0] >= 0 ? part : 0u) + (pid[1] >= 0 ? part : 0u);
+        const uint32_t bytes = (pid0 >= 0 ? part : 0u) + (pid1 >= 0 ? part : 0u);
         auto load64 = [&](uint32_t dst, uint32_t bar, int col) {
-          if (pid[0] >= 0) tma_load_3d(dst, &tm_k, bar, col, row, pid[0]);
-          if (pid[1] >= 0) tma_load_3d(dst + part, &tm_k, bar, col, row, pid[1]);
+          if (pid0 >= 0) tma_load_3d(dst, &tm_k, bar, col, row, pid0);
+          if (pid1 >= 0) tma_load_3d(dst + part, &tm_k, bar, col, row, pid1);
         };
         const uint32_t rs = tiles % C::kRopes;
         if (tiles >= C::kRopes && !wait_bar_warp(rope_empty(rs), (tiles / C::kRopes - 1) & 1, wc, kWaitKvEmpty)) {
@@ -749,7 +860,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
   } else if (warp == kWalkWarp) {
     // ================================================================ schedule
-    Walker walk(args, group_rows, static_cast<int>(misc[4]), static_cast<long long>(misc[5]), j1 - j0);
+    Walker walk(args, group_rows, static_cast<int>(misc[4]), static_cast<int>(misc[5]), j1 - j0);
     Seg s{};
     bool any = false;
     for (uint32_t i = 0;; ++i) {
@@ -776,9 +887,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       // What is to be joined: the unit that this share starts and others go on with
       // (its last one).
       const bool shared_unit = any && (s.flags & (Seg::kStarts | Seg::kEnds)) == Seg::kStarts;
-      args.rec[2 * share] = shared_unit ? make_int4(s.r0, s.n, s.rg, 0) : make_int4(0, 0, 0, 0);
-      if (shared_unit)
-        args.rec[2 * share + 1] = make_int4(cta_of(W, G, j1 - (s.e - s.a) + s.nt - 1), static_cast<int>(W), 0, 0);
+      args.rec[2 * share] = shared_unit ? make_int4(s.r0, s.n, s.rg, cta_of(W, G, j1 - (s.e - s.a) + s.nt - 1))
+                                        : make_int4(0, 0, 0, 0);
+      args.rec[2 * share + 1] = make_int4(j0 < j1, 0, 0, 0);
     }
     __syncwarp();
   }
@@ -810,53 +921,89 @@ __device__ __forceinline__ void merge(Part& a, const Part& b) {
   a.o.w = fmaf(a.o.w, x, b.o.w * y);
 }
 
-// Block (s, y): rows of the unit that share s starts and others go on with.  Four
-// groups of threads have 4 columns each of a row: four rows where the parts are
-// few, a quarter of one row's parts where they are many.
+// The rows of the units that shares start and others go on with.  Four groups of
+// threads have 4 columns each of a row: four rows where a unit has few parts, a
+// quarter of one row's parts where it has many.  Every block counts the call's
+// items and takes its own, so that there are no more blocks than work.
 constexpr int kJoinGroups = 4;
 constexpr int kJoinMany = 6;
 
 template <int N, int R>
 __global__ void __launch_bounds__(kJoinGroups * R / 4) join_kernel(const LatentAttnArgs a) {
   __shared__ Part side[kJoinGroups][R / 4];
-  const int share = blockIdx.x, G = a.shares;
+  __shared__ int4 recs[kSms];
+  __shared__ int before[kSms + 1];
+  __shared__ unsigned char busy[kSms];
+  const int G = a.shares, tid = threadIdx.x;
   wait_for_parent();
-  const int4 rec = a.rec[2 * share];
-  if (rec.y == 0) return;
-  const int4 more = a.rec[2 * share + 1];
-  const long long W = more.y;
-  const long long first = static_cast<long long>(rec.z) * a.span * N;       // of the sequence's rows
-  const int rows = static_cast<int>(min(static_cast<long long>(a.span * N), static_cast<long long>(rec.y) * a.Hq - first));
-  const int q4 = threadIdx.x % (R / 4), group = threadIdx.x / (R / 4);
-  const bool many = more.x - share + 1 > kJoinMany;
-  const int row = many ? blockIdx.y : kJoinGroups * blockIdx.y + group;
-  if ((many ? row : kJoinGroups * static_cast<int>(blockIdx.y)) >= rows) return;
-  Part p{-FLT_MAX, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
-  if (row < rows) {
-    const int step = many ? kJoinGroups : 1;
-#pragma unroll 4
-    for (int t = share + (many ? group : 0); t <= more.x; t += step) {
-      if (cta_first(W, G, t) == cta_first(W, G, t + 1)) continue;   // a share without work
-      const long long at = (2ll * (t * a.span + row / N) + (t == share ? 1 : 0)) * N + row % N;
-      if (!dcheck(inside(at, 1, 2ll * kSms * N), a.status, 696)) continue;
-      const float2 ml = a.part_ml[at];
-      merge(p, Part{ml.x, ml.y, reinterpret_cast<const float4*>(a.part_o + at * R)[q4]});
+  auto first_of = [&](const int4& r) { return static_cast<long long>(r.z) * a.span * N; };   // of the sequence's rows
+  auto rows_of = [&](const int4& r) {
+    return static_cast<int>(min(static_cast<long long>(a.span * N), static_cast<long long>(r.y) * a.Hq - first_of(r)));
+  };
+  auto many = [&](int share, const int4& r) { return r.w - share + 1 > kJoinMany; };
+  for (int t = tid; t < G; t += blockDim.x) {
+    const int4 r = a.rec[2 * t];
+    recs[t] = r;
+    busy[t] = a.rec[2 * t + 1].x != 0;
+    before[t + 1] = r.y == 0 ? 0 : (many(t, r) ? rows_of(r) : (rows_of(r) + kJoinGroups - 1) / kJoinGroups);
+  }
+  if (tid == 0) before[0] = 0;
+  __syncthreads();
+  if (tid < 32) {                        // running sums, 32 shares at a time
+    int sum = 0;
+    for (int t0 = 0; t0 < G; t0 += 32) {
+      int x = t0 + tid < G ? before[t0 + tid + 1] : 0;
+#pragma unroll
+      for (int off = 1; off < 32; off <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, x, off);
+        if (tid >= off) x += y;
+      }
+      if (t0 + tid < G) before[t0 + tid + 1] = sum + x;
+      sum += __shfl_sync(0xffffffffu, x, 31);
     }
   }
-  if (many) {
-    side[group][q4] = p;
-    __syncthreads();
-    if (group != 0) return;
+  __syncthreads();
+  const int q4 = tid % (R / 4), group = tid / (R / 4);
+  for (int item = blockIdx.x; item < before[G]; item += gridDim.x) {
+    int share = 0;
+    for (int hi = G; hi - share > 1;) {
+      const int mid = (share + hi) >> 1;
+      if (before[mid] <= item) share = mid; else hi = mid;
+    }
+    const int4 rec = recs[share];
+    const bool split = many(share, rec);
+    const int rows = rows_of(rec), at_row = item - before[share];
+    const int row = split ? at_row : kJoinGroups * at_row + group;
+    Part p{-FLT_MAX, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
+    if (row < rows) {
+      const int step = split ? kJoinGroups : 1;
+#pragma unroll 4
+      for (int t = share + (split ? group : 0); t <= rec.w; t += step) {
+        if (!busy[t]) continue;
+        const long long at = (2ll * (t * a.span + row / N) + (t == share ? 1 : 0)) * N + row % N;
+        if (!dcheck(inside(at, 1, 2ll * kSms * N), a.status, 696)) continue;
+        const float2 ml = a.part_ml[at];
+        merge(p, Part{ml.x, ml.y, reinterpret_cast<const float4*>(a.part_o + at * R)[q4]});
+      }
+    }
+    if (split) {
+      side[group][q4] = p;
+      __syncthreads();
+      if (group == 0) {
 #pragma unroll
-    for (int g = 1; g < kJoinGroups; ++g) merge(p, side[g][q4]);
+        for (int g = 1; g < kJoinGroups; ++g) merge(p, side[g][q4]);
+      }
+      __syncthreads();
+      if (group != 0) continue;
+    }
+    if (row >= rows) continue;
+    const long long out = static_cast<long long>(rec.x) * a.Hq + first_of(rec) + row;
+    if (!dcheck(inside(out, 1, static_cast<long long>(a.s.T) * a.Hq), a.status, 697)) continue;
+    const float inv = p.l == 0.f ? 0.f : 1.f / p.l;
+    *reinterpret_cast<uint2*>(a.o + out * R + 4 * q4) =
+        make_uint2(pack_bf16x2(p.o.x * inv, p.o.y * inv), pack_bf16x2(p.o.z * inv, p.o.w * inv));
+    if (q4 == 0) a.lse[out] = p.l == 0.f ? -INFINITY : (p.m + log2f(p.l)) * kLn2;
   }
-  if (row >= rows) return;
-  const long long out = static_cast<long long>(rec.x) * a.Hq + first + row;
-  if (!dcheck(inside(out, 1, static_cast<long long>(a.s.T) * a.Hq), a.status, 697)) return;
-  const float inv = p.l == 0.f ? 0.f : 1.f / p.l;
-  *reinterpret_cast<uint2*>(a.o + out * R + 4 * q4) =
-      make_uint2(pack_bf16x2(p.o.x * inv, p.o.y * inv), pack_bf16x2(p.o.z * inv, p.o.w * inv));
-  if (q4 == 0) a.lse[out] = p.l == 0.f ? -INFINITY : (p.m + log2f(p.l)) * kLn2;
 }
 
 template <int N, int R>
@@ -865,10 +1012,11 @@ cudaError_t launch_t(const CUtensorMap& tk, const CUtensorMap& tq, const LatentA
   static SmemLimit limit;
   cudaError_t e = limit.raise(reinterpret_cast<const void*>(kern), Cfg<N, R>::kSmem);
   if (e != cudaSuccess) return e;
-  kern<<<a.span * a.shares, kThreads, Cfg<N, R>::kSmem, stream>>>(tk, tq, a);
+  kern<<<a.span * a.shares, Cfg<N, R>::kThreads, Cfg<N, R>::kSmem, stream>>>(tk, tq, a);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   if (a.shares == 1) return cudaSuccess;   // nothing is shared
-  return launch_child(join_kernel<N, R>, dim3(a.shares, a.span * N), kJoinGroups * R / 4, 0, stream, a);
+  const int rows = a.shares * a.span * N, most = kSms * 2048 / (kJoinGroups * R / 4);
+  return launch_child(join_kernel<N, R>, rows < most ? rows : most, kJoinGroups * R / 4, 0, stream, a);
 }
 
 }  // namespace
