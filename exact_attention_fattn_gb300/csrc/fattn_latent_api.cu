@@ -91,7 +91,7 @@ Workspace workspace_of(const Layout& l, int rank) {
   const size_t rows = 2ull * kSms * l.rows;
   w.ml_off = align256(rows * rank * sizeof(float));
   w.rec_off = w.ml_off + align256(rows * sizeof(float2));
-  w.total = w.rec_off + align256(2ull * kSms * sizeof(int4));
+  w.total = w.rec_off + align256(kSms * sizeof(int4));
   return w;
 }
 

@@ -386,7 +386,7 @@ __global__ void __launch_bounds__(Cfg<N, R>::kThreads, 1)
   }
   // ---- the share: where its first tile lies.  The scan's scratch is in the
   // references' place, which nothing uses yet.
-  int W, j0, j1;
+  int W, busy, j0, j1;
   {
     long long* wtot = reinterpret_cast<long long*>(xs);
     const int per = (args.s.B + kThreads - 1) / kThreads;
@@ -420,8 +420,9 @@ __global__ void __launch_bounds__(Cfg<N, R>::kThreads, 1)
       all += wtot[w];
     }
     W = total_of(all, args.status);
-    j0 = share_first(W, G, share);
-    j1 = share_first(W, G, share + 1);
+    busy = min(G, W);                     // no share is empty between others
+    j0 = share < busy ? share_first(W, busy, share) : 0;
+    j1 = share < busy ? share_first(W, busy, share + 1) : 0;
     if (j0 < j1 && at <= j0 && j0 < at + sum) {
       int b = b0;
       for (long long w; b + 1 < b1 && at + (w = weight(info(b))) <= j0; ++b) at += w;
@@ -887,9 +888,8 @@ __global__ void __launch_bounds__(Cfg<N, R>::kThreads, 1)
       // What is to be joined: the unit that this share starts and others go on with
       // (its last one).
       const bool shared_unit = any && (s.flags & (Seg::kStarts | Seg::kEnds)) == Seg::kStarts;
-      args.rec[2 * share] = shared_unit ? make_int4(s.r0, s.n, s.rg, cta_of(W, G, j1 - (s.e - s.a) + s.nt - 1))
-                                        : make_int4(0, 0, 0, 0);
-      args.rec[2 * share + 1] = make_int4(j0 < j1, 0, 0, 0);
+      args.rec[share] = shared_unit ? make_int4(s.r0, s.n, s.rg, cta_of(W, busy, j1 - (s.e - s.a) + s.nt - 1))
+                                    : make_int4(0, 0, 0, 0);
     }
     __syncwarp();
   }
@@ -926,14 +926,13 @@ __device__ __forceinline__ void merge(Part& a, const Part& b) {
 // quarter of one row's parts where it has many.  Every block counts the call's
 // items and takes its own, so that there are no more blocks than work.
 constexpr int kJoinGroups = 4;
-constexpr int kJoinMany = 6;
+constexpr int kJoinMany = 12;
 
 template <int N, int R>
 __global__ void __launch_bounds__(kJoinGroups * R / 4) join_kernel(const LatentAttnArgs a) {
   __shared__ Part side[kJoinGroups][R / 4];
   __shared__ int4 recs[kSms];
   __shared__ int before[kSms + 1];
-  __shared__ unsigned char busy[kSms];
   const int G = a.shares, tid = threadIdx.x;
   wait_for_parent();
   auto first_of = [&](const int4& r) { return static_cast<long long>(r.z) * a.span * N; };   // of the sequence's rows
@@ -942,9 +941,8 @@ __global__ void __launch_bounds__(kJoinGroups * R / 4) join_kernel(const LatentA
   };
   auto many = [&](int share, const int4& r) { return r.w - share + 1 > kJoinMany; };
   for (int t = tid; t < G; t += blockDim.x) {
-    const int4 r = a.rec[2 * t];
+    const int4 r = a.rec[t];
     recs[t] = r;
-    busy[t] = a.rec[2 * t + 1].x != 0;
     before[t + 1] = r.y == 0 ? 0 : (many(t, r) ? rows_of(r) : (rows_of(r) + kJoinGroups - 1) / kJoinGroups);
   }
   if (tid == 0) before[0] = 0;
@@ -976,14 +974,21 @@ __global__ void __launch_bounds__(kJoinGroups * R / 4) join_kernel(const LatentA
     const int row = split ? at_row : kJoinGroups * at_row + group;
     Part p{-FLT_MAX, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
     if (row < rows) {
+      // Four parts' loads go out together; behind the last one it is loaded again and not counted.
       const int step = split ? kJoinGroups : 1;
-#pragma unroll 4
-      for (int t = share + (split ? group : 0); t <= rec.w; t += step) {
-        if (!busy[t]) continue;
-        const long long at = (2ll * (t * a.span + row / N) + (t == share ? 1 : 0)) * N + row % N;
-        if (!dcheck(inside(at, 1, 2ll * kSms * N), a.status, 696)) continue;
-        const float2 ml = a.part_ml[at];
-        merge(p, Part{ml.x, ml.y, reinterpret_cast<const float4*>(a.part_o + at * R)[q4]});
+      for (int t0 = share + (split ? group : 0); t0 <= rec.w; t0 += 4 * step) {
+        Part x[4] = {};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int t = min(t0 + k * step, rec.w);
+          const long long at = (2ll * (t * a.span + row / N) + (t == share ? 1 : 0)) * N + row % N;
+          if (!dcheck(inside(at, 1, 2ll * kSms * N), a.status, 696)) continue;
+          const float2 ml = a.part_ml[at];
+          x[k] = Part{ml.x, ml.y, reinterpret_cast<const float4*>(a.part_o + at * R)[q4]};
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          if (t0 + k * step <= rec.w) merge(p, x[k]);
       }
     }
     if (split) {
