@@ -57,7 +57,6 @@ _cache_p = ctypes.POINTER(CacheStruct)
 _latent_p = ctypes.POINTER(LatentCacheStruct)
 _pool_p = ctypes.POINTER(PagePoolStruct)
 _plane_p = ctypes.POINTER(PlaneStruct)
-_ll_p = ctypes.POINTER(_c_ll)
 
 # name -> (restype, argtypes); the order of argtypes follows include/fattn.h
 SIGNATURES = {
@@ -96,8 +95,8 @@ SIGNATURES = {
     "fattn_cache_select_workspace_bytes": (_c_size, [_c_int, _c_int, _c_int]),
     "fattn_cache_select": (_c_int, [_cache_p, _vp, _c_ll, _vp, _vp, _vp, _vp, _c_int, _c_int,
                                     _c_int, _vp, _c_size, _c_int, _c_int, _c_int, _c_int, _vp]),
-    "fattn_rope": (_c_int, [_vp, _ll_p, _vp, _ll_p, _vp, _c_int, _c_int, _c_int, _c_int, _vp, _c_ll, _c_int, _c_int,
-                            _c_int, _c_int, _vp]),
+    "fattn_rope": (_c_int, [_vp, _c_ll, _c_ll, _c_ll, _vp, _c_ll, _c_ll, _c_ll, _vp, _c_int, _c_int, _c_int, _c_int,
+                            _vp, _c_ll, _c_int, _c_int, _c_int, _c_int, _vp]),
     "fattn_latent_append": (_c_int, [_latent_p, _vp, _c_ll, _vp, _c_ll, _vp, _c_ll, _c_ll, _vp, _c_int, _vp, _c_int,
                                      _c_int, _vp, _vp, _vp, _c_int, _c_int, _c_int, _vp]),
     "fattn_latent_fwd_workspace_bytes": (_c_size, [_c_int, _c_int, _c_int, _c_int]),

@@ -160,7 +160,8 @@ int fattn_latent_fwd(const fattn_latent_cache* cache, const void* q, void* o, fl
   if ((rc = check_batch(cache, page_table, q_start, kv_len, T, B, max_pages)) != FATTN_OK) return rc;
   if ((rc = check_heads(T, Hq)) != FATTN_OK) return rc;
   if (!q || !aligned(q, 16) || !o || !aligned(o, 16) || !lse || !aligned(lse, 4)) return FATTN_ERR_INVALID_ARG;
-  if (!isfinite(scale) || !(scale > 0.f)) return FATTN_ERR_INVALID_ARG;
+  const float scale_log2 = scale * 1.4426950408889634f;
+  if (!isfinite(scale_log2) || !(scale > 0.f)) return FATTN_ERR_INVALID_ARG;
   const Layout l = layout_of(T, B, Hq);
   const Workspace w = workspace_of(l, cache->rank);
   if (!workspace || !aligned(workspace, 256) || workspace_bytes < w.total) return FATTN_ERR_INVALID_ARG;
@@ -175,8 +176,7 @@ int fattn_latent_fwd(const fattn_latent_cache* cache, const void* q, void* o, fl
   a.page_shift = page_shift(cache->page);
   a.Hq = Hq;
   a.causal = causal != 0;
-  a.scale_log2 = scale * 1.4426950408889634f;
-  if (!(a.scale_log2 > 0.f) || !isfinite(a.scale_log2)) return FATTN_ERR_INVALID_ARG;
+  a.scale_log2 = scale_log2;
   char* base = static_cast<char*>(workspace);
   a.part_o = reinterpret_cast<float*>(base);
   a.part_ml = reinterpret_cast<float2*>(base + w.ml_off);

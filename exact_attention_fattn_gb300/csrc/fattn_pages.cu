@@ -165,64 +165,70 @@ __global__ void __launch_bounds__(128) free_kernel(const Tables t, int* kv_len, 
 // ------------------------------------------------------------------ extend
 
 // Sequences from old_len to new_len tokens, in order: one whose next token falls
-// into a page that others name too gets a copy of it (the last of those that
-// write to it keeps it), and all get the pages they lack.
+// into a page that others name too gets a copy of it, but the last of those that
+// name it, if all of them write to it, keeps it; and all get the pages they lack.
+// A thread has up to kPerThread neighbouring sequences.  Whether a page's writers
+// are all that name it, and which is the last, two counters a page tell (`writers`,
+// `last`; sums and maxima, so their order does not matter).
+constexpr int kPerThread = kMaxSeqs / kScanThreads;
+constexpr int kOwnPages = 8;             // new pages that a sequence's own thread enters; more go to its warp
+
 __global__ void __launch_bounds__(kScanThreads) extend_kernel(const Tables t, const int* old_len, const int* new_len,
-                                                              int* free_list, CopyList list) {
+                                                              int* free_list, int* writers, int* last, CopyList list) {
   __shared__ long long side[32];
-  __shared__ __align__(16) int tails[kMaxSeqs];   // shared last page that sequence b writes to, or -1
-  __shared__ int starts[kMaxSeqs];      // pages taken by earlier sequences, times two, + 1 if b gets a copy
   __shared__ int found_all;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int tid = threadIdx.x, lane = tid & 31;
   allow_child();
-  auto lens = [&](int b, int& o, int& w) {
-    o = old_len[b];
-    w = new_len[b];
-    if (o >= 0 && w >= o && w <= t.cap()) return true;
-    o = w = 0;
-    return false;
-  };
-  for (int b = tid; b < t.B; b += kScanThreads) {
-    int o, w, tail = -1;
-    if (!lens(b, o, w)) record_bad_index(t.status, kSiteSeqStart);
+  const int per = (t.B + kScanThreads - 1) / kScanThreads, b0 = tid * per;
+  int tail[kPerThread], k0[kPerThread], k1[kPerThread], slot[kPerThread];   // shared last page, or -1; entries; the page's
+#pragma unroll
+  for (int i = 0; i < kPerThread; ++i) {
+    const int b = b0 + i;
+    tail[i] = -1;
+    k0[i] = k1[i] = slot[i] = 0;
+    if (i >= per || b >= t.B) continue;
+    const int o = old_len[b], w = new_len[b];
+    if (o < 0 || w < o || w > t.cap()) {
+      record_bad_index(t.status, kSiteSeqStart);
+      continue;
+    }
+    k0[i] = t.held(o);
+    k1[i] = t.held(w);
+    slot[i] = o >> t.page_shift;
     if (w > o && (o & ((1 << t.page_shift) - 1)) != 0) {
-      const int p = t.table[static_cast<long long>(b) * t.max_pages + (o >> t.page_shift)];
+      const int p = t.table[static_cast<long long>(b) * t.max_pages + slot[i]];
       if (!t.is_page(p)) record_bad_index(t.status, kSitePage);
-      else if (t.refs[p] >= 2) tail = p;
+      else if (t.refs[p] >= 2) tail[i] = p;
     }
-    tails[b] = tail;
+    if (tail[i] >= 0) {
+      writers[tail[i]] = 0;
+      last[tail[i]] = -1;
+    }
   }
-  __syncthreads();
-  // ---- pages that each sequence takes, and which of them are copies
-  const int per = (t.B + kScanThreads - 1) / kScanThreads;
-  const int b0 = min(t.B, tid * per), b1 = min(t.B, b0 + per);
-  long long sum = 0;                     // pages, and copies in the upper half
-  for (int b = b0; b < b1; ++b) {
-    int copy = 0;
-    if (tails[b] >= 0) {
-      int before = 0;
-      const int tail = tails[b];
-      int e = 0;
-      for (; e + 4 <= b; e += 4) {
-        const int4 x = *reinterpret_cast<const int4*>(tails + e);
-        before += (x.x == tail) + (x.y == tail) + (x.z == tail) + (x.w == tail);
+  const bool shared_tails = __syncthreads_or(tail[0] >= 0 || tail[1] >= 0 || tail[2] >= 0 || tail[3] >= 0);
+  static_assert(kPerThread == 4, "sequences of a thread");
+  if (shared_tails) {
+#pragma unroll
+    for (int i = 0; i < kPerThread; ++i)
+      if (tail[i] >= 0) {
+        atomicAdd(writers + tail[i], 1);
+        atomicMax(last + tail[i], b0 + i);
       }
-      for (; e < b; ++e) before += tails[e] == tail;
-      copy = t.refs[tails[b]] - before >= 2 ? 1 : 0;
-    }
-    int o, w;
-    lens(b, o, w);
-    starts[b] = copy;
-    sum += (static_cast<long long>(copy) << 40) + copy + t.held(w) - t.held(o);
+    __syncthreads();
+  }
+  // ---- pages that each sequence takes, copies in the upper half of the sum
+  long long sum = 0;
+#pragma unroll
+  for (int i = 0; i < kPerThread; ++i) {
+    if (tail[i] >= 0 && __ldcg(writers + tail[i]) >= t.refs[tail[i]] && __ldcg(last + tail[i]) == b0 + i) tail[i] = -1;
+    sum += (tail[i] >= 0 ? (1ll << 40) + 1 : 0ll) + k1[i] - k0[i];
   }
   long long total;
   long long at = block_scan(sum, side, total);
   const long long want = total & ((1ll << 40) - 1);
   // ---- the lowest free pages
-  if (tid == 0) found_all = want <= t.pages;
-  __syncthreads();
-  if (found_all) {
-    long long seen = 0;
+  long long seen = 0;
+  if (want <= t.pages) {
     for (long long base = 0; base < t.pages && seen < want; base += kScanThreads * kScanPages) {
       int r[kScanPages], n = 0;
       const int first = static_cast<int>(min(base + tid * kScanPages, static_cast<long long>(t.pages)));
@@ -239,10 +245,9 @@ __global__ void __launch_bounds__(kScanThreads) extend_kernel(const Tables t, co
         }
       seen += all;
     }
-    __syncthreads();
-    if (tid == 0) found_all = seen >= want;
-    __syncthreads();
   }
+  if (tid == 0) found_all = seen >= want;
+  __syncthreads();                       // and the list is there
   const bool granted = found_all;
   if (tid == 0) {
     *list.count = granted ? static_cast<int>(total >> 40) : 0;
@@ -251,35 +256,37 @@ __global__ void __launch_bounds__(kScanThreads) extend_kernel(const Tables t, co
       t.status->block = 0u;
     }
   }
-  // ---- copies, and where each sequence's pages begin (a call that takes more than the
-  // pool has was refused above, so the starts fit)
-  for (int b = b0; b < b1; ++b) {
-    int o, w;
-    lens(b, o, w);
-    const int copy = starts[b], begin = granted ? static_cast<int>(at & ((1ll << 40) - 1)) : 0;
-    starts[b] = 2 * begin + copy;
-    if (copy && granted) {
-      const int i = static_cast<int>(at >> 40), to = free_list[begin];
-      if (dcheck(inside(i, 1, t.B) && inside(begin, 1, t.pages), t.status, 672)) {
-        list.src[i] = tails[b];
-        list.dst[i] = to;
-        t.table[static_cast<long long>(b) * t.max_pages + (o >> t.page_shift)] = to;
-        atomicSub(t.refs + tails[b], 1);
+  // ---- copies and new entries
+#pragma unroll
+  for (int i = 0; i < kPerThread; ++i) {
+    int* row = t.table + static_cast<long long>(b0 + i) * t.max_pages;
+    int begin = granted ? static_cast<int>(at & ((1ll << 40) - 1)) : 0;
+    const int copy = tail[i] >= 0 ? 1 : 0, fresh = k1[i] - k0[i];
+    if (copy != 0 && granted) {
+      const int c = static_cast<int>(at >> 40), to = free_list[begin];
+      if (dcheck(inside(c, 1, t.B) && inside(begin, 1, t.pages), t.status, 672)) {
+        list.src[c] = tail[i];
+        list.dst[c] = to;
+        row[slot[i]] = to;
+        atomicSub(t.refs + tail[i], 1);
       }
+      ++begin;
     }
-    at += (static_cast<long long>(copy) << 40) + copy + t.held(w) - t.held(o);
+    at += (static_cast<long long>(copy) << 40) + copy + fresh;
+    if (fresh <= kOwnPages)
+      for (int k = 0; k < fresh; ++k)
+        if (dcheck(inside(k0[i] + k, 1, t.max_pages), t.status, 673)) row[k0[i] + k] = granted ? free_list[begin + k] : -1;
+    // a warp to a sequence that takes many
+    for (unsigned int many = __ballot_sync(0xffffffffu, fresh > kOwnPages); many != 0u; many &= many - 1) {
+      const int src = __ffs(many) - 1;
+      const int first = __shfl_sync(0xffffffffu, k0[i], src), n = __shfl_sync(0xffffffffu, fresh, src);
+      const int from = __shfl_sync(0xffffffffu, begin, src), b = __shfl_sync(0xffffffffu, b0 + i, src);
+      int* to = t.table + static_cast<long long>(b) * t.max_pages + first;
+      for (int k = lane; k < n; k += 32)
+        if (dcheck(inside(first + k, 1, t.max_pages), t.status, 676)) to[k] = granted ? free_list[from + k] : -1;
+    }
   }
-  __syncthreads();
   for (int i = tid; granted && i < want; i += kScanThreads) t.refs[free_list[i]] = 1;
-  // ---- new entries, a warp to a sequence
-  for (int b = warp; b < t.B; b += kScanThreads / 32) {
-    int o, w;
-    lens(b, o, w);
-    const int k0 = t.held(o), k1 = t.held(w), begin = (starts[b] >> 1) + (starts[b] & 1);
-    int* row = t.table + static_cast<long long>(b) * t.max_pages;
-    for (int k = k0 + lane; k < k1; k += 32)
-      if (dcheck(inside(k, 1, t.max_pages), t.status, 673)) row[k] = granted ? free_list[begin + k - k0] : -1;
-  }
 }
 
 // ------------------------------------------------------------------ compact
@@ -290,9 +297,11 @@ __global__ void __launch_bounds__(kScanThreads) plan_kernel(const Tables t, int*
   __shared__ long long side[32];
   const int tid = threadIdx.x;
   allow_child();
+  // Pools of up to one turn's pages keep their counts in registers for the second look.
+  const bool once = t.pages <= kScanThreads * kScanPages;
+  int r[kScanPages];
   long long held = 0;
   for (long long base = 0; base < t.pages; base += kScanThreads * kScanPages) {
-    int r[kScanPages];
     load_refs(t.refs, t.pages, static_cast<int>(min(base + tid * kScanPages, static_cast<long long>(t.pages))), 0, r);
 #pragma unroll
     for (int i = 0; i < kScanPages; ++i) held += r[i] > 0 ? 1 : 0;
@@ -301,9 +310,8 @@ __global__ void __launch_bounds__(kScanThreads) plan_kernel(const Tables t, int*
   block_scan(held, side, total);
   long long seen = 0;                    // holes, and pages to move in the upper half
   for (long long base = 0; base < t.pages; base += kScanThreads * kScanPages) {
-    int r[kScanPages];
     const int first = static_cast<int>(min(base + tid * kScanPages, static_cast<long long>(t.pages)));
-    load_refs(t.refs, t.pages, first, 0, r);
+    if (!once) load_refs(t.refs, t.pages, first, 0, r);
     long long n = 0;
 #pragma unroll
     for (int i = 0; i < kScanPages; ++i) {
@@ -451,9 +459,9 @@ Tables tables_of(const fattn_page_pool* pool, int* page_table, int B, int max_pa
   return t;
 }
 
-// count and limit, then two lists of pages, then one entry a page
+// count and limit, then two lists of pages, then three numbers a page
 struct PagesWorkspace {
-  size_t src, dst, map, total;
+  size_t src, dst, map, writers, last, total;
 };
 PagesWorkspace workspace_of(int pages, int B) {
   PagesWorkspace w;
@@ -461,7 +469,10 @@ PagesWorkspace workspace_of(int pages, int B) {
   w.src = 256;
   w.dst = w.src + list;
   w.map = w.dst + list;
-  w.total = w.map + align256(static_cast<size_t>(pages) * sizeof(int));
+  const size_t each = align256(static_cast<size_t>(pages) * sizeof(int));
+  w.writers = w.map + each;
+  w.last = w.writers + each;
+  w.total = w.last + each;
   return w;
 }
 
@@ -532,7 +543,9 @@ int fattn_pages_extend(const fattn_page_pool* pool, const fattn_plane* planes, i
                       reinterpret_cast<int*>(base + w.dst)};
   const Tables t = tables_of(pool, page_table, B, max_pages, status);
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  extend_kernel<<<1, kScanThreads, 0, st>>>(t, old_len, new_len, reinterpret_cast<int*>(base + w.map), list);
+  extend_kernel<<<1, kScanThreads, 0, st>>>(t, old_len, new_len, reinterpret_cast<int*>(base + w.map),
+                                          reinterpret_cast<int*>(base + w.writers),
+                                          reinterpret_cast<int*>(base + w.last), list);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return FATTN_ERR_CUDA;
   const int grid = copy_grid(static_cast<long long>(B) * p.pieces);

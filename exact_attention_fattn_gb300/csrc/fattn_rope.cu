@@ -167,19 +167,20 @@ bool strides_ok(const long long* s, int B, int H, int N, int d, bool written) {
 
 using namespace fattn;
 
-extern "C" int fattn_rope(const void* x, const long long* x_strides, void* y, const long long* y_strides,
-                          const float* rope, int rope_len, int rope_dim, int interleaved, int transposed,
-                          const int* positions, long long positions_stride, int B, int H, int N, int d,
+extern "C" int fattn_rope(const void* x, long long x_b, long long x_h, long long x_n, void* y, long long y_b,
+                          long long y_h, long long y_n, const float* rope, int rope_len, int rope_dim, int interleaved,
+                          int transposed, const int* positions, long long positions_b, int B, int H, int N, int d,
                           fattn_stream_t stream) {
   struct Range {
     Range() { nvtxRangePushA("fattn_rope"); }
     ~Range() { nvtxRangePop(); }
   } const range;
   if (d <= 0 || d > 1024 || d % 16 != 0) return FATTN_ERR_UNSUPPORTED;
-  if (B <= 0 || H <= 0 || N <= 0 || !x || !y || !x_strides || !y_strides || !rope) return FATTN_ERR_INVALID_ARG;
+  if (B <= 0 || H <= 0 || N <= 0 || !x || !y || !rope) return FATTN_ERR_INVALID_ARG;
   if (!aligned(x, 16) || !aligned(y, 16) || !aligned(rope, 16) || !aligned(positions, 4)) return FATTN_ERR_INVALID_ARG;
   if (rope_len <= 0 || rope_dim <= 0 || rope_dim > d || rope_dim % 16 != 0) return FATTN_ERR_INVALID_ARG;
-  if (positions_stride < 0 || positions_stride >= (1ll << 40)) return FATTN_ERR_INVALID_ARG;
+  if (positions_b < 0 || positions_b >= (1ll << 40)) return FATTN_ERR_INVALID_ARG;
+  const long long x_strides[3] = {x_b, x_h, x_n}, y_strides[3] = {y_b, y_h, y_n};
   if (!strides_ok(x_strides, B, H, N, d, false) || !strides_ok(y_strides, B, H, N, d, true))
     return FATTN_ERR_INVALID_ARG;
   const bool same = x == y;
@@ -190,15 +191,15 @@ extern "C" int fattn_rope(const void* x, const long long* x_strides, void* y, co
   RopeArgs a{};
   a.x = static_cast<const uint16_t*>(x);
   a.y = static_cast<uint16_t*>(y);
-  a.xb = x_strides[0], a.xh = x_strides[1], a.xn = x_strides[2];
-  a.yb = y_strides[0], a.yh = y_strides[1], a.yn = y_strides[2];
+  a.xb = x_b, a.xh = x_h, a.xn = x_n;
+  a.yb = y_b, a.yh = y_h, a.yn = y_n;
   a.rope = rope;
   a.rope_len = rope_len;
   a.rope_dim = rope_dim;
   a.interleaved = interleaved != 0;
   a.transposed = transposed != 0;
   a.positions = positions;
-  a.pos_stride = positions_stride;
+  a.pos_stride = positions_b;
   a.B = B, a.H = H, a.N = N, a.d = d;
   a.items = (same ? rope_dim : d) / 16;
   // Four heads a thread where that leaves work for all SMs, one where it does not.

@@ -10,7 +10,8 @@ from typing import NamedTuple
 import torch
 
 from . import _lib
-from .cache import PAGE_SIZES, Fp8Cache, _call, _check_cache, _workspace
+from .cache import (PAGE_SIZES, Fp8Cache, _call, _check_cache, _current_device, _raw_alloc, _raw_free, _raw_stream,
+                    _workspace)
 from .latent import LatentCache, _check_latent
 
 
@@ -77,6 +78,23 @@ def fattn_pages_workspace_bytes(pages: int, B: int) -> int:
     return int(_lib.load().fattn_pages_workspace_bytes(pages, B))
 
 
+def _with_workspace(fn, ps, dev, workspace, page_table, before, after):
+    """fn(pool, *before, workspace, its bytes, *after)."""
+    need = fattn_pages_workspace_bytes(ps.pages, page_table.shape[0])
+    scratch = 0
+    if workspace is None and need and _raw_alloc and _raw_free and _current_device() == dev:
+        # as in fattn_cache_fwd: a block that the stream's next calls may have
+        scratch = ws_ptr = _raw_alloc(need, _raw_stream(dev))
+    else:
+        ws = _workspace(workspace, need, page_table.device, dev)
+        ws_ptr, need = ws.data_ptr(), ws.numel()
+    try:
+        _call(fn, dev, ctypes.byref(ps), *before, ws_ptr, need, *after)
+    finally:
+        if scratch:
+            _raw_free(scratch)
+
+
 def fattn_pages_fork(pool: PagePool, cache, page_table, kv_len, parent, child):
     """Sequence child[i] (int32 [n], of length 0) becomes a copy of sequence
     parent[i]: its table entries, its length, and its pages counted once more.
@@ -98,9 +116,8 @@ def fattn_pages_extend(pool: PagePool, cache, page_table, old_len, new_len, work
     ``page_table``, the counts and the copies; lengths stay.  With too few free
     pages nobody gets any, and fattn_check_status() returns 8."""
     ps, planes, dev, (B, max_pages) = _setup(pool, cache, page_table, old_len, new_len)
-    ws = _workspace(workspace, fattn_pages_workspace_bytes(ps.pages, B), page_table.device, dev)
-    _call(_lib.load().fattn_pages_extend, dev, ctypes.byref(ps), planes, len(planes), page_table.data_ptr(),
-          old_len.data_ptr(), new_len.data_ptr(), ws.data_ptr(), ws.numel(), B, max_pages)
+    _with_workspace(_lib.load().fattn_pages_extend, ps, dev, workspace, page_table,
+                    (planes, len(planes), page_table.data_ptr(), old_len.data_ptr(), new_len.data_ptr()), (B, max_pages))
 
 
 def fattn_pages_free(pool: PagePool, cache, page_table, kv_len, rows):
@@ -119,6 +136,5 @@ def fattn_pages_compact(pool: PagePool, cache, page_table, kv_len, workspace=Non
     and the table.  ``kv_len`` says how many entries each sequence holds: the
     lengths that room was made for."""
     ps, planes, dev, (B, max_pages) = _setup(pool, cache, page_table, kv_len)
-    ws = _workspace(workspace, fattn_pages_workspace_bytes(ps.pages, B), page_table.device, dev)
-    _call(_lib.load().fattn_pages_compact, dev, ctypes.byref(ps), planes, len(planes), page_table.data_ptr(),
-          kv_len.data_ptr(), ws.data_ptr(), ws.numel(), B, max_pages)
+    _with_workspace(_lib.load().fattn_pages_compact, ps, dev, workspace, page_table,
+                    (planes, len(planes), page_table.data_ptr(), kv_len.data_ptr()), (B, max_pages))

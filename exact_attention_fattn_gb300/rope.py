@@ -2,14 +2,10 @@
 
 from __future__ import annotations
 
-import ctypes
-
 import torch
 
 from . import _lib
 from .cache import _call
-
-_Strides = ctypes.c_longlong * 3
 
 
 def _view(t, name, d, dev):
@@ -21,9 +17,7 @@ def _view(t, name, d, dev):
     s = t.stride()
     if t.shape[-1] != d or (d > 1 and s[-1] != 1):
         raise ValueError(f"the columns of {name} must be contiguous")
-    if len(s) == 3:
-        return _Strides(0, s[1], s[0])
-    return _Strides(s[0], s[1], s[2])
+    return (0, s[1], s[0]) if len(s) == 3 else s[:3]
 
 
 def _rotate(name, x, rope, positions, interleaved, transposed, out):
@@ -61,7 +55,7 @@ def _rotate(name, x, rope, positions, interleaved, transposed, out):
     rope_len, rope_dim = rope.shape
     if B * H * N == 0:
         return out
-    _call(_lib.load().fattn_rope, dev, x.data_ptr(), xs, out.data_ptr(), ys, rope.data_ptr(), rope_len, rope_dim,
+    _call(_lib.load().fattn_rope, dev, x.data_ptr(), *xs, out.data_ptr(), *ys, rope.data_ptr(), rope_len, rope_dim,
           1 if interleaved else 0, 1 if transposed else 0, pos, pos_stride, B, H, N, d)
     return out
 

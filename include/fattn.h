@@ -413,20 +413,20 @@ int fattn_cache_select(const fattn_cache* cache, const void* q, long long q_row,
  * transposed != 0 by the negated angles: the gradient, dx = R^T dy.  Pairs, the
  * table (fp32 [rope_len, rope_dim]) and the arithmetic (fp32, every product and sum
  * rounded, then one rounding to bf16) are those of fattn_cache_append.
- *   x, y       : bf16 rows of d columns, row (b, h, n) of [B, H, N, d] at
- *                b strides[0] + h strides[1] + n strides[2] elements; strides are multiples of 8,
- *                from 0 (x only) up to 2^40, and rows of y do not overlap.  y may be x with the same
- *                strides, and then only the rotated columns are touched; otherwise
- *                they share no element.  d is a multiple of 16 up to 1024 (FATTN_ERR_UNSUPPORTED)
- *   positions  : int, row (b, n) at positions[b * positions_stride + n] (0: the same for all
- *                b), or NULL: n.  Rows whose position is outside [0, rope_len) are not
- *                written and are FATTN_ERR_BAD_INDEX
+ *   x, y       : bf16 rows of d columns, row (b, h, n) of [B, H, N, d] at b x_b + h x_h + n x_n
+ *                elements; these are multiples of 8 from 0 (x only) up to 2^40, and rows
+ *                of y do not overlap.  y may be x with the same distances, and then only the
+ *                rotated columns are touched; otherwise they share no element.  d is a multiple
+ *                of 16 up to 1024 (FATTN_ERR_UNSUPPORTED)
+ *   positions  : int, row (b, n) at positions[b * positions_b + n] (0: the same for all b), or
+ *                NULL: n.  Rows whose position is outside [0, rope_len) are not written
+ *                and are FATTN_ERR_BAD_INDEX
  * rope_dim is a multiple of 16 up to d.  Returns a fattn_status.
  */
-int fattn_rope(const void* x, const long long* x_strides, void* y, const long long* y_strides,
-               const float* rope, int rope_len, int rope_dim, int interleaved, int transposed,
-               const int* positions, long long positions_stride, int B, int H, int N, int d,
-               fattn_stream_t stream);
+int fattn_rope(const void* x, long long x_b, long long x_h, long long x_n, void* y, long long y_b,
+               long long y_h, long long y_n, const float* rope, int rope_len, int rope_dim,
+               int interleaved, int transposed, const int* positions, long long positions_b, int B,
+               int H, int N, int d, fattn_stream_t stream);
 
 /*
  * Attention over a paged latent cache
