@@ -120,10 +120,14 @@ __device__ __forceinline__ void commit_lead(uint32_t bar, uint32_t lead) {
       "r"(lead)
       : "memory");
 }
-__device__ __forceinline__ void tma_load_2d(uint32_t dst, const void* tmap, uint32_t bar, int c0, int c1) {
+// Copies from a converged warp, one lane of it elected by each: under a branch on
+// the lane a copy's issue takes several times as long (a tile's nine 1700
+// cycles), as an MMA's does.
+__device__ __forceinline__ void tma_load_2d_w(uint32_t dst, const void* tmap, uint32_t bar, int c0, int c1) {
   asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%3, %4}], [%2];" ::"r"(dst),
+      "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+      "@e cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4}], [%2];\n\t}" ::"r"(dst),
       "l"(reinterpret_cast<uint64_t>(tmap)), "r"(bar), "r"(c0), "r"(c1)
       : "memory");
 }
@@ -428,6 +432,10 @@ __global__ void __launch_bounds__(Cfg<N, R>::kThreads, 1)
       for (long long w; b + 1 < b1 && at + (w = weight(info(b))) <= j0; ++b) at += w;
       misc[4] = static_cast<uint32_t>(b);
       misc[5] = static_cast<uint32_t>(j0 - at);
+      // The loader asks for the table's entries next (of a sequence's first group, here).
+      const long long page = (j0 - at) * kKeys >> args.page_shift;
+      if (page < args.s.max_pages)
+        asm volatile("prefetch.global.L1 [%0];" ::"l"(args.s.table + static_cast<long long>(b) * args.s.max_pages + page));
     }
   }
   tc_fence_before();
@@ -777,6 +785,8 @@ __global__ void __launch_bounds__(Cfg<N, R>::kThreads, 1)
     // ================================================================ TMA producer
     uint32_t tiles = 0, q_count = 0;
     uint32_t ropes = 0, pairs = 0;        // asked for so far
+    uint32_t ps = 0, eph = 0;             // the next pair's slot, and the turn of the ring
+    auto uniform = [](int v) { return __shfl_sync(0xffffffffu, v, 0); };
     const int page = 1 << args.page_shift, box = min(page, kKeys), boxes = kKeys / box;
     bool ok = true;
     for (uint32_t si = 0; ok && wait_seg(si); ++si) {
@@ -787,18 +797,16 @@ __global__ void __launch_bounds__(Cfg<N, R>::kThreads, 1)
       if (row0 >= rows_of(s)) continue;
       if (q_count > 0 && !wait_bar_warp(q_empty, (q_count - 1) & 1, wc, kWaitQFull)) break;
       ++q_count;
-      if (lane == 0) {
-        mbar_arrive_expect_tx(q_full, C::kChunks * C::kQChunk);
-        const int row = static_cast<int>(static_cast<long long>(s.r0) * args.Hq + row0);
-#pragma unroll 1
-        for (int i = 0; i < C::kChunks; ++i)
-          tma_load_2d(sbase + C::kQOff + i * C::kQChunk, &tm_q, q_full, i == 0 ? R : 64 * (i - 1), row);
-      }
-      __syncwarp();
+      mbar_arrive_expect_tx_w(q_full, C::kChunks * C::kQChunk);
+      const int q_row = uniform(static_cast<int>(static_cast<long long>(s.r0) * args.Hq + row0));
+#pragma unroll
+      for (int i = 0; i < C::kChunks; ++i)
+        tma_load_2d_w(sbase + C::kQOff + i * C::kQChunk, &tm_q, q_full, i == 0 ? R : 64 * (i - 1), q_row);
       // 32 of the table's entries, one a lane, and the next 32 on their way.
-      int base = (s.a * kKeys) >> args.page_shift;
+      const int first_tile = uniform(s.a), last_tile = uniform(s.e);
+      int base = (first_tile * kKeys) >> args.page_shift;
       int cur = page_of_lane(args, s.b, s.len, base), nxt = page_of_lane(args, s.b, s.len, base + 32);
-      for (int j = s.a; j < s.e; ++j, ++tiles) {
+      for (int j = first_tile; j < last_tile; ++j, ++tiles) {
         const int first = (j * kKeys) >> args.page_shift;
         if (first >= base + 32) {
           base += 32;
@@ -819,35 +827,34 @@ __global__ void __launch_bounds__(Cfg<N, R>::kThreads, 1)
         const uint32_t part = static_cast<uint32_t>(box) * 128u;
         const uint32_t bytes = (pid0 >= 0 ? part : 0u) + (pid1 >= 0 ? part : 0u);
         auto load64 = [&](uint32_t dst, uint32_t bar, int col) {
-          if (pid0 >= 0) tma_load_3d(dst, &tm_k, bar, col, row, pid0);
-          if (pid1 >= 0) tma_load_3d(dst + part, &tm_k, bar, col, row, pid1);
+          if (pid0 >= 0) tma_load_3d_w(dst, &tm_k, bar, col, row, pid0);
+          if (pid1 >= 0) tma_load_3d_w(dst + part, &tm_k, bar, col, row, pid1);
         };
         const uint32_t rs = tiles % C::kRopes;
         if (tiles >= C::kRopes && !wait_bar_warp(rope_empty(rs), (tiles / C::kRopes - 1) & 1, wc, kWaitKvEmpty)) {
           ok = false;
           break;
         }
-        if (lane == 0) {
-          mbar_arrive_expect_tx(rope_full(rs), bytes);
-          load64(sbase + C::kRopeOff + rs * C::kRopeTile, rope_full(rs), R);
-        }
+        mbar_arrive_expect_tx_w(rope_full(rs), bytes);
+        load64(sbase + C::kRopeOff + rs * C::kRopeTile, rope_full(rs), R);
         ++ropes;
+        if (lane == 0) valid[tiles % kValid] = mask;
         __syncwarp();
+#pragma unroll
         for (int p = 0; p < C::kPairs; ++p) {
-          const uint32_t at = tiles * C::kPairs + p, ps = at % C::kRing;
-          if (at >= C::kRing && !wait_bar_warp(pair_empty(ps), (at / C::kRing - 1) & 1, wc, kWaitKvEmpty)) {
+          if (pairs >= C::kRing && !wait_bar_warp(pair_empty(ps), eph ^ 1u, wc, kWaitKvEmpty)) {
             ok = false;
             break;
           }
-          if (lane == 0) {
-            if (p == 0) valid[tiles % kValid] = mask;
-            const uint32_t dst = sbase + C::kRingOff + ps * C::kPairTile;
-            mbar_arrive_expect_tx(pair_full(ps), 2 * bytes);
-            load64(dst, pair_full(ps), 128 * p);
-            load64(dst + C::kRopeTile, pair_full(ps), 128 * p + 64);
-          }
+          const uint32_t dst = sbase + C::kRingOff + ps * C::kPairTile;
+          mbar_arrive_expect_tx_w(pair_full(ps), 2 * bytes);
+          load64(dst, pair_full(ps), 128 * p);
+          load64(dst + C::kRopeTile, pair_full(ps), 128 * p + 64);
           ++pairs;
-          __syncwarp();
+          if (++ps == C::kRing) {
+            ps = 0;
+            eph ^= 1u;
+          }
         }
         if (!ok) break;
       }

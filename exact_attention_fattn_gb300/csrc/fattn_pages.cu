@@ -366,7 +366,7 @@ __device__ __forceinline__ void copy_span(uint8_t* to, const uint8_t* from, long
 
 // Copies the list's pages; blocks from copy_blocks on rewrite the table where
 // pages have moved (compact; to_page is nullptr otherwise).
-__global__ void __launch_bounds__(kCopyThreads) copy_kernel(const Tables t, const __grid_constant__ Planes planes,
+__global__ void __launch_bounds__(kCopyThreads, 8) copy_kernel(const Tables t, const __grid_constant__ Planes planes,
                                                             CopyList list, int copy_blocks, const int* kv_len,
                                                             const int* to_page, const int* limit) {
   wait_for_parent();
