@@ -168,16 +168,19 @@ int make_rows_map_u8(CUtensorMap* m, const void* ptr, int inner, long long rows,
   return r == CUDA_SUCCESS ? FATTN_OK : FATTN_ERR_CUDA;
 }
 
-int make_rows_map_bf16(CUtensorMap* m, const void* ptr, int dims, const long long* extents, const long long* strides,
-                       int box_rows) {
-  if (dims != 2 && dims != 3) return FATTN_ERR_INVALID_ARG;
-  cuuint64_t n[3], st[2];
-  for (int i = 0; i < dims; ++i) n[i] = static_cast<cuuint64_t>(extents[i]);
-  for (int i = 0; i + 1 < dims; ++i) st[i] = static_cast<cuuint64_t>(strides[i]) * 2;
-  const cuuint32_t box[3] = {64u, static_cast<cuuint32_t>(box_rows), 1u};
-  const cuuint32_t estr[3] = {1u, 1u, 1u};
+int make_map_bf16(CUtensorMap* m, const void* ptr, int dims, const long long* extents, const long long* strides,
+                  const int* box) {
+  if (dims < 2 || dims > 5) return FATTN_ERR_INVALID_ARG;
+  cuuint64_t n[5], st[4];
+  cuuint32_t bx[5], estr[5];
+  for (int i = 0; i < dims; ++i) {
+    n[i] = static_cast<cuuint64_t>(extents[i]);
+    bx[i] = static_cast<cuuint32_t>(box[i]);
+    estr[i] = 1u;
+    if (i > 0) st[i - 1] = static_cast<cuuint64_t>(strides[i - 1]) * 2;
+  }
   CUresult r = g_encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, static_cast<cuuint32_t>(dims), const_cast<void*>(ptr), n,
-                        st, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                        st, bx, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? FATTN_OK : FATTN_ERR_CUDA;
 }

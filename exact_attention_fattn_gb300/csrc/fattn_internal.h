@@ -248,17 +248,16 @@ constexpr int kLatentUnitCost = 2;   // tiles that a unit counts beyond its own
 // Rows of a unit for calls of `rows` rows an average sequence.
 constexpr int latent_rows(long long rows) { return rows <= 16 ? 16 : (rows <= 32 ? 32 : 64); }
 
-// rows: 16, 32 or 64 rows a unit; rank: 256 or 512.  tk: 3-D bf16 view {rank + 64, page,
-// pages} of the cache, boxes of 64 columns and min(page, 64) rows; tq: 2-D bf16
-// view {rank + 64, T * Hq} of the queries, boxes of 64 columns and `rows` rows; both
-// with a 128-byte swizzle.
+// rows: 16, 32 or 64 rows a unit; rank: 256 or 512.  tk: view {rank + 64, page, pages} of the
+// cache, boxes of 64 columns and min(page, 64) rows; tq: view {64, T * Hq, rank / 64 + 1} of
+// the queries by chunks of 64 columns, boxes of `rows` rows and all chunks.
 cudaError_t launch_latent_attn(int rows, int rank, const CUtensorMap& tk, const CUtensorMap& tq,
                                const LatentAttnArgs& a, cudaStream_t stream);
 
-// Tensor map of bf16 rows: `rank` dimensions (2 or 3) of the given extents, strides of
-// all but the first in elements, boxes {64, box_rows, 1}.  Returns a fattn_status.
-int make_rows_map_bf16(CUtensorMap* m, const void* ptr, int dims, const long long* extents, const long long* strides,
-                       int box_rows);
+// Tensor map of bf16 data: 2 to 5 dimensions, strides of all but the first in
+// elements, 128-byte swizzle (a box has 64 of the first).  Returns a fattn_status.
+int make_map_bf16(CUtensorMap* m, const void* ptr, int dims, const long long* extents, const long long* strides,
+                  const int* box);
 
 // Per-device state for entry points outside fattn_api.cu: checks the device,
 // gives the status word and the wait budget.  Returns a fattn_status.

@@ -195,10 +195,12 @@ int fattn_latent_fwd(const fattn_latent_cache* cache, const void* q, void* o, fl
   a.shares = static_cast<int>(units * per < shares ? units * per : shares);
   CUtensorMap tk, tq;
   const long long width = cache->rank + kLatentRope;
+  const int chunks = static_cast<int>(width / 64), box_rows = cache->page < kLatentKeys ? cache->page : kLatentKeys;
   const long long k_extents[3] = {width, cache->page, cache->pages}, k_strides[2] = {width, cache->page_stride};
-  const long long q_extents[2] = {width, static_cast<long long>(T) * Hq}, q_strides[1] = {width};
-  if ((rc = make_rows_map_bf16(&tk, cache->data, 3, k_extents, k_strides, cache->page < kLatentKeys ? cache->page : kLatentKeys)) != FATTN_OK ||
-      (rc = make_rows_map_bf16(&tq, q, 2, q_extents, q_strides, l.rows)) != FATTN_OK)
+  const long long q_extents[3] = {64, static_cast<long long>(T) * Hq, chunks}, q_strides[2] = {width, 64};
+  const int k_box[3] = {64, box_rows, 1}, q_box[3] = {64, l.rows, chunks};
+  if ((rc = make_map_bf16(&tk, cache->data, 3, k_extents, k_strides, k_box)) != FATTN_OK ||
+      (rc = make_map_bf16(&tq, q, 3, q_extents, q_strides, q_box)) != FATTN_OK)
     return rc;
   return launch_latent_attn(l.rows, cache->rank, tk, tq, a, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
              ? FATTN_OK

@@ -58,7 +58,7 @@ struct Cfg {
   static constexpr int kWalkWarp = kMmaWarp + 2;
   static constexpr int kThreads = 32 * (kMmaWarp + 4);
   static constexpr int kSegReaders = 4 * kHalves + 2;
-  static constexpr int kChunks = R / 64 + 1;         // 64-column parts of a query; the rotated one first
+  static constexpr int kChunks = R / 64 + 1;         // 64-column parts of a query; the rotated one last
   static constexpr int kPairs = R / 128;             // 128-column parts of a cached row
   static constexpr int kQChunk = N * 128;
   static constexpr int kRopeTile = kKeys * 128;      // 64 columns of a tile
@@ -120,18 +120,6 @@ __device__ __forceinline__ void commit_lead(uint32_t bar, uint32_t lead) {
       "r"(lead)
       : "memory");
 }
-// Copies from a converged warp, one lane of it elected by each: under a branch on
-// the lane a copy's issue takes several times as long (a tile's nine 1700
-// cycles), as an MMA's does.
-__device__ __forceinline__ void tma_load_2d_w(uint32_t dst, const void* tmap, uint32_t bar, int c0, int c1) {
-  asm volatile(
-      "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
-      "@e cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%3, %4}], [%2];\n\t}" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(tmap)), "r"(bar), "r"(c0), "r"(c1)
-      : "memory");
-}
-
 // Whether a phase has completed; unlike try_wait it does not stay to see.
 __device__ __forceinline__ bool bar_done(uint32_t bar, uint32_t parity) {
   uint32_t ok;
@@ -740,7 +728,7 @@ __global__ void __launch_bounds__(Cfg<N, R>::kThreads, 1)
           }
           tc_fence_after();
           const uint32_t d = tmem + C::col_s(tiles & 1);
-          product4(d, sbase + C::kRopeOff + rs * C::kRopeTile, sbase + C::kQOff, 0u);
+          product4(d, sbase + C::kRopeOff + rs * C::kRopeTile, sbase + C::kQOff + 2 * C::kPairs * C::kQChunk, 0u);
           commit_lead(rope_empty(rs), lead);
           if (++rs == C::kRopes) {
             rs = 0;
@@ -749,7 +737,7 @@ __global__ void __launch_bounds__(Cfg<N, R>::kThreads, 1)
 #pragma unroll
           for (int p = 0; p < C::kPairs; ++p) {
             if (p > 0 && !wait_bar_warp(pair_full(ks), kph, wc, kWaitKvFull)) return false;
-            const uint32_t k = sbase + C::kRingOff + ks * C::kPairTile, q = sbase + C::kQOff + (1 + 2 * p) * C::kQChunk;
+            const uint32_t k = sbase + C::kRingOff + ks * C::kPairTile, q = sbase + C::kQOff + 2 * p * C::kQChunk;
             product4(d, k, q, 1u);
             product4(d, k + C::kRopeTile, q + C::kQChunk, 1u);
             if (++ks == C::kRing) {
@@ -783,6 +771,10 @@ __global__ void __launch_bounds__(Cfg<N, R>::kThreads, 1)
     __syncwarp();
   } else if (warp == kLoadWarp) {
     // ================================================================ TMA producer
+    // Copies are issued by the converged warp, one lane of it elected by each: under a
+    // branch on the lane their issue takes longer (190 cycles instead of 110), as
+    // an MMA's does.  A block's queries are one copy; the cache's come 64 columns a
+    // copy (128 a copy: prompt piece 629 us, 64: 611).
     uint32_t tiles = 0, q_count = 0;
     uint32_t ropes = 0, pairs = 0;        // asked for so far
     uint32_t ps = 0, eph = 0;             // the next pair's slot, and the turn of the ring
@@ -799,9 +791,7 @@ __global__ void __launch_bounds__(Cfg<N, R>::kThreads, 1)
       ++q_count;
       mbar_arrive_expect_tx_w(q_full, C::kChunks * C::kQChunk);
       const int q_row = uniform(static_cast<int>(static_cast<long long>(s.r0) * args.Hq + row0));
-#pragma unroll
-      for (int i = 0; i < C::kChunks; ++i)
-        tma_load_2d_w(sbase + C::kQOff + i * C::kQChunk, &tm_q, q_full, i == 0 ? R : 64 * (i - 1), q_row);
+      tma_load_3d_w(sbase + C::kQOff, &tm_q, q_full, 0, q_row, 0);
       // 32 of the table's entries, one a lane, and the next 32 on their way.
       const int first_tile = uniform(s.a), last_tile = uniform(s.e);
       int base = (first_tile * kKeys) >> args.page_shift;
@@ -826,9 +816,10 @@ __global__ void __launch_bounds__(Cfg<N, R>::kThreads, 1)
         const int row = (j * kKeys) & (page - 1);
         const uint32_t part = static_cast<uint32_t>(box) * 128u;
         const uint32_t bytes = (pid0 >= 0 ? part : 0u) + (pid1 >= 0 ? part : 0u);
-        auto load64 = [&](uint32_t dst, uint32_t bar, int col) {
-          if (pid0 >= 0) tma_load_3d_w(dst, &tm_k, bar, col, row, pid0);
-          if (pid1 >= 0) tma_load_3d_w(dst + part, &tm_k, bar, col, row, pid1);
+        // A chunk of 64 columns, from two pages where they have 32 tokens.
+        auto load64 = [&](uint32_t dst, uint32_t bar, int chunk) {
+          if (pid0 >= 0) tma_load_3d_w(dst, &tm_k, bar, 64 * chunk, row, pid0);
+          if (pid1 >= 0) tma_load_3d_w(dst + part, &tm_k, bar, 64 * chunk, row, pid1);
         };
         const uint32_t rs = tiles % C::kRopes;
         if (tiles >= C::kRopes && !wait_bar_warp(rope_empty(rs), (tiles / C::kRopes - 1) & 1, wc, kWaitKvEmpty)) {
@@ -836,7 +827,7 @@ __global__ void __launch_bounds__(Cfg<N, R>::kThreads, 1)
           break;
         }
         mbar_arrive_expect_tx_w(rope_full(rs), bytes);
-        load64(sbase + C::kRopeOff + rs * C::kRopeTile, rope_full(rs), R);
+        load64(sbase + C::kRopeOff + rs * C::kRopeTile, rope_full(rs), R / 64);
         ++ropes;
         if (lane == 0) valid[tiles % kValid] = mask;
         __syncwarp();
@@ -848,8 +839,8 @@ __global__ void __launch_bounds__(Cfg<N, R>::kThreads, 1)
           }
           const uint32_t dst = sbase + C::kRingOff + ps * C::kPairTile;
           mbar_arrive_expect_tx_w(pair_full(ps), 2 * bytes);
-          load64(dst, pair_full(ps), 128 * p);
-          load64(dst + C::kRopeTile, pair_full(ps), 128 * p + 64);
+          load64(dst, pair_full(ps), 2 * p);
+          load64(dst + C::kRopeTile, pair_full(ps), 2 * p + 1);
           ++pairs;
           if (++ps == C::kRing) {
             ps = 0;
