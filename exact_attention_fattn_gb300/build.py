@@ -31,7 +31,7 @@ SOURCES = ["fattn_api.cu", "fattn_fwd.cu", "fattn_bwd.cu", "fattn_bwd2.cu", "fat
            "fattn_fp8.cu", "fattn_sched.cu", "fattn_cache_api.cu", "fattn_cache_append.cu",
            "fattn_cache_chunk.cu", "fattn_cache_decode.cu", "fattn_cache_join.cu",
            "fattn_cache_select.cu", "fattn_latent_api.cu", "fattn_latent_append.cu",
-           "fattn_latent_attn.cu", "fattn_pages.cu", "fattn_rope.cu"]
+           "fattn_latent_attn.cu", "fattn_latent_pair.cu", "fattn_pages.cu", "fattn_rope.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I", INCLUDE,
          "--expt-relaxed-constexpr"]

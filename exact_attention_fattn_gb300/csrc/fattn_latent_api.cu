@@ -88,7 +88,7 @@ struct Workspace {
 };
 Workspace workspace_of(const Layout& l, int rank) {
   Workspace w;
-  const size_t rows = 2ull * kSms * l.rows;
+  const size_t rows = 2ull * (l.rows == kLatentPairRows ? kSms / 2 : kSms) * l.rows;
   w.ml_off = align256(rows * rank * sizeof(float));
   w.rec_off = w.ml_off + align256(rows * sizeof(float2));
   w.total = w.rec_off + align256(kSms * sizeof(int4));
@@ -188,9 +188,11 @@ int fattn_latent_fwd(const fattn_latent_cache* cache, const void* q, void* o, fl
   if (sms > kSms) sms = kSms;
   // Tiles of all units, at most (the lengths are on the device).
   const long long units = static_cast<long long>(T) * Hq / (l.span * l.rows) + B;
-  const long long per = (static_cast<long long>(max_pages) * cache->page + kLatentKeys - 1) / kLatentKeys + kLatentUnitCost;
+  const bool on_pairs = l.rows == kLatentPairRows;
+  const int tile = on_pairs ? kLatentPairKeys : kLatentKeys;
+  const long long per = (static_cast<long long>(max_pages) * cache->page + tile - 1) / tile + kLatentUnitCost;
   if (units > 0x7fffffffll / per) return FATTN_ERR_TOO_LARGE;   // the kernels number them in 32 bits
-  const long long shares = sms / l.span;
+  const long long shares = (on_pairs ? sms / 2 : sms) / l.span;
   a.span = l.span;
   a.shares = static_cast<int>(units * per < shares ? units * per : shares);
   CUtensorMap tk, tq;
@@ -198,13 +200,14 @@ int fattn_latent_fwd(const fattn_latent_cache* cache, const void* q, void* o, fl
   const int chunks = static_cast<int>(width / 64), box_rows = cache->page < kLatentKeys ? cache->page : kLatentKeys;
   const long long k_extents[3] = {width, cache->page, cache->pages}, k_strides[2] = {width, cache->page_stride};
   const long long q_extents[3] = {64, static_cast<long long>(T) * Hq, chunks}, q_strides[2] = {width, 64};
-  const int k_box[3] = {64, box_rows, 1}, q_box[3] = {64, l.rows, chunks};
+  const int k_box[3] = {64, box_rows, 1}, q_box[3] = {64, on_pairs ? 64 : l.rows, chunks};
   if ((rc = make_map_bf16(&tk, cache->data, 3, k_extents, k_strides, k_box)) != FATTN_OK ||
       (rc = make_map_bf16(&tq, q, 3, q_extents, q_strides, q_box)) != FATTN_OK)
     return rc;
-  return launch_latent_attn(l.rows, cache->rank, tk, tq, a, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
-             ? FATTN_OK
-             : FATTN_ERR_CUDA;
+  const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  const cudaError_t e = on_pairs ? launch_latent_pair(cache->rank, tk, tq, a, st)
+                                 : launch_latent_attn(l.rows, cache->rank, tk, tq, a, st);
+  return e == cudaSuccess ? FATTN_OK : FATTN_ERR_CUDA;
 }
 
 }  // extern "C"

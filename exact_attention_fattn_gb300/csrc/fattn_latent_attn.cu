@@ -32,9 +32,7 @@
 // tensor memory and MMA issue, one for loads, one for the walk over the share (it
 // publishes one segment after the other) and an idle one.
 // TMEM: S at N (tile & 1), O^T at 2 N + N block.
-#include <float.h>
-
-#include "fattn_cache.cuh"
+#include "fattn_latent.cuh"
 
 namespace fattn {
 
@@ -42,9 +40,6 @@ namespace {
 
 constexpr int kKeys = kLatentKeys;
 constexpr int kSegs = 4;
-constexpr float kLn2 = 0.69314718055994530942f;
-constexpr float kTau = 8.f;
-constexpr int kSmemMax = 232448;
 constexpr int kValid = 8;             // tiles whose masks are kept; more than the ring holds
 
 template <int N, int R>
@@ -98,107 +93,6 @@ struct Cfg {
   static_assert(2 * N + N * kPairs <= 512, "tensor memory");
 };
 
-// ------------------------------------------------------------------ PTX
-
-__device__ __forceinline__ uint32_t elect_lane() {
-  uint32_t r;
-  asm volatile("{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\tselp.u32 %0, 1, 0, e;\n\t}" : "=r"(r));
-  return r;
-}
-__device__ __forceinline__ void mma_lead(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
-                                         uint32_t accumulate, uint32_t lead) {
-  asm volatile(
-      "{\n\t.reg .pred p, e;\n\tsetp.ne.b32 e, %5, 0;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(lead)
-      : "memory");
-}
-__device__ __forceinline__ void commit_lead(uint32_t bar, uint32_t lead) {
-  asm volatile(
-      "{\n\t.reg .pred e;\n\tsetp.ne.b32 e, %1, 0;\n\t"
-      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar),
-      "r"(lead)
-      : "memory");
-}
-// Whether a phase has completed; unlike try_wait it does not stay to see.
-__device__ __forceinline__ bool bar_done(uint32_t bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.test_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(bar), "r"(parity)
-      : "memory");
-  return __all_sync(0xffffffffu, ok != 0);
-}
-
-// 16 lanes x N columns: thread t gets, for each 8 columns i, r[4 i], r[4 i + 1] of
-// lane t / 4, columns 8 i + 2 (t % 4) and the next, and r[4 i + 2], r[4 i + 3] of
-// lane t / 4 + 8.  Valid after the wait.
-__device__ __forceinline__ void tmem_ld_rows(uint32_t taddr, uint32_t (&r)[4]) {
-  asm volatile("tcgen05.ld.sync.aligned.16x256b.x1.b32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(taddr)
-               : "memory");
-}
-__device__ __forceinline__ void tmem_ld_rows(uint32_t taddr, uint32_t (&r)[8]) {
-  asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
-               : "r"(taddr)
-               : "memory");
-}
-__device__ __forceinline__ void tmem_ld_rows(uint32_t taddr, uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, "
-      "%14, %15}, [%16];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-      : "r"(taddr)
-      : "memory");
-}
-__device__ __forceinline__ void tmem_ld_rows(uint32_t taddr, uint32_t (&r)[32]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.16x256b.x8.b32 "
-      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
-        "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
-        "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-      : "r"(taddr)
-      : "memory");
-}
-// 32 lanes x 16 columns, a lane's in its thread.
-__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, "
-      "%14, %15}, [%16];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-      : "r"(taddr)
-      : "memory");
-}
-// Waits for this thread's loads; the registers pass through, so that no use of
-// them is scheduled before.
-template <int K>
-__device__ __forceinline__ void tmem_ld_wait(uint32_t (&r)[K]) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-#pragma unroll
-  for (int i = 0; i < K; ++i) asm volatile("" : "+r"(r[i])::"memory");
-}
-// Four 8 x 8 matrices of 16-bit elements, each transposed on its way.
-__device__ __forceinline__ void stmatrix_x4_trans(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
-  asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b),
-               "r"(c), "r"(d)
-               : "memory");
-}
-// Entry `first` + lane of a sequence's row of the page table; -1 past its end.
-__device__ __forceinline__ int page_of_lane(const LatentAttnArgs& a, int b, int len, int first) {
-  const int p = first + static_cast<int>(threadIdx.x & 31);
-  if ((static_cast<long long>(p) << a.page_shift) >= len) return -1;
-  return __ldg(a.s.table + static_cast<long long>(b) * a.s.max_pages + p);
-}
 // Barrier of the softmax warps; true if `x` is in any thread.
 template <int THREADS>
 __device__ __forceinline__ bool barrier_any(bool x) {
@@ -215,115 +109,6 @@ template <int THREADS>
 __device__ __forceinline__ void barrier_sync() {
   asm volatile("barrier.cta.sync 1, %0;" ::"n"(THREADS) : "memory");
 }
-
-// ------------------------------------------------------------------ schedule
-
-// First tile of share c of W < 2^31 dealt to G <= 152 shares: floor(W c / G).
-__device__ __forceinline__ int share_first(int W, int G, int c) {
-  const int q = W / G;
-  return q * c + (W - q * G) * c / G;
-}
-
-// A sequence's groups of `rows` rows in order, with the key tiles that each sees.
-// The tokens before the group's end, end = tok * Hq + rem, are carried along, so that
-// long prompts cost no division a group.
-struct Groups {
-  int rows, all;             // rows of a group and of the sequence (T * Hq < 2^31 - 1024)
-  int end, tok, rem;
-  int dtok, drem;
-  int len, n, Hq, causal;
-  __device__ __forceinline__ Groups(const LatentAttnArgs& a, const SeqInfo& q, int group_rows, int first = 0)
-      : rows(group_rows), all(q.n * a.Hq), end(group_rows), len(q.len), n(q.n), Hq(a.Hq), causal(a.causal) {
-    dtok = group_rows / Hq;
-    drem = group_rows - dtok * Hq;
-    tok = dtok;
-    rem = drem;
-    if (first > 0) {
-      end = static_cast<int>(min(static_cast<long long>(first + 1) * group_rows, 0x7fffffffll));
-      tok = end / Hq;
-      rem = end - tok * Hq;
-    }
-  }
-  __device__ __forceinline__ bool live() const { return end - rows < all; }
-  __device__ __forceinline__ void next() {
-    end = static_cast<int>(min(static_cast<long long>(end) + rows, 0x7fffffffll));
-    tok += dtok;
-    rem += drem;
-    if (rem >= Hq) {
-      rem -= Hq;
-      ++tok;
-    }
-  }
-  // At least one, so that rows that see nothing are written, too.
-  __device__ __forceinline__ int tiles() const {
-    int keys = len;
-    if (causal) keys = len - n + min(n, tok + (rem > 0 ? 1 : 0));
-    return max(1, (keys + kKeys - 1) / kKeys);
-  }
-};
-
-// One share's part of a unit: key tiles [a, e) of nt for row group rg of a sequence.
-struct __align__(16) Seg {
-  int b, rg, r0, n;
-  int len, flags, a, e;
-  int nt, pad0, pad1, pad2;
-  static constexpr int kStarts = 1, kEnds = 2, kLast = 8;
-  __device__ __forceinline__ bool whole() const { return (flags & 3) == 3; }
-};
-static_assert(sizeof(Seg) == 48, "ring slot");
-
-// Walks a share.
-struct Walker {
-  const LatentAttnArgs& a;
-  int group_rows;
-  int left;                 // tiles (and what units count beyond) still to walk
-  int b, rg, at, nt;
-  SeqInfo q;
-  __device__ __forceinline__ long long all_rows() const { return static_cast<long long>(q.n) * a.Hq; }
-  __device__ __forceinline__ Walker(const LatentAttnArgs& args, int rows, int first_b, int rem, int todo)
-      : a(args), group_rows(rows), left(todo), b(first_b), rg(0), at(0), nt(0) {
-    if (left <= 0) return;
-    q = seq_info(a.s, b, a.page_shift);
-    Groups g(a, q, group_rows);
-    nt = g.tiles();
-    while (rem >= nt + kLatentUnitCost && g.live()) {
-      rem -= nt + kLatentUnitCost;
-      ++rg;
-      g.next();
-      nt = g.tiles();
-    }
-    at = rem;
-  }
-  __device__ __forceinline__ bool next(Seg& s) {
-    if (left <= 0) return false;
-    if (at >= nt) {                     // tiles that stand for the unit itself
-      left -= nt + kLatentUnitCost - at;
-      at = 0;
-      if (left <= 0) return false;
-      if (static_cast<long long>(++rg) * group_rows >= all_rows()) {
-        rg = 0;
-        // work is left, so a sequence with rows follows
-        do {
-          if (++b >= a.s.B) return false;
-          q = seq_info(a.s, b, a.page_shift);
-        } while (q.n == 0);
-      }
-      nt = Groups(a, q, group_rows, rg).tiles();
-    }
-    s.b = b;
-    s.rg = rg;
-    s.r0 = q.r0;
-    s.n = q.n;
-    s.len = q.len;
-    s.a = at;
-    s.e = min(nt, at + left);
-    s.nt = nt;
-    s.flags = (at == 0 ? Seg::kStarts : 0) | (s.e == nt ? Seg::kEnds : 0);
-    left -= s.e - s.a;
-    at = s.e;
-    return true;
-  }
-};
 
 // ------------------------------------------------------------------ kernel
 
@@ -376,56 +161,8 @@ __global__ void __launch_bounds__(Cfg<N, R>::kThreads, 1)
     tma_prefetch_desc(&tm_k);
     tma_prefetch_desc(&tm_q);
   }
-  // ---- the share: where its first tile lies.  The scan's scratch is in the
-  // references' place, which nothing uses yet.
-  int W, busy, j0, j1;
-  {
-    long long* wtot = reinterpret_cast<long long*>(xs);
-    const int per = (args.s.B + kThreads - 1) / kThreads;
-    const int b0 = min(args.s.B, tid * per), b1 = min(args.s.B, b0 + per);
-    auto info = [&](int b) {
-      return b == mine.b ? seq_info(args.s, mine.r0, mine.r1, mine.len, args.page_shift)
-                         : seq_info(args.s, b, args.page_shift);
-    };
-    auto weight = [&](const SeqInfo& q) {
-      long long w = 0;
-      for (Groups g(args, q, group_rows); g.live(); g.next()) w += g.tiles() + kLatentUnitCost;
-      return w;
-    };
-    long long sum = 0;
-    for (int b = b0; b < b1; ++b) {
-      const SeqInfo q = info(b);
-      if (!q.ok && blockIdx.x == 0) record_bad_index(args.status, kSiteSeqStart);
-      sum += weight(q);
-    }
-    long long incl = sum;
-#pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-      const long long t = __shfl_up_sync(0xffffffffu, incl, off);
-      if (lane >= off) incl += t;
-    }
-    if (lane == 31) wtot[warp] = incl;
-    __syncthreads();
-    long long at = incl - sum, all = 0;
-    for (int w = 0; w < kThreads / 32; ++w) {
-      if (w < warp) at += wtot[w];
-      all += wtot[w];
-    }
-    W = total_of(all, args.status);
-    busy = min(G, W);                     // no share is empty between others
-    j0 = share < busy ? share_first(W, busy, share) : 0;
-    j1 = share < busy ? share_first(W, busy, share + 1) : 0;
-    if (j0 < j1 && at <= j0 && j0 < at + sum) {
-      int b = b0;
-      for (long long w; b + 1 < b1 && at + (w = weight(info(b))) <= j0; ++b) at += w;
-      misc[4] = static_cast<uint32_t>(b);
-      misc[5] = static_cast<uint32_t>(j0 - at);
-      // The loader asks for the table's entries next (of a sequence's first group, here).
-      const long long page = (j0 - at) * kKeys >> args.page_shift;
-      if (page < args.s.max_pages)
-        asm volatile("prefetch.global.L1 [%0];" ::"l"(args.s.table + static_cast<long long>(b) * args.s.max_pages + page));
-    }
-  }
+  // The scan's scratch is in the references' place, which nothing uses yet.
+  const Share sh = locate_share<kKeys, kThreads>(args, mine, group_rows, G, share, reinterpret_cast<long long*>(xs), misc + 4);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -859,7 +596,7 @@ __global__ void __launch_bounds__(Cfg<N, R>::kThreads, 1)
     __syncwarp();
   } else if (warp == kWalkWarp) {
     // ================================================================ schedule
-    Walker walk(args, group_rows, static_cast<int>(misc[4]), static_cast<int>(misc[5]), j1 - j0);
+    Walker<kKeys> walk(args, group_rows, static_cast<int>(misc[4]), static_cast<int>(misc[5]), sh.j1 - sh.j0);
     Seg s{};
     bool any = false;
     for (uint32_t i = 0;; ++i) {
@@ -886,7 +623,7 @@ __global__ void __launch_bounds__(Cfg<N, R>::kThreads, 1)
       // What is to be joined: the unit that this share starts and others go on with
       // (its last one).
       const bool shared_unit = any && (s.flags & (Seg::kStarts | Seg::kEnds)) == Seg::kStarts;
-      args.rec[share] = shared_unit ? make_int4(s.r0, s.n, s.rg, cta_of(W, busy, j1 - (s.e - s.a) + s.nt - 1))
+      args.rec[share] = shared_unit ? make_int4(s.r0, s.n, s.rg, cta_of(sh.W, sh.busy, sh.j1 - (s.e - s.a) + s.nt - 1))
                                     : make_int4(0, 0, 0, 0);
     }
     __syncwarp();
@@ -1010,6 +747,19 @@ __global__ void __launch_bounds__(kJoinGroups * R / 4) join_kernel(const LatentA
 }
 
 template <int N, int R>
+cudaError_t launch_join_t(const LatentAttnArgs& a, cudaStream_t stream) {
+  const int rows = a.shares * a.span * N, most = kSms * 2048 / (kJoinGroups * R / 4);
+  return launch_child(join_kernel<N, R>, rows < most ? rows : most, kJoinGroups * R / 4, 0, stream, a);
+}
+
+template <int R>
+cudaError_t launch_join_rank(int rows, const LatentAttnArgs& a, cudaStream_t stream) {
+  if (rows == 16) return launch_join_t<16, R>(a, stream);
+  if (rows == 32) return launch_join_t<32, R>(a, stream);
+  return rows == 64 ? launch_join_t<64, R>(a, stream) : launch_join_t<128, R>(a, stream);
+}
+
+template <int N, int R>
 cudaError_t launch_t(const CUtensorMap& tk, const CUtensorMap& tq, const LatentAttnArgs& a, cudaStream_t stream) {
   auto kern = latent_kernel<N, R>;
   static SmemLimit limit;
@@ -1018,11 +768,14 @@ cudaError_t launch_t(const CUtensorMap& tk, const CUtensorMap& tq, const LatentA
   kern<<<a.span * a.shares, Cfg<N, R>::kThreads, Cfg<N, R>::kSmem, stream>>>(tk, tq, a);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   if (a.shares == 1) return cudaSuccess;   // nothing is shared
-  const int rows = a.shares * a.span * N, most = kSms * 2048 / (kJoinGroups * R / 4);
-  return launch_child(join_kernel<N, R>, rows < most ? rows : most, kJoinGroups * R / 4, 0, stream, a);
+  return launch_latent_join(N, R, a, stream);
 }
 
 }  // namespace
+
+cudaError_t launch_latent_join(int rows, int rank, const LatentAttnArgs& a, cudaStream_t stream) {
+  return rank == 256 ? launch_join_rank<256>(rows, a, stream) : launch_join_rank<512>(rows, a, stream);
+}
 
 cudaError_t launch_latent_attn(int rows, int rank, const CUtensorMap& tk, const CUtensorMap& tq,
                                const LatentAttnArgs& a, cudaStream_t stream) {

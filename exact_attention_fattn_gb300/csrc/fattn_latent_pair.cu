@@ -1,0 +1,810 @@
+// Attention over the paged latent cache for more than 64 rows a sequence: pairs of
+// CTAs on two SMs (cta_group::2) work on 128 rows, so that what bounds the kernel
+// for 64 rows, shared memory's 128 bytes a cycle, is used for twice the rows.
+//
+//   S^T = K Q^T      M = 128 (each CTA its 64 keys of a 128-key tile), N = 128 rows
+//     (each CTA stages 64 rows of Q)
+//   O^T += V^T P^T   M = 256 (each CTA half of the latent's columns, 128 at a time),
+//     N = 128 rows (each CTA stages 64 rows of P), all 128 keys
+//
+// A CTA needs its own keys' rows whole for the first product, and half of the columns
+// of all keys for the second.  The columns of its own keys that it has no use for
+// after the first product make room, in the same place, for the columns that it
+// needs of the other CTA's keys (from L2): the second product then finds each key
+// half's columns at one address in both CTAs, and a tile takes no more than 72 KB.
+// P goes where its rows are staged: half of it to the other CTA's shared memory.
+//
+// Per 128 keys and CTA: 2190 cycles of MMA; shared memory is read 245 KB (K 74, Q 74, V
+// 65, P 32) and written 122 KB, 2870 cycles.  Two CTAs with 64 rows each need 5100.
+//
+// Softmax: tensor memory gives lanes 0-63 a CTA's keys for rows 0-63, lanes 64-127 the
+// same keys for rows 64-127.  Both CTAs keep the same reference of every row.  A
+// tile's probabilities are computed with the references there are, and with them
+// goes a vote: had any row of either CTA a score above its reference by more than 2^8
+// (the first tile of a unit always has), the CTAs exchange the rows' maxima, move the
+// references alike, rescale and compute the tile's probabilities again.
+//
+// Work split and join as in fattn_latent_attn.cu, a pair in a CTA's place.
+//
+// Warps: 0-7 softmax and results, 8 tensor memory and (leader) MMA issue, 9 loads, 10
+// loads of the other CTA's keys, 11 the walk over the share.
+// TMEM: S at 64 (tile & 1), O^T at 128 + 128 block.
+#include "fattn_latent.cuh"
+
+namespace fattn {
+
+namespace {
+
+constexpr int kKeys = 128;            // of a tile, half of them a CTA's
+constexpr int kHalfKeys = 64;
+constexpr int kRows = 128;
+constexpr int kThreads = 384;
+constexpr int kSoftmaxWarps = 8;
+constexpr int kMmaWarp = 8;
+constexpr int kLoadWarp = 9;
+constexpr int kOtherWarp = 10;
+constexpr int kWalkWarp = 11;
+constexpr int kSegs = 2;
+constexpr int kSegReaders = kSoftmaxWarps + 3;
+constexpr int kValid = 4;             // tiles whose masks are kept; as many as the ring holds at most
+
+template <int R>
+struct Cfg {
+  static constexpr int kChunks = R / 64 + 1;
+  static constexpr int kPairs = R / 128;             // 128-column parts of a cached row
+  static constexpr int kBlocks = kPairs / 2;         // of them a CTA's own
+  static constexpr int kChunk = kHalfKeys * 128;     // 64 rows, 64 columns
+  static constexpr int kQOff = 0;
+  static constexpr int kQBytes = kChunks * kChunk;
+  static constexpr int kPOff = kQBytes;              // [2 key halves][64 rows][64 keys]
+  static constexpr int kRingOff = kPOff + 2 * kChunk;
+  static constexpr int kPairTile = 2 * kChunk;
+  static constexpr int kRing = 8;                    // pairs
+  static constexpr int kRopes = R == 512 ? 1 : 2;
+  static constexpr int kRopeOff = kRingOff + kRing * kPairTile;
+  static constexpr int kBarOff = kRopeOff + kRopes * kChunk;
+  static_assert(kRing >= 2 * kPairs && kRing / kPairs <= kValid, "ring");
+  // barriers; those with (l) count for both CTAs in the leader's shared memory
+  enum : int {
+    kFull = 0,                    // (l) pair slots
+    kEmpty = kFull + kRing,
+    kRopeFull = kEmpty + kRing,   // (l)
+    kRopeEmpty = kRopeFull + 2,
+    kOther = kRopeEmpty + 2,      // the other CTA's keys, in this CTA
+    kOtherBoth = kOther + 2,      // (l) in both
+    kQFull = kOtherBoth + 2,      // (l)
+    kQEmpty,
+    kSFull,
+    kMask = kSFull + 2,
+    kVote = kMask + kValid,       // probabilities and votes of both CTAs
+    kAgain,                       // (l) probabilities computed again
+    kExchange,                    // the other CTA's maxima or sums
+    kSync,                        // this CTA's softmax warps
+    kPvDone,
+    kMmaDone,
+    kSegFull,
+    kSegEmpty = kSegFull + kSegs,
+    kNumBars = kSegEmpty + kSegs
+  };
+  static constexpr int kMiscOff = kBarOff + kNumBars * 8;   // tmem, abort, flags[2], masks[4], start of the share
+  static constexpr int kSegOff = (kMiscOff + 40 + 15) / 16 * 16;
+  static constexpr int kOwnOff = kSegOff + kSegs * 48;      // [2][kRows] float
+  static constexpr int kPeerOff = kOwnOff + 2 * kRows * 4;  // [2][kRows] float
+  static constexpr int kAlphaOff = kPeerOff + 2 * kRows * 4;
+  static constexpr int kSmem = kAlphaOff + kRows * 4;
+  static_assert(kSmem <= kSmemMax && kNumBars < kThreads, "shared memory");
+  __device__ static constexpr uint32_t col_s(uint32_t buf) { return 64 * buf; }
+  __device__ static constexpr uint32_t col_o(int block) { return 128 + 128 * block; }
+};
+
+__device__ __forceinline__ void mma2_lead(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                          uint32_t accumulate, uint32_t lead) {
+  asm volatile(
+      "{\n\t.reg .pred p, e;\n\tsetp.ne.b32 e, %5, 0;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "@e tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(lead)
+      : "memory");
+}
+// To the barrier at this place in both CTAs.
+__device__ __forceinline__ void commit2_lead(uint32_t bar, uint32_t lead) {
+  const uint16_t mask = 3;
+  asm volatile(
+      "{\n\t.reg .pred e;\n\tsetp.ne.b32 e, %2, 0;\n\t"
+      "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n\t}" ::"r"(
+          bar),
+      "h"(mask), "r"(lead)
+      : "memory");
+}
+__device__ __forceinline__ void st_cluster_f32(uint32_t cluster_addr, float x) {
+  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(cluster_addr), "f"(x) : "memory");
+}
+__device__ __forceinline__ void st_cluster_u32(uint32_t cluster_addr, uint32_t x) {
+  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(cluster_addr), "r"(x) : "memory");
+}
+// An 8 x 8 matrix of 16-bit elements, two a lane, transposed.
+__device__ __forceinline__ uint32_t movmatrix_trans(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+
+// bar_done for what either CTA completes.
+__device__ __forceinline__ bool bar_done_cl(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return __all_sync(0xffffffffu, ok != 0);
+}
+
+// A wait on what either CTA of the pair completes, by a whole warp.
+__device__ __forceinline__ bool wait_cl(uint32_t bar, uint32_t parity, const Waits& w, unsigned int site) {
+  bool ok = true;
+  if (!mbar_try_wait_cl(bar, parity)) {
+    const long long t0 = clock64();
+    while (!mbar_try_wait_cl(bar, parity)) {
+      if (*w.abort) ok = false;
+      else if (clock64() - t0 > w.budget) {
+        *w.abort = site;
+        ok = false;
+      }
+      if (!ok) break;
+    }
+  }
+  return __all_sync(0xffffffffu, ok);
+}
+
+template <int R>
+__global__ void __launch_bounds__(kThreads, 1)
+    pair_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_q,
+                const __grid_constant__ LatentAttnArgs args) {
+  using C = Cfg<R>;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const uint32_t sbase = smem_u32(smem);
+  auto bar = [&](int i) { return sbase + C::kBarOff + 8u * i; };
+  volatile uint32_t* misc = reinterpret_cast<volatile uint32_t*>(smem + C::kMiscOff);
+  auto seg_at = [&](uint32_t i) -> const Seg& {
+    return *reinterpret_cast<const Seg*>(smem + C::kSegOff + 48u * (i % kSegs));
+  };
+  float* own = reinterpret_cast<float*>(smem + C::kOwnOff);        // [2 key quarters][kRows]
+  float* peers = reinterpret_cast<float*>(smem + C::kPeerOff);     // [exchange & 1][kRows]
+  float* alphas = reinterpret_cast<float*>(smem + C::kAlphaOff);   // [kRows]
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t rank = cluster_rank(), peer = rank ^ 1u;
+  const bool leader = rank == 0u;
+  const int pair = blockIdx.x >> 1, share = pair / args.span, block = pair - share * args.span;
+  const int G = args.shares, group_rows = args.span * kRows;
+  if (!dcheck((sbase & 1023u) == 0u && C::kSmem <= static_cast<int>(dynamic_smem_bytes()) && share < G, args.status, 701))
+    return;                               // in both CTAs alike
+
+  const SeqCheck mine(args.s, tid);
+  if (tid < C::kNumBars) {
+    uint32_t n = 1;
+    if (tid == C::kOtherBoth || tid == C::kOtherBoth + 1) n = 2;
+    if (tid == C::kVote || tid == C::kAgain) n = 2 * kSoftmaxWarps;
+    if (tid == C::kExchange) n = kRows / 32;
+    if (tid == C::kSync) n = kSoftmaxWarps;
+    if (tid >= C::kSegEmpty) n = kSegReaders;
+    mbar_init(bar(tid), n);
+    fence_barrier_init();
+  }
+  if (tid >= C::kNumBars && tid < C::kNumBars + 10) misc[tid - C::kNumBars] = 0u;
+  if (warp == kLoadWarp && lane == 0) {
+    tma_prefetch_desc(&tm_k);
+    tma_prefetch_desc(&tm_q);
+  }
+  __syncthreads();
+  cluster_sync_all();                     // the other CTA's barriers are there
+  if (warp == kMmaWarp) {
+    tmem_alloc_pair(smem_u32(const_cast<uint32_t*>(&misc[0])), 512);
+    tmem_relinquish_pair();
+  }
+  const Share sh = locate_share<kKeys, kThreads>(args, mine, group_rows, G, share, reinterpret_cast<long long*>(own),
+                                                 const_cast<uint32_t*>(misc) + 8);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = misc[0];
+  const Waits wc{args.wait_budget, misc + 1};
+  auto uniform = [](int v) { return __shfl_sync(0xffffffffu, v, 0); };
+  auto wait_seg = [&](uint32_t i) { return wait_cl(bar(C::kSegFull + i % kSegs), (i / kSegs) & 1, wc, kWaitSegment); };
+  auto done_seg = [&](uint32_t i) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar(C::kSegEmpty + i % kSegs));
+  };
+  auto first_row = [&](const Seg& s) { return static_cast<long long>(s.rg) * group_rows + block * kRows; };
+  auto rows_of = [&](const Seg& s) { return static_cast<long long>(s.n) * args.Hq; };
+
+  if (warp < kSoftmaxWarps) {
+    // ================================================================ softmax
+    // A warp has 32 of this CTA's 64 keys and 32 of the 128 rows, a thread four keys of
+    // eight rows.  Every wait ends, and a warp whose wait ran out leaves.
+    const float c = args.scale_log2;
+    const int quarter = warp & 3, cols = 32 * (warp >> 2);          // of 64 columns of S
+    const int row_base = 64 * (quarter >> 1) + cols, key_base = 32 * (quarter & 1) + (lane >> 2);
+    const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
+    auto row_at = [&](int i) { return row_base + 8 * (i >> 1) + 2 * (lane & 3) + (i & 1); };
+    const uint32_t home = quarter >> 1;                             // the CTA that stages these rows of P
+    const uint32_t p_dst = map_shared(sbase + C::kPOff + rank * C::kChunk, home);
+    uint32_t tiles = 0, syncs = 0, exchanges = 0;
+    auto arrive_both = [&](int b) {
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive_cluster(map_shared(bar(b), 0));
+        mbar_arrive_cluster(map_shared(bar(b), 1));
+      }
+    };
+    auto sync = [&]() -> bool {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(C::kSync));
+      return wait_cl(bar(C::kSync), syncs++ & 1, wc, kWaitDrain);
+    };
+    // The rows' combined numbers of this CTA's keys (in own[0], own[1]) to the other.
+    auto exchange = [&](bool sums) -> bool {
+      if (!sync()) return false;
+      if (tid < kRows) {
+        const float a = own[tid], b = own[kRows + tid];
+        st_cluster_f32(map_shared(smem_u32(peers + (exchanges & 1) * kRows + tid), peer), sums ? a + b : fmaxf(a, b));
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(map_shared(bar(C::kExchange), peer));
+      }
+      return wait_cl(bar(C::kExchange), exchanges++ & 1, wc, kWaitDrain);
+    };
+    for (uint32_t si = 0; wait_seg(si); ++si) {
+      const Seg s = seg_at(si);
+      done_seg(si);
+      if (s.flags & Seg::kLast) break;
+      const long long row0 = first_row(s), rows = rows_of(s);
+      if (row0 >= rows) continue;
+      const int live = static_cast<int>(min(static_cast<long long>(kRows), rows - row0));
+      // Keys that a row sees; rows behind the block's last see all (nothing of theirs is
+      // stored, and a row of S, P and O depends on its own query only).
+      auto lim_of = [&](int row) {
+        if (!args.causal || row >= live) return s.len;
+        return max(0, min(s.len, s.len - s.n + static_cast<int>(static_cast<unsigned int>(row0 + row) / args.Hq) + 1));
+      };
+      const int lim_min = lim_of(0);
+      int lim[8];
+      float m[8], l[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        lim[i] = lim_of(row_at(i));
+        m[i] = -FLT_MAX;
+        l[i] = 0.f;
+      }
+      bool holes = false, ok = true;
+      for (int j = s.a; j < s.e; ++j, ++tiles) {
+        const int kv0 = j * kKeys, mine0 = kv0 + kHalfKeys * static_cast<int>(rank);
+        const bool first = j == s.a;
+        if (!(ok = wait_cl(bar(C::kSFull + (tiles & 1)), (tiles >> 1) & 1, wc, kWaitSFull))) break;
+        tc_fence_after();
+        uint32_t lo[16], hi[16];           // keys of lanes 0-15 and 16-31 of the quarter
+        const uint32_t ts = tmem + lane_off + C::col_s(tiles & 1) + cols;
+        tmem_ld_rows(ts, lo);
+        tmem_ld_rows(ts + (16u << 16), hi);
+        if (!(ok = wait_cl(bar(C::kMask + tiles % kValid), (tiles / kValid) & 1, wc, kWaitKvFull))) break;
+        const uint32_t mask = misc[4 + tiles % kValid];
+        tmem_ld_wait(lo);
+        tmem_ld_wait(hi);
+        const bool edge = mask != 15u || kv0 + kKeys > s.len;
+        // keys 0, 8, 16, 24 beyond the thread's first
+        auto score = [&](int i, int k) -> uint32_t& {
+          return (k < 2 ? lo : hi)[4 * (i >> 1) + 2 * (k & 1) + (i & 1)];
+        };
+        if (edge) {
+          uint32_t want = 0u;
+#pragma unroll
+          for (int g = 0; g < 4; ++g) want |= (kv0 + 32 * g < s.len ? 1u : 0u) << g;
+          holes |= (want & ~mask) != 0u;
+        }
+        if (edge || kv0 + kKeys > lim_min) {
+          const bool there = mask >> (2 * rank + (quarter & 1)) & 1u;     // the warp's 32 keys
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              if (!there || mine0 + key_base + 8 * k >= lim[i]) score(i, k) = __float_as_uint(-INFINITY);
+        }
+        auto val = [&](int i, int k) { return __uint_as_float(score(i, k)); };
+        auto top_of = [&](int i) { return fmaxf(fmaxf(val(i, 0), val(i, 1)), fmaxf(val(i, 2), val(i, 3))); };
+        float top = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) top = fmaxf(top, fmaf(top_of(i), c, -m[i]));
+        float part[8];                     // this tile's sums
+        // Probabilities with the references there are, to where their rows are staged.
+        auto write_p = [&]() {
+#pragma unroll
+          for (int o = 0; o < 4; ++o) {    // eight rows
+            uint32_t w[4];                 // eight keys each
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const float p0 = ex2_approx(fmaf(val(2 * o, k), c, -m[2 * o]));
+              const float p1 = ex2_approx(fmaf(val(2 * o + 1, k), c, -m[2 * o + 1]));
+              w[k] = pack_bf16x2(p0, p1);
+              part[2 * o] = k == 0 ? p0 : part[2 * o] + p0;
+              part[2 * o + 1] = k == 0 ? p1 : part[2 * o + 1] + p1;
+            }
+            const int chunk = 4 * (quarter & 1);
+            if (home == rank) {
+              const int row = cols + 8 * o + (lane & 7);
+              const uint32_t dst = sbase + C::kPOff + rank * C::kChunk + row * 128 + (((chunk + (lane >> 3)) ^ (row & 7)) << 4);
+              if (dcheck(in_range(dst, 16, sbase + C::kPOff, sbase + C::kRingOff), args.status, 702))
+                stmatrix_x4_trans(dst, w[0], w[1], w[2], w[3]);
+            } else {
+              // Transposed in registers: lane 4 r + q has keys 2 q, 2 q + 1 of row r of each chunk; the
+              // four lanes of a row then swap words, so that lane q has all of chunk q.
+#pragma unroll
+              for (int k = 0; k < 4; ++k) w[k] = movmatrix_trans(w[k]);
+              const int q = lane & 3;
+              uint32_t t[4];
+              // step 1, lanes two apart: chunks q & 2
+              const uint32_t a0 = __shfl_xor_sync(0xffffffffu, q & 2 ? w[0] : w[2], 2);
+              const uint32_t a1 = __shfl_xor_sync(0xffffffffu, q & 2 ? w[1] : w[3], 2);
+              const uint32_t k0 = q & 2 ? w[2] : w[0], k1 = q & 2 ? w[3] : w[1];
+              // now chunk (q & 2) + 0: words q and q ^ 2 are k0, a0; chunk + 1: k1, a1
+              const uint32_t b0 = __shfl_xor_sync(0xffffffffu, q & 1 ? k0 : k1, 1);
+              const uint32_t b1 = __shfl_xor_sync(0xffffffffu, q & 1 ? a0 : a1, 1);
+              const uint32_t m0 = q & 1 ? k1 : k0, m1 = q & 1 ? a1 : a0;
+              // chunk q: word q is m0, q ^ 2 m1, q ^ 1 b0, q ^ 3 b1
+              t[0] = q == 0 ? m0 : (q == 2 ? m1 : (q == 1 ? b0 : b1));
+              t[1] = q == 1 ? m0 : (q == 3 ? m1 : (q == 0 ? b0 : b1));
+              t[2] = q == 2 ? m0 : (q == 0 ? m1 : (q == 3 ? b0 : b1));
+              t[3] = q == 3 ? m0 : (q == 1 ? m1 : (q == 2 ? b0 : b1));
+              const int row = cols + 8 * o + (lane >> 2);
+              const uint32_t off = row * 128 + (((chunk + q) ^ (row & 7)) << 4);
+              if (dcheck(off + 16 <= static_cast<uint32_t>(C::kChunk), args.status, 703))
+                st_cluster_v4(p_dst + off, t[0], t[1], t[2], t[3]);
+            }
+          }
+          fence_proxy_async_cluster();
+        };
+        if (!first) {
+          if (!(ok = wait_cl(bar(C::kPvDone), (tiles - 1) & 1, wc, kWaitMmaDone))) break;   // P is free
+          write_p();
+        }
+        tc_fence_before();
+        if (__any_sync(0xffffffffu, first || edge || top > kTau) && lane < 2)
+          st_cluster_u32(map_shared(smem_u32(const_cast<uint32_t*>(&misc[2 + (tiles & 1)])), lane), tiles + 1);
+        arrive_both(C::kVote);
+        if (!(ok = wait_cl(bar(C::kVote), tiles & 1, wc, kWaitPFull))) break;
+        if (misc[2 + (tiles & 1)] == tiles + 1) {
+          // ---- in both CTAs: some row's reference moves, or keys are missing
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            float t = top_of(i) * c;
+#pragma unroll
+            for (int off = 4; off < 32; off <<= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, off));
+            if (lane < 4) own[(quarter & 1) * kRows + row_at(i)] = t;
+          }
+          if (!(ok = exchange(false))) break;
+          const float* other = peers + ((exchanges - 1) & 1) * kRows;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int row = row_at(i);
+            const float t = fmaxf(fmaxf(own[row], own[kRows + row]), other[row]);
+            const bool move = t > m[i] + kTau;
+            const float al = move ? ex2_approx(m[i] - t) : 1.f;
+            if (move) m[i] = t;
+            l[i] *= al;
+            if ((quarter & 1) == 0 && lane < 4) alphas[row] = al;
+          }
+          if (!(ok = sync())) break;
+          if (!first) {
+            tc_fence_after();
+#pragma unroll 1
+            for (int p = 0; p < C::kBlocks * 4; ++p) {
+              uint32_t o[16];
+              const int r0 = 64 * (warp >> 2) + 16 * (p & 3);
+              const uint32_t at = tmem + lane_off + C::col_o(p >> 2) + r0;
+              tmem_ld16(at, o);
+              const float4* al = reinterpret_cast<const float4*>(alphas + r0);
+              tmem_ld_wait(o);
+#pragma unroll
+              for (int z = 0; z < 4; ++z) {
+                const float4 f = al[z];
+                o[4 * z] = __float_as_uint(__uint_as_float(o[4 * z]) * f.x);
+                o[4 * z + 1] = __float_as_uint(__uint_as_float(o[4 * z + 1]) * f.y);
+                o[4 * z + 2] = __float_as_uint(__uint_as_float(o[4 * z + 2]) * f.z);
+                o[4 * z + 3] = __float_as_uint(__uint_as_float(o[4 * z + 3]) * f.w);
+              }
+              tmem_st16(at, o);
+            }
+            tmem_st_wait();
+          }
+          write_p();
+          if (edge) {
+            // Slots behind the end and pages that do not exist hold anything, and zero times a
+            // NaN is a NaN.
+            if (!(ok = wait_cl(bar(C::kOther + (tiles & 1)), (tiles >> 1) & 1, wc, kWaitKvFull))) break;
+#pragma unroll 1
+            for (int id = tid; id < 2 * C::kBlocks * 2 * kHalfKeys * 8; id += 32 * kSoftmaxWarps) {
+              const int r = id >> 3 & (kHalfKeys - 1), half = id >> 9;      // half pairs, 64 rows of 8 pieces each
+              const int h = half / (2 * C::kBlocks);                        // the keys' CTA
+              if (kv0 + kHalfKeys * h + r < s.len && (mask >> (2 * h + (r >> 5)) & 1u)) continue;
+              const uint32_t slot = (tiles * C::kPairs + (half >> 1)) % C::kRing;
+              const uint32_t dst = sbase + C::kRingOff + slot * C::kPairTile + (half & 1) * C::kChunk + r * 128 + (id & 7) * 16;
+              if (dcheck(in_range(dst, 16, sbase + C::kRingOff, sbase + C::kRopeOff), args.status, 704))
+                st_shared_v4(dst, 0u, 0u, 0u, 0u);
+            }
+            fence_proxy_async_cluster();
+          }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster(map_shared(bar(C::kAgain), 0));
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) l[i] += part[i];
+      }
+      if (!ok) break;
+      // ---- results: this CTA's half of the columns, for all rows
+      if (!wait_cl(bar(C::kPvDone), (tiles - 1) & 1, wc, kWaitOFull)) break;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+#pragma unroll
+        for (int off = 4; off < 32; off <<= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], off);
+        if (lane < 4) own[(quarter & 1) * kRows + row_at(i)] = l[i];
+        if ((quarter & 1) == 0 && lane < 4) alphas[row_at(i)] = m[i];
+      }
+      if (!exchange(true)) break;
+      tc_fence_after();
+      const bool whole = s.whole();
+      const long long slot = 2ll * pair + (s.flags & Seg::kStarts);
+      const long long out0 = static_cast<long long>(s.r0) * args.Hq + row0;
+      if (tid < kRows) {
+        const float here = own[tid] + own[kRows + tid], there = peers[((exchanges - 1) & 1) * kRows + tid];
+        float lt = leader ? here + there : there + here;
+        const float mt = alphas[tid];
+        // All scores of keys that the row sees are -inf: its query holds an infinity.
+        if (lt == 0.f && !holes && lim_of(tid) > s.a * kKeys) lt = __int_as_float(0x7fffffff);
+        if (leader && tid < live) {
+          if (whole) args.lse[out0 + tid] = lt == 0.f ? -INFINITY : (mt + log2f(lt)) * kLn2;
+          else args.part_ml[slot * kRows + tid] = make_float2(mt, lt);
+        }
+        alphas[tid] = lt == 0.f ? 0.f : 1.f / lt;
+      }
+      if (!sync()) break;
+      const int col_base = R / 2 * static_cast<int>(rank) + 32 * quarter;     // of O
+      if (whole) {
+        // As in the kernel for 64 rows, through P's place: the other CTA writes to it again only
+        // after the next unit's first exchange.
+        const uint32_t stage = sbase + C::kPOff + warp * 2048;
+#pragma unroll 1
+        for (int t = 0; t < 2 * C::kBlocks; ++t) {
+          const int r0 = 64 * (warp >> 2) + 32 * (t & 1);
+          if (r0 >= live) continue;
+          uint32_t lo[16], hi[16];
+          const uint32_t at = tmem + lane_off + C::col_o(t >> 1) + r0;
+          tmem_ld_rows(at, lo);
+          tmem_ld_rows(at + (16u << 16), hi);
+          tmem_ld_wait(lo);
+          tmem_ld_wait(hi);
+          __syncwarp();
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float2 f = *reinterpret_cast<const float2*>(alphas + r0 + 8 * i + 2 * (lane & 3));
+            auto pair_of = [&](const uint32_t* r) {
+              return pack_bf16x2(__uint_as_float(r[0]) * f.x, __uint_as_float(r[1]) * f.y);
+            };
+            const int row = 8 * i + (lane & 7), chunk = lane >> 3;
+            stmatrix_x4_trans(stage + row * 64 + ((chunk ^ (row >> 1 & 3)) << 4), pair_of(lo + 4 * i), pair_of(lo + 4 * i + 2),
+                              pair_of(hi + 4 * i), pair_of(hi + 4 * i + 2));
+          }
+          __syncwarp();
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int row = 8 * i + (lane >> 2), chunk = lane & 3;
+            const uint4 w = ld_shared_v4(stage + row * 64 + ((chunk ^ (row >> 1 & 3)) << 4));
+            if (r0 + row < live &&
+                dcheck(inside(out0 + r0 + row, 1, static_cast<long long>(args.s.T) * args.Hq), args.status, 705))
+              *reinterpret_cast<uint4*>(args.o + (out0 + r0 + row) * R + col_base + 128 * (t >> 1) + 8 * chunk) = w;
+          }
+        }
+      } else {
+#pragma unroll 2
+        for (int p = 0; p < C::kBlocks * 4; ++p) {
+          const int r0 = 64 * (warp >> 2) + 16 * (p & 3);
+          if (r0 >= live) continue;
+          uint32_t o[16];
+          tmem_ld16(tmem + lane_off + C::col_o(p >> 2) + r0, o);
+          float* to = args.part_o + (slot * kRows + r0) * R + col_base + 128 * (p >> 2) + lane;
+          tmem_ld_wait(o);
+#pragma unroll
+          for (int z = 0; z < 16; ++z)
+            if (r0 + z < live && dcheck(slot < 2ll * kSms, args.status, 706)) to[z * R] = __uint_as_float(o[z]);
+        }
+      }
+    }
+  } else if (warp == kMmaWarp) {
+    // ================================================================ MMA issue
+    const uint32_t lead = elect_lane();
+    constexpr uint32_t idesc_s = idesc_bf16_f32(128, kRows, false, false);
+    constexpr uint32_t idesc_o = idesc_bf16_f32(256, kRows, true, false);
+    uint32_t tiles = 0, pvs = 0, again = 0, q_count = 0;
+    uint32_t rs = 0, rph = 0, ks = 0, kph = 0, vs = 0;   // slots and phases, as in the kernel for 64 rows
+    auto ready = [&](int b, uint32_t parity) { return bar_done_cl(bar(b), parity); };
+    auto product4 = [&](uint32_t d, uint32_t a, uint32_t b, uint32_t acc) {
+      const uint64_t da = sdesc_sw128(a, 16, 1024), db = sdesc_sw128(b, 16, 1024);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) mma2_lead(d, da + 2 * k, db + 2 * k, idesc_s, k > 0 ? 1u : acc, lead);
+    };
+    auto values = [&](uint32_t acc) -> bool {
+      // (the vote is there)
+      if (misc[2 + (pvs & 1)] == pvs + 1 && !wait_cl(bar(C::kAgain), again++ & 1, wc, kWaitPFull)) return false;
+      if (!wait_cl(bar(C::kOtherBoth + (pvs & 1)), (pvs >> 1) & 1, wc, kWaitKvFull)) return false;
+      tc_fence_after();
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const uint64_t db = sdesc_sw128(sbase + C::kPOff + h * C::kChunk, 16, 1024);
+#pragma unroll
+        for (int b = 0; b < C::kBlocks; ++b) {
+          const uint64_t da = sdesc_sw128(sbase + C::kRingOff + vs * C::kPairTile, C::kChunk, 1024);
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            mma2_lead(tmem + C::col_o(b), da + ((k * 2048) >> 4), db + 2 * k, idesc_o, h + k > 0 ? 1u : acc, lead);
+          commit2_lead(bar(C::kEmpty + vs), lead);
+          vs = vs + 1 == C::kRing ? 0u : vs + 1;
+        }
+      }
+      commit2_lead(bar(C::kPvDone), lead);
+      ++pvs;
+      return true;
+    };
+    auto run = [&](const int n) -> bool {
+      if (!wait_cl(bar(C::kQFull), q_count++ & 1, wc, kWaitQFull)) return false;
+      tc_fence_after();
+      for (int i = 0; i <= n; ++i) {
+        bool due = i > 0;                 // values of tile i - 1
+        if (i < n) {
+          // As in the kernel for 64 rows: scores first, but values while the scores' tile is on its way.
+          for (long long t0 = 0; !ready(C::kRopeFull + rs, rph) || !ready(C::kFull + ks, kph);) {
+            if (due && ready(C::kVote, pvs & 1)) {
+              if (!values(i > 1 ? 1u : 0u)) return false;
+              due = false;
+            }
+            const long long now = clock64();
+            if (t0 == 0) t0 = now;
+            if (now - t0 > wc.budget && *wc.abort == 0u) *wc.abort = kWaitKvFull;
+            if (!__all_sync(0xffffffffu, *wc.abort == 0u)) return false;
+          }
+          tc_fence_after();
+          const uint32_t d = tmem + C::col_s(tiles & 1);
+          product4(d, sbase + C::kRopeOff + rs * C::kChunk, sbase + C::kQOff + 2 * C::kPairs * C::kChunk, 0u);
+          commit2_lead(bar(C::kRopeEmpty + rs), lead);
+          if (++rs == C::kRopes) {
+            rs = 0;
+            rph ^= 1u;
+          }
+#pragma unroll
+          for (int p = 0; p < C::kPairs; ++p) {
+            if (p > 0 && !wait_cl(bar(C::kFull + ks), kph, wc, kWaitKvFull)) return false;
+            const uint32_t k = sbase + C::kRingOff + ks * C::kPairTile, q = sbase + C::kQOff + 2 * p * C::kChunk;
+            product4(d, k, q, 1u);
+            product4(d, k + C::kChunk, q + C::kChunk, 1u);
+            if (++ks == C::kRing) {
+              ks = 0;
+              kph ^= 1u;
+            }
+          }
+          commit2_lead(bar(C::kSFull + (tiles & 1)), lead);
+          if (i + 1 == n) commit2_lead(bar(C::kQEmpty), lead);
+          ++tiles;
+        }
+        if (due) {
+          if (!wait_cl(bar(C::kVote), pvs & 1, wc, kWaitPFull)) return false;
+          if (!values(i > 1 ? 1u : 0u)) return false;
+        }
+      }
+      return true;
+    };
+    for (uint32_t si = 0; wait_seg(si); ++si) {
+      const Seg& s = seg_at(si);
+      const int flags = uniform(s.flags), n = uniform(s.e - s.a);
+      const bool on = uniform(first_row(s) < rows_of(s) ? 1 : 0) != 0;
+      done_seg(si);
+      if (flags & Seg::kLast) break;
+      if (leader && on && !run(n)) break;
+    }
+    // No product may still be running when either CTA's memory goes.
+    if (leader) commit2_lead(bar(C::kMmaDone), lead);
+    mbar_drain_cl(bar(C::kMmaDone), 0);
+    __syncwarp();
+  } else if (warp == kLoadWarp || warp == kOtherWarp) {
+    // ================================================================ loads
+    // A tile's pages of the CTA's own keys, or of the other's: one, or two of 32 tokens.  A page
+    // that does not exist is read as page 0, so that both CTAs' copies always count the
+    // same bytes; its scores are masked and its values zeroed.
+    const int page = 1 << args.page_shift, box = min(page, kHalfKeys), boxes = kHalfKeys / box;
+    const uint32_t half = warp == kLoadWarp ? rank : peer;
+    uint32_t tiles = 0, q_count = 0, rs = 0, ropes = 0, ps = 0, eph = 0, pairs = 0;
+    bool ok = true;
+    for (uint32_t si = 0; ok && wait_seg(si); ++si) {
+      const Seg s = seg_at(si);
+      done_seg(si);
+      if (s.flags & Seg::kLast) break;
+      const long long row0 = first_row(s);
+      if (row0 >= rows_of(s)) continue;
+      if (warp == kLoadWarp) {
+        if (q_count > 0 && !wait_cl(bar(C::kQEmpty), (q_count - 1) & 1, wc, kWaitQFull)) break;
+        ++q_count;
+        if (leader) mbar_arrive_expect_tx_w(bar(C::kQFull), 2 * C::kQBytes);
+        tma2_load_3d_w(sbase + C::kQOff, &tm_q, map_shared(bar(C::kQFull), 0), 0,
+                       uniform(static_cast<int>(static_cast<long long>(s.r0) * args.Hq + row0) + 64 * static_cast<int>(rank)), 0);
+      }
+      const int first_tile = uniform(s.a), last_tile = uniform(s.e);
+      int base = (first_tile * kKeys) >> args.page_shift;
+      int cur = page_of_lane(args, s.b, s.len, base), nxt = page_of_lane(args, s.b, s.len, base + 32);
+      for (int j = first_tile; j < last_tile; ++j, ++tiles) {
+        const int first = (j * kKeys) >> args.page_shift;
+        if (first >= base + 32) {
+          base += 32;
+          cur = nxt;
+          nxt = page_of_lane(args, s.b, s.len, base + 32);
+        }
+        // The page of the tile's 32 keys from 32 g on.
+        auto page_at = [&](int g) { return __shfl_sync(0xffffffffu, cur, ((j * kKeys + 32 * g) >> args.page_shift) - base); };
+        auto good = [&](int p) { return p >= 0 && p < args.pages; };
+        int pid0 = page_at(2 * half), pid1 = page_at(2 * half + 1);
+        const int row = (j * kKeys + kHalfKeys * static_cast<int>(half)) & (page - 1);
+        if (warp == kLoadWarp) {
+          uint32_t mask = 0u;
+#pragma unroll
+          for (int g = 0; g < 4; ++g) {
+            const int p = page_at(g);
+            if (good(p)) mask |= 1u << g;
+            else if (leader && lane == 0 && j * kKeys + 32 * g < s.len) record_bad_index(args.status, kSitePage);
+          }
+          pid0 = good(pid0) ? pid0 : 0;
+          pid1 = good(pid1) ? pid1 : 0;
+          auto load64 = [&](uint32_t dst, uint32_t b, int col) {
+            tma2_load_3d_w(dst, &tm_k, b, col, row, pid0);
+            if (boxes == 2) tma2_load_3d_w(dst + 4096, &tm_k, b, col, row, pid1);
+          };
+          if (ropes >= C::kRopes && !wait_cl(bar(C::kRopeEmpty + rs), (ropes / C::kRopes - 1) & 1, wc, kWaitKvEmpty)) {
+            ok = false;
+            break;
+          }
+          if (leader) mbar_arrive_expect_tx_w(bar(C::kRopeFull + rs), 2 * C::kChunk);
+          load64(sbase + C::kRopeOff + rs * C::kChunk, map_shared(bar(C::kRopeFull + rs), 0), R);
+          ++ropes;
+          rs = rs + 1 == C::kRopes ? 0u : rs + 1;
+#pragma unroll
+          for (int p = 0; p < C::kPairs; ++p) {
+            if (pairs >= C::kRing && !wait_cl(bar(C::kEmpty + ps), eph ^ 1u, wc, kWaitKvEmpty)) {
+              ok = false;
+              break;
+            }
+            if (p == 0) {
+              if (lane == 0) {
+                misc[4 + tiles % kValid] = mask;
+                mbar_arrive(bar(C::kMask + tiles % kValid));
+              }
+              __syncwarp();
+            }
+            const uint32_t dst = sbase + C::kRingOff + ps * C::kPairTile, b = map_shared(bar(C::kFull + ps), 0);
+            if (leader) mbar_arrive_expect_tx_w(bar(C::kFull + ps), 2 * C::kPairTile);
+            load64(dst, b, 128 * p);
+            load64(dst + C::kChunk, b, 128 * p + 64);
+            ++pairs;
+            if (++ps == C::kRing) {
+              ps = 0;
+              eph ^= 1u;
+            }
+          }
+          if (!ok) break;
+        } else {
+          // The other's keys, this CTA's columns, in place of its own keys' other columns once the
+          // scores are computed.
+          pid0 = good(pid0) ? pid0 : 0;
+          pid1 = good(pid1) ? pid1 : 0;
+          const uint32_t b = bar(C::kOther + (tiles & 1));
+          if (!wait_cl(bar(C::kSFull + (tiles & 1)), (tiles >> 1) & 1, wc, kWaitSFull)) {
+            ok = false;
+            break;
+          }
+          mbar_arrive_expect_tx_w(b, C::kBlocks * C::kPairTile);
+#pragma unroll
+          for (int i = 0; i < 2 * C::kBlocks; ++i) {
+            const uint32_t slot = (tiles * C::kPairs + half * C::kBlocks + (i >> 1)) % C::kRing;
+            const uint32_t dst = sbase + C::kRingOff + slot * C::kPairTile + (i & 1) * C::kChunk;
+            const int col = R / 2 * static_cast<int>(rank) + 64 * i;
+            tma_load_3d_w(dst, &tm_k, b, col, row, pid0);
+            if (boxes == 2) tma_load_3d_w(dst + 4096, &tm_k, b, col, row, pid1);
+          }
+          if (!wait_cl(b, (tiles >> 1) & 1, wc, kWaitKvFull)) {
+            ok = false;
+            break;
+          }
+          if (lane == 0) mbar_arrive_cluster(map_shared(bar(C::kOtherBoth + (tiles & 1)), 0));
+          __syncwarp();
+        }
+      }
+    }
+    __syncwarp();
+  } else if (warp == kWalkWarp) {
+    // ================================================================ schedule
+    Walker<kKeys> walk(args, group_rows, static_cast<int>(misc[8]), static_cast<int>(misc[9]), sh.j1 - sh.j0);
+    Seg s{};
+    bool any = false;
+    for (uint32_t i = 0;; ++i) {
+      Seg x{};
+      const bool more = walk.next(x);
+      if (more) {
+        s = x;
+        any = true;
+      } else {
+        x.flags = Seg::kLast;
+      }
+      if (i >= kSegs && !wait_cl(bar(C::kSegEmpty + i % kSegs), (i / kSegs - 1) & 1, wc, kWaitSegment)) {
+        any = false;
+        break;
+      }
+      if (lane == 0) {
+        const_cast<Seg&>(seg_at(i)) = x;
+        mbar_arrive(bar(C::kSegFull + i % kSegs));
+      }
+      __syncwarp();
+      if (!more) break;
+    }
+    if (lane == 0 && block == 0 && leader) {
+      // What is to be joined: the unit that this share starts and others go on with
+      // (its last one).
+      const bool shared_unit = any && (s.flags & (Seg::kStarts | Seg::kEnds)) == Seg::kStarts;
+      args.rec[share] = shared_unit ? make_int4(s.r0, s.n, s.rg, cta_of(sh.W, sh.busy, sh.j1 - (s.e - s.a) + s.nt - 1))
+                                    : make_int4(0, 0, 0, 0);
+    }
+    __syncwarp();
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  // Every copy must have landed before the pair ends.  In good order the products waited
+  // for all of them; where a wait ran out they are given half a millisecond, hundreds
+  // of times what a copy takes (a CTA cannot wait for those that the other counts).
+  if (*wc.abort != 0u)
+    for (const long long t0 = clock64(); clock64() - t0 < (1 << 20);) {
+    }
+  cluster_sync_all();                     // neither CTA's memory is used any more
+  allow_child();
+  if (tid == 0) report_abort(misc[1], args.status);
+  if (warp == kMmaWarp) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem, 512);
+  }
+}
+
+template <int R>
+cudaError_t launch_t(const CUtensorMap& tk, const CUtensorMap& tq, const LatentAttnArgs& a, cudaStream_t stream) {
+  auto kern = pair_kernel<R>;
+  static SmemLimit limit;
+  cudaError_t e = limit.raise(reinterpret_cast<const void*>(kern), Cfg<R>::kSmem);
+  if (e != cudaSuccess) return e;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = 2;
+  attr.val.clusterDim.y = 1;
+  attr.val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = 2 * a.span * a.shares;
+  cfg.blockDim = kThreads;
+  cfg.dynamicSmemBytes = Cfg<R>::kSmem;
+  cfg.stream = stream;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  if ((e = cudaLaunchKernelEx(&cfg, kern, tk, tq, a)) != cudaSuccess) return e;
+  if (a.shares == 1) return cudaSuccess;   // nothing is shared
+  return launch_latent_join(kRows, R, a, stream);
+}
+
+}  // namespace
+
+cudaError_t launch_latent_pair(int rank, const CUtensorMap& tk, const CUtensorMap& tq, const LatentAttnArgs& a,
+                               cudaStream_t stream) {
+  return rank == 256 ? launch_t<256>(tk, tq, a, stream) : launch_t<512>(tk, tq, a, stream);
+}
+
+}  // namespace fattn
