@@ -160,15 +160,14 @@ struct Groups {
   }
 };
 
-// One share's part of a unit: key tiles [a, e) of nt for row group rg of a sequence.
+// One share's part of a unit: key tiles [a, e) for row group rg of a sequence.
 struct __align__(16) Seg {
   int b, rg, r0, n;
   int len, flags, a, e;
-  int nt, pad0, pad1, pad2;
   static constexpr int kStarts = 1, kEnds = 2, kLast = 8;
   __device__ __forceinline__ bool whole() const { return (flags & 3) == 3; }
 };
-static_assert(sizeof(Seg) == 48, "ring slot");
+static_assert(sizeof(Seg) == 32, "ring slot");
 
 // Walks a share.
 template <int KEYS>
@@ -216,7 +215,6 @@ struct Walker {
     s.len = q.len;
     s.a = at;
     s.e = min(nt, at + left);
-    s.nt = nt;
     s.flags = (at == 0 ? Seg::kStarts : 0) | (s.e == nt ? Seg::kEnds : 0);
     left -= s.e - s.a;
     at = s.e;

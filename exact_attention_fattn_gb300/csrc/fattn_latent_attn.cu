@@ -83,7 +83,7 @@ struct Cfg {
   static constexpr int kMiscOff = kBarOff + kNumBars * 8;       // tmem, abort, start of the share
   static constexpr int kValidOff = kMiscOff + 32;
   static constexpr int kSegOff = (kValidOff + 4 * kValid + 15) / 16 * 16;
-  static constexpr int kXOff = kSegOff + kSegs * 48;            // [4][N] float
+  static constexpr int kXOff = kSegOff + kSegs * 32;            // [4][N] float
   static constexpr int kAlphaOff = kXOff + 16 * N;              // [N] float
   static constexpr int kLimOff = kAlphaOff + 4 * N;             // [N] int
   static constexpr int kSmem = kLimOff + 4 * N;
@@ -133,7 +133,7 @@ __global__ void __launch_bounds__(Cfg<N, R>::kThreads, 1)
   uint32_t* misc = reinterpret_cast<uint32_t*>(smem + C::kMiscOff);
   volatile uint32_t* valid = reinterpret_cast<volatile uint32_t*>(smem + C::kValidOff);
   auto seg_at = [&](uint32_t i) -> const Seg& {
-    return *reinterpret_cast<const Seg*>(smem + C::kSegOff + 48u * (i % kSegs));
+    return *reinterpret_cast<const Seg*>(smem + C::kSegOff + 32u * (i % kSegs));
   };
   float* xs = reinterpret_cast<float*>(smem + C::kXOff);          // [4][N]
   float* alphas = reinterpret_cast<float*>(smem + C::kAlphaOff);   // [N]
@@ -623,7 +623,7 @@ __global__ void __launch_bounds__(Cfg<N, R>::kThreads, 1)
       // What is to be joined: the unit that this share starts and others go on with
       // (its last one).
       const bool shared_unit = any && (s.flags & (Seg::kStarts | Seg::kEnds)) == Seg::kStarts;
-      args.rec[share] = shared_unit ? make_int4(s.r0, s.n, s.rg, cta_of(sh.W, sh.busy, sh.j1 - (s.e - s.a) + s.nt - 1))
+      args.rec[share] = shared_unit ? make_int4(s.r0, s.n, s.rg, cta_of(sh.W, sh.busy, sh.j1 - (s.e - s.a) + walk.nt - 1))
                                     : make_int4(0, 0, 0, 0);
     }
     __syncwarp();

@@ -18,11 +18,14 @@
 // 65, P 32) and written 122 KB, 2870 cycles.  Two CTAs with 64 rows each need 5100.
 //
 // Softmax: tensor memory gives lanes 0-63 a CTA's keys for rows 0-63, lanes 64-127 the
-// same keys for rows 64-127.  Both CTAs keep the same reference of every row.  A
-// tile's probabilities are computed with the references there are, and with them
-// goes a vote: had any row of either CTA a score above its reference by more than 2^8
-// (the first tile of a unit always has), the CTAs exchange the rows' maxima, move the
-// references alike, rescale and compute the tile's probabilities again.
+// same keys for rows 64-127.  Both CTAs keep the same reference of every row, so they
+// vote on each tile: where any row of either has a score above its reference by more
+// than 2^8 (the first tile of a unit always has), they exchange the rows' maxima and
+// move the references alike.  While the votes travel the probabilities are computed
+// with the references there are.  What goes to the other CTA are asynchronous stores
+// that count on a barrier there: a release at cluster scope waits for all that the
+// thread has stored (votes and P by plain remote stores and releases took 5500 cycles
+// a tile, 2500 of them waiting for the votes).
 //
 // Work split and join as in fattn_latent_attn.cu, a pair in a CTA's place.
 //
@@ -46,7 +49,6 @@ constexpr int kOtherWarp = 10;
 constexpr int kWalkWarp = 11;
 constexpr int kSegs = 2;
 constexpr int kSegReaders = kSoftmaxWarps + 3;
-constexpr int kValid = 4;             // tiles whose masks are kept; as many as the ring holds at most
 
 template <int R>
 struct Cfg {
@@ -63,32 +65,35 @@ struct Cfg {
   static constexpr int kRopes = R == 512 ? 1 : 2;
   static constexpr int kRopeOff = kRingOff + kRing * kPairTile;
   static constexpr int kBarOff = kRopeOff + kRopes * kChunk;
-  static_assert(kRing >= 2 * kPairs && kRing / kPairs <= kValid, "ring");
+  static_assert(kRing >= 2 * kPairs && kRing % kPairs == 0, "ring");
+  static constexpr int kValid = kRing / kPairs;      // tiles whose masks are kept
   // barriers; those with (l) count for both CTAs in the leader's shared memory
   enum : int {
     kFull = 0,                    // (l) pair slots
     kEmpty = kFull + kRing,
     kRopeFull = kEmpty + kRing,   // (l)
-    kRopeEmpty = kRopeFull + 2,
-    kOther = kRopeEmpty + 2,      // the other CTA's keys, in this CTA
+    kRopeEmpty = kRopeFull + kRopes,
+    kOther = kRopeEmpty + kRopes, // the other CTA's keys, in this CTA
     kOtherBoth = kOther + 2,      // (l) in both
     kQFull = kOtherBoth + 2,      // (l)
     kQEmpty,
     kSFull,
     kMask = kSFull + 2,
-    kVote = kMask + kValid,       // probabilities and votes of both CTAs
-    kAgain,                       // (l) probabilities computed again
-    kExchange,                    // the other CTA's maxima or sums
-    kSync,                        // this CTA's softmax warps
-    kPvDone,
-    kMmaDone,
+    kVote = kMask + kValid,
+    kProb = kVote + 2,            // this CTA's rows of P, of either CTA's keys
+    kProbPeer = kProb + 2,        // (l) the other's
+    kExchange = kProbPeer + 2,    // the other CTA's maxima or sums
+    kSync = kExchange + 2,        // this CTA's softmax warps
+    kPvDone,                      // the products with either CTA's keys
+    kMmaDone = kPvDone + 2,
     kSegFull,
     kSegEmpty = kSegFull + kSegs,
     kNumBars = kSegEmpty + kSegs
   };
-  static constexpr int kMiscOff = kBarOff + kNumBars * 8;   // tmem, abort, flags[2], masks[4], start of the share
-  static constexpr int kSegOff = (kMiscOff + 40 + 15) / 16 * 16;
-  static constexpr int kOwnOff = kSegOff + kSegs * 48;      // [2][kRows] float
+  static constexpr int kMiscOff = kBarOff + kNumBars * 8;   // tmem, abort, votes[2], masks[]
+  static constexpr int kPeerVoteOff = kMiscOff + 16 + 4 * kValid;   // [2][8]
+  static constexpr int kSegOff = (kPeerVoteOff + 64 + 15) / 16 * 16;
+  static constexpr int kOwnOff = kSegOff + kSegs * 32;      // [2][kRows] float
   static constexpr int kPeerOff = kOwnOff + 2 * kRows * 4;  // [2][kRows] float
   static constexpr int kAlphaOff = kPeerOff + 2 * kRows * 4;
   static constexpr int kSmem = kAlphaOff + kRows * 4;
@@ -115,11 +120,11 @@ __device__ __forceinline__ void commit2_lead(uint32_t bar, uint32_t lead) {
       "h"(mask), "r"(lead)
       : "memory");
 }
-__device__ __forceinline__ void st_cluster_f32(uint32_t cluster_addr, float x) {
-  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(cluster_addr), "f"(x) : "memory");
-}
-__device__ __forceinline__ void st_cluster_u32(uint32_t cluster_addr, uint32_t x) {
-  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(cluster_addr), "r"(x) : "memory");
+// Like st_async_v4, four bytes.
+__device__ __forceinline__ void st_async_u32(uint32_t cluster_addr, uint32_t x, uint32_t cluster_bar) {
+  asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.b32 [%0], %1, [%2];" ::"r"(cluster_addr), "r"(x),
+               "r"(cluster_bar)
+               : "memory");
 }
 // An 8 x 8 matrix of 16-bit elements, two a lane, transposed.
 __device__ __forceinline__ uint32_t movmatrix_trans(uint32_t x) {
@@ -168,8 +173,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto bar = [&](int i) { return sbase + C::kBarOff + 8u * i; };
   volatile uint32_t* misc = reinterpret_cast<volatile uint32_t*>(smem + C::kMiscOff);
   auto seg_at = [&](uint32_t i) -> const Seg& {
-    return *reinterpret_cast<const Seg*>(smem + C::kSegOff + 48u * (i % kSegs));
+    return *reinterpret_cast<const Seg*>(smem + C::kSegOff + 32u * (i % kSegs));
   };
+  volatile uint32_t* peer_votes = reinterpret_cast<volatile uint32_t*>(smem + C::kPeerVoteOff);   // [2][8]
   float* own = reinterpret_cast<float*>(smem + C::kOwnOff);        // [2 key quarters][kRows]
   float* peers = reinterpret_cast<float*>(smem + C::kPeerOff);     // [exchange & 1][kRows]
   float* alphas = reinterpret_cast<float*>(smem + C::kAlphaOff);   // [kRows]
@@ -186,14 +192,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (tid < C::kNumBars) {
     uint32_t n = 1;
     if (tid == C::kOtherBoth || tid == C::kOtherBoth + 1) n = 2;
-    if (tid == C::kVote || tid == C::kAgain) n = 2 * kSoftmaxWarps;
-    if (tid == C::kExchange) n = kRows / 32;
-    if (tid == C::kSync) n = kSoftmaxWarps;
+    if (tid == C::kVote || tid == C::kVote + 1 || tid == C::kProb + static_cast<int>(rank) || tid == C::kSync)
+      n = kSoftmaxWarps;
     if (tid >= C::kSegEmpty) n = kSegReaders;
     mbar_init(bar(tid), n);
     fence_barrier_init();
   }
-  if (tid >= C::kNumBars && tid < C::kNumBars + 10) misc[tid - C::kNumBars] = 0u;
+  if (tid >= C::kNumBars && tid < C::kNumBars + 4 + C::kValid) misc[tid - C::kNumBars] = 0u;
   if (warp == kLoadWarp && lane == 0) {
     tma_prefetch_desc(&tm_k);
     tma_prefetch_desc(&tm_q);
@@ -205,7 +210,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_relinquish_pair();
   }
   const Share sh = locate_share<kKeys, kThreads>(args, mine, group_rows, G, share, reinterpret_cast<long long*>(own),
-                                                 const_cast<uint32_t*>(misc) + 8);
+                                                 reinterpret_cast<uint32_t*>(smem + C::kSegOff));   // read before the first segment
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -232,13 +237,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t home = quarter >> 1;                             // the CTA that stages these rows of P
     const uint32_t p_dst = map_shared(sbase + C::kPOff + rank * C::kChunk, home);
     uint32_t tiles = 0, syncs = 0, exchanges = 0;
-    auto arrive_both = [&](int b) {
-      __syncwarp();
-      if (lane == 0) {
-        mbar_arrive_cluster(map_shared(bar(b), 0));
-        mbar_arrive_cluster(map_shared(bar(b), 1));
-      }
-    };
     auto sync = [&]() -> bool {
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(C::kSync));
@@ -247,13 +245,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     // The rows' combined numbers of this CTA's keys (in own[0], own[1]) to the other.
     auto exchange = [&](bool sums) -> bool {
       if (!sync()) return false;
+      const int b = C::kExchange + (exchanges & 1);
       if (tid < kRows) {
-        const float a = own[tid], b = own[kRows + tid];
-        st_cluster_f32(map_shared(smem_u32(peers + (exchanges & 1) * kRows + tid), peer), sums ? a + b : fmaxf(a, b));
-        __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(map_shared(bar(C::kExchange), peer));
+        const float x = own[tid], y = own[kRows + tid];
+        st_async_u32(map_shared(smem_u32(peers + (exchanges & 1) * kRows + tid), peer),
+                     __float_as_uint(sums ? x + y : fmaxf(x, y)), map_shared(bar(b), peer));
       }
-      return wait_cl(bar(C::kExchange), exchanges++ & 1, wc, kWaitDrain);
+      if (tid == 0) mbar_arrive_expect_tx(bar(b), kRows * 4);
+      return wait_cl(bar(b), exchanges++ >> 1 & 1, wc, kWaitDrain);
     };
     for (uint32_t si = 0; wait_seg(si); ++si) {
       const Seg s = seg_at(si);
@@ -287,8 +286,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t ts = tmem + lane_off + C::col_s(tiles & 1) + cols;
         tmem_ld_rows(ts, lo);
         tmem_ld_rows(ts + (16u << 16), hi);
-        if (!(ok = wait_cl(bar(C::kMask + tiles % kValid), (tiles / kValid) & 1, wc, kWaitKvFull))) break;
-        const uint32_t mask = misc[4 + tiles % kValid];
+        if (!(ok = wait_cl(bar(C::kMask + tiles % C::kValid), (tiles / C::kValid) & 1, wc, kWaitKvFull))) break;
+        const uint32_t mask = misc[4 + tiles % C::kValid];
         tmem_ld_wait(lo);
         tmem_ld_wait(hi);
         const bool edge = mask != 15u || kv0 + kKeys > s.len;
@@ -315,65 +314,64 @@ __global__ void __launch_bounds__(kThreads, 1)
         float top = -INFINITY;
 #pragma unroll
         for (int i = 0; i < 8; ++i) top = fmaxf(top, fmaf(top_of(i), c, -m[i]));
+        // The vote; two barriers in turn, as a CTA may be one tile ahead.
+        const uint32_t turn = tiles & 1;
+        const bool over = __any_sync(0xffffffffu, first || edge || top > kTau);
+        if (lane == 0) {
+          st_async_u32(map_shared(smem_u32(const_cast<uint32_t*>(&peer_votes[8 * turn + warp])), peer), over ? 1u : 0u,
+                       map_shared(bar(C::kVote + turn), peer));
+          if (over) misc[2 + turn] = tiles + 1;
+          if (warp == 0) mbar_arrive_expect_tx(bar(C::kVote + turn), 4 * kSoftmaxWarps);
+          else mbar_arrive(bar(C::kVote + turn));
+        }
+        // Probabilities, bf16 pairs of neighbouring rows: eight rows o, eight keys k.
+        uint32_t w[4][4];
         float part[8];                     // this tile's sums
-        // Probabilities with the references there are, to where their rows are staged.
-        auto write_p = [&]() {
+        auto compute = [&]() {
 #pragma unroll
-          for (int o = 0; o < 4; ++o) {    // eight rows
-            uint32_t w[4];                 // eight keys each
+          for (int o = 0; o < 4; ++o)
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
               const float p0 = ex2_approx(fmaf(val(2 * o, k), c, -m[2 * o]));
               const float p1 = ex2_approx(fmaf(val(2 * o + 1, k), c, -m[2 * o + 1]));
-              w[k] = pack_bf16x2(p0, p1);
+              w[o][k] = pack_bf16x2(p0, p1);
               part[2 * o] = k == 0 ? p0 : part[2 * o] + p0;
               part[2 * o + 1] = k == 0 ? p1 : part[2 * o + 1] + p1;
             }
-            const int chunk = 4 * (quarter & 1);
-            if (home == rank) {
-              const int row = cols + 8 * o + (lane & 7);
-              const uint32_t dst = sbase + C::kPOff + rank * C::kChunk + row * 128 + (((chunk + (lane >> 3)) ^ (row & 7)) << 4);
-              if (dcheck(in_range(dst, 16, sbase + C::kPOff, sbase + C::kRingOff), args.status, 702))
-                stmatrix_x4_trans(dst, w[0], w[1], w[2], w[3]);
-            } else {
-              // Transposed in registers: lane 4 r + q has keys 2 q, 2 q + 1 of row r of each chunk; the
-              // four lanes of a row then swap words, so that lane q has all of chunk q.
+        };
+        // For the other CTA, transposed in registers: lane 4 r + q has keys 2 q, 2 q + 1 of row r of
+        // each chunk of eight keys; the four lanes of a row then swap words, so that lane q
+        // has all of chunk q.
+        auto transpose = [&]() {
+          const int q = lane & 3;
 #pragma unroll
-              for (int k = 0; k < 4; ++k) w[k] = movmatrix_trans(w[k]);
-              const int q = lane & 3;
-              uint32_t t[4];
-              // step 1, lanes two apart: chunks q & 2
-              const uint32_t a0 = __shfl_xor_sync(0xffffffffu, q & 2 ? w[0] : w[2], 2);
-              const uint32_t a1 = __shfl_xor_sync(0xffffffffu, q & 2 ? w[1] : w[3], 2);
-              const uint32_t k0 = q & 2 ? w[2] : w[0], k1 = q & 2 ? w[3] : w[1];
-              // now chunk (q & 2) + 0: words q and q ^ 2 are k0, a0; chunk + 1: k1, a1
-              const uint32_t b0 = __shfl_xor_sync(0xffffffffu, q & 1 ? k0 : k1, 1);
-              const uint32_t b1 = __shfl_xor_sync(0xffffffffu, q & 1 ? a0 : a1, 1);
-              const uint32_t m0 = q & 1 ? k1 : k0, m1 = q & 1 ? a1 : a0;
-              // chunk q: word q is m0, q ^ 2 m1, q ^ 1 b0, q ^ 3 b1
-              t[0] = q == 0 ? m0 : (q == 2 ? m1 : (q == 1 ? b0 : b1));
-              t[1] = q == 1 ? m0 : (q == 3 ? m1 : (q == 0 ? b0 : b1));
-              t[2] = q == 2 ? m0 : (q == 0 ? m1 : (q == 3 ? b0 : b1));
-              t[3] = q == 3 ? m0 : (q == 1 ? m1 : (q == 2 ? b0 : b1));
-              const int row = cols + 8 * o + (lane >> 2);
-              const uint32_t off = row * 128 + (((chunk + q) ^ (row & 7)) << 4);
-              if (dcheck(off + 16 <= static_cast<uint32_t>(C::kChunk), args.status, 703))
-                st_cluster_v4(p_dst + off, t[0], t[1], t[2], t[3]);
-            }
+          for (int o = 0; o < 4; ++o) {
+            uint32_t u[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) u[k] = movmatrix_trans(w[o][k]);
+            const uint32_t a0 = __shfl_xor_sync(0xffffffffu, q & 2 ? u[0] : u[2], 2);
+            const uint32_t a1 = __shfl_xor_sync(0xffffffffu, q & 2 ? u[1] : u[3], 2);
+            const uint32_t k0 = q & 2 ? u[2] : u[0], k1 = q & 2 ? u[3] : u[1];
+            const uint32_t b0 = __shfl_xor_sync(0xffffffffu, q & 1 ? k0 : k1, 1);
+            const uint32_t b1 = __shfl_xor_sync(0xffffffffu, q & 1 ? a0 : a1, 1);
+            const uint32_t m0 = q & 1 ? k1 : k0, m1 = q & 1 ? a1 : a0;
+            // of chunk q: word q is m0, q ^ 2 m1, q ^ 1 b0, q ^ 3 b1
+            w[o][0] = q == 0 ? m0 : (q == 2 ? m1 : (q == 1 ? b0 : b1));
+            w[o][1] = q == 1 ? m0 : (q == 3 ? m1 : (q == 0 ? b0 : b1));
+            w[o][2] = q == 2 ? m0 : (q == 0 ? m1 : (q == 3 ? b0 : b1));
+            w[o][3] = q == 3 ? m0 : (q == 1 ? m1 : (q == 2 ? b0 : b1));
           }
-          fence_proxy_async_cluster();
         };
         if (!first) {
-          if (!(ok = wait_cl(bar(C::kPvDone), (tiles - 1) & 1, wc, kWaitMmaDone))) break;   // P is free
-          write_p();
+          compute();
+          if (home != rank) transpose();
         }
-        tc_fence_before();
-        if (__any_sync(0xffffffffu, first || edge || top > kTau) && lane < 2)
-          st_cluster_u32(map_shared(smem_u32(const_cast<uint32_t*>(&misc[2 + (tiles & 1)])), lane), tiles + 1);
-        arrive_both(C::kVote);
-        if (!(ok = wait_cl(bar(C::kVote), tiles & 1, wc, kWaitPFull))) break;
-        if (misc[2 + (tiles & 1)] == tiles + 1) {
-          // ---- in both CTAs: some row's reference moves, or keys are missing
+        if (!(ok = wait_cl(bar(C::kVote + turn), (tiles >> 1) & 1, wc, kWaitPFull))) break;
+        const bool moved = misc[2 + turn] == tiles + 1 || __any_sync(0xffffffffu, peer_votes[8 * turn + (lane & 7)] != 0u);
+        // This CTA's keys' place in P is free.
+        if (!first && !(ok = wait_cl(bar(C::kPvDone + rank), (tiles - 1) & 1, wc, kWaitMmaDone))) break;
+        if (moved) {
+          // ---- in both CTAs: some row's reference may move
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             float t = top_of(i) * c;
@@ -395,6 +393,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           if (!(ok = sync())) break;
           if (!first) {
+            if (!(ok = wait_cl(bar(C::kPvDone + peer), (tiles - 1) & 1, wc, kWaitMmaDone))) break;
             tc_fence_after();
 #pragma unroll 1
             for (int p = 0; p < C::kBlocks * 4; ++p) {
@@ -416,11 +415,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             tmem_st_wait();
           }
-          write_p();
+          compute();
+          if (home != rank) transpose();
           if (edge) {
             // Slots behind the end and pages that do not exist hold anything, and zero times a
             // NaN is a NaN.
-            if (!(ok = wait_cl(bar(C::kOther + (tiles & 1)), (tiles >> 1) & 1, wc, kWaitKvFull))) break;
+            if (!(ok = wait_cl(bar(C::kOther + turn), (tiles >> 1) & 1, wc, kWaitKvFull))) break;
 #pragma unroll 1
             for (int id = tid; id < 2 * C::kBlocks * 2 * kHalfKeys * 8; id += 32 * kSoftmaxWarps) {
               const int r = id >> 3 & (kHalfKeys - 1), half = id >> 9;      // half pairs, 64 rows of 8 pieces each
@@ -431,18 +431,40 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (dcheck(in_range(dst, 16, sbase + C::kRingOff, sbase + C::kRopeOff), args.status, 704))
                 st_shared_v4(dst, 0u, 0u, 0u, 0u);
             }
-            fence_proxy_async_cluster();
+            fence_proxy_async_smem();
+            if (!(ok = sync())) break;
           }
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive_cluster(map_shared(bar(C::kAgain), 0));
+        }
+        // ---- P to where its rows are staged
+        const int chunk = 4 * (quarter & 1);
+#pragma unroll
+        for (int o = 0; o < 4; ++o) {
+          if (home == rank) {
+            const int row = cols + 8 * o + (lane & 7);
+            const uint32_t dst = sbase + C::kPOff + rank * C::kChunk + row * 128 + (((chunk + (lane >> 3)) ^ (row & 7)) << 4);
+            if (dcheck(in_range(dst, 16, sbase + C::kPOff, sbase + C::kRingOff), args.status, 702))
+              stmatrix_x4_trans(dst, w[o][0], w[o][1], w[o][2], w[o][3]);
+          } else {
+            const int row = cols + 8 * o + (lane >> 2);
+            const uint32_t off = row * 128 + (((chunk + (lane & 3)) ^ (row & 7)) << 4);
+            if (dcheck(off + 16 <= static_cast<uint32_t>(C::kChunk), args.status, 703))
+              st_async_v4(p_dst + off, w[o][0], w[o][1], w[o][2], w[o][3], map_shared(bar(C::kProb + rank), home));
+          }
+        }
+        fence_proxy_async_smem();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(bar(C::kProb + rank));
+          if (warp == 0) mbar_arrive_expect_tx(bar(C::kProb + peer), C::kChunk);   // the other's keys
         }
 #pragma unroll
         for (int i = 0; i < 8; ++i) l[i] += part[i];
       }
       if (!ok) break;
       // ---- results: this CTA's half of the columns, for all rows
-      if (!wait_cl(bar(C::kPvDone), (tiles - 1) & 1, wc, kWaitOFull)) break;
+      if (!wait_cl(bar(C::kPvDone), (tiles - 1) & 1, wc, kWaitOFull) || !wait_cl(bar(C::kPvDone + 1), (tiles - 1) & 1, wc, kWaitOFull))
+        break;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
 #pragma unroll
@@ -524,7 +546,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t lead = elect_lane();
     constexpr uint32_t idesc_s = idesc_bf16_f32(128, kRows, false, false);
     constexpr uint32_t idesc_o = idesc_bf16_f32(256, kRows, true, false);
-    uint32_t tiles = 0, pvs = 0, again = 0, q_count = 0;
+    uint32_t tiles = 0, pvs = 0, q_count = 0;
     uint32_t rs = 0, rph = 0, ks = 0, kph = 0, vs = 0;   // slots and phases, as in the kernel for 64 rows
     auto ready = [&](int b, uint32_t parity) { return bar_done_cl(bar(b), parity); };
     auto product4 = [&](uint32_t d, uint32_t a, uint32_t b, uint32_t acc) {
@@ -532,71 +554,76 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
       for (int k = 0; k < 4; ++k) mma2_lead(d, da + 2 * k, db + 2 * k, idesc_s, k > 0 ? 1u : acc, lead);
     };
-    auto values = [&](uint32_t acc) -> bool {
-      // (the vote is there)
-      if (misc[2 + (pvs & 1)] == pvs + 1 && !wait_cl(bar(C::kAgain), again++ & 1, wc, kWaitPFull)) return false;
+    // The product with CTA h's keys of tile pvs.
+    auto prob_there = [&](int h) { return ready(C::kProb + h, pvs & 1) && ready(C::kProbPeer + h, pvs & 1); };
+    auto values = [&](int h, uint32_t acc) -> bool {
+      // (P is there, part of it by the other CTA's stores)
       if (!wait_cl(bar(C::kOtherBoth + (pvs & 1)), (pvs >> 1) & 1, wc, kWaitKvFull)) return false;
+      fence_proxy_async_smem();
       tc_fence_after();
+      const uint64_t db = sdesc_sw128(sbase + C::kPOff + h * C::kChunk, 16, 1024);
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const uint64_t db = sdesc_sw128(sbase + C::kPOff + h * C::kChunk, 16, 1024);
+      for (int b = 0; b < C::kBlocks; ++b) {
+        const uint64_t da = sdesc_sw128(sbase + C::kRingOff + vs * C::kPairTile, C::kChunk, 1024);
 #pragma unroll
-        for (int b = 0; b < C::kBlocks; ++b) {
-          const uint64_t da = sdesc_sw128(sbase + C::kRingOff + vs * C::kPairTile, C::kChunk, 1024);
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            mma2_lead(tmem + C::col_o(b), da + ((k * 2048) >> 4), db + 2 * k, idesc_o, h + k > 0 ? 1u : acc, lead);
-          commit2_lead(bar(C::kEmpty + vs), lead);
-          vs = vs + 1 == C::kRing ? 0u : vs + 1;
-        }
+        for (int k = 0; k < 4; ++k)
+          mma2_lead(tmem + C::col_o(b), da + ((k * 2048) >> 4), db + 2 * k, idesc_o, k > 0 ? 1u : acc, lead);
+        commit2_lead(bar(C::kEmpty + vs), lead);
+        vs = vs + 1 == C::kRing ? 0u : vs + 1;
       }
-      commit2_lead(bar(C::kPvDone), lead);
-      ++pvs;
+      commit2_lead(bar(C::kPvDone + h), lead);
+      if (h == 1) ++pvs;
       return true;
     };
     auto run = [&](const int n) -> bool {
       if (!wait_cl(bar(C::kQFull), q_count++ & 1, wc, kWaitQFull)) return false;
       tc_fence_after();
       for (int i = 0; i <= n; ++i) {
-        bool due = i > 0;                 // values of tile i - 1
+        int due = i > 0 ? 0 : 2;          // next product with the values of tile i - 1
         if (i < n) {
-          // As in the kernel for 64 rows: scores first, but values while the scores' tile is on its way.
-          for (long long t0 = 0; !ready(C::kRopeFull + rs, rph) || !ready(C::kFull + ks, kph);) {
-            if (due && ready(C::kVote, pvs & 1)) {
-              if (!values(i > 1 ? 1u : 0u)) return false;
-              due = false;
-            }
-            const long long now = clock64();
-            if (t0 == 0) t0 = now;
-            if (now - t0 > wc.budget && *wc.abort == 0u) *wc.abort = kWaitKvFull;
-            if (!__all_sync(0xffffffffu, *wc.abort == 0u)) return false;
-          }
-          tc_fence_after();
+          // Scores of tile i, a part at a time as they come: the rotated columns, then 128 latent
+          // ones each.  While a part is not there, the values of the tile before go first
+          // where their probabilities are: only after that product are a tile's slots free.
           const uint32_t d = tmem + C::col_s(tiles & 1);
-          product4(d, sbase + C::kRopeOff + rs * C::kChunk, sbase + C::kQOff + 2 * C::kPairs * C::kChunk, 0u);
-          commit2_lead(bar(C::kRopeEmpty + rs), lead);
-          if (++rs == C::kRopes) {
-            rs = 0;
-            rph ^= 1u;
-          }
-#pragma unroll
-          for (int p = 0; p < C::kPairs; ++p) {
-            if (p > 0 && !wait_cl(bar(C::kFull + ks), kph, wc, kWaitKvFull)) return false;
-            const uint32_t k = sbase + C::kRingOff + ks * C::kPairTile, q = sbase + C::kQOff + 2 * p * C::kChunk;
-            product4(d, k, q, 1u);
-            product4(d, k + C::kChunk, q + C::kChunk, 1u);
-            if (++ks == C::kRing) {
-              ks = 0;
-              kph ^= 1u;
+#pragma unroll 1
+          for (int p = -1; p < C::kPairs; ++p) {
+            const int b = p < 0 ? C::kRopeFull + static_cast<int>(rs) : C::kFull + static_cast<int>(ks);
+            for (long long t0 = 0; !ready(b, p < 0 ? rph : kph);) {
+              if (due < 2 && prob_there(due)) {
+                if (!values(due, i > 1 || due > 0 ? 1u : 0u)) return false;
+                ++due;
+              }
+              const long long now = clock64();
+              if (t0 == 0) t0 = now;
+              if (now - t0 > wc.budget && *wc.abort == 0u) *wc.abort = kWaitKvFull;
+              if (!__all_sync(0xffffffffu, *wc.abort == 0u)) return false;
+            }
+            tc_fence_after();
+            if (p < 0) {
+              product4(d, sbase + C::kRopeOff + rs * C::kChunk, sbase + C::kQOff + 2 * C::kPairs * C::kChunk, 0u);
+              commit2_lead(bar(C::kRopeEmpty + rs), lead);
+              if (++rs == C::kRopes) {
+                rs = 0;
+                rph ^= 1u;
+              }
+            } else {
+              const uint32_t k = sbase + C::kRingOff + ks * C::kPairTile, q = sbase + C::kQOff + 2 * p * C::kChunk;
+              product4(d, k, q, 1u);
+              product4(d, k + C::kChunk, q + C::kChunk, 1u);
+              if (++ks == C::kRing) {
+                ks = 0;
+                kph ^= 1u;
+              }
             }
           }
           commit2_lead(bar(C::kSFull + (tiles & 1)), lead);
           if (i + 1 == n) commit2_lead(bar(C::kQEmpty), lead);
           ++tiles;
         }
-        if (due) {
-          if (!wait_cl(bar(C::kVote), pvs & 1, wc, kWaitPFull)) return false;
-          if (!values(i > 1 ? 1u : 0u)) return false;
+        for (; due < 2; ++due) {
+          if (!wait_cl(bar(C::kProb + due), pvs & 1, wc, kWaitPFull) ||
+              !wait_cl(bar(C::kProbPeer + due), pvs & 1, wc, kWaitPFull) || !values(due, i > 1 || due > 0 ? 1u : 0u))
+            return false;
         }
       }
       return true;
@@ -607,7 +634,20 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool on = uniform(first_row(s) < rows_of(s) ? 1 : 0) != 0;
       done_seg(si);
       if (flags & Seg::kLast) break;
-      if (leader && on && !run(n)) break;
+      if (!on) continue;
+      if (leader) {
+        if (!run(n)) break;
+      } else {
+        // This CTA's P, told to the leader.
+        bool ok = true;
+        for (int i = 0; i < 2 * n && (ok = wait_cl(bar(C::kProb + (i & 1)), pvs & 1, wc, kWaitPFull)); ++i) {
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster_relaxed(map_shared(bar(C::kProbPeer + (i & 1)), 0));
+          pvs += i & 1;
+        }
+        if (!ok) break;
+      }
     }
     // No product may still be running when either CTA's memory goes.
     if (leader) commit2_lead(bar(C::kMmaDone), lead);
@@ -680,8 +720,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (p == 0) {
               if (lane == 0) {
-                misc[4 + tiles % kValid] = mask;
-                mbar_arrive(bar(C::kMask + tiles % kValid));
+                misc[4 + tiles % C::kValid] = mask;
+                mbar_arrive(bar(C::kMask + tiles % C::kValid));
               }
               __syncwarp();
             }
@@ -719,7 +759,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             ok = false;
             break;
           }
-          if (lane == 0) mbar_arrive_cluster(map_shared(bar(C::kOtherBoth + (tiles & 1)), 0));
+          if (lane == 0) mbar_arrive_cluster_relaxed(map_shared(bar(C::kOtherBoth + (tiles & 1)), 0));
           __syncwarp();
         }
       }
@@ -727,7 +767,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
   } else if (warp == kWalkWarp) {
     // ================================================================ schedule
-    Walker<kKeys> walk(args, group_rows, static_cast<int>(misc[8]), static_cast<int>(misc[9]), sh.j1 - sh.j0);
+    const uint32_t* place = reinterpret_cast<const uint32_t*>(smem + C::kSegOff);
+    Walker<kKeys> walk(args, group_rows, static_cast<int>(place[0]), static_cast<int>(place[1]), sh.j1 - sh.j0);
+    __syncwarp();
     Seg s{};
     bool any = false;
     for (uint32_t i = 0;; ++i) {
@@ -754,7 +796,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // What is to be joined: the unit that this share starts and others go on with
       // (its last one).
       const bool shared_unit = any && (s.flags & (Seg::kStarts | Seg::kEnds)) == Seg::kStarts;
-      args.rec[share] = shared_unit ? make_int4(s.r0, s.n, s.rg, cta_of(sh.W, sh.busy, sh.j1 - (s.e - s.a) + s.nt - 1))
+      args.rec[share] = shared_unit ? make_int4(s.r0, s.n, s.rg, cta_of(sh.W, sh.busy, sh.j1 - (s.e - s.a) + walk.nt - 1))
                                     : make_int4(0, 0, 0, 0);
     }
     __syncwarp();
