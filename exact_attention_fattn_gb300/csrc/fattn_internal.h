@@ -245,9 +245,8 @@ struct LatentAttnArgs {
 constexpr int kLatentKeys = 64;      // keys of a tile
 constexpr int kLatentUnitCost = 2;   // tiles that a unit counts beyond its own
 
-// Rows of a block for calls of `rows` rows an average sequence; 128 are a pair of CTAs'.
-constexpr int latent_rows(long long rows) { return rows <= 16 ? 16 : (rows <= 32 ? 32 : (rows <= 64 ? 64 : 128)); }
-constexpr int kLatentPairRows = 128;
+constexpr int kLatentPairRank = 512;   // pairs of CTAs: the latent width that they are for,
+constexpr int kLatentPairRows = 128;   // rows of a unit and keys of a tile
 constexpr int kLatentPairKeys = 128;
 
 // rows: 16, 32 or 64 rows a unit; rank: 256 or 512.  tk: view {rank + 64, page, pages} of the
@@ -256,11 +255,11 @@ constexpr int kLatentPairKeys = 128;
 cudaError_t launch_latent_attn(int rows, int rank, const CUtensorMap& tk, const CUtensorMap& tq,
                                const LatentAttnArgs& a, cudaStream_t stream);
 
-// 128 rows a unit, on pairs of CTAs; tq with boxes of 64 rows.
-cudaError_t launch_latent_pair(int rank, const CUtensorMap& tk, const CUtensorMap& tq, const LatentAttnArgs& a,
+// 128 rows a unit, on pairs of CTAs, rank 512; tq with boxes of 64 rows.
+cudaError_t launch_latent_pair(const CUtensorMap& tk, const CUtensorMap& tq, const LatentAttnArgs& a,
                                cudaStream_t stream);
-// Joins the units of `rows` rows a block that shares of either kernel split.
-cudaError_t launch_latent_join(int rows, int rank, const LatentAttnArgs& a, cudaStream_t stream);
+// Joins the units that their shares split (part of launch_latent_pair).
+cudaError_t launch_latent_join_pairs(const LatentAttnArgs& a, cudaStream_t stream);
 
 // Tensor map of bf16 data: 2 to 5 dimensions, strides of all but the first in
 // elements, 128-byte swizzle (a box has 64 of the first).  Returns a fattn_status.

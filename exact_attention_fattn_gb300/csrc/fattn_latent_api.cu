@@ -71,13 +71,29 @@ CacheSeqs seqs_of(const int* page_table, const int* q_start, const int* kv_len, 
 // long as their 64 keys or 128 columns do, so a block has no more rows than it
 // needs), and the blocks that work side by side: as few groups as blocks of kMaxSpan
 // allow, and no idle block in the average sequence.
+//
+// Blocks of 128 rows on pairs of CTAs are for large calls of rank 512 (`reach`: keys
+// that a sequence's table has room for; what they really are is on the device), a call
+// in us on pairs and on single CTAs, 128 heads, one token a sequence:
+//   keys per pair    64 of 8000: 199 / 227   48 of 4000: 88 / 92   16 of 8000: 62 / 64
+//     below 1536:    24 of 4000: 54 / 55   96 of 1000: 68 / 66   40 of 2000: 54 / 53
+//                    16 of 1000: 28 / 24   48 of 300: 34 / 30    4 of 2000: 23 / 21
+//   rows not a multiple of 128 (32 sequences of 4000 keys, 64 heads, so many tokens):
+//     3: 100 / 91   5: 139 / 137   7: 171 / 183   9: 204 / 246
+//   rank 256, whose products leave the exchange between the two CTAs no room:
+//     32 of 8000: 67 / 65   16 of 8000: 44 / 39   16 of 1000: 22 / 17
+// Both need the same workspace, so that its size does not depend on the reach.
 struct Layout {
   int rows, span;
 };
-Layout layout_of(int T, int B, int Hq) {
-  const long long all = (static_cast<long long>(T) * Hq + B - 1) / B;
+Layout layout_of(int T, int B, int Hq, int rank, long long reach) {
+  const long long all = (static_cast<long long>(T) * Hq + B - 1) / B, halves = (all + 63) / 64;
+  const long long pairs = (halves + 1) / 2;                       // blocks of 128 rows
   Layout l;
-  l.rows = latent_rows(all);
+  l.rows = all <= 16 ? 16 : (all <= 32 ? 32 : 64);
+  if (rank == kLatentPairRank && (halves % 2 == 0 || halves >= 7) &&
+      static_cast<double>(B) * static_cast<double>(pairs) * static_cast<double>(reach) >= 1536. * (kSms / 2))
+    l.rows = kLatentPairRows;
   const long long blocks = (all + l.rows - 1) / l.rows, groups = (blocks + kMaxSpan - 1) / kMaxSpan;
   l.span = static_cast<int>((blocks + groups - 1) / groups);
   return l;
@@ -86,9 +102,10 @@ Layout layout_of(int T, int B, int Hq) {
 struct Workspace {
   size_t ml_off, rec_off, total;
 };
-Workspace workspace_of(const Layout& l, int rank) {
+Workspace workspace_of(int rows_a_block, int rank) {
+  static_assert(kSms % 2 == 0 && kLatentPairRows == 128, "pairs have the room of two blocks of 64 rows");
   Workspace w;
-  const size_t rows = 2ull * (l.rows == kLatentPairRows ? kSms / 2 : kSms) * l.rows;
+  const size_t rows = 2ull * kSms * (rows_a_block == kLatentPairRows ? 64 : rows_a_block);
   w.ml_off = align256(rows * rank * sizeof(float));
   w.rec_off = w.ml_off + align256(rows * sizeof(float2));
   w.total = w.rec_off + align256(kSms * sizeof(int4));
@@ -147,7 +164,7 @@ int fattn_latent_append(const fattn_latent_cache* cache, const void* latent, lon
 
 size_t fattn_latent_fwd_workspace_bytes(int T, int B, int Hq, int rank) {
   if (T <= 0 || B <= 0 || B > kMaxSeqs || (rank != 256 && rank != 512) || check_heads(T, Hq) != FATTN_OK) return 0;
-  return workspace_of(layout_of(T, B, Hq), rank).total;
+  return workspace_of(layout_of(T, B, Hq, rank, 0).rows, rank).total;
 }
 
 int fattn_latent_fwd(const fattn_latent_cache* cache, const void* q, void* o, float* lse,
@@ -162,8 +179,8 @@ int fattn_latent_fwd(const fattn_latent_cache* cache, const void* q, void* o, fl
   if (!q || !aligned(q, 16) || !o || !aligned(o, 16) || !lse || !aligned(lse, 4)) return FATTN_ERR_INVALID_ARG;
   const float scale_log2 = scale * 1.4426950408889634f;
   if (!isfinite(scale_log2) || !(scale > 0.f)) return FATTN_ERR_INVALID_ARG;
-  const Layout l = layout_of(T, B, Hq);
-  const Workspace w = workspace_of(l, cache->rank);
+  const Layout l = layout_of(T, B, Hq, cache->rank, static_cast<long long>(max_pages) * cache->page);
+  const Workspace w = workspace_of(l.rows, cache->rank);
   if (!workspace || !aligned(workspace, 256) || workspace_bytes < w.total) return FATTN_ERR_INVALID_ARG;
   LatentAttnArgs a{};
   if ((rc = call_setup(&a.status, &a.wait_budget)) != FATTN_OK) return rc;
@@ -205,7 +222,7 @@ int fattn_latent_fwd(const fattn_latent_cache* cache, const void* q, void* o, fl
       (rc = make_map_bf16(&tq, q, 3, q_extents, q_strides, q_box)) != FATTN_OK)
     return rc;
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  const cudaError_t e = on_pairs ? launch_latent_pair(cache->rank, tk, tq, a, st)
+  const cudaError_t e = on_pairs ? launch_latent_pair(tk, tq, a, st)
                                  : launch_latent_attn(l.rows, cache->rank, tk, tq, a, st);
   return e == cudaSuccess ? FATTN_OK : FATTN_ERR_CUDA;
 }

@@ -717,7 +717,7 @@ __global__ void __launch_bounds__(kJoinGroups * R / 4) join_kernel(const LatentA
         for (int k = 0; k < 4; ++k) {
           const int t = min(t0 + k * step, rec.w);
           const long long at = (2ll * (t * a.span + row / N) + (t == share ? 1 : 0)) * N + row % N;
-          if (!dcheck(inside(at, 1, 2ll * kSms * N), a.status, 696)) continue;
+          if (!dcheck(inside(at, 1, 2ll * (N == kLatentPairRows ? kSms / 2 : kSms) * N), a.status, 696)) continue;
           const float2 ml = a.part_ml[at];
           x[k] = Part{ml.x, ml.y, reinterpret_cast<const float4*>(a.part_o + at * R)[q4]};
         }
@@ -752,13 +752,6 @@ cudaError_t launch_join_t(const LatentAttnArgs& a, cudaStream_t stream) {
   return launch_child(join_kernel<N, R>, rows < most ? rows : most, kJoinGroups * R / 4, 0, stream, a);
 }
 
-template <int R>
-cudaError_t launch_join_rank(int rows, const LatentAttnArgs& a, cudaStream_t stream) {
-  if (rows == 16) return launch_join_t<16, R>(a, stream);
-  if (rows == 32) return launch_join_t<32, R>(a, stream);
-  return rows == 64 ? launch_join_t<64, R>(a, stream) : launch_join_t<128, R>(a, stream);
-}
-
 template <int N, int R>
 cudaError_t launch_t(const CUtensorMap& tk, const CUtensorMap& tq, const LatentAttnArgs& a, cudaStream_t stream) {
   auto kern = latent_kernel<N, R>;
@@ -768,13 +761,13 @@ cudaError_t launch_t(const CUtensorMap& tk, const CUtensorMap& tq, const LatentA
   kern<<<a.span * a.shares, Cfg<N, R>::kThreads, Cfg<N, R>::kSmem, stream>>>(tk, tq, a);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   if (a.shares == 1) return cudaSuccess;   // nothing is shared
-  return launch_latent_join(N, R, a, stream);
+  return launch_join_t<N, R>(a, stream);
 }
 
 }  // namespace
 
-cudaError_t launch_latent_join(int rows, int rank, const LatentAttnArgs& a, cudaStream_t stream) {
-  return rank == 256 ? launch_join_rank<256>(rows, a, stream) : launch_join_rank<512>(rows, a, stream);
+cudaError_t launch_latent_join_pairs(const LatentAttnArgs& a, cudaStream_t stream) {
+  return launch_join_t<kLatentPairRows, kLatentPairRank>(a, stream);
 }
 
 cudaError_t launch_latent_attn(int rows, int rank, const CUtensorMap& tk, const CUtensorMap& tq,

@@ -38,9 +38,10 @@ namespace fattn {
 
 namespace {
 
-constexpr int kKeys = 128;            // of a tile, half of them a CTA's
+constexpr int kRank = kLatentPairRank;
+constexpr int kKeys = kLatentPairKeys;   // of a tile, half of them a CTA's
 constexpr int kHalfKeys = 64;
-constexpr int kRows = 128;
+constexpr int kRows = kLatentPairRows;
 constexpr int kThreads = 384;
 constexpr int kSoftmaxWarps = 8;
 constexpr int kMmaWarp = 8;
@@ -50,10 +51,9 @@ constexpr int kWalkWarp = 11;
 constexpr int kSegs = 2;
 constexpr int kSegReaders = kSoftmaxWarps + 3;
 
-template <int R>
-struct Cfg {
-  static constexpr int kChunks = R / 64 + 1;
-  static constexpr int kPairs = R / 128;             // 128-column parts of a cached row
+struct C {
+  static constexpr int kChunks = kRank / 64 + 1;
+  static constexpr int kPairs = kRank / 128;         // 128-column parts of a cached row
   static constexpr int kBlocks = kPairs / 2;         // of them a CTA's own
   static constexpr int kChunk = kHalfKeys * 128;     // 64 rows, 64 columns
   static constexpr int kQOff = 0;
@@ -62,9 +62,8 @@ struct Cfg {
   static constexpr int kRingOff = kPOff + 2 * kChunk;
   static constexpr int kPairTile = 2 * kChunk;
   static constexpr int kRing = 8;                    // pairs
-  static constexpr int kRopes = R == 512 ? 1 : 2;
   static constexpr int kRopeOff = kRingOff + kRing * kPairTile;
-  static constexpr int kBarOff = kRopeOff + kRopes * kChunk;
+  static constexpr int kBarOff = kRopeOff + kChunk;
   static_assert(kRing >= 2 * kPairs && kRing % kPairs == 0, "ring");
   static constexpr int kValid = kRing / kPairs;      // tiles whose masks are kept
   // barriers; those with (l) count for both CTAs in the leader's shared memory
@@ -72,8 +71,8 @@ struct Cfg {
     kFull = 0,                    // (l) pair slots
     kEmpty = kFull + kRing,
     kRopeFull = kEmpty + kRing,   // (l)
-    kRopeEmpty = kRopeFull + kRopes,
-    kOther = kRopeEmpty + kRopes, // the other CTA's keys, in this CTA
+    kRopeEmpty,
+    kOther,                       // the other CTA's keys, in this CTA
     kOtherBoth = kOther + 2,      // (l) in both
     kQFull = kOtherBoth + 2,      // (l)
     kQEmpty,
@@ -163,11 +162,9 @@ __device__ __forceinline__ bool wait_cl(uint32_t bar, uint32_t parity, const Wai
   return __all_sync(0xffffffffu, ok);
 }
 
-template <int R>
 __global__ void __launch_bounds__(kThreads, 1)
     pair_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_q,
                 const __grid_constant__ LatentAttnArgs args) {
-  using C = Cfg<R>;
   extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t sbase = smem_u32(smem);
   auto bar = [&](int i) { return sbase + C::kBarOff + 8u * i; };
@@ -490,7 +487,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         alphas[tid] = lt == 0.f ? 0.f : 1.f / lt;
       }
       if (!sync()) break;
-      const int col_base = R / 2 * static_cast<int>(rank) + 32 * quarter;     // of O
+      const int col_base = kRank / 2 * static_cast<int>(rank) + 32 * quarter;     // of O
       if (whole) {
         // As in the kernel for 64 rows, through P's place: the other CTA writes to it again only
         // after the next unit's first exchange.
@@ -523,7 +520,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint4 w = ld_shared_v4(stage + row * 64 + ((chunk ^ (row >> 1 & 3)) << 4));
             if (r0 + row < live &&
                 dcheck(inside(out0 + r0 + row, 1, static_cast<long long>(args.s.T) * args.Hq), args.status, 705))
-              *reinterpret_cast<uint4*>(args.o + (out0 + r0 + row) * R + col_base + 128 * (t >> 1) + 8 * chunk) = w;
+              *reinterpret_cast<uint4*>(args.o + (out0 + r0 + row) * kRank + col_base + 128 * (t >> 1) + 8 * chunk) = w;
           }
         }
       } else {
@@ -533,11 +530,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (r0 >= live) continue;
           uint32_t o[16];
           tmem_ld16(tmem + lane_off + C::col_o(p >> 2) + r0, o);
-          float* to = args.part_o + (slot * kRows + r0) * R + col_base + 128 * (p >> 2) + lane;
+          float* to = args.part_o + (slot * kRows + r0) * kRank + col_base + 128 * (p >> 2) + lane;
           tmem_ld_wait(o);
 #pragma unroll
           for (int z = 0; z < 16; ++z)
-            if (r0 + z < live && dcheck(slot < 2ll * kSms, args.status, 706)) to[z * R] = __uint_as_float(o[z]);
+            if (r0 + z < live && dcheck(slot < 2ll * (kSms / 2), args.status, 706)) to[z * kRank] = __uint_as_float(o[z]);
         }
       }
     }
@@ -547,7 +544,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr uint32_t idesc_s = idesc_bf16_f32(128, kRows, false, false);
     constexpr uint32_t idesc_o = idesc_bf16_f32(256, kRows, true, false);
     uint32_t tiles = 0, pvs = 0, q_count = 0;
-    uint32_t rs = 0, rph = 0, ks = 0, kph = 0, vs = 0;   // slots and phases, as in the kernel for 64 rows
+    uint32_t ks = 0, kph = 0, vs = 0;   // slots and phases, as in the kernel for 64 rows
     auto ready = [&](int b, uint32_t parity) { return bar_done_cl(bar(b), parity); };
     auto product4 = [&](uint32_t d, uint32_t a, uint32_t b, uint32_t acc) {
       const uint64_t da = sdesc_sw128(a, 16, 1024), db = sdesc_sw128(b, 16, 1024);
@@ -587,8 +584,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint32_t d = tmem + C::col_s(tiles & 1);
 #pragma unroll 1
           for (int p = -1; p < C::kPairs; ++p) {
-            const int b = p < 0 ? C::kRopeFull + static_cast<int>(rs) : C::kFull + static_cast<int>(ks);
-            for (long long t0 = 0; !ready(b, p < 0 ? rph : kph);) {
+            const int b = p < 0 ? C::kRopeFull : C::kFull + static_cast<int>(ks);
+            for (long long t0 = 0; !ready(b, p < 0 ? tiles & 1 : kph);) {
               if (due < 2 && prob_there(due)) {
                 if (!values(due, i > 1 || due > 0 ? 1u : 0u)) return false;
                 ++due;
@@ -600,12 +597,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             tc_fence_after();
             if (p < 0) {
-              product4(d, sbase + C::kRopeOff + rs * C::kChunk, sbase + C::kQOff + 2 * C::kPairs * C::kChunk, 0u);
-              commit2_lead(bar(C::kRopeEmpty + rs), lead);
-              if (++rs == C::kRopes) {
-                rs = 0;
-                rph ^= 1u;
-              }
+              product4(d, sbase + C::kRopeOff, sbase + C::kQOff + 2 * C::kPairs * C::kChunk, 0u);
+              commit2_lead(bar(C::kRopeEmpty), lead);
             } else {
               const uint32_t k = sbase + C::kRingOff + ks * C::kPairTile, q = sbase + C::kQOff + 2 * p * C::kChunk;
               product4(d, k, q, 1u);
@@ -660,7 +653,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // same bytes; its scores are masked and its values zeroed.
     const int page = 1 << args.page_shift, box = min(page, kHalfKeys), boxes = kHalfKeys / box;
     const uint32_t half = warp == kLoadWarp ? rank : peer;
-    uint32_t tiles = 0, q_count = 0, rs = 0, ropes = 0, ps = 0, eph = 0, pairs = 0;
+    uint32_t tiles = 0, q_count = 0, ps = 0, eph = 0, pairs = 0;
     bool ok = true;
     for (uint32_t si = 0; ok && wait_seg(si); ++si) {
       const Seg s = seg_at(si);
@@ -704,14 +697,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             tma2_load_3d_w(dst, &tm_k, b, col, row, pid0);
             if (boxes == 2) tma2_load_3d_w(dst + 4096, &tm_k, b, col, row, pid1);
           };
-          if (ropes >= C::kRopes && !wait_cl(bar(C::kRopeEmpty + rs), (ropes / C::kRopes - 1) & 1, wc, kWaitKvEmpty)) {
+          if (tiles > 0 && !wait_cl(bar(C::kRopeEmpty), (tiles - 1) & 1, wc, kWaitKvEmpty)) {
             ok = false;
             break;
           }
-          if (leader) mbar_arrive_expect_tx_w(bar(C::kRopeFull + rs), 2 * C::kChunk);
-          load64(sbase + C::kRopeOff + rs * C::kChunk, map_shared(bar(C::kRopeFull + rs), 0), R);
-          ++ropes;
-          rs = rs + 1 == C::kRopes ? 0u : rs + 1;
+          if (leader) mbar_arrive_expect_tx_w(bar(C::kRopeFull), 2 * C::kChunk);
+          load64(sbase + C::kRopeOff, map_shared(bar(C::kRopeFull), 0), kRank);
 #pragma unroll
           for (int p = 0; p < C::kPairs; ++p) {
             if (pairs >= C::kRing && !wait_cl(bar(C::kEmpty + ps), eph ^ 1u, wc, kWaitKvEmpty)) {
@@ -751,7 +742,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int i = 0; i < 2 * C::kBlocks; ++i) {
             const uint32_t slot = (tiles * C::kPairs + half * C::kBlocks + (i >> 1)) % C::kRing;
             const uint32_t dst = sbase + C::kRingOff + slot * C::kPairTile + (i & 1) * C::kChunk;
-            const int col = R / 2 * static_cast<int>(rank) + 64 * i;
+            const int col = kRank / 2 * static_cast<int>(rank) + 64 * i;
             tma_load_3d_w(dst, &tm_k, b, col, row, pid0);
             if (boxes == 2) tma_load_3d_w(dst + 4096, &tm_k, b, col, row, pid1);
           }
@@ -819,11 +810,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-template <int R>
-cudaError_t launch_t(const CUtensorMap& tk, const CUtensorMap& tq, const LatentAttnArgs& a, cudaStream_t stream) {
-  auto kern = pair_kernel<R>;
+}  // namespace
+
+cudaError_t launch_latent_pair(const CUtensorMap& tk, const CUtensorMap& tq, const LatentAttnArgs& a, cudaStream_t stream) {
+  auto kern = pair_kernel;
   static SmemLimit limit;
-  cudaError_t e = limit.raise(reinterpret_cast<const void*>(kern), Cfg<R>::kSmem);
+  cudaError_t e = limit.raise(reinterpret_cast<const void*>(kern), C::kSmem);
   if (e != cudaSuccess) return e;
   cudaLaunchAttribute attr{};
   attr.id = cudaLaunchAttributeClusterDimension;
@@ -833,20 +825,13 @@ cudaError_t launch_t(const CUtensorMap& tk, const CUtensorMap& tq, const LatentA
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = 2 * a.span * a.shares;
   cfg.blockDim = kThreads;
-  cfg.dynamicSmemBytes = Cfg<R>::kSmem;
+  cfg.dynamicSmemBytes = C::kSmem;
   cfg.stream = stream;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
   if ((e = cudaLaunchKernelEx(&cfg, kern, tk, tq, a)) != cudaSuccess) return e;
   if (a.shares == 1) return cudaSuccess;   // nothing is shared
-  return launch_latent_join(kRows, R, a, stream);
-}
-
-}  // namespace
-
-cudaError_t launch_latent_pair(int rank, const CUtensorMap& tk, const CUtensorMap& tq, const LatentAttnArgs& a,
-                               cudaStream_t stream) {
-  return rank == 256 ? launch_t<256>(tk, tq, a, stream) : launch_t<512>(tk, tq, a, stream);
+  return launch_latent_join_pairs(a, stream);
 }
 
 }  // namespace fattn

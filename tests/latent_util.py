@@ -1,6 +1,8 @@
 """Seeded ragged batches over a paged latent cache, and the error bounds of the
 attention over it, shared by the latent cache's tests."""
 
+import copy
+
 import numpy as np
 import torch
 
@@ -47,6 +49,17 @@ class LatentBatch:
         self.latent = to_bf16(r.standard_normal((self.T, rank)))
         self.k_rope = to_bf16(r.standard_normal((self.T, ROPE)))
         self.q_rope = to_bf16(r.standard_normal((self.T, heads, ROPE)))
+
+    def tables(self):
+        """This batch and, with more than 64 rows a sequence, itself with tables that
+        have room for many more pages: that decides which kernel works on them."""
+        yield self
+        if self.rank == 512 and self.T * self.heads > 64 * len(self.lens):
+            b = copy.copy(self)
+            b.max_pages = self.max_pages + 120000 // self.page
+            b.table = np.full((len(self.lens), b.max_pages), 1 << 30, dtype=np.int32)
+            b.table[:, :self.max_pages] = self.table
+            yield b
 
     def device(self, gap=0):
         """(cache, page_table, q_start, kv_len) on the GPU; gap: elements left

@@ -13,7 +13,7 @@ def test_every_kernel_has_range_checks():
     sources = [s for s in build.SOURCES if s.startswith(("fattn_latent_", "fattn_pages", "fattn_rope"))]
     texts = {s: open(os.path.join(build.CSRC, s)).read() for s in sources}
     with_kernels = [s for s in sources if "__global__" in texts[s]]
-    assert len(with_kernels) == 4
+    assert len(with_kernels) == 5
     for s in with_kernels:
         calls = re.findall(r"dcheck\(.*?, (?:a|args|t)\.status,\s*(\d+)\)", texts[s], flags=re.S)
         assert calls, s

@@ -71,7 +71,7 @@ def test_rope(interleaved):
 
 
 def test_captured_step():
-    b = LatentBatch(440, [900, 300], [2, 1], 40, 512, 64)
+    *_, b = LatentBatch(440, [900, 300], [2, 1], 100, 512, 64).tables()
     c, *where = b.device()
     q = b.rows(b.q)
     want = F.fattn_latent_fwd(q, c, *where, scale=0.1)

@@ -34,11 +34,12 @@ def run(b, causal=True, gap=0, scale=0.07, q=None, **kw):
 
 
 def check(b, causal=True, scale=0.07, **kw):
-    o, l = run(b, causal, scale=scale, **kw)
     want = C.attend(b.q, b.data, b.rank, b.table, b.q_start, b.kv_len, causal, scale)
-    check_latent(o, l, want, b.rank + ROPE)
     behind = int(b.q_start[-1])
-    assert (o[behind:] == 7.0).all() and (l[behind:] == 7.0).all()   # padding rows stay as they were
+    for x in b.tables():
+        o, l = run(x, causal, scale=scale, **kw)
+        check_latent(o, l, want, b.rank + ROPE)
+        assert (o[behind:] == 7.0).all() and (l[behind:] == 7.0).all()   # padding rows stay as they were
     return o, l, want
 
 
@@ -86,8 +87,8 @@ def test_every_key_counts_once():
             (7, 256, 128, [3000, 130, 128, 127], [40, 130, 1, 9]), (64, 256, 64, [100] * 200, [1] * 200)]:
         b = LatentBatch(int(r.integers(1 << 30)), lens, news, heads, rank, page, pad_rows=1, whole=True)
         b.q[:] = 0.0
-        for causal in (True, False):
-            o, l = run(b, causal)
+        for causal, x in ((c, x) for c in (True, False) for x in b.tables()):
+            o, l = run(x, causal)
             for s, (t, n) in enumerate(zip(lens, news)):
                 v = C.tokens(b.data, b.table[s], t)[:, :rank]
                 for i in range(n):
@@ -112,9 +113,10 @@ def test_one_key_takes_all(heads):
         b2 = LatentBatch(9, lens, [1], heads, 512, 64)
         b2.data, b2.q = data, b.q * 0.0
         b2.q[..., -1] = 64.0
-        o, l = run(b2, scale=0.1)
-        assert np.array_equal(o[0], np.broadcast_to(data[b.table[0, at // 64], at % 64, :512], o[0].shape))
-        assert (np.abs(l - 409.6) <= 409.6 * 2.0 ** -21).all()
+        for x in b2.tables():
+            o, l = run(x, scale=0.1)
+            assert np.array_equal(o[0], np.broadcast_to(data[b.table[0, at // 64], at % 64, :512], o[0].shape))
+            assert (np.abs(l - 409.6) <= 409.6 * 2.0 ** -21).all()
 
 
 @pytest.mark.parametrize("scale_q", [20.0, 0.01])
@@ -124,8 +126,9 @@ def test_large_and_small_scores(scale_q, heads):
     check(LatentBatch(21, [2000, 100], [1, 3], heads, 512, 64, scale_q=scale_q))
 
 
-def test_rising_scores_move_the_reference_in_every_tile():
-    b = LatentBatch(22, [64 * 12], [1], 20, 256, 64)
+@pytest.mark.parametrize("heads,rank", [(20, 256), (128, 512)])
+def test_rising_scores_move_the_reference_in_every_tile(heads, rank):
+    b = LatentBatch(22, [64 * 12], [1], heads, rank, 64)
     for i in range(64 * 12):
         b.data[b.table[0, i // 64], i % 64, -1] = i // 4      # whole numbers below 256: bf16 has them
     b.q[..., -1] = 8.0
@@ -158,21 +161,23 @@ def test_gaps_between_pages_and_wide_tables():
 def test_pages_that_do_not_exist():
     """Tokens of missing pages count as absent and are reported; also where a row
     then sees nothing."""
-    for page in (32, 64, 128):
-        b = LatentBatch(34, [700, 90, 300, 20], [1, 1, 2, 1], 16, 512, page)
+    for page, heads in ((32, 16), (64, 16), (128, 16), (32, 128), (128, 128)):
+        b = LatentBatch(34, [700, 90, 300, 20], [1, 1, 2, 1], heads, 512, page)
         b.table[0, 1], b.table[2, 0], b.table[3, 0] = b.pages, -3, 1 << 30
-        c, *where = b.device()
-        o, l = F.fattn_latent_fwd(b.rows(b.q), c, *where, scale=0.07)
-        assert F.fattn_check_status() == _lib.FATTN_ERR_BAD_INDEX
         want = C.attend(b.q, b.data, b.rank, b.table, b.q_start, b.kv_len, True, 0.07)
-        check_latent(*arrays(o, l), want, b.rank + ROPE)
+        for x in b.tables():
+            c, *where = x.device()
+            o, l = F.fattn_latent_fwd(b.rows(b.q), c, *where, scale=0.07)
+            assert F.fattn_check_status() == _lib.FATTN_ERR_BAD_INDEX
+            check_latent(*arrays(o, l), want, b.rank + ROPE)
         assert np.isneginf(want[1][-1]).all()
     ok()
 
 
 @pytest.mark.parametrize("what", ["longer than its table", "negative length", "q_start past the rows", "q_start back"])
-def test_senseless_sequences(what):
-    b = LatentBatch(35, [60, 90, 40], [5, 20, 3], 20, 256, 32)
+@pytest.mark.parametrize("rank", [256, 512])
+def test_senseless_sequences(what, rank):
+    *_, b = LatentBatch(35, [60, 90, 40], [5, 20, 3], 20, rank, 32).tables()
     c, table, qs, kl = b.device()
     want = F.fattn_latent_fwd(b.rows(b.q), c, table, qs, kl, scale=0.07)
     ok()
@@ -192,12 +197,12 @@ def test_senseless_sequences(what):
     ok()
 
 
-@pytest.mark.parametrize("heads,news", [(3, 1), (3, 3), (40, 2), (128, 1)])
+@pytest.mark.parametrize("heads,news,rank", [(3, 1, 256), (3, 3, 256), (40, 2, 256), (128, 1, 256), (128, 1, 512), (128, 3, 512)])
 @pytest.mark.parametrize("bad", [np.inf, -np.inf, np.nan])
-def test_infinite_queries(heads, news, bad):
+def test_infinite_queries(heads, news, rank, bad):
     """A query with an infinity has infinite scores and so a NaN row, also where all of
     them are -inf; it is no row that sees nothing.  Other rows and heads stay."""
-    b = LatentBatch(36, [150, 70], [news, news], heads, 256, 32)
+    *_, b = LatentBatch(36, [150, 70], [news, news], heads, rank, 32).tables()
     b.data[..., 9] = np.abs(b.data[..., 9]) + 0.5       # one sign: all scores are inf, or all -inf
     c, *where = b.device()
     o0, l0 = F.fattn_latent_fwd(b.rows(b.q), c, *where, scale=0.07)
@@ -222,8 +227,9 @@ def test_infinite_query_over_many_ctas():
     assert np.isnan(l[0, 3]) and np.isnan(o[0, 3]).all() and np.isfinite(np.delete(l[0], 3)).all()
 
 
-def test_same_bits_every_time_and_in_any_company():
-    b = LatentBatch(38, [5000, 130, 777], [1, 2, 1], 128, 512, 64)
+@pytest.mark.parametrize("kernel", [0, 1])
+def test_same_bits_every_time_and_in_any_company(kernel):
+    b = list(LatentBatch(38, [5000, 130, 777], [1, 2, 1], 128, 512, 64).tables())[kernel]
     c, *where = b.device()
     q = b.rows(b.q)
     first = F.fattn_latent_fwd(q, c, *where, scale=0.07)
@@ -252,6 +258,19 @@ def test_offsets_past_32_bits():
     F.fattn_latent_append(lat, key, F.LatentCache(data, 512), *rest)
     ok()
     assert torch.equal(data[int(table[0, 4]), 299 % 64, :512], lat[0])
+
+
+def test_offsets_past_32_bits_on_pairs():
+    pages, page = 62000, 64
+    data = torch.empty((pages, page, 576), dtype=torch.bfloat16, device="cuda")
+    *_, b = LatentBatch(44, [300, 70], [1, 2], 128, 512, page, spare=0).tables()
+    ids = np.array([61999, 3, 60000, 30000, 58255, 61000, 59000])
+    data[torch.from_numpy(ids[:b.pages]).cuda()] = torch.from_numpy(b.data).to(torch.bfloat16).cuda()
+    table = np.where(b.table < b.pages, ids[np.minimum(b.table, b.pages - 1)], b.table).astype(np.int32)
+    rest = [torch.from_numpy(x).cuda() for x in (table, b.q_start, b.kv_len)]
+    o, l = F.fattn_latent_fwd(b.rows(b.q), F.LatentCache(data, 512), *rest, scale=0.07)
+    ok()
+    check_latent(*arrays(o, l), C.attend(b.q, b.data, 512, b.table, b.q_start, b.kv_len, True, 0.07), 576)
 
 
 def test_random_batches():

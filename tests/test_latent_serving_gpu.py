@@ -86,7 +86,7 @@ def test_serving(kind, page):
 @pytest.mark.parametrize("news,heads", [(1, 16), (1, 128), (40, 20)])
 def test_captured_step_on_other_lengths(news, heads):
     """A captured append and attention, replayed on other lengths, rows and pages."""
-    big = LatentBatch(60, [900, 500, 300], [news] * 3, heads, 512, 64)
+    *_, big = LatentBatch(60, [900, 500, 300], [news] * 3, heads, 512, 64).tables()
     c, table, qs, kl = big.device()
     lat, key, qr = big.rows(big.latent), big.rows(big.k_rope), big.rows(big.q_rope)
     q = big.rows(big.q)
@@ -110,8 +110,9 @@ def test_captured_step_on_other_lengths(news, heads):
             table.copy_(table.roll(-1, 0))
 
 
-def test_two_graphs_with_one_workspace():
-    b = LatentBatch(61, [3000, 77], [1, 1], 64, 512, 64)
+@pytest.mark.parametrize("heads", [64, 128])
+def test_two_graphs_with_one_workspace(heads):
+    *_, b = LatentBatch(61, [3000, 77], [1, 1], heads, 512, 64).tables()
     b2 = LatentBatch(62, [10, 5000, 600], [1, 2, 1], 16, 512, 64)
     ws = torch.zeros(max(F.fattn_latent_fwd_workspace_bytes(x.T, len(x.lens), x.heads, 512) for x in (b, b2)),
                      dtype=torch.uint8, device="cuda")
@@ -132,7 +133,7 @@ def test_two_graphs_with_one_workspace():
 
 def test_threads_and_streams():
     """Eight host threads, a stream each, batches of different layouts at once."""
-    bs = [LatentBatch(70 + i, [200 + 90 * i] * n, [new] * n, h, 256 if i & 1 else 512, 32)
+    bs = [[*LatentBatch(70 + i, [200 + 90 * i] * n, [new] * n, h, 256 if i & 1 else 512, 32).tables()][-1]
           for i, (n, new, h) in enumerate([(1, 1, 16), (90, 1, 3), (4, 1, 128), (7, 2, 40), (1, 90, 20), (3, 5, 64), (30, 1, 33), (2, 1, 1)])]
     dev, qs = [b.device() for b in bs], [b.rows(b.q) for b in bs]
     want = [F.fattn_latent_fwd(q, *d, scale=0.07) for q, d in zip(qs, dev)]
@@ -165,7 +166,7 @@ def test_threads_and_streams():
 def test_a_wait_budget_that_runs_out(news, heads):
     """Waits that give up are reported, and the next call, on the same memory and on
     tensor memory that the last one handed back, is right."""
-    b = LatentBatch(80, [3000, 700], [news, news], heads, 512, 64)
+    *_, b = LatentBatch(80, [3000, 700], [news, news], heads, 512, 64).tables()
     dev, q = b.device(), b.rows(b.q)
     want = F.fattn_latent_fwd(q, *dev, scale=0.07)
     ok()
