@@ -75,11 +75,10 @@ CacheSeqs seqs_of(const int* page_table, const int* q_start, const int* kv_len, 
 // Blocks of 128 rows on pairs of CTAs are for large calls of rank 512 (`reach`: keys
 // that a sequence's table has room for; what they really are is on the device), a call
 // in us on pairs and on single CTAs, 128 heads, one token a sequence:
-//   keys per pair    64 of 8000: 199 / 227   48 of 4000: 88 / 92   16 of 8000: 62 / 64
-//     below 1536:    24 of 4000: 54 / 55   96 of 1000: 68 / 66   40 of 2000: 54 / 53
-//                    16 of 1000: 28 / 24   48 of 300: 34 / 30    4 of 2000: 23 / 21
+//   64 of 2000 keys: 69 / 76    48 of 4000: 81 / 92    16 of 8000: 59 / 64
+//   below 1024 keys a pair:   16 of 1000: 28 / 24   48 of 300: 33 / 31   4 of 2000: 23 / 21
 //   rows not a multiple of 128 (32 sequences of 4000 keys, 64 heads, so many tokens):
-//     3: 100 / 91   5: 139 / 137   7: 171 / 183   9: 204 / 246
+//     3: 99 / 91   5: 137 / 136   7: 168 / 182   9: 202 / 246
 //   rank 256, whose products leave the exchange between the two CTAs no room:
 //     32 of 8000: 67 / 65   16 of 8000: 44 / 39   16 of 1000: 22 / 17
 // Both need the same workspace, so that its size does not depend on the reach.
@@ -92,7 +91,7 @@ Layout layout_of(int T, int B, int Hq, int rank, long long reach) {
   Layout l;
   l.rows = all <= 16 ? 16 : (all <= 32 ? 32 : 64);
   if (rank == kLatentPairRank && (halves % 2 == 0 || halves >= 7) &&
-      static_cast<double>(B) * static_cast<double>(pairs) * static_cast<double>(reach) >= 1536. * (kSms / 2))
+      static_cast<double>(B) * static_cast<double>(pairs) * static_cast<double>(reach) >= 1024. * (kSms / 2))
     l.rows = kLatentPairRows;
   const long long blocks = (all + l.rows - 1) / l.rows, groups = (blocks + kMaxSpan - 1) / kMaxSpan;
   l.span = static_cast<int>((blocks + groups - 1) / groups);
