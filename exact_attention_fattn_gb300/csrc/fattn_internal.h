@@ -243,7 +243,12 @@ struct LatentAttnArgs {
 };
 
 constexpr int kLatentKeys = 64;      // keys of a tile
-constexpr int kLatentUnitCost = 2;   // tiles that a unit counts beyond its own
+// Tiles that a unit of so many rows a block counts beyond its own when the work is dealt:
+// its queries and results.  In us with 0, 2, 3, 4: 64 sequences of 500 to 8000 keys, 16
+// heads 67.3, 67.0, 67.6, 68.1, 128 heads 109, 104.7, 101.9, 100.3; 24 of 4000 keys, 128
+// heads 57.3, 53.5, 51.5, 53.4; 32 of 1000 to 4000 keys, 1 to 5 tokens of 40 heads
+// (rank 256) 40.5, 37.7, 37.1, 37.7.
+constexpr int latent_unit_cost(int rows) { return rows < 64 ? 2 : 3; }
 
 constexpr int kLatentPairRank = 512;   // pairs of CTAs: the latent width that they are for,
 constexpr int kLatentPairRows = 128;   // rows of a unit and keys of a tile

@@ -170,7 +170,7 @@ struct __align__(16) Seg {
 static_assert(sizeof(Seg) == 32, "ring slot");
 
 // Walks a share.
-template <int KEYS>
+template <int KEYS, int COST>
 struct Walker {
   const LatentAttnArgs& a;
   int group_rows;
@@ -184,8 +184,8 @@ struct Walker {
     q = seq_info(a.s, b, a.page_shift);
     Groups<KEYS> g(a, q, group_rows);
     nt = g.tiles();
-    while (rem >= nt + kLatentUnitCost && g.live()) {
-      rem -= nt + kLatentUnitCost;
+    while (rem >= nt + COST && g.live()) {
+      rem -= nt + COST;
       ++rg;
       g.next();
       nt = g.tiles();
@@ -195,7 +195,7 @@ struct Walker {
   __device__ __forceinline__ bool next(Seg& s) {
     if (left <= 0) return false;
     if (at >= nt) {                     // tiles that stand for the unit itself
-      left -= nt + kLatentUnitCost - at;
+      left -= nt + COST - at;
       at = 0;
       if (left <= 0) return false;
       if (static_cast<long long>(++rg) * group_rows >= all_rows()) {
@@ -231,7 +231,7 @@ struct Share {
 // shared memory): place[0] is the sequence of its first tile, place[1] the tiles of
 // that sequence before it, to be read behind a barrier.  `mine` has thread t's numbers
 // of sequence t.
-template <int KEYS, int THREADS>
+template <int KEYS, int COST, int THREADS>
 __device__ __forceinline__ Share locate_share(const LatentAttnArgs& args, const SeqCheck& mine, int group_rows, int G,
                                               int share, long long* side, uint32_t* place) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -243,7 +243,7 @@ __device__ __forceinline__ Share locate_share(const LatentAttnArgs& args, const 
   };
   auto weight = [&](const SeqInfo& q) {
     long long w = 0;
-    for (Groups<KEYS> g(args, q, group_rows); g.live(); g.next()) w += g.tiles() + kLatentUnitCost;
+    for (Groups<KEYS> g(args, q, group_rows); g.live(); g.next()) w += g.tiles() + COST;
     return w;
   };
   long long sum = 0;

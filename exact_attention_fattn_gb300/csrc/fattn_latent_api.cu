@@ -206,7 +206,7 @@ int fattn_latent_fwd(const fattn_latent_cache* cache, const void* q, void* o, fl
   const long long units = static_cast<long long>(T) * Hq / (l.span * l.rows) + B;
   const bool on_pairs = l.rows == kLatentPairRows;
   const int tile = on_pairs ? kLatentPairKeys : kLatentKeys;
-  const long long per = (static_cast<long long>(max_pages) * cache->page + tile - 1) / tile + kLatentUnitCost;
+  const long long per = (static_cast<long long>(max_pages) * cache->page + tile - 1) / tile + latent_unit_cost(l.rows);
   if (units > 0x7fffffffll / per) return FATTN_ERR_TOO_LARGE;   // the kernels number them in 32 bits
   const long long shares = (on_pairs ? sms / 2 : sms) / l.span;
   a.span = l.span;

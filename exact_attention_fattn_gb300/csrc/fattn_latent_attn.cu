@@ -162,7 +162,7 @@ __global__ void __launch_bounds__(Cfg<N, R>::kThreads, 1)
     tma_prefetch_desc(&tm_q);
   }
   // The scan's scratch is in the references' place, which nothing uses yet.
-  const Share sh = locate_share<kKeys, kThreads>(args, mine, group_rows, G, share, reinterpret_cast<long long*>(xs), misc + 4);
+  const Share sh = locate_share<kKeys, latent_unit_cost(N), kThreads>(args, mine, group_rows, G, share, reinterpret_cast<long long*>(xs), misc + 4);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -596,7 +596,7 @@ __global__ void __launch_bounds__(Cfg<N, R>::kThreads, 1)
     __syncwarp();
   } else if (warp == kWalkWarp) {
     // ================================================================ schedule
-    Walker<kKeys> walk(args, group_rows, static_cast<int>(misc[4]), static_cast<int>(misc[5]), sh.j1 - sh.j0);
+    Walker<kKeys, latent_unit_cost(N)> walk(args, group_rows, static_cast<int>(misc[4]), static_cast<int>(misc[5]), sh.j1 - sh.j0);
     Seg s{};
     bool any = false;
     for (uint32_t i = 0;; ++i) {

@@ -213,7 +213,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_alloc_pair(smem_u32(const_cast<uint32_t*>(&misc[0])), 512);
     tmem_relinquish_pair();
   }
-  const Share sh = locate_share<kKeys, kThreads>(args, mine, group_rows, G, share, reinterpret_cast<long long*>(own),
+  const Share sh = locate_share<kKeys, latent_unit_cost(kRows), kThreads>(args, mine, group_rows, G, share, reinterpret_cast<long long*>(own),
                                                  reinterpret_cast<uint32_t*>(smem + C::kSegOff));   // read before the first segment
   tc_fence_before();
   __syncthreads();
@@ -787,7 +787,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp == kWalkWarp) {
     // ================================================================ schedule
     const uint32_t* place = reinterpret_cast<const uint32_t*>(smem + C::kSegOff);
-    Walker<kKeys> walk(args, group_rows, static_cast<int>(place[0]), static_cast<int>(place[1]), sh.j1 - sh.j0);
+    Walker<kKeys, latent_unit_cost(kRows)> walk(args, group_rows, static_cast<int>(place[0]), static_cast<int>(place[1]), sh.j1 - sh.j0);
     __syncwarp();
     Seg s{};
     bool any = false;
