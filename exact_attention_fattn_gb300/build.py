@@ -22,8 +22,8 @@ BUILD_DIR = os.path.join(PKG, "_build")
 # Debug variant for tests: every kernel range-checks its computed shared-
 # memory, TMEM and global indices (a failed check is reported as
 # FATTN_ERR_DEBUG_CHECK, not a trap), and the forward's K/V ring, the paged
-# cache's K ring have their minimum depth of two stages, so that the ring phases
-# wrap as often as they can.
+# cache's K ring and the latent cache's ring have their minimum depth of two
+# stages, so that the ring phases wrap as often as they can.
 DEBUG_LIB_PATH = os.path.join(PKG, "libfattn_debug.so")
 DEBUG_BUILD_DIR = os.path.join(PKG, "_build_debug")
 DEBUG_FLAGS = ["-DFATTN_DEBUG", "-DFATTN_FWD_STAGES=2", "-DFATTN_CACHE_K_STAGES=2", "-DFATTN_LATENT_MIN_RING"]

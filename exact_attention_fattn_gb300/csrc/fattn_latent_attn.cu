@@ -28,6 +28,16 @@
 // keys come out of DRAM once.  Units that shares split are joined in a second
 // kernel, in order.
 //
+// Bound: the cache's bytes for 16 and 32 rows, shared memory for 64, whose 1920 cycles of
+// products a 64-key tile (rank 512) are reads at 128 bytes a cycle, beside 576 for the
+// tile's way in.  Measured, rank 512, one new token each: 64 sequences of 500 to 8000 keys, 16 heads
+// 67 us (0.73 of the measured copy rate), 32 heads 76, 64 heads 80.5; 3 of 100000 to
+// 131071, 32 heads 85 (0.70); one of 1000, 16 heads 12.0, of which the two launches, the
+// schedule and the join are nearly all.  Products are issued in a fixed order by converged
+// code: under branches that the compiler takes for divergent each took 82 cycles (64
+// sequences of 128 heads 178 us, then 152; copies under a lane's branch, 190 cycles each,
+// 124.4, then 121.8).
+//
 // Warps: 0-3 softmax and results (0-7 with 64 rows, half of them each), then one for
 // tensor memory and MMA issue, one for loads, one for the walk over the share (it
 // publishes one segment after the other) and an idle one.

@@ -7,7 +7,9 @@
 // Bound: the bytes of x and y.  A thread has 8 pairs (two 16-byte loads) of up to
 // four heads of one row, so that their cosines and sines are loaded once and the
 // heads' loads go out together; neighbouring threads have a row's neighbouring
-// pairs, then rows or heads, whichever lie closer.
+// pairs, then rows or heads, whichever lie closer.  Measured, [2, 32, 4096, 128] (136 MB):
+// 21.7 us, 0.93 of the measured copy rate (two heads a thread 22.0, eight 24.8); a
+// few rows 2.8 us.
 #include <stdint.h>
 
 #include <nvtx3/nvToolsExt.h>
