@@ -667,14 +667,18 @@ __device__ __forceinline__ void merge(Part& a, const Part& b) {
 }
 
 // The rows of the units that shares start and others go on with.  Four groups of
-// threads have 4 columns each of a row: four rows where a unit has few parts, a
-// quarter of one row's parts where it has many.  Every block counts the call's
-// items and takes its own, so that there are no more blocks than work.
+// threads have 4 columns each of a row: a row or two of their own where a unit has few
+// parts, a quarter of one row's parts where it has many.  A thread's four loads go out together:
+// four parts of a row, or two of two rows for blocks of 128, whose units have few parts
+// (whole calls: 64 sequences of 500 to 8000 keys, 128 heads 102.5 us with four of one, 101.2
+// so; 8 of 4000, 64 rows a block, 28.5 and 30.4).  Every block counts the call's items and
+// takes its own, so that there are no more blocks than work.
 constexpr int kJoinGroups = 4;
 constexpr int kJoinMany = 12;
 
 template <int N, int R>
 __global__ void __launch_bounds__(kJoinGroups * R / 4) join_kernel(const LatentAttnArgs a) {
+  constexpr int kPer = N == kLatentPairRows ? 2 : 1, kAhead = 4 / kPer, kItem = kPer * kJoinGroups;
   __shared__ Part side[kJoinGroups][R / 4];
   __shared__ int4 recs[kSms];
   __shared__ int before[kSms + 1];
@@ -688,7 +692,7 @@ __global__ void __launch_bounds__(kJoinGroups * R / 4) join_kernel(const LatentA
   for (int t = tid; t < G; t += blockDim.x) {
     const int4 r = a.rec[t];
     recs[t] = r;
-    before[t + 1] = r.y == 0 ? 0 : (many(t, r) ? rows_of(r) : (rows_of(r) + kJoinGroups - 1) / kJoinGroups);
+    before[t + 1] = r.y == 0 ? 0 : (many(t, r) ? rows_of(r) : (rows_of(r) + kItem - 1) / kItem);
   }
   if (tid == 0) before[0] = 0;
   __syncthreads();
@@ -716,43 +720,57 @@ __global__ void __launch_bounds__(kJoinGroups * R / 4) join_kernel(const LatentA
     const int4 rec = recs[share];
     const bool split = many(share, rec);
     const int rows = rows_of(rec), at_row = item - before[share];
-    const int row = split ? at_row : kJoinGroups * at_row + group;
-    Part p{-FLT_MAX, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
-    if (row < rows) {
-      // Four parts' loads go out together; behind the last one it is loaded again and not counted.
-      const int step = split ? kJoinGroups : 1;
-      for (int t0 = share + (split ? group : 0); t0 <= rec.w; t0 += 4 * step) {
-        Part x[4] = {};
+    const int row0 = split ? at_row : kItem * at_row + group;
+    Part p[kPer];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const int t = min(t0 + k * step, rec.w);
+    for (int i = 0; i < kPer; ++i) p[i] = Part{-FLT_MAX, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
+    // Behind the last part it is loaded again and not counted.
+    const int step = split ? kJoinGroups : 1, ahead = split ? 4 : kAhead;
+    auto part_of = [&](int t0, int i, int k) { return t0 + (split ? i * kAhead + k : k) * step; };
+    auto row_of = [&](int i) { return split ? row0 : row0 + i * kJoinGroups; };
+    for (int t0 = share + (split ? group : 0); t0 <= rec.w; t0 += ahead * step) {
+      Part x[kPer][kAhead] = {};
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        const int row = row_of(i);
+        if (row >= rows) continue;
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+          const int t = min(part_of(t0, i, k), rec.w);
           const long long at = (2ll * (t * a.span + row / N) + (t == share ? 1 : 0)) * N + row % N;
           if (!dcheck(inside(at, 1, 2ll * (N == kLatentPairRows ? kSms / 2 : kSms) * N), a.status, 696)) continue;
           const float2 ml = a.part_ml[at];
-          x[k] = Part{ml.x, ml.y, reinterpret_cast<const float4*>(a.part_o + at * R)[q4]};
+          x[i][k] = Part{ml.x, ml.y, reinterpret_cast<const float4*>(a.part_o + at * R)[q4]};
         }
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-          if (t0 + k * step <= rec.w) merge(p, x[k]);
       }
+#pragma unroll
+      for (int i = 0; i < kPer; ++i)
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k)
+          if (part_of(t0, i, k) <= rec.w) merge(p[i], x[i][k]);
     }
     if (split) {
-      side[group][q4] = p;
+      if constexpr (kPer > 1) merge(p[0], p[1]);
+      side[group][q4] = p[0];
       __syncthreads();
       if (group == 0) {
 #pragma unroll
-        for (int g = 1; g < kJoinGroups; ++g) merge(p, side[g][q4]);
+        for (int g = 1; g < kJoinGroups; ++g) merge(p[0], side[g][q4]);
       }
       __syncthreads();
       if (group != 0) continue;
     }
-    if (row >= rows) continue;
-    const long long out = static_cast<long long>(rec.x) * a.Hq + first_of(rec) + row;
-    if (!dcheck(inside(out, 1, static_cast<long long>(a.s.T) * a.Hq), a.status, 697)) continue;
-    const float inv = p.l == 0.f ? 0.f : 1.f / p.l;
-    *reinterpret_cast<uint2*>(a.o + out * R + 4 * q4) =
-        make_uint2(pack_bf16x2(p.o.x * inv, p.o.y * inv), pack_bf16x2(p.o.z * inv, p.o.w * inv));
-    if (q4 == 0) a.lse[out] = p.l == 0.f ? -INFINITY : (p.m + log2f(p.l)) * kLn2;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int row = row_of(i);
+      if ((split && i > 0) || row >= rows) continue;
+      const long long out = static_cast<long long>(rec.x) * a.Hq + first_of(rec) + row;
+      if (!dcheck(inside(out, 1, static_cast<long long>(a.s.T) * a.Hq), a.status, 697)) continue;
+      const float inv = p[i].l == 0.f ? 0.f : 1.f / p[i].l;
+      *reinterpret_cast<uint2*>(a.o + out * R + 4 * q4) =
+          make_uint2(pack_bf16x2(p[i].o.x * inv, p[i].o.y * inv), pack_bf16x2(p[i].o.z * inv, p[i].o.w * inv));
+      if (q4 == 0) a.lse[out] = p[i].l == 0.f ? -INFINITY : (p[i].m + log2f(p[i].l)) * kLn2;
+    }
   }
 }
 
