@@ -5,15 +5,16 @@
 // are taken first, so results do not depend on timing.
 //
 // Bound: latency for the counts (a few integers a page; one CTA, so that the
-// order needs no second launch), bytes for the copies.  A CTA copies one piece of
-// a page at a time, four 16-byte loads a thread in flight, and takes the next
-// piece of the call's list, whose length only the device knows.
+// order needs no second launch), bytes for the copies.  A piece of a page goes through
+// shared memory by two bulk copies, which one thread of a CTA issues; two CTAs an SM, six
+// pieces of 16 KB each.  The list's length only the device knows.
 //
 // Measured: 18 of 24 sequences forked from 6 (latent cache, 300 to 4000 tokens) and
-// room for one token each, both calls 14.5 us; 576 of 768 from 192 (8-bit cache, 8 heads of
-// 128, 500 to 2000 tokens) and room for 100 more, 39 us, 22.5 of them the copies at
-// the measured copy rate; 291 MB of a pool moved together, 63.4 us, 0.68 of it
-// (eight blocks of 256 threads an SM, so 32 registers; with 40 68.7).
+// room for one token each, both calls 14.1 us; 576 of 768 from 192 (8-bit cache, 8 heads of
+// 128, 500 to 2000 tokens) and room for 100 more, 38 us; 291 MB of a pool moved together
+// 57.5 us, 49 of them the copies, 0.87 of the measured copy rate (loads and stores of 16
+// bytes a thread, 2048 threads an SM: 39 and 63.4; pieces of 24 KB 36.5 and 57.9, of
+// 8 KB, with a division a piece, 58 and 75).
 #include <stdint.h>
 
 #include <nvtx3/nvToolsExt.h>
@@ -29,7 +30,11 @@ constexpr int kPlanes = 5;
 constexpr int kMaxSeqs = 4096;
 constexpr int kScanThreads = 1024;
 constexpr int kScanPages = 16;          // counts a thread looks at in one turn
-constexpr int kCopyThreads = 256;
+constexpr int kPlainThreads = 128;
+constexpr int kCopyThreads = 32 + kPlainThreads;
+constexpr int kStages = 6;              // pieces in shared memory, of each of two CTAs an SM
+constexpr int kBehind = 2;              // of them on their way out
+constexpr long long kBulkBytes = 2048;  // smaller parts of a page go by plain copies
 constexpr int kPieceBytes = 16384;      // of a page's largest plane, a CTA's turn
 constexpr unsigned int kStatusNoPages = FATTN_ERR_NO_PAGES;
 
@@ -57,6 +62,8 @@ struct Planes {
   long long stride[kPlanes];
   long long bytes[kPlanes];
   int wide[kPlanes];          // 16-byte copies
+  int bulk[kPlanes];
+  int per[kPlanes];           // bytes of a piece
   int n, pieces;
 };
 
@@ -353,42 +360,85 @@ __global__ void __launch_bounds__(kScanThreads) plan_kernel(const Tables t, int*
 
 // ------------------------------------------------------------------ copies
 
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+               "l"(src), "r"(bytes), "r"(bar)
+               : "memory");
+}
+// A group of its own; all but the last kBehind groups have then read their source.
+__device__ __forceinline__ void bulk_store(void* dst, uint32_t src, uint32_t bytes) {
+  asm volatile(
+      "cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;\n\t"
+      "cp.async.bulk.commit_group;\n\t"
+      "cp.async.bulk.wait_group.read %3;" ::"l"(dst),
+      "r"(src), "r"(bytes), "n"(kBehind)
+      : "memory");
+}
+__device__ __forceinline__ void bulk_wait_group0() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+
 template <class V>
-__device__ __forceinline__ void copy_span(uint8_t* to, const uint8_t* from, long long bytes) {
-  constexpr int kAhead = 4;
+__device__ __forceinline__ void copy_span(uint8_t* to, const uint8_t* from, long long bytes, int thread) {
   const V* s = reinterpret_cast<const V*>(from);
   V* d = reinterpret_cast<V*>(to);
   const int n = static_cast<int>(bytes / sizeof(V));
-  int i = threadIdx.x;
-  for (; i + (kAhead - 1) * kCopyThreads < n; i += kAhead * kCopyThreads) {
-    V x[kAhead];
-#pragma unroll
-    for (int k = 0; k < kAhead; ++k) x[k] = s[i + k * kCopyThreads];
-#pragma unroll
-    for (int k = 0; k < kAhead; ++k) d[i + k * kCopyThreads] = x[k];
-  }
-  for (; i < n; i += kCopyThreads) d[i] = s[i];
+  for (int i = thread; i < n; i += kPlainThreads) d[i] = s[i];
 }
 
-// Copies the list's pages; blocks from copy_blocks on rewrite the table where
-// pages have moved (compact; to_page is nullptr otherwise).
-__global__ void __launch_bounds__(kCopyThreads, 8) copy_kernel(const Tables t, const __grid_constant__ Planes planes,
-                                                            CopyList list, int copy_blocks, const int* kv_len,
-                                                            const int* to_page, const int* limit) {
+// Piece `piece` of plane k of a page: its first byte and its length, which may be 0.
+__device__ __forceinline__ int piece_of(const Planes& p, int k, int piece, long long& lo) {
+  lo = min(p.bytes[k], static_cast<long long>(piece) * p.per[k]);
+  return static_cast<int>(min(p.bytes[k], lo + p.per[k]) - lo);
+}
+
+// Copies the list's pages and, where kv_len is given, rewrites the table where pages have
+// moved (compact).  One thread moves a CTA's pieces through shared memory by bulk copies,
+// kStages - kBehind on their way in; the others take what is small or not aligned to
+// 16 bytes, and the table.
+__global__ void __launch_bounds__(kCopyThreads) copy_kernel(const Tables t, const __grid_constant__ Planes planes,
+                                                            CopyList list, const int* kv_len, const int* to_page,
+                                                            const int* limit, long long wait_budget) {
+  extern __shared__ __align__(128) uint8_t stages[];
+  __shared__ uint64_t full[kStages];
+  __shared__ uint8_t* out[kStages];
+  __shared__ uint32_t length[kStages];
+  __shared__ uint32_t abort;
+  const uint32_t sbase = smem_u32(stages);
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kStages; ++i) mbar_init(smem_u32(&full[i]), 1);
+    fence_barrier_init();
+    abort = 0u;
+  }
   wait_for_parent();
   const int n = *list.count;
   if (n == 0) return;
-  if (static_cast<int>(blockIdx.x) >= copy_blocks) {
+  const long long items = static_cast<long long>(n) * planes.pieces;
+  if (threadIdx.x >= 32) {
+    const int me = threadIdx.x - 32;
+    for (long long w = blockIdx.x; w < items; w += gridDim.x) {
+      const int i = static_cast<int>(w / planes.pieces), piece = static_cast<int>(w - static_cast<long long>(i) * planes.pieces);
+      for (int k = 0; k < planes.n; ++k) {
+        if (planes.bulk[k]) continue;
+        const long long from = list.src[i], to = list.dst[i];
+        if (!dcheck(inside(from, 1, t.pages) && inside(to, 1, t.pages), t.status, 675)) continue;
+        long long lo;
+        const int span = piece_of(planes, k, piece, lo);
+        uint8_t* d = planes.base[k] + to * planes.stride[k] + lo;
+        const uint8_t* s = planes.base[k] + from * planes.stride[k] + lo;
+        if (planes.wide[k]) copy_span<uint4>(d, s, span, me);
+        else copy_span<uint32_t>(d, s, span, me);
+      }
+    }
+    if (kv_len == nullptr) return;
     const int lim = *limit;
-    for (int b = blockIdx.x - copy_blocks; b < t.B; b += gridDim.x - copy_blocks) {
+    for (int b = blockIdx.x; b < t.B; b += gridDim.x) {
       const int len = kv_len[b];
       if (len < 0 || len > t.cap()) {
-        if (threadIdx.x == 0) record_bad_index(t.status, kSiteSeqStart);
+        if (me == 0) record_bad_index(t.status, kSiteSeqStart);
         continue;
       }
       int* row = t.table + static_cast<long long>(b) * t.max_pages;
       const int held = t.held(len);
-      for (int k = threadIdx.x; k < held; k += kCopyThreads) {
+      for (int k = me; k < held; k += kPlainThreads) {
         const int p = row[k];
         if (!t.is_page(p)) record_bad_index(t.status, kSitePage);
         else if (p >= lim) row[k] = to_page[p];
@@ -396,21 +446,70 @@ __global__ void __launch_bounds__(kCopyThreads, 8) copy_kernel(const Tables t, c
     }
     return;
   }
-  const long long items = static_cast<long long>(n) * planes.pieces;
-  for (long long w = blockIdx.x; w < items; w += copy_blocks) {
-    const int i = static_cast<int>(w / planes.pieces), piece = static_cast<int>(w - static_cast<long long>(i) * planes.pieces);
-    const long long from = list.src[i], to = list.dst[i];
-    if (!dcheck(inside(from, 1, t.pages) && inside(to, 1, t.pages), t.status, 675)) continue;
-    for (int k = 0; k < planes.n; ++k) {
-      const long long unit = planes.wide[k] ? 16 : 4;
-      const long long per = (planes.bytes[k] / unit + planes.pieces - 1) / planes.pieces * unit;
-      const long long lo = min(planes.bytes[k], piece * per), span = min(planes.bytes[k], lo + per) - lo;
-      uint8_t* d = planes.base[k] + to * planes.stride[k] + lo;
-      const uint8_t* s = planes.base[k] + from * planes.stride[k] + lo;
-      if (planes.wide[k]) copy_span<uint4>(d, s, span);
-      else copy_span<uint32_t>(d, s, span);
+  if (threadIdx.x != 0) return;
+  // The next piece to load, of page i's planes from k on; the numbers of the page after
+  // it are asked for a turn early.
+  const int pages_on = gridDim.x / planes.pieces, pieces_on = gridDim.x - pages_on * planes.pieces;
+  int i = blockIdx.x / planes.pieces, piece = blockIdx.x - i * planes.pieces, k = 0;
+  int next_from = i < n ? list.src[i] : 0, next_to = i < n ? list.dst[i] : 0;
+  long long from = 0, to = 0;
+  bool fresh = true;
+  auto next = [&](const uint8_t*& src, uint8_t*& dst) -> uint32_t {
+    while (i < n) {
+      if (fresh) {
+        from = next_from;
+        to = next_to;
+        const int ahead = i + pages_on + (piece + pieces_on >= planes.pieces ? 1 : 0);
+        if (ahead < n) {
+          next_from = list.src[ahead];
+          next_to = list.dst[ahead];
+        }
+        fresh = false;
+        k = dcheck(inside(from, 1, t.pages) && inside(to, 1, t.pages), t.status, 677) ? 0 : planes.n;
+      }
+      while (k < planes.n) {
+        const int p = k++;
+        if (!planes.bulk[p]) continue;
+        long long lo;
+        const int span = piece_of(planes, p, piece, lo);
+        if (span == 0 || !dcheck(span <= kPieceBytes, t.status, 678)) continue;
+        src = planes.base[p] + from * planes.stride[p] + lo;
+        dst = planes.base[p] + to * planes.stride[p] + lo;
+        return static_cast<uint32_t>(span);
+      }
+      i += pages_on;
+      piece += pieces_on;
+      if (piece >= planes.pieces) {
+        piece -= planes.pieces;
+        ++i;
+      }
+      fresh = true;
     }
+    return 0u;
+  };
+  const WaitCtx wc{wait_budget, &abort, t.status};
+  unsigned int loads = 0, stores = 0;
+  bool more = true;
+  while (true) {
+    // A stage is free once the store from it has read it: all but the last kBehind have.
+    while (more && loads - (stores > kBehind ? stores - kBehind : 0u) < kStages) {
+      const uint8_t* src = nullptr;
+      const unsigned int at = loads % kStages;
+      const uint32_t bytes = next(src, out[at]);
+      if (!(more = bytes != 0u)) break;
+      length[at] = bytes;
+      mbar_arrive_expect_tx(smem_u32(&full[at]), bytes);
+      bulk_load(sbase + at * kPieceBytes, src, bytes, smem_u32(&full[at]));
+      ++loads;
+    }
+    if (stores == loads) break;
+    const unsigned int at = stores % kStages;
+    if (!mbar_wait(smem_u32(&full[at]), (stores / kStages) & 1, wc, kWaitKvFull)) break;
+    bulk_store(out[at], sbase + at * kPieceBytes, length[at]);
+    ++stores;
   }
+  bulk_wait_group0();
+  for (; stores < loads; ++stores) mbar_wait_drain(smem_u32(&full[stores % kStages]), (stores / kStages) & 1);
 }
 
 // ------------------------------------------------------------------ host
@@ -445,11 +544,16 @@ int check_planes(const fattn_page_pool* pool, const fattn_plane* planes, int n, 
     out.stride[i] = p.stride;
     out.bytes[i] = p.bytes;
     out.wide[i] = aligned(p.base, 16) && p.bytes % 16 == 0 && p.stride % 16 == 0;
+    out.bulk[i] = out.wide[i] && p.bytes >= kBulkBytes;
     most = p.bytes > most ? p.bytes : most;
   }
   (void)pool;
   out.n = n;
   out.pieces = static_cast<int>((most + kPieceBytes - 1) / kPieceBytes);
+  for (int i = 0; i < n; ++i) {
+    const long long unit = out.wide[i] ? 16 : 4;
+    out.per[i] = static_cast<int>((out.bytes[i] / unit + out.pieces - 1) / out.pieces * unit);
+  }
   return FATTN_OK;
 }
 
@@ -482,9 +586,17 @@ PagesWorkspace workspace_of(int pages, int B) {
   return w;
 }
 
-int copy_grid(long long most_items) {
-  const long long all = 8ll * kSms;       // 2048 threads an SM
-  return static_cast<int>(most_items < all ? most_items : all);
+int launch_copies(const Tables& t, const Planes& p, const CopyList& list, long long most_pages, const int* kv_len,
+                  const int* to_page, const int* limit, long long budget, cudaStream_t stream) {
+  static SmemLimit limit_of;
+  constexpr int kBytes = kStages * kPieceBytes;
+  if (limit_of.raise(reinterpret_cast<const void*>(copy_kernel), kBytes) != cudaSuccess) return FATTN_ERR_CUDA;
+  const long long items = most_pages * p.pieces;
+  const int grid = static_cast<int>(items < 2 * kSms ? items : 2 * kSms);
+  return launch_child(copy_kernel, grid, kCopyThreads, kBytes, stream, t, p, list, kv_len, to_page, limit, budget) ==
+                 cudaSuccess
+             ? FATTN_OK
+             : FATTN_ERR_CUDA;
 }
 
 int from_launch(cudaError_t e) { return e == cudaSuccess ? FATTN_OK : FATTN_ERR_CUDA; }
@@ -554,10 +666,7 @@ int fattn_pages_extend(const fattn_page_pool* pool, const fattn_plane* planes, i
                                           reinterpret_cast<int*>(base + w.last), list);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return FATTN_ERR_CUDA;
-  const int grid = copy_grid(static_cast<long long>(B) * p.pieces);
-  return from_launch(launch_child(copy_kernel, grid, kCopyThreads, 0, st, t, p, list, grid,
-                                  static_cast<const int*>(nullptr), static_cast<const int*>(nullptr),
-                                  static_cast<const int*>(nullptr)));
+  return launch_copies(t, p, list, B, nullptr, nullptr, nullptr, budget, st);
 }
 
 int fattn_pages_compact(const fattn_page_pool* pool, const fattn_plane* planes, int n_planes, int* page_table,
@@ -582,10 +691,7 @@ int fattn_pages_compact(const fattn_page_pool* pool, const fattn_plane* planes, 
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   plan_kernel<<<1, kScanThreads, 0, st>>>(t, to_page, list, limit);
   if (cudaGetLastError() != cudaSuccess) return FATTN_ERR_CUDA;
-  const int copies = copy_grid((static_cast<long long>(pool->pages) / 2 + 1) * p.pieces);
-  const int rows = B < 2 * kSms ? B : 2 * kSms;
-  return from_launch(launch_child(copy_kernel, copies + rows, kCopyThreads, 0, st, t, p, list, copies, kv_len,
-                                  static_cast<const int*>(to_page), static_cast<const int*>(limit)));
+  return launch_copies(t, p, list, static_cast<long long>(pool->pages) / 2 + 1, kv_len, to_page, limit, budget, st);
 }
 
 }  // extern "C"
