@@ -107,6 +107,9 @@ __device__ __forceinline__ void stmatrix_x4_trans(uint32_t addr, uint32_t a, uin
                "r"(c), "r"(d)
                : "memory");
 }
+__device__ __forceinline__ void prefetch_l2(const void* from, int bytes) {
+  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(from), "r"(bytes) : "memory");
+}
 // Entry `first` + lane of a sequence's row of the page table; -1 past its end.
 __device__ __forceinline__ int page_of_lane(const LatentAttnArgs& a, int b, int len, int first) {
   const int p = first + static_cast<int>(threadIdx.x & 31);

@@ -31,8 +31,8 @@
 // Bound: the cache's bytes for 16 and 32 rows, shared memory for 64, whose 1920 cycles of
 // products a 64-key tile (rank 512) are reads at 128 bytes a cycle, beside 576 for the
 // tile's way in.  Measured, rank 512, one new token each: 64 sequences of 500 to 8000 keys, 16 heads
-// 67 us (0.73 of the measured copy rate), 32 heads 76, 64 heads 80.5; 3 of 100000 to
-// 131071, 32 heads 85 (0.70); one of 1000, 16 heads 12.0, of which the two launches, the
+// 64.5 us (0.75 of the measured copy rate), 32 heads 75, 64 heads 81; 3 of 100000 to
+// 131071, 32 heads 84 (0.71); one of 1000, 16 heads 12.0, of which the two launches, the
 // schedule and the join are nearly all.  Products are issued in a fixed order by converged
 // code: under branches that the compiler takes for divergent each took 82 cycles (64
 // sequences of 128 heads 178 us, then 152; copies under a lane's branch, 190 cycles each,
@@ -595,6 +595,29 @@ __global__ void __launch_bounds__(Cfg<N, R>::kThreads, 1)
           }
         }
         if (!ok) break;
+        // The next tile on its way to L2 in one piece, ahead of the boxes that wait for slots (64
+        // sequences of 500 to 8000 keys, 16 heads 67.5 us without, 65.0 so, 66.1 two ahead,
+        // 68.7 three).  With 64 rows it gains 2 % where a sequence has one block, but its code
+        // costs 4 % where it has several (32 sequences of 4000 keys, 160 rows: 92 and 88).
+        if constexpr (N < 64) {
+          if (j + 1 < last_tile) {
+            const int key = (j + 1) * kKeys;
+            auto page_ahead = [&](int k) {
+              const int at = (k >> args.page_shift) - base;
+              const int a = __shfl_sync(0xffffffffu, cur, at & 31), b = __shfl_sync(0xffffffffu, nxt, at & 31);
+              return at < 32 ? a : b;
+            };
+            constexpr int kWidth = R + kLatentRope;
+            auto fetch = [&](int p, int k) {
+              if (p >= 0 && p < args.pages && lane == 0)
+                prefetch_l2(args.data + p * args.page_stride + (k & (page - 1)) * kWidth, box * kWidth * 2);
+            };
+            const int p0 = page_ahead(key), p1 = page_ahead(key + 32);
+            fetch(p0, key);
+            if (boxes == 2) fetch(p1, key + 32);
+            __syncwarp();
+          }
+        }
       }
     }
     // Every copy this warp started must have landed before the CTA exits.

@@ -27,8 +27,8 @@
 // thread has stored (votes and P by plain remote stores and releases took 5500 cycles
 // a tile, 2500 of them waiting for the votes).
 //
-// Measured: 2 pieces of 1024 tokens, 16 heads, before keys up to 8192: 470 us (64 rows a CTA:
-// 614), 1060 TFLOP/s; 64 single tokens of 128 heads over 500 to 8000 keys 102 (120).  A tile
+// Measured: 2 pieces of 1024 tokens, 16 heads, before keys up to 8192: 467 us (64 rows a CTA:
+// 614), 1070 TFLOP/s; 64 single tokens of 128 heads over 500 to 8000 keys 101 (120).  A tile
 // takes 4100 cycles in the first.  Neither the products bound it (with a quarter of
 // their columns 459) nor L2 (two pairs a cluster with one copy of the keys for both 512)
 // nor the softmax (16 warps 477): a tile's slots are free only after its second product,
@@ -138,10 +138,6 @@ __device__ __forceinline__ uint32_t movmatrix_trans(uint32_t x) {
   uint32_t y;
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
   return y;
-}
-
-__device__ __forceinline__ void prefetch_l2(const void* from, int bytes) {
-  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(from), "r"(bytes) : "memory");
 }
 
 // bar_done for what either CTA completes.  Acquired at the CTA's scope, as what the barriers of
