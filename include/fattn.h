@@ -483,9 +483,10 @@ int fattn_latent_append(const fattn_latent_cache* cache, const void* latent, lon
  * (fattn_latent_append writes no others).
  * Rounding: probabilities are rounded to bf16 (2^-8) for the second product, and O to
  * bf16 (2^-8); scores, sums, maxima and the accumulators are fp32.
- * The rows of an average sequence, T * Hq / B, decide how the call is laid out; a batch that
- * mixes pieces of prompts with many single tokens is faster as two calls.
- * Results do not depend on timing.  Returns a fattn_status.
+ * The rows of an average sequence, T * Hq / B, and for more than 64 of them the room of the
+ * tables, max_pages * page, decide how the call is laid out (sums are then taken in another
+ * order); a batch that mixes pieces of prompts with many single tokens is faster as two
+ * calls.  Results do not depend on timing.  Returns a fattn_status.
  */
 size_t fattn_latent_fwd_workspace_bytes(int T, int B, int Hq, int rank);
 int fattn_latent_fwd(const fattn_latent_cache* cache, const void* q, void* o, float* lse,

@@ -56,9 +56,9 @@ class LatentBatch:
         yield self
         if self.rank == 512 and self.T * self.heads > 64 * len(self.lens):
             b = copy.copy(self)
-            b.max_pages = self.max_pages + 120000 // self.page
+            b.max_pages = self.table.shape[1] + 120000 // self.page
             b.table = np.full((len(self.lens), b.max_pages), 1 << 30, dtype=np.int32)
-            b.table[:, :self.max_pages] = self.table
+            b.table[:, :self.table.shape[1]] = self.table
             yield b
 
     def device(self, gap=0):

@@ -151,11 +151,38 @@ def test_rows_that_see_nothing():
         check(LatentBatch(32, [0, 5], [3, 9], heads, 256, 64), causal=False)
 
 
-def test_gaps_between_pages_and_wide_tables():
-    b = LatentBatch(33, [200, 513], [1, 1], 16, 512, 64)
+@pytest.mark.parametrize("heads,page", [(16, 64), (128, 32), (128, 128)])
+def test_gaps_between_pages_and_wide_tables(heads, page):
+    b = LatentBatch(33, [200, 513], [1, 1], heads, 512, page)
     check(b, gap=64)
     b.table = np.concatenate([b.table, np.full((2, 3000), -7, np.int32)], axis=1)
     check(b)
+
+
+@pytest.mark.parametrize("heads", [3, 16, 64, 128])
+def test_no_rows_at_all(heads):
+    """Only padding: nothing is written, in any layout."""
+    b = LatentBatch(45, [70, 300], [0, 0], heads, 512, 64, pad_rows=3)
+    for x in b.tables():
+        o, l = run(x)
+        assert (o == 7.0).all() and (l == 7.0).all()
+
+
+@pytest.mark.parametrize("heads,pages,page", [(16, 3, 32), (64, 5, 64), (128, 608, 128)])
+def test_tables_that_are_full(heads, pages, page):
+    """Lengths that fill the table to its last slot (128 heads: on pairs)."""
+    b = LatentBatch(46, [pages * page], [1], heads, 512, page)
+    b.table, b.max_pages = np.ascontiguousarray(b.table[:, :pages]), pages
+    o, l = run(b)
+    check_latent(o, l, C.attend(b.q, b.data, 512, b.table, b.q_start, b.kv_len, True, 0.07), 576)
+
+
+def test_many_sequences_of_many_rows():
+    """More sequences than a pair has threads, and most heads."""
+    r = np.random.default_rng(47)
+    lens = [int(x) for x in r.integers(1, 40, 700)]
+    check(LatentBatch(47, lens, [1 if i % 7 else 0 for i in range(700)], 80, 512, 32, pad_rows=3))
+    check(LatentBatch(48, [90, 5], [1, 2], 1024, 512, 64))
 
 
 def test_pages_that_do_not_exist():
@@ -344,7 +371,7 @@ def test_append_many_sequences_and_in_place():
 @pytest.mark.parametrize("column", [0, 255, 256, 511, 512, 575])
 def test_tokens_that_are_not_finite(bad, column):
     """Such a token makes the rows that attend to it NaN, and no others."""
-    b = LatentBatch(53, [90, 70], [40, 3], 4, 512, 32)
+    *_, b = LatentBatch(53, [90, 70], [40, 3], 4, 512, 32).tables()
     if column < 512:
         b.latent[20, column] = bad
     else:
