@@ -2,6 +2,8 @@
 caches against the oracle's one sequence after the other, and what the calls
 refuse or report."""
 
+import ctypes
+
 import numpy as np
 import pytest
 import torch
@@ -294,6 +296,65 @@ def test_large_pages_past_32_bits():
     ok()
     assert int(pool.refs[61999]) == 0 and int(pool.refs[61998]) == 0 and int((pool.refs == 0).sum()) == 2
     assert int(pool.refs[7]) == 1
+
+
+@pytest.mark.parametrize("seed", [0, 1, 2])
+def test_planes_of_any_size(seed):
+    """Through the C ABI: parts of a page of a few bytes up to several pieces, aligned to
+    4, 8 or 16 bytes, with gaps between the pages that stay as they were."""
+    r = np.random.default_rng(90 + seed)
+    pages, B, width = 300, 9, 20
+    sizes = [[4, 2048, 16400, 70000, 131072], [2032, 2064, 16384, 32, 49156], [100000, 16, 8, 65536, 4100]][seed]
+    aligns = [[4, 16, 16, 16, 16], [16, 16, 16, 16, 4], [16, 16, 8, 4, 16]][seed]
+    gaps = [int(x) for x in r.integers(0, 5, 5) * 16]
+    bufs, planes, want = [], [], []
+    for size, align, gap in zip(sizes, aligns, gaps):
+        stride = size + gap + (-(size + gap)) % align
+        buf = torch.from_numpy(r.integers(0, 256, 16 + pages * stride).astype(np.uint8)).cuda()
+        base = align % 16                                # 16-byte aligned, or 4 or 8 bytes further
+        bufs.append((buf, base, stride, size))
+        planes.append((buf.data_ptr() + base, stride, size))
+        want.append(buf.cpu().numpy().copy())
+    held = r.permutation(pages)[:B * 10].reshape(B, 10)
+    table = np.full((B, width), -1)
+    table[:, :10] = held
+    refs = np.zeros(pages, int)
+    refs[held] = 1
+    kv = np.full(B, 10 * 32 - 5)
+    d_table, d_refs, d_kv = (torch.tensor(x, dtype=torch.int32, device="cuda") for x in (table, refs, kv))
+    lib = _lib.load()
+    need = int(lib.fattn_pages_workspace_bytes(pages, B))
+    ws = torch.full((need,), 0xFF, dtype=torch.uint8, device="cuda")
+    pool = _lib.PagePoolStruct(d_refs.data_ptr(), pages, 32)
+    arr = (_lib.PlaneStruct * 5)(*planes)
+    assert lib.fattn_pages_compact(ctypes.byref(pool), arr, 5, d_table.data_ptr(), d_kv.data_ptr(), ws.data_ptr(), need, B,
+                                   width, torch.cuda.current_stream().cuda_stream) == 0
+    ok()
+    views = [np.lib.stride_tricks.as_strided(w[base:], (pages, size), (stride, 1)) for w, (_, base, stride, size) in zip(want, bufs)]
+    P.compact(refs, table, views, 32, kv)
+    assert np.array_equal(d_table.cpu().numpy(), table) and np.array_equal(d_refs.cpu().numpy(), refs)
+    for w, (buf, *_) in zip(want, bufs):
+        assert np.array_equal(buf.cpu().numpy(), w)
+
+
+def test_a_wait_budget_that_runs_out():
+    """Copies that give up are reported, and the next call is right."""
+    for i in range(3):
+        p = Pool("latent", 400, 20, 12, 128, seed=i)
+        p.extend([100 + 50 * j for j in range(20)])
+        p.free(list(range(0, 20, 2)))
+        F.fattn_set_wait_budget(1)
+        try:
+            F.fattn_pages_compact(p.pool, p.cache, p.table, p.kv)
+            assert F.fattn_check_status() in (_lib.FATTN_OK, _lib.FATTN_ERR_TIMEOUT)
+        finally:
+            F.fattn_set_wait_budget(0)
+    p = Pool("latent", 400, 20, 12, 128, seed=5)
+    p.extend([100 + 50 * j for j in range(20)])
+    p.free(list(range(0, 20, 2)))
+    p.compact()
+    p.same()
+    ok()
 
 
 def test_refusals_of_the_binding():
