@@ -107,6 +107,26 @@ __device__ __forceinline__ void stmatrix_x4_trans(uint32_t addr, uint32_t a, uin
                "r"(c), "r"(d)
                : "memory");
 }
+// A wait by a whole warp.  What comes after a first look stands once in a kernel, not at each of
+// 20 to 30 places: its roles share the instruction caches, and the pieces of 1024 tokens
+// take 414 us on pairs with it and 453 with the loop at each place.
+static __device__ __noinline__ bool wait_on(uint32_t bar, uint32_t parity, long long budget, volatile uint32_t* abort,
+                                     unsigned int site) {
+  bool ok = true;
+  const long long t0 = clock64();
+  while (!mbar_try_wait(bar, parity)) {
+    if (*abort) ok = false;
+    else if (clock64() - t0 > budget) {
+      *abort = site;
+      ok = false;
+    }
+    if (!ok) break;
+  }
+  return __all_sync(0xffffffffu, ok);
+}
+__device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, const Waits& w, unsigned int site) {
+  return __all_sync(0xffffffffu, mbar_try_wait(bar, parity)) || wait_on(bar, parity, w.budget, w.abort, site);
+}
 __device__ __forceinline__ void prefetch_l2(const void* from, int bytes) {
   asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(from), "r"(bytes) : "memory");
 }

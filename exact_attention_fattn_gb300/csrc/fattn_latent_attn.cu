@@ -178,7 +178,7 @@ __global__ void __launch_bounds__(Cfg<N, R>::kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = misc[0];
   const Waits wc{args.wait_budget, reinterpret_cast<volatile uint32_t*>(&misc[1])};
-  auto wait_seg = [&](uint32_t i) { return wait_bar_warp(seg_full(i), (i / kSegs) & 1, wc, kWaitSegment); };
+  auto wait_seg = [&](uint32_t i) { return wait_warp(seg_full(i), (i / kSegs) & 1, wc, kWaitSegment); };
   auto done_seg = [&](uint32_t i) {
     __syncwarp();
     if (lane == 0) mbar_arrive(seg_empty(i));
@@ -230,9 +230,9 @@ __global__ void __launch_bounds__(Cfg<N, R>::kThreads, 1)
         const int kv0 = j * kKeys;
         const uint32_t pair0 = tiles * C::kPairs;
         uint32_t x[NW / 2];
-        fail |= !wait_bar_warp(s_full(tiles & 1), (tiles >> 1) & 1, wc, kWaitSFull);
+        fail |= !wait_warp(s_full(tiles & 1), (tiles >> 1) & 1, wc, kWaitSFull);
         // The masks came with the tile; its slots are not used again before P V.
-        fail |= !wait_bar_warp(pair_full(pair0 % C::kRing), (pair0 / C::kRing) & 1, wc, kWaitKvFull);
+        fail |= !wait_warp(pair_full(pair0 % C::kRing), (pair0 / C::kRing) & 1, wc, kWaitKvFull);
         tc_fence_after();
         tmem_ld_rows(tmem + lane_off + C::col_s(tiles & 1) + col0, x);
         const uint32_t mask = valid[tiles % kValid];
@@ -265,7 +265,7 @@ __global__ void __launch_bounds__(Cfg<N, R>::kThreads, 1)
             for (int off = 4; off < 32; off <<= 1) mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], off));
             if (lane < 4) xs[quarter * N + col_of(i)] = mx[i];
           }
-          if (j > s.a) fail |= !wait_bar_warp(pv_done, (tiles - 1) & 1, wc, kWaitMmaDone);
+          if (j > s.a) fail |= !wait_warp(pv_done, (tiles - 1) & 1, wc, kWaitMmaDone);
           if (softmax_any(fail)) {
             fail = true;
             break;
@@ -315,7 +315,7 @@ __global__ void __launch_bounds__(Cfg<N, R>::kThreads, 1)
           l[i] += p00 + p10;
           l[i + 1] += p01 + p11;
         }
-        if (tiles > 0) fail |= !wait_bar_warp(pv_done, (tiles - 1) & 1, wc, kWaitMmaDone);   // P is free
+        if (tiles > 0) fail |= !wait_warp(pv_done, (tiles - 1) & 1, wc, kWaitMmaDone);   // P is free
 #pragma unroll
         for (int i = 0; i < NW / 16; ++i) {
           const int row = col0 + 16 * i + 8 * (lane >> 4) + (lane & 7), chunk = 2 * quarter + (lane >> 3 & 1);
@@ -341,7 +341,7 @@ __global__ void __launch_bounds__(Cfg<N, R>::kThreads, 1)
         mbar_arrive(p_full);
       }
       // ---- results
-      fail |= !wait_bar_warp(pv_done, (tiles - 1) & 1, wc, kWaitOFull);
+      fail |= !wait_warp(pv_done, (tiles - 1) & 1, wc, kWaitOFull);
 #pragma unroll
       for (int i = 0; i < NC; ++i) {
 #pragma unroll
@@ -406,7 +406,7 @@ __global__ void __launch_bounds__(Cfg<N, R>::kThreads, 1)
         }
       } else {
         // 16 rows at a time, a column a lane: whole lines.
-#pragma unroll 2
+#pragma unroll 1
         for (int p = 0; p < C::kPairs * NW / 16; ++p) {
           const int pair = 16 * p / NW, r0 = col0 + 16 * p % NW;
           if (r0 >= live) continue;
@@ -444,7 +444,7 @@ __global__ void __launch_bounds__(Cfg<N, R>::kThreads, 1)
     uint32_t rs = 0, rph = 0, ks = 0, kph = 0, vs = 0;
     auto values = [&](uint32_t acc) {
       const uint64_t db = sdesc_sw128(sbase + C::kPOff, 16, 1024);
-#pragma unroll
+#pragma unroll 1
       for (int p = 0; p < C::kPairs; ++p) {
         const uint64_t da = sdesc_sw128(sbase + C::kRingOff + vs * C::kPairTile, C::kRopeTile, 1024);
 #pragma unroll
@@ -457,7 +457,7 @@ __global__ void __launch_bounds__(Cfg<N, R>::kThreads, 1)
       ++pvs;
     };
     auto run = [&](const int n) -> bool {
-      if (!wait_bar_warp(q_full, q_count++ & 1, wc, kWaitQFull)) return false;
+      if (!wait_warp(q_full, q_count++ & 1, wc, kWaitQFull)) return false;
       tc_fence_after();
       for (int i = 0; i <= n; ++i) {
         bool due = i > 0;                 // values of tile i - 1
@@ -483,7 +483,7 @@ __global__ void __launch_bounds__(Cfg<N, R>::kThreads, 1)
           }
 #pragma unroll
           for (int p = 0; p < C::kPairs; ++p) {
-            if (p > 0 && !wait_bar_warp(pair_full(ks), kph, wc, kWaitKvFull)) return false;
+            if (p > 0 && !wait_warp(pair_full(ks), kph, wc, kWaitKvFull)) return false;
             const uint32_t k = sbase + C::kRingOff + ks * C::kPairTile, q = sbase + C::kQOff + 2 * p * C::kQChunk;
             product4(d, k, q, 1u);
             product4(d, k + C::kRopeTile, q + C::kQChunk, 1u);
@@ -497,7 +497,7 @@ __global__ void __launch_bounds__(Cfg<N, R>::kThreads, 1)
           ++tiles;
         }
         if (due) {
-          if (!wait_bar_warp(p_full, pvs & 1, wc, kWaitPFull)) return false;
+          if (!wait_warp(p_full, pvs & 1, wc, kWaitPFull)) return false;
           tc_fence_after();
           values(i > 1 ? 1u : 0u);
         }
@@ -534,7 +534,7 @@ __global__ void __launch_bounds__(Cfg<N, R>::kThreads, 1)
       if (s.flags & Seg::kLast) break;
       const long long row0 = first_row(s);
       if (row0 >= rows_of(s)) continue;
-      if (q_count > 0 && !wait_bar_warp(q_empty, (q_count - 1) & 1, wc, kWaitQFull)) break;
+      if (q_count > 0 && !wait_warp(q_empty, (q_count - 1) & 1, wc, kWaitQFull)) break;
       ++q_count;
       mbar_arrive_expect_tx_w(q_full, C::kChunks * C::kQChunk);
       const int q_row = uniform(static_cast<int>(static_cast<long long>(s.r0) * args.Hq + row0));
@@ -569,7 +569,7 @@ __global__ void __launch_bounds__(Cfg<N, R>::kThreads, 1)
           if (pid1 >= 0) tma_load_3d_w(dst + part, &tm_k, bar, 64 * chunk, row, pid1);
         };
         const uint32_t rs = tiles % C::kRopes;
-        if (tiles >= C::kRopes && !wait_bar_warp(rope_empty(rs), (tiles / C::kRopes - 1) & 1, wc, kWaitKvEmpty)) {
+        if (tiles >= C::kRopes && !wait_warp(rope_empty(rs), (tiles / C::kRopes - 1) & 1, wc, kWaitKvEmpty)) {
           ok = false;
           break;
         }
@@ -578,9 +578,9 @@ __global__ void __launch_bounds__(Cfg<N, R>::kThreads, 1)
         ++ropes;
         if (lane == 0) valid[tiles % kValid] = mask;
         __syncwarp();
-#pragma unroll
+#pragma unroll 1
         for (int p = 0; p < C::kPairs; ++p) {
-          if (pairs >= C::kRing && !wait_bar_warp(pair_empty(ps), eph ^ 1u, wc, kWaitKvEmpty)) {
+          if (pairs >= C::kRing && !wait_warp(pair_empty(ps), eph ^ 1u, wc, kWaitKvEmpty)) {
             ok = false;
             break;
           }
@@ -641,7 +641,7 @@ __global__ void __launch_bounds__(Cfg<N, R>::kThreads, 1)
       } else {
         x.flags = Seg::kLast;
       }
-      if (i >= kSegs && !wait_bar_warp(seg_empty(i), (i / kSegs - 1) & 1, wc, kWaitSegment)) {
+      if (i >= kSegs && !wait_warp(seg_empty(i), (i / kSegs - 1) & 1, wc, kWaitSegment)) {
         any = false;
         break;
       }

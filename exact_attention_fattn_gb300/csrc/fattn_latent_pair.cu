@@ -156,23 +156,6 @@ __device__ __forceinline__ bool bar_done_cl(uint32_t bar, uint32_t parity) {
   return __all_sync(0xffffffffu, ok != 0);
 }
 
-// A wait on what either CTA of the pair completes, by a whole warp.
-__device__ __forceinline__ bool wait_cl(uint32_t bar, uint32_t parity, const Waits& w, unsigned int site) {
-  bool ok = true;
-  if (!mbar_try_wait(bar, parity)) {
-    const long long t0 = clock64();
-    while (!mbar_try_wait(bar, parity)) {
-      if (*w.abort) ok = false;
-      else if (clock64() - t0 > w.budget) {
-        *w.abort = site;
-        ok = false;
-      }
-      if (!ok) break;
-    }
-  }
-  return __all_sync(0xffffffffu, ok);
-}
-
 __global__ void __launch_bounds__(kThreads, 1)
     pair_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_q,
                 const __grid_constant__ LatentAttnArgs args) {
@@ -225,7 +208,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = misc[0];
   const Waits wc{args.wait_budget, misc + 1};
   auto uniform = [](int v) { return __shfl_sync(0xffffffffu, v, 0); };
-  auto wait_seg = [&](uint32_t i) { return wait_cl(bar(C::kSegFull + i % kSegs), (i / kSegs) & 1, wc, kWaitSegment); };
+  auto wait_seg = [&](uint32_t i) { return wait_warp(bar(C::kSegFull + i % kSegs), (i / kSegs) & 1, wc, kWaitSegment); };
   auto done_seg = [&](uint32_t i) {
     __syncwarp();
     if (lane == 0) mbar_arrive(bar(C::kSegEmpty + i % kSegs));
@@ -248,7 +231,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto sync = [&]() -> bool {
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(C::kSync));
-      return wait_cl(bar(C::kSync), syncs++ & 1, wc, kWaitDrain);
+      return wait_warp(bar(C::kSync), syncs++ & 1, wc, kWaitDrain);
     };
     // The rows' combined numbers of this CTA's keys (in own[0], own[1]) to the other.
     auto exchange = [&](bool sums) -> bool {
@@ -260,7 +243,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                      __float_as_uint(sums ? x + y : fmaxf(x, y)), map_shared(bar(b), peer));
       }
       if (tid == 0) mbar_arrive_expect_tx(bar(b), kRows * 4);
-      return wait_cl(bar(b), exchanges++ >> 1 & 1, wc, kWaitDrain);
+      return wait_warp(bar(b), exchanges++ >> 1 & 1, wc, kWaitDrain);
     };
     for (uint32_t si = 0; wait_seg(si); ++si) {
       const Seg s = seg_at(si);
@@ -288,13 +271,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int j = s.a; j < s.e; ++j, ++tiles) {
         const int kv0 = j * kKeys, mine0 = kv0 + kHalfKeys * static_cast<int>(rank);
         const bool first = j == s.a;
-        if (!(ok = wait_cl(bar(C::kSFull + (tiles & 1)), (tiles >> 1) & 1, wc, kWaitSFull))) break;
+        if (!(ok = wait_warp(bar(C::kSFull + (tiles & 1)), (tiles >> 1) & 1, wc, kWaitSFull))) break;
         tc_fence_after();
         uint32_t lo[16], hi[16];           // keys of lanes 0-15 and 16-31 of the quarter
         const uint32_t ts = tmem + lane_off + C::col_s(tiles & 1) + cols;
         tmem_ld_rows(ts, lo);
         tmem_ld_rows(ts + (16u << 16), hi);
-        if (!(ok = wait_cl(bar(C::kMask + tiles % C::kValid), (tiles / C::kValid) & 1, wc, kWaitKvFull))) break;
+        if (!(ok = wait_warp(bar(C::kMask + tiles % C::kValid), (tiles / C::kValid) & 1, wc, kWaitKvFull))) break;
         const uint32_t mask = misc[4 + tiles % C::kValid];
         tmem_ld_wait(lo);
         tmem_ld_wait(hi);
@@ -374,10 +357,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           compute();
           if (home != rank) transpose();
         }
-        if (!(ok = wait_cl(bar(C::kVote + turn), (tiles >> 1) & 1, wc, kWaitPFull))) break;
+        if (!(ok = wait_warp(bar(C::kVote + turn), (tiles >> 1) & 1, wc, kWaitPFull))) break;
         const bool moved = misc[2 + turn] == tiles + 1 || __any_sync(0xffffffffu, peer_votes[8 * turn + (lane & 7)] != 0u);
         // This CTA's keys' place in P is free.
-        if (!first && !(ok = wait_cl(bar(C::kPvDone + rank), (tiles - 1) & 1, wc, kWaitMmaDone))) break;
+        if (!first && !(ok = wait_warp(bar(C::kPvDone + rank), (tiles - 1) & 1, wc, kWaitMmaDone))) break;
         if (moved) {
           // ---- in both CTAs: some row's reference may move
 #pragma unroll
@@ -401,7 +384,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           if (!(ok = sync())) break;
           if (!first) {
-            if (!(ok = wait_cl(bar(C::kPvDone + peer), (tiles - 1) & 1, wc, kWaitMmaDone))) break;
+            if (!(ok = wait_warp(bar(C::kPvDone + peer), (tiles - 1) & 1, wc, kWaitMmaDone))) break;
             tc_fence_after();
 #pragma unroll 1
             for (int p = 0; p < C::kBlocks * 4; ++p) {
@@ -428,7 +411,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (edge) {
             // Slots behind the end and pages that do not exist hold anything, and zero times a
             // NaN is a NaN.
-            if (!(ok = wait_cl(bar(C::kOther + turn), (tiles >> 1) & 1, wc, kWaitKvFull))) break;
+            if (!(ok = wait_warp(bar(C::kOther + turn), (tiles >> 1) & 1, wc, kWaitKvFull))) break;
 #pragma unroll 1
             for (int id = tid; id < 2 * C::kBlocks * 2 * kHalfKeys * 8; id += 32 * kSoftmaxWarps) {
               const int r = id >> 3 & (kHalfKeys - 1), half = id >> 9;      // half pairs, 64 rows of 8 pieces each
@@ -471,7 +454,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (!ok) break;
       // ---- results: this CTA's half of the columns, for all rows
-      if (!wait_cl(bar(C::kPvDone), (tiles - 1) & 1, wc, kWaitOFull) || !wait_cl(bar(C::kPvDone + 1), (tiles - 1) & 1, wc, kWaitOFull))
+      if (!wait_warp(bar(C::kPvDone), (tiles - 1) & 1, wc, kWaitOFull) || !wait_warp(bar(C::kPvDone + 1), (tiles - 1) & 1, wc, kWaitOFull))
         break;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
@@ -535,7 +518,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       } else {
-#pragma unroll 2
+#pragma unroll 1
         for (int p = 0; p < C::kBlocks * 4; ++p) {
           const int r0 = 64 * (warp >> 2) + 16 * (p & 3);
           if (r0 >= live) continue;
@@ -566,7 +549,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto prob_there = [&](int h) { return ready(C::kProb + h, pvs & 1) && ready(C::kProbPeer + h, pvs & 1); };
     auto values = [&](int h, uint32_t acc) -> bool {
       // (P is there, part of it by the other CTA's stores)
-      if (!wait_cl(bar(C::kOtherBoth + (pvs & 1)), (pvs >> 1) & 1, wc, kWaitKvFull)) return false;
+      if (!wait_warp(bar(C::kOtherBoth + (pvs & 1)), (pvs >> 1) & 1, wc, kWaitKvFull)) return false;
       fence_proxy_async_smem();
       tc_fence_after();
       const uint64_t db = sdesc_sw128(sbase + C::kPOff + h * C::kChunk, 16, 1024);
@@ -584,7 +567,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       return true;
     };
     auto run = [&](const int n) -> bool {
-      if (!wait_cl(bar(C::kQFull), q_count++ & 1, wc, kWaitQFull)) return false;
+      if (!wait_warp(bar(C::kQFull), q_count++ & 1, wc, kWaitQFull)) return false;
       tc_fence_after();
       for (int i = 0; i <= n; ++i) {
         int due = i > 0 ? 0 : 2;          // next product with the values of tile i - 1
@@ -625,8 +608,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           ++tiles;
         }
         for (; due < 2; ++due) {
-          if (!wait_cl(bar(C::kProb + due), pvs & 1, wc, kWaitPFull) ||
-              !wait_cl(bar(C::kProbPeer + due), pvs & 1, wc, kWaitPFull) || !values(due, i > 1 || due > 0 ? 1u : 0u))
+          if (!wait_warp(bar(C::kProb + due), pvs & 1, wc, kWaitPFull) ||
+              !wait_warp(bar(C::kProbPeer + due), pvs & 1, wc, kWaitPFull) || !values(due, i > 1 || due > 0 ? 1u : 0u))
             return false;
         }
       }
@@ -644,7 +627,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       } else {
         // This CTA's P, told to the leader.
         bool ok = true;
-        for (int i = 0; i < 2 * n && (ok = wait_cl(bar(C::kProb + (i & 1)), pvs & 1, wc, kWaitPFull)); ++i) {
+        for (int i = 0; i < 2 * n && (ok = wait_warp(bar(C::kProb + (i & 1)), pvs & 1, wc, kWaitPFull)); ++i) {
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) mbar_arrive_cluster_relaxed(map_shared(bar(C::kProbPeer + (i & 1)), 0));
@@ -673,7 +656,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const long long row0 = first_row(s);
       if (row0 >= rows_of(s)) continue;
       if (warp == kLoadWarp) {
-        if (q_count > 0 && !wait_cl(bar(C::kQEmpty), (q_count - 1) & 1, wc, kWaitQFull)) break;
+        if (q_count > 0 && !wait_warp(bar(C::kQEmpty), (q_count - 1) & 1, wc, kWaitQFull)) break;
         ++q_count;
         if (leader) mbar_arrive_expect_tx_w(bar(C::kQFull), 2 * C::kQBytes);
         tma2_load_3d_w(sbase + C::kQOff, &tm_q, map_shared(bar(C::kQFull), 0), 0,
@@ -708,15 +691,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             tma2_load_3d_w(dst, &tm_k, b, col, row, pid0);
             if (boxes == 2) tma2_load_3d_w(dst + 4096, &tm_k, b, col, row, pid1);
           };
-          if (tiles > 0 && !wait_cl(bar(C::kRopeEmpty), (tiles - 1) & 1, wc, kWaitKvEmpty)) {
+          if (tiles > 0 && !wait_warp(bar(C::kRopeEmpty), (tiles - 1) & 1, wc, kWaitKvEmpty)) {
             ok = false;
             break;
           }
           if (leader) mbar_arrive_expect_tx_w(bar(C::kRopeFull), 2 * C::kChunk);
           load64(sbase + C::kRopeOff, map_shared(bar(C::kRopeFull), 0), kRank);
-#pragma unroll
+#pragma unroll 1
           for (int p = 0; p < C::kPairs; ++p) {
-            if (pairs >= C::kRing && !wait_cl(bar(C::kEmpty + ps), eph ^ 1u, wc, kWaitKvEmpty)) {
+            if (pairs >= C::kRing && !wait_warp(bar(C::kEmpty + ps), eph ^ 1u, wc, kWaitKvEmpty)) {
               ok = false;
               break;
             }
@@ -765,7 +748,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           pid0 = good(pid0) ? pid0 : 0;
           pid1 = good(pid1) ? pid1 : 0;
           const uint32_t b = bar(C::kOther + (tiles & 1));
-          if (!wait_cl(bar(C::kSFull + (tiles & 1)), (tiles >> 1) & 1, wc, kWaitSFull)) {
+          if (!wait_warp(bar(C::kSFull + (tiles & 1)), (tiles >> 1) & 1, wc, kWaitSFull)) {
             ok = false;
             break;
           }
@@ -778,7 +761,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             tma_load_3d_w(dst, &tm_k, b, col, row, pid0);
             if (boxes == 2) tma_load_3d_w(dst + 4096, &tm_k, b, col, row, pid1);
           }
-          if (!wait_cl(b, (tiles >> 1) & 1, wc, kWaitKvFull)) {
+          if (!wait_warp(b, (tiles >> 1) & 1, wc, kWaitKvFull)) {
             ok = false;
             break;
           }
@@ -804,7 +787,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       } else {
         x.flags = Seg::kLast;
       }
-      if (i >= kSegs && !wait_cl(bar(C::kSegEmpty + i % kSegs), (i / kSegs - 1) & 1, wc, kWaitSegment)) {
+      if (i >= kSegs && !wait_warp(bar(C::kSegEmpty + i % kSegs), (i / kSegs - 1) & 1, wc, kWaitSegment)) {
         any = false;
         break;
       }
