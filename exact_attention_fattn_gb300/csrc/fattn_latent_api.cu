@@ -75,12 +75,13 @@ CacheSeqs seqs_of(const int* page_table, const int* q_start, const int* kv_len, 
 // Blocks of 128 rows on pairs of CTAs are for large calls of rank 512 (`reach`: keys
 // that a sequence's table has room for; what they really are is on the device), a call
 // in us on pairs and on single CTAs, 128 heads, one token a sequence:
-//   64 of 2000 keys: 69 / 76    48 of 4000: 81 / 92    16 of 8000: 59 / 64
-//   below 1024 keys a pair:   16 of 1000: 28 / 24   48 of 300: 33 / 31   4 of 2000: 23 / 21
+//   64 of 2000 keys: 64 / 76    48 of 4000: 78 / 93    16 of 8000: 53 / 64
+//   128 tokens of 64 heads on 4000: 82 / 103    8 tokens of 16 heads, 16 of 4000: 40 / 42
+//   below 800 keys a pair:   16 of 1000: 27 / 24   48 of 300: 28 / 28   4 of 2000: 23 / 20
 //   rows not a multiple of 128 (32 sequences of 4000 keys, 64 heads, so many tokens):
-//     3: 99 / 91   5: 137 / 136   7: 168 / 182   9: 202 / 246
-//   rank 256, whose products leave the exchange between the two CTAs no room:
-//     32 of 8000: 67 / 65   16 of 8000: 44 / 39   16 of 1000: 22 / 17
+//     3: 92 / 92   5: 126 / 137   7: 157 / 184   9: 189 / 246
+// For rank 256, half the products a tile, they were built and gain little, and only in the
+// largest calls (32 of 8000: 61 / 63   64 of 2000: 47 / 45   16 of 1000: 22 / 17).
 // Both need the same workspace, so that its size does not depend on the reach.
 struct Layout {
   int rows, span;
@@ -90,8 +91,8 @@ Layout layout_of(int T, int B, int Hq, int rank, long long reach) {
   const long long pairs = (halves + 1) / 2;                       // blocks of 128 rows
   Layout l;
   l.rows = all <= 16 ? 16 : (all <= 32 ? 32 : 64);
-  if (rank == kLatentPairRank && (halves % 2 == 0 || halves >= 7) &&
-      static_cast<double>(B) * static_cast<double>(pairs) * static_cast<double>(reach) >= 1024. * (kSms / 2))
+  if (rank == kLatentPairRank && (halves % 2 == 0 || halves >= 5) &&
+      static_cast<double>(B) * static_cast<double>(pairs) * static_cast<double>(reach) >= 800. * (kSms / 2))
     l.rows = kLatentPairRows;
   const long long blocks = (all + l.rows - 1) / l.rows, groups = (blocks + kMaxSpan - 1) / kMaxSpan;
   l.span = static_cast<int>((blocks + groups - 1) / groups);

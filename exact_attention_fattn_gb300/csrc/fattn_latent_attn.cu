@@ -31,8 +31,8 @@
 // Bound: the cache's bytes for 16 and 32 rows, shared memory for 64, whose 1920 cycles of
 // products a 64-key tile (rank 512) are reads at 128 bytes a cycle, beside 576 for the
 // tile's way in.  Measured, rank 512, one new token each: 64 sequences of 500 to 8000 keys, 16 heads
-// 64.5 us (0.75 of the measured copy rate), 32 heads 75, 64 heads 81; 3 of 100000 to
-// 131071, 32 heads 84 (0.71); one of 1000, 16 heads 12.0, of which the two launches, the
+// 61.5 us (0.78 of the measured copy rate), 32 heads 68, 64 heads 80; 3 of 100000 to
+// 131071, 32 heads 75.5 (0.79); one of 1000, 16 heads 12.0, of which the two launches, the
 // schedule and the join are nearly all.  Products are issued in a fixed order by converged
 // code: under branches that the compiler takes for divergent each took 82 cycles (64
 // sequences of 128 heads 178 us, then 152; copies under a lane's branch, 190 cycles each,

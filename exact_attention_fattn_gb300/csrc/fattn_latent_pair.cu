@@ -27,13 +27,15 @@
 // thread has stored (votes and P by plain remote stores and releases took 5500 cycles
 // a tile, 2500 of them waiting for the votes).
 //
-// Measured: 2 pieces of 1024 tokens, 16 heads, before keys up to 8192: 467 us (64 rows a CTA:
-// 614), 1070 TFLOP/s; 64 single tokens of 128 heads over 500 to 8000 keys 101 (120).  A tile
-// takes 4100 cycles in the first.  Neither the products bound it (with a quarter of
-// their columns 459) nor L2 (two pairs a cluster with one copy of the keys for both 512)
-// nor the softmax (16 warps 477): a tile's slots are free only after its second product,
-// and from there copies, scores, softmax and the way of P to the other CTA follow one another
-// with two tiles in turn, which is all that fits beside Q.
+// Measured: 2 pieces of 1024 tokens, 16 heads, before keys up to 8192: 414 us (64 rows a CTA:
+// 570), 1205 TFLOP/s; 64 single tokens of 128 heads over 500 to 8000 keys 98 (123).  A tile
+// takes 3800 cycles in the first, 1750 of them issue of the products.  When it took 467 us
+// neither the products bound it (with a quarter of their columns 459) nor L2 (two pairs a
+// cluster with one copy of the keys for both 512) nor the softmax (16 warps 477): a tile's
+// slots are free only after its second product, and from there copies, scores, softmax and
+// the way of P to the other CTA follow one another with two tiles in turn, which is all that
+// fits beside Q.  Less code in that chain is what helped (waits that stand once, copies'
+// loops rolled): the roles share the instruction caches.
 //
 // Work split and join as in fattn_latent_attn.cu, a pair in a CTA's place.
 //
