@@ -27,8 +27,8 @@
 // thread has stored (votes and P by plain remote stores and releases took 5500 cycles
 // a tile, 2500 of them waiting for the votes).
 //
-// Measured: 2 pieces of 1024 tokens, 16 heads, before keys up to 8192: 414 us (64 rows a CTA:
-// 570), 1205 TFLOP/s; 64 single tokens of 128 heads over 500 to 8000 keys 98 (123).  A tile
+// Measured: 2 pieces of 1024 tokens, 16 heads, before keys up to 8192: 417 us (64 rows a CTA:
+// 570), 1195 TFLOP/s; 64 single tokens of 128 heads over 500 to 8000 keys 98 (123).  A tile
 // takes 3800 cycles in the first, 1750 of them issue of the products.  When it took 467 us
 // neither the products bound it (with a quarter of their columns 459) nor L2 (two pairs a
 // cluster with one copy of the keys for both 512) nor the softmax (16 warps 477): a tile's
@@ -142,20 +142,26 @@ __device__ __forceinline__ uint32_t movmatrix_trans(uint32_t x) {
   return y;
 }
 
-// bar_done for what either CTA completes.  Acquired at the CTA's scope, as what the barriers of
-// this kernel order is read from this CTA's own shared memory, or by the tensor
-// core (at the cluster's scope: 483 us instead of 467 for two pieces of 1024 tokens, 16 heads,
-// before keys up to 8192).
-__device__ __forceinline__ bool bar_done_cl(uint32_t bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.test_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(bar), "r"(parity)
-      : "memory");
-  return __all_sync(0xffffffffu, ok != 0);
+// wait_warp for what the other CTA has stored and this one loads: votes, maxima and sums.  The
+// other waits acquire at the CTA's scope: what they order is this CTA's own, or read by the
+// tensor core after copies and stores that count on the barrier themselves.  All at the
+// cluster's: 422 us for two pieces of 1024 tokens, 16 heads, before keys up to 8192, so 417.
+__device__ __noinline__ bool wait_on_pair(uint32_t bar, uint32_t parity, long long budget, volatile uint32_t* abort,
+                                          unsigned int site) {
+  bool ok = true;
+  const long long t0 = clock64();
+  while (!mbar_try_wait_cl(bar, parity)) {
+    if (*abort) ok = false;
+    else if (clock64() - t0 > budget) {
+      *abort = site;
+      ok = false;
+    }
+    if (!ok) break;
+  }
+  return __all_sync(0xffffffffu, ok);
+}
+__device__ __forceinline__ bool wait_pair(uint32_t bar, uint32_t parity, const Waits& w, unsigned int site) {
+  return __all_sync(0xffffffffu, mbar_try_wait_cl(bar, parity)) || wait_on_pair(bar, parity, w.budget, w.abort, site);
 }
 
 __global__ void __launch_bounds__(kThreads, 1)
@@ -245,7 +251,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                      __float_as_uint(sums ? x + y : fmaxf(x, y)), map_shared(bar(b), peer));
       }
       if (tid == 0) mbar_arrive_expect_tx(bar(b), kRows * 4);
-      return wait_warp(bar(b), exchanges++ >> 1 & 1, wc, kWaitDrain);
+      return wait_pair(bar(b), exchanges++ >> 1 & 1, wc, kWaitDrain);
     };
     for (uint32_t si = 0; wait_seg(si); ++si) {
       const Seg s = seg_at(si);
@@ -359,7 +365,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           compute();
           if (home != rank) transpose();
         }
-        if (!(ok = wait_warp(bar(C::kVote + turn), (tiles >> 1) & 1, wc, kWaitPFull))) break;
+        if (!(ok = wait_pair(bar(C::kVote + turn), (tiles >> 1) & 1, wc, kWaitPFull))) break;
         const bool moved = misc[2 + turn] == tiles + 1 || __any_sync(0xffffffffu, peer_votes[8 * turn + (lane & 7)] != 0u);
         // This CTA's keys' place in P is free.
         if (!first && !(ok = wait_warp(bar(C::kPvDone + rank), (tiles - 1) & 1, wc, kWaitMmaDone))) break;
@@ -541,7 +547,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr uint32_t idesc_o = idesc_bf16_f32(256, kRows, true, false);
     uint32_t tiles = 0, pvs = 0, q_count = 0;
     uint32_t ks = 0, kph = 0, vs = 0;   // slots and phases, as in the kernel for 64 rows
-    auto ready = [&](int b, uint32_t parity) { return bar_done_cl(bar(b), parity); };
+    auto ready = [&](int b, uint32_t parity) { return bar_done(bar(b), parity); };
     auto product4 = [&](uint32_t d, uint32_t a, uint32_t b, uint32_t acc) {
       const uint64_t da = sdesc_sw128(a, 16, 1024), db = sdesc_sw128(b, 16, 1024);
 #pragma unroll
