@@ -40,7 +40,7 @@
 //
 // Warps: 0-3 softmax and results (0-7 with 64 rows, half of them each), then one for
 // tensor memory and MMA issue, one for loads, one for the walk over the share (it
-// publishes one segment after the other) and an idle one.
+// publishes one segment after the other) and one for the loads of a tile's second page.
 // TMEM: S at N (tile & 1), O^T at 2 N + N block.
 #include "fattn_latent.cuh"
 
@@ -61,8 +61,9 @@ struct Cfg {
   static constexpr int kMmaWarp = 4 * kHalves;
   static constexpr int kLoadWarp = kMmaWarp + 1;
   static constexpr int kWalkWarp = kMmaWarp + 2;
+  static constexpr int kLoad2Warp = kMmaWarp + 3;
   static constexpr int kThreads = 32 * (kMmaWarp + 4);
-  static constexpr int kSegReaders = 4 * kHalves + 2;
+  static constexpr int kSegReaders = 4 * kHalves + 3;
   static constexpr int kChunks = R / 64 + 1;         // 64-column parts of a query; the rotated one last
   static constexpr int kPairs = R / 128;             // 128-column parts of a cached row
   static constexpr int kQChunk = N * 128;
@@ -128,6 +129,7 @@ __global__ void __launch_bounds__(Cfg<N, R>::kThreads, 1)
                   const __grid_constant__ LatentAttnArgs args) {
   using C = Cfg<N, R>;
   constexpr int kThreads = C::kThreads, kMmaWarp = C::kMmaWarp, kLoadWarp = C::kLoadWarp, kWalkWarp = C::kWalkWarp;
+  constexpr int kLoad2Warp = C::kLoad2Warp;
   extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t sbase = smem_u32(smem);
   const uint32_t bar0 = sbase + C::kBarOff;
@@ -516,12 +518,15 @@ __global__ void __launch_bounds__(Cfg<N, R>::kThreads, 1)
     commit_lead(mma_done, lead);
     mbar_wait_drain(mma_done, 0);
     __syncwarp();
-  } else if (warp == kLoadWarp) {
+  } else if (warp == kLoadWarp || warp == kLoad2Warp) {
     // ================================================================ TMA producer
     // Copies are issued by the converged warp, one lane of it elected by each: under a
     // branch on the lane their issue takes longer (190 cycles instead of 110), as
     // an MMA's does.  A block's queries are one copy; the cache's come 64 columns a
     // copy (128 a copy: prompt piece 629 us, 64: 611).
+    // Where a tile has two pages, the second warp loads the second one (pages of 32
+    // tokens: 64 sequences of 500 to 8000 keys, 16 heads FIG1, by one warp 65.5).
+    const bool second = warp == kLoad2Warp;
     uint32_t tiles = 0, q_count = 0;
     uint32_t ropes = 0, pairs = 0;        // asked for so far
     uint32_t ps = 0, eph = 0;             // the next pair's slot, and the turn of the ring
@@ -533,12 +538,14 @@ __global__ void __launch_bounds__(Cfg<N, R>::kThreads, 1)
       done_seg(si);
       if (s.flags & Seg::kLast) break;
       const long long row0 = first_row(s);
-      if (row0 >= rows_of(s)) continue;
-      if (q_count > 0 && !wait_warp(q_empty, (q_count - 1) & 1, wc, kWaitQFull)) break;
-      ++q_count;
-      mbar_arrive_expect_tx_w(q_full, C::kChunks * C::kQChunk);
-      const int q_row = uniform(static_cast<int>(static_cast<long long>(s.r0) * args.Hq + row0));
-      tma_load_3d_w(sbase + C::kQOff, &tm_q, q_full, 0, q_row, 0);
+      if (row0 >= rows_of(s) || (second && boxes == 1)) continue;
+      if (!second) {
+        if (q_count > 0 && !wait_warp(q_empty, (q_count - 1) & 1, wc, kWaitQFull)) break;
+        ++q_count;
+        mbar_arrive_expect_tx_w(q_full, C::kChunks * C::kQChunk);
+        const int q_row = uniform(static_cast<int>(static_cast<long long>(s.r0) * args.Hq + row0));
+        tma_load_3d_w(sbase + C::kQOff, &tm_q, q_full, 0, q_row, 0);
+      }
       // 32 of the table's entries, one a lane, and the next 32 on their way.
       const int first_tile = uniform(s.a), last_tile = uniform(s.e);
       int base = (first_tile * kKeys) >> args.page_shift;
@@ -555,7 +562,7 @@ __global__ void __launch_bounds__(Cfg<N, R>::kThreads, 1)
         int pid0 = page_at(first), pid1 = boxes == 2 ? page_at(first + 1) : -1;
         if (pid0 >= args.pages || pid1 >= args.pages || (pid0 < 0 && j * kKeys < s.len) ||
             (boxes == 2 && pid1 < 0 && j * kKeys + box < s.len)) {
-          if (lane == 0) record_bad_index(args.status, kSitePage);
+          if (lane == 0 && !second) record_bad_index(args.status, kSitePage);
           if (pid0 >= args.pages) pid0 = -1;
           if (pid1 >= args.pages) pid1 = -1;
         }
@@ -563,20 +570,20 @@ __global__ void __launch_bounds__(Cfg<N, R>::kThreads, 1)
         const int row = (j * kKeys) & (page - 1);
         const uint32_t part = static_cast<uint32_t>(box) * 128u;
         const uint32_t bytes = (pid0 >= 0 ? part : 0u) + (pid1 >= 0 ? part : 0u);
-        // A chunk of 64 columns, from two pages where they have 32 tokens.
+        // A chunk of 64 columns, from this warp's page.
+        const int pid = second ? pid1 : pid0;
         auto load64 = [&](uint32_t dst, uint32_t bar, int chunk) {
-          if (pid0 >= 0) tma_load_3d_w(dst, &tm_k, bar, 64 * chunk, row, pid0);
-          if (pid1 >= 0) tma_load_3d_w(dst + part, &tm_k, bar, 64 * chunk, row, pid1);
+          if (pid >= 0) tma_load_3d_w(dst + (second ? part : 0u), &tm_k, bar, 64 * chunk, row, pid);
         };
         const uint32_t rs = tiles % C::kRopes;
         if (tiles >= C::kRopes && !wait_warp(rope_empty(rs), (tiles / C::kRopes - 1) & 1, wc, kWaitKvEmpty)) {
           ok = false;
           break;
         }
-        mbar_arrive_expect_tx_w(rope_full(rs), bytes);
+        if (!second) mbar_arrive_expect_tx_w(rope_full(rs), bytes);
         load64(sbase + C::kRopeOff + rs * C::kRopeTile, rope_full(rs), R / 64);
         ++ropes;
-        if (lane == 0) valid[tiles % kValid] = mask;
+        if (lane == 0 && !second) valid[tiles % kValid] = mask;
         __syncwarp();
 #pragma unroll 1
         for (int p = 0; p < C::kPairs; ++p) {
@@ -585,7 +592,7 @@ __global__ void __launch_bounds__(Cfg<N, R>::kThreads, 1)
             break;
           }
           const uint32_t dst = sbase + C::kRingOff + ps * C::kPairTile;
-          mbar_arrive_expect_tx_w(pair_full(ps), 2 * bytes);
+          if (!second) mbar_arrive_expect_tx_w(pair_full(ps), 2 * bytes);
           load64(dst, pair_full(ps), 2 * p);
           load64(dst + C::kRopeTile, pair_full(ps), 2 * p + 1);
           ++pairs;
@@ -600,7 +607,7 @@ __global__ void __launch_bounds__(Cfg<N, R>::kThreads, 1)
         // 68.7 three).  With 64 rows it gains 2 % where a sequence has one block, but its code
         // costs 4 % where it has several (32 sequences of 4000 keys, 160 rows: 92 and 88).
         if constexpr (N < 64) {
-          if (j + 1 < last_tile) {
+          if (!second && j + 1 < last_tile) {
             const int key = (j + 1) * kKeys;
             auto page_ahead = [&](int k) {
               const int at = (k >> args.page_shift) - base;
@@ -620,12 +627,19 @@ __global__ void __launch_bounds__(Cfg<N, R>::kThreads, 1)
         }
       }
     }
-    // Every copy this warp started must have landed before the CTA exits.
-    for (uint32_t r = ropes > C::kRopes ? ropes - C::kRopes : 0; r < ropes; ++r)
-      mbar_wait_drain(rope_full(r % C::kRopes), (r / C::kRopes) & 1);
-    for (uint32_t r = pairs > C::kRing ? pairs - C::kRing : 0; r < pairs; ++r)
-      mbar_wait_drain(pair_full(r % C::kRing), (r / C::kRing) & 1);
-    if (q_count > 0) mbar_wait_drain(q_full, (q_count - 1) & 1);
+    // Every copy must have landed before the CTA exits.  Where a wait ran out, the two warps may
+    // have asked for different tiles; then the copies are given half a millisecond,
+    // hundreds of times what one takes.
+    const Waits drain{kDrainCycles, wc.abort};
+    bool landed = true;
+    for (uint32_t r = ropes > C::kRopes ? ropes - C::kRopes : 0; landed && r < ropes; ++r)
+      landed = wait_warp(rope_full(r % C::kRopes), (r / C::kRopes) & 1, drain, kWaitDrain);
+    for (uint32_t r = pairs > C::kRing ? pairs - C::kRing : 0; landed && r < pairs; ++r)
+      landed = wait_warp(pair_full(r % C::kRing), (r / C::kRing) & 1, drain, kWaitDrain);
+    if (landed && q_count > 0) landed = wait_warp(q_full, (q_count - 1) & 1, drain, kWaitDrain);
+    if (!landed)
+      for (const long long t0 = clock64(); clock64() - t0 < (1 << 20);) {
+      }
     __syncwarp();
   } else if (warp == kWalkWarp) {
     // ================================================================ schedule
