@@ -31,8 +31,8 @@
 // Bound: the cache's bytes for 16 and 32 rows, shared memory for 64, whose 1920 cycles of
 // products a 64-key tile (rank 512) are reads at 128 bytes a cycle, beside 576 for the
 // tile's way in.  Measured, rank 512, one new token each: 64 sequences of 500 to 8000 keys, 16 heads
-// 61.5 us (0.78 of the measured copy rate), 32 heads 68, 64 heads 80; 3 of 100000 to
-// 131071, 32 heads 75.5 (0.79); one of 1000, 16 heads 12.0, of which the two launches, the
+// 62 us (0.78 of the measured copy rate), 32 heads 68, 64 heads 78.5; 3 of 100000 to
+// 131071, 32 heads 75.7 (0.79); one of 1000, 16 heads 12.0, of which the two launches, the
 // schedule and the join are nearly all.  Products are issued in a fixed order by converged
 // code: under branches that the compiler takes for divergent each took 82 cycles (64
 // sequences of 128 heads 178 us, then 152; copies under a lane's branch, 190 cycles each,
@@ -63,7 +63,7 @@ struct Cfg {
   static constexpr int kWalkWarp = kMmaWarp + 2;
   static constexpr int kLoad2Warp = kMmaWarp + 3;
   static constexpr int kThreads = 32 * (kMmaWarp + 4);
-  static constexpr int kSegReaders = 4 * kHalves + 3;
+  static constexpr int kSegReaders = 4 * kHalves + 2;   // and one more for pages of 32 tokens
   static constexpr int kChunks = R / 64 + 1;         // 64-column parts of a query; the rotated one last
   static constexpr int kPairs = R / 128;             // 128-column parts of a cached row
   static constexpr int kQChunk = N * 128;
@@ -161,7 +161,7 @@ __global__ void __launch_bounds__(Cfg<N, R>::kThreads, 1)
   const SeqCheck mine(args.s, tid);
   if (tid < C::kNumBars) {
     const uint32_t bar = bar0 + 8u * tid;
-    mbar_init(bar, bar == p_full ? C::kSoftmax : (bar >= seg_empty(0) ? C::kSegReaders : 1));
+    mbar_init(bar, bar == p_full ? C::kSoftmax : (bar >= seg_empty(0) ? C::kSegReaders + (args.page_shift == 5 ? 1 : 0) : 1));
     fence_barrier_init();
   }
   if (tid == C::kNumBars) misc[1] = 0u;
@@ -189,6 +189,23 @@ __global__ void __launch_bounds__(Cfg<N, R>::kThreads, 1)
   // blocks' padding below 2^10).
   auto first_row = [&](const Seg& s) { return static_cast<long long>(s.rg) * group_rows + block * N; };
   auto rows_of = [&](const Seg& s) { return static_cast<long long>(s.n) * args.Hq; };
+
+  // Every copy must have landed before the CTA exits.  Where a wait ran out, the two warps that
+  // load may have asked for different tiles; then the copies are given half a
+  // millisecond, hundreds of times what one takes.
+  auto land = [&](uint32_t ropes, uint32_t pairs, uint32_t q_count) {
+    const Waits drain{kDrainCycles, wc.abort};
+    bool landed = true;
+    for (uint32_t r = ropes > C::kRopes ? ropes - C::kRopes : 0; landed && r < ropes; ++r)
+      landed = wait_warp(rope_full(r % C::kRopes), (r / C::kRopes) & 1, drain, kWaitDrain);
+    for (uint32_t r = pairs > C::kRing ? pairs - C::kRing : 0; landed && r < pairs; ++r)
+      landed = wait_warp(pair_full(r % C::kRing), (r / C::kRing) & 1, drain, kWaitDrain);
+    if (landed && q_count > 0) landed = wait_warp(q_full, (q_count - 1) & 1, drain, kWaitDrain);
+    if (!landed)
+      for (const long long t0 = clock64(); clock64() - t0 < (1 << 20);) {
+      }
+    __syncwarp();
+  };
 
   if (warp < kMmaWarp) {
     // ================================================================ softmax
@@ -518,15 +535,12 @@ __global__ void __launch_bounds__(Cfg<N, R>::kThreads, 1)
     commit_lead(mma_done, lead);
     mbar_wait_drain(mma_done, 0);
     __syncwarp();
-  } else if (warp == kLoadWarp || warp == kLoad2Warp) {
+  } else if (warp == kLoadWarp) {
     // ================================================================ TMA producer
     // Copies are issued by the converged warp, one lane of it elected by each: under a
     // branch on the lane their issue takes longer (190 cycles instead of 110), as
     // an MMA's does.  A block's queries are one copy; the cache's come 64 columns a
     // copy (128 a copy: prompt piece 629 us, 64: 611).
-    // Where a tile has two pages, the second warp loads the second one (pages of 32
-    // tokens: 64 sequences of 500 to 8000 keys, 16 heads FIG1, by one warp 65.5).
-    const bool second = warp == kLoad2Warp;
     uint32_t tiles = 0, q_count = 0;
     uint32_t ropes = 0, pairs = 0;        // asked for so far
     uint32_t ps = 0, eph = 0;             // the next pair's slot, and the turn of the ring
@@ -538,14 +552,12 @@ __global__ void __launch_bounds__(Cfg<N, R>::kThreads, 1)
       done_seg(si);
       if (s.flags & Seg::kLast) break;
       const long long row0 = first_row(s);
-      if (row0 >= rows_of(s) || (second && boxes == 1)) continue;
-      if (!second) {
-        if (q_count > 0 && !wait_warp(q_empty, (q_count - 1) & 1, wc, kWaitQFull)) break;
-        ++q_count;
-        mbar_arrive_expect_tx_w(q_full, C::kChunks * C::kQChunk);
-        const int q_row = uniform(static_cast<int>(static_cast<long long>(s.r0) * args.Hq + row0));
-        tma_load_3d_w(sbase + C::kQOff, &tm_q, q_full, 0, q_row, 0);
-      }
+      if (row0 >= rows_of(s)) continue;
+      if (q_count > 0 && !wait_warp(q_empty, (q_count - 1) & 1, wc, kWaitQFull)) break;
+      ++q_count;
+      mbar_arrive_expect_tx_w(q_full, C::kChunks * C::kQChunk);
+      const int q_row = uniform(static_cast<int>(static_cast<long long>(s.r0) * args.Hq + row0));
+      tma_load_3d_w(sbase + C::kQOff, &tm_q, q_full, 0, q_row, 0);
       // 32 of the table's entries, one a lane, and the next 32 on their way.
       const int first_tile = uniform(s.a), last_tile = uniform(s.e);
       int base = (first_tile * kKeys) >> args.page_shift;
@@ -562,7 +574,7 @@ __global__ void __launch_bounds__(Cfg<N, R>::kThreads, 1)
         int pid0 = page_at(first), pid1 = boxes == 2 ? page_at(first + 1) : -1;
         if (pid0 >= args.pages || pid1 >= args.pages || (pid0 < 0 && j * kKeys < s.len) ||
             (boxes == 2 && pid1 < 0 && j * kKeys + box < s.len)) {
-          if (lane == 0 && !second) record_bad_index(args.status, kSitePage);
+          if (lane == 0) record_bad_index(args.status, kSitePage);
           if (pid0 >= args.pages) pid0 = -1;
           if (pid1 >= args.pages) pid1 = -1;
         }
@@ -570,20 +582,19 @@ __global__ void __launch_bounds__(Cfg<N, R>::kThreads, 1)
         const int row = (j * kKeys) & (page - 1);
         const uint32_t part = static_cast<uint32_t>(box) * 128u;
         const uint32_t bytes = (pid0 >= 0 ? part : 0u) + (pid1 >= 0 ? part : 0u);
-        // A chunk of 64 columns, from this warp's page.
-        const int pid = second ? pid1 : pid0;
+        // A chunk of 64 columns, of the first page where there are two.
         auto load64 = [&](uint32_t dst, uint32_t bar, int chunk) {
-          if (pid >= 0) tma_load_3d_w(dst + (second ? part : 0u), &tm_k, bar, 64 * chunk, row, pid);
+          if (pid0 >= 0) tma_load_3d_w(dst, &tm_k, bar, 64 * chunk, row, pid0);
         };
         const uint32_t rs = tiles % C::kRopes;
         if (tiles >= C::kRopes && !wait_warp(rope_empty(rs), (tiles / C::kRopes - 1) & 1, wc, kWaitKvEmpty)) {
           ok = false;
           break;
         }
-        if (!second) mbar_arrive_expect_tx_w(rope_full(rs), bytes);
+        mbar_arrive_expect_tx_w(rope_full(rs), bytes);
         load64(sbase + C::kRopeOff + rs * C::kRopeTile, rope_full(rs), R / 64);
         ++ropes;
-        if (lane == 0 && !second) valid[tiles % kValid] = mask;
+        if (lane == 0) valid[tiles % kValid] = mask;
         __syncwarp();
 #pragma unroll 1
         for (int p = 0; p < C::kPairs; ++p) {
@@ -592,7 +603,7 @@ __global__ void __launch_bounds__(Cfg<N, R>::kThreads, 1)
             break;
           }
           const uint32_t dst = sbase + C::kRingOff + ps * C::kPairTile;
-          if (!second) mbar_arrive_expect_tx_w(pair_full(ps), 2 * bytes);
+          mbar_arrive_expect_tx_w(pair_full(ps), 2 * bytes);
           load64(dst, pair_full(ps), 2 * p);
           load64(dst + C::kRopeTile, pair_full(ps), 2 * p + 1);
           ++pairs;
@@ -607,7 +618,7 @@ __global__ void __launch_bounds__(Cfg<N, R>::kThreads, 1)
         // 68.7 three).  With 64 rows it gains 2 % where a sequence has one block, but its code
         // costs 4 % where it has several (32 sequences of 4000 keys, 160 rows: 92 and 88).
         if constexpr (N < 64) {
-          if (!second && j + 1 < last_tile) {
+          if (j + 1 < last_tile) {
             const int key = (j + 1) * kKeys;
             auto page_ahead = [&](int k) {
               const int at = (k >> args.page_shift) - base;
@@ -627,20 +638,44 @@ __global__ void __launch_bounds__(Cfg<N, R>::kThreads, 1)
         }
       }
     }
-    // Every copy must have landed before the CTA exits.  Where a wait ran out, the two warps may
-    // have asked for different tiles; then the copies are given half a millisecond,
-    // hundreds of times what one takes.
-    const Waits drain{kDrainCycles, wc.abort};
-    bool landed = true;
-    for (uint32_t r = ropes > C::kRopes ? ropes - C::kRopes : 0; landed && r < ropes; ++r)
-      landed = wait_warp(rope_full(r % C::kRopes), (r / C::kRopes) & 1, drain, kWaitDrain);
-    for (uint32_t r = pairs > C::kRing ? pairs - C::kRing : 0; landed && r < pairs; ++r)
-      landed = wait_warp(pair_full(r % C::kRing), (r / C::kRing) & 1, drain, kWaitDrain);
-    if (landed && q_count > 0) landed = wait_warp(q_full, (q_count - 1) & 1, drain, kWaitDrain);
-    if (!landed)
-      for (const long long t0 = clock64(); clock64() - t0 < (1 << 20);) {
+    land(ropes, pairs, q_count);
+  } else if (warp == kLoad2Warp && args.page_shift == 5) {
+    // ================================================================ second pages
+    // Where a tile has two pages (of 32 tokens) this warp loads the second one: 64 sequences of
+    // 500 to 8000 keys, 64 heads 79.7 us, by one warp 84 (one role for both with its loads by
+    // conditions 79.9, and 2 % slower for larger pages).
+    uint32_t ropes = 0, pairs = 0, ps = 0, eph = 0;
+    bool ok = true;
+    for (uint32_t si = 0; ok && wait_seg(si); ++si) {
+      const Seg s = seg_at(si);
+      done_seg(si);
+      if (s.flags & Seg::kLast) break;
+      if (first_row(s) >= rows_of(s)) continue;
+      int base = 2 * s.a;
+      int cur = page_of_lane(args, s.b, s.len, base);
+      for (int j = s.a; ok && j < s.e; ++j, ++ropes) {
+        if (2 * j >= base + 32) cur = page_of_lane(args, s.b, s.len, base += 32);
+        const int pid = __shfl_sync(0xffffffffu, cur, 2 * j + 1 - base);
+        const bool there = pid >= 0 && pid < args.pages;
+        const uint32_t rs = ropes % C::kRopes;
+        if (ropes >= C::kRopes && !(ok = wait_warp(rope_empty(rs), (ropes / C::kRopes - 1) & 1, wc, kWaitKvEmpty))) break;
+        if (there) tma_load_3d_w(sbase + C::kRopeOff + rs * C::kRopeTile + 4096, &tm_k, rope_full(rs), R, 0, pid);
+#pragma unroll 1
+        for (int p = 0; p < C::kPairs; ++p, ++pairs) {
+          if (pairs >= C::kRing && !(ok = wait_warp(pair_empty(ps), eph ^ 1u, wc, kWaitKvEmpty))) break;
+          const uint32_t dst = sbase + C::kRingOff + ps * C::kPairTile + 4096;
+          if (there) {
+            tma_load_3d_w(dst, &tm_k, pair_full(ps), 128 * p, 0, pid);
+            tma_load_3d_w(dst + C::kRopeTile, &tm_k, pair_full(ps), 128 * p + 64, 0, pid);
+          }
+          if (++ps == C::kRing) {
+            ps = 0;
+            eph ^= 1u;
+          }
+        }
       }
-    __syncwarp();
+    }
+    land(ropes, pairs, 0);
   } else if (warp == kWalkWarp) {
     // ================================================================ schedule
     Walker<kKeys, latent_unit_cost(N)> walk(args, group_rows, static_cast<int>(misc[4]), static_cast<int>(misc[5]), sh.j1 - sh.j0);
