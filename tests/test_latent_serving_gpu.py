@@ -162,19 +162,21 @@ def test_threads_and_streams():
         assert torch.equal(g[0], w[0]) and torch.equal(g[1], w[1])
 
 
-@pytest.mark.parametrize("news,heads", [(1, 16), (1, 128), (60, 20)])
-def test_a_wait_budget_that_runs_out(news, heads):
+@pytest.mark.parametrize("page", [32, 64])
+@pytest.mark.parametrize("news,heads", [(1, 16), (1, 40), (1, 128), (60, 20)])
+def test_a_wait_budget_that_runs_out(news, heads, page):
     """Waits that give up are reported, and the next call, on the same memory and on
     tensor memory that the last one handed back, is right."""
-    *_, b = LatentBatch(80, [3000, 700], [news, news], heads, 512, 64).tables()
+    *_, b = LatentBatch(80, [3000, 700], [news, news], heads, 512, page).tables()
     dev, q = b.device(), b.rows(b.q)
     want = F.fattn_latent_fwd(q, *dev, scale=0.07)
     ok()
-    F.fattn_set_wait_budget(1)
     try:
-        for _ in range(3):
-            F.fattn_latent_fwd(q, *dev, scale=0.07)
-            assert F.fattn_check_status() in (_lib.FATTN_OK, _lib.FATTN_ERR_TIMEOUT)
+        for cycles in (1, 400, 1500, 4000):       # gives up at other places
+            F.fattn_set_wait_budget(cycles)
+            for _ in range(3):
+                F.fattn_latent_fwd(q, *dev, scale=0.07)
+                assert F.fattn_check_status() in (_lib.FATTN_OK, _lib.FATTN_ERR_TIMEOUT)
     finally:
         F.fattn_set_wait_budget(0)
     for _ in range(3):
