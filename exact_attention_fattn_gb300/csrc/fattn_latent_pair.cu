@@ -99,6 +99,21 @@ struct C {
     kSegEmpty = kSegFull + kSegs,
     kNumBars = kSegEmpty + kSegs
   };
+  // Whether softmax warp `warp` of CTA `cta` arrives on that CTA's kProb + h: a warp that does has
+  // also rescaled its part of O.  The first product, h = 0, writes to both CTAs' O, so all
+  // warps of both count; the leader's need not again for the second.
+  static constexpr bool counts_on(int h, int cta, int warp) { return h == 0 || h == cta || warp == 0; }
+  // Arrivals that a phase of barrier `i` of CTA `cta` takes.
+  static constexpr int arrivals(int i, int cta) {
+    if (i == kOtherBoth || i == kOtherBoth + 1) return 2;
+    if (i == kProb || i == kProb + 1) {
+      int n = 0;
+      for (int w = 0; w < kSoftmaxWarps; ++w) n += counts_on(i - kProb, cta, w) ? 1 : 0;
+      return n;
+    }
+    if (i == kVote || i == kVote + 1 || i == kSync) return kSoftmaxWarps;
+    return i >= kSegEmpty ? kSegReaders : 1;
+  }
   static constexpr int kMiscOff = kBarOff + kNumBars * 8;   // tmem, abort, votes[2], masks[]
   static constexpr int kPeerVoteOff = kMiscOff + 16 + 4 * kValid;   // [2][8]
   static constexpr int kSegOff = (kPeerVoteOff + 64 + 15) / 16 * 16;
@@ -189,12 +204,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   const SeqCheck mine(args.s, tid);
   if (tid < C::kNumBars) {
-    uint32_t n = 1;
-    if (tid == C::kOtherBoth || tid == C::kOtherBoth + 1) n = 2;
-    if (tid == C::kVote || tid == C::kVote + 1 || tid == C::kProb + static_cast<int>(rank) || tid == C::kSync)
-      n = kSoftmaxWarps;
-    if (tid >= C::kSegEmpty) n = kSegReaders;
-    mbar_init(bar(tid), n);
+    mbar_init(bar(tid), C::arrivals(tid, rank));
     fence_barrier_init();
   }
   if (tid >= C::kNumBars && tid < C::kNumBars + 4 + C::kValid) misc[tid - C::kNumBars] = 0u;
@@ -456,6 +466,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) {
           mbar_arrive(bar(C::kProb + rank));
           if (warp == 0) mbar_arrive_expect_tx(bar(C::kProb + peer), C::kChunk);   // the other's keys
+          else if (C::counts_on(peer, rank, warp)) mbar_arrive(bar(C::kProb + peer));
         }
 #pragma unroll
         for (int i = 0; i < 8; ++i) l[i] += part[i];
