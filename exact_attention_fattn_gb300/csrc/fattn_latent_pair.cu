@@ -463,10 +463,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         fence_proxy_async_smem();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(bar(C::kProb + rank));
-          if (warp == 0) mbar_arrive_expect_tx(bar(C::kProb + peer), C::kChunk);   // the other's keys
-          else if (C::counts_on(peer, rank, warp)) mbar_arrive(bar(C::kProb + peer));
+        if (lane == 0) mbar_arrive(bar(C::kProb + rank));
+        if (warp == 0) {
+          // What the other CTA stores of P.  Its stores of the last tile must be there before its
+          // barrier is armed for this one's: the products of that tile told the other CTA (it
+          // waits for both), but the leader only of the first.
+          if (leader && tiles > 0 && !(ok = wait_warp(bar(C::kProb + peer), (tiles - 1) & 1, wc, kWaitPFull))) break;
+          if (lane == 0) mbar_arrive_expect_tx(bar(C::kProb + peer), C::kChunk);
+        } else if (C::counts_on(peer, rank, warp) && lane == 0) {
+          mbar_arrive(bar(C::kProb + peer));
         }
 #pragma unroll
         for (int i = 0; i < 8; ++i) l[i] += part[i];

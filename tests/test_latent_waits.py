@@ -59,3 +59,14 @@ def test_every_warp_of_a_pair_has_rescaled_before_the_first_product(tmp_path):
         for there in itertools.product((0, 1), repeat=WARPS):       # the warps that have arrived
             if h == 0 and sum(a and b for a, b in zip(there, on)) >= n:
                 assert all(there), (cta, there)
+
+
+def test_a_pairs_barrier_is_armed_only_when_its_last_phase_is_over():
+    """Warp 0 of the leader arms the barrier of what the other CTA stores of P once a tile. An
+    arrival beyond a phase's count is undefined, so it looks first whether the last tile's
+    stores are all there (nothing else that it has waited for by then says so)."""
+    text = source("fattn_latent_pair.cu")
+    arm = text.index("mbar_arrive_expect_tx(bar(C::kProb + peer)")
+    wait = re.search(r"if \(leader && tiles > 0 && "
+                     r"!\(ok = wait_warp\(bar\(C::kProb \+ peer\), \(tiles - 1\) & 1, wc, \w+\)\)\)\s*break;", text)
+    assert wait and wait.end() < arm
