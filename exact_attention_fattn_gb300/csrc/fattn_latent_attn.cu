@@ -91,6 +91,15 @@ struct Cfg {
   // pair_full[] pair_empty[] rope_full[] rope_empty[] q_full q_empty s_full[2] p_full
   // pv_done mma_done seg_full[] seg_empty[]
   static constexpr int kNumBars = 2 * kRing + 2 * kRopes + 7 + 2 * kSegs;
+  // Arrivals that a phase of barrier `i` takes.  Where tiles have two pages, each of the two warps
+  // that load arrives for its own, also for a page that is not there: neither may be a turn
+  // of the ring behind the other, or it would wait for a phase that is over.
+  static constexpr int arrivals(int i, bool two_pages) {
+    const int rest = 2 * (kRing + kRopes);
+    if (i < kRing || (i >= 2 * kRing && i < 2 * kRing + kRopes)) return two_pages ? 2 : 1;
+    if (i == rest + 4) return kSoftmax;
+    return i >= rest + 7 + kSegs ? kSegReaders + (two_pages ? 1 : 0) : 1;
+  }
   static constexpr int kMiscOff = kBarOff + kNumBars * 8;       // tmem, abort, start of the share
   static constexpr int kValidOff = kMiscOff + 32;
   static constexpr int kSegOff = (kValidOff + 4 * kValid + 15) / 16 * 16;
@@ -160,8 +169,7 @@ __global__ void __launch_bounds__(Cfg<N, R>::kThreads, 1)
   // The first sequence's numbers of each thread, on their way to the scan below.
   const SeqCheck mine(args.s, tid);
   if (tid < C::kNumBars) {
-    const uint32_t bar = bar0 + 8u * tid;
-    mbar_init(bar, bar == p_full ? C::kSoftmax : (bar >= seg_empty(0) ? C::kSegReaders + (args.page_shift == 5 ? 1 : 0) : 1));
+    mbar_init(bar0 + 8u * tid, C::arrivals(tid, args.page_shift == 5));
     fence_barrier_init();
   }
   if (tid == C::kNumBars) misc[1] = 0u;
@@ -580,8 +588,7 @@ __global__ void __launch_bounds__(Cfg<N, R>::kThreads, 1)
         }
         const uint32_t mask = (pid0 >= 0 ? (boxes == 1 ? 3u : 1u) : 0u) | (pid1 >= 0 ? 2u : 0u);
         const int row = (j * kKeys) & (page - 1);
-        const uint32_t part = static_cast<uint32_t>(box) * 128u;
-        const uint32_t bytes = (pid0 >= 0 ? part : 0u) + (pid1 >= 0 ? part : 0u);
+        const uint32_t bytes = pid0 >= 0 ? static_cast<uint32_t>(box) * 128u : 0u;   // of this warp's page
         // A chunk of 64 columns, of the first page where there are two.
         auto load64 = [&](uint32_t dst, uint32_t bar, int chunk) {
           if (pid0 >= 0) tma_load_3d_w(dst, &tm_k, bar, 64 * chunk, row, pid0);
@@ -659,11 +666,14 @@ __global__ void __launch_bounds__(Cfg<N, R>::kThreads, 1)
         const bool there = pid >= 0 && pid < args.pages;
         const uint32_t rs = ropes % C::kRopes;
         if (ropes >= C::kRopes && !(ok = wait_warp(rope_empty(rs), (ropes / C::kRopes - 1) & 1, wc, kWaitKvEmpty))) break;
+        const uint32_t bytes = there ? 4096u : 0u;
+        mbar_arrive_expect_tx_w(rope_full(rs), bytes);
         if (there) tma_load_3d_w(sbase + C::kRopeOff + rs * C::kRopeTile + 4096, &tm_k, rope_full(rs), R, 0, pid);
 #pragma unroll 1
         for (int p = 0; p < C::kPairs; ++p, ++pairs) {
           if (pairs >= C::kRing && !(ok = wait_warp(pair_empty(ps), eph ^ 1u, wc, kWaitKvEmpty))) break;
           const uint32_t dst = sbase + C::kRingOff + ps * C::kPairTile + 4096;
+          mbar_arrive_expect_tx_w(pair_full(ps), 2 * bytes);
           if (there) {
             tma_load_3d_w(dst, &tm_k, pair_full(ps), 128 * p, 0, pid);
             tma_load_3d_w(dst + C::kRopeTile, &tm_k, pair_full(ps), 128 * p + 64, 0, pid);

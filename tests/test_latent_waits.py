@@ -4,8 +4,11 @@ order in which the warps that arrive may be."""
 
 import itertools
 import os
+import random
 import re
 import subprocess
+
+import pytest
 
 from exact_attention_fattn_gb300 import build
 
@@ -70,3 +73,114 @@ def test_a_pairs_barrier_is_armed_only_when_its_last_phase_is_over():
     wait = re.search(r"if \(leader && tiles > 0 && "
                      r"!\(ok = wait_warp\(bar\(C::kProb \+ peer\), \(tiles - 1\) & 1, wc, \w+\)\)\)\s*break;", text)
     assert wait and wait.end() < arm
+
+
+SINGLE = r"""
+#include <cstdio>
+struct C {
+  static constexpr int kRing = %d, kRopes = %d, kSegs = %d, kSoftmax = 128, kSegReaders = 6;
+%s
+};
+int main() {
+  for (int two = 0; two < 2; ++two)
+    std::printf("%%d %%d %%d\n", C::arrivals(0, two), C::arrivals(2 * C::kRing, two),
+                C::arrivals(2 * (C::kRing + C::kRopes) + 7 + C::kSegs, two));
+}
+"""
+SEGS = 4
+
+
+class Bar:
+    """A barrier as a wait by parity sees it."""
+
+    def __init__(self, count):
+        self.count, self.left, self.phase = count, count, 0
+
+    def arrive(self):
+        assert self.left > 0, "an arrival beyond the phase's count"
+        self.left -= 1
+        if self.left == 0:
+            self.left, self.phase = self.count, self.phase + 1
+
+    def done(self, parity):
+        return self.phase & 1 != parity
+
+
+def simulate(tiles, ring, counts, late):
+    """Sequences of one tile each, tiles[i]: whether tile i has a second page; a ring of slots, two
+    warps that load and one that uses the tiles.  late(turn): the second one's turn is
+    left out.  Returns the tiles used without their second page, or None if all wait."""
+    full_count, seg_count = counts
+    full, empty = [Bar(full_count) for _ in range(ring)], [Bar(1) for _ in range(ring)]
+    published, seg_empty = [0], [Bar(seg_count) for _ in range(SEGS)]
+    second, wrong, used = [False] * len(tiles), [], [0]
+
+    def walk():
+        for i in range(len(tiles)):
+            while i >= SEGS and not seg_empty[i % SEGS].done((i // SEGS - 1) & 1):
+                yield
+            published[0] = i + 1
+
+    def load(which):
+        for i in range(len(tiles)):
+            while published[0] <= i:
+                yield
+            seg_empty[i % SEGS].arrive()
+            while i >= ring and not empty[i % ring].done((i // ring - 1) & 1):
+                yield
+            if which == 1:
+                second[i] = True
+            if which == 0 or full_count == 2:
+                full[i % ring].arrive()
+            yield
+
+    def use():
+        for i in range(len(tiles)):
+            # with one arrival the copy's bytes hold the phase up where there is a second page
+            while not full[i % ring].done((i // ring) & 1) or (full_count == 1 and tiles[i] and not second[i]):
+                yield
+            if tiles[i] and not second[i]:
+                wrong.append(i)
+            empty[i % ring].arrive()
+            used[0] = i + 1
+            yield
+
+    def others():                       # the segments' other readers
+        for i in range(len(tiles)):
+            while used[0] <= i:
+                yield
+            for _ in range(seg_count - 2):
+                seg_empty[i % SEGS].arrive()
+
+    roles = [walk(), load(0), use(), others(), load(1)]
+    alive = [True] * 5
+    for turn in range(2000):
+        for k, r in enumerate(roles):
+            if alive[k] and not (k == 4 and late(turn)):
+                try:
+                    next(r)
+                except StopIteration:
+                    alive[k] = False
+    return wrong if not any(alive) else None
+
+
+@pytest.mark.parametrize("ring", [2, 3, 6])
+def test_neither_warp_that_loads_falls_a_turn_of_the_ring_behind(ring, tmp_path):
+    """Sequences of 1 to 32 tokens have no second page, so nothing but the barriers' counts holds
+    the first warp back.  However late the second one is, every tile is used, with its pages."""
+    text = source("fattn_latent_attn.cu")
+    out = run(SINGLE % (8, ring, SEGS, function(text, "arrivals")), tmp_path)
+    (pair1, rope1, seg1), (pair2, rope2, seg2) = [[int(x) for x in line.split()] for line in out.splitlines()]
+    assert (pair1, rope1) == (1, 1) and seg2 == seg1 + 1 and pair2 == rope2
+    r = random.Random(ring)
+    for n in range(60):
+        tiles = [i % 9 == 8 if n % 3 == 0 else r.random() < 0.2 for i in range(40)]
+        k = n % 20 + 1
+        for late in (lambda turn: turn % k != 0, lambda turn: turn < 5 * k, lambda turn: r.random() < 1 - 1 / k):
+            assert simulate(tiles, ring, (pair2, seg2), late) == []
+
+
+def test_the_simulation_tells_a_warp_that_is_left_behind():
+    """With one arrival a tile, of the first warp, the second one misses a phase."""
+    tiles = [i % 9 == 8 for i in range(40)]
+    assert simulate(tiles, 2, (1, 7), lambda turn: turn < 50) is None

@@ -47,3 +47,21 @@ def test_references_that_move_in_every_tile(page, step):
         got = F.fattn_latent_fwd(q, c, *where, scale=0.4)
         assert torch.equal(got[0], first[0]) and torch.equal(got[1], first[1])
     assert F.fattn_check_status() == 0
+
+
+@pytest.mark.parametrize("rank,heads", [(256, 16), (512, 16), (256, 40), (512, 64), (512, 20)])
+def test_tiles_of_one_page_and_of_two_in_turn(rank, heads):
+    """Pages of 32 tokens: many sequences of up to 32, which have one, among some of up to 64 and
+    of a few tiles; the warp of the second pages must not miss its turn."""
+    r = np.random.default_rng(rank + heads)
+    short = [int(x) for x in r.integers(1, 33, 900)]
+    lens = [int(r.integers(33, 65)) if i % 9 == 8 else (int(r.integers(65, 400)) if i % 50 == 20 else t) for i, t in enumerate(short)]
+    b = LatentBatch(510 + heads, lens, [1] * len(lens), heads, rank, 32)
+    check(b)
+    c, *where = b.device()
+    q = b.rows(b.q)
+    first = F.fattn_latent_fwd(q, c, *where, scale=0.07)
+    for _ in range(20):
+        got = F.fattn_latent_fwd(q, c, *where, scale=0.07)
+        assert torch.equal(got[0], first[0]) and torch.equal(got[1], first[1])
+    assert F.fattn_check_status() == 0
