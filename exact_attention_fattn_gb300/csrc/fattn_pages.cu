@@ -179,14 +179,17 @@ __global__ void __launch_bounds__(128) free_kernel(const Tables t, int* kv_len, 
 
 // Sequences from old_len to new_len tokens, in order: one whose next token falls
 // into a page that others name too gets a copy of it, but the last of those that
-// name it, if all of them write to it, keeps it; and all get the pages they lack.
+// name it, if all of them write to it, keeps it; and all get the pages they lack.  Where
+// the pool has too few, a sequence that needs one, or would write to a page that it
+// shares, has length -1 from then on in new_len: an append that follows in the same graph,
+// where no host can look in between, passes over it.
 // A thread has up to kPerThread neighbouring sequences.  Whether a page's writers
 // are all that name it, and which is the last, two counters a page tell (`writers`,
 // `last`; sums and maxima, so their order does not matter).
 constexpr int kPerThread = kMaxSeqs / kScanThreads;
 constexpr int kOwnPages = 8;             // new pages that a sequence's own thread enters; more go to its warp
 
-__global__ void __launch_bounds__(kScanThreads) extend_kernel(const Tables t, const int* old_len, const int* new_len,
+__global__ void __launch_bounds__(kScanThreads) extend_kernel(const Tables t, const int* old_len, int* new_len,
                                                               int* free_list, int* writers, int* last, CopyList list) {
   __shared__ long long side[32];
   __shared__ int found_all;
@@ -194,6 +197,7 @@ __global__ void __launch_bounds__(kScanThreads) extend_kernel(const Tables t, co
   allow_child();
   const int per = (t.B + kScanThreads - 1) / kScanThreads, b0 = tid * per;
   int tail[kPerThread], k0[kPerThread], k1[kPerThread], slot[kPerThread];   // shared last page, or -1; entries; the page's
+  unsigned int shares = 0u;              // whether there is one
 #pragma unroll
   for (int i = 0; i < kPerThread; ++i) {
     const int b = b0 + i;
@@ -203,6 +207,7 @@ __global__ void __launch_bounds__(kScanThreads) extend_kernel(const Tables t, co
     const int o = old_len[b], w = new_len[b];
     if (o < 0 || w < o || w > t.cap()) {
       record_bad_index(t.status, kSiteSeqStart);
+      new_len[b] = -1;
       continue;
     }
     k0[i] = t.held(o);
@@ -214,6 +219,7 @@ __global__ void __launch_bounds__(kScanThreads) extend_kernel(const Tables t, co
       else if (t.refs[p] >= 2) tail[i] = p;
     }
     if (tail[i] >= 0) {
+      shares |= 1u << i;
       writers[tail[i]] = 0;
       last[tail[i]] = -1;
     }
@@ -275,6 +281,7 @@ __global__ void __launch_bounds__(kScanThreads) extend_kernel(const Tables t, co
     int* row = t.table + static_cast<long long>(b0 + i) * t.max_pages;
     int begin = granted ? static_cast<int>(at & ((1ll << 40) - 1)) : 0;
     const int copy = tail[i] >= 0 ? 1 : 0, fresh = k1[i] - k0[i];
+    if (!granted && (fresh > 0 || (shares >> i & 1u) != 0u)) new_len[b0 + i] = -1;
     if (copy != 0 && granted) {
       const int c = static_cast<int>(at >> 40), to = free_list[begin];
       if (dcheck(inside(c, 1, t.B) && inside(begin, 1, t.pages), t.status, 672)) {
@@ -643,7 +650,7 @@ size_t fattn_pages_workspace_bytes(int pages, int B) {
 }
 
 int fattn_pages_extend(const fattn_page_pool* pool, const fattn_plane* planes, int n_planes, int* page_table,
-                       const int* old_len, const int* new_len, void* workspace, size_t workspace_bytes, int B,
+                       const int* old_len, int* new_len, void* workspace, size_t workspace_bytes, int B,
                        int max_pages, fattn_stream_t stream) {
   const Range range("fattn_pages_extend");
   int rc = check_pool(pool, page_table, old_len, B, max_pages);

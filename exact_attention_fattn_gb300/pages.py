@@ -114,7 +114,9 @@ def fattn_pages_extend(pool: PagePool, cache, page_table, old_len, new_len, work
     [B]), before they are appended: a copy of its last page where that is shared
     and written to, then the pages it lacks, lowest free ones first.  Changes
     ``page_table``, the counts and the copies; lengths stay.  With too few free
-    pages nobody gets any, and fattn_check_status() returns 8."""
+    pages nobody gets any, fattn_check_status() returns 8, and ``new_len`` is -1
+    for the sequences that lack room (they still have ``old_len`` tokens): append
+    and attention with it pass over them and serve the others."""
     ps, planes, dev, (B, max_pages) = _setup(pool, cache, page_table, old_len, new_len)
     _with_workspace(_lib.load().fattn_pages_extend, ps, dev, workspace, page_table,
                     (planes, len(planes), page_table.data_ptr(), old_len.data_ptr(), new_len.data_ptr()), (B, max_pages))

@@ -51,7 +51,7 @@ typedef enum {
   FATTN_ERR_BAD_INDEX = 7,   /* a cache call's q_start, kv_len, page_table, positions or selected
                                 pages are out of range; the kernel skipped what they point at */
   FATTN_ERR_NO_PAGES = 8     /* fattn_pages_extend: the pool has too few free pages; no sequence
-                                was given any */
+                                was given any, and those that lack room have new_len -1 */
 } fattn_status;
 
 /*
@@ -537,17 +537,21 @@ int fattn_pages_fork(const fattn_page_pool* pool, int* page_table, int* kv_len, 
  * shares, the sequence gets a copy of that page for itself (the last that still has the
  * page keeps it), and then the pages it lacks.
  *   old_len, new_len : int [B] on the device, 0 <= old_len <= new_len <= max_pages * page; a
- *                      sequence with others is FATTN_ERR_BAD_INDEX and gets nothing
+ *                      sequence with others is FATTN_ERR_BAD_INDEX and gets nothing.  new_len
+ *                      is in and out: -1 for a sequence without room for its tokens
  *   workspace        : at least fattn_pages_workspace_bytes(pages, B), 256-byte aligned; contents on
  *                      entry ignored; calls that may overlap need one each
  * With too few free pages no sequence gets any: tables and counts stay as they are, but
- * that the entries to be filled become -1 (so that appending leaves those tokens out), and
- * fattn_check_status() reports FATTN_ERR_NO_PAGES.  Shared pages then still are, so
- * nothing may be appended before the host has looked.  Returns a fattn_status.
+ * that the entries to be filled become -1, and fattn_check_status() reports
+ * FATTN_ERR_NO_PAGES.  A sequence that needed a page, or would write into one that it shares,
+ * has new_len -1 then; its length is still old_len.  Append and attention, given new_len as their
+ * kv_len, leave it alone (FATTN_ERR_BAD_INDEX, which the first error hides) and serve
+ * the others, also in a captured step, where the host cannot look in between.  Returns a
+ * fattn_status.
  */
 size_t fattn_pages_workspace_bytes(int pages, int B);
 int fattn_pages_extend(const fattn_page_pool* pool, const fattn_plane* planes, int n_planes,
-                       int* page_table, const int* old_len, const int* new_len, void* workspace,
+                       int* page_table, const int* old_len, int* new_len, void* workspace,
                        size_t workspace_bytes, int B, int max_pages, fattn_stream_t stream);
 
 /*

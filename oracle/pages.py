@@ -32,8 +32,8 @@ def fork(refs, table, kv_len, page, parent, child):
 
 
 def extend(refs, table, planes, page, old, new):
-    """Returns whether there were pages enough; nothing but entries to be filled
-    (-1) changes if not."""
+    """Returns whether there were pages enough; if not, nothing changes but entries
+    to be filled (-1) and the new lengths of those that lack room (-1)."""
     free = [int(p) for p in np.nonzero(refs == 0)[0]]
     r, t, copies, fills = refs.copy(), table.copy(), [], []
     for b in range(len(old)):
@@ -45,7 +45,12 @@ def extend(refs, table, planes, page, old, new):
         fills += [(b, i) for i in range(held(old[b], page), last)]
     if len(fills) > len(free):
         for b in range(len(old)):
+            at = int(old[b]) // page
+            shared = new[b] > old[b] and old[b] % page and refs[table[b, at]] >= 2
+            lacks = shared or held(new[b], page) > held(old[b], page)
             table[b, held(old[b], page):held(new[b], page)] = -1
+            if lacks:
+                new[b] = -1
         return False
     for (b, i), p in zip(fills, free):
         table[b, i] = p
