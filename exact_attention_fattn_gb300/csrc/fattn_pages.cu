@@ -12,7 +12,7 @@
 // Measured: 18 of 24 sequences forked from 6 (latent cache, 300 to 4000 tokens) and
 // room for one token each, both calls 14.1 us; 576 of 768 from 192 (8-bit cache, 8 heads of
 // 128, 500 to 2000 tokens) and room for 100 more, 38 us; 291 MB of a pool moved together
-// 57.5 us, 49 of them the copies, 0.87 of the measured copy rate (loads and stores of 16
+// 58 us, 49 of them the copies, 0.87 of the measured copy rate (loads and stores of 16
 // bytes a thread, 2048 threads an SM: 39 and 63.4; pieces of 24 KB 36.5 and 57.9, of
 // 8 KB, with a division a piece, 58 and 75).
 #include <stdint.h>
@@ -312,11 +312,20 @@ __global__ void __launch_bounds__(kScanThreads) extend_kernel(const Tables t, co
 // ------------------------------------------------------------------ compact
 
 // The k-th held page from `total` on goes to the k-th free page below, total the
-// number of pages held.
-__global__ void __launch_bounds__(kScanThreads) plan_kernel(const Tables t, int* to_page, CopyList list, int* limit) {
+// number of pages held.  move_of[page]: k, for both pages of move k; other pages' entries
+// hold anything, so that a reader looks whether the list has the page at that place.
+// A sequence whose length makes no sense has entries that nobody could rewrite, so
+// nothing moves then (limit -1).
+__global__ void __launch_bounds__(kScanThreads) plan_kernel(const Tables t, const int* kv_len, int* move_of,
+                                                            CopyList list, int* limit) {
   __shared__ long long side[32];
   const int tid = threadIdx.x;
   allow_child();
+  bool senseless = false;
+  for (int b = tid; b < t.B; b += kScanThreads) {
+    const int len = kv_len[b];
+    senseless |= len < 0 || len > t.cap();
+  }
   // Pools of up to one turn's pages keep their counts in registers for the second look.
   const bool once = t.pages <= kScanThreads * kScanPages;
   int r[kScanPages];
@@ -325,6 +334,14 @@ __global__ void __launch_bounds__(kScanThreads) plan_kernel(const Tables t, int*
     load_refs(t.refs, t.pages, static_cast<int>(min(base + tid * kScanPages, static_cast<long long>(t.pages))), 0, r);
 #pragma unroll
     for (int i = 0; i < kScanPages; ++i) held += r[i] > 0 ? 1 : 0;
+  }
+  if (__syncthreads_or(senseless)) {
+    if (tid == 0) {
+      record_bad_index(t.status, kSiteSeqStart);
+      *list.count = 0;
+      *limit = -1;
+    }
+    return;
   }
   long long total;
   block_scan(held, side, total);
@@ -355,7 +372,7 @@ __global__ void __launch_bounds__(kScanThreads) plan_kernel(const Tables t, int*
   const int moves = static_cast<int>(seen >> 32);
   for (int i = tid; i < moves; i += kScanThreads) {
     const int from = list.src[i], to = list.dst[i];
-    to_page[from] = to;
+    move_of[from] = move_of[to] = i;
     t.refs[to] = t.refs[from];
     t.refs[from] = 0;
   }
@@ -402,7 +419,7 @@ __device__ __forceinline__ int piece_of(const Planes& p, int k, int piece, long 
 // kStages - kBehind on their way in; the others take what is small or not aligned to
 // 16 bytes, and the table.
 __global__ void __launch_bounds__(kCopyThreads) copy_kernel(const Tables t, const __grid_constant__ Planes planes,
-                                                            CopyList list, const int* kv_len, const int* to_page,
+                                                            CopyList list, const int* kv_len, const int* move_of,
                                                             const int* limit, long long wait_budget) {
   extern __shared__ __align__(128) uint8_t stages[];
   __shared__ uint64_t full[kStages];
@@ -417,7 +434,7 @@ __global__ void __launch_bounds__(kCopyThreads) copy_kernel(const Tables t, cons
   }
   wait_for_parent();
   const int n = *list.count;
-  if (n == 0) return;
+  if (n == 0 && kv_len == nullptr) return;
   const long long items = static_cast<long long>(n) * planes.pieces;
   if (threadIdx.x >= 32) {
     const int me = threadIdx.x - 32;
@@ -437,18 +454,22 @@ __global__ void __launch_bounds__(kCopyThreads) copy_kernel(const Tables t, cons
     }
     if (kv_len == nullptr) return;
     const int lim = *limit;
+    if (lim < 0) return;
     for (int b = blockIdx.x; b < t.B; b += gridDim.x) {
-      const int len = kv_len[b];
-      if (len < 0 || len > t.cap()) {
-        if (me == 0) record_bad_index(t.status, kSiteSeqStart);
-        continue;
-      }
       int* row = t.table + static_cast<long long>(b) * t.max_pages;
-      const int held = t.held(len);
+      const int held = t.held(kv_len[b]);
       for (int k = me; k < held; k += kPlainThreads) {
         const int p = row[k];
-        if (!t.is_page(p)) record_bad_index(t.status, kSitePage);
-        else if (p >= lim) row[k] = to_page[p];
+        if (!t.is_page(p)) {
+          record_bad_index(t.status, kSitePage);
+          continue;
+        }
+        // From the limit on only pages that moved were held, and below it those that were
+        // moved to were not: such an entry stays, and is reported.
+        const int i = move_of[p];
+        const bool listed = i >= 0 && i < n && (p >= lim ? list.src : list.dst)[i] == p;
+        if (listed != (p >= lim)) record_bad_index(t.status, kSiteRefs);
+        else if (listed) row[k] = list.dst[i];
       }
     }
     return;
@@ -594,13 +615,13 @@ PagesWorkspace workspace_of(int pages, int B) {
 }
 
 int launch_copies(const Tables& t, const Planes& p, const CopyList& list, long long most_pages, const int* kv_len,
-                  const int* to_page, const int* limit, long long budget, cudaStream_t stream) {
+                  const int* move_of, const int* limit, long long budget, cudaStream_t stream) {
   static SmemLimit limit_of;
   constexpr int kBytes = kStages * kPieceBytes;
   if (limit_of.raise(reinterpret_cast<const void*>(copy_kernel), kBytes) != cudaSuccess) return FATTN_ERR_CUDA;
   const long long items = most_pages * p.pieces;
   const int grid = static_cast<int>(items < 2 * kSms ? items : 2 * kSms);
-  return launch_child(copy_kernel, grid, kCopyThreads, kBytes, stream, t, p, list, kv_len, to_page, limit, budget) ==
+  return launch_child(copy_kernel, grid, kCopyThreads, kBytes, stream, t, p, list, kv_len, move_of, limit, budget) ==
                  cudaSuccess
              ? FATTN_OK
              : FATTN_ERR_CUDA;
@@ -693,12 +714,12 @@ int fattn_pages_compact(const fattn_page_pool* pool, const fattn_plane* planes, 
   const CopyList list{reinterpret_cast<int*>(base), reinterpret_cast<int*>(base + w.src),
                       reinterpret_cast<int*>(base + w.dst)};
   int* limit = reinterpret_cast<int*>(base) + 1;
-  int* to_page = reinterpret_cast<int*>(base + w.map);
+  int* move_of = reinterpret_cast<int*>(base + w.map);
   const Tables t = tables_of(pool, page_table, B, max_pages, status);
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  plan_kernel<<<1, kScanThreads, 0, st>>>(t, to_page, list, limit);
+  plan_kernel<<<1, kScanThreads, 0, st>>>(t, kv_len, move_of, list, limit);
   if (cudaGetLastError() != cudaSuccess) return FATTN_ERR_CUDA;
-  return launch_copies(t, p, list, static_cast<long long>(pool->pages) / 2 + 1, kv_len, to_page, limit, budget, st);
+  return launch_copies(t, p, list, static_cast<long long>(pool->pages) / 2 + 1, kv_len, move_of, limit, budget, st);
 }
 
 }  // extern "C"

@@ -136,7 +136,7 @@ def fattn_pages_free(pool: PagePool, cache, page_table, kv_len, rows):
 def fattn_pages_compact(pool: PagePool, cache, page_table, kv_len, workspace=None):
     """Move the pages that are held to the lowest ones, in the cache, the counts
     and the table.  ``kv_len`` says how many entries each sequence holds: the
-    lengths that room was made for."""
+    lengths that room was made for; with one out of range nothing moves."""
     ps, planes, dev, (B, max_pages) = _setup(pool, cache, page_table, kv_len)
     _with_workspace(_lib.load().fattn_pages_compact, ps, dev, workspace, page_table,
                     (planes, len(planes), page_table.data_ptr(), kv_len.data_ptr()), (B, max_pages))

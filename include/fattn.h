@@ -567,8 +567,9 @@ int fattn_pages_free(const fattn_page_pool* pool, int* page_table, int* kv_len, 
  * Move the pool's pages together: with U pages held, the k-th held page from U on goes to the
  * k-th free page below U, in every plane, count and table entry.  kv_len [B] says which
  * entries sequences hold (pages taken for tokens beyond it would be lost: give the
- * lengths that fattn_pages_extend was given).  Workspace as for fattn_pages_extend.
- * Returns a fattn_status.
+ * lengths that fattn_pages_extend was given).  With a length out of range nothing moves; an
+ * entry that names a page outside the pool, or one that was free, stays (both
+ * FATTN_ERR_BAD_INDEX).  Workspace as for fattn_pages_extend.  Returns a fattn_status.
  */
 int fattn_pages_compact(const fattn_page_pool* pool, const fattn_plane* planes, int n_planes,
                         int* page_table, const int* kv_len, void* workspace, size_t workspace_bytes,

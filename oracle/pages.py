@@ -74,6 +74,10 @@ def free(refs, table, kv_len, page, rows):
 
 
 def compact(refs, table, planes, page, kv_len):
+    """Nothing moves where a length is out of range; entries whose page has no
+    count stay."""
+    if not all(0 <= n <= table.shape[1] * page for n in kv_len):
+        return
     total = int((refs > 0).sum())
     src = [p for p in range(total, len(refs)) if refs[p] > 0]
     dst = [p for p in range(total) if refs[p] <= 0]
