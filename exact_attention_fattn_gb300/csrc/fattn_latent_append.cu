@@ -107,8 +107,9 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
 #pragma unroll
     for (int k = 0; k < kHeads; ++k) {
       const long long off = min(k, a.Hq - 1 - h0) * a.qr_head;
-      u[k] = __ldg(reinterpret_cast<const uint4*>(src + off + c0));
-      v[k] = __ldg(reinterpret_cast<const uint4*>(src + off + c1));
+      // q may be the same columns, so these are no read-only data
+      u[k] = *reinterpret_cast<const uint4*>(src + off + c0);
+      v[k] = *reinterpret_cast<const uint4*>(src + off + c1);
     }
     const Token t = token_of(a, token);
     if (!t.ok) return;
