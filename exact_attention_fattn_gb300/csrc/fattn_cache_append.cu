@@ -191,8 +191,8 @@ __device__ __forceinline__ void rotate_q(const CacheAppendArgs& a, int item) {
 #pragma unroll
   for (int i = 0; i < kQHeads; ++i) {
     w[i] = make_uint4(0u, 0u, 0u, 0u);
-    if (on && h0 + i < a.Hq)
-      w[i] = __ldg(reinterpret_cast<const uint4*>(a.q + row * a.q_row + (h0 + i) * D + 8 * cc));
+    if (on && h0 + i < a.Hq)               // q_out may be q, so this is no read-only data
+      w[i] = *reinterpret_cast<const uint4*>(a.q + row * a.q_row + (h0 + i) * D + 8 * cc);
   }
   const Angles ang(cs, a.rope_dim, a.interleaved, cc);
 #pragma unroll

@@ -16,10 +16,11 @@ def source(name):
 
 @pytest.mark.parametrize("name,block", [
     ("fattn_rope.cu", r"const uint16_t\* x = a\.x.*?\n\}"),
-    ("fattn_latent_append.cu", r"const uint16_t\* src = a\.q_rope.*?return;\n  \}")])
+    ("fattn_latent_append.cu", r"const uint16_t\* src = a\.q_rope.*?return;\n  \}"),
+    ("fattn_cache_append.cu", r"uint4 w\[kQHeads\];.*?const Angles")])
 def test_what_may_be_written_in_place_is_read_plainly(name, block):
     text = re.search(block, source(name), flags=re.S).group(0)
-    base = "x" if name == "fattn_rope.cu" else "src"
+    base = {"fattn_rope.cu": "x", "fattn_latent_append.cu": "src", "fattn_cache_append.cu": r"a\.q"}[name]
     assert re.search(r"\*reinterpret_cast<const uint4\*>\(" + base, text)
     assert not re.search(r"(__ldg|ld\.global\.nc|__restrict__)[^;]*\b" + base + r"\b", text)
     assert "__restrict__" not in source(name)
