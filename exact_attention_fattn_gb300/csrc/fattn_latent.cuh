@@ -12,6 +12,21 @@ constexpr float kLn2 = 0.69314718055994530942f;
 constexpr float kTau = 8.f;            // a row's reference moves when a score passes it by 2^8
 constexpr int kSmemMax = 232448;       // bytes a CTA may have
 
+// P V has bf16 probabilities and the row's sum l fp32 ones, from which L comes.  O is divided by
+// r, the sum of the bf16 ones, so that its weights add up to one; by l, a row that
+// one key dominates would be off by that key's rounding, up to 2^-8.  A share's part of a row is
+// stored as O l / r, so that parts are joined by their l alone.
+// x and y plus the halves of a word.
+__device__ __forceinline__ void add_bf16(float& x, float& y, uint32_t w) {
+  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
+      "add.rn.f32.bf16 %0, l, %0;\n\tadd.rn.f32.bf16 %1, h, %1;\n\t}"
+      : "+f"(x), "+f"(y)
+      : "r"(w));
+}
+__device__ __forceinline__ float row_factor(float l, float r, bool whole) {
+  return l == 0.f ? 0.f : (whole ? 1.f : l) / r;
+}
+
 // ------------------------------------------------------------------ PTX
 
 __device__ __forceinline__ uint32_t elect_lane() {

@@ -19,8 +19,8 @@
 // and sums l it keeps in registers.  A row's reference moves only when a score
 // passes it by more than 2^8; whether one does is one vote of the warps, so
 // that most tiles need no maximum over keys at all.  P is rounded to bf16 (half a
-// step: 2^-8 of a probability), as V is; scores, sums, references and accumulators
-// are fp32.
+// step: 2^-8 of a probability), as V is, and O divided by the sum r of what the
+// rounding leaves; scores, sums, references and accumulators are fp32.
 //
 // Work split: the key tiles of all units, in order, are dealt in equal contiguous
 // shares; a unit is a group of `span` row blocks of one sequence, and a share is
@@ -246,11 +246,11 @@ __global__ void __launch_bounds__(Cfg<N, R>::kThreads, 1)
       }
       softmax_sync();
       const int lim_min = lims[0];        // rows see no fewer keys than the first
-      float m[NC], l[NC];
+      float m[NC], l[NC], r[NC];
 #pragma unroll
       for (int i = 0; i < NC; ++i) {
         m[i] = -FLT_MAX;
-        l[i] = 0.f;
+        l[i] = r[i] = 0.f;
       }
       bool holes = false;
       for (int j = s.a; j < s.e; ++j, ++tiles) {
@@ -305,6 +305,7 @@ __global__ void __launch_bounds__(Cfg<N, R>::kThreads, 1)
             const float al = move ? ex2_approx(m[i] - t) : 1.f;
             if (move) m[i] = t;
             l[i] *= al;
+            r[i] *= al;
             if (quarter == 0 && lane < 4) alphas[col] = al;
           }
           softmax_sync();
@@ -366,15 +367,27 @@ __global__ void __launch_bounds__(Cfg<N, R>::kThreads, 1)
         fence_proxy_async_smem();
         tc_fence_before();
         mbar_arrive(p_full);
+#pragma unroll
+        for (int i = 0; i < NC; i += 2) {
+          add_bf16(r[i], r[i + 1], pk[i]);
+          add_bf16(r[i], r[i + 1], pk[i + 1]);
+        }
       }
       // ---- results
       fail |= !wait_warp(pv_done, (tiles - 1) & 1, wc, kWaitOFull);
+      float* rs = reinterpret_cast<float*>(smem + C::kPOff);   // [4][N]: no product reads P any more
 #pragma unroll
       for (int i = 0; i < NC; ++i) {
 #pragma unroll
-        for (int off = 4; off < 32; off <<= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], off);
+        for (int off = 4; off < 32; off <<= 1) {
+          l[i] += __shfl_xor_sync(0xffffffffu, l[i], off);
+          r[i] += __shfl_xor_sync(0xffffffffu, r[i], off);
+        }
         const int col = col_of(i);
-        if (lane < 4) xs[quarter * N + col] = l[i];
+        if (lane < 4) {
+          xs[quarter * N + col] = l[i];
+          rs[quarter * N + col] = r[i];
+        }
         if (quarter == 0 && lane < 4) alphas[col] = m[i];
       }
       if (softmax_any(fail)) break;
@@ -384,14 +397,14 @@ __global__ void __launch_bounds__(Cfg<N, R>::kThreads, 1)
       const long long out0 = static_cast<long long>(s.r0) * args.Hq + row0;
       if (tid < N) {
         float lt = (xs[tid] + xs[N + tid]) + (xs[2 * N + tid] + xs[3 * N + tid]);
-        const float mt = alphas[tid];
+        const float rt = (rs[tid] + rs[N + tid]) + (rs[2 * N + tid] + rs[3 * N + tid]), mt = alphas[tid];
         // All scores of keys that the row sees are -inf: its query holds an infinity.
         if (lt == 0.f && !holes && lims[tid] > s.a * kKeys) lt = __int_as_float(0x7fffffff);
         if (tid < live) {
           if (whole) args.lse[out0 + tid] = lt == 0.f ? -INFINITY : (mt + log2f(lt)) * kLn2;
           else args.part_ml[slot * N + tid] = make_float2(mt, lt);
         }
-        alphas[tid] = lt == 0.f ? 0.f : 1.f / lt;
+        alphas[tid] = row_factor(lt, rt, whole);
       }
       softmax_sync();
       if (whole) {
@@ -440,10 +453,13 @@ __global__ void __launch_bounds__(Cfg<N, R>::kThreads, 1)
           uint32_t o[16];
           tmem_ld16(tmem + lane_off + C::col_o(pair) + r0, o);
           float* part = args.part_o + (slot * N + r0) * R + 128 * pair + 32 * quarter + lane;
+          float f[16];
+#pragma unroll
+          for (int z = 0; z < 16; z += 4) *reinterpret_cast<float4*>(f + z) = *reinterpret_cast<const float4*>(alphas + r0 + z);
           tmem_ld_wait(o);
 #pragma unroll
           for (int z = 0; z < 16; ++z)
-            if (r0 + z < live && dcheck(slot < 2ll * kSms, args.status, 695)) part[z * R] = __uint_as_float(o[z]);
+            if (r0 + z < live && dcheck(slot < 2ll * kSms, args.status, 695)) part[z * R] = __uint_as_float(o[z]) * f[z];
         }
       }
     }

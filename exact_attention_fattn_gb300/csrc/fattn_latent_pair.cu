@@ -27,8 +27,8 @@
 // thread has stored (votes and P by plain remote stores and releases took 5500 cycles
 // a tile, 2500 of them waiting for the votes).
 //
-// Measured: 2 pieces of 1024 tokens, 16 heads, before keys up to 8192: 417 us (64 rows a CTA:
-// 570), 1195 TFLOP/s; 64 single tokens of 128 heads over 500 to 8000 keys 98 (123).  A tile
+// Measured: 2 pieces of 1024 tokens, 16 heads, before keys up to 8192: 421 us (64 rows a CTA:
+// 570), 1185 TFLOP/s; 64 single tokens of 128 heads over 500 to 8000 keys 100 (123).  A tile
 // takes 3800 cycles in the first, 1750 of them issue of the products.  When it took 467 us
 // neither the products bound it (with a quarter of their columns 459) nor L2 (two pairs a
 // cluster with one copy of the keys for both 512) nor the softmax (16 warps 477): a tile's
@@ -193,6 +193,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   float* own = reinterpret_cast<float*>(smem + C::kOwnOff);        // [2 key quarters][kRows]
   float* peers = reinterpret_cast<float*>(smem + C::kPeerOff);     // [exchange & 1][kRows]
   float* alphas = reinterpret_cast<float*>(smem + C::kAlphaOff);   // [kRows]
+  // Sums of the rounded probabilities, in P's place when a unit's products are done: this CTA's
+  // [2 key quarters][kRows], then the other's [kRows].
+  float* own_r = reinterpret_cast<float*>(smem + C::kPOff);
+  float* peer_r = own_r + 2 * kRows;
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t rank = cluster_rank(), peer = rank ^ 1u;
@@ -243,6 +247,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int row_base = 64 * (quarter >> 1) + cols, key_base = 32 * (quarter & 1) + (lane >> 2);
     const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
     auto row_at = [&](int i) { return row_base + 8 * (i >> 1) + 2 * (lane & 3) + (i & 1); };
+    auto row_transposed = [&](int o) { return row_base + 8 * o + (lane >> 2); };
     const uint32_t home = quarter >> 1;                             // the CTA that stages these rows of P
     const uint32_t p_dst = map_shared(sbase + C::kPOff + rank * C::kChunk, home);
     uint32_t tiles = 0, syncs = 0, exchanges = 0;
@@ -259,8 +264,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float x = own[tid], y = own[kRows + tid];
         st_async_u32(map_shared(smem_u32(peers + (exchanges & 1) * kRows + tid), peer),
                      __float_as_uint(sums ? x + y : fmaxf(x, y)), map_shared(bar(b), peer));
+        if (sums)
+          st_async_u32(map_shared(smem_u32(peer_r + tid), peer), __float_as_uint(own_r[tid] + own_r[kRows + tid]),
+                       map_shared(bar(b), peer));
       }
-      if (tid == 0) mbar_arrive_expect_tx(bar(b), kRows * 4);
+      if (tid == 0) mbar_arrive_expect_tx(bar(b), kRows * (sums ? 8 : 4));
       return wait_pair(bar(b), exchanges++ >> 1 & 1, wc, kWaitDrain);
     };
     for (uint32_t si = 0; wait_seg(si); ++si) {
@@ -276,14 +284,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!args.causal || row >= live) return s.len;
         return max(0, min(s.len, s.len - s.n + static_cast<int>(static_cast<unsigned int>(row0 + row) / args.Hq) + 1));
       };
+      // A block's rows are of 128 tokens at most, so that what a row sees beyond the first fits a byte.
       const int lim_min = lim_of(0);
-      int lim[8];
+      uint32_t lim_more[2] = {0u, 0u};
+      auto lim = [&](int i) { return lim_min + static_cast<int>(lim_more[i >> 2] >> (8 * (i & 3)) & 255u); };
       float m[8], l[8];
+      // Sums of the rounded probabilities, taken when P is on its way: of rows row_at(i), or, where
+      // they have been transposed for the other CTA, two of row_transposed(i / 2).
+      float r[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        lim[i] = lim_of(row_at(i));
+        lim_more[i >> 2] |= static_cast<uint32_t>(lim_of(min(row_at(i), live - 1)) - lim_min) << (8 * (i & 3));
         m[i] = -FLT_MAX;
-        l[i] = 0.f;
+        l[i] = r[i] = 0.f;
       }
       bool holes = false, ok = true;
       for (int j = s.a; j < s.e; ++j, ++tiles) {
@@ -316,7 +329,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int i = 0; i < 8; ++i)
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-              if (!there || mine0 + key_base + 8 * k >= lim[i]) score(i, k) = __float_as_uint(-INFINITY);
+              if (!there || mine0 + key_base + 8 * k >= lim(i)) score(i, k) = __float_as_uint(-INFINITY);
         }
         auto val = [&](int i, int k) { return __uint_as_float(score(i, k)); };
         auto top_of = [&](int i) { return fmaxf(fmaxf(val(i, 0), val(i, 1)), fmaxf(val(i, 2), val(i, 3))); };
@@ -398,9 +411,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float al = move ? ex2_approx(m[i] - t) : 1.f;
             if (move) m[i] = t;
             l[i] *= al;
+            if (home == rank) r[i] *= al;
             if ((quarter & 1) == 0 && lane < 4) alphas[row] = al;
           }
           if (!(ok = sync())) break;
+          if (home != rank) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) r[i] *= alphas[row_transposed(i >> 1)];
+          }
           if (!first) {
             if (!(ok = wait_warp(bar(C::kPvDone + peer), (tiles - 1) & 1, wc, kWaitMmaDone))) break;
             tc_fence_after();
@@ -475,6 +493,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
 #pragma unroll
         for (int i = 0; i < 8; ++i) l[i] += part[i];
+#pragma unroll
+        for (int o = 0; o < 4; ++o)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) add_bf16(r[2 * o], r[2 * o + 1], w[o][k]);
       }
       if (!ok) break;
       // ---- results: this CTA's half of the columns, for all rows
@@ -487,6 +509,22 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane < 4) own[(quarter & 1) * kRows + row_at(i)] = l[i];
         if ((quarter & 1) == 0 && lane < 4) alphas[row_at(i)] = m[i];
       }
+      if (home == rank) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+#pragma unroll
+          for (int off = 4; off < 32; off <<= 1) r[i] += __shfl_xor_sync(0xffffffffu, r[i], off);
+          if (lane < 4) own_r[(quarter & 1) * kRows + row_at(i)] = r[i];
+        }
+      } else {
+#pragma unroll
+        for (int o = 0; o < 4; ++o) {
+          float x = r[2 * o] + r[2 * o + 1];
+#pragma unroll
+          for (int off = 1; off < 4; off <<= 1) x += __shfl_xor_sync(0xffffffffu, x, off);
+          if ((lane & 3) == 0) own_r[(quarter & 1) * kRows + row_transposed(o)] = x;
+        }
+      }
       if (!exchange(true)) break;
       tc_fence_after();
       const bool whole = s.whole();
@@ -494,15 +532,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       const long long out0 = static_cast<long long>(s.r0) * args.Hq + row0;
       if (tid < kRows) {
         const float here = own[tid] + own[kRows + tid], there = peers[((exchanges - 1) & 1) * kRows + tid];
+        const float here_r = own_r[tid] + own_r[kRows + tid], there_r = peer_r[tid];
         float lt = leader ? here + there : there + here;
-        const float mt = alphas[tid];
+        const float rt = leader ? here_r + there_r : there_r + here_r, mt = alphas[tid];
         // All scores of keys that the row sees are -inf: its query holds an infinity.
         if (lt == 0.f && !holes && lim_of(tid) > s.a * kKeys) lt = __int_as_float(0x7fffffff);
         if (leader && tid < live) {
           if (whole) args.lse[out0 + tid] = lt == 0.f ? -INFINITY : (mt + log2f(lt)) * kLn2;
           else args.part_ml[slot * kRows + tid] = make_float2(mt, lt);
         }
-        alphas[tid] = lt == 0.f ? 0.f : 1.f / lt;
+        alphas[tid] = row_factor(lt, rt, whole);
       }
       if (!sync()) break;
       const int col_base = kRank / 2 * static_cast<int>(rank) + 32 * quarter;     // of O
@@ -549,10 +588,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           uint32_t o[16];
           tmem_ld16(tmem + lane_off + C::col_o(p >> 2) + r0, o);
           float* to = args.part_o + (slot * kRows + r0) * kRank + col_base + 128 * (p >> 2) + lane;
+          float f[16];
+#pragma unroll
+          for (int z = 0; z < 16; z += 4) *reinterpret_cast<float4*>(f + z) = *reinterpret_cast<const float4*>(alphas + r0 + z);
           tmem_ld_wait(o);
 #pragma unroll
           for (int z = 0; z < 16; ++z)
-            if (r0 + z < live && dcheck(slot < 2ll * (kSms / 2), args.status, 706)) to[z * kRank] = __uint_as_float(o[z]);
+            if (r0 + z < live && dcheck(slot < 2ll * (kSms / 2), args.status, 706)) to[z * kRank] = __uint_as_float(o[z]) * f[z];
         }
       }
     }

@@ -482,7 +482,8 @@ int fattn_latent_append(const fattn_latent_cache* cache, const void* latent, lon
  * Slots behind a sequence's end may hold anything; latents before it are finite
  * (fattn_latent_append writes no others).
  * Rounding: probabilities are rounded to bf16 (2^-8) for the second product, and O to
- * bf16 (2^-8); scores, sums, maxima and the accumulators are fp32.
+ * bf16 (2^-8); scores, sums, maxima and the accumulators are fp32.  O is divided by the sum
+ * of the rounded probabilities, so that its weights add up to one; L is of the others.
  * The rows of an average sequence, T * Hq / B, and for more than 64 of them the room of the
  * tables, max_pages * page, decide how the call is laid out (sums are then taken in another
  * order); a batch that mixes pieces of prompts with many single tokens is faster as two
