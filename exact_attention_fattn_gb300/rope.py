@@ -9,14 +9,16 @@ from .cache import _call
 
 
 def _view(t, name, d, dev):
-    """Strides of a [B, H, N, d] tensor, or of [T, H, d] rows as [1, H, T, d]."""
+    """Strides of a [B, H, N, d] tensor, or of [T, H, d] rows as [1, H, T, d]; 0 for
+    dimensions of one, whose strides may be any number."""
     if t.dtype is not torch.bfloat16:
         raise TypeError(f"{name} must be bfloat16, got {t.dtype}")
     if t.get_device() != dev:
         raise ValueError(f"{name} must be on the table's device")
-    s = t.stride()
-    if t.shape[-1] != d or (d > 1 and s[-1] != 1):
+    shape, s = t.shape, t.stride()
+    if shape[-1] != d or (d > 1 and s[-1] != 1):
         raise ValueError(f"the columns of {name} must be contiguous")
+    s = [x if n > 1 else 0 for n, x in zip(shape, s)]
     return (0, s[1], s[0]) if len(s) == 3 else s[:3]
 
 
