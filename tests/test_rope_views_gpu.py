@@ -1,4 +1,5 @@
-"""Rotations of views whose strides say little: dimensions of one."""
+"""Rotations of views whose strides say little: dimensions of one, and tensors past 32
+bits of elements, first and last row against the oracle."""
 
 import numpy as np
 import pytest
@@ -36,3 +37,27 @@ def test_dimensions_of_one_with_any_stride(view, call):
     assert torch.equal(call(x, t, out=y).float().cpu(), want)
     assert torch.equal(call(x, t, out=x).float().cpu(), want)     # in place
     assert F.fattn_check_status() == 0
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_rows_past_32_bits_of_elements(interleaved):
+    """The first rows, the last ones and those around 2^31 and 2^32 elements are the oracle's of what
+    was there before; none of them stays as it was."""
+    B, H, N, d = 33, 32, 32768, 128
+    x = torch.empty((B, H, N, d), dtype=torch.bfloat16, device="cuda")
+    assert x.numel() > 1 << 32
+    x.view(-1, 1 << 20).copy_(torch.arange(1 << 20, device="cuda").remainder(251).to(torch.bfloat16))
+    t = F.fattn_rope_table(N, d)
+    flat = x.view(-1, d)
+    rows = sorted({r + k for r in (0, (1 << 31) // d, (1 << 32) // d, B * H * N) for k in (-3, -2, -1, 0, 1, 2)
+                   if 0 <= r + k < B * H * N})
+    at = torch.tensor(rows, device="cuda")
+    flat[at] += torch.randn(len(rows), d, device="cuda").to(torch.bfloat16)
+    before = flat[at].clone()
+    assert F.fattn_rope(x, t, interleaved=interleaved, out=x) is x
+    assert F.fattn_check_status() == 0
+    pos = np.array([r % N for r in rows])
+    got = flat[at].float().cpu()
+    assert torch.equal(got, turned(before, t, pos, interleaved))
+    moved = (got != before.float().cpu()).any(dim=1).numpy()
+    assert (moved == (pos > 0)).all()                             # position 0 turns by nothing
