@@ -384,11 +384,6 @@ __global__ void __launch_bounds__(kScanThreads) plan_kernel(const Tables t, cons
 
 // ------------------------------------------------------------------ copies
 
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
-  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
-               "l"(src), "r"(bytes), "r"(bar)
-               : "memory");
-}
 // A group of its own; all but the last kBehind groups have then read their source.
 __device__ __forceinline__ void bulk_store(void* dst, uint32_t src, uint32_t bytes) {
   asm volatile(
@@ -527,7 +522,7 @@ __global__ void __launch_bounds__(kCopyThreads) copy_kernel(const Tables t, cons
       if (!(more = bytes != 0u)) break;
       length[at] = bytes;
       mbar_arrive_expect_tx(smem_u32(&full[at]), bytes);
-      bulk_load(sbase + at * kPieceBytes, src, bytes, smem_u32(&full[at]));
+      bulk_load_1d(sbase + at * kPieceBytes, src, bytes, smem_u32(&full[at]));
       ++loads;
     }
     if (stores == loads) break;
