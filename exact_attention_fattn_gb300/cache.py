@@ -53,7 +53,8 @@ def fattn_rope_table(positions: int, rope_dim: int, theta: float = 10000.0, devi
     are divided by the factor: all of them (``original`` 0), or, with
     ``original`` the trained length, those that turn less than ramp[0] times in
     it, while those that turn ramp[1] times or more stay and those between go
-    over linearly; the table is then multiplied by ``magnitude`` (by default
+    over linearly in their turns (a model whose angles go over in another way
+    brings a table of its own: any fp32 one is taken); the table is then multiplied by ``magnitude`` (by default
     0.1 ln(factor) + 1), which scales the scores by its square."""
     if positions < 1 or rope_dim < 16 or rope_dim % 16:
         raise ValueError("rope_dim must be a multiple of 16, and there must be a position")

@@ -31,12 +31,12 @@
 // Bound: the cache's bytes for 16 and 32 rows, shared memory for 64, whose 1920 cycles of
 // products a 64-key tile (rank 512) are reads at 128 bytes a cycle, beside 576 for the
 // tile's way in.  Measured, rank 512, one new token each: 64 sequences of 500 to 8000 keys, 16 heads
-// 62 us (0.78 of the measured copy rate), 32 heads 68, 64 heads 78.5; 3 of 100000 to
-// 131071, 32 heads 75.7 (0.79); one of 1000, 16 heads 12.0, of which the two launches, the
+// 62 us (0.78 of the measured copy rate), 32 heads 68.6, 64 heads 78.7; 3 of 100000 to
+// 131071, 32 heads 75.6 (0.79); one of 1000, 16 heads 12.0, of which the two launches, the
 // schedule and the join are nearly all.  Products are issued in a fixed order by converged
-// code: under branches that the compiler takes for divergent each took 82 cycles (64
-// sequences of 128 heads 178 us, then 152; copies under a lane's branch, 190 cycles each,
-// 124.4, then 121.8).
+// code: under branches that the compiler takes for divergent each took 82 cycles (when this
+// kernel still had the calls of 128 heads, 64 sequences of them 178 us, then 152; copies
+// under a lane's branch, 190 cycles each, 124.4, then 121.8).
 //
 // Warps: 0-3 softmax and results (0-7 with 64 rows, half of them each), then one for
 // tensor memory and MMA issue, one for loads, one for the walk over the share (it
@@ -563,8 +563,8 @@ __global__ void __launch_bounds__(Cfg<N, R>::kThreads, 1)
     // ================================================================ TMA producer
     // Copies are issued by the converged warp, one lane of it elected by each: under a
     // branch on the lane their issue takes longer (190 cycles instead of 110), as
-    // an MMA's does.  A block's queries are one copy; the cache's come 64 columns a
-    // copy (128 a copy: prompt piece 629 us, 64: 611).
+    // an MMA's does.  A block's queries are one copy; the cache's come 64 columns a copy (128 a
+    // copy: two pieces of 1024 tokens, which pairs have now, 629 us, 64: 611).
     uint32_t tiles = 0, q_count = 0;
     uint32_t ropes = 0, pairs = 0;        // asked for so far
     uint32_t ps = 0, eph = 0;             // the next pair's slot, and the turn of the ring
@@ -665,7 +665,7 @@ __global__ void __launch_bounds__(Cfg<N, R>::kThreads, 1)
   } else if (warp == kLoad2Warp && args.page_shift == 5) {
     // ================================================================ second pages
     // Where a tile has two pages (of 32 tokens) this warp loads the second one: 64 sequences of
-    // 500 to 8000 keys, 64 heads 79.7 us, by one warp 84 (one role for both with its loads by
+    // 500 to 8000 keys, 64 heads 79.0 us, by one warp 84 (one role for both with its loads by
     // conditions 79.9, and 2 % slower for larger pages).
     uint32_t ropes = 0, pairs = 0, ps = 0, eph = 0;
     bool ok = true;

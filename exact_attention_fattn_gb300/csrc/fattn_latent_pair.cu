@@ -27,8 +27,8 @@
 // thread has stored (votes and P by plain remote stores and releases took 5500 cycles
 // a tile, 2500 of them waiting for the votes).
 //
-// Measured: 2 pieces of 1024 tokens, 16 heads, before keys up to 8192: 421 us (64 rows a CTA:
-// 570), 1185 TFLOP/s; 64 single tokens of 128 heads over 500 to 8000 keys 100 (123).  A tile
+// Measured: 2 pieces of 1024 tokens, 16 heads, before keys up to 8192: 420 us (64 rows a CTA:
+// 570), 1187 TFLOP/s; 64 single tokens of 128 heads over 500 to 8000 keys 100 (123).  A tile
 // takes 3800 cycles in the first, 1750 of them issue of the products.  When it took 467 us
 // neither the products bound it (with a quarter of their columns 459) nor L2 (two pairs a
 // cluster with one copy of the keys for both 512) nor the softmax (16 warps 477): a tile's

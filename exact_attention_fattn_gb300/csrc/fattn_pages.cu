@@ -14,7 +14,7 @@
 // 128, 500 to 2000 tokens) and room for 100 more, 38 us; 291 MB of a pool moved together
 // 58 us, 49 of them the copies, 0.87 of the measured copy rate (loads and stores of 16
 // bytes a thread, 2048 threads an SM: 39 and 63.4; pieces of 24 KB 36.5 and 57.9, of
-// 8 KB, with a division a piece, 58 and 75).
+// 8 KB, with a division a piece, 58 and 75); 576 of 768 sequences of 1250 tokens freed 3.2 us.
 #include <stdint.h>
 
 #include <nvtx3/nvToolsExt.h>

@@ -108,7 +108,9 @@ def fattn_latent_fwd(q, cache: LatentCache, page_table, q_start, kv_len, scale: 
     """Attention of bf16 [T, Hq, rank + 64] rows (absorbed queries and their
     rotated parts) over their sequences' cached tokens; returns (O bf16 [T, Hq,
     rank], L fp32 [T, Hq]).  ``scale`` is that of the heads before their
-    projection was absorbed, so it has no default."""
+    projection was absorbed, so it has no default.  One layout serves the whole
+    batch, chosen by its average sequence and, for many rows, the table's room:
+    pieces of prompts and many single tokens are faster in two calls than in one."""
     cs, dev = _check_latent(cache)
     B, max_pages = _check_batch(page_table, q_start, kv_len, dev)
     if q.dtype is not torch.bfloat16:
